@@ -1,5 +1,6 @@
 """GB300 (sm_103a) exact attention (forward, split-KV merge, e4m3 forward,
-backward): Python binding of ``libfa_gb300.so``.
+backward, sliding windows, rotary positions and a paged e4m3 cache): Python
+binding of ``libfa_gb300.so``.
 
 The functions below carry the names of the C ABI in ``include/fa.h`` and only
 marshal arguments: every step of the computation runs in the library's CUDA
@@ -23,15 +24,34 @@ STATUS_NAMES = {
     0: "FA_OK", 1: "FA_ERR_NULL", 2: "FA_ERR_ALIGN", 3: "FA_ERR_SHAPE", 4: "FA_ERR_HEADDIM",
     5: "FA_ERR_SPLITS", 6: "FA_ERR_WORKSPACE", 7: "FA_ERR_CUDA", 8: "FA_ERR_TIMEOUT",
     9: "FA_ERR_SCALE", 10: "FA_ERR_SCRATCH", 11: "FA_ERR_CAUSAL", 12: "FA_ERR_SEQLENS",
-    13: "FA_ERR_TILE",
+    13: "FA_ERR_TILE", 14: "FA_ERR_PAGES", 15: "FA_ERR_POSITIONS", 16: "FA_ERR_GROUP",
+    17: "FA_ERR_WINDOW", 18: "FA_ERR_ROPE", 19: "FA_ERR_PAGE_SIZE", 20: "FA_ERR_STRIDE",
 }
 # Causal mask modes (include/fa.h): key j visible to query i iff j <= i (top-left)
 # or j <= i + Nk - Nq (bottom-right).
 CAUSAL_NONE, CAUSAL_TOP_LEFT, CAUSAL_BOTTOM_RIGHT = 0, 1, 2
 _CAUSAL_NAMES = {"none": 0, "top_left": 1, "bottom_right": 2}
 FA_MAX_SPLITS = 256
+FA_MAX_AXES = 4
 
 _lib = None
+
+
+class _Rotation(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * FA_MAX_AXES),
+                ("max_pos", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int),
+                ("x_stride", ctypes.c_longlong * 3), ("y_stride", ctypes.c_longlong * 3)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("d", ctypes.c_int)]
 
 
 class FAError(RuntimeError):
@@ -76,6 +96,17 @@ def load_library() -> ctypes.CDLL:
     lib.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp]
     lib.fa_bwd.restype = i
+    ll = ctypes.c_longlong
+    lib.fa_rope.argtypes = [vp, vp, vp, i, i, i, i, vp]
+    lib.fa_rope.restype = i
+    lib.fa_kv_append_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, ll, ll, ll, vp]
+    lib.fa_kv_append_fp8.restype = i
+    lib.fa_paged_num_splits.argtypes = [i, i, i, i, i, i, i, i]
+    lib.fa_paged_num_splits.restype = i
+    lib.fa_paged_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_paged_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_fwd_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, vp]
+    lib.fa_fwd_paged_fp8.restype = i
     lib.fa_fwd_grid_ctas.argtypes = [i, i, i, i, i]
     lib.fa_fwd_grid_ctas.restype = ctypes.c_longlong
     lib.fa_device_status.argtypes = [vp, i]
@@ -389,7 +420,9 @@ def fa_fwd_grid_ctas(B: int, H: int, Nq: int, d: int, num_splits: int = 1) -> in
 
 
 def fa_device_status(clear: bool = True, stream=None) -> int:
-    """Synchronises the stream and returns the device status (FA_OK or FA_ERR_TIMEOUT)."""
+    """Synchronises the stream and returns the device status (FA_OK, FA_ERR_TIMEOUT, or
+    what a kernel found wrong in its device-side arguments: FA_ERR_SEQLENS,
+    FA_ERR_PAGES, FA_ERR_POSITIONS)."""
     return int(load_library().fa_device_status(_stream_handle(stream), int(bool(clear))))
 
 
@@ -432,6 +465,314 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
     st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Nq, Nk, d, scale,
             causal_code(causal), int(num_splits), _stream_handle(stream))
     _check(st, "fa_fwd_splitkv_static")
+
+
+# ------------------------------------------ rotary positions and the paged cache
+class _Launch:
+    """The device and stream of one call: ``stream`` or the device's current
+    one, with the tensors' device current while the library launches."""
+
+    __slots__ = ("handle", "device", "other", "guard")
+
+    def __init__(self, device, stream):
+        import torch
+
+        self.device = device
+        self.other = stream
+        if stream is None:
+            self.handle = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        else:
+            if getattr(stream, "device", device) != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.handle = _stream_handle(stream)
+
+    def __enter__(self):
+        import torch
+
+        self.guard = None
+        if self.device.index is not None and torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def used(self, *tensors):
+        """Tensors allocated for this call stay allocated until its stream has
+        passed it, when that is not the allocating stream."""
+        if self.other is None:
+            return
+        import torch
+
+        st = self.other
+        if not hasattr(st, "cuda_stream"):
+            st = torch.cuda.ExternalStream(int(st), device=self.device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(st)
+
+
+def _heads_view(t, name):
+    """(B, H, N, d, [batch, head, token strides]) of a bf16 CUDA tensor [B, H, N, d]
+    or, packed token-major, [N, H, d], whose columns are contiguous."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if not t.is_cuda or t.dim() not in (3, 4) or t.numel() == 0 or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be a non-empty CUDA tensor [B, H, N, d] or [N, H, d] with contiguous columns")
+    if t.dim() == 4:
+        (B, H, N, d), (sb, sh, sn, _) = t.shape, t.stride()
+    else:
+        (N, H, d), (sn, sh, _) = t.shape, t.stride()
+        B, sb = 1, 0
+    return B, H, N, d, (sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
+
+
+def _rotation(table, positions, sections, interleaved, tokens, device):
+    import torch
+
+    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.device != device:
+        raise ValueError(f"table must be contiguous float32 [max_pos, rot] on {device}")
+    axes = 1
+    if positions is not None:
+        if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.device != device:
+            raise ValueError(f"positions must be contiguous int32 [axes, tokens] on {device}")
+        axes = int(positions.shape[0]) if positions.dim() > 1 else 1
+        if positions.numel() != axes * tokens:
+            raise ValueError(f"positions must hold {tokens} tokens for each axis, got {tuple(positions.shape)}")
+    if axes > FA_MAX_AXES:
+        raise FAError(18, "rotation")
+    if sections is None:
+        sections = (int(table.shape[1]) // 2,) if axes == 1 else ()
+    if len(sections) != axes:
+        raise ValueError(f"sections must give the pairs of each of the {axes} axes")
+    return _Rotation(table.data_ptr(), positions.data_ptr() if positions is not None else None, int(table.shape[1]),
+                     axes, (ctypes.c_int * FA_MAX_AXES)(*[int(x) for x in sections]), int(table.shape[0]),
+                     int(bool(interleaved)))
+
+
+def fa_rope(q, k, q_out, k_out, table, positions, sections=None, interleaved=False, inverse=False, stream=None):
+    """Rotates ``q`` and ``k`` (or ``q`` alone: ``k`` and ``k_out`` None) into caller-owned outputs
+    (include/fa.h, fa_rope). Tensors are bf16 [B, H, N, d] or [N, H, d], of any strides that are
+    multiples of 8 with contiguous columns; an output may be its input. ``table`` fp32
+    [max_pos, rot] holds cosines, then sines; ``positions`` int32 [axes, B, N] or [axes, N] on the
+    device ([B, N] or [N] for one axis); ``sections`` the pairs of each axis. ``inverse`` turns
+    backwards: the rotation's gradient."""
+    B, H, N, d, xs = _heads_view(q, "q")
+    dev = q.device
+    if positions is None:
+        raise TypeError("positions must be a tensor")
+    if positions.dim() == (2 if q.dim() == 4 else 1):
+        positions = positions.unsqueeze(0)
+    rope = _rotation(table, positions, sections, interleaved, B * N, dev)
+    args = []
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            args.append(None)
+            continue
+        tb, th, tn, td, ts = _heads_view(t, name)
+        ob, oh, on, od, os_ = _heads_view(out, name + "_out")
+        if t.dim() != q.dim() or (tb, tn, td) != (B, N, d) or out.shape != t.shape:
+            raise ValueError(f"shape mismatch: {name} {tuple(t.shape)}, {name}_out {tuple(out.shape)}, "
+                             f"q {tuple(q.shape)}")
+        if t.device != dev or out.device != dev:
+            raise ValueError("every tensor must be on q's device")
+        if any(s == 0 and n > 1 for s, n in zip(os_, (ob, oh, on))):
+            raise ValueError(f"{name}_out must not be an expanded tensor")
+        args.append(_RopeTensor(t.data_ptr(), out.data_ptr(), th, (ctypes.c_longlong * 3)(*ts),
+                                (ctypes.c_longlong * 3)(*os_)))
+    with _Launch(dev, stream) as handle:
+        st = load_library().fa_rope(ctypes.byref(args[0]), ctypes.byref(args[1]) if args[1] else None,
+                                    ctypes.byref(rope), B, N, d, int(bool(inverse)), handle)
+    _check(st, "fa_rope")
+
+
+def rope(q, k, table, positions, sections=None, interleaved=False, inverse=False, stream=None):
+    """Allocate outputs and run :func:`fa_rope`. Returns ``(q_out, k_out)``, or ``q_out`` where
+    ``k`` is None."""
+    import torch
+
+    make = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    q_out, k_out = make(q), None if k is None else make(k)
+    fa_rope(q, k, q_out, k_out, table, positions, sections, interleaved, inverse, stream)
+    if stream is not None:
+        _Launch(q.device, stream).used(q_out, k_out)
+    return q_out if k is None else (q_out, k_out)
+
+
+def _tokens_view(t, name, device, heads=None, d=None):
+    """(tokens, heads, d, token stride) of a packed bf16 CUDA tensor [tokens, heads, d] whose heads
+    and columns are contiguous (its tokens may be further apart)."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bfloat16 tensor")
+    if not t.is_cuda or t.device != device or t.dim() != 3 or t.numel() == 0:
+        raise ValueError(f"{name} must be a non-empty tensor [tokens, heads, d] on {device}")
+    n, h, w = t.shape
+    sn, sh, sd = t.stride()
+    if sd != 1 or (h > 1 and sh != w):
+        raise ValueError(f"{name}: heads and columns of a token must be contiguous")
+    if (heads is not None and h != heads) or (d is not None and w != d):
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    return n, h, w, sn if n > 1 else h * w
+
+
+def _cache_view(k_cache, v_cache, k_scale, v_scale, device):
+    import torch
+
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+            raise TypeError(f"{name} must hold e4m3 codes (uint8 or float8_e4m3fn), got {t.dtype}")
+        if t.dim() != 4 or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be contiguous [num_pages, Hkv, page_size, d] on {device}")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError(f"shape mismatch k_cache{tuple(k_cache.shape)} v_cache{tuple(v_cache.shape)}")
+    pages, heads, size, d = (int(x) for x in k_cache.shape)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(t, name, (pages, heads), torch.float32, device)
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
+                       size, d)
+
+
+def _batch_view(page_table, cu_seqlens, seqlens_k, device):
+    import torch
+
+    for name, t, dim in (("page_table", page_table, 2), ("cu_seqlens", cu_seqlens, 1), ("seqlens_k", seqlens_k, 1)):
+        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be contiguous int32 with {dim} dimension(s) on {device}")
+    B = int(seqlens_k.shape[0])
+    if B < 1 or int(cu_seqlens.shape[0]) != B + 1 or int(page_table.shape[0]) != B:
+        raise ValueError("page_table [B, max_pages], cu_seqlens [B+1] and seqlens_k [B] must agree on B >= 1")
+    return B, int(page_table.shape[1])
+
+
+def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
+                     max_seqlen: int, table=None, positions=None, sections=None, interleaved=False, stream=None):
+    """Appends keys (rotated) and values to a paged e4m3 cache in place and rotates the queries
+    (include/fa.h, fa_kv_append_fp8). ``q`` [total, H, d] into ``q_out`` (both may be None), ``k`` and
+    ``v`` bf16 [total, Hkv, d], whose tokens may be strided (a fused projection's rows); ``k_cache``
+    and ``v_cache`` [num_pages, Hkv, page_size, d] e4m3 codes, ``k_scale`` and ``v_scale`` fp32
+    [num_pages, Hkv]; ``page_table`` int32 [B, max_pages], ``cu_seqlens`` int32 [B+1] of the new
+    tokens (``max_seqlen`` the most of a sequence), ``seqlens_k`` int32 [B] the cache lengths with
+    them. ``table`` None: no rotation; ``positions`` None: the cache positions."""
+    import torch
+
+    dev = k.device
+    n, hkv, d, ks = _tokens_view(k, "k", dev)
+    vn, _, _, vs = _tokens_view(v, "v", dev, hkv, d)
+    if vn != n:
+        raise ValueError("k and v must have the same tokens")
+    cache = _cache_view(k_cache, v_cache, k_scale, v_scale, dev)
+    if (cache.Hkv, cache.d) != (hkv, d):
+        raise ValueError(f"k has {hkv} heads of {d}, the cache {cache.Hkv} of {cache.d}")
+    B, max_pages = _batch_view(page_table, cu_seqlens, seqlens_k, dev)
+    H = qs = 0
+    if q is not None:
+        qn, H, _, qs = _tokens_view(q, "q", dev, None, d)
+        if qn != n:
+            raise ValueError("q and k must have the same tokens")
+        _need(q_out, "q_out", (n, H, d), torch.bfloat16, dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rope = None
+    if table is not None:
+        rope = _rotation(table, positions.view(1, -1) if positions is not None and positions.dim() == 1 else positions,
+                         sections, interleaved, n, dev)
+    elif positions is not None:
+        raise ValueError("positions without a table")
+    with _Launch(dev, stream) as handle:
+        st = load_library().fa_kv_append_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out),
+                                             ctypes.byref(rope) if rope else None, ctypes.byref(cache),
+                                             _ptr(page_table), _ptr(cu_seqlens), _ptr(seqlens_k), B, H, n,
+                                             int(max_seqlen), max_pages, qs, ks, vs, handle)
+    _check(st, "fa_kv_append_fp8")
+
+
+def kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k, max_seqlen: int,
+                  table=None, positions=None, sections=None, interleaved=False, stream=None):
+    """Allocate the rotated queries and run :func:`fa_kv_append_fp8`; returns them (None without
+    ``q``). Tokens past ``cu_seqlens[B]`` are left as allocated."""
+    import torch
+
+    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
+                     max_seqlen, table, positions, sections, interleaved, stream)
+    if stream is not None:
+        _Launch(k.device, stream).used(q_out)
+    return q_out
+
+
+def fa_paged_num_splits(B: int, H: int, Hkv: int, max_seqlen_q: int, max_seqlen_k: int, d: int, window: int = 0,
+                        sinks: int = 0) -> int:
+    """The key splits the library proposes for a paged call (0 for arguments out of range)."""
+    return int(load_library().fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks))
+
+
+def fa_paged_workspace_bytes(total_q: int, H: int, d: int, num_splits: int) -> int:
+    return int(load_library().fa_paged_workspace_bytes(total_q, H, d, num_splits))
+
+
+def fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k,
+                     max_seqlen_q: int, max_seqlen_k: int, workspace=None, num_splits: int = 1, window: int = 0,
+                     sinks: int = 0, scale: float | None = None, stream=None):
+    """Attention of ``q`` bf16 [total_q, H, d] (the last tokens of each sequence) over a paged e4m3
+    cache into caller-owned ``o`` bf16 [total_q, H, d] and ``lse`` fp32 [H, total_q] (include/fa.h,
+    fa_fwd_paged_fp8). ``workspace`` fp32 of at least ``fa_paged_workspace_bytes`` bytes where
+    ``num_splits > 1``."""
+    import torch
+
+    dev = q.device
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q must be bfloat16, got {q.dtype}")
+    if q.dim() != 3 or not q.is_contiguous() or not q.is_cuda:
+        raise ValueError("q must be a contiguous CUDA tensor [total_q, H, d]")
+    n, H, d = q.shape
+    cache = _cache_view(k_cache, v_cache, k_scale, v_scale, dev)
+    if cache.d != d:
+        raise ValueError(f"q has head dim {d}, the cache {cache.d}")
+    B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, dev)
+    _need(o, "o", (n, H, d), torch.bfloat16, dev)
+    _need(lse, "lse", (H, n), torch.float32, dev)
+    num_splits = int(num_splits)
+    if num_splits > 1:
+        _need_workspace(workspace, fa_paged_workspace_bytes(n, H, d, num_splits), "workspace", dev)
+    scale = default_scale(d) if scale is None else float(scale)
+    with _Launch(dev, stream) as handle:
+        st = load_library().fa_fwd_paged_fp8(_ptr(q), ctypes.byref(cache), _ptr(page_table), _ptr(cu_seqlens_q),
+                                             _ptr(seqlens_k), _ptr(o), _ptr(lse),
+                                             _ptr(workspace if num_splits > 1 else None), B, H, n,
+                                             int(max_seqlen_q), int(max_seqlen_k), max_pages, scale, int(window),
+                                             int(sinks), num_splits, handle)
+    _check(st, "fa_fwd_paged_fp8")
+
+
+def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_k,
+                        max_seqlen_q: int, max_seqlen_k: int, window: int = 0, sinks: int = 0,
+                        scale: float | None = None, num_splits: int | None = None, stream=None):
+    """Allocate ``o``, ``lse`` and the workspace and run :func:`fa_fwd_paged_fp8` (``num_splits``
+    None: the library's proposal). Returns ``(o, lse)``; rows past ``cu_seqlens_q[B]`` are left as
+    allocated."""
+    import torch
+
+    n, H, d = q.shape
+    if num_splits is None:
+        num_splits = fa_paged_num_splits(int(seqlens_k.shape[0]), H, int(k_cache.shape[1]), int(max_seqlen_q),
+                                         int(max_seqlen_k), d, int(window), int(sinks)) or 1
+    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
+    nbytes = fa_paged_workspace_bytes(n, H, d, num_splits)
+    ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device) if nbytes else None
+    fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+                     max_seqlen_k, ws, num_splits, window, sinks, scale, stream)
+    if stream is not None:
+        _Launch(q.device, stream).used(o, lse, ws)
+    return o, lse
 
 
 _SIDE_STREAMS = {}

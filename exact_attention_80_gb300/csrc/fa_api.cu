@@ -487,9 +487,11 @@ fa_status fa_device_status(cudaStream_t stream, int clear) {
         if (cudaStreamSynchronize(stream) != cudaSuccess) return FA_ERR_CUDA;
     }
     // Bounded waits that gave up take precedence; otherwise a rejected
-    // variable-length partition.
-    if (host & ~fa::kStatusBadSeqlens) return FA_ERR_TIMEOUT;
-    return host ? FA_ERR_SEQLENS : FA_OK;
+    // variable-length partition, page or position, in that order.
+    if (host & ~fa::kStatusNotWaits) return FA_ERR_TIMEOUT;
+    if (host & fa::kStatusBadSeqlens) return FA_ERR_SEQLENS;
+    if (host & fa::kStatusBadPage) return FA_ERR_PAGES;
+    return host ? FA_ERR_POSITIONS : FA_OK;
 }
 
 const char* fa_status_string(fa_status status) {
@@ -512,6 +514,18 @@ const char* fa_status_string(fa_status status) {
             return "FA_ERR_SEQLENS: cu_seqlens are not a valid partition (see fa_fwd_varlen)";
         case FA_ERR_TILE:
             return "FA_ERR_TILE: rows_per_cta is not offered for this head dim (see fa_fwd_rows)";
+        case FA_ERR_PAGES:
+            return "FA_ERR_PAGES: a page-table entry is not a page of the cache";
+        case FA_ERR_POSITIONS: return "FA_ERR_POSITIONS: a rotary position is outside the table";
+        case FA_ERR_GROUP: return "FA_ERR_GROUP: H must be a multiple of Hkv";
+        case FA_ERR_WINDOW:
+            return "FA_ERR_WINDOW: window and sinks must be >= 0, and sinks 0 without a window";
+        case FA_ERR_ROPE:
+            return "FA_ERR_ROPE: rot must be a multiple of 16 in [16, d], with 1 to FA_MAX_AXES axes whose "
+                   "sections sum to rot / 2";
+        case FA_ERR_PAGE_SIZE: return "FA_ERR_PAGE_SIZE: page_size must be 16, 32, 64 or 128";
+        case FA_ERR_STRIDE:
+            return "FA_ERR_STRIDE: a stride is negative, too large or not a multiple of 8 elements";
     }
     return "unknown fa_status";
 }

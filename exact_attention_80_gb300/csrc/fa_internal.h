@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <mutex>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime_api.h>
 
 #include "fa.h"
@@ -24,6 +25,11 @@ enum : unsigned {
     // Not a wait: variable-length offsets that are not a valid partition
     // (decreasing, past the token count, or longer than max_seqlen_q).
     kStatusBadSeqlens = 1u << 7,
+    // A page-table entry a call needed is not a page of the cache.
+    kStatusBadPage = 1u << 8,
+    // A rotary position is outside the table.
+    kStatusBadPosition = 1u << 9,
+    kStatusNotWaits = kStatusBadSeqlens | kStatusBadPage | kStatusBadPosition,
 };
 
 // Default bound of one wait, in SM clock cycles (~1 s at 2 GHz). Legitimate
@@ -171,6 +177,9 @@ bool valid_causal(int causal);
 // finite scale > 0; q, k, v 16-byte aligned.
 fa_status check_common(const void* q, const void* k, const void* v, int B, int H, int Nq, int Nk,
                        int d, float scale);
+bool valid_d(int d);
+// The driver's cuTensorMapEncodeTiled, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // bf16 [BH][N][d] as a 3-D TMA map, box {64, box_rows, 1}, 128-byte swizzle.
 bool encode_rows_map(CUtensorMap* map, const void* base, int d, int N, int BH, int box_rows);
 

@@ -1,0 +1,767 @@
+// fa_paged.cu — attention over the paged e4m3 cache: the kernel for few query
+// rows per kv head (single tokens, drafted tokens), the merge of its key
+// splits, and the C entry points.
+//
+// A CTA owns (sequence, kv head, 16 query rows, key split). Its rows are the
+// (query token, head of the group) pairs of the kv head, so a group's heads
+// share every byte of K and V that is read. What bounds it is that reading: a
+// key costs 2 d bytes and at 16 rows only 64 d multiply-adds, so the products
+// run on mma.sync (m16n8k16, f16 operands, fp32 sums), which needs no tile of
+// 128 rows.
+//
+// Each of the CTA's four warps takes every fourth tile of 32 keys with a ring of
+// its own: TMA copies of whole pages (or their 32-key parts) into swizzled
+// shared memory, one mbarrier per slot, no barrier between the warps until
+// their states meet at the end. e4m3 codes convert to f16 exactly (one
+// instruction per two codes), in the registers of the fragments:
+//   * K as the B operand of S = Q K^T. The contraction index may be permuted at
+//     will if Q is permuted alike, so a lane reads 16 consecutive codes of a
+//     key row with one 16-byte load and feeds four MMAs with them.
+//   * V as the B operand of O += P V, through ldmatrix.trans on pairs of codes:
+//     a 32-bit result holds two keys of two neighbouring columns; one byte
+//     permute separates the columns, which go to two MMAs.
+// Q (bf16) enters as f16 after a power-of-two scale per row that brings its
+// largest element to [2^7, 2^8): elements down to 2^-22 of it stay exact.
+//
+// The recurrence in base 2, with a tile's K scale ks and V scale vs per key:
+//   x_j = s_j * (ks_j * scale * log2 e) + log2 vs_j,  p_j = 2^(x_j - m + 10),
+//   O += p_j code_j,  l += p_j / vs_j:  O / l = sum_j softmax_j vs_j code_j.
+// The V scale sits in the exponent, so P stays in f16's range whatever the
+// scales are; the reference m moves only when a row's largest x passes it by
+// more than 4 (p <= 2^14), so O is seldom rescaled.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include "fa.h"
+#include "fa_paged.cuh"
+#include "fa_rope.cuh"
+
+namespace fa {
+
+fa_status check_cache(const fa_paged_cache* c) {
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return FA_ERR_NULL;
+    if (!valid_d(c->d)) return FA_ERR_HEADDIM;
+    if (c->page_size < 16 || c->page_size > 128 || (c->page_size & (c->page_size - 1))) return FA_ERR_PAGE_SIZE;
+    // Row indices of the cache seen as [num_pages * Hkv * page_size][d] are
+    // 32-bit TMA coordinates.
+    if (c->num_pages < 1 || c->Hkv < 1 || c->Hkv > 65535) return FA_ERR_SHAPE;
+    const unsigned long long rows = static_cast<unsigned long long>(c->num_pages) * c->Hkv;
+    if (rows > 0x7fffffffull / c->page_size) return FA_ERR_SHAPE;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+        return FA_ERR_ALIGN;
+    return FA_OK;
+}
+
+namespace {
+
+constexpr int kRows = 16;      // query rows per CTA
+constexpr int kKeys = 32;      // keys per warp tile
+constexpr int kWarps = 4;
+constexpr float kPShift = 10.f;  // p = 2^(x - m + 10)
+constexpr float kPSlack = 4.f;   // the reference moves when x passes it by more
+
+template <int D>
+struct PagedLayout {
+    static constexpr int ROW_BYTES = D < 128 ? D : 128;  // bytes of a swizzled row
+    static constexpr int PARTS = D / ROW_BYTES;          // row parts (128-byte columns of a key)
+    static constexpr uint32_t TILE = kKeys * D;          // bytes of K (or V) of a tile
+    static constexpr uint32_t SLOT = 2 * TILE;
+    static constexpr int STAGES = D == 64 ? 6 : 3;
+    static constexpr uint32_t RING = STAGES * SLOT;      // per warp
+    static constexpr bool Q_SHARED = D == 256;           // Q fragments in shared memory, not registers
+    static constexpr uint32_t Q_BYTES = Q_SHARED ? kRows * D * 2 : 0;
+    static constexpr uint32_t Q_OFF = kWarps * RING;
+    static constexpr uint32_t BAR_OFF = Q_OFF + Q_BYTES;
+    static constexpr uint32_t ML_OFF = BAR_OFF + kWarps * STAGES * 8;  // [warp][m, l][16 rows]
+    static constexpr uint32_t BYTES = ML_OFF + kWarps * 2 * kRows * 4;
+    static constexpr size_t ALLOC = BYTES + 1024;
+    static_assert(RING >= kRows * D * 4, "a warp's O is staged in its ring");
+    static_assert(TILE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
+};
+
+struct PagedParams {
+    CUtensorMap tm_k, tm_v;  // e4m3 [num_pages * Hkv * page_size][d], box {row part, min(page_size, 32)}
+    const __nv_bfloat16* q;  // [total_q][H][d]
+    __nv_bfloat16* o;
+    float* lse;              // [H][total_q]
+    const float* k_scale;    // [num_pages][Hkv]
+    const float* v_scale;
+    const int* page_table;   // [B][max_pages]
+    const int* cu;
+    const int* lens;
+    float* ws_o;             // [splits][total_q * H][d]
+    float* ws_m;             // base-2 units of the scaled score
+    float* ws_l;
+    int B, H, Hkv, G, total_q, max_q, max_k, num_pages, log_page, max_pages;
+    int window, sinks;
+    int row_blocks, num_splits, tiles_per_split;
+    float scale_log2;
+    long long wait_limit;
+    unsigned* status;
+};
+
+// The key tiles a row block visits, as a list: tiles 0 .. ns - 1 (sinks), then
+// tile `lo` on, n in all. Positions p0 .. p1 are the block's first and last.
+struct KeyList {
+    int ns, lo, n;
+    __device__ __forceinline__ int tile(int i) const { return i < ns ? i : lo + (i - ns); }
+};
+__device__ __forceinline__ KeyList key_list(int window, int sinks, int p0, int p1) {
+    KeyList k;
+    const int end = p1 < 0 ? 0 : p1 / kKeys + 1;
+    k.ns = 0, k.lo = 0;
+    if (window > 0) {
+        const int first = max(0, p0 - window + 1) / kKeys;
+        const int st = min((sinks + kKeys - 1) / kKeys, end);
+        if (first > st) k.ns = st, k.lo = first;
+    }
+    k.n = k.ns + max(0, end - k.lo);
+    return k;
+}
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, long long limit, unsigned* status,
+                                             unsigned what) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long start = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (clock64() - start > limit) {
+            atomicOr(status, what);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ld_shared_v4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Byte offset of 16-byte unit `unit` of key row `row` in a swizzled tile: rows
+// of 128 bytes (units XOR row mod 8; further row parts 32 rows behind), or of
+// 64 bytes (units XOR row / 2 mod 4).
+template <int D>
+__device__ __forceinline__ uint32_t tile_unit(int row, int unit) {
+    if constexpr (D == 64) return row * 64 + ((unit ^ ((row >> 1) & 3)) << 4);
+    else return (unit >> 3) * (kKeys * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
+}
+// Key row (0..7 of an 8-key group) behind fragment index j: with 128-byte rows
+// the two rows that one quarter of a warp reads together lie four apart, so
+// that their swizzled units fall into different banks.
+template <int D>
+__device__ __forceinline__ int key_of(int j) {
+    return D == 64 ? j : (j >> 1) | ((j & 1) << 2);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
+    fa_paged_rows_kernel(const __grid_constant__ PagedParams p) {
+    using L = PagedLayout<D>;
+    constexpr int C = D / 64;    // 64-column parts of the contraction: one 16-byte load each
+    constexpr int X = D / 16;    // 16-column units of O
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring = sbase + warp * L::RING;
+    const uint32_t bar0 = sbase + L::BAR_OFF + warp * L::STAGES * 8;
+    if (lane == 0) {
+        for (int s = 0; s < L::STAGES; ++s) mbar_init(bar0 + 8 * s, 1);
+        fence_mbar_init();
+        if (warp == 0) {
+            tma_prefetch_desc(&p.tm_k);
+            tma_prefetch_desc(&p.tm_v);
+        }
+    }
+    __syncwarp();
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+
+    // Unit: row blocks fastest (they share K and V in L2), then splits, heads.
+    unsigned lin = blockIdx.x;
+    const int rb = static_cast<int>(lin % p.row_blocks);
+    lin /= p.row_blocks;
+    const int split = static_cast<int>(lin % p.num_splits);
+    lin /= p.num_splits;
+    const int h = static_cast<int>(lin % p.Hkv);
+    const int b = static_cast<int>(lin / p.Hkv);
+    NewTokens nt;
+    if (!new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt)) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
+        return;
+    }
+    const int rows = nt.n * p.G;
+    const int r0 = rb * kRows;
+    if (r0 >= rows) return;
+    const int start = nt.len - nt.n;  // position of the first query
+    const int p0 = start + r0 / p.G;
+    const int p1 = start + (min(r0 + kRows, rows) - 1) / p.G;
+    const KeyList list = key_list(p.window, p.sinks, p0, p1);
+    const int used = max(1, (list.n + p.tiles_per_split - 1) / p.tiles_per_split);
+    if (split >= used) return;
+    const int i0 = split * p.tiles_per_split;
+    const int i1 = min(list.n, i0 + p.tiles_per_split);
+    const int mine = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);  // this warp's tiles: i0 + warp + 4 k
+    const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+    const int page_size = 1 << p.log_page;
+    const int last_page = (nt.len - 1) >> p.log_page;
+
+    // The page behind the first (half = 0) or second 16 keys of tile kt, or -1
+    // where the sequence has none there (nothing is read) or its entry is bad.
+    auto page_of = [&](int kt, int half) -> int {
+        const int idx = (kt * kKeys + 16 * half) >> p.log_page;
+        if (idx > last_page) return -1;
+        const int id = table[idx];
+        if (id < 0 || id >= p.num_pages) {
+            atomicOr(p.status, kStatusBadPage);
+            return -1;
+        }
+        return id;
+    };
+    // Copies of tile kt, whose pages are id0 and (pages of 16 tokens) id1, into
+    // slot s: a page that is not there is left out, and its keys are masked.
+    auto issue = [&](int s, int kt, int id0, int id1) {
+        const uint32_t dst = ring + s * L::SLOT, bar = bar0 + 8 * s;
+        const bool two = page_size < kKeys;
+        const uint32_t each = (two ? 16 : kKeys) * D * 2;
+        mbar_arrive_expect_tx(bar, (id0 >= 0 ? each : 0u) + (two && id1 >= 0 ? each : 0u));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int id = half ? id1 : id0;
+            if ((half && !two) || id < 0) continue;
+            const int row = ((id * p.Hkv + h) << p.log_page) + ((kt * kKeys + 16 * half) & (page_size - 1));
+#pragma unroll
+            for (int c = 0; c < L::PARTS; ++c) {
+                const uint32_t at = dst + c * (kKeys * 128) + half * 16 * L::ROW_BYTES;
+                tma_load_2d(at, &p.tm_k, bar, c * 128, row);
+                tma_load_2d(at + L::TILE, &p.tm_v, bar, c * 128, row);
+            }
+        }
+    };
+    // Page ids of the warp's next 32 tiles to copy, one per lane.
+    int ids0 = -1, ids1 = -1;
+    auto fetch_ids = [&](int k) {
+        const int i = i0 + warp + kWarps * (k + lane);
+        ids0 = ids1 = -1;
+        if (i < i1) {
+            const int kt = list.tile(i);
+            ids0 = page_of(kt, 0);
+            if (page_size < kKeys) ids1 = page_of(kt, 1);
+        }
+    };
+    auto issue_next = [&](int k) {  // tile number k of the warp
+        if ((k & 31) == 0) fetch_ids(k);
+        const int a = __shfl_sync(0xffffffffu, ids0, k & 31), c = __shfl_sync(0xffffffffu, ids1, k & 31);
+        if (lane == 0) issue(k % L::STAGES, list.tile(i0 + warp + kWarps * k), a, c);
+        __syncwarp();
+    };
+    const int ahead = min(mine, L::STAGES);
+    for (int k = 0; k < ahead; ++k) issue_next(k);
+
+    // Q rows r0 + g and r0 + g + 8 as f16 A fragments: contraction index 2 t, 2 t + 1
+    // (and + 8) of step (c, ks) is column 64 c + 16 t + 4 ks + 0, 1 (and 2, 3).
+    float rowf[2];  // scale of a row's scores, base 2, without the K scale
+    int pos[2];     // its position (rows past the last one repeat the first; they are not written)
+    uint32_t qf[L::Q_SHARED ? 1 : C][4][4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = r0 + g + 8 * e;
+        const bool ok = r < rows;
+        const int i = (ok ? r : r0) / p.G, j = (ok ? r : r0) - i * p.G;
+        pos[e] = ok ? start + i : p1;
+        const __nv_bfloat16* src =
+            p.q + (static_cast<long long>(nt.first + i) * p.H + h * p.G + j) * D + 16 * t;
+        uint4 raw[C][2];
+        float mx = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                raw[c][u] = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * u);
+                float x[8];
+                unpack_bf16x8(raw[c][u], x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]));
+            }
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // Exponent of the largest element to 7; f and 1 / f stay normal.
+        const int ex = mx > 0.f ? min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 120) : 0;
+        const float f = exp2i(7 - ex > 120 ? 120 : 7 - ex);
+        rowf[e] = p.scale_log2 * (1.f / f);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x[8];
+                unpack_bf16x8(raw[c][u], x);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t a = pack_f16x2(x[4 * k] * f, x[4 * k + 1] * f);
+                    const uint32_t z = pack_f16x2(x[4 * k + 2] * f, x[4 * k + 3] * f);
+                    const int ks = 2 * u + k;
+                    if constexpr (L::Q_SHARED) {
+                        if (warp == 0) {
+                            uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::Q_OFF) + ((c * 4 + ks) * 32 + lane) * 4;
+                            dst[e] = a;
+                            dst[2 + e] = z;
+                        }
+                    } else {
+                        qf[c][ks][e] = a;
+                        qf[c][ks][2 + e] = z;
+                    }
+                }
+            }
+        }
+    }
+    if constexpr (L::Q_SHARED) __syncthreads();
+
+    float o[X][2][4];  // [16-column unit][even, odd column of a pair][row g: 2, row g + 8: 2]
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[x][e][k] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const int pmin = p0, pmax = p1;
+    // Scales of the warp's current 32 tiles, one tile per lane: K scale, log2 of
+    // the V scale and its reciprocal for both 16-key halves.
+    float sk[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f}, si[2] = {1.f, 1.f};
+    bool ok = true;
+
+    for (int k = 0; k < mine; ++k) {
+        if ((k & 31) == 0) {
+            const int i = i0 + warp + kWarps * (k + lane);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int id = (i < i1 && (half == 0 || page_size < kKeys)) ? page_of(list.tile(i), half) : -1;
+                const long long cell = static_cast<long long>(id) * p.Hkv + h;
+                const float vs = id >= 0 ? p.v_scale[cell] : 1.f;
+                sk[half] = id >= 0 ? p.k_scale[cell] : 1.f;
+                sv[half] = log2f(vs);
+                si[half] = 1.f / vs;
+            }
+            if (page_size >= kKeys) sk[1] = sk[0], sv[1] = sv[0], si[1] = si[0];
+        }
+        const int slot = k % L::STAGES;
+        ok = __all_sync(0xffffffffu, wait_bounded(bar0 + 8 * slot, (k / L::STAGES) & 1, p.wait_limit, p.status,
+                                                  kStatusWaitKvFull));
+        if (!ok) break;
+        const int key0 = list.tile(i0 + warp + kWarps * k) * kKeys;
+        const uint32_t ks_at = ring + slot * L::SLOT, vs_at = ks_at + L::TILE;
+
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            uint32_t kw[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) ld_shared_v4(kw[n], ks_at + tile_unit<D>(8 * n + key_of<D>(g), 4 * c + t));
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t a[4];
+                if constexpr (L::Q_SHARED) {
+                    ld_shared_v4(a, sbase + L::Q_OFF + ((c * 4 + ks) * 32 + lane) * 16);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[e] = qf[c][ks][e];
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    mma_f16(s[n], a, decode_e4m3x2_f16(static_cast<uint16_t>(kw[n][ks] & 0xffffu)),
+                            decode_e4m3x2_f16(static_cast<uint16_t>(kw[n][ks] >> 16)));
+            }
+        }
+
+        // x = s * (ks scale log2 e) + log2 vs, masked where a row does not see the key.
+        float kc[2], kv[2], ki[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            kc[half] = __shfl_sync(0xffffffffu, sk[half], k & 31);
+            kv[half] = __shfl_sync(0xffffffffu, sv[half], k & 31);
+            ki[half] = __shfl_sync(0xffffffffu, si[half], k & 31);
+        }
+        const bool masked = !(key0 + kKeys - 1 <= pmin &&
+                              (p.window <= 0 || key0 > pmax - p.window || key0 + kKeys <= p.sinks));
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float x = fmaf(s[n][e], rowf[e >> 1] * kc[n >> 1], kv[n >> 1]);
+                if (masked) {
+                    const int key = key0 + 8 * n + key_of<D>(2 * t + (e & 1));
+                    const int q = pos[e >> 1];
+                    if (!(key <= q && (p.window <= 0 || key > q - p.window || key < p.sinks))) x = -INFINITY;
+                }
+                s[n][e] = x;
+                top[e >> 1] = fmaxf(top[e >> 1], x);
+            }
+        }
+        float alpha[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+            top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+            const bool move = top[e] > m[e] + kPSlack;
+            const float mn = move ? top[e] : m[e];
+            alpha[e] = move ? ex2(m[e] - mn) : 1.f;
+            m[e] = mn;
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[x][e][j] *= alpha[j >> 1];
+            l[0] *= alpha[0];
+            l[1] *= alpha[1];
+        }
+        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - kPShift, m[1] == -INFINITY ? 0.f : m[1] - kPShift};
+        uint32_t pf[2][4];  // P of 16 keys as an A fragment
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            float e0 = ex2(s[n][0] - ref[0]), e1 = ex2(s[n][1] - ref[0]);
+            float e2 = ex2(s[n][2] - ref[1]), e3 = ex2(s[n][3] - ref[1]);
+            l[0] = fmaf(e0 + e1, ki[n >> 1], l[0]);
+            l[1] = fmaf(e2 + e3, ki[n >> 1], l[1]);
+            pf[n >> 1][2 * (n & 1)] = pack_f16x2(e0, e1);
+            pf[n >> 1][2 * (n & 1) + 1] = pack_f16x2(e2, e3);
+        }
+
+        // O += P V. Fragment index kk of 8 keys is key row key_of(kk); a key that
+        // no row sees may hold anything (a slot never written, a NaN): its bytes
+        // are cleared.
+        const int mrow = lane & 7, mhi = (lane >> 3) & 1, mx4 = lane >> 4;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+            if (masked) {
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    keep[hi] = 0u;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = key0 + 16 * kk + 8 * hi + key_of<D>(2 * t + e);
+                        const bool seen = key <= pmax && (p.window <= 0 || key > pmin - p.window || key < p.sinks);
+                        if (seen) keep[hi] |= e ? 0xffff0000u : 0x0000ffffu;
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < X; x += 2) {
+                uint32_t w[4];
+                ldmatrix_x4_trans(w, vs_at + tile_unit<D>(16 * kk + 8 * mhi + key_of<D>(mrow), x + mx4));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t lo = w[2 * u], hi = w[2 * u + 1];
+                    if (masked) lo &= keep[0], hi &= keep[1];
+                    lo = __byte_perm(lo, 0u, 0x3120);
+                    hi = __byte_perm(hi, 0u, 0x3120);
+                    mma_f16(o[x + u][0], pf[kk], decode_e4m3x2_f16(static_cast<uint16_t>(lo & 0xffffu)),
+                            decode_e4m3x2_f16(static_cast<uint16_t>(hi & 0xffffu)));
+                    mma_f16(o[x + u][1], pf[kk], decode_e4m3x2_f16(static_cast<uint16_t>(lo >> 16)),
+                            decode_e4m3x2_f16(static_cast<uint16_t>(hi >> 16)));
+                }
+            }
+        }
+        __syncwarp();
+        if (k + L::STAGES < mine) issue_next(k + L::STAGES);
+    }
+    if (!ok) {
+        // Copies still in flight land before the CTA goes away.
+        for (int s = 0; s < ahead; ++s) wait_bounded(bar0 + 8 * s, 0, p.wait_limit, p.status, kStatusWaitDrain);
+    }
+
+    // The warps' states meet: O rows staged in each warp's ring, m and l beside.
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    }
+    float* ml = reinterpret_cast<float*>(smem + L::ML_OFF) + warp * 2 * kRows;
+    if (t == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            ml[g + 8 * e] = m[e];
+            ml[kRows + g + 8 * e] = l[e];
+        }
+    }
+    float* stage = reinterpret_cast<float*>(smem + warp * L::RING);
+#pragma unroll
+    for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(stage + (g + 8 * e) * D + 16 * x + 4 * t) =
+                make_float4(o[x][0][2 * e], o[x][1][2 * e], o[x][0][2 * e + 1], o[x][1][2 * e + 1]);
+    if (__syncthreads_or(!ok)) return;
+
+    const float* mls = reinterpret_cast<const float*>(smem + L::ML_OFF);
+    constexpr int VEC = D / 4;  // float4 units of a row
+    for (int u = threadIdx.x; u < kRows * VEC; u += kWarps * 32) {
+        const int r = u / VEC, c = u - r * VEC;
+        if (r0 + r >= rows) break;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mls[w * 2 * kRows + r]);
+        float ll = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = mls[w * 2 * kRows + r];
+            const float f = mw == -INFINITY ? 0.f : ex2(mw - mm);
+            const float4 x = *reinterpret_cast<const float4*>(smem + w * L::RING + (r * VEC + c) * 16);
+            ll = fmaf(f, mls[w * 2 * kRows + kRows + r], ll);
+            a.x = fmaf(f, x.x, a.x), a.y = fmaf(f, x.y, a.y), a.z = fmaf(f, x.z, a.z), a.w = fmaf(f, x.w, a.w);
+        }
+        const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
+        const long long row = static_cast<long long>(nt.first + i) * p.H + h * p.G + j;
+        if (used == 1) {
+            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            *reinterpret_cast<uint2*>(p.o + row * D + 4 * c) =
+                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+            // l is a sum of 2^(x - m + 10): the shift comes out again.
+            if (c == 0)
+                p.lse[static_cast<long long>(h * p.G + j) * p.total_q + nt.first + i] =
+                    ll > 0.f ? (mm - kPShift + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+        } else {
+            const long long at = static_cast<long long>(split) * p.total_q * p.H + row;
+            *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
+            if (c == 0) {
+                p.ws_m[at] = mm;
+                p.ws_l[at] = ll;
+            }
+        }
+    }
+}
+
+// Merge of the key splits, one warp per (token, head) row whose block used more
+// than one: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
+template <int D>
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
+    constexpr int PER = D / 32;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int head = static_cast<int>(unit % p.H);
+    const long long rest = unit / p.H;
+    const int i = static_cast<int>(rest % p.max_q);
+    const int b = static_cast<int>(rest / p.max_q);
+    NewTokens nt;
+    if (b >= p.B || !new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt) || i >= nt.n) return;
+    // The row block of this row decides how many splits it used.
+    const int r = i * p.G + head % p.G;
+    const int r0 = r / kRows * kRows, rows = nt.n * p.G;
+    const int start = nt.len - nt.n;
+    const KeyList list =
+        key_list(p.window, p.sinks, start + r0 / p.G, start + (min(r0 + kRows, rows) - 1) / p.G);
+    const int used = (list.n + p.tiles_per_split - 1) / p.tiles_per_split;
+    if (used <= 1) return;
+    const long long row = static_cast<long long>(nt.first + i) * p.H + head;
+    const long long stride = static_cast<long long>(p.total_q) * p.H;
+    float mm = -INFINITY;
+    for (int s = lane; s < used; s += 32) mm = fmaxf(mm, p.ws_m[s * stride + row]);
+    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f, acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int s0 = 0; s0 < used; s0 += 32) {
+        const int s = s0 + lane;
+        const float f = s < used ? ex2(p.ws_m[s * stride + row] - ref) : 0.f;
+        ll = s < used ? fmaf(f, p.ws_l[s * stride + row], ll) : ll;
+        const int n = min(32, used - s0);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float* src = p.ws_o + ((s0 + k) * stride + row) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+                const float2 a = *reinterpret_cast<const float2*>(src + e);
+                acc[e] = fmaf(fk, a.x, acc[e]);
+                acc[e + 1] = fmaf(fk, a.y, acc[e + 1]);
+            }
+        }
+    }
+    for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * PER);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0)
+        p.lse[static_cast<long long>(head) * p.total_q + nt.first + i] =
+            ll > 0.f ? (ref - kPShift + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// e4m3 cache as [rows][d], box {min(d, 128), box_rows}, swizzled by row size.
+bool encode_cache_map(CUtensorMap* map, const void* base, int d, long long rows, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(d < 128 ? d : 128), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Most key tiles a row block can list.
+long long most_tiles(int max_q, int max_k, int window, int sinks) {
+    const long long all = (static_cast<long long>(max_k) + kKeys - 1) / kKeys;
+    if (window <= 0) return all;
+    const long long part = (static_cast<long long>(window) + std::min(max_q, kRows) + kKeys - 1) / kKeys + 1 +
+                           (static_cast<long long>(sinks) + kKeys - 1) / kKeys;
+    return std::min(all, part);
+}
+
+template <int D>
+cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
+    using L = PagedLayout<D>;
+    static ContextCache<int> attr_set;
+    int done = 0;
+    cudaError_t e = attr_set.get(&done, [](int* out) {
+        *out = 1;
+        return cudaFuncSetAttribute(fa_paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(L::ALLOC));
+    });
+    if (e != cudaSuccess) return e;
+    const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    e = launch_dependent(fa_paged_rows_kernel<D>, dim3(static_cast<unsigned>(ctas)), kWarps * 32, L::ALLOC, stream, p);
+    if (e != cudaSuccess || p.num_splits == 1) return e;
+    const long long blocks = (static_cast<long long>(p.B) * p.max_q * p.H + 3) / 4;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    return launch_dependent(fa_paged_merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), 128, 0, stream, p);
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" {
+
+int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k, int d, int window, int sinks) {
+    if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || !fa::valid_d(d)) return 0;
+    const long long rows = static_cast<long long>(max_seqlen_q) * (H / Hkv);
+    const long long units = static_cast<long long>(B) * Hkv * ((rows + fa::kRows - 1) / fa::kRows);
+    const long long tiles = fa::most_tiles(max_seqlen_q, max_seqlen_k, window, sinks);
+    const long long want = (4ll * 304 + units - 1) / units;         // CTAs for four waves of two per SM
+    const long long most = std::max(1ll, tiles / (2 * fa::kWarps)); // two tiles per warp at least
+    return static_cast<int>(std::max(1ll, std::min({want, most, static_cast<long long>(FA_MAX_SPLITS)})));
+}
+
+size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits) {
+    if (total_q < 1 || H < 1 || !fa::valid_d(d) || num_splits < 1 || num_splits > FA_MAX_SPLITS) return 0;
+    if (num_splits == 1) return 0;
+    return static_cast<size_t>(num_splits) * total_q * H * (static_cast<size_t>(d) + 2) * sizeof(float);
+}
+
+fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens_q,
+                           const int* seqlens_k, void* o, float* lse, void* workspace, int B, int H, int total_q,
+                           int max_seqlen_q, int max_seqlen_k, int max_pages, float scale, int window, int sinks,
+                           int num_splits, cudaStream_t stream) {
+    if (!q || !cache || !page_table || !cu_seqlens_q || !seqlens_k || !o || !lse) return FA_ERR_NULL;
+    const fa_status sc = fa::check_cache(cache);
+    if (sc != FA_OK) return sc;
+    const int Hkv = cache->Hkv, d = cache->d;
+    if (B < 1 || H < 1 || total_q < 1 || max_seqlen_q < 1 || max_seqlen_q > total_q || max_seqlen_k < 1 ||
+        max_pages < 1)
+        return FA_ERR_SHAPE;
+    if (H < Hkv || H % Hkv) return FA_ERR_GROUP;
+    if (static_cast<long long>(max_pages) * cache->page_size > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
+    if (max_seqlen_k > max_pages * cache->page_size) return FA_ERR_SHAPE;
+    if (static_cast<long long>(max_seqlen_q) * (H / Hkv) > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_SCALE;
+    if (window < 0 || sinks < 0 || (window == 0 && sinks != 0) || sinks > 0x40000000 || window > 0x40000000)
+        return FA_ERR_WINDOW;
+    if (num_splits < 1 || num_splits > FA_MAX_SPLITS) return FA_ERR_SPLITS;
+    if (!fa::aligned(q, 16) || !fa::aligned(o, 16) || !fa::aligned(lse, 4) || !fa::aligned(page_table, 4) ||
+        !fa::aligned(cu_seqlens_q, 4) || !fa::aligned(seqlens_k, 4))
+        return FA_ERR_ALIGN;
+    if (num_splits > 1 && (!workspace || !fa::aligned(workspace, 16))) return FA_ERR_WORKSPACE;
+    fa::PagedParams p;
+    std::memset(&p, 0, sizeof(p));
+    const long long rows = static_cast<long long>(cache->num_pages) * Hkv * cache->page_size;
+    const int box = std::min(cache->page_size, fa::kKeys);
+    if (!fa::encode_cache_map(&p.tm_k, cache->k, d, rows, box) || !fa::encode_cache_map(&p.tm_v, cache->v, d, rows, box))
+        return FA_ERR_CUDA;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.page_table = page_table;
+    p.cu = cu_seqlens_q;
+    p.lens = seqlens_k;
+    if (num_splits > 1) {
+        const size_t part = static_cast<size_t>(num_splits) * total_q * H;
+        p.ws_o = static_cast<float*>(workspace);
+        p.ws_m = p.ws_o + part * d;
+        p.ws_l = p.ws_m + part;
+    }
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.G = H / Hkv;
+    p.total_q = total_q;
+    p.max_q = max_seqlen_q;
+    p.max_k = max_seqlen_k;
+    p.num_pages = cache->num_pages;
+    p.log_page = fa::log2_exact(cache->page_size);
+    p.max_pages = max_pages;
+    p.window = window;
+    p.sinks = sinks;
+    p.row_blocks = static_cast<int>((static_cast<long long>(max_seqlen_q) * p.G + fa::kRows - 1) / fa::kRows);
+    p.num_splits = num_splits;
+    const long long tiles = fa::most_tiles(max_seqlen_q, max_seqlen_k, window, sinks);
+    p.tiles_per_split = static_cast<int>((tiles + num_splits - 1) / num_splits);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.wait_limit = fa::kDefaultWaitLimit;
+    if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+    const cudaError_t e = d == 64    ? fa::launch_paged<64>(p, stream)
+                          : d == 128 ? fa::launch_paged<128>(p, stream)
+                                     : fa::launch_paged<256>(p, stream);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -62,7 +62,14 @@ typedef enum {
     FA_ERR_SCRATCH = 10,   /* fa_fwd_splitkv_static: partial states exceed FA_STATIC_SCRATCH_BYTES */
     FA_ERR_CAUSAL = 11,    /* causal is not FA_CAUSAL_NONE, _TOP_LEFT or _BOTTOM_RIGHT */
     FA_ERR_SEQLENS = 12,   /* fa_fwd_varlen: cu_seqlens not a valid partition (from fa_device_status) */
-    FA_ERR_TILE = 13       /* fa_fwd_rows: rows_per_cta not offered for this head dim */
+    FA_ERR_TILE = 13,      /* fa_fwd_rows: rows_per_cta not offered for this head dim */
+    FA_ERR_PAGES = 14,     /* a page-table entry is not a page of the cache (from fa_device_status) */
+    FA_ERR_POSITIONS = 15, /* a rotary position is outside the table (from fa_device_status) */
+    FA_ERR_GROUP = 16,     /* H is not a multiple of Hkv */
+    FA_ERR_WINDOW = 17,    /* window or sinks out of range */
+    FA_ERR_ROPE = 18,      /* rotation: rot, axes or sections out of range */
+    FA_ERR_PAGE_SIZE = 19, /* page_size is not 16, 32, 64 or 128 */
+    FA_ERR_STRIDE = 20     /* a stride is negative, too large or not a multiple of 8 elements */
 } fa_status;
 
 #define FA_CAUSAL_NONE 0
@@ -269,11 +276,127 @@ fa_status fa_fwd_rows(const void* q, const void* k, const void* v, void* o, floa
 long long fa_fwd_grid_ctas(int B, int H, int Nq, int d, int num_splits);
 
 /*
+ * fa_rotation — rotary positions. The first `rot` columns of a head (rot a
+ * multiple of 16, at most d; the others are left as they are) form rot / 2
+ * pairs: columns (i, i + rot / 2), or (2 i, 2 i + 1) when `interleaved`. Pair i
+ * of a token turns by the angle whose cosine and sine are table[pos][i] and
+ * table[pos][rot / 2 + i], pos being the token's position on the pair's axis:
+ *   y_a = x_a cos - x_b sin,   y_b = x_b cos + x_a sin.
+ * With several axes (time, height and width of images and video) the first
+ * sections[0] pairs turn with axis 0, the next sections[1] with axis 1, and so
+ * on; the sections sum to rot / 2 (with one axis they are not read).
+ *   table      fp32 [max_pos][rot], 16-byte aligned (angles of far positions
+ *              are formed by the caller, in as many bits as they need)
+ *   positions  int32 [axes][tokens] on the device
+ * A position outside [0, max_pos) is found on the device: what it belongs to
+ * is not written, and fa_device_status later reports FA_ERR_POSITIONS.
+ */
+#define FA_MAX_AXES 4
+typedef struct {
+    const float* table;
+    const int* positions;
+    int rot, axes;
+    int sections[FA_MAX_AXES];
+    int max_pos;
+    int interleaved;
+} fa_rotation;
+
+/*
+ * fa_rope — rotates queries and keys (k may be NULL) in one launch. Each
+ * tensor is bf16 [B][H][N][d] by its strides in elements, {batch, head, token}
+ * (multiples of 8; columns contiguous), so it may be head-major, token-major
+ * (B = 1) or part of a fused projection; x and y may be the same memory with
+ * the same strides. Token (b, n) takes positions[axis][b * N + n]. `inverse`
+ * != 0 turns backwards: the gradient with respect to x of a rotation is the
+ * inverse rotation of the gradient with respect to y. Sums and products are
+ * rounded one by one in fp32 and once to bf16.
+ */
+typedef struct {
+    const void* x;
+    void* y;
+    int H;
+    long long x_stride[3], y_stride[3];
+} fa_rope_tensor;
+fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, const fa_rotation* rope, int B, int N, int d,
+                  int inverse, cudaStream_t stream);
+
+/*
+ * fa_paged_cache — keys and values in pages: k and v hold e4m3 codes
+ * [num_pages][Hkv][page_size][d], k_scale and v_scale fp32 [num_pages][Hkv]:
+ * the value of a code is its e4m3 value times its page's and head's scale.
+ * page_size is 16, 32, 64 or 128. Sequence b's token j lies in slot
+ * j % page_size of page page_table[b][j / page_size] (int32 [B][max_pages] on
+ * the device; entries behind a sequence's last page are not read). Scales are
+ * powers of two in [2^-100, 2^120] where fa_kv_append_fp8 wrote them;
+ * fa_fwd_paged_fp8 takes any positive scales in that range.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int num_pages, Hkv, page_size, d;
+} fa_paged_cache;
+
+/*
+ * fa_kv_append_fp8 — appends new keys and values to the cache, rotating the
+ * keys on the way, and rotates the new queries, in one launch.
+ *   k, v [total_new][Hkv][d], q [total_new][H][d] bf16 (read; tokens k_stride,
+ *   v_stride, q_stride elements apart, heads d apart), q_out [total_new][H][d]
+ *   bf16 (written, contiguous). q and q_out may both be NULL.
+ *   cu_seqlens int32 [B + 1]: sequence b brings tokens cu_seqlens[b] ..
+ *   cu_seqlens[b + 1] - 1 (at most max_new); seqlens_k int32 [B]: its cache
+ *   length with them, so they take cache positions seqlens_k[b] - n .. - 1.
+ *   rope: as above, positions [axes][total_new]; positions NULL means the
+ *   cache positions (one axis); rope NULL appends without a rotation.
+ * A block (page and head) of K or V has the scale 2^e, e the least with
+ * amax <= 448 * 2^e over the block's tokens (e >= -100). The first slot of a
+ * page starts a block anew; an append behind earlier tokens keeps the larger of
+ * the old and the new scale, and rounds the earlier codes again where it grew.
+ * The other slots keep their bytes. A sequence whose offsets or length are
+ * broken, and a page that is not one of the cache, is neither read nor written
+ * (FA_ERR_SEQLENS, FA_ERR_PAGES from fa_device_status); a position outside the
+ * table leaves that token's query, and its page's new keys, unwritten. Two
+ * sequences must not append to the same page in one call.
+ */
+fa_status fa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_out, const fa_rotation* rope,
+                           const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens,
+                           const int* seqlens_k, int B, int H, int total_new, int max_new, int max_pages,
+                           long long q_stride, long long k_stride, long long v_stride, cudaStream_t stream);
+
+/*
+ * fa_fwd_paged_fp8 — attention of new queries over the cache.
+ *   q, o bf16 [total_q][H][d], lse fp32 [H][total_q], packed as fa_fwd_varlen
+ *   packs them; H is a multiple of Hkv and query head h reads kv head
+ *   h / (H / Hkv). Sequence b's queries are its last tokens: query i of n is at
+ *   position p = seqlens_k[b] - n + i and sees key j iff j <= p and
+ *   (window = 0, or j > p - window, or j < sinks).
+ *   seqlens_k[b] <= max_seqlen_k <= max_pages * page_size.
+ * The keys of a row block are split into num_splits parts (FA_MAX_SPLITS at
+ * most; fa_paged_num_splits proposes a number), whose partial states meet in
+ * the workspace (fa_paged_workspace_bytes; none for one split) and are merged
+ * by a second launch. Slots behind a sequence's end may hold anything. Queries
+ * past cu_seqlens_q[B] are not written. Broken offsets and lengths: that
+ * sequence is neither read nor written, FA_ERR_SEQLENS from fa_device_status;
+ * a page that is not one of the cache: FA_ERR_PAGES, the sequence's result is
+ * undefined. Scores and sums are fp32; Q enters the products as f16 after an
+ * exact power-of-two scale per row, P as f16 (relative rounding 2^-11).
+ */
+int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k, int d, int window, int sinks);
+size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits);
+fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens_q,
+                           const int* seqlens_k, void* o, float* lse, void* workspace, int B, int H, int total_q,
+                           int max_seqlen_q, int max_seqlen_k, int max_pages, float scale, int window, int sinks,
+                           int num_splits, cudaStream_t stream);
+
+/*
  * fa_device_status — SYNCHRONISES `stream`, then reads the library's device
  * error word: FA_OK; FA_ERR_TIMEOUT if any kernel since the last clear gave up
  * on a bounded wait (it then exits cleanly and leaves its outputs undefined);
- * else FA_ERR_SEQLENS if fa_fwd_varlen met offsets that are not a valid
- * partition. `clear` != 0 resets the word. FA_ERR_CUDA if the read fails.
+ * else FA_ERR_SEQLENS if a call met sequence offsets or lengths that are not
+ * valid, FA_ERR_PAGES a page that is not one of the cache, FA_ERR_POSITIONS a
+ * rotary position outside the table. `clear` != 0 resets the word. FA_ERR_CUDA
+ * if the read fails.
  */
 fa_status fa_device_status(cudaStream_t stream, int clear);
 
