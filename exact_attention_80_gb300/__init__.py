@@ -107,6 +107,12 @@ def load_library() -> ctypes.CDLL:
     lib.fa_paged_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_fwd_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, vp]
     lib.fa_fwd_paged_fp8.restype = i
+    lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
+    lib.fa_fwd_window.restype = i
+    lib.fa_bwd_window_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_bwd_window_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
+    lib.fa_bwd_window.restype = i
     lib.fa_fwd_grid_ctas.argtypes = [i, i, i, i, i]
     lib.fa_fwd_grid_ctas.restype = ctypes.c_longlong
     lib.fa_device_status.argtypes = [vp, i]
@@ -773,6 +779,86 @@ def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     if stream is not None:
         _Launch(q.device, stream).used(o, lse, ws)
     return o, lse
+
+
+# ------------------------------------------------ sliding windows, grouped heads
+def _grouped(q, k, v):
+    import torch
+
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+        if t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [B, H, N, d]")
+    if k.device != q.device or v.device != q.device:
+        raise ValueError("q, k and v must be on the same device")
+    B, H, Nq, d = q.shape
+    if k.shape[0] != B or k.shape[3] != d or v.shape != k.shape:
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
+    return B, H, k.shape[1], Nq, k.shape[2], d
+
+
+def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """Sliding-window forward with sinks into caller-owned ``o`` (bf16 [B,H,Nq,d]) and ``lse`` (fp32
+    [B,H,Nq]); ``k`` and ``v`` [B,Hkv,Nk,d], H a multiple of Hkv (include/fa.h, fa_fwd_window).
+    ``window`` 0: no window, the bottom-right causal mask."""
+    B, H, Hkv, Nq, Nk, d = _grouped(q, k, v)
+    _need_o_lse(o, lse, B, H, Nq, d, q.device)
+    scale = default_scale(d) if scale is None else float(scale)
+    with _Launch(q.device, stream) as handle:
+        st = load_library().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, Nq, Nk, d, scale,
+                                          int(window), int(sinks), handle)
+    _check(st, "fa_fwd_window")
+
+
+def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
+    """Allocate ``o`` and ``lse`` and run :func:`fa_fwd_window`. Returns ``(o, lse)``."""
+    import torch
+
+    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
+    if stream is not None:
+        _Launch(q.device, stream).used(o, lse)
+    return o, lse
+
+
+def fa_bwd_window_workspace_bytes(B: int, H: int, Nq: int, d: int) -> int:
+    return int(load_library().fa_bwd_window_workspace_bytes(B, H, Nq, d))
+
+
+def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
+                  scale: float | None = None, stream=None):
+    """Backward of :func:`fa_fwd_window` into caller-owned ``dq``, ``dk``, ``dv`` (bf16, shaped like q,
+    k, v); ``workspace`` fp32 of at least ``fa_bwd_window_workspace_bytes`` bytes."""
+    import torch
+
+    B, H, Hkv, Nq, Nk, d = _grouped(q, k, v)
+    dev = q.device
+    for t, name, like in ((o, "o", q), (dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
+        _need(t, name, like.shape, torch.bfloat16, dev)
+    _need(lse, "lse", (B, H, Nq), torch.float32, dev)
+    _need_workspace(workspace, fa_bwd_window_workspace_bytes(B, H, Nq, d), "workspace", dev)
+    scale = default_scale(d) if scale is None else float(scale)
+    with _Launch(dev, stream) as handle:
+        st = load_library().fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
+                                          _ptr(dk), _ptr(dv), _ptr(workspace), B, H, Hkv, Nq, Nk, d, scale,
+                                          int(window), int(sinks), handle)
+    _check(st, "fa_bwd_window")
+
+
+def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
+                              stream=None):
+    """Allocate ``(dq, dk, dv)`` and the workspace and run :func:`fa_bwd_window`."""
+    import torch
+
+    B, H, Hkv, Nq, Nk, d = _grouped(q, k, v)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = torch.empty(max(1, fa_bwd_window_workspace_bytes(B, H, Nq, d) // 4), dtype=torch.float32, device=q.device)
+    fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, ws, window, sinks, scale, stream)
+    if stream is not None:
+        _Launch(q.device, stream).used(dq, dk, dv, ws)
+    return dq, dk, dv
 
 
 _SIDE_STREAMS = {}

@@ -79,8 +79,6 @@ FwdConfig fwd_config(int d) {
     return c;
 }
 
-namespace {
-
 cudaError_t sm_count(int* out) {
     static std::atomic<int> cache[64] = {};
     int dev = 0;
@@ -97,8 +95,6 @@ cudaError_t sm_count(int* out) {
     if (e == cudaSuccess && dev >= 0 && dev < 64) cache[dev].store(*out, std::memory_order_relaxed);
     return e;
 }
-
-}  // namespace
 
 // Argument checks and tensor maps shared with the backward's entry points
 // (declared in fa_internal.h).

@@ -87,6 +87,9 @@ struct BwdParams {
     float scale_log2;   // scale * log2(e)
     long long wait_limit;
     unsigned* status;
+    // Sliding window (bottom-right; 0: none) with sinks, and heads that share kv
+    // heads in groups: K, V, dK, dV have BHkv = B * Hkv heads.
+    int window, sinks, group, H, Hkv, BHkv;
 };
 
 namespace {
@@ -185,15 +188,30 @@ __device__ __forceinline__ void bwd_steps(const BwdParams& p, int kt, int& h0, i
     n = max(0, steps - h0);
 }
 
+// The steps of a key tile under a window: rows from the one at its first key to
+// the last whose window reaches its last key, or to the end where the tile
+// holds a sink.
+__device__ __forceinline__ void bwd_steps_win(const BwdParams& p, int kt, int& h0, int& n) {
+    const int off = p.Nk - p.Nq;
+    const int k0 = kt * kBwdKeys;
+    const int k1 = min(k0 + kBwdKeys, p.Nk) - 1;
+    const int first = max(0, k0 - off);
+    int last = p.Nq - 1;
+    if (p.window > 0 && k0 >= p.sinks) last = min(last, k1 - off + p.window - 1);
+    h0 = first / kBwdHalf;
+    n = last < first ? 0 : last / kBwdHalf - h0 + 1;
+}
+
 // P^T and dS^T of one 32-query chunk for this thread's key row: s and dp are
 // the chunk's S^T and dP^T columns, nl and nd the chunk's -LSE log2e and -D in
 // shared memory (the same addresses for every lane: broadcast loads). MASK:
 // `lim` is the first visible chunk column (causal) and `key_ok` whether the
-// key exists; without MASK every entry is visible.
-template <bool MASK>
+// key exists; without MASK every entry is visible. WIN: `end` is the first
+// column past the key's window.
+template <bool MASK, bool WIN = false>
 __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_t (&dp)[32], uint32_t nl,
                                           uint32_t nd, float sl2, int lim, bool key_ok, uint32_t (&pk)[16],
-                                          uint32_t (&dk)[16]) {
+                                          uint32_t (&dk)[16], int end = 0) {
     const uint64_t sl2x2 = f2pack(sl2, sl2);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
@@ -213,7 +231,7 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
             // The exponential runs for every element and the mask selects after
             // it (x is finite or -inf: no NaN), so there are no branches.
             const float ex = ex2(x[h]);
-            pv[h] = MASK ? ((key_ok && 4 * u + h >= lim) ? ex : 0.f) : ex;
+            pv[h] = MASK ? ((key_ok && 4 * u + h >= lim && (!WIN || 4 * u + h < end)) ? ex : 0.f) : ex;
         }
         const uint64_t g01 = fadd2(f2pack(__uint_as_float(dp[4 * u]), __uint_as_float(dp[4 * u + 1])),
                                    f2pack(d4[0], d4[1]));
@@ -244,7 +262,12 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
 // While the tensor core runs one step's MMAs, the compute group forms P^T and
 // dS^T of the other and the readout group adds the previous dQ^T to the
 // accumulator. With one ring slot (d = 256) the steps run in order.
-template <int D>
+//   WIN: sliding window with sinks and grouped heads. A CTA takes one key tile
+// of a kv head and walks the steps of every query head of the group in turn,
+// K and V staying resident and dV and dK accumulating over the whole group.
+// Units are ordered tile by tile over all kv heads: the tiles of the sinks,
+// which see every row behind them, start first.
+template <int D, bool WIN = false>
 __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
     using L = LayoutBwd<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -259,8 +282,8 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     // CTA = (head, key-tile unit, head-dim part), the part fastest.
     const int hd = static_cast<int>(blockIdx.x % L::HALVES);
     const int unit_lin = static_cast<int>(blockIdx.x / L::HALVES);
-    const int bh = unit_lin / p.tile_units;
-    const int ui = unit_lin % p.tile_units;
+    const int bh = WIN ? unit_lin % p.BHkv : unit_lin / p.tile_units;
+    const int ui = WIN ? unit_lin / p.BHkv : unit_lin % p.tile_units;
     int kts[2], h0s[2], ns[2];
     int nt = 1;
     kts[0] = ui;
@@ -270,13 +293,21 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     } else {
         kts[1] = ui;
     }
-    bwd_steps(p, kts[0], h0s[0], ns[0]);
+    if constexpr (WIN) bwd_steps_win(p, kts[0], h0s[0], ns[0]);
+    else bwd_steps(p, kts[0], h0s[0], ns[0]);
     if (nt == 2) bwd_steps(p, kts[1], h0s[1], ns[1]);
     else ns[1] = 0, h0s[1] = 0;
-    const int n_all = ns[0] + ns[1];
+    if constexpr (WIN) nt = p.group;
+    const int n_all = WIN ? ns[0] * p.group : ns[0] + ns[1];
     // The second tile reuses K/V, dV and dK only if both tiles have steps.
-    const bool handoff = nt == 2 && ns[0] > 0 && ns[1] > 0;
-    const size_t row0 = static_cast<size_t>(bh) * p.Nq_pad;
+    const bool handoff = !WIN && nt == 2 && ns[0] > 0 && ns[1] > 0;
+    // Pass tt of a CTA: its key tile, first step and number of steps; the head
+    // of Q, dO and the accumulator.
+    auto KT = [&](int tt) { return WIN ? kts[0] : kts[tt]; };
+    auto H0 = [&](int tt) { return WIN ? h0s[0] : h0s[tt]; };
+    auto NS = [&](int tt) { return WIN ? ns[0] : ns[tt]; };
+    auto ZQ = [&](int tt) { return WIN ? (bh / p.Hkv) * p.H + (bh % p.Hkv) * p.group + tt : bh; };
+    auto ROW0 = [&](int tt) { return static_cast<size_t>(ZQ(tt)) * p.Nq_pad; };
 
     if (threadIdx.x == 0) {
         mbar_init(bar(L::BAR_KV), 1);
@@ -328,21 +359,23 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         int issued = 0;    // global steps whose Q/dO loads were issued
         int kv_loads = 0;
         for (int tt = 0; tt < nt && ok; ++tt) {
-            const int n = ns[tt];
+            const int n = NS(tt);
             if (n == 0) continue;
-            if (kv_loads > 0)  // the previous tile's MMAs are done with K and V
+            const int zq = ZQ(tt);
+            const size_t row0 = ROW0(tt);
+            if (!WIN && kv_loads > 0)  // the previous tile's MMAs are done with K and V
                 ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_KVFREE), (kv_loads - 1) & 1, p, abort_flag,
                                                       kStatusWaitKvEmpty));
             if (!ok) break;
-            if (leader) {
-                const int k0 = kts[tt] * kBwdKeys;
+            if (leader && (!WIN || tt == 0)) {
+                const int k0 = KT(tt) * kBwdKeys;
                 mbar_arrive_expect_tx(bar(L::BAR_KV), 2 * L::V_BYTES);
                 for (int c = 0; c < L::CHUNKS; ++c) {
                     tma_load_3d(sbase + L::K_OFF + c * L::KV_CHUNK, &p.tm_k, bar(L::BAR_KV), 64 * c, k0, bh);
                     tma_load_3d(sbase + L::V_OFF + c * L::KV_CHUNK, &p.tm_v, bar(L::BAR_KV), 64 * c, k0, bh);
                 }
             }
-            ++kv_loads;
+            if (!WIN || tt == 0) ++kv_loads;
             for (int h = 0; h < n && ok; ++h) {
                 const int G = issued;
                 const int st = G % L::STAGES;
@@ -351,14 +384,14 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                                                           abort_flag, kStatusWaitKvEmpty));
                 if (!ok) break;
                 if (leader) {
-                    const int q0 = (h0s[tt] + h) * kBwdHalf;
+                    const int q0 = (H0(tt) + h) * kBwdHalf;
                     const uint32_t sb = sbase + L::STAGE_OFF + st * L::STAGE_BYTES;
                     const uint32_t rb = sbase + L::ROWS_OFF + st * 2 * L::ROWS_BYTES;
                     mbar_arrive_expect_tx(bar(L::BAR_QFULL + st), L::STAGE_BYTES + 2 * L::ROWS_BYTES);
                     for (int c = 0; c < L::CHUNKS; ++c) {
-                        tma_load_3d(sb + L::Q_IN + c * L::QH_CHUNK, &p.tm_q, bar(L::BAR_QFULL + st), 64 * c, q0, bh);
+                        tma_load_3d(sb + L::Q_IN + c * L::QH_CHUNK, &p.tm_q, bar(L::BAR_QFULL + st), 64 * c, q0, zq);
                         tma_load_3d(sb + L::DO_IN + c * L::QH_CHUNK, &p.tm_do, bar(L::BAR_QFULL + st), 64 * c, q0,
-                                    bh);
+                                    zq);
                     }
                     bulk_load(rb + L::NL_IN, p.nlse2 + row0 + q0, L::ROWS_BYTES, bar(L::BAR_QFULL + st));
                     bulk_load(rb + L::ND_IN, p.ndd + row0 + q0, L::ROWS_BYTES, bar(L::BAR_QFULL + st));
@@ -470,10 +503,12 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         int gb = 0;        // global index of the tile's first step
         int kv_loads = 0;
         for (int tt = 0; tt < nt && ok; ++tt) {
-            const int n = ns[tt];
+            const int n = NS(tt);
             if (n == 0) continue;
-            ok = wait_all(bar(L::BAR_KV), kv_loads & 1, kStatusWaitKvFull);
-            ++kv_loads;
+            if (!WIN || tt == 0) {
+                ok = wait_all(bar(L::BAR_KV), kv_loads & 1, kStatusWaitKvFull);
+                ++kv_loads;
+            }
             if (!ok) break;
             tc_fence_after();
             // The tile's first MMA into dV and dK waits until the compute group
@@ -483,7 +518,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                     if (!wait_all(bar(L::BAR_ACCFREE), 0, kStatusWaitO)) return false;
                     tc_fence_after();
                 }
-                return issue_vkq(G, true);
+                return issue_vkq(G, !WIN || tt == 0);
             };
             if constexpr (L::STAGES >= 3) {
                 if (ok) ok = issue_sdp(gb);
@@ -521,9 +556,9 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         bool ok = true;
         int gb = 0;
         for (int tt = 0; tt < nt && ok; ++tt) {
-            const int n = ns[tt];
-            const int h0 = h0s[tt];
-            const int k0 = kts[tt] * kBwdKeys;
+            const int n = NS(tt);
+            const int h0 = H0(tt);
+            const int k0 = KT(tt) * kBwdKeys;
             const int key = k0 + r;
             const bool key_ok = key < p.Nk;
             const bool key_tail = k0 + kBwdKeys > p.Nk;
@@ -534,7 +569,9 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                 // Every entry of the step is visible unless the tile holds missing
                 // keys or (causal) crosses the diagonal; padded query rows carry
                 // -inf as -LSE log2e, so their P is 0 either way.
-                const bool masked = key_tail || (p.causal && k0 + kBwdKeys - 1 > q0 + off);
+                bool masked = key_tail || (p.causal && k0 + kBwdKeys - 1 > q0 + off);
+                if constexpr (WIN)  // the step's last row has left the window of the tile's first key
+                    masked = masked || (p.window > 0 && k0 <= q0 + kBwdHalf - 1 + off - p.window);
                 ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_SFULL + b), (G >> 1) & 1, p, abort_flag, kStatusWaitS));
                 if (!ok) break;
                 tc_fence_after();
@@ -552,7 +589,12 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                 if (masked) {
                     // Key row `key` is visible to query q iff key <= q + off.
                     const int lim = p.causal ? key - off - q0 - 32 * g : -1;
-                    bwd_chunk<true>(sraw, draw, nl, nd, sl2, lim, key_ok, pk, dk);
+                    if constexpr (WIN) {
+                        const int end = p.window > 0 && key >= p.sinks ? lim + p.window : 64;
+                        bwd_chunk<true, true>(sraw, draw, nl, nd, sl2, lim, key_ok, pk, dk, end);
+                    } else {
+                        bwd_chunk<true>(sraw, draw, nl, nd, sl2, lim, key_ok, pk, dk);
+                    }
                 } else {
                     bwd_chunk<false>(sraw, draw, nl, nd, sl2, 0, true, pk, dk);
                 }
@@ -582,13 +624,14 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             // warp (`ok` is warp-uniform), and only the stores check that the key
             // exists. After the first of two tiles the TMEM reads are handed back
             // (ACCFREE) before the stores.
-            if (ok && n > 0) {
+            const bool last_pass = !WIN || tt == nt - 1;
+            if (ok && n > 0 && last_pass) {
                 const int G = gb + n - 1;
                 ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_DQFULL + (G & 1)), (G >> 1) & 1, p, abort_flag,
                                                       kStatusWaitO));
                 if (ok) tc_fence_after();
             }
-            if (ok) {
+            if (ok && last_pass) {
                 // This CTA's head-dim part of the key row's dK and dV.
                 __nv_bfloat16* dkp =
                     static_cast<__nv_bfloat16*>(p.dk) + (static_cast<size_t>(bh) * p.Nk + key) * D + hd * L::DH;
@@ -643,7 +686,8 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         bool ok = true;
         int gb = 0;
         for (int tt = 0; tt < nt && ok; ++tt) {
-            const int n = ns[tt];
+            const int n = NS(tt);
+            const size_t row0 = ROW0(tt);
             for (int h = 0; h < n && ok; ++h) {
                 const int G = gb + h;
                 const int b = G & 1;
@@ -657,7 +701,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::BAR_DQREAD + b));
-                float* dst = p.dq_acc + (row0 + static_cast<size_t>(h0s[tt] + h) * kBwdHalf) * D + hd * L::DH + r;
+                float* dst = p.dq_acc + (row0 + static_cast<size_t>(H0(tt) + h) * kBwdHalf) * D + hd * L::DH + r;
 #pragma unroll
                 for (int e = 0; e < 32; ++e) atomicAdd(dst + e * D, __uint_as_float(lo[e]));
 #pragma unroll
@@ -719,6 +763,84 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const __nv_bfloat16* __
     }
 }
 
+// Rows that see at most this many keys form D from P and dP (below).
+constexpr int kFewKeys = 16;
+
+// fa_bwd_pre_kernel under a window. A row that sees few keys has an O about as
+// large as a single V row, and where one weight is near 1 that key's dP - D is
+// a small difference: the rounding of bf16 O then dominates dS (measured on
+// N(0, 1) inputs with two visible keys: dQ, dK off by 3.8e-3 against 2.3e-3).
+// Such a row gets D = sum_j P_j dP_j from q, K, V and dO in fp32, at two dot
+// products per key; from about sixteen keys on the rounding averages out.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_win_pre_kernel(const __nv_bfloat16* __restrict__ q,
+                                                             const __nv_bfloat16* __restrict__ k,
+                                                             const __nv_bfloat16* __restrict__ v,
+                                                             const __nv_bfloat16* __restrict__ o,
+                                                             const __nv_bfloat16* __restrict__ dout,
+                                                             const float* __restrict__ lse,
+                                                             const __grid_constant__ BwdParams p, long long rows_pad) {
+    constexpr int PER = D / 32;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows_pad) return;
+    const long long bh = row / p.Nq_pad;
+    const int i = static_cast<int>(row - bh * p.Nq_pad);
+    auto load = [&](const __nv_bfloat16* src, float (&x)[PER]) {
+        const __nv_bfloat162* s2 = reinterpret_cast<const __nv_bfloat162*>(src + lane * PER);
+#pragma unroll
+        for (int e = 0; e < PER / 2; ++e) {
+            const float2 a = __bfloat1622float2(s2[e]);
+            x[2 * e] = a.x;
+            x[2 * e + 1] = a.y;
+        }
+    };
+    auto dot = [&](const float (&a)[PER], const float (&b)[PER]) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) s = fmaf(a[e], b[e], s);
+        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        return s;
+    };
+    float dd = 0.f, nl = -INFINITY;
+    if (i < p.Nq) {
+        const size_t src_row = static_cast<size_t>(bh) * p.Nq + i;
+        const float l = lse[src_row];
+        nl = (l == -INFINITY) ? -INFINITY : -(l * kLog2e);
+        float g[PER];
+        load(dout + src_row * D, g);
+        // Visible keys: [0, ns) and [w0, pos].
+        const int pos = i + p.Nk - p.Nq;
+        const int w0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+        const int ns = min(p.sinks, w0);
+        const int seen = pos < 0 ? 0 : ns + pos + 1 - w0;
+        if (seen > kFewKeys) {
+            float a[PER];
+            load(o + src_row * D, a);
+            dd = dot(a, g);
+        } else if (nl != -INFINITY) {
+            float a[PER];
+            load(q + src_row * D, a);
+            const long long b = bh / p.H;
+            const size_t base = static_cast<size_t>(b * p.Hkv + (bh - b * p.H) / p.group) * p.Nk;
+            for (int n = 0; n < seen; ++n) {
+                const size_t key = base + (n < ns ? n : w0 + (n - ns));
+                float kr[PER], vr[PER];
+                load(k + key * D, kr);
+                load(v + key * D, vr);
+                dd = fmaf(ex2(fmaf(dot(a, kr), p.scale_log2, nl)), dot(g, vr), dd);
+            }
+        }
+    }
+    if (lane == 0) {
+        const_cast<float*>(p.ndd)[row] = -dd;
+        const_cast<float*>(p.nlse2)[row] = nl;
+    }
+    float* z = p.dq_acc + static_cast<size_t>(row) * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e) reinterpret_cast<float2*>(z)[e] = make_float2(0.f, 0.f);
+}
+
 // dQ = scale * accumulator, to bf16: one warp per query row, D / 32 columns
 // per lane, reading the accumulator's padded rows.
 template <int D>
@@ -763,7 +885,7 @@ cudaError_t launch_bwd_pre(const void* o, const void* dout, const float* lse, fl
     return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
     using L = LayoutBwd<D>;
     // Kernel attributes belong to the context: set once per device and context.
@@ -771,13 +893,13 @@ cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         *out = 1;
-        return cudaFuncSetAttribute(fa_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_bwd_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC_BYTES));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.BH) * p.tile_units * L::HALVES;
+    const long long ctas = static_cast<long long>(WIN ? p.BHkv : p.BH) * p.tile_units * L::HALVES;
     if (ctas < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    fa_bwd_kernel<D><<<static_cast<unsigned>(ctas), L::THREADS, L::ALLOC_BYTES, stream>>>(p);
+    fa_bwd_kernel<D, WIN><<<static_cast<unsigned>(ctas), L::THREADS, L::ALLOC_BYTES, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -798,7 +920,24 @@ cudaError_t launch_bwd(const BwdParams& p, const void* o, const void* dout, cons
                        cudaStream_t stream) {
     cudaError_t e = launch_bwd_pre<D>(o, dout, lse, const_cast<float*>(p.nlse2), const_cast<float*>(p.ndd),
                                       p.dq_acc, p.BH, p.Nq, p.Nq_pad, stream);
-    if (e == cudaSuccess) e = launch_bwd_main<D>(p, stream);
+    if (e == cudaSuccess) e = launch_bwd_main<D, false>(p, stream);
+    if (e == cudaSuccess) e = launch_bwd_dq<D>(p.dq_acc, dq, p.BH, p.Nq, p.Nq_pad, p.scale, stream);
+    return e;
+}
+
+// The same under a window.
+template <int D>
+cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, const void* v, const void* o,
+                           const void* dout, const float* lse, void* dq, cudaStream_t stream) {
+    const long long rows_pad = static_cast<long long>(p.BH) * p.Nq_pad;
+    const long long blocks = (rows_pad + 7) / 8;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    using T = const __nv_bfloat16*;
+    fa_bwd_win_pre_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+        static_cast<T>(q), static_cast<T>(k), static_cast<T>(v), static_cast<T>(o), static_cast<T>(dout), lse, p,
+        rows_pad);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_bwd_main<D, true>(p, stream);
     if (e == cudaSuccess) e = launch_bwd_dq<D>(p.dq_acc, dq, p.BH, p.Nq, p.Nq_pad, p.scale, stream);
     return e;
 }
@@ -866,6 +1005,60 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
     const cudaError_t e = d == 64    ? fa::launch_bwd<64>(p, o, dout, lse, dq, stream)
                           : d == 128 ? fa::launch_bwd<128>(p, o, dout, lse, dq, stream)
                                      : fa::launch_bwd<256>(p, o, dout, lse, dq, stream);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Nq, int d) { return fa_bwd_workspace_bytes(B, H, Nq, d); }
+
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                        const float* lse, void* dq, void* dk, void* dv, void* workspace, int B, int H, int Hkv,
+                        int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream) {
+    fa_status s = fa::check_common(q, k, v, B, H, Nq, Nk, d, scale);
+    if (s != FA_OK) return s;
+    s = fa::check_window(H, Hkv, Nq, Nk, window, sinks);
+    if (s != FA_OK) return s;
+    if (!o || !dout || !lse || !dq || !dk || !dv) return FA_ERR_NULL;
+    if (!fa::aligned(o, 16) || !fa::aligned(dout, 16) || !fa::aligned(lse, 4) || !fa::aligned(dq, 16) ||
+        !fa::aligned(dk, 16) || !fa::aligned(dv, 16))
+        return FA_ERR_ALIGN;
+    if (!workspace || !fa::aligned(workspace, 16)) return FA_ERR_WORKSPACE;
+    const int BH = B * H;
+    const int Nq_pad = (Nq + 127) / 128 * 128;
+    const size_t rows_pad = static_cast<size_t>(BH) * Nq_pad;
+    float* dq_acc = static_cast<float*>(workspace);
+    float* nlse2 = dq_acc + rows_pad * d;
+    float* ndd = nlse2 + rows_pad;
+    fa::BwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.BHkv = B * Hkv;
+    if (!fa::encode_rows_map(&p.tm_q, q, d, Nq, BH, 64) || !fa::encode_rows_map(&p.tm_k, k, d, Nk, p.BHkv, 128) ||
+        !fa::encode_rows_map(&p.tm_v, v, d, Nk, p.BHkv, 128) || !fa::encode_rows_map(&p.tm_do, dout, d, Nq, BH, 64))
+        return FA_ERR_CUDA;
+    p.nlse2 = nlse2;
+    p.ndd = ndd;
+    p.dq_acc = dq_acc;
+    p.dk = dk;
+    p.dv = dv;
+    p.BH = BH;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.group = H / Hkv;
+    p.Nq = Nq;
+    p.Nk = Nk;
+    p.Nq_pad = Nq_pad;
+    p.causal = 1;
+    p.causal_br = 1;
+    p.window = window;
+    p.sinks = sinks;
+    p.k_tiles = (Nk + 127) / 128;
+    p.tile_units = p.k_tiles;
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.wait_limit = fa::kDefaultWaitLimit;
+    if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+    const cudaError_t e = d == 64    ? fa::launch_bwd_win<64>(p, q, k, v, o, dout, lse, dq, stream)
+                          : d == 128 ? fa::launch_bwd_win<128>(p, q, k, v, o, dout, lse, dq, stream)
+                                     : fa::launch_bwd_win<256>(p, q, k, v, o, dout, lse, dq, stream);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -52,6 +52,7 @@
 #include <type_traits>
 
 #include "fa_fwd_common.cuh"
+#include "fa_fwd_win.cuh"
 
 namespace fa {
 
@@ -635,7 +636,8 @@ __device__ __forceinline__ void tm_persist_control(const FwdParams& p, uint32_t 
 // M64: one 64-row query tile per CTA (fa_fwd_rows with 64 rows): M = 64 MMAs,
 // whose accumulator rows 16 q + i sit in TMEM lanes 32 q + i (i < 16) of lane
 // quarter q; lanes 16-31 of each quarter hold no row.
-template <int D, bool F8, bool DUAL = false, bool PERSIST = false, bool M64 = false>
+// WIN: sliding window with sinks and grouped heads (bf16; tm_window_control).
+template <int D, bool F8, bool DUAL = false, bool PERSIST = false, bool M64 = false, bool WIN = false>
 __device__ __forceinline__ void tm_forward(const FwdParams& p) {
     using L = LayoutTM<D, F8, PERSIST>;
     constexpr int QT = L::Q_TILES;
@@ -701,6 +703,8 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         tm_persist_control<D, F8>(p, sbase, tmem, abort_flag, warp);
       } else if constexpr (DUAL) {
         tm_dual_control<D, F8>(p, sbase, tmem, abort_flag, warp);
+      } else if constexpr (WIN) {
+        tm_window_control<D, L>(p, sbase, tmem, abort_flag, warp);
       } else {
       Work<QT> w;
       compute_work<QT, BN>(p, blockIdx.x, w);
@@ -959,8 +963,9 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
             lin = persist_unit(p, k);
             if (lin < 0) continue;
         }
-        std::conditional_t<DUAL, WorkDual, Work<QT>> w;
+        std::conditional_t<DUAL, WorkDual, std::conditional_t<WIN, WorkWin<QT>, Work<QT>>> w;
         if constexpr (DUAL) compute_work_dual<BN>(p, lin, w);
+        else if constexpr (WIN) compute_work_win<QT, BN>(p, lin, w);
         else compute_work<QT, BN>(p, lin, w);
         const int q_row = (M64 && lane >= 16) ? (1 << 30) : (DUAL ? w.q0 : tile_row0(p, w.q0, t)) + r;
         // This tile's key split: the CTA's, or its own in a dual-range CTA.
@@ -988,6 +993,7 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
 #pragma unroll
         for (int i = 1; i < QT; ++i)
             if (t == i) n = w.n[i];
+        if constexpr (WIN) n = t ? w.steps[1] : w.steps[0];
 
         float m = -INFINITY;       // exponent reference (base-2 units of scale*log2e*s)
         float m_true = -INFINITY;  // true running row max, same units
@@ -1014,6 +1020,10 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
             // Mask: keys past the split / sequence end, and (causal) keys after
             // this row + causal_off. Keys past the sequence end are zero fill
             // (or the next packed sequence's tokens), so they must become -inf.
+            if constexpr (WIN) {
+                const int hole = t ? w.hole[1] : w.hole[0];
+                win_mask<BN>(p, q_row + w.causal_off, w.list.tile(j < w.list.ns ? j : j + hole) * BN, s);
+            } else {
             const int kv0 = (kv_tile0_t + j) * BN;
             int valid = kv_end_t - kv0;
             if (p.causal) valid = min(valid, q_row + w.causal_off - kv0 + 1);
@@ -1021,6 +1031,7 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
 #pragma unroll
                 for (int c = 0; c < BN; ++c)
                     if (c >= valid) s[c] = -INFINITY;
+            }
             }
             __syncwarp();
 
@@ -1194,6 +1205,13 @@ template <int D>
 __global__ void __launch_bounds__(LayoutTM<D>::THREADS, 1)
     fa_fwd_tm_kernel(const __grid_constant__ FwdParams p) {
     tm_forward<D, false>(p);
+}
+
+// bf16, sliding window with sinks, grouped heads.
+template <int D>
+__global__ void __launch_bounds__(LayoutTM<D>::THREADS, 1)
+    fa_fwd_tmw_kernel(const __grid_constant__ FwdParams p) {
+    tm_forward<D, false, false, false, false, true>(p);
 }
 
 // bf16, one 64-row query tile per CTA (fa_fwd_rows with 64 rows).

@@ -33,7 +33,10 @@
 // (again bounded), TMEM is freed and the CTA exits.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_fwd_common.cuh"
+#include "fa_fwd_win.cuh"
 
 namespace fa {
 
@@ -136,7 +139,9 @@ struct LayoutTP {
     static_assert(65536 / THREADS >= LAUNCH_REGS || !REG_SPLIT, "launch registers");
 };
 
-template <int D, bool F8>
+// WIN: sliding window with sinks and grouped heads (one query tile: a step per
+// tile of its list).
+template <int D, bool F8, bool WIN = false>
 __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     using L = LayoutTP<D, F8>;
     constexpr int QT = L::Q_TILES;
@@ -161,8 +166,9 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
 
-    Work<QT> w;
-    compute_work<QT, BN>(p, blockIdx.x, w);
+    std::conditional_t<WIN, WorkWin<QT>, Work<QT>> w;
+    if constexpr (WIN) compute_work_win<QT, BN>(p, blockIdx.x, w);
+    else compute_work<QT, BN>(p, blockIdx.x, w);
 
     if (threadIdx.x == 0) {
         mbar_init(bar(L::BAR_QFULL), 1);
@@ -253,11 +259,18 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
                 if (leader) {
                     mbar_arrive_expect_tx(bar(L::BAR_KVFULL + pos.slot), L::SLOT_BYTES);
                     const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
-                    const int row = w.kbase + (w.kv_tile0 + tile) * BN;
+                    int row, zk;
+                    if constexpr (WIN) {
+                        row = w.list.tile(tile) * BN;
+                        zk = w.zk;
+                    } else {
+                        row = w.kbase + (w.kv_tile0 + tile) * BN;
+                        zk = w.zq;
+                    }
 #pragma unroll
                     for (int c = 0; c < L::CHUNKS; ++c)
                         tma_load_3d(sbase + L::SLOT_OFF + pos.slot * L::SLOT_BYTES + c * (BN * 128), map,
-                                    bar(L::BAR_KVFULL + pos.slot), L::CHUNK_ELEMS * c, row, w.zq);
+                                    bar(L::BAR_KVFULL + pos.slot), L::CHUNK_ELEMS * c, row, zk);
                 }
                 issued = e + 1;
                 pos.advance();
@@ -483,6 +496,9 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
             // Mask: keys past the split / sequence end, and (causal) keys after
             // this row + causal_off. Keys past the sequence end are zero fill
             // (or the next packed sequence's tokens), so they must become -inf.
+            if constexpr (WIN) {
+                win_mask<BN>(p, q_row + w.causal_off, w.list.tile(j) * BN, s);
+            } else {
             const int kv0 = (w.kv_tile0 + j) * BN;
             int valid = w.kv_end - kv0;
             if (p.causal) valid = min(valid, q_row + w.causal_off - kv0 + 1);
@@ -490,6 +506,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
 #pragma unroll
                 for (int c = 0; c < BN; ++c)
                     if (c >= valid) s[c] = -INFINITY;
+            }
             }
             __syncwarp();
 
@@ -641,6 +658,13 @@ template <int D>
 __global__ void __launch_bounds__(LayoutTP<D>::THREADS, 1)
     fa_fwd_tp_kernel(const __grid_constant__ FwdParams p) {
     tp_forward<D, false>(p);
+}
+
+// bf16, sliding window with sinks, grouped heads.
+template <int D>
+__global__ void __launch_bounds__(LayoutTP<D>::THREADS, 1)
+    fa_fwd_tpw_kernel(const __grid_constant__ FwdParams p) {
+    tp_forward<D, false, true>(p);
 }
 
 // e4m3 Q, K, V with per-tensor descales (FA-3 page, section 7.3: 8-bit inputs

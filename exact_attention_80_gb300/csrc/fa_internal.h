@@ -73,6 +73,9 @@ struct FwdParams {
     long long wait_limit;    // cycles
     int test_withhold_q;     // failure-detection test hook: 1 = never load Q
     unsigned* status;        // device status word
+    // Sliding-window launches (bottom-right): window 0 = none; heads in groups
+    // of `group` = H / Hkv share a kv head.
+    int window, sinks, group, Hkv;
 };
 
 // Backward (d = 128): one CTA per (head, 128-key tile).
@@ -96,6 +99,10 @@ cudaError_t launch_fwd_d128_persist(const FwdParams& p, unsigned grid, cudaStrea
 cudaError_t launch_fwd_f8_d64_persist(const FwdParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_fwd_f8_d128_persist(const FwdParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_fwd_d256(const FwdParams& p, unsigned grid, cudaStream_t stream);
+// Sliding window with sinks, grouped heads (plain mode, dense bf16).
+cudaError_t launch_fwd_win_d64(const FwdParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_fwd_win_d128(const FwdParams& p, unsigned grid, cudaStream_t stream);
+cudaError_t launch_fwd_win_d256(const FwdParams& p, unsigned grid, cudaStream_t stream);
 // e4m3 Q, K, V (tm_q/tm_k/tm_v are byte maps, box {128, rows, 1}, or {64,
 // rows, 1} with the 64-byte swizzle at d = 64); d = 64, 128, 256.
 cudaError_t launch_fwd_f8_d64(const FwdParams& p, unsigned grid, cudaStream_t stream);
@@ -178,6 +185,10 @@ bool valid_causal(int causal);
 fa_status check_common(const void* q, const void* k, const void* v, int B, int H, int Nq, int Nk,
                        int d, float scale);
 bool valid_d(int d);
+// Head groups, window and sinks of the sliding-window entry points.
+fa_status check_window(int H, int Hkv, int Nq, int Nk, int window, int sinks);
+// SMs of the current device (cached).
+cudaError_t sm_count(int* out);
 // The driver's cuTensorMapEncodeTiled, or null.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // bf16 [BH][N][d] as a 3-D TMA map, box {64, box_rows, 1}, 128-byte swizzle.

@@ -276,6 +276,33 @@ fa_status fa_fwd_rows(const void* q, const void* k, const void* v, void* o, floa
 long long fa_fwd_grid_ctas(int B, int H, int Nq, int d, int num_splits);
 
 /*
+ * fa_fwd_window — sliding-window attention with sinks and grouped heads.
+ *   q, o bf16 [B][H][Nq][d], k, v bf16 [B][Hkv][Nk][d] (H a multiple of Hkv;
+ *   query head h reads kv head h / (H / Hkv)), lse fp32 [B][H][Nq].
+ * Query row i has position p = i + Nk - Nq and sees key j iff j <= p and
+ * (window = 0, or j > p - window, or j < sinks): the last `window` keys up to
+ * itself, and the first `sinks` ones. window = 0 is the bottom-right causal mask
+ * (with sinks = 0). Rows that see no key (p < 0) get O = 0, LSE = -inf. Only the
+ * key tiles a unit's rows see are read. K and V must be finite, as in fa_fwd: a
+ * key that some rows of a tile see and others do not is multiplied by zero for
+ * the others.
+ */
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
+                        int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream);
+
+/*
+ * fa_bwd_window — its backward: dq [B][H][Nq][d], dk, dv [B][Hkv][Nk][d] bf16
+ * from q, k, v, the forward's o and lse, and dout; the gradients of a kv head
+ * are summed over the query heads of its group in fp32. As fa_bwd otherwise
+ * (dQ is summed over key tiles by fp32 atomics, so its last bits can differ
+ * between runs). workspace: fa_bwd_window_workspace_bytes, 16-byte aligned.
+ */
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Nq, int d);
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                        const float* lse, void* dq, void* dk, void* dv, void* workspace, int B, int H, int Hkv,
+                        int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream);
+
+/*
  * fa_rotation — rotary positions. The first `rot` columns of a head (rot a
  * multiple of 16, at most d; the others are left as they are) form rot / 2
  * pairs: columns (i, i + rot / 2), or (2 i, 2 i + 1) when `interleaved`. Pair i

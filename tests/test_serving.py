@@ -347,7 +347,7 @@ def check_paged(o, lse, ref, ref_lse, a, rows=None):
     assert np.all(err <= lim), f"worst {np.max(err - lim)} at {np.unravel_index(np.argmax(err - lim), err.shape)}"
     empty = np.isneginf(ref_lse)
     assert np.array_equal(np.isneginf(lse), empty)
-    assert np.all(np.abs(lse - ref_lse)[~empty] <= 5e-4)
+    assert np.all(np.abs(lse[~empty] - ref_lse[~empty]) <= 5e-4)
 
 
 @pytest.mark.parametrize("case", range(len(PAGED)))
