@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa_gb300.so")
@@ -35,23 +36,6 @@ FA_MAX_SPLITS = 256
 FA_MAX_AXES = 4
 
 _lib = None
-
-
-class _Rotation(ctypes.Structure):
-    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot", ctypes.c_int),
-                ("axes", ctypes.c_int), ("sections", ctypes.c_int * FA_MAX_AXES),
-                ("max_pos", ctypes.c_int), ("interleaved", ctypes.c_int)]
-
-
-class _RopeTensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int),
-                ("x_stride", ctypes.c_longlong * 3), ("y_stride", ctypes.c_longlong * 3)]
-
-
-class _PagedCache(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int),
-                ("page_size", ctypes.c_int), ("d", ctypes.c_int)]
 
 
 class FAError(RuntimeError):
@@ -96,16 +80,16 @@ def load_library() -> ctypes.CDLL:
     lib.fa_bwd_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, vp]
     lib.fa_bwd.restype = i
-    ll = ctypes.c_longlong
-    lib.fa_rope.argtypes = [vp, vp, vp, i, i, i, i, vp]
+    ll, packed = ctypes.c_longlong, ctypes.c_char_p  # packed: a struct of the interface, as bytes
+    lib.fa_rope.argtypes = [packed, packed, packed, i, i, i, i, vp]
     lib.fa_rope.restype = i
-    lib.fa_kv_append_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, ll, ll, ll, vp]
+    lib.fa_kv_append_fp8.argtypes = [vp, vp, vp, vp, packed, packed, vp, vp, vp, i, i, i, i, i, ll, ll, ll, vp]
     lib.fa_kv_append_fp8.restype = i
     lib.fa_paged_num_splits.argtypes = [i, i, i, i, i, i, i, i]
     lib.fa_paged_num_splits.restype = i
     lib.fa_paged_workspace_bytes.argtypes = [i, i, i, i]
     lib.fa_paged_workspace_bytes.restype = ctypes.c_size_t
-    lib.fa_fwd_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, vp]
+    lib.fa_fwd_paged_fp8.argtypes = [vp, packed, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, vp]
     lib.fa_fwd_paged_fp8.restype = i
     lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
     lib.fa_fwd_window.restype = i
@@ -474,90 +458,106 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
 
 
 # ------------------------------------------ rotary positions and the paged cache
+# These calls are short (a decode step of a few sequences runs in a few
+# microseconds on the GPU), so their checks touch each tensor once, and the
+# interface's structs are packed as bytes.
+_ROTATION = struct.Struct(f"PPii{FA_MAX_AXES}iii")   # fa_rotation
+_ROPE_TENSOR = struct.Struct("PPi6q")                # fa_rope_tensor
+_PAGED_CACHE = struct.Struct("PPPPiiii")             # fa_paged_cache
+
+
+def _raw_stream(index):
+    """Handle of the current stream of device ``index``."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class _Launch:
-    """The device and stream of one call: ``stream`` or the device's current
-    one, with the tensors' device current while the library launches."""
+    """The stream of one call on device ``index``: ``stream``, or the device's
+    current one. As a context it makes that device the current one while the
+    library launches and yields the stream's handle."""
 
-    __slots__ = ("handle", "device", "other", "guard")
+    __slots__ = ("index", "stream", "guard")
 
-    def __init__(self, device, stream):
-        import torch
-
-        self.device = device
-        self.other = stream
-        if stream is None:
-            self.handle = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-        else:
-            if getattr(stream, "device", device) != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.handle = _stream_handle(stream)
+    def __init__(self, index, stream):
+        self.index = index
+        self.stream = stream
+        on = getattr(stream, "device", None)
+        if on is not None and on.index != index:
+            raise ValueError(f"stream is on {on}, the tensors on device {index}")
 
     def __enter__(self):
         import torch
 
         self.guard = None
-        if self.device.index is not None and torch.cuda.current_device() != self.device.index:
-            self.guard = torch.cuda.device(self.device)
+        if self.index >= 0 and torch.cuda.current_device() != self.index:
+            self.guard = torch.cuda.device(self.index)
             self.guard.__enter__()
-        return self.handle
+        st = self.stream
+        return _raw_stream(self.index) if st is None else int(getattr(st, "cuda_stream", st))
 
     def __exit__(self, *exc):
         if self.guard is not None:
             self.guard.__exit__(*exc)
 
-    def used(self, *tensors):
-        """Tensors allocated for this call stay allocated until its stream has
-        passed it, when that is not the allocating stream."""
-        if self.other is None:
-            return
-        import torch
 
-        st = self.other
-        if not hasattr(st, "cuda_stream"):
-            st = torch.cuda.ExternalStream(int(st), device=self.device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(st)
+def _used_on(stream, *tensors):
+    """Tensors allocated for a call stay allocated until ``stream`` has passed it
+    (None: the allocating stream, which needs nothing)."""
+    if stream is None:
+        return
+    import torch
+
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream if hasattr(stream, "cuda_stream") else
+                            torch.cuda.ExternalStream(int(stream), device=t.device))
 
 
 def _heads_view(t, name):
-    """(B, H, N, d, [batch, head, token strides]) of a bf16 CUDA tensor [B, H, N, d]
-    or, packed token-major, [N, H, d], whose columns are contiguous."""
+    """(B, H, N, d, batch, head and token strides) of a bf16 CUDA tensor [B, H, N, d] or, packed
+    token-major, [N, H, d], whose columns are contiguous."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    if not t.is_cuda or t.dim() not in (3, 4) or t.numel() == 0 or t.stride(-1) != 1:
-        raise ValueError(f"{name} must be a non-empty CUDA tensor [B, H, N, d] or [N, H, d] with contiguous columns")
-    if t.dim() == 4:
-        (B, H, N, d), (sb, sh, sn, _) = t.shape, t.stride()
-    else:
-        (N, H, d), (sn, sh, _) = t.shape, t.stride()
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 4:
+        (B, H, N, d), (sb, sh, sn, sd) = shape, strides
+    elif len(shape) == 3:
+        (N, H, d), (sn, sh, sd) = shape, strides
         B, sb = 1, 0
-    return B, H, N, d, (sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
+    else:
+        sd = 0
+    if sd != 1 or not t.is_cuda or 0 in shape:
+        raise ValueError(f"{name} must be a non-empty CUDA tensor [B, H, N, d] or [N, H, d] with contiguous columns")
+    return B, H, N, d, sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0
 
 
-def _rotation(table, positions, sections, interleaved, tokens, device):
+def _rotation(table, positions, axes, sections, interleaved, tokens, index):
+    """fa_rotation of a table and of positions that hold ``axes`` rows."""
     import torch
 
-    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.device != device:
-        raise ValueError(f"table must be contiguous float32 [max_pos, rot] on {device}")
-    axes = 1
+    rows, rot = table.shape
+    if table.dtype is not torch.float32 or not table.is_contiguous() or table.get_device() != index:
+        raise ValueError(f"table must be contiguous float32 [max_pos, rot] on device {index}")
+    at = 0
     if positions is not None:
-        if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.device != device:
-            raise ValueError(f"positions must be contiguous int32 [axes, tokens] on {device}")
-        axes = int(positions.shape[0]) if positions.dim() > 1 else 1
+        if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != index:
+            raise ValueError(f"positions must be contiguous int32 [axes, tokens] on device {index}")
         if positions.numel() != axes * tokens:
             raise ValueError(f"positions must hold {tokens} tokens for each axis, got {tuple(positions.shape)}")
+        at = positions.data_ptr()
     if axes > FA_MAX_AXES:
         raise FAError(18, "rotation")
     if sections is None:
-        sections = (int(table.shape[1]) // 2,) if axes == 1 else ()
+        sections = (rot // 2,) if axes == 1 else ()
     if len(sections) != axes:
         raise ValueError(f"sections must give the pairs of each of the {axes} axes")
-    return _Rotation(table.data_ptr(), positions.data_ptr() if positions is not None else None, int(table.shape[1]),
-                     axes, (ctypes.c_int * FA_MAX_AXES)(*[int(x) for x in sections]), int(table.shape[0]),
-                     int(bool(interleaved)))
+    return _ROTATION.pack(table.data_ptr(), at, rot, axes, *sections, *(0,) * (FA_MAX_AXES - axes), rows,
+                          1 if interleaved else 0)
 
 
 def fa_rope(q, k, q_out, k_out, table, positions, sections=None, interleaved=False, inverse=False, stream=None):
@@ -567,34 +567,37 @@ def fa_rope(q, k, q_out, k_out, table, positions, sections=None, interleaved=Fal
     [max_pos, rot] holds cosines, then sines; ``positions`` int32 [axes, B, N] or [axes, N] on the
     device ([B, N] or [N] for one axis); ``sections`` the pairs of each axis. ``inverse`` turns
     backwards: the rotation's gradient."""
-    B, H, N, d, xs = _heads_view(q, "q")
-    dev = q.device
-    if positions is None:
-        raise TypeError("positions must be a tensor")
-    if positions.dim() == (2 if q.dim() == 4 else 1):
-        positions = positions.unsqueeze(0)
-    rope = _rotation(table, positions, sections, interleaved, B * N, dev)
-    args = []
+    index = q.get_device()
+    packed = []
+    first = None
     for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
         if t is None:
             if out is not None:
                 raise ValueError(f"{name}_out without {name}")
-            args.append(None)
+            packed.append(None)
             continue
-        tb, th, tn, td, ts = _heads_view(t, name)
-        ob, oh, on, od, os_ = _heads_view(out, name + "_out")
-        if t.dim() != q.dim() or (tb, tn, td) != (B, N, d) or out.shape != t.shape:
+        B, H, N, d, sb, sh, sn = _heads_view(t, name)
+        if first is None:
+            first = (B, N, d, t.dim())
+        if out is t:
+            ob, oh, on = sb, sh, sn
+        else:
+            ob, oh, on = _heads_view(out, name + "_out")[4:]
+        if (B, N, d, t.dim()) != first or out.shape != t.shape:
             raise ValueError(f"shape mismatch: {name} {tuple(t.shape)}, {name}_out {tuple(out.shape)}, "
                              f"q {tuple(q.shape)}")
-        if t.device != dev or out.device != dev:
+        if t.get_device() != index or out.get_device() != index:
             raise ValueError("every tensor must be on q's device")
-        if any(s == 0 and n > 1 for s, n in zip(os_, (ob, oh, on))):
+        if (ob == 0 and B > 1) or (oh == 0 and H > 1) or (on == 0 and N > 1):
             raise ValueError(f"{name}_out must not be an expanded tensor")
-        args.append(_RopeTensor(t.data_ptr(), out.data_ptr(), th, (ctypes.c_longlong * 3)(*ts),
-                                (ctypes.c_longlong * 3)(*os_)))
-    with _Launch(dev, stream) as handle:
-        st = load_library().fa_rope(ctypes.byref(args[0]), ctypes.byref(args[1]) if args[1] else None,
-                                    ctypes.byref(rope), B, N, d, int(bool(inverse)), handle)
+        packed.append(_ROPE_TENSOR.pack(t.data_ptr(), out.data_ptr(), H, sb, sh, sn, ob, oh, on))
+    B, N, d, dim = first
+    if positions is None:
+        raise TypeError("positions must be a tensor")
+    axes = positions.shape[0] if positions.dim() == dim - 1 else 1
+    rope = _rotation(table, positions, axes, sections, interleaved, B * N, index)
+    with _Launch(index, stream) as handle:
+        st = load_library().fa_rope(packed[0], packed[1], rope, B, N, d, 1 if inverse else 0, handle)
     _check(st, "fa_rope")
 
 
@@ -603,59 +606,72 @@ def rope(q, k, table, positions, sections=None, interleaved=False, inverse=False
     ``k`` is None."""
     import torch
 
-    make = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
-    q_out, k_out = make(q), None if k is None else make(k)
+    q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
     fa_rope(q, k, q_out, k_out, table, positions, sections, interleaved, inverse, stream)
-    if stream is not None:
-        _Launch(q.device, stream).used(q_out, k_out)
+    _used_on(stream, q_out, k_out)
     return q_out if k is None else (q_out, k_out)
 
 
-def _tokens_view(t, name, device, heads=None, d=None):
+def _tokens_view(t, name, index):
     """(tokens, heads, d, token stride) of a packed bf16 CUDA tensor [tokens, heads, d] whose heads
     and columns are contiguous (its tokens may be further apart)."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    if not t.is_cuda or t.device != device or t.dim() != 3 or t.numel() == 0:
-        raise ValueError(f"{name} must be a non-empty tensor [tokens, heads, d] on {device}")
-    n, h, w = t.shape
+    shape = t.shape
+    if len(shape) != 3 or not t.is_cuda or t.get_device() != index or 0 in shape:
+        raise ValueError(f"{name} must be a non-empty tensor [tokens, heads, d] on device {index}")
+    n, h, d = shape
     sn, sh, sd = t.stride()
-    if sd != 1 or (h > 1 and sh != w):
+    if sd != 1 or (h > 1 and sh != d):
         raise ValueError(f"{name}: heads and columns of a token must be contiguous")
-    if (heads is not None and h != heads) or (d is not None and w != d):
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    return n, h, w, sn if n > 1 else h * w
+    return n, h, d, sn if n > 1 else h * d
 
 
-def _cache_view(k_cache, v_cache, k_scale, v_scale, device):
+def _cache_view(k_cache, v_cache, k_scale, v_scale, index):
+    """(fa_paged_cache, Hkv, d) of a cache's tensors."""
     import torch
 
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache and v_cache must be [num_pages, Hkv, page_size, d], got {tuple(shape)} and "
+                         f"{tuple(v_cache.shape)}")
+    pages, heads, size, d = shape
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
             raise TypeError(f"{name} must hold e4m3 codes (uint8 or float8_e4m3fn), got {t.dtype}")
-        if t.dim() != 4 or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be contiguous [num_pages, Hkv, page_size, d] on {device}")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError(f"shape mismatch k_cache{tuple(k_cache.shape)} v_cache{tuple(v_cache.shape)}")
-    pages, heads, size, d = (int(x) for x in k_cache.shape)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(t, name, (pages, heads), torch.float32, device)
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
-                       size, d)
+        if not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name} must be contiguous on device {index}")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be float32, got {t.dtype}")
+        if tuple(t.shape) != (pages, heads) or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name} must be contiguous {(pages, heads)} on device {index}")
+    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                             heads, size, d), heads, d
 
 
-def _batch_view(page_table, cu_seqlens, seqlens_k, device):
+def _batch_view(page_table, cu_seqlens, seqlens_k, index):
+    """(B, max_pages) of a batch's device arrays."""
     import torch
 
-    for name, t, dim in (("page_table", page_table, 2), ("cu_seqlens", cu_seqlens, 1), ("seqlens_k", seqlens_k, 1)):
-        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
-            raise ValueError(f"{name} must be contiguous int32 with {dim} dimension(s) on {device}")
-    B = int(seqlens_k.shape[0])
-    if B < 1 or int(cu_seqlens.shape[0]) != B + 1 or int(page_table.shape[0]) != B:
+    for t, name in ((page_table, "page_table"), (cu_seqlens, "cu_seqlens"), (seqlens_k, "seqlens_k")):
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name} must be contiguous int32 on device {index}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    if B < 1 or tuple(cu_seqlens.shape) != (B + 1,) or tuple(seqlens_k.shape) != (B,):
         raise ValueError("page_table [B, max_pages], cu_seqlens [B+1] and seqlens_k [B] must agree on B >= 1")
-    return B, int(page_table.shape[1])
+    return B, max_pages
+
+
+def _check_out(t, name, shape, dtype, index):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be contiguous {shape} on device {index}, got {tuple(t.shape)}")
 
 
 def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
@@ -669,34 +685,32 @@ def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_ta
     them. ``table`` None: no rotation; ``positions`` None: the cache positions."""
     import torch
 
-    dev = k.device
-    n, hkv, d, ks = _tokens_view(k, "k", dev)
-    vn, _, _, vs = _tokens_view(v, "v", dev, hkv, d)
-    if vn != n:
-        raise ValueError("k and v must have the same tokens")
-    cache = _cache_view(k_cache, v_cache, k_scale, v_scale, dev)
-    if (cache.Hkv, cache.d) != (hkv, d):
-        raise ValueError(f"k has {hkv} heads of {d}, the cache {cache.Hkv} of {cache.d}")
-    B, max_pages = _batch_view(page_table, cu_seqlens, seqlens_k, dev)
-    H = qs = 0
+    index = k.get_device()
+    n, hkv, d, ks = _tokens_view(k, "k", index)
+    vn, vh, vd, vs = _tokens_view(v, "v", index)
+    cache, heads, width = _cache_view(k_cache, v_cache, k_scale, v_scale, index)
+    if (vn, vh, vd) != (n, hkv, d) or (heads, width) != (hkv, d):
+        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and a cache of {heads} heads of {width} do not agree")
+    B, max_pages = _batch_view(page_table, cu_seqlens, seqlens_k, index)
+    H = qs = qp = op = 0
     if q is not None:
-        qn, H, _, qs = _tokens_view(q, "q", dev, None, d)
-        if qn != n:
-            raise ValueError("q and k must have the same tokens")
-        _need(q_out, "q_out", (n, H, d), torch.bfloat16, dev)
+        qn, H, qd, qs = _tokens_view(q, "q", index)
+        if (qn, qd) != (n, d):
+            raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not agree")
+        _check_out(q_out, "q_out", (n, H, d), torch.bfloat16, index)
+        qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     rope = None
     if table is not None:
-        rope = _rotation(table, positions.view(1, -1) if positions is not None and positions.dim() == 1 else positions,
-                         sections, interleaved, n, dev)
+        axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
+        rope = _rotation(table, positions, axes, sections, interleaved, n, index)
     elif positions is not None:
         raise ValueError("positions without a table")
-    with _Launch(dev, stream) as handle:
-        st = load_library().fa_kv_append_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out),
-                                             ctypes.byref(rope) if rope else None, ctypes.byref(cache),
-                                             _ptr(page_table), _ptr(cu_seqlens), _ptr(seqlens_k), B, H, n,
-                                             int(max_seqlen), max_pages, qs, ks, vs, handle)
+    with _Launch(index, stream) as handle:
+        st = load_library().fa_kv_append_fp8(qp, k.data_ptr(), v.data_ptr(), op, rope, cache, page_table.data_ptr(),
+                                             cu_seqlens.data_ptr(), seqlens_k.data_ptr(), B, H, n, max_seqlen,
+                                             max_pages, qs, ks, vs, handle)
     _check(st, "fa_kv_append_fp8")
 
 
@@ -706,22 +720,21 @@ def kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     ``q``). Tokens past ``cu_seqlens[B]`` are left as allocated."""
     import torch
 
-    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
                      max_seqlen, table, positions, sections, interleaved, stream)
-    if stream is not None:
-        _Launch(k.device, stream).used(q_out)
+    _used_on(stream, q_out)
     return q_out
 
 
 def fa_paged_num_splits(B: int, H: int, Hkv: int, max_seqlen_q: int, max_seqlen_k: int, d: int, window: int = 0,
                         sinks: int = 0) -> int:
     """The key splits the library proposes for a paged call (0 for arguments out of range)."""
-    return int(load_library().fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks))
+    return load_library().fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks)
 
 
 def fa_paged_workspace_bytes(total_q: int, H: int, d: int, num_splits: int) -> int:
-    return int(load_library().fa_paged_workspace_bytes(total_q, H, d, num_splits))
+    return load_library().fa_paged_workspace_bytes(total_q, H, d, num_splits)
 
 
 def fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k,
@@ -733,28 +746,26 @@ def fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, 
     ``num_splits > 1``."""
     import torch
 
-    dev = q.device
-    if q.dtype != torch.bfloat16:
-        raise TypeError(f"q must be bfloat16, got {q.dtype}")
-    if q.dim() != 3 or not q.is_contiguous() or not q.is_cuda:
-        raise ValueError("q must be a contiguous CUDA tensor [total_q, H, d]")
-    n, H, d = q.shape
-    cache = _cache_view(k_cache, v_cache, k_scale, v_scale, dev)
-    if cache.d != d:
-        raise ValueError(f"q has head dim {d}, the cache {cache.d}")
-    B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, dev)
-    _need(o, "o", (n, H, d), torch.bfloat16, dev)
-    _need(lse, "lse", (H, n), torch.float32, dev)
-    num_splits = int(num_splits)
+    index = q.get_device()
+    n, H, d, qs = _tokens_view(q, "q", index)
+    if qs != H * d:
+        raise ValueError("q must be contiguous")
+    cache, _, width = _cache_view(k_cache, v_cache, k_scale, v_scale, index)
+    if width != d:
+        raise ValueError(f"q has head dim {d}, the cache {width}")
+    B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, index)
+    _check_out(o, "o", (n, H, d), torch.bfloat16, index)
+    _check_out(lse, "lse", (H, n), torch.float32, index)
+    ws = 0
     if num_splits > 1:
-        _need_workspace(workspace, fa_paged_workspace_bytes(n, H, d, num_splits), "workspace", dev)
-    scale = default_scale(d) if scale is None else float(scale)
-    with _Launch(dev, stream) as handle:
-        st = load_library().fa_fwd_paged_fp8(_ptr(q), ctypes.byref(cache), _ptr(page_table), _ptr(cu_seqlens_q),
-                                             _ptr(seqlens_k), _ptr(o), _ptr(lse),
-                                             _ptr(workspace if num_splits > 1 else None), B, H, n,
-                                             int(max_seqlen_q), int(max_seqlen_k), max_pages, scale, int(window),
-                                             int(sinks), num_splits, handle)
+        _need_workspace(workspace, fa_paged_workspace_bytes(n, H, d, num_splits), "workspace", q.device)
+        ws = workspace.data_ptr()
+    with _Launch(index, stream) as handle:
+        st = load_library().fa_fwd_paged_fp8(q.data_ptr(), cache, page_table.data_ptr(), cu_seqlens_q.data_ptr(),
+                                             seqlens_k.data_ptr(), o.data_ptr(), lse.data_ptr(), ws, B, H, n,
+                                             max_seqlen_q, max_seqlen_k, max_pages,
+                                             default_scale(d) if scale is None else scale, window, sinks,
+                                             num_splits, handle)
     _check(st, "fa_fwd_paged_fp8")
 
 
@@ -768,16 +779,16 @@ def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
 
     n, H, d = q.shape
     if num_splits is None:
-        num_splits = fa_paged_num_splits(int(seqlens_k.shape[0]), H, int(k_cache.shape[1]), int(max_seqlen_q),
-                                         int(max_seqlen_k), d, int(window), int(sinks)) or 1
-    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        num_splits = fa_paged_num_splits(seqlens_k.shape[0], H, k_cache.shape[1], max_seqlen_q, max_seqlen_k, d, window,
+                                         sinks) or 1
+    o = torch.empty_like(q)
     lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
-    nbytes = fa_paged_workspace_bytes(n, H, d, num_splits)
-    ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device) if nbytes else None
+    ws = None
+    if num_splits > 1:
+        ws = torch.empty(fa_paged_workspace_bytes(n, H, d, num_splits) // 4, dtype=torch.float32, device=q.device)
     fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
                      max_seqlen_k, ws, num_splits, window, sinks, scale, stream)
-    if stream is not None:
-        _Launch(q.device, stream).used(o, lse, ws)
+    _used_on(stream, o, lse, ws)
     return o, lse
 
 
@@ -785,29 +796,34 @@ def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
 def _grouped(q, k, v):
     import torch
 
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16:
+    index = q.get_device()
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
         if t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
             raise ValueError(f"{name} must be a contiguous CUDA tensor [B, H, N, d]")
-    if k.device != q.device or v.device != q.device:
-        raise ValueError("q, k and v must be on the same device")
+        if t.get_device() != index:
+            raise ValueError("q, k and v must be on the same device")
     B, H, Nq, d = q.shape
-    if k.shape[0] != B or k.shape[3] != d or v.shape != k.shape:
+    Bk, Hkv, Nk, dk = k.shape
+    if (Bk, dk) != (B, d) or v.shape != k.shape:
         raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
-    return B, H, k.shape[1], Nq, k.shape[2], d
+    return B, H, Hkv, Nq, Nk, d, index
 
 
 def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | None = None, stream=None):
     """Sliding-window forward with sinks into caller-owned ``o`` (bf16 [B,H,Nq,d]) and ``lse`` (fp32
     [B,H,Nq]); ``k`` and ``v`` [B,Hkv,Nk,d], H a multiple of Hkv (include/fa.h, fa_fwd_window).
     ``window`` 0: no window, the bottom-right causal mask."""
-    B, H, Hkv, Nq, Nk, d = _grouped(q, k, v)
-    _need_o_lse(o, lse, B, H, Nq, d, q.device)
-    scale = default_scale(d) if scale is None else float(scale)
-    with _Launch(q.device, stream) as handle:
-        st = load_library().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, Nq, Nk, d, scale,
-                                          int(window), int(sinks), handle)
+    import torch
+
+    B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
+    _check_out(o, "o", (B, H, Nq, d), torch.bfloat16, index)
+    _check_out(lse, "lse", (B, H, Nq), torch.float32, index)
+    with _Launch(index, stream) as handle:
+        st = load_library().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H,
+                                          Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale, window, sinks,
+                                          handle)
     _check(st, "fa_fwd_window")
 
 
@@ -815,16 +831,15 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
     """Allocate ``o`` and ``lse`` and run :func:`fa_fwd_window`. Returns ``(o, lse)``."""
     import torch
 
-    o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    o = torch.empty_like(q)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
-    if stream is not None:
-        _Launch(q.device, stream).used(o, lse)
+    _used_on(stream, o, lse)
     return o, lse
 
 
 def fa_bwd_window_workspace_bytes(B: int, H: int, Nq: int, d: int) -> int:
-    return int(load_library().fa_bwd_window_workspace_bytes(B, H, Nq, d))
+    return load_library().fa_bwd_window_workspace_bytes(B, H, Nq, d)
 
 
 def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
@@ -833,17 +848,16 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
     k, v); ``workspace`` fp32 of at least ``fa_bwd_window_workspace_bytes`` bytes."""
     import torch
 
-    B, H, Hkv, Nq, Nk, d = _grouped(q, k, v)
-    dev = q.device
+    B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
     for t, name, like in ((o, "o", q), (dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
-        _need(t, name, like.shape, torch.bfloat16, dev)
-    _need(lse, "lse", (B, H, Nq), torch.float32, dev)
-    _need_workspace(workspace, fa_bwd_window_workspace_bytes(B, H, Nq, d), "workspace", dev)
-    scale = default_scale(d) if scale is None else float(scale)
-    with _Launch(dev, stream) as handle:
-        st = load_library().fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq),
-                                          _ptr(dk), _ptr(dv), _ptr(workspace), B, H, Hkv, Nq, Nk, d, scale,
-                                          int(window), int(sinks), handle)
+        _check_out(t, name, tuple(like.shape), torch.bfloat16, index)
+    _check_out(lse, "lse", (B, H, Nq), torch.float32, index)
+    _need_workspace(workspace, fa_bwd_window_workspace_bytes(B, H, Nq, d), "workspace", q.device)
+    with _Launch(index, stream) as handle:
+        st = load_library().fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                                          lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                          workspace.data_ptr(), B, H, Hkv, Nq, Nk, d,
+                                          default_scale(d) if scale is None else scale, window, sinks, handle)
     _check(st, "fa_bwd_window")
 
 
@@ -852,12 +866,11 @@ def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0
     """Allocate ``(dq, dk, dv)`` and the workspace and run :func:`fa_bwd_window`."""
     import torch
 
-    B, H, Hkv, Nq, Nk, d = _grouped(q, k, v)
+    B, H, _, Nq, _, d, _ = _grouped(q, k, v)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws = torch.empty(max(1, fa_bwd_window_workspace_bytes(B, H, Nq, d) // 4), dtype=torch.float32, device=q.device)
     fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, ws, window, sinks, scale, stream)
-    if stream is not None:
-        _Launch(q.device, stream).used(dq, dk, dv, ws)
+    _used_on(stream, dq, dk, dv, ws)
     return dq, dk, dv
 
 

@@ -61,9 +61,6 @@ namespace {
 constexpr int kRows = 16;      // query rows per CTA
 constexpr int kKeys = 32;      // keys per warp tile
 constexpr int kWarps = 4;
-constexpr float kPShift = 10.f;  // p = 2^(x - m + 10)
-constexpr float kPSlack = 4.f;   // the reference moves when x passes it by more
-
 template <int D>
 struct PagedLayout {
     static constexpr int ROW_BYTES = D < 128 ? D : 128;  // bytes of a swizzled row
@@ -83,46 +80,6 @@ struct PagedLayout {
     static_assert(TILE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
 };
 
-struct PagedParams {
-    CUtensorMap tm_k, tm_v;  // e4m3 [num_pages * Hkv * page_size][d], box {row part, min(page_size, 32)}
-    const __nv_bfloat16* q;  // [total_q][H][d]
-    __nv_bfloat16* o;
-    float* lse;              // [H][total_q]
-    const float* k_scale;    // [num_pages][Hkv]
-    const float* v_scale;
-    const int* page_table;   // [B][max_pages]
-    const int* cu;
-    const int* lens;
-    float* ws_o;             // [splits][total_q * H][d]
-    float* ws_m;             // base-2 units of the scaled score
-    float* ws_l;
-    int B, H, Hkv, G, total_q, max_q, max_k, num_pages, log_page, max_pages;
-    int window, sinks;
-    int row_blocks, num_splits, tiles_per_split;
-    float scale_log2;
-    long long wait_limit;
-    unsigned* status;
-};
-
-// The key tiles a row block visits, as a list: tiles 0 .. ns - 1 (sinks), then
-// tile `lo` on, n in all. Positions p0 .. p1 are the block's first and last.
-struct KeyList {
-    int ns, lo, n;
-    __device__ __forceinline__ int tile(int i) const { return i < ns ? i : lo + (i - ns); }
-};
-__device__ __forceinline__ KeyList key_list(int window, int sinks, int p0, int p1) {
-    KeyList k;
-    const int end = p1 < 0 ? 0 : p1 / kKeys + 1;
-    k.ns = 0, k.lo = 0;
-    if (window > 0) {
-        const int first = max(0, p0 - window + 1) / kKeys;
-        const int st = min((sinks + kKeys - 1) / kKeys, end);
-        if (first > st) k.ns = st, k.lo = first;
-    }
-    k.n = k.ns + max(0, end - k.lo);
-    return k;
-}
-
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, long long limit, unsigned* status,
                                              unsigned what) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -134,14 +91,6 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, long
         }
     }
     return true;
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -163,12 +112,6 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t (&r)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Byte offset of 16-byte unit `unit` of key row `row` in a swizzled tile: rows
 // of 128 bytes (units XOR row mod 8; further row parts 32 rows behind), or of
 // 64 bytes (units XOR row / 2 mod 4).
@@ -229,7 +172,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
     const int start = nt.len - nt.n;  // position of the first query
     const int p0 = start + r0 / p.G;
     const int p1 = start + (min(r0 + kRows, rows) - 1) / p.G;
-    const KeyList list = key_list(p.window, p.sinks, p0, p1);
+    const KeyList list = key_list<kKeys>(p.window, p.sinks, p0, p1);
     const int used = max(1, (list.n + p.tiles_per_split - 1) / p.tiles_per_split);
     if (split >= used) return;
     const int i0 = split * p.tiles_per_split;
@@ -591,10 +534,11 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     if (b >= p.B || !new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt) || i >= nt.n) return;
     // The row block of this row decides how many splits it used.
     const int r = i * p.G + head % p.G;
-    const int r0 = r / kRows * kRows, rows = nt.n * p.G;
+    const int r0 = r / p.block_rows * p.block_rows, rows = nt.n * p.G;
     const int start = nt.len - nt.n;
-    const KeyList list =
-        key_list(p.window, p.sinks, start + r0 / p.G, start + (min(r0 + kRows, rows) - 1) / p.G);
+    const int p0 = start + r0 / p.G, p1 = start + (min(r0 + p.block_rows, rows) - 1) / p.G;
+    const KeyList list = p.block_keys == kTcKeys ? key_list<kTcKeys>(p.window, p.sinks, p0, p1)
+                                                 : key_list<kKeys>(p.window, p.sinks, p0, p1);
     const int used = (list.n + p.tiles_per_split - 1) / p.tiles_per_split;
     if (used <= 1) return;
     const long long row = static_cast<long long>(nt.first + i) * p.H + head;
@@ -646,13 +590,28 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int d, long long rows,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Most key tiles a row block can list.
-long long most_tiles(int max_q, int max_k, int window, int sinks) {
-    const long long all = (static_cast<long long>(max_k) + kKeys - 1) / kKeys;
-    if (window <= 0) return all;
-    const long long part = (static_cast<long long>(window) + std::min(max_q, kRows) + kKeys - 1) / kKeys + 1 +
-                           (static_cast<long long>(sinks) + kKeys - 1) / kKeys;
-    return std::min(all, part);
+// How a call is cut: by the tensor-core kernel of fa_paged_tc.cu, or by this
+// file's.
+struct Plan {
+    bool tc;
+    int block_rows, block_keys;
+    long long row_blocks;
+    long long tiles;  // most key tiles a row block can list
+};
+Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
+    Plan c;
+    const long long rows = static_cast<long long>(max_q) * G;
+    c.tc = d <= 128 && rows > kRows;
+    c.block_rows = c.tc ? kTcRows : kRows;
+    c.block_keys = c.tc ? kTcKeys : kKeys;
+    c.row_blocks = (rows + c.block_rows - 1) / c.block_rows;
+    const long long K = c.block_keys;
+    c.tiles = (max_k + K - 1) / K;
+    if (window > 0) {
+        const long long span = std::min(max_q, c.block_rows);  // tokens a block's rows can cover
+        c.tiles = std::min(c.tiles, (window + span + K - 1) / K + 1 + (sinks + K - 1) / K);
+    }
+    return c;
 }
 
 template <int D>
@@ -660,7 +619,7 @@ cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
     using L = PagedLayout<D>;
     static ContextCache<int> attr_set;
     int done = 0;
-    cudaError_t e = attr_set.get(&done, [](int* out) {
+    const cudaError_t e = attr_set.get(&done, [](int* out) {
         *out = 1;
         return cudaFuncSetAttribute(fa_paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC));
@@ -668,8 +627,12 @@ cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    e = launch_dependent(fa_paged_rows_kernel<D>, dim3(static_cast<unsigned>(ctas)), kWarps * 32, L::ALLOC, stream, p);
-    if (e != cudaSuccess || p.num_splits == 1) return e;
+    return launch_dependent(fa_paged_rows_kernel<D>, dim3(static_cast<unsigned>(ctas)), kWarps * 32, L::ALLOC, stream,
+                            p);
+}
+
+template <int D>
+cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     const long long blocks = (static_cast<long long>(p.B) * p.max_q * p.H + 3) / 4;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_paged_merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), 128, 0, stream, p);
@@ -682,11 +645,15 @@ extern "C" {
 
 int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k, int d, int window, int sinks) {
     if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || !fa::valid_d(d)) return 0;
-    const long long rows = static_cast<long long>(max_seqlen_q) * (H / Hkv);
-    const long long units = static_cast<long long>(B) * Hkv * ((rows + fa::kRows - 1) / fa::kRows);
-    const long long tiles = fa::most_tiles(max_seqlen_q, max_seqlen_k, window, sinks);
+    const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
+    const long long units = static_cast<long long>(B) * Hkv * c.row_blocks;
+    if (c.tc) {
+        // One CTA per SM: split only while the units leave SMs idle.
+        const long long fill = 152 / units;
+        return static_cast<int>(std::max(1ll, std::min({fill, c.tiles / 4, static_cast<long long>(FA_MAX_SPLITS)})));
+    }
     const long long want = (4ll * 304 + units - 1) / units;         // CTAs for four waves of two per SM
-    const long long most = std::max(1ll, tiles / (2 * fa::kWarps)); // two tiles per warp at least
+    const long long most = std::max(1ll, c.tiles / (2 * fa::kWarps)); // two tiles per warp at least
     return static_cast<int>(std::max(1ll, std::min({want, most, static_cast<long long>(FA_MAX_SPLITS)})));
 }
 
@@ -722,7 +689,8 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     fa::PagedParams p;
     std::memset(&p, 0, sizeof(p));
     const long long rows = static_cast<long long>(cache->num_pages) * Hkv * cache->page_size;
-    const int box = std::min(cache->page_size, fa::kKeys);
+    const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
+    const int box = c.tc ? cache->page_size : std::min(cache->page_size, fa::kKeys);
     if (!fa::encode_cache_map(&p.tm_k, cache->k, d, rows, box) || !fa::encode_cache_map(&p.tm_v, cache->v, d, rows, box))
         return FA_ERR_CUDA;
     p.q = static_cast<const __nv_bfloat16*>(q);
@@ -751,16 +719,21 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     p.max_pages = max_pages;
     p.window = window;
     p.sinks = sinks;
-    p.row_blocks = static_cast<int>((static_cast<long long>(max_seqlen_q) * p.G + fa::kRows - 1) / fa::kRows);
+    p.block_rows = c.block_rows;
+    p.block_keys = c.block_keys;
+    p.row_blocks = static_cast<int>(c.row_blocks);
     p.num_splits = num_splits;
-    const long long tiles = fa::most_tiles(max_seqlen_q, max_seqlen_k, window, sinks);
-    p.tiles_per_split = static_cast<int>((tiles + num_splits - 1) / num_splits);
+    p.tiles_per_split = static_cast<int>((c.tiles + num_splits - 1) / num_splits);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit = fa::kDefaultWaitLimit;
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-    const cudaError_t e = d == 64    ? fa::launch_paged<64>(p, stream)
-                          : d == 128 ? fa::launch_paged<128>(p, stream)
-                                     : fa::launch_paged<256>(p, stream);
+    cudaError_t e = c.tc       ? fa::launch_paged_tc(p, d, stream)
+                    : d == 64  ? fa::launch_paged<64>(p, stream)
+                    : d == 128 ? fa::launch_paged<128>(p, stream)
+                               : fa::launch_paged<256>(p, stream);
+    if (e == cudaSuccess && num_splits > 1)
+        e = d == 64 ? fa::launch_merge<64>(p, stream)
+                    : d == 128 ? fa::launch_merge<128>(p, stream) : fa::launch_merge<256>(p, stream);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

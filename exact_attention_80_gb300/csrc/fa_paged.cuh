@@ -2,6 +2,7 @@
 // attention over it.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "fa_internal.h"
@@ -51,8 +52,72 @@ __device__ __forceinline__ bool new_tokens(const int* cu, const int* lens, int b
     return ok;
 }
 
+constexpr float kPShift = 10.f;  // p = 2^(x - m + 10)
+constexpr float kPSlack = 4.f;   // the reference moves when x passes it by more
+
+
+struct PagedParams {
+    CUtensorMap tm_k, tm_v;  // e4m3 [num_pages * Hkv * page_size][d], box {row part, keys per copy}
+    const __nv_bfloat16* q;  // [total_q][H][d]
+    __nv_bfloat16* o;
+    float* lse;              // [H][total_q]
+    const float* k_scale;    // [num_pages][Hkv]
+    const float* v_scale;
+    const int* page_table;   // [B][max_pages]
+    const int* cu;
+    const int* lens;
+    float* ws_o;             // [splits][total_q * H][d]
+    float* ws_m;             // base-2 units of the scaled score
+    float* ws_l;
+    int B, H, Hkv, G, total_q, max_q, max_k, num_pages, log_page, max_pages;
+    int window, sinks;
+    int row_blocks, num_splits, tiles_per_split;  // row blocks of block_rows rows, tiles of block_keys keys
+    int block_rows, block_keys;
+    float scale_log2;
+    long long wait_limit;
+    unsigned* status;
+};
+
+// The key tiles a row block visits, as a list: tiles 0 .. ns - 1 (sinks), then
+// tile `lo` on, n in all. Positions p0 .. p1 are the block's first and last.
+struct KeyList {
+    int ns, lo, n;
+    __device__ __forceinline__ int tile(int i) const { return i < ns ? i : lo + (i - ns); }
+};
+template <int KEYS>
+__device__ __forceinline__ KeyList key_list(int window, int sinks, int p0, int p1) {
+    KeyList k;
+    const int end = p1 < 0 ? 0 : p1 / KEYS + 1;
+    k.ns = 0, k.lo = 0;
+    if (window > 0) {
+        const int first = max(0, p0 - window + 1) / KEYS;
+        const int st = min((sinks + KEYS - 1) / KEYS, end);
+        if (first > st) k.ns = st, k.lo = first;
+    }
+    k.n = k.ns + max(0, end - k.lo);
+    return k;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Host side (fa_paged.cu): checks a cache's description.
 fa_status check_cache(const fa_paged_cache* cache);
+// The kernel for many query rows (fa_paged_tc.cu): rows per unit, keys per tile.
+constexpr int kTcRows = 256;
+constexpr int kTcKeys = 128;
+cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream);
 inline int log2_exact(int x) {
     int n = 0;
     while ((1 << n) < x) ++n;

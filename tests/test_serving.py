@@ -337,6 +337,16 @@ PAGED = [
     ([100, 70], [400, 70], 64, 4, 2, 128, 0, 0, None),
     ([130, 17], [130, 500], 16, 3, 1, 256, 64, 1, 2),
     ([200], [777], 128, 10, 2, 64, 300, 33, None),
+    # many query rows: row tiles of 128, key tiles of 128
+    ([300, 17, 64], [1000, 17, 500], 16, 8, 2, 128, 0, 0, 3),
+    ([64, 200], [640, 200], 32, 8, 1, 64, 0, 0, 2),
+    ([257, 130], [1500, 131], 64, 2, 2, 128, 0, 0, None),
+    ([257, 1], [1500, 640], 64, 4, 2, 64, 130, 4, None),
+    ([40, 300], [1300, 900], 16, 16, 2, 128, 200, 140, 2),
+    ([513], [513], 128, 1, 1, 128, 1, 0, None),
+    ([3, 3, 3], [1000, 128, 129], 128, 64, 1, 128, 0, 0, 8),
+    ([20, 33], [2000, 4000], 32, 12, 4, 64, 0, 0, 16),
+    ([1, 1], [2000, 300], 32, 64, 2, 128, 0, 0, None),
 ]
 
 
