@@ -93,7 +93,7 @@ def load_library() -> ctypes.CDLL:
     lib.fa_fwd_paged_fp8.restype = i
     lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
     lib.fa_fwd_window.restype = i
-    lib.fa_bwd_window_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_bwd_window_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
     lib.fa_bwd_window_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
     lib.fa_bwd_window.restype = i
@@ -474,33 +474,22 @@ def _raw_stream(index):
     return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-class _Launch:
-    """The stream of one call on device ``index``: ``stream``, or the device's
-    current one. As a context it makes that device the current one while the
-    library launches and yields the stream's handle."""
+def _on_stream(index, stream, fn, *args):
+    """``fn(*args, handle)`` on device ``index`` and ``stream`` (None: the
+    device's current stream), that device being the current one meanwhile."""
+    import torch
 
-    __slots__ = ("index", "stream", "guard")
-
-    def __init__(self, index, stream):
-        self.index = index
-        self.stream = stream
+    if stream is None:
+        if torch.cuda.current_device() == index:
+            return fn(*args, _raw_stream(index))
+    else:
         on = getattr(stream, "device", None)
         if on is not None and on.index != index:
             raise ValueError(f"stream is on {on}, the tensors on device {index}")
-
-    def __enter__(self):
-        import torch
-
-        self.guard = None
-        if self.index >= 0 and torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        st = self.stream
-        return _raw_stream(self.index) if st is None else int(getattr(st, "cuda_stream", st))
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+    if index < 0:  # no device to make current
+        return fn(*args, _raw_stream(index) if stream is None else int(getattr(stream, "cuda_stream", stream)))
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index) if stream is None else int(getattr(stream, "cuda_stream", stream)))
 
 
 def _used_on(stream, *tensors):
@@ -523,15 +512,17 @@ def _heads_view(t, name):
 
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bfloat16 tensor")
-    shape, strides = t.shape, t.stride()
-    if len(shape) == 4:
-        (B, H, N, d), (sb, sh, sn, sd) = shape, strides
-    elif len(shape) == 3:
-        (N, H, d), (sn, sh, sd) = shape, strides
+    dim = t.dim()
+    if dim == 4:
+        B, H, N, d = t.shape
+        sb, sh, sn, sd = t.stride()
+    elif dim == 3:
+        N, H, d = t.shape
+        sn, sh, sd = t.stride()
         B, sb = 1, 0
     else:
         sd = 0
-    if sd != 1 or not t.is_cuda or 0 in shape:
+    if sd != 1 or not t.is_cuda or B * H * N * d == 0:
         raise ValueError(f"{name} must be a non-empty CUDA tensor [B, H, N, d] or [N, H, d] with contiguous columns")
     return B, H, N, d, sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0
 
@@ -560,6 +551,48 @@ def _rotation(table, positions, axes, sections, interleaved, tokens, index):
                           1 if interleaved else 0)
 
 
+def _rope(q, k, q_out, k_out, table, positions, sections, interleaved, inverse, stream):
+    """The checks and the call of fa_rope; outputs None are allocated."""
+    import torch
+
+    index = q.get_device()
+    B, H, N, d, sb, sh, sn = _heads_view(q, "q")
+    dim = q.dim()
+    outs, packed = [], []
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out without {name}")
+            outs.append(None)
+            packed.append(None)
+            continue
+        if t is not q:
+            Bk, H, Nk, dk, sb, sh, sn = _heads_view(t, name)
+            if (Bk, Nk, dk) != (B, N, d) or t.dim() != dim or t.get_device() != index:
+                raise ValueError(f"shape or device mismatch: {name} {tuple(t.shape)}, q {tuple(q.shape)}")
+        if out is None:
+            out = torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+            ob, oh, on = (H * N * d, N * d, d) if dim == 4 else (0, d, H * d)
+        elif out is t:
+            ob, oh, on = sb, sh, sn
+        else:
+            if out.shape != t.shape or out.get_device() != index:
+                raise ValueError(f"{name}_out must have {name}'s shape {tuple(t.shape)} and device")
+            ob, oh, on = _heads_view(out, name + "_out")[4:]
+        if (ob == 0 and B > 1) or (oh == 0 and H > 1) or (on == 0 and N > 1):
+            raise ValueError(f"{name}_out must not be an expanded tensor")
+        outs.append(out)
+        packed.append(_ROPE_TENSOR.pack(t.data_ptr(), out.data_ptr(), H, sb, sh, sn, ob, oh, on))
+    if positions is None:
+        raise TypeError("positions must be a tensor")
+    axes = positions.shape[0] if positions.dim() == dim - 1 else 1
+    rope = _rotation(table, positions, axes, sections, interleaved, B * N, index)
+    st = _on_stream(index, stream, load_library().fa_rope, packed[0], packed[1], rope, B, N, d, 1 if inverse else 0)
+    if st != FA_OK:
+        raise FAError(st, "fa_rope")
+    return outs
+
+
 def fa_rope(q, k, q_out, k_out, table, positions, sections=None, interleaved=False, inverse=False, stream=None):
     """Rotates ``q`` and ``k`` (or ``q`` alone: ``k`` and ``k_out`` None) into caller-owned outputs
     (include/fa.h, fa_rope). Tensors are bf16 [B, H, N, d] or [N, H, d], of any strides that are
@@ -567,48 +600,17 @@ def fa_rope(q, k, q_out, k_out, table, positions, sections=None, interleaved=Fal
     [max_pos, rot] holds cosines, then sines; ``positions`` int32 [axes, B, N] or [axes, N] on the
     device ([B, N] or [N] for one axis); ``sections`` the pairs of each axis. ``inverse`` turns
     backwards: the rotation's gradient."""
-    index = q.get_device()
-    packed = []
-    first = None
-    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if t is None:
-            if out is not None:
-                raise ValueError(f"{name}_out without {name}")
-            packed.append(None)
-            continue
-        B, H, N, d, sb, sh, sn = _heads_view(t, name)
-        if first is None:
-            first = (B, N, d, t.dim())
-        if out is t:
-            ob, oh, on = sb, sh, sn
-        else:
-            ob, oh, on = _heads_view(out, name + "_out")[4:]
-        if (B, N, d, t.dim()) != first or out.shape != t.shape:
-            raise ValueError(f"shape mismatch: {name} {tuple(t.shape)}, {name}_out {tuple(out.shape)}, "
-                             f"q {tuple(q.shape)}")
-        if t.get_device() != index or out.get_device() != index:
-            raise ValueError("every tensor must be on q's device")
-        if (ob == 0 and B > 1) or (oh == 0 and H > 1) or (on == 0 and N > 1):
-            raise ValueError(f"{name}_out must not be an expanded tensor")
-        packed.append(_ROPE_TENSOR.pack(t.data_ptr(), out.data_ptr(), H, sb, sh, sn, ob, oh, on))
-    B, N, d, dim = first
-    if positions is None:
-        raise TypeError("positions must be a tensor")
-    axes = positions.shape[0] if positions.dim() == dim - 1 else 1
-    rope = _rotation(table, positions, axes, sections, interleaved, B * N, index)
-    with _Launch(index, stream) as handle:
-        st = load_library().fa_rope(packed[0], packed[1], rope, B, N, d, 1 if inverse else 0, handle)
-    _check(st, "fa_rope")
+    if q_out is None or (k is not None and k_out is None):
+        raise TypeError("outputs must be tensors")
+    _rope(q, k, q_out, k_out, table, positions, sections, interleaved, inverse, stream)
 
 
 def rope(q, k, table, positions, sections=None, interleaved=False, inverse=False, stream=None):
-    """Allocate outputs and run :func:`fa_rope`. Returns ``(q_out, k_out)``, or ``q_out`` where
+    """:func:`fa_rope` into new contiguous outputs. Returns ``(q_out, k_out)``, or ``q_out`` where
     ``k`` is None."""
-    import torch
-
-    q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
-    fa_rope(q, k, q_out, k_out, table, positions, sections, interleaved, inverse, stream)
-    _used_on(stream, q_out, k_out)
+    q_out, k_out = _rope(q, k, None, None, table, positions, sections, interleaved, inverse, stream)
+    if stream is not None:
+        _used_on(stream, q_out, k_out)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -674,15 +676,9 @@ def _check_out(t, name, shape, dtype, index):
         raise ValueError(f"{name} must be contiguous {shape} on device {index}, got {tuple(t.shape)}")
 
 
-def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
-                     max_seqlen: int, table=None, positions=None, sections=None, interleaved=False, stream=None):
-    """Appends keys (rotated) and values to a paged e4m3 cache in place and rotates the queries
-    (include/fa.h, fa_kv_append_fp8). ``q`` [total, H, d] into ``q_out`` (both may be None), ``k`` and
-    ``v`` bf16 [total, Hkv, d], whose tokens may be strided (a fused projection's rows); ``k_cache``
-    and ``v_cache`` [num_pages, Hkv, page_size, d] e4m3 codes, ``k_scale`` and ``v_scale`` fp32
-    [num_pages, Hkv]; ``page_table`` int32 [B, max_pages], ``cu_seqlens`` int32 [B+1] of the new
-    tokens (``max_seqlen`` the most of a sequence), ``seqlens_k`` int32 [B] the cache lengths with
-    them. ``table`` None: no rotation; ``positions`` None: the cache positions."""
+def _append(q, k, v, q_out, make, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k, max_seqlen,
+            table, positions, sections, interleaved, stream):
+    """The checks and the call of fa_kv_append_fp8; ``make``: allocate q_out."""
     import torch
 
     index = k.get_device()
@@ -697,7 +693,10 @@ def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_ta
         qn, H, qd, qs = _tokens_view(q, "q", index)
         if (qn, qd) != (n, d):
             raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not agree")
-        _check_out(q_out, "q_out", (n, H, d), torch.bfloat16, index)
+        if make:
+            q_out = torch.empty((n, H, d), dtype=torch.bfloat16, device=q.device)
+        else:
+            _check_out(q_out, "q_out", (n, H, d), torch.bfloat16, index)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -707,23 +706,35 @@ def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_ta
         rope = _rotation(table, positions, axes, sections, interleaved, n, index)
     elif positions is not None:
         raise ValueError("positions without a table")
-    with _Launch(index, stream) as handle:
-        st = load_library().fa_kv_append_fp8(qp, k.data_ptr(), v.data_ptr(), op, rope, cache, page_table.data_ptr(),
-                                             cu_seqlens.data_ptr(), seqlens_k.data_ptr(), B, H, n, max_seqlen,
-                                             max_pages, qs, ks, vs, handle)
-    _check(st, "fa_kv_append_fp8")
+    st = _on_stream(index, stream, load_library().fa_kv_append_fp8, qp, k.data_ptr(), v.data_ptr(), op, rope, cache,
+                    page_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), B, H, n, max_seqlen, max_pages,
+                    qs, ks, vs)
+    if st != FA_OK:
+        raise FAError(st, "fa_kv_append_fp8")
+    return q_out
+
+
+def fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
+                     max_seqlen: int, table=None, positions=None, sections=None, interleaved=False, stream=None):
+    """Appends keys (rotated) and values to a paged e4m3 cache in place and rotates the queries
+    (include/fa.h, fa_kv_append_fp8). ``q`` [total, H, d] into ``q_out`` (both may be None), ``k`` and
+    ``v`` bf16 [total, Hkv, d], whose tokens may be strided (a fused projection's rows); ``k_cache``
+    and ``v_cache`` [num_pages, Hkv, page_size, d] e4m3 codes, ``k_scale`` and ``v_scale`` fp32
+    [num_pages, Hkv]; ``page_table`` int32 [B, max_pages], ``cu_seqlens`` int32 [B+1] of the new
+    tokens (``max_seqlen`` the most of a sequence), ``seqlens_k`` int32 [B] the cache lengths with
+    them. ``table`` None: no rotation; ``positions`` None: the cache positions."""
+    _append(q, k, v, q_out, False, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k, max_seqlen,
+            table, positions, sections, interleaved, stream)
 
 
 def kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k, max_seqlen: int,
                   table=None, positions=None, sections=None, interleaved=False, stream=None):
-    """Allocate the rotated queries and run :func:`fa_kv_append_fp8`; returns them (None without
-    ``q``). Tokens past ``cu_seqlens[B]`` are left as allocated."""
-    import torch
-
-    q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    fa_kv_append_fp8(q, k, v, q_out, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
-                     max_seqlen, table, positions, sections, interleaved, stream)
-    _used_on(stream, q_out)
+    """:func:`fa_kv_append_fp8` into new rotated queries; returns them (None without ``q``). Tokens
+    past ``cu_seqlens[B]`` are left as allocated."""
+    q_out = _append(q, k, v, None, True, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
+                    max_seqlen, table, positions, sections, interleaved, stream)
+    if stream is not None:
+        _used_on(stream, q_out)
     return q_out
 
 
@@ -737,6 +748,44 @@ def fa_paged_workspace_bytes(total_q: int, H: int, d: int, num_splits: int) -> i
     return load_library().fa_paged_workspace_bytes(total_q, H, d, num_splits)
 
 
+def _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+           max_seqlen_k, workspace, num_splits, window, sinks, scale, stream):
+    """The checks and the call of fa_fwd_paged_fp8; ``o`` None: outputs and the workspace are
+    allocated (``num_splits`` None: the library's proposal). Returns ``(o, lse, workspace)``."""
+    import torch
+
+    index = q.get_device()
+    n, H, d, qs = _tokens_view(q, "q", index)
+    if qs != H * d:
+        raise ValueError("q must be contiguous")
+    cache, hkv, width = _cache_view(k_cache, v_cache, k_scale, v_scale, index)
+    if width != d:
+        raise ValueError(f"q has head dim {d}, the cache {width}")
+    B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, index)
+    lib = load_library()
+    if o is None:
+        if num_splits is None:
+            num_splits = lib.fa_paged_num_splits(B, H, hkv, max_seqlen_q, max_seqlen_k, d, window, sinks) or 1
+        device = q.device
+        o = torch.empty((n, H, d), dtype=torch.bfloat16, device=device)
+        lse = torch.empty((H, n), dtype=torch.float32, device=device)
+        if num_splits > 1:
+            workspace = torch.empty(lib.fa_paged_workspace_bytes(n, H, d, num_splits) // 4, dtype=torch.float32,
+                                    device=device)
+    else:
+        _check_out(o, "o", (n, H, d), torch.bfloat16, index)
+        _check_out(lse, "lse", (H, n), torch.float32, index)
+        if num_splits > 1:
+            _need_workspace(workspace, fa_paged_workspace_bytes(n, H, d, num_splits), "workspace", q.device)
+    st = _on_stream(index, stream, lib.fa_fwd_paged_fp8, q.data_ptr(), cache, page_table.data_ptr(),
+                    cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                    workspace.data_ptr() if num_splits > 1 else 0, B, H, n, max_seqlen_q, max_seqlen_k, max_pages,
+                    default_scale(d) if scale is None else scale, window, sinks, num_splits)
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_paged_fp8")
+    return o, lse, workspace
+
+
 def fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k,
                      max_seqlen_q: int, max_seqlen_k: int, workspace=None, num_splits: int = 1, window: int = 0,
                      sinks: int = 0, scale: float | None = None, stream=None):
@@ -744,51 +793,22 @@ def fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, 
     cache into caller-owned ``o`` bf16 [total_q, H, d] and ``lse`` fp32 [H, total_q] (include/fa.h,
     fa_fwd_paged_fp8). ``workspace`` fp32 of at least ``fa_paged_workspace_bytes`` bytes where
     ``num_splits > 1``."""
-    import torch
-
-    index = q.get_device()
-    n, H, d, qs = _tokens_view(q, "q", index)
-    if qs != H * d:
-        raise ValueError("q must be contiguous")
-    cache, _, width = _cache_view(k_cache, v_cache, k_scale, v_scale, index)
-    if width != d:
-        raise ValueError(f"q has head dim {d}, the cache {width}")
-    B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, index)
-    _check_out(o, "o", (n, H, d), torch.bfloat16, index)
-    _check_out(lse, "lse", (H, n), torch.float32, index)
-    ws = 0
-    if num_splits > 1:
-        _need_workspace(workspace, fa_paged_workspace_bytes(n, H, d, num_splits), "workspace", q.device)
-        ws = workspace.data_ptr()
-    with _Launch(index, stream) as handle:
-        st = load_library().fa_fwd_paged_fp8(q.data_ptr(), cache, page_table.data_ptr(), cu_seqlens_q.data_ptr(),
-                                             seqlens_k.data_ptr(), o.data_ptr(), lse.data_ptr(), ws, B, H, n,
-                                             max_seqlen_q, max_seqlen_k, max_pages,
-                                             default_scale(d) if scale is None else scale, window, sinks,
-                                             num_splits, handle)
-    _check(st, "fa_fwd_paged_fp8")
+    if o is None:
+        raise TypeError("o and lse must be tensors")
+    _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+           max_seqlen_k, workspace, num_splits, window, sinks, scale, stream)
 
 
 def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_k,
                         max_seqlen_q: int, max_seqlen_k: int, window: int = 0, sinks: int = 0,
                         scale: float | None = None, num_splits: int | None = None, stream=None):
-    """Allocate ``o``, ``lse`` and the workspace and run :func:`fa_fwd_paged_fp8` (``num_splits``
-    None: the library's proposal). Returns ``(o, lse)``; rows past ``cu_seqlens_q[B]`` are left as
+    """:func:`fa_fwd_paged_fp8` into new outputs, with a workspace of its own (``num_splits`` None:
+    the library's proposal). Returns ``(o, lse)``; rows past ``cu_seqlens_q[B]`` are left as
     allocated."""
-    import torch
-
-    n, H, d = q.shape
-    if num_splits is None:
-        num_splits = fa_paged_num_splits(seqlens_k.shape[0], H, k_cache.shape[1], max_seqlen_q, max_seqlen_k, d, window,
-                                         sinks) or 1
-    o = torch.empty_like(q)
-    lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
-    ws = None
-    if num_splits > 1:
-        ws = torch.empty(fa_paged_workspace_bytes(n, H, d, num_splits) // 4, dtype=torch.float32, device=q.device)
-    fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
-                     max_seqlen_k, ws, num_splits, window, sinks, scale, stream)
-    _used_on(stream, o, lse, ws)
+    o, lse, ws = _paged(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
+                        max_seqlen_q, max_seqlen_k, None, num_splits, window, sinks, scale, stream)
+    if stream is not None:
+        _used_on(stream, o, lse, ws)
     return o, lse
 
 
@@ -820,10 +840,9 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
     _check_out(o, "o", (B, H, Nq, d), torch.bfloat16, index)
     _check_out(lse, "lse", (B, H, Nq), torch.float32, index)
-    with _Launch(index, stream) as handle:
-        st = load_library().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H,
-                                          Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale, window, sinks,
-                                          handle)
+    st = _on_stream(index, stream, load_library().fa_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
+                    window, sinks)
     _check(st, "fa_fwd_window")
 
 
@@ -838,8 +857,9 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
     return o, lse
 
 
-def fa_bwd_window_workspace_bytes(B: int, H: int, Nq: int, d: int) -> int:
-    return load_library().fa_bwd_window_workspace_bytes(B, H, Nq, d)
+def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int, window: int,
+                                  sinks: int = 0) -> int:
+    return load_library().fa_bwd_window_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, sinks)
 
 
 def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
@@ -852,12 +872,12 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
     for t, name, like in ((o, "o", q), (dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
         _check_out(t, name, tuple(like.shape), torch.bfloat16, index)
     _check_out(lse, "lse", (B, H, Nq), torch.float32, index)
-    _need_workspace(workspace, fa_bwd_window_workspace_bytes(B, H, Nq, d), "workspace", q.device)
-    with _Launch(index, stream) as handle:
-        st = load_library().fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
-                                          lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                          workspace.data_ptr(), B, H, Hkv, Nq, Nk, d,
-                                          default_scale(d) if scale is None else scale, window, sinks, handle)
+    _need_workspace(workspace, fa_bwd_window_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, sinks), "workspace",
+                    q.device)
+    st = _on_stream(index, stream, load_library().fa_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale, window,
+                    sinks)
     _check(st, "fa_bwd_window")
 
 
@@ -866,9 +886,10 @@ def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0
     """Allocate ``(dq, dk, dv)`` and the workspace and run :func:`fa_bwd_window`."""
     import torch
 
-    B, H, _, Nq, _, d, _ = _grouped(q, k, v)
+    B, H, Hkv, Nq, Nk, d, _ = _grouped(q, k, v)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = torch.empty(max(1, fa_bwd_window_workspace_bytes(B, H, Nq, d) // 4), dtype=torch.float32, device=q.device)
+    nbytes = fa_bwd_window_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, sinks)
+    ws = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
     fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, ws, window, sinks, scale, stream)
     _used_on(stream, dq, dk, dv, ws)
     return dq, dk, dv

@@ -58,6 +58,7 @@
 // landed) instead of in pairs.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "fa.h"
@@ -90,6 +91,12 @@ struct BwdParams {
     // Sliding window (bottom-right; 0: none) with sinks, and heads that share kv
     // heads in groups: K, V, dK, dV have BHkv = B * Hkv heads.
     int window, sinks, group, H, Hkv, BHkv;
+    // A tile's steps (all heads of its group in turn) are cut into parts, each a
+    // CTA's: sink_parts for the first sink_tiles tiles, parts for the others.
+    // With more than one part the CTAs leave fp32 partial sums, [unit][dK, dV]
+    // [128 keys][d], which the last launch adds in order.
+    int sink_tiles, sink_parts, parts;
+    float* dkv_part;
 };
 
 namespace {
@@ -264,9 +271,12 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
 // accumulator. With one ring slot (d = 256) the steps run in order.
 //   WIN: sliding window with sinks and grouped heads. A CTA takes one key tile
 // of a kv head and walks the steps of every query head of the group in turn,
-// K and V staying resident and dV and dK accumulating over the whole group.
-// Units are ordered tile by tile over all kv heads: the tiles of the sinks,
-// which see every row behind them, start first.
+// K and V staying resident and dV and dK accumulating over the whole group; or
+// a part of those steps, where the units would not fill the GPU otherwise, and
+// for the tiles of the sinks, which see every row behind them (16 heads of 8192
+// rows in groups of four, window 1024, 4 sinks, d = 128: a sink tile has 512
+// steps, another 72). Units are ordered tile by tile over all kv heads, the
+// sinks' first.
 template <int D, bool WIN = false>
 __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
     using L = LayoutBwd<D>;
@@ -283,7 +293,16 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     const int hd = static_cast<int>(blockIdx.x % L::HALVES);
     const int unit_lin = static_cast<int>(blockIdx.x / L::HALVES);
     const int bh = WIN ? unit_lin % p.BHkv : unit_lin / p.tile_units;
-    const int ui = WIN ? unit_lin / p.BHkv : unit_lin % p.tile_units;
+    int ui = WIN ? unit_lin / p.BHkv : unit_lin % p.tile_units;
+    int part = 0, parts = 1;
+    if constexpr (WIN) {
+        const int sink_units = p.sink_tiles * p.sink_parts;
+        const bool sink = ui < sink_units;
+        parts = sink ? p.sink_parts : p.parts;
+        if (!sink) ui -= sink_units;
+        part = ui % parts;
+        ui = ui / parts + (sink ? 0 : p.sink_tiles);
+    }
     int kts[2], h0s[2], ns[2];
     int nt = 1;
     kts[0] = ui;
@@ -297,16 +316,29 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     else bwd_steps(p, kts[0], h0s[0], ns[0]);
     if (nt == 2) bwd_steps(p, kts[1], h0s[1], ns[1]);
     else ns[1] = 0, h0s[1] = 0;
-    if constexpr (WIN) nt = p.group;
-    const int n_all = WIN ? ns[0] * p.group : ns[0] + ns[1];
+    // WIN: this part's steps, s0 .. s1 - 1 of the group's ns[0] * group, as
+    // passes over consecutive heads from head_first on.
+    int s0 = 0, s1 = 0, head_first = 0;
+    if constexpr (WIN) {
+        const int all = ns[0] * p.group;
+        const int each = (all + parts - 1) / parts;
+        s0 = min(part * each, all);
+        s1 = min(s0 + each, all);
+        head_first = ns[0] > 0 ? s0 / ns[0] : 0;
+        nt = s1 > s0 ? (s1 - 1) / ns[0] - head_first + 1 : 1;
+    }
+    const int n_all = WIN ? s1 - s0 : ns[0] + ns[1];
     // The second tile reuses K/V, dV and dK only if both tiles have steps.
     const bool handoff = !WIN && nt == 2 && ns[0] > 0 && ns[1] > 0;
     // Pass tt of a CTA: its key tile, first step and number of steps; the head
     // of Q, dO and the accumulator.
     auto KT = [&](int tt) { return WIN ? kts[0] : kts[tt]; };
-    auto H0 = [&](int tt) { return WIN ? h0s[0] : h0s[tt]; };
-    auto NS = [&](int tt) { return WIN ? ns[0] : ns[tt]; };
-    auto ZQ = [&](int tt) { return WIN ? (bh / p.Hkv) * p.H + (bh % p.Hkv) * p.group + tt : bh; };
+    auto HB = [&](int tt) { return max(s0 - (head_first + tt) * ns[0], 0); };
+    auto H0 = [&](int tt) { return WIN ? h0s[0] + HB(tt) : h0s[tt]; };
+    auto NS = [&](int tt) {
+        return WIN ? max(0, min(s1 - (head_first + tt) * ns[0], ns[0]) - HB(tt)) : ns[tt];
+    };
+    auto ZQ = [&](int tt) { return WIN ? (bh / p.Hkv) * p.H + (bh % p.Hkv) * p.group + head_first + tt : bh; };
     auto ROW0 = [&](int tt) { return static_cast<size_t>(ZQ(tt)) * p.Nq_pad; };
 
     if (threadIdx.x == 0) {
@@ -654,6 +686,20 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(L::BAR_ACCFREE));
                     }
+                    if constexpr (WIN) {
+                        if (parts > 1) {
+                            float* at = p.dkv_part + (static_cast<size_t>(unit_lin) * 2 * kBwdKeys + r) * D +
+                                        hd * L::DH + cc * 32;
+                            uint4* dk4 = reinterpret_cast<uint4*>(at);
+                            uint4* dv4 = reinterpret_cast<uint4*>(at + kBwdKeys * D);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                dk4[e] = make_uint4(kr[4 * e], kr[4 * e + 1], kr[4 * e + 2], kr[4 * e + 3]);
+                                dv4[e] = make_uint4(vr[4 * e], vr[4 * e + 1], vr[4 * e + 2], vr[4 * e + 3]);
+                            }
+                            continue;
+                        }
+                    }
                     uint32_t kp[16], vp[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -780,52 +826,55 @@ __global__ void __launch_bounds__(256) fa_bwd_win_pre_kernel(const __nv_bfloat16
                                                              const __nv_bfloat16* __restrict__ dout,
                                                              const float* __restrict__ lse,
                                                              const __grid_constant__ BwdParams p, long long rows_pad) {
-    constexpr int PER = D / 32;
-    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows_pad) return;
+    // D / 8 threads per row, sixteen bytes of it each.
+    constexpr int LANES = D / 8;
+    const long long row = static_cast<long long>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+    const int lane = threadIdx.x % LANES;
+    if (row >= rows_pad) return;  // rows_pad is a multiple of 128: whole blocks
+    const unsigned mine = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
     const long long bh = row / p.Nq_pad;
     const int i = static_cast<int>(row - bh * p.Nq_pad);
-    auto load = [&](const __nv_bfloat16* src, float (&x)[PER]) {
-        const __nv_bfloat162* s2 = reinterpret_cast<const __nv_bfloat162*>(src + lane * PER);
+    auto load = [&](const __nv_bfloat16* src, float (&x)[8]) {
+        const uint4 u = reinterpret_cast<const uint4*>(src)[lane];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int e = 0; e < PER / 2; ++e) {
-            const float2 a = __bfloat1622float2(s2[e]);
-            x[2 * e] = a.x;
-            x[2 * e + 1] = a.y;
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(w[e] << 16);
+            x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
         }
     };
-    auto dot = [&](const float (&a)[PER], const float (&b)[PER]) {
+    auto dot = [&](const float (&a)[8], const float (&b)[8]) {
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) s = fmaf(a[e], b[e], s);
-        for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+        for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+        for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(mine, s, w);
         return s;
     };
+    float4* z = reinterpret_cast<float4*>(p.dq_acc + static_cast<size_t>(row) * D);
+    z[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+    z[lane + LANES] = make_float4(0.f, 0.f, 0.f, 0.f);
     float dd = 0.f, nl = -INFINITY;
     if (i < p.Nq) {
         const size_t src_row = static_cast<size_t>(bh) * p.Nq + i;
         const float l = lse[src_row];
-        nl = (l == -INFINITY) ? -INFINITY : -(l * kLog2e);
-        float g[PER];
+        float g[8], a[8];
         load(dout + src_row * D, g);
+        nl = (l == -INFINITY) ? -INFINITY : -(l * kLog2e);
         // Visible keys: [0, ns) and [w0, pos].
         const int pos = i + p.Nk - p.Nq;
         const int w0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
         const int ns = min(p.sinks, w0);
         const int seen = pos < 0 ? 0 : ns + pos + 1 - w0;
         if (seen > kFewKeys) {
-            float a[PER];
             load(o + src_row * D, a);
             dd = dot(a, g);
         } else if (nl != -INFINITY) {
-            float a[PER];
             load(q + src_row * D, a);
             const long long b = bh / p.H;
             const size_t base = static_cast<size_t>(b * p.Hkv + (bh - b * p.H) / p.group) * p.Nk;
             for (int n = 0; n < seen; ++n) {
                 const size_t key = base + (n < ns ? n : w0 + (n - ns));
-                float kr[PER], vr[PER];
+                float kr[8], vr[8];
                 load(k + key * D, kr);
                 load(v + key * D, vr);
                 dd = fmaf(ex2(fmaf(dot(a, kr), p.scale_log2, nl)), dot(g, vr), dd);
@@ -836,9 +885,6 @@ __global__ void __launch_bounds__(256) fa_bwd_win_pre_kernel(const __nv_bfloat16
         const_cast<float*>(p.ndd)[row] = -dd;
         const_cast<float*>(p.nlse2)[row] = nl;
     }
-    float* z = p.dq_acc + static_cast<size_t>(row) * D + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER / 2; ++e) reinterpret_cast<float2*>(z)[e] = make_float2(0.f, 0.f);
 }
 
 // dQ = scale * accumulator, to bf16: one warp per query row, D / 32 columns
@@ -871,6 +917,92 @@ __global__ void __launch_bounds__(256) fa_bwd_dq_kernel(const float* __restrict_
     }
 }
 
+// The last launch under a window: dQ as fa_bwd_dq_kernel, and behind its rows
+// the keys of the tiles whose dK and dV were left in parts, added part by part
+// (a fixed order) and written in bf16. D / 8 threads per row, 16-byte stores.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_win_post_kernel(const __grid_constant__ BwdParams p,
+                                                              __nv_bfloat16* __restrict__ dq, long long q_rows,
+                                                              long long k_rows) {
+    constexpr int LANES = D / 8;
+    const long long lin = static_cast<long long>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+    const int c = (threadIdx.x % LANES) * 8;
+    float x[8];
+    auto add = [&](const float* src, bool first) {
+        const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
+        const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = first ? y[e] : x[e] + y[e];
+    };
+    auto put = [&](__nv_bfloat16* dst, float f) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
+                                                    pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
+    };
+    if (lin < q_rows) {
+        const long long bh = lin / p.Nq;
+        add(p.dq_acc + (bh * p.Nq_pad + (lin - bh * p.Nq)) * D + c, true);
+        put(dq + lin * D + c, p.scale);
+        return;
+    }
+    long long k = lin - q_rows;
+    if (k >= k_rows) return;
+    // Row k of (tensor, tile in parts, kv head, key of the tile).
+    const int r = static_cast<int>(k % kBwdKeys);
+    k /= kBwdKeys;
+    const int bh = static_cast<int>(k % p.BHkv);
+    k /= p.BHkv;
+    const int is_v = static_cast<int>(k & 1);
+    const int first = p.sink_parts > 1 ? 0 : p.sink_tiles;  // first tile in parts
+    const int kt = first + static_cast<int>(k >> 1);
+    const int key = kt * kBwdKeys + r;
+    if (key >= p.Nk) return;
+    const bool sink = kt < p.sink_tiles;
+    const int parts = sink ? p.sink_parts : p.parts;
+    const long long unit0 = sink ? static_cast<long long>(kt) * parts
+                                 : static_cast<long long>(p.sink_tiles) * p.sink_parts +
+                                       static_cast<long long>(kt - p.sink_tiles) * parts;
+    for (int i = 0; i < parts; ++i)
+        add(p.dkv_part + ((((unit0 + i) * p.BHkv + bh) * 2 + is_v) * kBwdKeys + r) * D + c, i == 0);
+    put(static_cast<__nv_bfloat16*>(is_v ? p.dv : p.dk) + (static_cast<long long>(bh) * p.Nk + key) * D + c,
+        is_v ? 1.f : p.scale);
+}
+
+// How a windowed backward is cut into parts (host side). Each step of a CTA
+// takes about as long as any other, a CTA's start and end about kUnitCost
+// steps, leaving and adding partial sums kPartCost more; 152 CTAs run at once. `parts` minimises the waves' length, and a sink
+// tile is cut into pieces of about the same number of steps.
+struct BwdParts {
+    int sink_tiles, sink_parts, parts;
+    size_t part_floats;  // floats of the partial sums
+};
+BwdParts bwd_parts(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks) {
+    constexpr long long kUnitCost = 4, kPartCost = 6;
+    BwdParts c = {0, 1, 1, 0};
+    const int halves = d == 256 ? 2 : 1;
+    const long long k_tiles = (static_cast<long long>(Nk) + kBwdKeys - 1) / kBwdKeys;
+    const long long all = (static_cast<long long>(Nq) + kBwdHalf - 1) / kBwdHalf;
+    const long long G = H / Hkv, heads = static_cast<long long>(B) * Hkv;
+    if (window > 0) c.sink_tiles = static_cast<int>(std::min(k_tiles, (static_cast<long long>(sinks) + kBwdKeys - 1) / kBwdKeys));
+    const long long reach = window > 0 ? std::min(all, (kBwdKeys + static_cast<long long>(window) + kBwdHalf - 2) / kBwdHalf + 1) : all;
+    const long long steps = G * reach, sink_steps = G * all;
+    const long long tiles = std::max(1ll, k_tiles - c.sink_tiles);
+    long long best = -1;
+    for (int p = 1; p <= 16 && (p == 1 || p <= steps); ++p) {
+        const long long waves = (heads * tiles * halves * p + 151) / 152;
+        const long long cost = waves * ((steps + p - 1) / p + kUnitCost + (p > 1 ? kPartCost : 0));
+        if (best < 0 || cost < best) best = cost, c.parts = p;
+    }
+    if (c.sink_tiles > 0) {
+        const long long piece = std::max(8ll, (steps + c.parts - 1) / c.parts);
+        c.sink_parts = static_cast<int>(std::min(64ll, (sink_steps + piece - 1) / piece));
+    }
+    const long long units = heads * (c.sink_tiles * static_cast<long long>(c.sink_parts) +
+                                     (c.parts > 1 ? (k_tiles - c.sink_tiles) * c.parts : 0));
+    if (c.parts > 1 || (c.sink_tiles > 0 && c.sink_parts > 1))
+        c.part_floats = static_cast<size_t>(units) * 2 * kBwdKeys * d;
+    return c;
+}
+
 }  // namespace
 
 template <int D>
@@ -897,7 +1029,10 @@ cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
                                     static_cast<int>(L::ALLOC_BYTES));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(WIN ? p.BHkv : p.BH) * p.tile_units * L::HALVES;
+    const long long units = WIN ? static_cast<long long>(p.BHkv) * (p.sink_tiles * p.sink_parts +
+                                                                      (p.k_tiles - p.sink_tiles) * p.parts)
+                                : static_cast<long long>(p.BH) * p.tile_units;
+    const long long ctas = units * L::HALVES;
     if (ctas < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     fa_bwd_kernel<D, WIN><<<static_cast<unsigned>(ctas), L::THREADS, L::ALLOC_BYTES, stream>>>(p);
     return cudaGetLastError();
@@ -930,7 +1065,8 @@ template <int D>
 cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, const void* v, const void* o,
                            const void* dout, const float* lse, void* dq, cudaStream_t stream) {
     const long long rows_pad = static_cast<long long>(p.BH) * p.Nq_pad;
-    const long long blocks = (rows_pad + 7) / 8;
+    const long long per_pre = 256 / (D / 8);
+    const long long blocks = (rows_pad + per_pre - 1) / per_pre;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     using T = const __nv_bfloat16*;
     fa_bwd_win_pre_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
@@ -938,8 +1074,16 @@ cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, con
         rows_pad);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_bwd_main<D, true>(p, stream);
-    if (e == cudaSuccess) e = launch_bwd_dq<D>(p.dq_acc, dq, p.BH, p.Nq, p.Nq_pad, p.scale, stream);
-    return e;
+    if (e != cudaSuccess) return e;
+    const long long q_rows = static_cast<long long>(p.BH) * p.Nq;
+    const long long in_parts = (p.sink_parts > 1 ? p.sink_tiles : 0) + (p.parts > 1 ? p.k_tiles - p.sink_tiles : 0);
+    const long long k_rows = in_parts * 2 * p.BHkv * kBwdKeys;
+    const long long per_block = 256 / (D / 8);
+    const long long post = (q_rows + k_rows + per_block - 1) / per_block;
+    if (post > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    fa_bwd_win_post_kernel<D><<<static_cast<unsigned>(post), 256, 0, stream>>>(
+        p, static_cast<__nv_bfloat16*>(dq), q_rows, k_rows);
+    return cudaGetLastError();
 }
 
 }  // namespace fa
@@ -1008,7 +1152,12 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t fa_bwd_window_workspace_bytes(int B, int H, int Nq, int d) { return fa_bwd_workspace_bytes(B, H, Nq, d); }
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks) {
+    if (Nk < 1 || fa::check_window(H, Hkv, Nq, Nk, window, sinks) != FA_OK) return 0;
+    const size_t base = fa_bwd_workspace_bytes(B, H, Nq, d);
+    if (base == 0) return 0;
+    return base + fa::bwd_parts(B, H, Hkv, Nq, Nk, d, window, sinks).part_floats * sizeof(float);
+}
 
 fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
                         const float* lse, void* dq, void* dk, void* dv, void* workspace, int B, int H, int Hkv,
@@ -1052,6 +1201,11 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
     p.sinks = sinks;
     p.k_tiles = (Nk + 127) / 128;
     p.tile_units = p.k_tiles;
+    const fa::BwdParts c = fa::bwd_parts(B, H, Hkv, Nq, Nk, d, window, sinks);
+    p.sink_tiles = c.sink_tiles;
+    p.sink_parts = c.sink_parts;
+    p.parts = c.parts;
+    p.dkv_part = ndd + rows_pad;  // 16-byte aligned: rows_pad is a multiple of 128
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit = fa::kDefaultWaitLimit;

@@ -11,12 +11,14 @@
 // the page's scale was for an earlier owner does not count.
 //
 // An item is (sequence, page it touches, kv head, K or V). Its threads hold the
-// item's new values in registers (sixteen a thread: two 16-byte vectors of one
-// token), so the input is read once: rotate, reduce |.| over the item, form the
-// scale, round, store. Memory-bound for prompts, launch-bound for single
-// tokens. An item's threads are a power of two: within a warp for few new
-// tokens (a single token at d = 128 takes eight threads, so one warp serves
-// four items), or a whole block of up to 512.
+// item's new values in registers (sixteen columns of up to four tokens each), so
+// the input is read once: rotate, reduce |.| over the item, form the scale,
+// round, store. Launch-bound for single tokens; for prompts bound by the loads
+// in flight, since positions and table rows are two loads behind the offsets:
+// hence four tokens a thread rather than one (141 us with one, for the prompts
+// measured at the kernel). An item's threads are a power of two: within a warp
+// (a single token at d = 128 takes eight threads, so one warp serves four
+// items; a page of 16 takes one warp), or a whole block of up to 512.
 #include <algorithm>
 #include <cstring>
 
@@ -45,10 +47,10 @@ struct AppendLaunch {
     int log_slots;               // log2(token slots an item's threads cover)
     int log_group;               // log2(threads per item)
     int touch;                   // pages a sequence can touch
-    long long items;             // B * touch * Hkv * 2
-    unsigned item_blocks;        // blocks [0, item_blocks) take items, the rest queries
+    unsigned items;              // B * touch * Hkv * 2
+    unsigned item_blocks;        // blocks that take items; the others take queries
     int q_log_tb, q_chunks;      // queries: log2(tokens per block), token blocks per sequence
-    int q_heads_chunk;
+    int q_heads_chunk, q_heads_blocks;
     unsigned* status;
 };
 
@@ -85,8 +87,10 @@ __device__ __forceinline__ uint4 recode16(const uint4& u, float f) {
 }
 
 // The queries of one token block: rotated (or copied) into q_out.
-__device__ __forceinline__ void append_queries(const AppendLaunch& p) {
-    const unsigned lin = blockIdx.x - p.item_blocks;
+template <bool SPLIT>
+__device__ __forceinline__ void append_queries(const AppendLaunch& p, unsigned lin) {
+    const int hb = static_cast<int>(lin % static_cast<unsigned>(p.q_heads_blocks));
+    lin /= static_cast<unsigned>(p.q_heads_blocks);
     const int b = static_cast<int>(lin / static_cast<unsigned>(p.q_chunks));
     const int chunk = static_cast<int>(lin % static_cast<unsigned>(p.q_chunks));
     const int v = threadIdx.x & ((1 << p.log_parts) - 1);
@@ -95,48 +99,56 @@ __device__ __forceinline__ void append_queries(const AppendLaunch& p) {
     const int hs = rest >> p.q_log_tb;
     const int hstep = blockDim.x >> (p.log_parts + p.q_log_tb);
     NewTokens t;
-    if (!new_tokens(p.cu, p.lens, b, p.total, p.max_new, p.max_pages << p.log_page, t) || i >= t.n) return;
+    const bool in = new_tokens(p.cu, p.lens, b, p.total, p.max_new, p.max_pages << p.log_page, t) && i < t.n;
     const long long tok = t.first + i;
-    const int own = t.len - t.n + i;
-    if (!rope_positions_ok(p.r, tok, own)) {
+    const bool turn = p.r.table && v < (p.r.rot >> 4);
+    float c[8], s[8];
+    bool ok = true;
+    if (in && turn) ok = rope_coeffs<SPLIT>(p.r, v, tok, t.len - t.n + i, c, s);
+    ok = token_ok(ok, p.log_parts);
+    if (!in) return;
+    if (!ok) {
         if (v == 0 && hs == 0) atomicOr(p.status, kStatusBadPosition);
         return;
     }
-    const bool turn = p.r.table && v < (p.r.rot >> 4);
-    float c[8], s[8];
-    if (turn) rope_coeffs(p.r, v, tok, own, c, s);
-    const int lo = blockIdx.y * p.q_heads_chunk;
+    const int lo = hb * p.q_heads_chunk;
     const int hi = min(lo + p.q_heads_chunk, p.H);
     rope_heads(p.r, v, turn, c, s, p.q + tok * p.q_stride, p.q_out + tok * static_cast<long long>(p.H) * p.d, p.d,
                p.d, lo + hs, hi, hstep);
 }
 
-// PER: token slots of an item held by one thread (items wider than a block).
+// PER: token slots of an item held by one thread.
 // BLOCK: an item is a whole block (its reduction goes through shared memory);
 // otherwise a power-of-two group within a warp.
-template <int PER, bool BLOCK>
-__global__ void __launch_bounds__(512) fa_kv_append_kernel(const __grid_constant__ AppendLaunch p) {
+template <int PER, bool BLOCK, bool SPLIT>
+__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : 3) fa_kv_append_kernel(const __grid_constant__ AppendLaunch p) {
     __shared__ float red[16];
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    if (blockIdx.x >= p.item_blocks) {
-        append_queries(p);
+    // Item blocks are spread evenly among the query blocks: items wait for long
+    // chains of loads, queries for bandwidth, so each fills the other's gaps
+    // (six ragged prompts of 4001 tokens, 32 + 2 * 8 heads, d = 128: 87 us; the
+    // items alone take 47, the queries 52).
+    const unsigned long long total_blocks = gridDim.x;
+    const unsigned before = static_cast<unsigned>(blockIdx.x * static_cast<unsigned long long>(p.item_blocks) / total_blocks);
+    const unsigned after =
+        static_cast<unsigned>((blockIdx.x + 1ull) * static_cast<unsigned long long>(p.item_blocks) / total_blocks);
+    if (before == after) {
+        append_queries<SPLIT>(p, blockIdx.x - before);
         return;
     }
-    if (blockIdx.y > 0) return;  // the grid's second axis is the query heads' chunks
-
-    const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.log_group;
+    const unsigned item = before * (blockDim.x >> p.log_group) + (threadIdx.x >> p.log_group);
     const int g = threadIdx.x & ((1 << p.log_group) - 1);
     // An item's threads agree on everything below up to the item's end; in a
     // group within a warp the whole warp runs the reduction.
     bool live = item < p.items;
-    long long lin = live ? item : 0;
-    const int which = static_cast<int>(lin & 1);
-    lin >>= 1;
-    const int h = static_cast<int>(lin % p.Hkv);
-    lin /= p.Hkv;
-    const int touch = static_cast<int>(lin % p.touch);
-    const int b = static_cast<int>(lin / p.touch);
+    unsigned lin = live ? item : 0u;
+    const int which = lin >= p.items / 2 ? 1 : 0;  // all of K's items, then V's
+    if (which) lin -= p.items / 2;
+    const int h = static_cast<int>(lin % static_cast<unsigned>(p.Hkv));
+    lin /= static_cast<unsigned>(p.Hkv);
+    const int touch = static_cast<int>(lin % static_cast<unsigned>(p.touch));
+    const int b = static_cast<int>(lin / static_cast<unsigned>(p.touch));
 
     NewTokens t;
     const bool valid = new_tokens(p.cu, p.lens, b, p.total, p.max_new, p.max_pages << p.log_page, t);
@@ -148,16 +160,6 @@ __global__ void __launch_bounds__(512) fa_kv_append_kernel(const __grid_constant
     const int lo = touch == 0 ? (start & (page_size - 1)) : 0;             // first new slot of the page
     const int hi = min(page_size, t.len - (blk << p.log_page));            // end of the new slots
     live = live && lo < hi;
-    int page = -1;
-    if (live) {
-        page = p.page_table[static_cast<long long>(b) * p.max_pages + blk];
-        if (page < 0 || page >= p.num_pages) {
-            if (g == 0 && which == 0 && h == 0) atomicOr(p.status, kStatusBadPage);
-            live = false;
-        }
-    }
-    // A position outside the table spoils the whole item: found by the
-    // threads that hold its tokens, agreed on with the reduction.
     const int v = g & ((1 << p.log_parts) - 1);
     const int slot0 = g >> p.log_parts;
     const int slot_step = 1 << (p.log_group - p.log_parts);
@@ -166,43 +168,53 @@ __global__ void __launch_bounds__(512) fa_kv_append_kernel(const __grid_constant
     if (which == 0 && p.r.table) rope_columns(p.r, v, c0, c1);
     else c0 = 16 * v, c1 = 16 * v + 8;
 
-    float x[PER][8], y[PER][8];
-    float amax = 0.f;
+    // The new values stay packed in registers: rotating them twice, for the
+    // maximum and for the codes, costs less than the registers of their fp32
+    // values (101 against 118 us for the prompts above: three blocks per SM
+    // rather than two).
+    uint4 a[PER], c[PER];
     const __nv_bfloat16* src = which ? p.kv[1] : p.kv[0];
     const long long stride = which ? p.kv_stride[1] : p.kv_stride[0];
     const long long tok0 = static_cast<long long>(t.first) + (blk << p.log_page) - start;  // token of slot 0
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int slot = lo + slot0 + i * slot_step;
+        a[i] = c[i] = make_uint4(0u, 0u, 0u, 0u);
         if (live && slot < hi) {
             const __nv_bfloat16* row = src + (tok0 + slot) * stride + static_cast<long long>(h) * p.d;
-            const uint4 a = *reinterpret_cast<const uint4*>(row + c0);
-            const uint4 c = *reinterpret_cast<const uint4*>(row + c1);
-            unpack_bf16x8(a, x[i]);
-            unpack_bf16x8(c, y[i]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) x[i][k] = y[i][k] = 0.f;
+            a[i] = *reinterpret_cast<const uint4*>(row + c0);
+            c[i] = *reinterpret_cast<const uint4*>(row + c1);
         }
     }
-    bool bad = false;
-    if (which == 0 && p.r.table) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int slot = lo + slot0 + i * slot_step;
-            if (live && slot < hi) {
-                const int own = (blk << p.log_page) + slot;
-                if (!rope_positions_ok(p.r, tok0 + slot, own)) bad = true;
-                else if (turn) {
-                    float c[8], s[8];
-                    rope_coeffs(p.r, v, tok0 + slot, own, c, s);
-                    rope_apply(p.r.interleaved != 0, c, s, x[i], y[i]);
-                }
-            }
+    int page = -1;
+    if (live) {
+        page = p.page_table[static_cast<long long>(b) * p.max_pages + blk];
+        if (page < 0 || page >= p.num_pages) {
+            if (g == 0 && which == 0 && h == 0) atomicOr(p.status, kStatusBadPage);
+            live = false;
         }
     }
+    // A position outside the table spoils the whole item: found by the threads
+    // that hold its pairs, agreed on with the reduction.
+    auto values = [&](int i, float (&x)[8], float (&y)[8]) {
+        const int slot = lo + slot0 + i * slot_step;
+        unpack_bf16x8(a[i], x);
+        unpack_bf16x8(c[i], y);
+        if (turn && live && slot < hi && !bad) {
+            float co[8], si[8];
+            if (rope_coeffs<SPLIT>(p.r, v, tok0 + slot, (blk << p.log_page) + slot, co, si))
+                rope_apply(p.r.interleaved != 0, co, si, x, y);
+            else bad = true;
+        }
+    };
+    float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) amax = fmaxf(amax, amax16(x[i], y[i]));
+    for (int i = 0; i < PER; ++i) {
+        float x[8], y[8];
+        values(i, x, y);
+        amax = fmaxf(amax, amax16(x, y));
+    }
     if (bad) amax = -1.f;  // marks the item: the reduction below keeps it apart
 
     // Item-wide maximum, and whether any thread found a bad position.
@@ -228,6 +240,9 @@ __global__ void __launch_bounds__(512) fa_kv_append_kernel(const __grid_constant
         __syncwarp();
     }
     if (!live) return;
+    // The codes below read the table again: keeping every cosine and sine across
+    // the reduction would take more registers than there are.
+    asm volatile("" ::: "memory");
     if (mn < 0.f) {
         if (g == 0) atomicOr(p.status, kStatusBadPosition);
         return;
@@ -249,9 +264,11 @@ __global__ void __launch_bounds__(512) fa_kv_append_kernel(const __grid_constant
     for (int i = 0; i < PER; ++i) {
         const int slot = lo + slot0 + i * slot_step;
         if (slot < hi) {
+            float x[8], y[8];
+            values(i, x, y);
             uint8_t* row = base + slot * p.d;
-            *reinterpret_cast<uint2*>(row + c0) = encode8(x[i], inv);
-            *reinterpret_cast<uint2*>(row + c1) = encode8(y[i], inv);
+            *reinterpret_cast<uint2*>(row + c0) = encode8(x, inv);
+            *reinterpret_cast<uint2*>(row + c1) = encode8(y, inv);
         }
     }
     if (g == 0) sc[cell] = s_new;
@@ -314,17 +331,19 @@ extern "C" fa_status fa_kv_append_fp8(const void* q, const void* k, const void* 
     // Slots of a page that one append can fill, rounded up to a power of two.
     p.log_slots = 0;
     while (p.log_slots < p.log_page && (1 << p.log_slots) < max_new) ++p.log_slots;
-    const int log_lanes = p.log_parts + p.log_slots;  // threads wanted per item: at most 2^11
-    p.log_group = std::min(log_lanes, 9);
-    const int per = 1 << (log_lanes - p.log_group);
+    const int log_lanes = p.log_parts + p.log_slots;  // sixteen-column pieces of an item: at most 2^11
+    const int log_per = std::min(std::max(log_lanes - 5, 0), 2);
+    p.log_group = log_lanes - log_per;
+    const int per = 1 << log_per;
     p.touch = static_cast<int>((static_cast<long long>(cache->page_size) - 1 + max_new + cache->page_size - 1) >>
                                p.log_page);
-    p.items = static_cast<long long>(B) * p.touch * Hkv * 2;
+    const long long items = static_cast<long long>(B) * p.touch * Hkv * 2;
+    if (items > 0x7fffffffll) return FA_ERR_SHAPE;
+    p.items = static_cast<unsigned>(items);
     const unsigned threads = p.log_group > 5 ? 1u << p.log_group : (q ? 256u : 128u);
     const long long per_block = static_cast<long long>(threads) >> p.log_group;
-    const long long item_blocks = (p.items + per_block - 1) / per_block;
+    const long long item_blocks = (items + per_block - 1) / per_block;
     long long q_blocks = 0;
-    unsigned gy = 1;
     if (q) {
         int log_threads = 0;
         while ((1u << log_threads) < threads) ++log_threads;
@@ -336,16 +355,18 @@ extern "C" fa_status fa_kv_append_fp8(const void* q, const void* k, const void* 
         int chunk = 16 * hstep;
         while (chunk > hstep && q_blocks * ((H + chunk - 1) / chunk) < 4ll * 152) chunk >>= 1;
         p.q_heads_chunk = chunk;
-        gy = static_cast<unsigned>((H + chunk - 1) / chunk);
+        p.q_heads_blocks = (H + chunk - 1) / chunk;
+        q_blocks *= p.q_heads_blocks;
     }
-    if (item_blocks + q_blocks > 0x7fffffffll || gy > 65535u) return FA_ERR_SHAPE;
+    if (item_blocks + q_blocks > 0x7fffffffll) return FA_ERR_SHAPE;
     p.item_blocks = static_cast<unsigned>(item_blocks);
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-    const dim3 grid(static_cast<unsigned>(item_blocks + q_blocks), gy, 1);
-    auto kernel = p.log_group <= 5 ? fa::fa_kv_append_kernel<1, false>
-                  : per == 1       ? fa::fa_kv_append_kernel<1, true>
-                  : per == 2       ? fa::fa_kv_append_kernel<2, true>
-                                   : fa::fa_kv_append_kernel<4, true>;
+    const dim3 grid(static_cast<unsigned>(item_blocks + q_blocks), 1, 1);
+    const bool split = fa::rope_split(p.r);
+    auto kernel = p.log_group > 5 ? (split ? fa::fa_kv_append_kernel<4, true, true> : fa::fa_kv_append_kernel<4, true, false>)
+                  : per == 1 ? (split ? fa::fa_kv_append_kernel<1, false, true> : fa::fa_kv_append_kernel<1, false, false>)
+                  : per == 2 ? (split ? fa::fa_kv_append_kernel<2, false, true> : fa::fa_kv_append_kernel<2, false, false>)
+                             : (split ? fa::fa_kv_append_kernel<4, false, true> : fa::fa_kv_append_kernel<4, false, false>);
     const cudaError_t e = fa::launch_dependent(kernel, grid, threads, 0, stream, p);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -24,11 +24,11 @@
 // largest element to [2^7, 2^8): elements down to 2^-22 of it stay exact.
 //
 // The recurrence in base 2, with a tile's K scale ks and V scale vs per key:
-//   x_j = s_j * (ks_j * scale * log2 e) + log2 vs_j,  p_j = 2^(x_j - m + 10),
+//   x_j = s_j * (ks_j * scale * log2 e) + log2 vs_j,  p_j = 2^(x_j - m + 7),
 //   O += p_j code_j,  l += p_j / vs_j:  O / l = sum_j softmax_j vs_j code_j.
 // The V scale sits in the exponent, so P stays in f16's range whatever the
 // scales are; the reference m moves only when a row's largest x passes it by
-// more than 4 (p <= 2^14), so O is seldom rescaled.
+// more than 8 (p <= 2^15), so O is seldom rescaled.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -306,6 +306,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
     // the V scale and its reciprocal for both 16-key halves.
     float sk[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f}, si[2] = {1.f, 1.f};
     bool ok = true;
+    // The lane's parts of its shared-memory addresses: K's 16-byte loads of 64
+    // columns each, V's ldmatrix rows of 32 columns each.
+    uint32_t k_lane[C], v_lane[X / 2];
+#pragma unroll
+    for (int c = 0; c < C; ++c) k_lane[c] = tile_unit<D>(key_of<D>(g), 4 * c + t);
+#pragma unroll
+    for (int x = 0; x < X; x += 2)
+        v_lane[x / 2] = tile_unit<D>(8 * ((lane >> 3) & 1) + key_of<D>(lane & 7), x + (lane >> 4));
 
     for (int k = 0; k < mine; ++k) {
         if ((k & 31) == 0) {
@@ -336,8 +344,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             uint32_t kw[4][4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) ld_shared_v4(kw[n], ks_at + tile_unit<D>(8 * n + key_of<D>(g), 4 * c + t));
+            const uint32_t at = ks_at + k_lane[c];
+            static_for<4>([&](auto n) { ld_shared_v4_at<n * 8 * L::ROW_BYTES>(kw[n], at); });
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 uint32_t a[4];
@@ -349,8 +357,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
                 }
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
-                    mma_f16(s[n], a, decode_e4m3x2_f16(static_cast<uint16_t>(kw[n][ks] & 0xffffu)),
-                            decode_e4m3x2_f16(static_cast<uint16_t>(kw[n][ks] >> 16)));
+                {
+                    uint32_t b0, b1;
+                    decode_e4m3x4_f16(kw[n][ks], b0, b1);
+                    mma_f16(s[n], a, b0, b1);
+                }
             }
         }
 
@@ -414,7 +425,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         // O += P V. Fragment index kk of 8 keys is key row key_of(kk); a key that
         // no row sees may hold anything (a slot never written, a NaN): its bytes
         // are cleared.
-        const int mrow = lane & 7, mhi = (lane >> 3) & 1, mx4 = lane >> 4;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
@@ -433,17 +443,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
 #pragma unroll
             for (int x = 0; x < X; x += 2) {
                 uint32_t w[4];
-                ldmatrix_x4_trans(w, vs_at + tile_unit<D>(16 * kk + 8 * mhi + key_of<D>(mrow), x + mx4));
+                ldmatrix_x4_trans(w, vs_at + v_lane[x / 2] + kk * 16 * L::ROW_BYTES);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t lo = w[2 * u], hi = w[2 * u + 1];
                     if (masked) lo &= keep[0], hi &= keep[1];
-                    lo = __byte_perm(lo, 0u, 0x3120);
-                    hi = __byte_perm(hi, 0u, 0x3120);
-                    mma_f16(o[x + u][0], pf[kk], decode_e4m3x2_f16(static_cast<uint16_t>(lo & 0xffffu)),
-                            decode_e4m3x2_f16(static_cast<uint16_t>(hi & 0xffffu)));
-                    mma_f16(o[x + u][1], pf[kk], decode_e4m3x2_f16(static_cast<uint16_t>(lo >> 16)),
-                            decode_e4m3x2_f16(static_cast<uint16_t>(hi >> 16)));
+                    uint32_t e0, e1, d0, d1;  // even and odd columns, keys 0-7 and 8-15
+                    decode_e4m3x4_f16(__byte_perm(lo, 0u, 0x3120), e0, d0);
+                    decode_e4m3x4_f16(__byte_perm(hi, 0u, 0x3120), e1, d1);
+                    mma_f16(o[x + u][0], pf[kk], e0, e1);
+                    mma_f16(o[x + u][1], pf[kk], d0, d1);
                 }
             }
         }
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
             const float inv = ll > 0.f ? 1.f / ll : 0.f;
             *reinterpret_cast<uint2*>(p.o + row * D + 4 * c) =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-            // l is a sum of 2^(x - m + 10): the shift comes out again.
+            // l is a sum of 2^(x - m + 7): the shift comes out again.
             if (c == 0)
                 p.lse[static_cast<long long>(h * p.G + j) * p.total_q + nt.first + i] =
                     ll > 0.f ? (mm - kPShift + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
@@ -517,57 +526,91 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
     }
 }
 
-// Merge of the key splits, one warp per (token, head) row whose block used more
-// than one: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s.
-template <int D>
+// Merge of the key splits of the (token, head) rows whose block used more than
+// one: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s. W warps (1 or
+// 4) share a row, each with eight partial rows in flight: the merge of a single
+// sequence's few rows over many splits is a matter of latency alone.
+template <int D, int W>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
-    constexpr int PER = D / 32;
+    constexpr int PER = D / 32, U = 8;
+    __shared__ float weight[4][FA_MAX_SPLITS];
+    __shared__ float sums[W > 1 ? 4 : 1][W > 1 ? D : 1];
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wi = warp % W;
+    const long long unit = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
     const int head = static_cast<int>(unit % p.H);
     const long long rest = unit / p.H;
     const int i = static_cast<int>(rest % p.max_q);
     const int b = static_cast<int>(rest / p.max_q);
     NewTokens nt;
-    if (b >= p.B || !new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt) || i >= nt.n) return;
-    // The row block of this row decides how many splits it used.
-    const int r = i * p.G + head % p.G;
-    const int r0 = r / p.block_rows * p.block_rows, rows = nt.n * p.G;
-    const int start = nt.len - nt.n;
-    const int p0 = start + r0 / p.G, p1 = start + (min(r0 + p.block_rows, rows) - 1) / p.G;
-    const KeyList list = p.block_keys == kTcKeys ? key_list<kTcKeys>(p.window, p.sinks, p0, p1)
-                                                 : key_list<kKeys>(p.window, p.sinks, p0, p1);
-    const int used = (list.n + p.tiles_per_split - 1) / p.tiles_per_split;
-    if (used <= 1) return;
-    const long long row = static_cast<long long>(nt.first + i) * p.H + head;
+    bool live = b < p.B && new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt) && i < nt.n;
+    int used = 0;
+    if (live) {
+        // The row block of this row decides how many splits it used.
+        const int r = i * p.G + head % p.G;
+        const int r0 = r / p.block_rows * p.block_rows, rows = nt.n * p.G;
+        const int start = nt.len - nt.n;
+        const int p0 = start + r0 / p.G, p1 = start + (min(r0 + p.block_rows, rows) - 1) / p.G;
+        const KeyList list = p.block_keys == kTcKeys ? key_list<kTcKeys>(p.window, p.sinks, p0, p1)
+                                                     : key_list<kKeys>(p.window, p.sinks, p0, p1);
+        used = (list.n + p.tiles_per_split - 1) / p.tiles_per_split;
+        live = used > 1;
+    }
+    const long long row = live ? static_cast<long long>(nt.first + i) * p.H + head : 0;
     const long long stride = static_cast<long long>(p.total_q) * p.H;
+    if (!live) used = 0;
+    const float* src = p.ws_o + row * D + lane * PER;
+    float x[U][PER];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * W;
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+                const float2 a = s < used ? *reinterpret_cast<const float2*>(src + s * stride * D + e) : make_float2(0.f, 0.f);
+                x[u][e] = a.x;
+                x[u][e + 1] = a.y;
+            }
+        }
+    };
+    load(wi);
     float mm = -INFINITY;
     for (int s = lane; s < used; s += 32) mm = fmaxf(mm, p.ws_m[s * stride + row]);
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     const float ref = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f, acc[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int s0 = 0; s0 < used; s0 += 32) {
-        const int s = s0 + lane;
-        const float f = s < used ? ex2(p.ws_m[s * stride + row] - ref) : 0.f;
-        ll = s < used ? fmaf(f, p.ws_l[s * stride + row], ll) : ll;
-        const int n = min(32, used - s0);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const float* src = p.ws_o + ((s0 + k) * stride + row) * D + lane * PER;
-#pragma unroll
-            for (int e = 0; e < PER; e += 2) {
-                const float2 a = *reinterpret_cast<const float2*>(src + e);
-                acc[e] = fmaf(fk, a.x, acc[e]);
-                acc[e + 1] = fmaf(fk, a.y, acc[e + 1]);
-            }
-        }
+    float ll = 0.f;
+    for (int s = lane; s < used; s += 32) {
+        const float f = ex2(p.ws_m[s * stride + row] - ref);
+        weight[warp][s] = f;
+        ll = fmaf(f, p.ws_l[s * stride + row], ll);
     }
     for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+    __syncwarp();
+    float acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int s0 = wi; s0 < used; s0 += U * W) {
+        if (s0 != wi) load(s0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * W;
+            const float f = s < used ? weight[warp][s] : 0.f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
+        }
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < PER; ++e) sums[warp][lane * PER + e] = acc[e];
+        __syncthreads();
+        if (wi != 0) return;
+        for (int k = 1; k < W; ++k)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] += sums[warp + k][lane * PER + e];
+    }
+    if (!live) return;
     const float inv = ll > 0.f ? 1.f / ll : 0.f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * PER);
 #pragma unroll
@@ -593,7 +636,7 @@ bool encode_cache_map(CUtensorMap* map, const void* base, int d, long long rows,
 // How a call is cut: by the tensor-core kernel of fa_paged_tc.cu, or by this
 // file's.
 struct Plan {
-    bool tc;
+    bool tc, dual;
     int block_rows, block_keys;
     long long row_blocks;
     long long tiles;  // most key tiles a row block can list
@@ -602,7 +645,8 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     Plan c;
     const long long rows = static_cast<long long>(max_q) * G;
     c.tc = d <= 128 && rows > kRows;
-    c.block_rows = c.tc ? kTcRows : kRows;
+    c.dual = c.tc && rows <= kTcRows;
+    c.block_rows = !c.tc ? kRows : c.dual ? kTcRows : 2 * kTcRows;
     c.block_keys = c.tc ? kTcKeys : kKeys;
     c.row_blocks = (rows + c.block_rows - 1) / c.block_rows;
     const long long K = c.block_keys;
@@ -614,8 +658,34 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     return c;
 }
 
+// Splits that finish earliest, in rounds of 128 keys; a CTA's start and end cost
+// about three, leaving and merging partial states some more. One sequence: waves
+// of CTAs of equal length. Several: their lengths differ, so the longest CTA
+// comes on top of an even share of all of them, at two thirds of the longest
+// length (measured: 64 contexts of 8192 to 32768, 512 units: 600 us with one
+// split, 511 with three, 480 with eight; one of 131072, 8 units: 52 us with 38
+// splits, one wave, 74 with 152).
+int best_splits(int B, long long units, long long rounds, int slots, int per_cta, bool many_rows) {
+    // (Partial sums of 256 rows cost more than they even out: two chunks of 2048
+    // tokens over 16384 keys, 341 us with one split, 430 with four.)
+    if (many_rows && units >= slots) return 1;
+    const long long most = std::max(1ll, std::min(static_cast<long long>(FA_MAX_SPLITS), rounds / 2));
+    const double start = many_rows ? 8. : 3.;
+    long long best = 1;
+    double best_cost = -1.;
+    for (long long s = 1; s <= most; ++s) {
+        const long long ctas = units * ((s + per_cta - 1) / per_cta);
+        const double each = static_cast<double>((rounds + s - 1) / s) + start;
+        const double cost = (B == 1 || many_rows ? static_cast<double>((ctas + slots - 1) / slots) * each
+                                                 : (1. + 0.65 * static_cast<double>(ctas) / slots) * each) +
+                            (s > 1 ? 4. + 0.1 * static_cast<double>(B == 1 ? s : 4 * s) : 0.);
+        if (best_cost < 0. || cost < best_cost) best = s, best_cost = cost;
+    }
+    return static_cast<int>(best);
+}
+
 template <int D>
-cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
+cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
     using L = PagedLayout<D>;
     static ContextCache<int> attr_set;
     int done = 0;
@@ -627,15 +697,19 @@ cudaError_t launch_paged(const PagedParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(fa_paged_rows_kernel<D>, dim3(static_cast<unsigned>(ctas)), kWarps * 32, L::ALLOC, stream,
-                            p);
+    return launch_dependent(fa_paged_rows_kernel<D>, dim3(static_cast<unsigned>(ctas)), kWarps * 32, L::ALLOC,
+                            stream, p);
 }
 
 template <int D>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
-    const long long blocks = (static_cast<long long>(p.B) * p.max_q * p.H + 3) / 4;
+    const long long rows = static_cast<long long>(p.B) * p.max_q * p.H;
+    // Four warps a row while that leaves the grid within about one wave.
+    const bool four = p.num_splits > 8 && rows <= 4096;
+    const long long blocks = four ? rows : (rows + 3) / 4;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(fa_paged_merge_kernel<D>, dim3(static_cast<unsigned>(blocks)), 128, 0, stream, p);
+    return launch_dependent(four ? fa_paged_merge_kernel<D, 4> : fa_paged_merge_kernel<D, 1>,
+                            dim3(static_cast<unsigned>(blocks)), 128, 0, stream, p);
 }
 
 }  // namespace
@@ -647,14 +721,9 @@ int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_
     if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || !fa::valid_d(d)) return 0;
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
     const long long units = static_cast<long long>(B) * Hkv * c.row_blocks;
-    if (c.tc) {
-        // One CTA per SM: split only while the units leave SMs idle.
-        const long long fill = 152 / units;
-        return static_cast<int>(std::max(1ll, std::min({fill, c.tiles / 4, static_cast<long long>(FA_MAX_SPLITS)})));
-    }
-    const long long want = (4ll * 304 + units - 1) / units;         // CTAs for four waves of two per SM
-    const long long most = std::max(1ll, c.tiles / (2 * fa::kWarps)); // two tiles per warp at least
-    return static_cast<int>(std::max(1ll, std::min({want, most, static_cast<long long>(FA_MAX_SPLITS)})));
+    const long long rounds = std::max(1ll, c.tiles * c.block_keys / 128);
+    // CTAs at once: one per SM for the tensor-core kernel and head dim 256.
+    return fa::best_splits(B, units, rounds, c.tc || d == 256 ? 152 : 304, c.dual ? 2 : 1, c.tc && !c.dual);
 }
 
 size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits) {
@@ -723,14 +792,16 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     p.block_keys = c.block_keys;
     p.row_blocks = static_cast<int>(c.row_blocks);
     p.num_splits = num_splits;
+    p.dual = c.dual ? 1 : 0;
+    p.row_warps = c.dual ? (max_seqlen_q * p.G + 31) / 32 : 4;
     p.tiles_per_split = static_cast<int>((c.tiles + num_splits - 1) / num_splits);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit = fa::kDefaultWaitLimit;
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
     cudaError_t e = c.tc       ? fa::launch_paged_tc(p, d, stream)
-                    : d == 64  ? fa::launch_paged<64>(p, stream)
-                    : d == 128 ? fa::launch_paged<128>(p, stream)
-                               : fa::launch_paged<256>(p, stream);
+                    : d == 64  ? fa::launch_rows<64>(p, stream)
+                    : d == 128 ? fa::launch_rows<128>(p, stream)
+                               : fa::launch_rows<256>(p, stream);
     if (e == cudaSuccess && num_splits > 1)
         e = d == 64 ? fa::launch_merge<64>(p, stream)
                     : d == 128 ? fa::launch_merge<128>(p, stream) : fa::launch_merge<256>(p, stream);

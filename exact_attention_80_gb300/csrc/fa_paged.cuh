@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <utility>
+
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -18,15 +20,18 @@ constexpr int kScaleExpMax = 120;
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Two e4m3 codes (the low and high byte of `pair`) as packed f16: exact.
-__device__ __forceinline__ uint32_t decode_e4m3x2_f16(uint16_t pair) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(pair));
-    return r;
+// Four e4m3 codes as two packed f16 pairs (codes 0 and 1, 2 and 3): exact.
+__device__ __forceinline__ void decode_e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 __device__ __forceinline__ void decode_e4m3x4(uint32_t w, float (&x)[4]) {
-    const uint32_t lo = decode_e4m3x2_f16(static_cast<uint16_t>(w & 0xffffu));
-    const uint32_t hi = decode_e4m3x2_f16(static_cast<uint16_t>(w >> 16));
+    uint32_t lo, hi;
+    decode_e4m3x4_f16(w, lo, hi);
     const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
     const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
@@ -52,8 +57,8 @@ __device__ __forceinline__ bool new_tokens(const int* cu, const int* lens, int b
     return ok;
 }
 
-constexpr float kPShift = 10.f;  // p = 2^(x - m + 10)
-constexpr float kPSlack = 4.f;   // the reference moves when x passes it by more
+constexpr float kPShift = 7.f;  // p = 2^(x - m + 7)
+constexpr float kPSlack = 8.f;  // the reference moves when x passes it by more, so p <= 2^15
 
 
 struct PagedParams {
@@ -73,6 +78,9 @@ struct PagedParams {
     int window, sinks;
     int row_blocks, num_splits, tiles_per_split;  // row blocks of block_rows rows, tiles of block_keys keys
     int block_rows, block_keys;
+    // fa_paged_tc.cu: the two tile slots take the same rows and two splits; warps
+    // of a row tile that can have rows.
+    int dual, row_warps;
     float scale_log2;
     long long wait_limit;
     unsigned* status;
@@ -106,6 +114,34 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// 16-byte shared-memory accesses at a register plus a constant.
+template <int OFF>
+__device__ __forceinline__ void ld_shared_v4_at(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr), "n"(OFF)
+                 : "memory");
+}
+template <int OFF>
+__device__ __forceinline__ void st_shared_v4_at(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0 + %1], {%2, %3, %4, %5};" ::"r"(addr), "n"(OFF), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+// f(Index<0>) .. f(Index<N - 1>): a loop whose index is a constant, for immediate
+// operands.
+template <int V>
+struct Index {
+    static constexpr int value = V;
+    __host__ __device__ constexpr operator int() const { return V; }
+};
+template <int... I, typename F>
+__device__ __forceinline__ void static_for_impl(std::integer_sequence<int, I...>, F&& f) {
+    (f(Index<I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    static_for_impl(std::make_integer_sequence<int, N>{}, f);
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -114,8 +150,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // Host side (fa_paged.cu): checks a cache's description.
 fa_status check_cache(const fa_paged_cache* cache);
-// The kernel for many query rows (fa_paged_tc.cu): rows per unit, keys per tile.
-constexpr int kTcRows = 256;
+// The kernel for many query rows (fa_paged_tc.cu): rows per tile (a CTA takes two
+// tiles, or one tile twice over two splits), keys per tile.
+constexpr int kTcRows = 128;
 constexpr int kTcKeys = 128;
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream);
 inline int log2_exact(int x) {

@@ -12,15 +12,21 @@
 //     error below that): twice the MMAs at twice the rate of bf16, and no
 //     conversion of K.
 //   * O += P V runs as kind::f16: P in f16 (relative rounding 2^-11) in TMEM
-//     over its S columns, V converted from its codes (exact) by two warps that
-//     the dense forward leaves idle, once per key tile for both row tiles.
+//     over its S columns, V converted from its codes (exact) by four warps of
+//     their own, once per key tile for both row tiles.
 // The block scales enter where fa_paged.cu has them: the K scale multiplies the
 // score, log2 of the V scale adds to the exponent, and the row sum takes its
 // reciprocal; scores are handled in groups of 16 keys, the smallest page.
 //
+// DUAL: at most 128 rows (drafts, short chunks). Both tile slots take the same
+// rows, each with a key split of its own, so that the two still alternate on the
+// tensor core (16 sequences of five drafted tokens over up to 16200 keys: 120
+// us, against 200 with one tile slot idle).
+//
 // Roles, by warp: 0 producer (Q is written by the softmax threads; K and V pages
-// by TMA into two rings), 1 issuer, 2-3 converters, 4-11 softmax (thread = row
-// = TMEM lane). Step j, per tile as its P arrives: O_t += P_t(j) V_j, then at
+// by TMA into two rings), 1 issuer, 2-3 idle, 4-11 softmax (thread = row = TMEM
+// lane), 12-15 converters (two warps took 2200 cycles a tile beside the
+// softmax, four take 1150). Step j, per tile as its P arrives: O_t += P_t(j) V_j, then at
 // once S_t(j+1) over the same columns. Every wait is bounded as in the dense
 // forward.
 #include <cuda_bf16.h>
@@ -32,23 +38,25 @@
 namespace fa {
 namespace {
 
-template <int D>
+template <int D, bool DUAL>
 struct TcLayout {
     static constexpr int BM = 128, BN = kTcKeys;
     static constexpr int ROW_BYTES = D < 128 ? D : 128;   // swizzled row of codes
-    static constexpr int KSTAGES = D == 64 ? 4 : 3;
-    static constexpr int VSTAGES = D == 64 ? 4 : 2;
-    static constexpr int THREADS = 384;
+    // Dual slots share one row tile, which leaves room for deeper rings.
+    static constexpr int KSTAGES = D == 64 ? 6 : DUAL ? 4 : 3;
+    static constexpr int VSTAGES = D == 64 ? 6 : DUAL ? 3 : 2;
+    static constexpr int THREADS = 512;
+    static constexpr int CONV_WARP0 = 12, CONV_WARPS = 4;
     static constexpr uint32_t Q_TERM = BM * D;            // one e4m3 term of a row tile
     static constexpr uint32_t Q_TILE = 2 * Q_TERM;
     static constexpr uint32_t SLOT = BN * D;              // codes of a K or V tile
     static constexpr uint32_t V16 = BN * D * 2;           // V tile in f16: 64-column chunks of 128-byte rows
     static constexpr uint32_t Q_OFF = 0;
-    static constexpr uint32_t K_OFF = Q_OFF + 2 * Q_TILE;
+    static constexpr uint32_t K_OFF = Q_OFF + (DUAL ? 1 : 2) * Q_TILE;
     static constexpr uint32_t V_OFF = K_OFF + KSTAGES * SLOT;
     static constexpr uint32_t V16_OFF = V_OFF + VSTAGES * SLOT;
     static constexpr uint32_t BAR_OFF = V16_OFF + 2 * V16;
-    static constexpr int BAR_QFULL = 0;                    // [tile] one arrival per softmax warp
+    static constexpr int BAR_QFULL = 0;                    // [tile] one arrival per softmax warp with rows
     static constexpr int BAR_KFULL = 2;
     static constexpr int BAR_KEMPTY = BAR_KFULL + KSTAGES;
     static constexpr int BAR_VFULL = BAR_KEMPTY + KSTAGES;
@@ -56,7 +64,7 @@ struct TcLayout {
     static constexpr int BAR_HFULL = BAR_VEMPTY + VSTAGES;   // [buffer] V in f16 (one arrival per converter warp)
     static constexpr int BAR_HEMPTY = BAR_HFULL + 2;         // [buffer]
     static constexpr int BAR_SFULL = BAR_HEMPTY + 2;         // [tile]
-    static constexpr int BAR_PFULL = BAR_SFULL + 2;          // [tile] one arrival per softmax warp
+    static constexpr int BAR_PFULL = BAR_SFULL + 2;          // [tile] one arrival per softmax warp with rows
     static constexpr int BAR_OFULL = BAR_PFULL + 2;          // [tile]
     static constexpr int BAR_DRAIN = BAR_OFULL + 2;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
@@ -66,8 +74,8 @@ struct TcLayout {
     // TMEM columns: S_t (P_t over its first half), then O_t.
     __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * BN; }
     __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
-    static constexpr int LAUNCH_REGS = 168, CTRL_REGS = 88, SOFTMAX_REGS = 208;
-    static_assert(128 * CTRL_REGS + 256 * SOFTMAX_REGS == THREADS * LAUNCH_REGS, "register split");
+    static constexpr int LAUNCH_REGS = 128, CTRL_REGS = 56, SOFTMAX_REGS = 200;
+    static_assert(256 * CTRL_REGS + 256 * SOFTMAX_REGS == THREADS * LAUNCH_REGS, "register split");
     static_assert(ALLOC <= 232448, "shared memory over the 227 KB per-CTA limit");
     static_assert(ALLOC > 232448 / 2, "two CTAs per SM would contend for TMEM");
     static_assert(256 + 2 * D <= 512, "O overflows TMEM");
@@ -81,20 +89,24 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 
 struct TcWork {
     NewTokens nt;
-    int b, h, rows, start, used, split;
+    int b, h, rows, start, used;
+    int split[2];  // key split of each tile slot
     int row0[2];   // first row of each tile slot
     KeyList list;
-    int i0;        // first list entry of the split
+    int i0[2];     // first list entry of its split
     int n[2];      // key tiles each row tile visits
     int nmax;
     int p0, p1;    // positions of the unit's first and last row
     bool live;
 };
 
+template <bool DUAL>
 __device__ __forceinline__ void tc_work(const PagedParams& p, TcWork& w) {
+    constexpr int ROWS = DUAL ? kTcRows : 2 * kTcRows;
+    const int per_unit = DUAL ? (p.num_splits + 1) / 2 : p.num_splits;
     unsigned lin = blockIdx.x;
-    w.split = static_cast<int>(lin % p.num_splits);
-    lin /= p.num_splits;
+    const int si = static_cast<int>(lin % per_unit);
+    lin /= per_unit;
     // The last rows of a sequence see the most keys: they start first.
     const int unit = p.row_blocks - 1 - static_cast<int>(lin % p.row_blocks);
     lin /= p.row_blocks;
@@ -107,27 +119,27 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, TcWork& w) {
         return;
     }
     w.rows = w.nt.n * p.G;
-    const int r0 = unit * kTcRows;
+    const int r0 = unit * ROWS;
     w.live = r0 < w.rows;
     if (!w.live) return;
     w.start = w.nt.len - w.nt.n;
     w.p0 = w.start + r0 / p.G;
-    w.p1 = w.start + (min(r0 + kTcRows, w.rows) - 1) / p.G;
+    w.p1 = w.start + (min(r0 + ROWS, w.rows) - 1) / p.G;
     w.list = key_list<kTcKeys>(p.window, p.sinks, w.p0, w.p1);
     w.used = max(1, (w.list.n + p.tiles_per_split - 1) / p.tiles_per_split);
-    w.live = w.split < w.used;
+    w.live = (DUAL ? 2 * si : si) < w.used;
     if (!w.live) return;
-    w.i0 = w.split * p.tiles_per_split;
-    const int i1 = min(w.list.n, w.i0 + p.tiles_per_split);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         // Slot 0 takes the later rows, whose tile ends last: the issuer serves
-        // it first.
-        w.row0[t] = r0 + (1 - t) * 128;
-        if (w.row0[t] >= w.rows) continue;
-        const int last = w.start + (min(w.row0[t] + 128, w.rows) - 1) / p.G;
+        // it first. Dual: the same rows, splits 2 si and 2 si + 1.
+        w.split[t] = DUAL ? 2 * si + t : si;
+        w.row0[t] = DUAL ? r0 : r0 + (1 - t) * kTcRows;
+        w.i0[t] = w.split[t] * p.tiles_per_split;
+        if (w.row0[t] >= w.rows || w.split[t] >= w.used) continue;
+        const int last = w.start + (min(w.row0[t] + kTcRows, w.rows) - 1) / p.G;
         const int end = w.list.ns + max(0, last / kTcKeys + 1 - w.list.lo);
-        w.n[t] = max(0, min(i1, end) - w.i0);
+        w.n[t] = max(0, min(min(w.list.n, w.i0[t] + p.tiles_per_split), end) - w.i0[t]);
         w.nmax = max(w.nmax, w.n[t]);
     }
 }
@@ -163,9 +175,9 @@ __device__ __forceinline__ int tc_page(const PagedParams& p, const TcWork& w, co
     return id;
 }
 
-template <int D>
-__global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(const __grid_constant__ PagedParams p) {
-    using L = TcLayout<D>;
+template <int D, bool DUAL>
+__global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_kernel(const __grid_constant__ PagedParams p) {
+    using L = TcLayout<D, DUAL>;
     constexpr int BN = L::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -184,14 +196,14 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
         }
         for (int s = 0; s < L::VSTAGES; ++s) {
             mbar_init(bar(L::BAR_VFULL + s), 1);
-            mbar_init(bar(L::BAR_VEMPTY + s), 2);
+            mbar_init(bar(L::BAR_VEMPTY + s), L::CONV_WARPS);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(bar(L::BAR_HFULL + t), 2);
+            mbar_init(bar(L::BAR_HFULL + t), L::CONV_WARPS);
             mbar_init(bar(L::BAR_HEMPTY + t), 1);
-            mbar_init(bar(L::BAR_QFULL + t), 4);
+            mbar_init(bar(L::BAR_QFULL + t), p.row_warps);
             mbar_init(bar(L::BAR_SFULL + t), 1);
-            mbar_init(bar(L::BAR_PFULL + t), 4);
+            mbar_init(bar(L::BAR_PFULL + t), p.row_warps);
             mbar_init(bar(L::BAR_OFULL + t), 1);
         }
         mbar_init(bar(L::BAR_DRAIN), 1);
@@ -211,57 +223,83 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
     tc_fence_after();
     const uint32_t tmem = misc[0];
 
-    if (warp < 4) {
+    if (warp < 4 || warp >= L::CONV_WARP0) {
         setmaxnreg_dec<L::CTRL_REGS>();
         TcWork w;
-        tc_work(p, w);
+        tc_work<DUAL>(p, w);
         if (w.live && warp == 0) {
             // -------------------------------------------------------- producer
-            // Entry e: K_0; then per step j: V_j, K_{j+1}. A tile's pages are
-            // copied one by one; pages behind the sequence's end are left out.
+            // Entries in the issuer's order: K_0; then per step j: V_j, K_{j+1}.
+            // Dual: K_0 of both slots; then per step and slot V_j, K_{j+1}. A
+            // tile's pages are copied one by one; pages behind the sequence's end
+            // are left out.
             const bool leader = elect_one();
             const int* table = p.page_table + static_cast<long long>(w.b) * p.max_pages;
             const int per = BN >> p.log_page;  // pages per tile (page_size <= 128)
             const uint32_t page_bytes = static_cast<uint32_t>(D) << p.log_page;
-            auto ids_of = [&](int j) {  // lane i: page i of the tile of step j
-                return j < w.nmax && lane < per
-                           ? tc_page(p, w, table, w.list.tile(w.i0 + j) * BN + (lane << p.log_page))
+            // Page ids come 32 at a time, a lane each, the next 32 on their way: a
+            // tile's copies never wait for the page table. Batch q of a
+            // sequence holds the pages 32 q .. of its tiles in order.
+            const int log_per = __popc(per - 1);
+            auto batch_of = [&](int t, int q) {
+                const int page = 32 * q + lane, j = page >> log_per;
+                return j < (DUAL ? w.n[t] : w.nmax)
+                           ? tc_page(p, w, table, w.list.tile(w.i0[t] + j) * BN + ((page & (per - 1)) << p.log_page))
                            : -1;
             };
-            auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, int ids) {
-                const unsigned here = __ballot_sync(0xffffffffu, ids >= 0);
+            auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, int ids, int first) {
+                const unsigned here = __ballot_sync(0xffffffffu, ids >= 0 && lane >= first && lane < first + per);
                 if (leader) mbar_arrive_expect_tx(full, __popc(here) * page_bytes);
                 for (int i = 0; i < per; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, ids, i);
+                    const int id = __shfl_sync(0xffffffffu, ids, first + i);
                     if (id >= 0 && leader)
                         tma_load_2d(dst + i * page_bytes, map, full, 0, (id * p.Hkv + w.h) << p.log_page);
                 }
             };
-            int ids_k = ids_of(0), ids_v = ids_k;
             int k_issued = 0, v_issued = 0;
             bool ok = true;
-            auto load_k = [&]() -> bool {
+            auto load_k = [&](int ids, int first) -> bool {
                 const int s = k_issued % L::KSTAGES;
                 if (k_issued >= L::KSTAGES &&
                     !tc_wait_warp(bar(L::BAR_KEMPTY + s), (k_issued / L::KSTAGES - 1) & 1, p, abort_flag,
                                   kStatusWaitKvEmpty))
                     return false;
-                copy(&p.tm_k, sbase + L::K_OFF + s * L::SLOT, bar(L::BAR_KFULL + s), ids_k);
+                copy(&p.tm_k, sbase + L::K_OFF + s * L::SLOT, bar(L::BAR_KFULL + s), ids, first);
                 ++k_issued;
                 return true;
             };
-            if (w.nmax > 0) ok = load_k();
-            for (int j = 0; j < w.nmax && ok; ++j) {
-                ids_k = ids_of(j + 1);
+            auto load_v = [&](int ids, int first) -> bool {
                 const int s = v_issued % L::VSTAGES;
-                if (v_issued >= L::VSTAGES)
-                    ok = tc_wait_warp(bar(L::BAR_VEMPTY + s), (v_issued / L::VSTAGES - 1) & 1, p, abort_flag,
-                                      kStatusWaitKvEmpty);
-                if (!ok) break;
-                copy(&p.tm_v, sbase + L::V_OFF + s * L::SLOT, bar(L::BAR_VFULL + s), ids_v);
+                if (v_issued >= L::VSTAGES &&
+                    !tc_wait_warp(bar(L::BAR_VEMPTY + s), (v_issued / L::VSTAGES - 1) & 1, p, abort_flag,
+                                  kStatusWaitKvEmpty))
+                    return false;
+                copy(&p.tm_v, sbase + L::V_OFF + s * L::SLOT, bar(L::BAR_VFULL + s), ids, first);
                 ++v_issued;
-                if (j + 1 < w.nmax) ok = load_k();
-                ids_v = ids_k;
+                return true;
+            };
+            constexpr int SEQS = DUAL ? 2 : 1;  // sequences of tiles
+            int cur[SEQS], next[SEQS];          // the batch of the tile whose V comes next, and the one behind it
+#pragma unroll
+            for (int t = 0; t < SEQS; ++t) {
+                cur[t] = batch_of(t, 0);
+                next[t] = batch_of(t, 1);
+                if (ok && (DUAL ? w.n[t] : w.nmax) > 0) ok = load_k(cur[t], 0);
+            }
+            for (int j = 0; j < w.nmax && ok; ++j) {
+                const int first = (j << log_per) & 31;        // of tile j in its batch
+                const int first_next = (first + per) & 31;    // of tile j + 1
+#pragma unroll
+                for (int t = 0; t < SEQS; ++t) {
+                    const int n = DUAL ? w.n[t] : w.nmax;
+                    if (!ok || j >= n) continue;
+                    ok = load_v(cur[t], first);
+                    if (first_next == 0) {
+                        cur[t] = next[t];
+                        next[t] = batch_of(t, ((j + 1) << log_per >> 5) + 1);
+                    }
+                    if (ok && j + 1 < n) ok = load_k(cur[t], first_next);
+                }
             }
             if (ok) {
                 // No arrival may be in flight when the CTA exits.
@@ -290,7 +328,7 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
                 return (static_cast<uint64_t>(hi) << 32) | (lo + (off >> 4));
             };
             auto issue_s = [&](int t, int slot) {
-                const uint32_t qa = L::Q_OFF + t * L::Q_TILE, kb = L::K_OFF + slot * L::SLOT;
+                const uint32_t qa = L::Q_OFF + (DUAL ? 0 : t) * L::Q_TILE, kb = L::K_OFF + slot * L::SLOT;
 #pragma unroll
                 for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -315,90 +353,135 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
                 ++k_used;
                 return r;
             };
-            bool ok = wait_k();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (ok && w.n[t] > 0) {
-                    ok = tc_wait_warp(bar(L::BAR_QFULL + t), 0, p, abort_flag, kStatusWaitQ);
-                    if (!ok) break;
+            bool ok = true;
+            if constexpr (DUAL) {
+                int v_used = 0;  // V entries waited for
+                // S of slot t from the next K entry.
+                auto next_s = [&](int t) -> bool {
+                    const int slot = k_used % L::KSTAGES;
+                    if (!wait_k()) return false;
                     tc_fence_after();
-                    issue_s(t, 0);
+                    issue_s(t, slot);
+                    if (leader) umma_commit(bar(L::BAR_KEMPTY + slot));
+                    return true;
+                };
+                ok = tc_wait_warp(bar(L::BAR_QFULL + 0), 0, p, abort_flag, kStatusWaitQ);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (ok && w.n[t] > 0) ok = next_s(t);
+                for (int j = 0; j < w.nmax && ok; ++j) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || j >= w.n[t]) continue;
+                        const int buf = v_used & 1;
+                        ok = tc_wait_warp(bar(L::BAR_HFULL + buf), (v_used >> 1) & 1, p, abort_flag, kStatusWaitKvFull);
+                        if (ok) ok = tc_wait_warp(bar(L::BAR_PFULL + t), j & 1, p, abort_flag, kStatusWaitP);
+                        if (!ok) break;
+                        ++v_used;
+                        tc_fence_after();
+                        issue_pv(t, buf, j > 0);
+                        if (leader) umma_commit(bar(L::BAR_HEMPTY + buf));
+                        if (j + 1 < w.n[t]) ok = next_s(t);
+                        else if (leader) umma_commit(bar(L::BAR_OFULL + t));
+                    }
                 }
-            }
-            if (ok && leader) umma_commit(bar(L::BAR_KEMPTY + 0));
-            for (int j = 0; j < w.nmax && ok; ++j) {
-                const int buf = j & 1;
-                const bool k_next = j + 1 < w.nmax;
-                const int sk = (j + 1) % L::KSTAGES;
-                bool have_k = false, have_v = false;
+            } else {
+                ok = wait_k();
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (!ok || j >= w.n[t]) continue;
-                    if (!have_v) {
-                        ok = tc_wait_warp(bar(L::BAR_HFULL + buf), (j >> 1) & 1, p, abort_flag, kStatusWaitKvFull);
-                        have_v = true;
-                    }
-                    if (ok) ok = tc_wait_warp(bar(L::BAR_PFULL + t), j & 1, p, abort_flag, kStatusWaitP);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(t, buf, j > 0);
-                    if (k_next && !have_k) {
-                        ok = wait_k();
-                        have_k = true;
+                    if (ok && w.n[t] > 0) {
+                        ok = tc_wait_warp(bar(L::BAR_QFULL + t), 0, p, abort_flag, kStatusWaitQ);
                         if (!ok) break;
                         tc_fence_after();
+                        issue_s(t, 0);
                     }
-                    if (j + 1 < w.n[t]) issue_s(t, sk);
-                    else if (leader) umma_commit(bar(L::BAR_OFULL + t));
                 }
-                if (!ok) break;
-                if (leader) umma_commit(bar(L::BAR_HEMPTY + buf));
-                if (k_next && leader) umma_commit(bar(L::BAR_KEMPTY + sk));
+                if (ok && leader) umma_commit(bar(L::BAR_KEMPTY + 0));
+                for (int j = 0; j < w.nmax && ok; ++j) {
+                    const int buf = j & 1;
+                    const bool k_next = j + 1 < w.nmax;
+                    const int sk = (j + 1) % L::KSTAGES;
+                    bool have_k = false, have_v = false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || j >= w.n[t]) continue;
+                        if (!have_v) {
+                            ok = tc_wait_warp(bar(L::BAR_HFULL + buf), (j >> 1) & 1, p, abort_flag, kStatusWaitKvFull);
+                            have_v = true;
+                        }
+                        if (ok) ok = tc_wait_warp(bar(L::BAR_PFULL + t), j & 1, p, abort_flag, kStatusWaitP);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(t, buf, j > 0);
+                        if (k_next && !have_k) {
+                            ok = wait_k();
+                            have_k = true;
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        if (j + 1 < w.n[t]) issue_s(t, sk);
+                        else if (leader) umma_commit(bar(L::BAR_OFULL + t));
+                    }
+                    if (!ok) break;
+                    if (leader) umma_commit(bar(L::BAR_HEMPTY + buf));
+                    if (k_next && leader) umma_commit(bar(L::BAR_KEMPTY + sk));
+                }
             }
             if (leader) umma_commit(bar(L::BAR_DRAIN));
             tc_wait(bar(L::BAR_DRAIN), 0, p, abort_flag, kStatusWaitDrain, false);
-        } else if (w.live && warp >= 2) {
+        } else if (w.live && warp >= L::CONV_WARP0) {
             // -------------------------------------------------------- converters
             // Eight rows a quarter warp apart in their swizzle, so loads and
             // stores are free of bank conflicts. A key that no row of the unit
             // sees becomes zeros: its slot may never have been written, and a
             // weight of zero does not undo a NaN.
-            constexpr int UNITS = D / 16;  // 16-code units per key
+            // A lane converts one 16-code unit u of every ROW_STEP-th key from row0
+            // on: its addresses are a register and constants.
+            constexpr int ROW_STEP = D == 64 ? 32 : 16, PIECES = BN / ROW_STEP;
+            const int r8 = lane & 7, cw = warp - L::CONV_WARP0;
+            const int u = D == 64 ? lane >> 3 : (cw & 1) * 4 + (lane >> 3);
+            const int row0 = (D == 64 ? cw : cw >> 1) * 8 + r8;
+            const uint32_t src_lane = sbase + L::V_OFF + row0 * L::ROW_BYTES +
+                                      ((D == 64 ? u ^ (r8 >> 1) : u ^ r8) << 4);
+            const uint32_t dst_lane = sbase + L::V16_OFF + (u >> 2) * (BN * 128) + row0 * 128 +
+                                      (((2 * (u & 3)) ^ r8) << 4);
+            const int entries = DUAL ? w.n[0] + w.n[1] : w.nmax;
+            const int both = 2 * min(w.n[0], w.n[1]);  // dual: entries that alternate between the slots
             bool ok = true;
-            for (int j = 0; j < w.nmax && ok; ++j) {
-                const int s = j % L::VSTAGES, buf = j & 1;
-                if (j >= 2) ok = tc_wait_warp(bar(L::BAR_HEMPTY + buf), ((j >> 1) - 1) & 1, p, abort_flag, kStatusWaitKvEmpty);
-                if (ok) ok = tc_wait_warp(bar(L::BAR_VFULL + s), (j / L::VSTAGES) & 1, p, abort_flag, kStatusWaitKvFull);
+            for (int e = 0; e < entries && ok; ++e) {
+                const int s = e % L::VSTAGES, buf = e & 1;
+                if (e >= 2)
+                    ok = tc_wait_warp(bar(L::BAR_HEMPTY + buf), ((e >> 1) - 1) & 1, p, abort_flag, kStatusWaitKvEmpty);
+                if (ok)
+                    ok = tc_wait_warp(bar(L::BAR_VFULL + s), (e / L::VSTAGES) & 1, p, abort_flag, kStatusWaitKvFull);
                 if (!ok) break;
-                const int key0 = w.list.tile(w.i0 + j) * BN;
-                const bool whole = key0 + BN - 1 <= w.p1 && (p.window <= 0 || key0 > w.p0 - p.window || key0 + BN <= p.sinks);
-                const uint32_t src = sbase + L::V_OFF + s * L::SLOT, dst = sbase + L::V16_OFF + buf * L::V16;
-                const int r8 = lane & 7;
-#pragma unroll 4
-                for (int i = (warp - 2) * 4 + (lane >> 3); i < (BN / 8) * UNITS; i += 8) {
-                    const int u = i % UNITS, r = (i / UNITS) * 8 + r8;
-                    const uint32_t at = D == 64 ? src + r * 64 + ((u ^ ((r >> 1) & 3)) << 4)
-                                                : src + r * 128 + ((u ^ r8) << 4);
-                    uint32_t c[4];
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
-                                 : "r"(at)
-                                 : "memory");
-                    if (!whole) {
-                        const int key = key0 + r;
-                        const bool seen = key <= w.p1 && (p.window <= 0 || key > w.p0 - p.window || key < p.sinks);
-                        if (!seen) c[0] = c[1] = c[2] = c[3] = 0u;
-                    }
-                    uint32_t f[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        f[2 * k] = decode_e4m3x2_f16(static_cast<uint16_t>(c[k] & 0xffffu));
-                        f[2 * k + 1] = decode_e4m3x2_f16(static_cast<uint16_t>(c[k] >> 16));
-                    }
-                    const uint32_t line = dst + (u >> 2) * (BN * 128) + r * 128;
-                    st_shared_v4(line + (((2 * (u & 3)) ^ r8) << 4), f[0], f[1], f[2], f[3]);
-                    st_shared_v4(line + (((2 * (u & 3) + 1) ^ r8) << 4), f[4], f[5], f[6], f[7]);
+                int at_list = w.i0[0] + e;
+                if constexpr (DUAL) {
+                    const int t = e < both ? e & 1 : (w.n[1] > w.n[0] ? 1 : 0);
+                    const int j = e < both ? e >> 1 : e - both / 2;
+                    at_list = (t ? w.i0[1] : w.i0[0]) + j;
                 }
+                const int key0 = w.list.tile(at_list) * BN;
+                const bool whole = key0 + BN - 1 <= w.p1 && (p.window <= 0 || key0 > w.p0 - p.window || key0 + BN <= p.sinks);
+                const uint32_t src = src_lane + s * L::SLOT, dst = dst_lane + buf * L::V16;
+                // Four pieces' loads are in flight before the first is converted.
+                static_for<PIECES / 4>([&](auto batch) {
+                    constexpr int P0 = decltype(batch)::value * 4;
+                    uint32_t c[4][4];
+                    static_for<4>([&](auto k) { ld_shared_v4_at<(P0 + k) * ROW_STEP * L::ROW_BYTES>(c[k], src); });
+                    static_for<4>([&](auto k) {
+                        if (!whole) {
+                            const int key = key0 + row0 + (P0 + k) * ROW_STEP;
+                            const bool seen = key <= w.p1 && (p.window <= 0 || key > w.p0 - p.window || key < p.sinks);
+                            if (!seen) c[k][0] = c[k][1] = c[k][2] = c[k][3] = 0u;
+                        }
+                        uint32_t f[8];
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4) decode_e4m3x4_f16(c[k][e4], f[2 * e4], f[2 * e4 + 1]);
+                        st_shared_v4_at<(P0 + k) * ROW_STEP * 128>(dst, f[0], f[1], f[2], f[3]);
+                        st_shared_v4_at<(P0 + k) * ROW_STEP * 128>(dst ^ 16u, f[4], f[5], f[6], f[7]);
+                    });
+                });
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -407,20 +490,26 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
                 }
             }
             // The issuer's last releases must have arrived before the CTA exits.
-            for (int j = max(0, w.nmax - 2); j < w.nmax && ok; ++j)
-                ok = tc_wait_warp(bar(L::BAR_HEMPTY + (j & 1)), (j >> 1) & 1, p, abort_flag, kStatusWaitKvEmpty);
+            for (int e = max(0, entries - 2); e < entries && ok; ++e)
+                ok = tc_wait_warp(bar(L::BAR_HEMPTY + (e & 1)), (e >> 1) & 1, p, abort_flag, kStatusWaitKvEmpty);
         }
     } else {
         // ------------------------------------------------------------ softmax
         setmaxnreg_inc<L::SOFTMAX_REGS>();
         TcWork w;
-        tc_work(p, w);
+        tc_work<DUAL>(p, w);
         const int t = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const int n = t ? w.n[1] : w.n[0];
         const int first_row = t ? w.row0[1] : w.row0[0];
-        if (w.live && first_row < w.rows) {
+        const int split = t ? w.split[1] : w.split[0];
+        const int i0 = t ? w.i0[1] : w.i0[0];
+        // Warps of a tile that no sequence of the call has rows for (20 of 128 rows:
+        // three of four) leave their lanes of Q, S and P as they are: those rows
+        // of O mean nothing and are not read. They take no part in the barriers
+        // either; polling them would slow the others' shared-memory traffic.
+        if (w.live && first_row < w.rows && split < w.used && quarter < p.row_warps) {
             const int row = first_row + r;
             const bool row_ok = row < w.rows;
             const int i = (row_ok ? row : w.rows - 1) / p.G;
@@ -444,7 +533,7 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
                 rowf *= 1.f / f;
                 const uint32_t hi_at = sbase + L::Q_OFF + t * L::Q_TILE + r * L::ROW_BYTES;
 #pragma unroll 2
-                for (int u = 0; u < D / 16; ++u) {
+                for (int u = 0; u < (DUAL && t == 1 ? 0 : D / 16); ++u) {
                     float x[16];
                     float(&x0)[8] = *reinterpret_cast<float(*)[8]>(x);
                     float(&x1)[8] = *reinterpret_cast<float(*)[8]>(x + 8);
@@ -473,95 +562,183 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
             const uint32_t tO = tmem + lane_field + L::O_COL(t);
             const int* table = p.page_table + static_cast<long long>(w.b) * p.max_pages;
             // Scales of the next tile, 16-key group `lane & 7` per lane, loaded a
-            // tile ahead; the page ids two tiles ahead.
-            auto id_of = [&](int j) {
-                return j < n ? tc_page(p, w, table, w.list.tile(w.i0 + j) * BN + 16 * (lane & 7)) : -1;
+            // tile ahead; the page-table entries two tiles ahead, and looked at
+            // only then (a test right behind the load would wait for it).
+            auto entry_of = [&](int j) {
+                const int key = j < n ? w.list.tile(i0 + j) * BN + 16 * (lane & 7) : w.nt.len;
+                return key < w.nt.len ? table[key >> p.log_page] : -1;
             };
             auto scales_of = [&](int id, float& ks, float& vs) {
+                // (The producer reports bad entries.)
+                const bool have = id >= 0 && id < p.num_pages;
                 const long long cell = static_cast<long long>(id) * p.Hkv + w.h;
-                ks = id >= 0 ? p.k_scale[cell] : 1.f;
-                vs = id >= 0 ? p.v_scale[cell] : 1.f;
+                ks = have ? p.k_scale[cell] : 1.f;
+                vs = have ? p.v_scale[cell] : 1.f;
             };
             float ks_next, vs_next;
-            scales_of(id_of(0), ks_next, vs_next);
-            int id_next = id_of(1);
+            scales_of(entry_of(0), ks_next, vs_next);
+            int id_next = entry_of(1);
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < n; ++j) {
+                // The groups' factors, before the wait for S: a shuffle between the
+                // exponentials would hold each group up.
                 const float ks = ks_next, lv = log2f(vs_next), iv = 1.f / vs_next;
+                float kg[BN / 16], vg[BN / 16], ig[BN / 16];
+                if constexpr (!DUAL) {
+#pragma unroll
+                    for (int g = 0; g < BN / 16; ++g) {
+                        kg[g] = __shfl_sync(0xffffffffu, ks, g) * rowf;
+                        vg[g] = __shfl_sync(0xffffffffu, lv, g);
+                        ig[g] = __shfl_sync(0xffffffffu, iv, g);
+                    }
+                }
                 scales_of(id_next, ks_next, vs_next);
-                id_next = id_of(j + 2);
+                id_next = entry_of(j + 2);
                 ok = tc_wait_warp(bar(L::BAR_SFULL + t), j & 1, p, abort_flag, kStatusWaitS);
                 if (!ok) break;
                 tc_fence_after();
-                float s[BN];
-#pragma unroll
-                for (int cc = 0; cc < BN / 32; ++cc) {
-                    uint32_t raw[32];
-                    tmem_ld32(tS + cc * 32, raw);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(raw[e]);
-                }
-                tmem_wait_ld();
-                const int key0 = w.list.tile(w.i0 + j) * BN;
+                const int key0 = w.list.tile(i0 + j) * BN;
                 const int valid = pos - key0 + 1;
-                if (valid < BN) {
+                float top = -INFINITY, m_new = m, m_use = 0.f, alpha = 1.f, sum = 0.f;
+                auto reference = [&] {
+                    const bool move = top > m + kPSlack;
+                    m_new = move ? top : m;
+                    m_use = m_new == -INFINITY ? 0.f : m_new;
+                    alpha = move ? ex2(m - m_use) : 1.f;
+                };
+                if constexpr (DUAL) {
+                    // 32 columns of S at a time, read twice (for the maximum, then for
+                    // the exponentials), in loops that are not unrolled: where few
+                    // warps run this code, long straight stretches of it wait for
+                    // their instructions (20 rows: 120 us against 140; the other way
+                    // round for full tiles, 2 x 2048 tokens over 16384 keys: 395
+                    // against 328).
+                    const bool whole = __all_sync(0xffffffffu, valid >= BN && (p.window <= 0 || valid <= p.window ||
+                                                                                p.sinks - key0 >= BN));
+                    auto chunk = [&](int cc, float (&s)[32], float (&kc)[2], float (&vc)[2]) {
+                        uint32_t raw[32];
+                        tmem_ld32(tS + cc * 32, raw);
 #pragma unroll
-                    for (int c = 0; c < BN; ++c)
-                        if (c >= valid) s[c] = -INFINITY;
-                }
-                if (p.window > 0) {
-                    const int from = valid - p.window, sink = p.sinks - key0;
-                    if (from > 0 && sink < BN) {
+                        for (int g = 0; g < 2; ++g) {
+                            kc[g] = __shfl_sync(0xffffffffu, ks, 2 * cc + g) * rowf;
+                            vc[g] = __shfl_sync(0xffffffffu, lv, 2 * cc + g);
+                        }
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(raw[e]);
+                        if (!whole) {
+                            const int end = valid - 32 * cc, from = p.window > 0 ? end - p.window : 0;
+                            const int sink = p.sinks - key0 - 32 * cc;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (c >= end || (c < from && c >= sink)) s[c] = -INFINITY;
+                        }
+                    };
+#pragma unroll 1
+                    for (int cc = 0; cc < BN / 32; ++cc) {
+                        float s[32], kc[2], vc[2];
+                        chunk(cc, s, kc, vc);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            float a = max3f(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
+                            float b = max3f(s[16 * g + 3], s[16 * g + 4], s[16 * g + 5]);
+                            a = max3f(a, s[16 * g + 6], s[16 * g + 7]);
+                            b = max3f(b, s[16 * g + 8], s[16 * g + 9]);
+                            a = max3f(a, s[16 * g + 10], s[16 * g + 11]);
+                            b = max3f(b, s[16 * g + 12], s[16 * g + 13]);
+                            a = max3f(a, s[16 * g + 14], s[16 * g + 15]);
+                            top = fmaxf(top, fmaf(fmaxf(a, b), kc[g], vc[g]));
+                        }
+                    }
+                    reference();
+#pragma unroll 1
+                    for (int cc = 0; cc < BN / 32; ++cc) {
+                        float s[32], kc[2], vc[2];
+                        chunk(cc, s, kc, vc);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const float ng = vc[g] - m_use + kPShift;
+                            const uint64_t k2 = f2pack(kc[g], kc[g]), n2 = f2pack(ng, ng);
+                            uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int c = 16 * g + 2 * e;
+                                float x0, x1;
+                                f2unpack(ffma2(f2pack(s[c], s[c + 1]), k2, n2), x0, x1);
+                                const float e0 = ex2(x0), e1 = ex2(x1);
+                                part[e & 1] = fadd2(part[e & 1], f2pack(e0, e1));
+                                pk[8 * g + e] = pack_f16x2(e0, e1);
+                            }
+                            float a, b;
+                            f2unpack(fadd2(part[0], part[1]), a, b);
+                            sum = fmaf(a + b, __shfl_sync(0xffffffffu, iv, 2 * cc + g), sum);
+                        }
+                        // P's 16 columns lie over S columns that have been read.
+                        tmem_st16(tS + cc * 16, pk);
+                    }
+                } else {
+                    float s[BN];
+#pragma unroll
+                    for (int cc = 0; cc < BN / 32; ++cc) {
+                        uint32_t raw[32];
+                        tmem_ld32(tS + cc * 32, raw);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(raw[e]);
+                    }
+                    tmem_wait_ld();
+                    if (valid < BN) {
 #pragma unroll
                         for (int c = 0; c < BN; ++c)
-                            if (c < from && c >= sink) s[c] = -INFINITY;
+                            if (c >= valid) s[c] = -INFINITY;
                     }
-                }
-                __syncwarp();
-                // Row maximum of x = s (rowf ks) + log2 vs, group by group.
-                float top = -INFINITY;
+                    if (p.window > 0) {
+                        const int from = valid - p.window, sink = p.sinks - key0;
+                        if (from > 0 && sink < BN) {
 #pragma unroll
-                for (int g = 0; g < BN / 16; ++g) {
-                    const float kg = __shfl_sync(0xffffffffu, ks, g) * rowf, vg = __shfl_sync(0xffffffffu, lv, g);
-                    float a = max3f(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
-                    float b = max3f(s[16 * g + 3], s[16 * g + 4], s[16 * g + 5]);
-                    a = max3f(a, s[16 * g + 6], s[16 * g + 7]);
-                    b = max3f(b, s[16 * g + 8], s[16 * g + 9]);
-                    a = max3f(a, s[16 * g + 10], s[16 * g + 11]);
-                    b = max3f(b, s[16 * g + 12], s[16 * g + 13]);
-                    a = max3f(a, s[16 * g + 14], s[16 * g + 15]);
-                    top = fmaxf(top, fmaf(fmaxf(a, b), kg, vg));
-                }
-                const bool move = top > m + kPSlack;
-                const float m_new = move ? top : m;
-                const float m_use = m_new == -INFINITY ? 0.f : m_new;
-                const float alpha = move ? ex2(m - m_use) : 1.f;
-                float sum = 0.f;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int gg = 0; gg < 4; ++gg) {
-                        const int g = 4 * h + gg;
-                        const float kg = __shfl_sync(0xffffffffu, ks, g) * rowf;
-                        const float ng = __shfl_sync(0xffffffffu, lv, g) - m_use + kPShift;
-                        const uint64_t k2 = f2pack(kg, kg), n2 = f2pack(ng, ng);
-                        uint64_t part[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int c = 16 * g + 2 * e;
-                            float x0, x1;
-                            f2unpack(ffma2(f2pack(s[c], s[c + 1]), k2, n2), x0, x1);
-                            const float e0 = ex2(x0), e1 = ex2(x1);
-                            part[e & 1] = fadd2(part[e & 1], f2pack(e0, e1));
-                            pk[8 * gg + e] = pack_f16x2(e0, e1);
+                            for (int c = 0; c < BN; ++c)
+                                if (c < from && c >= sink) s[c] = -INFINITY;
                         }
-                        float a, b;
-                        f2unpack(fadd2(part[0], part[1]), a, b);
-                        sum = fmaf(a + b, __shfl_sync(0xffffffffu, iv, g), sum);
                     }
-                    tmem_st32(tS + h * 32, pk);
+                    __syncwarp();
+                    // Row maximum of x = s (rowf ks) + log2 vs, group by group.
+#pragma unroll
+                    for (int g = 0; g < BN / 16; ++g) {
+                        float a = max3f(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
+                        float b = max3f(s[16 * g + 3], s[16 * g + 4], s[16 * g + 5]);
+                        a = max3f(a, s[16 * g + 6], s[16 * g + 7]);
+                        b = max3f(b, s[16 * g + 8], s[16 * g + 9]);
+                        a = max3f(a, s[16 * g + 10], s[16 * g + 11]);
+                        b = max3f(b, s[16 * g + 12], s[16 * g + 13]);
+                        a = max3f(a, s[16 * g + 14], s[16 * g + 15]);
+                        top = fmaxf(top, fmaf(fmaxf(a, b), kg[g], vg[g]));
+                    }
+                    reference();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int gg = 0; gg < 4; ++gg) {
+                            const int g = 4 * h + gg;
+                            const float ng = vg[g] - m_use + kPShift;
+                            const uint64_t k2 = f2pack(kg[g], kg[g]), n2 = f2pack(ng, ng);
+                            uint64_t part[2] = {0ull, 0ull};
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int c = 16 * g + 2 * e;
+                                float x0, x1;
+                                f2unpack(ffma2(f2pack(s[c], s[c + 1]), k2, n2), x0, x1);
+                                const float e0 = ex2(x0), e1 = ex2(x1);
+                                part[e & 1] = fadd2(part[e & 1], f2pack(e0, e1));
+                                pk[8 * gg + e] = pack_f16x2(e0, e1);
+                            }
+                            float a, b;
+                            f2unpack(fadd2(part[0], part[1]), a, b);
+                            sum = fmaf(a + b, ig[g], sum);
+                        }
+                        tmem_st32(tS + h * 32, pk);
+                    }
                 }
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     const uint64_t ax2 = f2pack(alpha, alpha);
@@ -593,7 +770,7 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
             }
             if (ok) {
                 const float f = w.used == 1 ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-                const long long at = static_cast<long long>(w.split) * p.total_q * p.H + out_row;
+                const long long at = static_cast<long long>(split) * p.total_q * p.H + out_row;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -643,31 +820,34 @@ __global__ void __launch_bounds__(TcLayout<D>::THREADS, 1) fa_paged_tc_kernel(co
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, bool DUAL>
 cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
-    using L = TcLayout<D>;
+    using L = TcLayout<D, DUAL>;
     static ContextCache<int> attr_set;
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         // The setmaxnreg split is sized for exactly LAUNCH_REGS per thread.
         cudaFuncAttributes a;
-        cudaError_t err = cudaFuncGetAttributes(&a, fa_paged_tc_kernel<D>);
+        cudaError_t err = cudaFuncGetAttributes(&a, fa_paged_tc_kernel<D, DUAL>);
         if (err != cudaSuccess) return err;
         if (a.numRegs != L::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
         *out = 1;
-        return cudaFuncSetAttribute(fa_paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_paged_tc_kernel<D, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    const int per_unit = DUAL ? (p.num_splits + 1) / 2 : p.num_splits;
+    const long long ctas = static_cast<long long>(p.B) * p.Hkv * per_unit * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(fa_paged_tc_kernel<D>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC, stream, p);
+    return launch_dependent(fa_paged_tc_kernel<D, DUAL>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
+                            stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream) {
-    return d == 64 ? launch_tc<64>(p, stream) : launch_tc<128>(p, stream);
+    if (p.dual) return d == 64 ? launch_tc<64, true>(p, stream) : launch_tc<128, true>(p, stream);
+    return d == 64 ? launch_tc<64, false>(p, stream) : launch_tc<128, false>(p, stream);
 }
 
 }  // namespace fa

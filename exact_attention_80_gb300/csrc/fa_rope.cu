@@ -36,7 +36,8 @@ struct RopeLaunch {
 
 constexpr int kRopeThreads = 256;
 
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_constant__ RopeLaunch p) {
+template <bool SPLIT>
+__global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_constant__ RopeLaunch p) {
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
     const int v = threadIdx.x & ((1 << p.log_parts) - 1);
@@ -44,14 +45,17 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     const long long tok = (static_cast<long long>(blockIdx.x) << p.log_tb) + (rest & ((1 << p.log_tb) - 1));
     const int hs = rest >> p.log_tb;
     const int hstep = kRopeThreads >> (p.log_parts + p.log_tb);
-    if (tok >= p.tokens) return;
-    if (!rope_positions_ok(p.r, tok, 0)) {
+    const bool turn = v < (p.r.rot >> 4);
+    float c[8], s[8];
+    const bool in = tok < p.tokens;
+    bool ok = true;
+    if (in && turn) ok = rope_coeffs<SPLIT>(p.r, v, tok, 0, c, s);
+    ok = token_ok(ok, p.log_parts);
+    if (!in) return;
+    if (!ok) {
         if (v == 0 && hs == 0 && blockIdx.y == 0) atomicOr(p.status, kStatusBadPosition);
         return;
     }
-    const bool turn = v < (p.r.rot >> 4);
-    float c[8], s[8];
-    if (turn) rope_coeffs(p.r, v, tok, 0, c, s);
     const long long b = tok / p.N;
     const long long n = tok - b * p.N;
     const int lo = blockIdx.y * p.heads_chunk;
@@ -155,6 +159,7 @@ extern "C" fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, c
     p.heads_chunk = chunk;
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
     const dim3 grid(static_cast<unsigned>(bx), static_cast<unsigned>((heads + chunk - 1) / chunk), 1);
-    const cudaError_t e = fa::launch_dependent(fa::fa_rope_kernel, grid, fa::kRopeThreads, 0, stream, p);
+    const cudaError_t e = fa::launch_dependent(
+        fa::rope_split(p.r) ? fa::fa_rope_kernel<true> : fa::fa_rope_kernel<false>, grid, fa::kRopeThreads, 0, stream, p);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

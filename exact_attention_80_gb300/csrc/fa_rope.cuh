@@ -41,30 +41,23 @@ __device__ __forceinline__ void rope_columns(const RopeParams& r, int v, int& c0
     c1 = (pair && !r.interleaved) ? 8 * v + (r.rot >> 1) : 16 * v + 8;
 }
 
-// Whether every position of token `tok` lies in the table; `own_pos` stands in
-// where there is no position array.
-__device__ __forceinline__ bool rope_positions_ok(const RopeParams& r, long long tok, int own_pos) {
-    if (!r.table) return true;
-    if (!r.positions) return own_pos >= 0 && own_pos < r.max_pos;
-    bool ok = true;
-    for (int a = 0; a < r.axes; ++a) {
-        const int p = r.positions[a * r.pos_stride + tok];
-        ok = ok && p >= 0 && p < r.max_pos;
-    }
-    return ok;
-}
-
-// Cosines and (signed) sines of pairs 8 v .. 8 v + 7 of token `tok`, whose
-// positions are known to be in the table.
-__device__ __forceinline__ void rope_coeffs(const RopeParams& r, int v, long long tok, int own_pos,
+// Cosines and (signed) sines of pairs 8 v .. 8 v + 7 of token `tok` (own_pos
+// stands in where there is no position array). False where a position of these
+// pairs is outside the table, which is then not read. SPLIT: sections may end
+// inside the eight pairs (rope_split); without it they share one axis, and the
+// table is read in 16-byte pieces.
+template <bool SPLIT>
+__device__ __forceinline__ bool rope_coeffs(const RopeParams& r, int v, long long tok, int own_pos,
                                             float (&c)[8], float (&s)[8]) {
     const int i0 = 8 * v;
     const int half = r.rot >> 1;
     int a = 0;
     while (a + 1 < r.axes && i0 >= r.sec_end[a]) ++a;
-    if (r.axes == 1 || i0 + 8 <= r.sec_end[a]) {
-        const long long pos = r.positions ? r.positions[a * r.pos_stride + tok] : own_pos;
-        const float* row = r.table + pos * r.rot + i0;
+    const int* at = r.positions + a * r.pos_stride + tok;
+    if constexpr (!SPLIT) {
+        const int pos = r.positions ? *at : own_pos;
+        if (static_cast<unsigned>(pos) >= static_cast<unsigned>(r.max_pos)) return false;
+        const float* row = r.table + static_cast<long long>(pos) * r.rot + i0;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float4 x = reinterpret_cast<const float4*>(row)[k];
@@ -72,17 +65,30 @@ __device__ __forceinline__ void rope_coeffs(const RopeParams& r, int v, long lon
             c[4 * k] = x.x, c[4 * k + 1] = x.y, c[4 * k + 2] = x.z, c[4 * k + 3] = x.w;
             s[4 * k] = y.x, s[4 * k + 1] = y.y, s[4 * k + 2] = y.z, s[4 * k + 3] = y.w;
         }
-    } else {  // a section ends inside these pairs
+    } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            while (a + 1 < r.axes && i0 + k >= r.sec_end[a]) ++a;
-            const float* row = r.table + static_cast<long long>(r.positions[a * r.pos_stride + tok]) * r.rot + i0 + k;
+            while (a + 1 < r.axes && i0 + k >= r.sec_end[a]) {
+                ++a;
+                at += r.pos_stride;
+            }
+            if (static_cast<unsigned>(*at) >= static_cast<unsigned>(r.max_pos)) return false;
+            const float* row = r.table + static_cast<long long>(*at) * r.rot + i0 + k;
             c[k] = row[0];
             s[k] = row[half];
         }
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) s[k] *= r.sign;
+    return true;
+}
+
+// Whether `ok` holds for all threads of a token, 2^log_parts neighbours of a
+// warp whose threads all come here.
+__device__ __forceinline__ bool token_ok(bool ok, int log_parts) {
+    const unsigned bad = __ballot_sync(0xffffffffu, !ok);
+    const unsigned mine = ((1u << (1 << log_parts)) - 1u) << (threadIdx.x & 31 & ~((1 << log_parts) - 1));
+    return (bad & mine) == 0u;
 }
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& u, float (&x)[8]) {
@@ -157,6 +163,12 @@ __device__ __forceinline__ void rope_heads(const RopeParams& r, int v, bool turn
     }
 }
 
+// Host side: whether a section ends inside a thread's eight pairs.
+inline bool rope_split(const RopeParams& r) {
+    for (int a = 0; a + 1 < r.axes; ++a)
+        if (r.sec_end[a] % 8 != 0) return true;
+    return false;
+}
 // Host side: checks a rotation's description (fa_rope.cu).
 fa_status check_rope(const fa_rotation* rope, int d, long long tokens);
 RopeParams rope_params(const fa_rotation* rope, long long tokens, bool inverse);

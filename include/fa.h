@@ -297,7 +297,7 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
  * (dQ is summed over key tiles by fp32 atomics, so its last bits can differ
  * between runs). workspace: fa_bwd_window_workspace_bytes, 16-byte aligned.
  */
-size_t fa_bwd_window_workspace_bytes(int B, int H, int Nq, int d);
+size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks);
 fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
                         const float* lse, void* dq, void* dk, void* dv, void* workspace, int B, int H, int Hkv,
                         int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream);
