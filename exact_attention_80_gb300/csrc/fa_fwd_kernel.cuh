@@ -33,6 +33,7 @@ cudaError_t launch_fwd(const FwdParams& p, unsigned grid, cudaStream_t stream) {
         std::conditional_t<F8, std::conditional_t<D == 256, LayoutTP<D, true>, LayoutTM<D, true>>, FwdLayout<D>>>;
     constexpr auto kernel = [] {
         if constexpr (WIN && D == 256) return fa_fwd_tpw_kernel<D>;
+        else if constexpr (WIN && PERSIST) return fa_fwd_tmwp_kernel<D>;
         else if constexpr (WIN) return fa_fwd_tmw_kernel<D>;
         else if constexpr (M64) return fa_fwd_tm64_kernel<D>;
         else if constexpr (PERSIST && F8) return fa_fwd_tmp8_kernel<D>;

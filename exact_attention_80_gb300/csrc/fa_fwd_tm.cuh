@@ -699,12 +699,12 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
       if constexpr (L::REG_SPLIT) setmaxnreg_dec<L::CTRL_REGS>();
       // The work record is derived inside each role, after its register limit
       // is set, so that no role carries fields it does not use.
-      if constexpr (PERSIST) {
+      if constexpr (WIN) {
+        tm_window_control<D, L, PERSIST>(p, sbase, tmem, abort_flag, warp);
+      } else if constexpr (PERSIST) {
         tm_persist_control<D, F8>(p, sbase, tmem, abort_flag, warp);
       } else if constexpr (DUAL) {
         tm_dual_control<D, F8>(p, sbase, tmem, abort_flag, warp);
-      } else if constexpr (WIN) {
-        tm_window_control<D, L>(p, sbase, tmem, abort_flag, warp);
       } else {
       Work<QT> w;
       compute_work<QT, BN>(p, blockIdx.x, w);
@@ -1006,6 +1006,35 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
             ok = wait_phase_warp(bar(L::BAR_SFULL + t), (s_phase + j) & 1, p, abort_flag, kStatusWaitS);
             if (!ok) break;
             tc_fence_after();
+            if constexpr (WIN) {
+                if (j == 0 && w.small) {
+                    // The sinks alone, a row's first keys: every row of the unit
+                    // sees all of them.
+                    uint32_t raw[32], pk[16];
+                    tmem_ld32(tS, raw);
+                    tmem_wait_ld();
+                    float s_max = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < kSmallSinks; ++c)
+                        s_max = fmaxf(s_max, c < p.sinks ? __uint_as_float(raw[c]) : -INFINITY);
+                    m = m_true = s_max * sl2;
+#pragma unroll
+                    for (int c = 0; c < kSmallSinks; c += 2) {
+                        const float e0 = c < p.sinks ? ex2(__fmaf_rn(__uint_as_float(raw[c]), sl2, -m)) : 0.f;
+                        const float e1 = c + 1 < p.sinks ? ex2(__fmaf_rn(__uint_as_float(raw[c + 1]), sl2, -m)) : 0.f;
+                        l += e0 + e1;
+                        pk[c / 2] = pack_bf16x2(e0, e1);
+                    }
+                    const float p_max = ex2(__fmaf_rn(s_max, sl2, -m));
+                    lc = round_bf16(p_max) - p_max;
+                    tmem_st16(tS, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::BAR_PFULL + t));
+                    continue;
+                }
+            }
 
             float s[BN];
 #pragma unroll
@@ -1022,7 +1051,8 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
             // (or the next packed sequence's tokens), so they must become -inf.
             if constexpr (WIN) {
                 const int hole = t ? w.hole[1] : w.hole[0];
-                win_mask<BN>(p, q_row + w.causal_off, w.list.tile(j < w.list.ns ? j : j + hole) * BN, s);
+                const int kv0 = w.list.tile(j < w.list.ns ? j : j + hole) * BN;
+                win_mask<BN>(p, q_row + w.causal_off, kv0, s);
             } else {
             const int kv0 = (kv_tile0_t + j) * BN;
             int valid = kv_end_t - kv0;
@@ -1212,6 +1242,13 @@ template <int D>
 __global__ void __launch_bounds__(LayoutTM<D>::THREADS, 1)
     fa_fwd_tmw_kernel(const __grid_constant__ FwdParams p) {
     tm_forward<D, false, false, false, false, true>(p);
+}
+
+// The same, persistent CTAs.
+template <int D>
+__global__ void __launch_bounds__(LayoutTM<D, false, true>::THREADS, 1)
+    fa_fwd_tmwp_kernel(const __grid_constant__ FwdParams p) {
+    tm_forward<D, false, false, true, false, true>(p);
 }
 
 // bf16, one 64-row query tile per CTA (fa_fwd_rows with 64 rows).

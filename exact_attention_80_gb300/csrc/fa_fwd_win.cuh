@@ -16,6 +16,8 @@
 
 namespace fa {
 
+constexpr int kSmallSinks = 32;
+
 struct WinList {
     int ns, lo, n;  // tiles 0 .. ns - 1, then tile lo on; n in all
     __device__ __forceinline__ int tile(int j) const { return j < ns ? j : lo + (j - ns); }
@@ -46,6 +48,9 @@ struct WorkWin : Work<QT> {
     WinList list;
     int hole[QT];     // steps ns .. ns + hole - 1 are not the tile's
     int steps[QT];    // steps the tile has a part in: n - hole
+    // Step 0 is the sinks alone, kSmallSinks of them at most: its S and PV take
+    // that many keys instead of a whole tile's.
+    bool small;
 };
 
 template <int QT, int BN>
@@ -73,6 +78,8 @@ __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long l
     w.rm.len_q = p.Nq;
     w.list = win_list<BN>(p, w.q0 + w.causal_off, min(w.q0 + QT * kBM, p.Nq) - 1 + w.causal_off);
     w.nmax = w.list.n;
+    // (Behind a gap no window reaches tile 0.)
+    w.small = QT == 2 && w.list.ns == 1 && p.sinks <= kSmallSinks;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
         const int row0 = tile_row0(p, w.q0, t);
@@ -90,7 +97,11 @@ __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long l
     }
 }
 
-// -inf where the row at position pos does not see key kv0 + c.
+// -inf where the row at position pos does not see key kv0 + c. (Masking only the
+// 32-key chunks that an edge crosses, and leaving out the exponentials of chunks
+// that no row of the warp sees, costs more than it saves: the branches keep the
+// chunks' instructions apart, 216 -> 332 us for 2 x 32 heads of 8192, window
+// 1024, d = 64.)
 template <int BN>
 __device__ __forceinline__ void win_mask(const FwdParams& p, int pos, int kv0, float (&s)[BN]) {
     const int valid = pos - kv0 + 1;
@@ -109,66 +120,107 @@ __device__ __forceinline__ void win_mask(const FwdParams& p, int pos, int kv0, f
     }
 }
 
-// Control warps of a two-tile CTA with a window: tm_forward's producer and
-// issuer with the tile list and the holes. A tile that skips step j + 1 gets no
-// S there; its next S is issued in the step before its next one.
-template <int D, typename L>
+// Units a CTA walks: its own, or (PERSIST) one of each round as persist_unit
+// gives them; -1 where a round has none for it.
+template <bool PERSIST>
+__device__ __forceinline__ int win_rounds(const FwdParams& p) {
+    return PERSIST ? static_cast<int>((p.total_units + gridDim.x - 1) / gridDim.x) : 1;
+}
+template <bool PERSIST>
+__device__ __forceinline__ long long win_unit(const FwdParams& p, int k) {
+    if constexpr (!PERSIST) return blockIdx.x;
+    const long long g = gridDim.x;
+    const long long c = (k & 1) ? g - 1 - blockIdx.x : blockIdx.x;
+    const long long lin = static_cast<long long>(k) * g + c;
+    return lin < p.total_units ? lin : -1;
+}
+
+// Control warps of a two-tile CTA with a window: the producer and the issuer of
+// the dense kernel with the tile list and the holes. A tile that skips step
+// j + 1 gets no S there; its next S is issued in the step before its next one.
+// PERSIST: the K/V ring and every barrier's phase carry over from unit to unit.
+// The next unit's K_0 and Q load while the current one's last steps run (Q_t as
+// soon as the unit's last S_t MMA is done, QEMPTY_t), and its first S MMAs are
+// issued right behind the current unit's last PV; O_t is first overwritten by
+// the unit's PV_t(0), which waits for a P that the softmax threads hand over
+// only after their epilogue.
+template <int D, typename L, bool PERSIST>
 __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t sbase, uint32_t tmem,
                                                   volatile uint32_t* abort_flag, int warp) {
     constexpr int QT = L::Q_TILES;
     constexpr int BN = L::BN;
     constexpr int ST = L::STAGES;
     auto bar = [&](int i) -> uint32_t { return sbase + L::BAR_OFF + 8u * i; };
-    WorkWin<QT> w;
-    compute_work_win<QT, BN>(p, blockIdx.x, w);
-    if (w.nmax == 0) return;
+    const int rounds = win_rounds<PERSIST>(p);
     const bool leader = elect_one();
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        auto load_q = [&](int t) {
-            if (leader && w.steps[t] > 0) {
+        RingPos<ST> pos;
+        int issued = 0;        // K/V entries issued, all units
+        int q_loads[QT] = {};  // Q_t loads issued
+        bool ok = true;
+        auto load_q = [&](const WorkWin<QT>& w, int t) -> bool {
+            if (w.steps[t] == 0) return true;
+            if (PERSIST && q_loads[t] > 0 &&
+                !__all_sync(0xffffffffu, wait_phase(bar(L::BAR_QEMPTY + t), (q_loads[t] - 1) & 1, p, abort_flag,
+                                                    kStatusWaitQ)))
+                return false;
+            if (leader) {
                 mbar_arrive_expect_tx(bar(L::BAR_QFULL + t), L::Q_TILE_BYTES);
 #pragma unroll
                 for (int c = 0; c < L::CHUNKS; ++c)
                     tma_load_3d(sbase + L::Q_OFF + t * L::Q_TILE_BYTES + c * (kBM * L::ROW_BYTES), &p.tm_q,
                                 bar(L::BAR_QFULL + t), L::CHUNK_ELEMS * c, tile_row0(p, w.q0, t), w.zq);
             }
+            ++q_loads[t];
+            return true;
         };
-        load_q(0);
-        const int total = 2 * w.nmax;
-        RingPos<ST> pos;
-        int issued = 0;
-        bool ok = true;
-        for (int e = 0; e < total; ++e) {
-            const bool is_v = (e & 1) != 0;
-            if (e >= ST) {
-                ok = __all_sync(0xffffffffu, wait_phase(bar(L::BAR_KVEMPTY + pos.slot), pos.phase ^ 1u, p,
-                                                        abort_flag, kStatusWaitKvEmpty));
+        for (int k = 0; k < rounds && ok; ++k) {
+            const long long lin = win_unit<PERSIST>(p, k);
+            if (lin < 0) continue;
+            WorkWin<QT> w;
+            compute_work_win<QT, BN>(p, lin, w);
+            if (w.nmax == 0) continue;
+            if (!PERSIST) ok = load_q(w, 0);
+            // Entry e: K_0; then per step j: V_j, K_{j+1}.
+            for (int e = 0; e < 2 * w.nmax && ok; ++e) {
+                if (issued >= ST)
+                    ok = __all_sync(0xffffffffu, wait_phase(bar(L::BAR_KVEMPTY + pos.slot), pos.phase ^ 1u, p,
+                                                            abort_flag, kStatusWaitKvEmpty));
                 if (!ok) break;
-            }
-            if (leader) {
-                mbar_arrive_expect_tx(bar(L::BAR_KVFULL + pos.slot), L::SLOT_BYTES);
-                const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
-                const int row = w.list.tile(e >> 1) * BN;
+                if (leader) {
+                    mbar_arrive_expect_tx(bar(L::BAR_KVFULL + pos.slot), L::SLOT_BYTES);
+                    const CUtensorMap* map = (e & 1) ? &p.tm_v : &p.tm_k;
+                    const int row = w.list.tile(e >> 1) * BN;
 #pragma unroll
-                for (int c = 0; c < L::CHUNKS; ++c)
-                    tma_load_3d(sbase + L::SLOT_OFF + pos.slot * L::SLOT_BYTES + c * (BN * L::ROW_BYTES), map,
-                                bar(L::BAR_KVFULL + pos.slot), L::CHUNK_ELEMS * c, row, w.zk);
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_load_3d(sbase + L::SLOT_OFF + pos.slot * L::SLOT_BYTES + c * (BN * L::ROW_BYTES), map,
+                                    bar(L::BAR_KVFULL + pos.slot), L::CHUNK_ELEMS * c, row, w.zk);
+                }
+                ++issued;
+                pos.advance();
+                if (e == 0) {
+                    if (PERSIST) ok = load_q(w, 0);
+                    if (ok) ok = load_q(w, 1);
+                }
             }
-            issued = e + 1;
-            pos.advance();
-            if (e == 0) load_q(1);
         }
         if (ok) {
-            for (int e = max(0, total - ST); e < total && ok; ++e)
+            // No commit arrival may be in flight when the CTA exits: the last uses
+            // of the K/V slots and of the Q tiles.
+            for (int e = max(0, issued - ST); e < issued && ok; ++e)
                 ok = __all_sync(0xffffffffu, wait_phase(bar(L::BAR_KVEMPTY + e % ST), (e / ST) & 1, p, abort_flag,
                                                         kStatusWaitKvEmpty));
+            for (int t = 0; t < QT && ok && PERSIST; ++t)
+                if (q_loads[t] > 0)
+                    ok = __all_sync(0xffffffffu, wait_phase(bar(L::BAR_QEMPTY + t), (q_loads[t] - 1) & 1, p,
+                                                            abort_flag, kStatusWaitQ));
         }
         if (!ok) {
 #pragma unroll
             for (int t = 0; t < QT; ++t)
-                if (w.steps[t] > 0 && issued > 0)
-                    wait_phase(bar(L::BAR_QFULL + t), 0, p, abort_flag, kStatusWaitDrain, false);
+                if (q_loads[t] > 0)
+                    wait_phase(bar(L::BAR_QFULL + t), (q_loads[t] - 1) & 1, p, abort_flag, kStatusWaitDrain, false);
             for (int e = max(0, issued - ST); e < issued; ++e)
                 wait_phase(bar(L::BAR_KVFULL + e % ST), (e / ST) & 1, p, abort_flag, kStatusWaitDrain, false);
         }
@@ -178,6 +230,7 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             return __all_sync(0xffffffffu, wait_phase(b, parity, p, abort_flag, what));
         };
         constexpr uint32_t IDESC_S = make_idesc_bf16(kBM, BN, false, false);
+        constexpr uint32_t IDESC_SMALL = make_idesc_bf16(kBM, kSmallSinks, false, false);
         constexpr uint32_t IDESC_O = make_idesc_bf16(kBM, D, false, true);
         const uint64_t kmaj0 = make_sdesc_rows<L::ROW_BYTES>(sbase, 16, 8 * L::ROW_BYTES);
         const uint64_t vmn0 = make_sdesc_rows<L::ROW_BYTES>(sbase, BN * L::ROW_BYTES, 8 * L::ROW_BYTES);
@@ -186,97 +239,111 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
         auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
             return (static_cast<uint64_t>(hi) << 32) | (lo + (off >> 4));
         };
-        auto issue_s = [&](int t, int slot) {
+        auto issue_s = [&](int t, int slot, bool small) {
             const uint32_t qa = L::Q_OFF + t * L::Q_TILE_BYTES;
             const uint32_t kb = L::SLOT_OFF + slot * L::SLOT_BYTES;
+            const uint32_t idesc = small ? IDESC_SMALL : IDESC_S;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t in_row = (kk & 3) * 32;
                 if (leader)
                     umma_ss(tmem + L::S_COL(t), desc(kmaj_lo, kmaj_hi, qa + (kk >> 2) * (kBM * 128) + in_row),
-                            desc(kmaj_lo, kmaj_hi, kb + (kk >> 2) * (BN * 128) + in_row), IDESC_S, kk > 0 ? 1u : 0u);
+                            desc(kmaj_lo, kmaj_hi, kb + (kk >> 2) * (BN * 128) + in_row), idesc, kk > 0 ? 1u : 0u);
             }
             if (leader) umma_commit(bar(L::BAR_SFULL + t));
         };
-        auto issue_pv = [&](int t, int slot, bool accumulate) {
+        auto issue_pv = [&](int t, int slot, bool accumulate, bool small) {
             const uint32_t vb = L::SLOT_OFF + slot * L::SLOT_BYTES;
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-                if (leader)
+                if (leader && (!small || kk < kSmallSinks / 16))
                     umma_ts(tmem + L::O_COL(t), tmem + L::S_COL(t) + kk * 8, desc(vmn_lo, vmn_hi, vb + kk * 2048),
                             IDESC_O, (accumulate || kk > 0) ? 1u : 0u);
         };
-        auto active = [&](int t, int j) {
-            return j < w.n[t] && !(j >= w.list.ns && j < w.list.ns + w.hole[t]);
-        };
         RingPos<ST> pos;
-        int slot_v = 0, slot_k = 0;
-        auto wait_kv = [&](int j) -> bool {  // V_j, then K_{j+1} if any step needs it
-            slot_v = pos.slot;
-            if (!wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull)) return false;
-            pos.advance();
-            if (j + 1 < w.nmax) {
-                slot_k = pos.slot;
+        int p_seen[QT] = {};  // P_t phases waited for, all units
+        int q_seen[QT] = {};  // Q_t phases waited for
+        bool ok = true;
+        for (int k = 0; k < rounds && ok; ++k) {
+            const long long lin = win_unit<PERSIST>(p, k);
+            if (lin < 0) continue;
+            WorkWin<QT> w;
+            compute_work_win<QT, BN>(p, lin, w);
+            if (w.nmax == 0) continue;
+            auto active = [&](int t, int j) {
+                return j < w.n[t] && !(j >= w.list.ns && j < w.list.ns + w.hole[t]);
+            };
+            int slot_v = 0, slot_k = 0;
+            auto wait_kv = [&](int j) -> bool {  // V_j, then K_{j+1} if any step needs it
+                slot_v = pos.slot;
                 if (!wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull)) return false;
                 pos.advance();
-            }
-            return true;
-        };
-        int done[QT] = {};       // steps whose PV was issued
-        bool q_here[QT] = {};    // Q_t landed
-        // S of the tile's step j + 1, whose K is in `slot`.
-        auto next_s = [&](int t, int slot) -> bool {
-            if (!q_here[t]) {
-                if (!wait_all(bar(L::BAR_QFULL + t), 0, kStatusWaitQ)) return false;
-                q_here[t] = true;
-                tc_fence_after();
-            }
-            issue_s(t, slot);
-            return true;
-        };
-        bool ok = wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull);
-        if (ok) {
-            tc_fence_after();
-#pragma unroll
-            for (int t = 0; t < QT; ++t)
-                if (ok && active(t, 0)) ok = next_s(t, pos.slot);
-        }
-        if (ok) {
-            if (leader) umma_commit(bar(L::BAR_KVEMPTY + pos.slot));
-            pos.advance();
-            ok = wait_kv(0);
-        }
-        // Per step as tm_forward's issuer: the next step's K/V waits sit between
-        // tile 1's PV and S at d = 128, behind tile 0's batch at d = 64.
-        constexpr bool kKvWaitMid1 = (D >= 128);
-        for (int j = 0; j < w.nmax && ok; ++j) {
-            const int sv = slot_v, sk = slot_k;
-            const bool k_next = (j + 1 < w.nmax);
-#pragma unroll
-            for (int t = 0; t < QT && ok; ++t) {
-                const bool act = active(t, j);
-                if (act) {
-                    ok = wait_all(bar(L::BAR_PFULL + t), done[t] & 1, kStatusWaitP);
-                    if (!ok) break;
+                if (j + 1 < w.nmax) {
+                    slot_k = pos.slot;
+                    if (!wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull)) return false;
+                    pos.advance();
+                }
+                return true;
+            };
+            int done[QT] = {};     // PVs issued in this unit
+            int issued_s[QT] = {}; // S MMAs issued in this unit
+            // S of the tile's step j, whose K is in `slot`.
+            auto next_s = [&](int t, int j, int slot) -> bool {
+                if (issued_s[t] == 0) {
+                    if (!wait_all(bar(L::BAR_QFULL + t), q_seen[t] & 1, kStatusWaitQ)) return false;
+                    ++q_seen[t];
                     tc_fence_after();
-                    issue_pv(t, sv, done[t] > 0);
-                    ++done[t];
                 }
-                if (t == QT - 1 && kKvWaitMid1 && k_next) {
-                    ok = wait_kv(j + 1);
-                    if (!ok) break;
-                }
-                if (active(t, j + 1)) {
-                    ok = next_s(t, sk);
-                } else if (act && j + 1 >= w.n[t]) {
-                    if (leader) umma_commit(bar(L::BAR_OFULL + t));
-                }
-                if (t == 0 && !kKvWaitMid1 && k_next && ok) ok = wait_kv(j + 1);
+                issue_s(t, slot, w.small && j == 0);
+                if (++issued_s[t] == w.steps[t] && PERSIST && leader) umma_commit(bar(L::BAR_QEMPTY + t));
+                return true;
+            };
+            ok = wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+                    if (ok && active(t, 0)) ok = next_s(t, 0, pos.slot);
             }
-            if (!ok) break;
-            if (leader) umma_commit(bar(L::BAR_KVEMPTY + sv));
-            if (k_next && leader) umma_commit(bar(L::BAR_KVEMPTY + sk));
+            if (ok) {
+                if (leader) umma_commit(bar(L::BAR_KVEMPTY + pos.slot));
+                pos.advance();
+                ok = wait_kv(0);
+            }
+            // Per step as tm_forward's issuer: the next step's K/V waits sit between
+            // tile 1's PV and S at d = 128, behind tile 0's batch at d = 64.
+            constexpr bool kKvWaitMid1 = (D >= 128);
+            for (int j = 0; j < w.nmax && ok; ++j) {
+                const int sv = slot_v, sk = slot_k;
+                const bool k_next = (j + 1 < w.nmax);
+#pragma unroll
+                for (int t = 0; t < QT && ok; ++t) {
+                    const bool act = active(t, j);
+                    if (act) {
+                        ok = wait_all(bar(L::BAR_PFULL + t), p_seen[t] & 1, kStatusWaitP);
+                        if (!ok) break;
+                        ++p_seen[t];
+                        tc_fence_after();
+                        issue_pv(t, sv, done[t] > 0, w.small && j == 0);
+                        ++done[t];
+                    }
+                    if (t == QT - 1 && kKvWaitMid1 && k_next) {
+                        ok = wait_kv(j + 1);
+                        if (!ok) break;
+                    }
+                    if (active(t, j + 1)) {
+                        ok = next_s(t, j + 1, sk);
+                    } else if (act && j + 1 >= w.n[t]) {
+                        if (leader) umma_commit(bar(L::BAR_OFULL + t));
+                    }
+                    if (t == 0 && !kKvWaitMid1 && k_next && ok) ok = wait_kv(j + 1);
+                }
+                if (!ok) break;
+                if (leader) umma_commit(bar(L::BAR_KVEMPTY + sv));
+                if (k_next && leader) umma_commit(bar(L::BAR_KVEMPTY + sk));
+            }
         }
+        // Every MMA this thread issued must finish before TMEM can be freed.
         if (leader) umma_commit(bar(L::BAR_DRAIN));
         wait_phase(bar(L::BAR_DRAIN), 0, p, abort_flag, kStatusWaitDrain, false);
     }

@@ -104,6 +104,13 @@ CASES = [
     (1, 6, 2, 520, 600, 0, 0),        # no window
     (1, 2, 1, 129, 1000, 40, 128),
     (1, 8, 1, 1025, 1025, 96, 0),     # one kv head for all
+    # more query units than SMs: persistent CTAs (d = 64, 128)
+    (2, 80, 20, 513, 513, 129, 4),
+    (1, 160, 160, 300, 700, 64, 40),
+    (1, 200, 100, 400, 300, 0, 0),    # the first 100 rows see no key
+    (1, 160, 40, 260, 900, 200, 32),
+    (1, 320, 80, 256, 256, 3, 1),
+    (3, 60, 20, 257, 1000, 1, 130),
 ]
 
 
