@@ -63,6 +63,7 @@
 
 #include "fa.h"
 #include "fa_internal.h"
+#include "fa_launch.h"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -924,6 +925,8 @@ template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_win_post_kernel(const __grid_constant__ BwdParams p,
                                                               __nv_bfloat16* __restrict__ dq, long long q_rows,
                                                               long long k_rows) {
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
     constexpr int LANES = D / 8;
     const long long lin = static_cast<long long>(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
     const int c = (threadIdx.x % LANES) * 8;
@@ -985,16 +988,18 @@ BwdParts bwd_parts(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int
     if (window > 0) c.sink_tiles = static_cast<int>(std::min(k_tiles, (static_cast<long long>(sinks) + kBwdKeys - 1) / kBwdKeys));
     const long long reach = window > 0 ? std::min(all, (kBwdKeys + static_cast<long long>(window) + kBwdHalf - 2) / kBwdHalf + 1) : all;
     const long long steps = G * reach, sink_steps = G * all;
-    const long long tiles = std::max(1ll, k_tiles - c.sink_tiles);
     long long best = -1;
     for (int p = 1; p <= 16 && (p == 1 || p <= steps); ++p) {
-        const long long waves = (heads * tiles * halves * p + 151) / 152;
-        const long long cost = waves * ((steps + p - 1) / p + kUnitCost + (p > 1 ? kPartCost : 0));
-        if (best < 0 || cost < best) best = cost, c.parts = p;
-    }
-    if (c.sink_tiles > 0) {
-        const long long piece = std::max(8ll, (steps + c.parts - 1) / c.parts);
-        c.sink_parts = static_cast<int>(std::min(64ll, (sink_steps + piece - 1) / piece));
+        const long long piece = std::max(8ll, (steps + p - 1) / p);
+        const long long sp = c.sink_tiles > 0 ? std::min(64ll, (sink_steps + piece - 1) / piece) : 1;
+        const long long ctas = heads * halves * ((k_tiles - c.sink_tiles) * p + c.sink_tiles * sp);
+        const long long longest = std::max((steps + p - 1) / p, c.sink_tiles > 0 ? (sink_steps + sp - 1) / sp : 0);
+        const long long cost = (ctas + 151) / 152 * (longest + kUnitCost + (p > 1 ? kPartCost : 0));
+        if (best < 0 || cost < best) {
+            best = cost;
+            c.parts = p;
+            c.sink_parts = static_cast<int>(sp);
+        }
     }
     const long long units = heads * (c.sink_tiles * static_cast<long long>(c.sink_parts) +
                                      (c.parts > 1 ? (k_tiles - c.sink_tiles) * c.parts : 0));
@@ -1081,9 +1086,8 @@ cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, con
     const long long per_block = 256 / (D / 8);
     const long long post = (q_rows + k_rows + per_block - 1) / per_block;
     if (post > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    fa_bwd_win_post_kernel<D><<<static_cast<unsigned>(post), 256, 0, stream>>>(
-        p, static_cast<__nv_bfloat16*>(dq), q_rows, k_rows);
-    return cudaGetLastError();
+    return launch_dependent(fa_bwd_win_post_kernel<D>, dim3(static_cast<unsigned>(post)), 256, 0, stream, p,
+                            static_cast<__nv_bfloat16*>(dq), q_rows, k_rows);
 }
 
 }  // namespace fa

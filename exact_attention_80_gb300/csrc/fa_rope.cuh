@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
+#include "fa_launch.h"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -172,23 +173,5 @@ inline bool rope_split(const RopeParams& r) {
 // Host side: checks a rotation's description (fa_rope.cu).
 fa_status check_rope(const fa_rotation* rope, int d, long long tokens);
 RopeParams rope_params(const fa_rotation* rope, long long tokens, bool inverse);
-
-// Launch with programmatic stream serialization: the kernel waits for the grid
-// before it in the stream (griddep_wait) before it touches global memory.
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
-                             A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 }  // namespace fa
