@@ -9,8 +9,8 @@
 // run on mma.sync (m16n8k16, f16 operands, fp32 sums), which needs no tile of
 // 128 rows.
 //
-// Each of the CTA's four warps takes every fourth tile of 32 keys with a ring of
-// its own: TMA copies of whole pages (or their 32-key parts) into swizzled
+// Each of the CTA's four warps takes every fourth tile of 32 (16) keys with a ring of
+// its own: TMA copies of whole pages (or their parts) into swizzled
 // shared memory, one mbarrier per slot, no barrier between the warps until
 // their states meet at the end. e4m3 codes convert to f16 exactly (one
 // instruction per two codes), in the registers of the fragments:
@@ -59,15 +59,26 @@ fa_status check_cache(const fa_paged_cache* c) {
 namespace {
 
 constexpr int kRows = 16;      // query rows per CTA
-constexpr int kKeys = 32;      // keys per warp tile
 constexpr int kWarps = 4;
+// Keys of a warp's tile, and CTAs an SM holds. A warp's tile is a chain of
+// dependent steps, so throughput comes from the warps beside it: short tiles and
+// two- or three-slot rings, for as many CTAs as the registers allow. Measured on
+// 64 contexts of 8192 to 32768 tokens (32 at d = 256, up to 16384), TB/s:
+//   d = 64:  two CTAs of six-slot rings 3.4, three 4.5, four 5.0, five 4.8; tiles
+//            of 64 keys, three CTAs, 4.8
+//   d = 128: two CTAs of three-slot rings 5.7, three of two slots 6.5
+//   d = 256: tiles of 32 keys, one CTA, 4.7; of 16 keys, two CTAs, 5.6
+__host__ __device__ constexpr int rows_keys(int d) { return d == 256 ? 16 : 32; }
+__host__ __device__ constexpr int rows_ctas(int d) { return d == 64 ? 4 : d == 128 ? 3 : 2; }
 template <int D>
 struct PagedLayout {
     static constexpr int ROW_BYTES = D < 128 ? D : 128;  // bytes of a swizzled row
     static constexpr int PARTS = D / ROW_BYTES;          // row parts (128-byte columns of a key)
-    static constexpr uint32_t TILE = kKeys * D;          // bytes of K (or V) of a tile
+    static constexpr int KEYS = rows_keys(D);            // keys of a warp's tile
+    static constexpr int GROUPS = KEYS / 16;             // scales of a tile: one per 16 keys, the smallest page
+    static constexpr uint32_t TILE = KEYS * D;           // bytes of K (or V) of a tile
     static constexpr uint32_t SLOT = 2 * TILE;
-    static constexpr int STAGES = D == 64 ? 6 : 3;
+    static constexpr int STAGES = D == 64 ? 3 : 2;
     static constexpr uint32_t RING = STAGES * SLOT;      // per warp
     static constexpr bool Q_SHARED = D == 256;           // Q fragments in shared memory, not registers
     static constexpr uint32_t Q_BYTES = Q_SHARED ? kRows * D * 2 : 0;
@@ -113,12 +124,12 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 // Byte offset of 16-byte unit `unit` of key row `row` in a swizzled tile: rows
-// of 128 bytes (units XOR row mod 8; further row parts 32 rows behind), or of
+// of 128 bytes (units XOR row mod 8; further row parts a tile's rows behind), or of
 // 64 bytes (units XOR row / 2 mod 4).
 template <int D>
 __device__ __forceinline__ uint32_t tile_unit(int row, int unit) {
     if constexpr (D == 64) return row * 64 + ((unit ^ ((row >> 1) & 3)) << 4);
-    else return (unit >> 3) * (kKeys * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
+    else return (unit >> 3) * (rows_keys(D) * 128) + row * 128 + (((unit & 7) ^ (row & 7)) << 4);
 }
 // Key row (0..7 of an 8-key group) behind fragment index j: with 128-byte rows
 // the two rows that one quarter of a warp reads together lie four apart, so
@@ -129,9 +140,10 @@ __device__ __forceinline__ int key_of(int j) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     fa_paged_rows_kernel(const __grid_constant__ PagedParams p) {
     using L = PagedLayout<D>;
+    constexpr int KEYS = L::KEYS, NT = KEYS / 8, GROUPS = L::GROUPS;
     constexpr int C = D / 64;    // 64-column parts of the contraction: one 16-byte load each
     constexpr int X = D / 16;    // 16-column units of O
     extern __shared__ uint8_t smem_raw[];
@@ -172,7 +184,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
     const int start = nt.len - nt.n;  // position of the first query
     const int p0 = start + r0 / p.G;
     const int p1 = start + (min(r0 + kRows, rows) - 1) / p.G;
-    const KeyList list = key_list<kKeys>(p.window, p.sinks, p0, p1);
+    const KeyList list = key_list<KEYS>(p.window, p.sinks, p0, p1);
     const int used = max(1, (list.n + p.tiles_per_split - 1) / p.tiles_per_split);
     if (split >= used) return;
     const int i0 = split * p.tiles_per_split;
@@ -182,10 +194,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
     const int page_size = 1 << p.log_page;
     const int last_page = (nt.len - 1) >> p.log_page;
 
-    // The page behind the first (half = 0) or second 16 keys of tile kt, or -1
-    // where the sequence has none there (nothing is read) or its entry is bad.
-    auto page_of = [&](int kt, int half) -> int {
-        const int idx = (kt * kKeys + 16 * half) >> p.log_page;
+    // Page i of the tile's pages (or the one page it lies in), or -1 where the
+    // sequence has none there (nothing is read) or its entry is bad.
+    const int per = page_size < KEYS ? KEYS >> p.log_page : 1;  // pages of a tile
+    auto page_of = [&](int kt, int i) -> int {
+        const int idx = ((kt * KEYS) >> p.log_page) + i;
         if (idx > last_page) return -1;
         const int id = table[idx];
         if (id < 0 || id >= p.num_pages) {
@@ -194,41 +207,41 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         }
         return id;
     };
-    // Copies of tile kt, whose pages are id0 and (pages of 16 tokens) id1, into
-    // slot s: a page that is not there is left out, and its keys are masked.
-    auto issue = [&](int s, int kt, int id0, int id1) {
-        const uint32_t dst = ring + s * L::SLOT, bar = bar0 + 8 * s;
-        const bool two = page_size < kKeys;
-        const uint32_t each = (two ? 16 : kKeys) * D * 2;
-        mbar_arrive_expect_tx(bar, (id0 >= 0 ? each : 0u) + (two && id1 >= 0 ? each : 0u));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int id = half ? id1 : id0;
-            if ((half && !two) || id < 0) continue;
-            const int row = ((id * p.Hkv + h) << p.log_page) + ((kt * kKeys + 16 * half) & (page_size - 1));
-#pragma unroll
-            for (int c = 0; c < L::PARTS; ++c) {
-                const uint32_t at = dst + c * (kKeys * 128) + half * 16 * L::ROW_BYTES;
-                tma_load_2d(at, &p.tm_k, bar, c * 128, row);
-                tma_load_2d(at + L::TILE, &p.tm_v, bar, c * 128, row);
-            }
-        }
-    };
-    // Page ids of the warp's next 32 tiles to copy, one per lane.
-    int ids0 = -1, ids1 = -1;
+    // Page ids of the warp's next 32 tiles to copy, one tile per lane.
+    int ids[GROUPS];
     auto fetch_ids = [&](int k) {
         const int i = i0 + warp + kWarps * (k + lane);
-        ids0 = ids1 = -1;
-        if (i < i1) {
-            const int kt = list.tile(i);
-            ids0 = page_of(kt, 0);
-            if (page_size < kKeys) ids1 = page_of(kt, 1);
-        }
+#pragma unroll
+        for (int e = 0; e < GROUPS; ++e) ids[e] = i < i1 && e < per ? page_of(list.tile(i), e) : -1;
     };
-    auto issue_next = [&](int k) {  // tile number k of the warp
+    // Copies of tile number k of the warp into its slot: a page that is not there
+    // is left out, and its keys are masked.
+    auto issue_next = [&](int k) {
         if ((k & 31) == 0) fetch_ids(k);
-        const int a = __shfl_sync(0xffffffffu, ids0, k & 31), c = __shfl_sync(0xffffffffu, ids1, k & 31);
-        if (lane == 0) issue(k % L::STAGES, list.tile(i0 + warp + kWarps * k), a, c);
+        int id[GROUPS], there = 0;
+#pragma unroll
+        for (int e = 0; e < GROUPS; ++e) {
+            id[e] = __shfl_sync(0xffffffffu, ids[e], k & 31);
+            there += id[e] >= 0 ? 1 : 0;
+        }
+        if (lane == 0) {
+            const int s = k % L::STAGES;
+            const uint32_t dst = ring + s * L::SLOT, bar = bar0 + 8 * s;
+            const int rows_each = min(page_size, KEYS);
+            const int key0 = list.tile(i0 + warp + kWarps * k) * KEYS;
+            mbar_arrive_expect_tx(bar, there * rows_each * D * 2);
+#pragma unroll
+            for (int e = 0; e < GROUPS; ++e) {
+                if (id[e] < 0) continue;
+                const int row = ((id[e] * p.Hkv + h) << p.log_page) + (per == 1 ? key0 & (page_size - 1) : 0);
+#pragma unroll
+                for (int c = 0; c < L::PARTS; ++c) {
+                    const uint32_t at = dst + c * (KEYS * 128) + e * rows_each * L::ROW_BYTES;
+                    tma_load_2d(at, &p.tm_k, bar, c * 128, row);
+                    tma_load_2d(at + L::TILE, &p.tm_v, bar, c * 128, row);
+                }
+            }
+        }
         __syncwarp();
     };
     const int ahead = min(mine, L::STAGES);
@@ -303,8 +316,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     const int pmin = p0, pmax = p1;
     // Scales of the warp's current 32 tiles, one tile per lane: K scale, log2 of
-    // the V scale and its reciprocal for both 16-key halves.
-    float sk[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f}, si[2] = {1.f, 1.f};
+    // the V scale and its reciprocal for each page of the tile.
+    float sk[GROUPS], sv[GROUPS], si[GROUPS];
+    const int group_shift = per == 1 ? 31 : p.log_page - 4;  // 16-key group to page of the tile
     bool ok = true;
     // The lane's parts of its shared-memory addresses: K's 16-byte loads of 64
     // columns each, V's ldmatrix rows of 32 columns each.
@@ -319,33 +333,32 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         if ((k & 31) == 0) {
             const int i = i0 + warp + kWarps * (k + lane);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int id = (i < i1 && (half == 0 || page_size < kKeys)) ? page_of(list.tile(i), half) : -1;
+            for (int e = 0; e < GROUPS; ++e) {
+                const int id = i < i1 && e < per ? page_of(list.tile(i), e) : -1;
                 const long long cell = static_cast<long long>(id) * p.Hkv + h;
                 const float vs = id >= 0 ? p.v_scale[cell] : 1.f;
-                sk[half] = id >= 0 ? p.k_scale[cell] : 1.f;
-                sv[half] = log2f(vs);
-                si[half] = 1.f / vs;
+                sk[e] = id >= 0 ? p.k_scale[cell] : 1.f;
+                sv[e] = log2f(vs);
+                si[e] = 1.f / vs;
             }
-            if (page_size >= kKeys) sk[1] = sk[0], sv[1] = sv[0], si[1] = si[0];
         }
         const int slot = k % L::STAGES;
         ok = __all_sync(0xffffffffu, wait_bounded(bar0 + 8 * slot, (k / L::STAGES) & 1, p.wait_limit, p.status,
                                                   kStatusWaitKvFull));
         if (!ok) break;
-        const int key0 = list.tile(i0 + warp + kWarps * k) * kKeys;
+        const int key0 = list.tile(i0 + warp + kWarps * k) * KEYS;
         const uint32_t ks_at = ring + slot * L::SLOT, vs_at = ks_at + L::TILE;
 
-        float s[4][4];
+        float s[NT][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            uint32_t kw[4][4];
+            uint32_t kw[NT][4];
             const uint32_t at = ks_at + k_lane[c];
-            static_for<4>([&](auto n) { ld_shared_v4_at<n * 8 * L::ROW_BYTES>(kw[n], at); });
+            static_for<NT>([&](auto n) { ld_shared_v4_at<n * 8 * L::ROW_BYTES>(kw[n], at); });
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
                 uint32_t a[4];
@@ -356,8 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
                     for (int e = 0; e < 4; ++e) a[e] = qf[c][ks][e];
                 }
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-                {
+                for (int n = 0; n < NT; ++n) {
                     uint32_t b0, b1;
                     decode_e4m3x4_f16(kw[n][ks], b0, b1);
                     mma_f16(s[n], a, b0, b1);
@@ -366,18 +378,24 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         }
 
         // x = s * (ks scale log2 e) + log2 vs, masked where a row does not see the key.
-        float kc[2], kv[2], ki[2];
+        float kc[GROUPS], kv[GROUPS], ki[GROUPS];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            kc[half] = __shfl_sync(0xffffffffu, sk[half], k & 31);
-            kv[half] = __shfl_sync(0xffffffffu, sv[half], k & 31);
-            ki[half] = __shfl_sync(0xffffffffu, si[half], k & 31);
+        for (int e = 0; e < GROUPS; ++e) {
+            // (The tile's page behind group e; the arrays keep constant indices.)
+            const int page = e >> group_shift;
+            float a = sk[0], b = sv[0], c = si[0];
+#pragma unroll
+            for (int i = 1; i < GROUPS; ++i)
+                if (page == i) a = sk[i], b = sv[i], c = si[i];
+            kc[e] = __shfl_sync(0xffffffffu, a, k & 31);
+            kv[e] = __shfl_sync(0xffffffffu, b, k & 31);
+            ki[e] = __shfl_sync(0xffffffffu, c, k & 31);
         }
-        const bool masked = !(key0 + kKeys - 1 <= pmin &&
-                              (p.window <= 0 || key0 > pmax - p.window || key0 + kKeys <= p.sinks));
+        const bool masked = !(key0 + KEYS - 1 <= pmin &&
+                              (p.window <= 0 || key0 > pmax - p.window || key0 + KEYS <= p.sinks));
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float x = fmaf(s[n][e], rowf[e >> 1] * kc[n >> 1], kv[n >> 1]);
@@ -411,9 +429,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
             l[1] *= alpha[1];
         }
         const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - kPShift, m[1] == -INFINITY ? 0.f : m[1] - kPShift};
-        uint32_t pf[2][4];  // P of 16 keys as an A fragment
+        uint32_t pf[GROUPS][4];  // P of 16 keys as an A fragment
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int n = 0; n < NT; ++n) {
             float e0 = ex2(s[n][0] - ref[0]), e1 = ex2(s[n][1] - ref[0]);
             float e2 = ex2(s[n][2] - ref[1]), e3 = ex2(s[n][3] - ref[1]);
             l[0] = fmaf(e0 + e1, ki[n >> 1], l[0]);
@@ -426,7 +444,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2)
         // no row sees may hold anything (a slot never written, a NaN): its bytes
         // are cleared.
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int kk = 0; kk < GROUPS; ++kk) {
             uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
             if (masked) {
 #pragma unroll
@@ -554,7 +572,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
         const int start = nt.len - nt.n;
         const int p0 = start + r0 / p.G, p1 = start + (min(r0 + p.block_rows, rows) - 1) / p.G;
         const KeyList list = p.block_keys == kTcKeys ? key_list<kTcKeys>(p.window, p.sinks, p0, p1)
-                                                     : key_list<kKeys>(p.window, p.sinks, p0, p1);
+                                                     : key_list<rows_keys(D)>(p.window, p.sinks, p0, p1);
         used = (list.n + p.tiles_per_split - 1) / p.tiles_per_split;
         live = used > 1;
     }
@@ -647,7 +665,7 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     c.tc = d <= 128 && rows > kRows;
     c.dual = c.tc && rows <= kTcRows;
     c.block_rows = !c.tc ? kRows : c.dual ? kTcRows : 2 * kTcRows;
-    c.block_keys = c.tc ? kTcKeys : kKeys;
+    c.block_keys = c.tc ? kTcKeys : rows_keys(d);
     c.row_blocks = (rows + c.block_rows - 1) / c.block_rows;
     const long long K = c.block_keys;
     c.tiles = (max_k + K - 1) / K;
@@ -659,18 +677,18 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 }
 
 // Splits that finish earliest, in rounds of 128 keys; a CTA's start and end cost
-// about three, leaving and merging partial states some more. One sequence: waves
+// about two, leaving and merging partial states some more. One sequence: waves
 // of CTAs of equal length. Several: their lengths differ, so the longest CTA
 // comes on top of an even share of all of them, at two thirds of the longest
 // length (measured: 64 contexts of 8192 to 32768, 512 units: 600 us with one
-// split, 511 with three, 480 with eight; one of 131072, 8 units: 52 us with 38
-// splits, one wave, 74 with 152).
+// split, 511 with three, 480 with eight; one of 131072, 8 units: 52 us in one
+// wave of splits, 74 in four).
 int best_splits(int B, long long units, long long rounds, int slots, int per_cta, bool many_rows) {
     // (Partial sums of 256 rows cost more than they even out: two chunks of 2048
     // tokens over 16384 keys, 341 us with one split, 430 with four.)
     if (many_rows && units >= slots) return 1;
     const long long most = std::max(1ll, std::min(static_cast<long long>(FA_MAX_SPLITS), rounds / 2));
-    const double start = many_rows ? 8. : 3.;
+    const double start = many_rows ? 8. : 2.;
     long long best = 1;
     double best_cost = -1.;
     for (long long s = 1; s <= most; ++s) {
@@ -722,8 +740,8 @@ int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
     const long long units = static_cast<long long>(B) * Hkv * c.row_blocks;
     const long long rounds = std::max(1ll, c.tiles * c.block_keys / 128);
-    // CTAs at once: one per SM for the tensor-core kernel and head dim 256.
-    return fa::best_splits(B, units, rounds, c.tc || d == 256 ? 152 : 304, c.dual ? 2 : 1, c.tc && !c.dual);
+    // CTAs at once: one per SM for the tensor-core kernel.
+    return fa::best_splits(B, units, rounds, 152 * (c.tc ? 1 : fa::rows_ctas(d)), c.dual ? 2 : 1, c.tc && !c.dual);
 }
 
 size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits) {
@@ -759,7 +777,7 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     std::memset(&p, 0, sizeof(p));
     const long long rows = static_cast<long long>(cache->num_pages) * Hkv * cache->page_size;
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
-    const int box = c.tc ? cache->page_size : std::min(cache->page_size, fa::kKeys);
+    const int box = std::min(cache->page_size, c.block_keys);
     if (!fa::encode_cache_map(&p.tm_k, cache->k, d, rows, box) || !fa::encode_cache_map(&p.tm_v, cache->v, d, rows, box))
         return FA_ERR_CUDA;
     p.q = static_cast<const __nv_bfloat16*>(q);
