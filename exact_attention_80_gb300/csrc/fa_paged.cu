@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             for (int e = 0; e < GROUPS; ++e) {
                 const int id = i < i1 && e < per ? page_of(list.tile(i), e) : -1;
                 const long long cell = static_cast<long long>(id) * p.Hkv + h;
-                const float vs = id >= 0 ? p.v_scale[cell] : 1.f;
+                const float vs = id >= 0 ? usable_scale(p.v_scale[cell]) : 1.f;
                 sk[e] = id >= 0 ? p.k_scale[cell] : 1.f;
                 sv[e] = log2f(vs);
                 si[e] = 1.f / vs;
@@ -662,7 +662,11 @@ struct Plan {
 Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     Plan c;
     const long long rows = static_cast<long long>(max_q) * G;
-    c.tc = d <= 128 && rows > kRows;
+    // The tensor-core kernel from 17 rows at d = 128, from 33 at d = 64: up to there
+    // two blocks of 16 rows, which read K and V twice, are as fast (16 sequences of
+    // 32 rows over up to 16200 keys: 144 against 138 us at d = 128, 100 against 115
+    // at d = 64; at 36 rows 191 against 140 and 127 against 114).
+    c.tc = d <= 128 && rows > (d == 64 ? 2 * kRows : kRows);
     c.dual = c.tc && rows <= kTcRows;
     c.block_rows = !c.tc ? kRows : c.dual ? kTcRows : 2 * kTcRows;
     c.block_keys = c.tc ? kTcKeys : rows_keys(d);

@@ -17,6 +17,11 @@ namespace fa {
 constexpr int kScaleExpMin = -100;
 constexpr int kScaleExpMax = 120;
 
+// A V scale as the kernels use it (its logarithm and reciprocal): within the
+// range of a scale, so that a block whose scale was never set, or is zero
+// because its values are, counts as values next to zero.
+__device__ __forceinline__ float usable_scale(float s) { return fminf(fmaxf(s, 0x1p-100f), 0x1p+120f); }
+
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 

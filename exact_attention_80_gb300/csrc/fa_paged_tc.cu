@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
             for (int j = 0; j < n; ++j) {
                 // The groups' factors, before the wait for S: a shuffle between the
                 // exponentials would hold each group up.
-                const float ks = ks_next, lv = log2f(vs_next), iv = 1.f / vs_next;
+                const float vs = usable_scale(vs_next);
+                const float ks = ks_next, lv = log2f(vs), iv = 1.f / vs;
                 float kg[BN / 16], vg[BN / 16], ig[BN / 16];
                 if constexpr (!DUAL) {
 #pragma unroll

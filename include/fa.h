@@ -355,7 +355,8 @@ fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, const fa_rot
  * j % page_size of page page_table[b][j / page_size] (int32 [B][max_pages] on
  * the device; entries behind a sequence's last page are not read). Scales are
  * powers of two in [2^-100, 2^120] where fa_kv_append_fp8 wrote them;
- * fa_fwd_paged_fp8 takes any positive scales in that range.
+ * fa_fwd_paged_fp8 takes any scales in that range, and a smaller V scale (zero,
+ * for a block of zeros) as 2^-100. Cached values must be finite.
  */
 typedef struct {
     void* k;
