@@ -972,8 +972,9 @@ __global__ void __launch_bounds__(256) fa_bwd_win_post_kernel(const __grid_const
 
 // How a windowed backward is cut into parts (host side). Each step of a CTA
 // takes about as long as any other, a CTA's start and end about kUnitCost
-// steps, leaving and adding partial sums kPartCost more; 152 CTAs run at once. `parts` minimises the waves' length, and a sink
-// tile is cut into pieces of about the same number of steps.
+// steps, leaving and adding partial sums kPartCost more; 152 CTAs run at once.
+// `parts` minimises the waves' length, and a sink tile is cut into pieces of
+// about the same number of steps.
 struct BwdParts {
     int sink_tiles, sink_parts, parts;
     size_t part_floats;  // floats of the partial sums

@@ -153,10 +153,11 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : 3) fa_kv_append
     NewTokens t;
     const bool valid = new_tokens(p.cu, p.lens, b, p.total, p.max_new, p.max_pages << p.log_page, t);
     if (!valid && live && g == 0 && which == 0 && h == 0 && touch == 0) atomicOr(p.status, kStatusBadSeqlens);
-    live = live && valid && t.n > 0;
     const int page_size = 1 << p.log_page;
     const int start = t.len - t.n;                    // slot of the sequence's first new token
     const int blk = (start >> p.log_page) + touch;    // page index within the sequence
+    // (Page indices past the table would overflow as slots where max_new is large.)
+    live = live && valid && t.n > 0 && blk < p.max_pages;
     const int lo = touch == 0 ? (start & (page_size - 1)) : 0;             // first new slot of the page
     const int hi = min(page_size, t.len - (blk << p.log_page));            // end of the new slots
     live = live && lo < hi;
@@ -288,6 +289,7 @@ extern "C" fa_status fa_kv_append_fp8(const void* q, const void* k, const void* 
     if (sc != FA_OK) return sc;
     const int d = cache->d, Hkv = cache->Hkv;
     if (B < 1 || total_new < 1 || max_new < 1 || max_new > total_new || max_pages < 1) return FA_ERR_SHAPE;
+    if (total_new > 0x7fffffff - 4096) return FA_ERR_SHAPE;  // token indices of whole blocks are int
     if (q && (H < 1 || H > 65535)) return FA_ERR_SHAPE;
     if (static_cast<long long>(max_pages) * cache->page_size > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
     if (!fa::aligned(k, 16) || !fa::aligned(v, 16) || !fa::aligned(q, 16) || !fa::aligned(q_out, 16) ||
@@ -298,7 +300,7 @@ extern "C" fa_status fa_kv_append_fp8(const void* q, const void* k, const void* 
         return FA_ERR_STRIDE;
     if (q && (q_stride % 8 || q_stride < 0 || q_stride > most)) return FA_ERR_STRIDE;
     if (rope) {
-        const fa_status s = fa::check_rope(rope, d, total_new);
+        const fa_status s = fa::check_rope(rope, d);
         if (s != FA_OK) return s;
     }
     fa::AppendLaunch p;

@@ -65,7 +65,6 @@ __device__ __forceinline__ bool new_tokens(const int* cu, const int* lens, int b
 constexpr float kPShift = 7.f;  // p = 2^(x - m + 7)
 constexpr float kPSlack = 8.f;  // the reference moves when x passes it by more, so p <= 2^15
 
-
 struct PagedParams {
     CUtensorMap tm_k, tm_v;  // e4m3 [num_pages * Hkv * page_size][d], box {row part, keys per copy}
     const __nv_bfloat16* q;  // [total_q][H][d]

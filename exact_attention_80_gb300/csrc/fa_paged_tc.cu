@@ -775,6 +775,7 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
+                    __syncwarp();  // rows past the last one skip the stores below
                     if (n > 0) {
                         tmem_ld32(tO + cc * 32, o);
                         tmem_wait_ld();

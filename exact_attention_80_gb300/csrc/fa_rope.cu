@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fa_rope_kernel(const __grid_c
 
 }  // namespace
 
-fa_status check_rope(const fa_rotation* rope, int d, long long tokens) {
+fa_status check_rope(const fa_rotation* rope, int d) {
     if (!rope->table) return FA_ERR_NULL;
     if (!aligned(rope->table, 16) || !aligned(rope->positions, 4)) return FA_ERR_ALIGN;
     if (rope->rot < 16 || rope->rot > d || rope->rot % 16 != 0) return FA_ERR_ROPE;
@@ -87,7 +87,6 @@ fa_status check_rope(const fa_rotation* rope, int d, long long tokens) {
         }
         if (sum != rope->rot / 2) return FA_ERR_ROPE;
     }
-    (void)tokens;
     return FA_OK;
 }
 
@@ -119,7 +118,7 @@ extern "C" fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, c
     if (B < 1 || N < 1 || static_cast<long long>(B) * N > 0x7fffffffll) return FA_ERR_SHAPE;
     if (!fa::valid_d(d)) return FA_ERR_HEADDIM;
     const long long tokens = static_cast<long long>(B) * N;
-    const fa_status s = fa::check_rope(rope, d, tokens);
+    const fa_status s = fa::check_rope(rope, d);
     if (s != FA_OK) return s;
     fa::RopeLaunch p;
     std::memset(&p, 0, sizeof(p));
@@ -136,6 +135,8 @@ extern "C" fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, c
             if (t->x_stride[j] < 0 || t->y_stride[j] < 0 || t->x_stride[j] > (1ll << 40) ||
                 t->y_stride[j] > (1ll << 40))
                 return FA_ERR_STRIDE;
+            // (Inputs may be expanded; outputs would be written many times.)
+            if (t->y_stride[j] == 0 && (j == 0 ? B : j == 1 ? t->H : N) > 1) return FA_ERR_STRIDE;
             p.t[i].xs[j] = t->x_stride[j];
             p.t[i].ys[j] = t->y_stride[j];
         }

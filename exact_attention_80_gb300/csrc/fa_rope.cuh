@@ -171,7 +171,7 @@ inline bool rope_split(const RopeParams& r) {
     return false;
 }
 // Host side: checks a rotation's description (fa_rope.cu).
-fa_status check_rope(const fa_rotation* rope, int d, long long tokens);
+fa_status check_rope(const fa_rotation* rope, int d);
 RopeParams rope_params(const fa_rotation* rope, long long tokens, bool inverse);
 
 }  // namespace fa

@@ -333,7 +333,8 @@ typedef struct {
  * tensor is bf16 [B][H][N][d] by its strides in elements, {batch, head, token}
  * (multiples of 8; columns contiguous), so it may be head-major, token-major
  * (B = 1) or part of a fused projection; x and y may be the same memory with
- * the same strides. Token (b, n) takes positions[axis][b * N + n]. `inverse`
+ * the same strides (other overlaps are not allowed); strides of 0 expand x, not
+ * y. Token (b, n) takes positions[axis][b * N + n]. `inverse`
  * != 0 turns backwards: the gradient with respect to x of a rotation is the
  * inverse rotation of the gradient with respect to y. Sums and products are
  * rounded one by one in fp32 and once to bf16.
@@ -353,10 +354,13 @@ fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, const fa_rot
  * the value of a code is its e4m3 value times its page's and head's scale.
  * page_size is 16, 32, 64 or 128. Sequence b's token j lies in slot
  * j % page_size of page page_table[b][j / page_size] (int32 [B][max_pages] on
- * the device; entries behind a sequence's last page are not read). Scales are
+ * the device; entries behind a sequence's last page are not read, those of pages
+ * that a window hides may be, and must be pages of the cache). Scales are
  * powers of two in [2^-100, 2^120] where fa_kv_append_fp8 wrote them;
  * fa_fwd_paged_fp8 takes any scales in that range, and a smaller V scale (zero,
- * for a block of zeros) as 2^-100. Cached values must be finite.
+ * for a block of zeros) as 2^-100. The V scales that carry a row's weight should
+ * lie within 2^100 of one another: a key's weight is held relative to the largest
+ * weight times V scale of its row. Cached values must be finite.
  */
 typedef struct {
     void* k;
@@ -384,8 +388,9 @@ typedef struct {
  * The other slots keep their bytes. A sequence whose offsets or length are
  * broken, and a page that is not one of the cache, is neither read nor written
  * (FA_ERR_SEQLENS, FA_ERR_PAGES from fa_device_status); a position outside the
- * table leaves that token's query, and its page's new keys, unwritten. Two
- * sequences must not append to the same page in one call.
+ * table leaves that token's query, and its page's new keys, unwritten. Pages that
+ * are only read may be shared, but no two sequences may append to the same page
+ * in one call, nor one whose table names it twice.
  */
 fa_status fa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_out, const fa_rotation* rope,
                            const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens,

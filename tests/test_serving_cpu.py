@@ -39,6 +39,7 @@ def _tensor(x=FAKE, y=FAKE, H=2, xs=(0, 64, 128), ys=(0, 64, 128)):
     (_tensor(H=0), None, _rotation(), (1, 8, 64), 3), (_tensor(), None, _rotation(), (0, 8, 64), 3),
     (_tensor(), None, _rotation(), (1, 0, 64), 3), (_tensor(), None, _rotation(), (1 << 16, 1 << 16, 64), 3),
     (_tensor(), None, _rotation(), (1, 8, 96), 4),
+    (_tensor(ys=(0, 0, 128)), None, _rotation(), (1, 8, 64), STRIDE),
     (_tensor(), None, _rotation(rot=8), (1, 8, 64), ROPE), (_tensor(), None, _rotation(rot=40), (1, 8, 64), ROPE),
     (_tensor(), None, _rotation(rot=128), (1, 8, 64), ROPE), (_tensor(), None, _rotation(axes=0), (1, 8, 64), ROPE),
     (_tensor(), None, _rotation(axes=5), (1, 8, 64), ROPE), (_tensor(), None, _rotation(max_pos=0), (1, 8, 64), ROPE),
@@ -66,7 +67,7 @@ def _append(lib, q=FAKE, k=FAKE, v=FAKE, q_out=FAKE, rope=None, cache=None, tabl
     (dict(q_out=0), 1), (dict(cache=_cache(k=0)), 1), (dict(cache=_cache(vs=0)), 1), (dict(rope=_rotation(table=0)), 1),
     (dict(k=FAKE + 8), 2), (dict(q_out=FAKE + 4), 2), (dict(table=FAKE + 2), 2), (dict(cache=_cache(v=FAKE + 8)), 2),
     (dict(cache=_cache(ks=FAKE + 2)), 2),
-    (dict(B=0), 3), (dict(total=0), 3), (dict(max_new=0), 3), (dict(max_new=9), 3), (dict(max_pages=0), 3),
+    (dict(B=0), 3), (dict(total=0), 3), (dict(max_new=0), 3), (dict(max_new=9), 3), (dict(max_pages=0), 3), (dict(total=2**31 - 1), 3),
     (dict(H=0), 3), (dict(cache=_cache(pages=0)), 3), (dict(cache=_cache(Hkv=0)), 3),
     (dict(cache=_cache(pages=1 << 28, Hkv=8)), 3), (dict(max_pages=1 << 30), 3),
     (dict(cache=_cache(d=96)), 4),

@@ -1,0 +1,262 @@
+"""Rotary positions, the paged cache and the window in the calls around the usual
+ones: several at once, replayed graphs that share a workspace, padded batches and
+loose bounds, expanded inputs, offsets past 32 bits, scales of empty blocks.
+
+Results of the same kernel on the same values are compared bit by bit; others
+with the float64 oracle at the tolerances of test_serving.py: 2^-8 |o| + 2^-10
+sum_j w_j |v_j|.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import exact_attention_80_gb300 as fa  # noqa: E402
+import oracle.serving as orc  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    fa.load_library()
+    fa.fa_device_status(clear=True)
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_OK
+
+
+def normal(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(torch.bfloat16).cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def cache_of(lens, page, Hkv, d, seed, max_pages=None):
+    """A cache filled by the append itself, its pages in order: (codes and scales, table)."""
+    need = [-(-n // page) for n in lens]
+    P = sum(need)
+    width = max_pages or max(need)
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    c = [torch.zeros((P, Hkv, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.ones((P, Hkv), device="cuda") for _ in range(2)]
+    total = sum(lens)
+    cu = i32([0] + list(np.cumsum(lens)))
+    fa.kv_append_fp8(None, normal((total, Hkv, d), seed), normal((total, Hkv, d), seed + 1), *c, *s, table.cuda(), cu,
+                     i32(lens), max(lens))
+    return c + s, table.cuda()
+
+
+def paged_oracle(q, cache, table, ns, lens, window=0, sinks=0):
+    cu = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    return orc.paged(f64(q), kc, vc, ks, vs, table.cpu().numpy(), cu, lens, fa.default_scale(q.shape[-1]), window, sinks)
+
+
+def check(o, lse, want):
+    ref, ref_lse, a = want
+    assert np.all(np.abs(f64(o) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * a)
+    assert np.all(np.abs(f64(lse) - ref_lse) <= 5e-4)
+
+
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_blocks_of_zeros(n):
+    """V blocks whose scale is zero (a program that never wrote one) count as zeros beside the others."""
+    lens, H, Hkv, d, page = [400], 4, 2, 128, 16
+    cache, table = cache_of(lens, page, Hkv, d, 1)
+    zero = torch.tensor([3, 11, 24], device="cuda")
+    cache[1][zero] = 0
+    cache[3][zero] = 0.0
+    q = normal((n, H, d), 5)
+    o, lse = fa.attention_paged_fp8(q, *cache, table, i32([0, n]), i32(lens), n, 400)
+    ok()
+    cache[3][zero] = 2.0 ** -100
+    check(o, lse, paged_oracle(q, cache, table, [n], lens))
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+def test_loose_bounds_and_padded_batches(splits):
+    """Bounds above what the batch holds, sequences with nothing new at either end, and padding rows give
+    the results of the tight call."""
+    lens, H, Hkv, d, page = [33, 300, 700, 5], 8, 2, 128, 16
+    cache, table = cache_of(lens, page, Hkv, d, 3, max_pages=100)
+    q = normal((9, H, d), 5)
+    cu = i32([0, 0, 2, 3, 3])
+    ns = [0, 2, 1, 0]
+    o = torch.full_like(q, 9.0)
+    lse = torch.full((H, 9), 9.0, device="cuda")
+    ws = torch.empty(fa.fa_paged_workspace_bytes(9, H, d, max(splits, 2)) // 4, device="cuda")
+    fa.fa_fwd_paged_fp8(q, *cache, o, lse, table, cu, i32(lens), 4, 1600, ws, splits)
+    ok()
+    check(o[:3], lse[:, :3], paged_oracle(q[:3], cache, table, ns, lens))
+    assert torch.all(o[3:] == 9.0) and torch.all(lse[:, 3:] == 9.0)
+    # The append with a bound of the whole batch: the same bytes as with a tight one.
+    k, v = normal((9, Hkv, d), 6), normal((9, Hkv, d), 7)
+    one, two = [x.clone() for x in cache], [x.clone() for x in cache]
+    fa.kv_append_fp8(None, k, v, *one, table, cu, i32(lens), 2)
+    fa.kv_append_fp8(None, k, v, *two, table, cu, i32(lens), 9)
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(one, two)) and not torch.equal(one[0], cache[0])
+
+
+def test_expanded_inputs():
+    """One token's k and v for every token, one head's q for every head (strides of zero)."""
+    lens, Hkv, d, page = [40], 2, 64, 16
+    k, v = normal((1, Hkv, d), 1).expand(40, Hkv, d), normal((1, Hkv, d), 2).expand(40, Hkv, d)
+    out = []
+    for a, b in ((k, v), (k.contiguous(), v.contiguous())):
+        c = [torch.zeros((3, Hkv, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+        s = [torch.ones((3, Hkv), device="cuda") for _ in range(2)]
+        fa.kv_append_fp8(None, a, b, *c, *s, i32([[0, 1, 2]]), i32([0, 40]), i32(lens), 40)
+        out.append(c + s)
+    ok()
+    assert all(torch.equal(x, y) for x, y in zip(*out))
+    table = torch.rand(64, d, device="cuda")
+    x = normal((1, 1, 7, d), 3).expand(2, 5, 7, d)
+    pos = torch.randint(0, 64, (2, 7), dtype=torch.int32, device="cuda")
+    assert torch.equal(fa.rope(x, None, table, pos), fa.rope(x.contiguous(), None, table, pos))
+    ok()
+
+
+def test_calls_at_once():
+    """Calls of every kernel on four streams at the same time, many times over: the bits of the calls alone."""
+    d, page, H, Hkv = 128, 16, 8, 2
+    lens = [900, 300, 2000]
+    cache, table = cache_of(lens, page, Hkv, d, 1)
+    jobs = []
+    for ns in ([1, 1, 1], [9, 3, 7], [200, 140, 333]):  # rows, dual and full tiles
+        q = normal((sum(ns), H, d), sum(ns))
+        cu, ln = i32([0] + list(np.cumsum(ns))), i32(lens)
+        jobs.append(lambda s, q=q, cu=cu, ln=ln, n=max(ns): fa.attention_paged_fp8(q, *cache, table, cu, ln, n, 2000,
+                                                                                  num_splits=3, stream=s))
+    wq, wk, wv = normal((1, H, 1000, d), 2), normal((1, Hkv, 1000, d), 3), normal((1, Hkv, 1000, d), 4)
+    jobs.append(lambda s: fa.attention_window(wq, wk, wv, 200, 4, stream=s))
+    table_r, pos = torch.rand(64, d, device="cuda"), torch.randint(0, 64, (1, 1000), dtype=torch.int32, device="cuda")
+    jobs.append(lambda s: fa.rope(wq, wk, table_r, pos, stream=s))
+    alone = []
+    for job in jobs:
+        alone.append(job(None))
+        ok()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        for j, job in enumerate(jobs):
+            got.append((j, job(streams[(i + j) % 4])))
+    ok()
+    for j, out in got:
+        assert all(torch.equal(x, y) for x, y in zip(out, alone[j])), j
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different shapes with one workspace, replayed in turns on one stream."""
+    d, page, H, Hkv = 128, 16, 8, 2
+    lens = [900, 300]
+    cache, table = cache_of(lens, page, Hkv, d, 1)
+    ws = torch.empty(fa.fa_paged_workspace_bytes(64, H, d, 8) // 4, device="cuda")
+    runs = []
+    for ns, splits in (([1, 1], 8), ([30, 34], 3)):
+        n = sum(ns)
+        q, o, lse = normal((n, H, d), n), torch.empty((n, H, d), dtype=torch.bfloat16, device="cuda"), \
+            torch.empty((H, n), device="cuda")
+        cu, ln = i32([0] + list(np.cumsum(ns))), i32(lens)
+        args = (q, *cache, o, lse, table, cu, ln, max(ns), 900, ws, splits)
+        fa.fa_fwd_paged_fp8(*args)
+        ok()
+        want = (o.clone(), lse.clone())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fa.fa_fwd_paged_fp8(*args)
+        runs.append((g, o, lse, want, args))  # (a graph does not keep its tensors)
+    for _ in range(10):
+        for g, o, lse, _, _ in runs:
+            o.zero_()
+            lse.zero_()
+            g.replay()
+        ok()
+        for g, o, lse, want, _ in runs:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_cache_past_32_bit_offsets(n):
+    """Pages whose codes lie more than 2^32 bytes into the cache."""
+    d, page, H, Hkv = 128, 64, 8, 4
+    pages = (5 << 30) // (Hkv * page * d)
+    lens = [500]
+    small, st = cache_of(lens, page, Hkv, d, 1)
+    q, k, v = normal((n, H, d), 5), normal((n, Hkv, d), 6), normal((n, Hkv, d), 7)
+    big = [torch.empty((pages, Hkv, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    big += [torch.empty((pages, Hkv), device="cuda") for _ in range(2)]
+    table = st.clone()
+    for i in range(8):
+        at = pages - 1 - 2 * i
+        table[0, i] = at
+        for x, y in zip(big, small):
+            x[at] = y[i]
+    cu, ln = i32([0, n]), i32(lens)
+    for cache, t in ((big, table), (small, st)):
+        fa.kv_append_fp8(None, k, v, *cache, t, cu, ln, n)
+    got = fa.attention_paged_fp8(q, *big, table, cu, ln, n, 500, num_splits=2)
+    want = fa.attention_paged_fp8(q, *small, st, cu, ln, n, 500, num_splits=2)
+    ok()
+    for i in range(8):
+        assert all(torch.equal(x[table[0, i]], y[i]) for x, y in zip(big, small))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rope_past_32_bit_offsets():
+    N, d = 33, 64
+    far = (1 << 31) + 64
+    buf = torch.empty(far + 2 * N * d, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((2, 2, N, d), (far, N * d, d, 1))
+    x.copy_(normal((2, 2, N, d), 1))
+    table, pos = torch.rand(64, d, device="cuda"), torch.randint(0, 64, (2, N), dtype=torch.int32, device="cuda")
+    want = fa.rope(x.contiguous(), None, table, pos)
+    fa.fa_rope(x, None, x, None, table, pos)
+    ok()
+    assert torch.equal(x, want)
+
+
+def test_window_past_32_bit_offsets():
+    """2^31 query elements: the last rows of the last head, forward and backward, against the call on
+    the keys and rows that they depend on alone."""
+    H, Hkv, d, W = 64, 8, 128, 100
+    N = (1 << 31) // (H * d) + 192
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, do = (torch.randn((1, H, N, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn((1, Hkv, N, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    o, lse = fa.attention_window(q, k, v, W)
+    dq, dk, dv = fa.attention_window_backward(q, k, v, o, lse, do, W)
+    ok()
+    # Rows N - R and later see the last R + W - 1 keys; the last R keys are seen by
+    # rows N - R and later alone.
+    R = 64
+    G = H // Hkv
+    qs, dos = (f64(t[:, -G:, -R:]) for t in (q, do))
+    ks, vs = (f64(t[:, -1:, -(R + W - 1):]) for t in (k, v))
+    scale = fa.default_scale(d)
+    ro, rl = orc.window_forward(qs, ks, vs, scale, W, 0)
+    rq, rk, rv = orc.window_backward(qs, ks, vs, dos, scale, W, 0)
+    rel = lambda x, y: np.linalg.norm(f64(x) - y) / np.linalg.norm(y)  # noqa: E731
+    # Norms of errors that are independent roundings: O one rounding of P and one of O
+    # (2^-9 on average, at most 2^-7); gradients a few more.
+    assert rel(o[:, -G:, -R:], ro) <= 2.0 ** -7 and np.abs(f64(lse[:, -G:, -R:]) - rl).max() <= 1e-3
+    assert rel(dq[:, -G:, -R:], rq) <= 2.0 ** -7
+    assert rel(dk[:, -1:, -R:], rk[:, :, -R:]) <= 2.0 ** -7 and rel(dv[:, -1:, -R:], rv[:, :, -R:]) <= 2.0 ** -7
