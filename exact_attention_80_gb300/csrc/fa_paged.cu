@@ -525,19 +525,21 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         }
         const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
         const long long row = static_cast<long long>(nt.first + i) * p.H + h * p.G + j;
+        // States that the row does not use are marked as empty for the merge.
+        if (split == 0 && p.num_splits > 1)
+            for (int s = (used == 1 ? 0 : used) + c; s < p.num_splits; s += VEC)
+                p.ws_m[static_cast<long long>(s) * p.total_q * p.H + row] = -INFINITY;
         if (used == 1) {
-            const float inv = ll > 0.f ? 1.f / ll : 0.f;
+            const float inv = ll == 0.f ? 0.f : 1.f / ll;
             *reinterpret_cast<uint2*>(p.o + row * D + 4 * c) =
                 make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-            // l is a sum of 2^(x - m + 7): the shift comes out again.
             if (c == 0)
-                p.lse[static_cast<long long>(h * p.G + j) * p.total_q + nt.first + i] =
-                    ll > 0.f ? (mm - kPShift + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+                p.lse[static_cast<long long>(h * p.G + j) * p.total_q + nt.first + i] = state_lse(mm, ll);
         } else {
             const long long at = static_cast<long long>(split) * p.total_q * p.H + row;
             *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
             if (c == 0) {
-                p.ws_m[at] = mm;
+                p.ws_m[at] = state_ref(mm, ll);
                 p.ws_l[at] = ll;
             }
         }
@@ -545,9 +547,11 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
 }
 
 // Merge of the key splits of the (token, head) rows whose block used more than
-// one: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s. W warps (1 or
-// 4) share a row, each with eight partial rows in flight: the merge of a single
-// sequence's few rows over many splits is a matter of latency alone.
+// one: M = max m_s, O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s. States with
+// m = -inf were not used (all of them where the row is finished already) or
+// saw no key. W warps (1 or 4) share a row, each with eight partial rows in
+// flight: the merge of a single sequence's few rows over many splits is a matter
+// of latency alone.
 template <int D, int W>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
     constexpr int PER = D / 32, U = 8;
@@ -564,21 +568,9 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     const int b = static_cast<int>(rest / p.max_q);
     NewTokens nt;
     bool live = b < p.B && new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt) && i < nt.n;
-    int used = 0;
-    if (live) {
-        // The row block of this row decides how many splits it used.
-        const int r = i * p.G + head % p.G;
-        const int r0 = r / p.block_rows * p.block_rows, rows = nt.n * p.G;
-        const int start = nt.len - nt.n;
-        const int p0 = start + r0 / p.G, p1 = start + (min(r0 + p.block_rows, rows) - 1) / p.G;
-        const KeyList list = p.block_keys == kTcKeys ? key_list<kTcKeys>(p.window, p.sinks, p0, p1)
-                                                     : key_list<rows_keys(D)>(p.window, p.sinks, p0, p1);
-        used = (list.n + p.tiles_per_split - 1) / p.tiles_per_split;
-        live = used > 1;
-    }
     const long long row = live ? static_cast<long long>(nt.first + i) * p.H + head : 0;
     const long long stride = static_cast<long long>(p.total_q) * p.H;
-    if (!live) used = 0;
+    const int states = live ? p.num_splits : 0;
     const float* src = p.ws_o + row * D + lane * PER;
     float x[U][PER];
     auto load = [&](int s0) {
@@ -587,22 +579,29 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
             const int s = s0 + u * W;
 #pragma unroll
             for (int e = 0; e < PER; e += 2) {
-                const float2 a = s < used ? *reinterpret_cast<const float2*>(src + s * stride * D + e) : make_float2(0.f, 0.f);
+                const float2 a = s < states ? *reinterpret_cast<const float2*>(src + s * stride * D + e) : make_float2(0.f, 0.f);
                 x[u][e] = a.x;
                 x[u][e + 1] = a.y;
             }
         }
     };
     load(wi);
+    int used = 0;
     float mm = -INFINITY;
-    for (int s = lane; s < used; s += 32) mm = fmaxf(mm, p.ws_m[s * stride + row]);
+    for (int s = lane; s < states; s += 32) {
+        const float m = p.ws_m[s * stride + row];
+        if (m != -INFINITY) used = s + 1, mm = fmaxf(mm, m);
+    }
+    used = __reduce_max_sync(0xffffffffu, used);
+    live = used > 0;
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     const float ref = mm == -INFINITY ? 0.f : mm;
     float ll = 0.f;
     for (int s = lane; s < used; s += 32) {
-        const float f = ex2(p.ws_m[s * stride + row] - ref);
+        const float m = p.ws_m[s * stride + row];
+        const float f = ex2(m - ref);
         weight[warp][s] = f;
-        ll = fmaf(f, p.ws_l[s * stride + row], ll);
+        if (m != -INFINITY) ll = fmaf(f, p.ws_l[s * stride + row], ll);
     }
     for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
     __syncwarp();
@@ -615,6 +614,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * W;
             const float f = s < used ? weight[warp][s] : 0.f;
+            if (f == 0.f) continue;  // an unused state holds anything
 #pragma unroll
             for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
         }
@@ -629,13 +629,12 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
             for (int e = 0; e < PER; ++e) acc[e] += sums[warp + k][lane * PER + e];
     }
     if (!live) return;
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * PER);
 #pragma unroll
     for (int e = 0; e < PER; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0)
-        p.lse[static_cast<long long>(head) * p.total_q + nt.first + i] =
-            ll > 0.f ? (ref - kPShift + log2f(ll)) * 0.69314718055994530942f : -INFINITY;
+        p.lse[static_cast<long long>(head) * p.total_q + nt.first + i] = state_lse(ref, ll);
 }
 
 // e4m3 cache as [rows][d], box {min(d, 128), box_rows}, swizzled by row size.
@@ -687,7 +686,26 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 // length (measured: 64 contexts of 8192 to 32768, 512 units: 600 us with one
 // split, 511 with three, 480 with eight; one of 131072, 8 units: 52 us in one
 // wave of splits, 74 in four).
-int best_splits(int B, long long units, long long rounds, int slots, int per_cta, bool many_rows) {
+//
+// Pairs of slots (dual): a CTA takes pieces of whatever length balances the
+// sequences at hand (tc_piece), so only the most pieces of a sequence are chosen
+// here: an even share of all of them, ten rounds a piece for its start and end,
+// and half a piece for the last ones, with sequences at two thirds of the longest
+// on average (five drafted tokens, pieces of the longest against us: 16 contexts
+// of up to 16200 keys, 2: 138, 3: 113, 4: 117, 5: 124; 64 of 32768, 1: 741, 2: 709,
+// 3: 739; 80 of 8192, 1: 268, 2: 289).
+int best_splits(int B, long long units, long long rounds, int slots, bool dual, bool many_rows) {
+    if (dual && B > 1) {
+        int best = 1;
+        double best_cost = -1.;
+        const double R = static_cast<double>(rounds), start = 10.;
+        for (int c = 1; c <= FA_MAX_SPLITS / 2 && (c == 1 || 2 * c <= rounds); ++c) {
+            const double even = units * (0.65 * R + (c == 1 ? 1. : 0.65 * c + 0.35) * start) / kTcAtOnce + 0.5 * R / c;
+            const double cost = std::max(even, R / c + start);
+            if (best_cost < 0. || cost < best_cost) best = c, best_cost = cost;
+        }
+        return static_cast<int>(std::min(2ll * best, std::max(1ll, rounds)));
+    }
     // (Partial sums of 256 rows cost more than they even out: two chunks of 2048
     // tokens over 16384 keys, 341 us with one split, 430 with four.)
     if (many_rows && units >= slots) return 1;
@@ -696,7 +714,7 @@ int best_splits(int B, long long units, long long rounds, int slots, int per_cta
     long long best = 1;
     double best_cost = -1.;
     for (long long s = 1; s <= most; ++s) {
-        const long long ctas = units * ((s + per_cta - 1) / per_cta);
+        const long long ctas = dual ? units * tc_pieces(static_cast<int>(s)) : units * s;
         const double each = static_cast<double>((rounds + s - 1) / s) + start;
         const double cost = (B == 1 || many_rows ? static_cast<double>((ctas + slots - 1) / slots) * each
                                                  : (1. + 0.65 * static_cast<double>(ctas) / slots) * each) +
@@ -745,7 +763,7 @@ int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_
     const long long units = static_cast<long long>(B) * Hkv * c.row_blocks;
     const long long rounds = std::max(1ll, c.tiles * c.block_keys / 128);
     // CTAs at once: one per SM for the tensor-core kernel.
-    return fa::best_splits(B, units, rounds, 152 * (c.tc ? 1 : fa::rows_ctas(d)), c.dual ? 2 : 1, c.tc && !c.dual);
+    return fa::best_splits(B, units, rounds, 152 * (c.tc ? 1 : fa::rows_ctas(d)), c.dual, c.tc && !c.dual);
 }
 
 size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits) {
@@ -816,6 +834,7 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     p.num_splits = num_splits;
     p.dual = c.dual ? 1 : 0;
     p.row_warps = c.dual ? (max_seqlen_q * p.G + 31) / 32 : 4;
+    p.balance = c.dual && num_splits > 1 && B > 1 && B <= fa::kTcBalance;
     p.tiles_per_split = static_cast<int>((c.tiles + num_splits - 1) / num_splits);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit = fa::kDefaultWaitLimit;

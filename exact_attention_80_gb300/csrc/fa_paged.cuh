@@ -83,12 +83,20 @@ struct PagedParams {
     int row_blocks, num_splits, tiles_per_split;  // row blocks of block_rows rows, tiles of block_keys keys
     int block_rows, block_keys;
     // fa_paged_tc.cu: the two tile slots take the same rows and two splits; warps
-    // of a row tile that can have rows.
-    int dual, row_warps;
+    // of a row tile that can have rows; whether the CTAs choose the pieces' length.
+    int dual, row_warps, balance;
     float scale_log2;
     long long wait_limit;
     unsigned* status;
 };
+
+// What a partial state leaves as its reference m: -inf marks a state that saw no
+// key, or that no CTA filled; a NaN sum stays one through the merge.
+__device__ __forceinline__ float state_ref(float m, float l) { return l > 0.f ? m : l == 0.f ? -INFINITY : l; }
+// LSE of a row's reference and sum (of 2^(x - m + 7): the shift comes out again).
+__device__ __forceinline__ float state_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * 0.69314718055994530942f;
+}
 
 // The key tiles a row block visits, as a list: tiles 0 .. ns - 1 (sinks), then
 // tile `lo` on, n in all. Positions p0 .. p1 are the block's first and last.
@@ -158,6 +166,11 @@ fa_status check_cache(const fa_paged_cache* cache);
 // tiles, or one tile twice over two splits), keys per tile.
 constexpr int kTcRows = 128;
 constexpr int kTcKeys = 128;
+constexpr int kTcAtOnce = 152;      // its CTAs running at a time: one per SM
+constexpr int kTcStart = 5;         // start and end of a CTA, in key tiles of a pair of slots
+constexpr int kTcBalance = 64;      // sequences up to which a call's pieces are balanced
+// Pieces of a unit at most, where a piece leaves the states of two slots.
+__host__ __device__ __forceinline__ int tc_pieces(int num_splits) { return num_splits > 1 ? num_splits / 2 : 1; }
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream);
 inline int log2_exact(int x) {
     int n = 0;

@@ -89,21 +89,56 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 
 struct TcWork {
     NewTokens nt;
-    int b, h, rows, start, used;
-    int split[2];  // key split of each tile slot
+    int b, h, rows, start;
+    int used;      // states that its rows leave (1: the result)
+    int split[2];  // state of each tile slot
     int row0[2];   // first row of each tile slot
     KeyList list;
-    int i0[2];     // first list entry of its split
+    int i0[2];     // first list entry of its part
     int n[2];      // key tiles each row tile visits
     int nmax;
     int p0, p1;    // positions of the unit's first and last row
     bool live;
 };
 
+// Key tiles of a piece, the share of a CTA's two slots, where all row blocks are
+// one per sequence: their lengths differ, and so the pieces are cut as long as
+// makes the waves of CTAs shortest (16 sequences of five drafted tokens over 4600
+// to 16200 keys, 8 kv heads: 113 us, against 123 with the same length for all
+// calls of the shape). Called by a whole warp; every lane tries one length.
+__device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
+    int n[kTcBalance / 32];
+    int longest = 0;
+#pragma unroll
+    for (int i = 0; i < kTcBalance / 32; ++i) {
+        const int b = lane + 32 * i;
+        NewTokens t;
+        n[i] = 0;
+        if (b < p.B && new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, t) && t.n > 0)
+            n[i] = key_list<kTcKeys>(p.window, p.sinks, t.len - t.n, t.len - 1).n;
+        longest = max(longest, n[i]);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const int least = 2 * p.tiles_per_split;  // as the workspace allows
+    if (longest <= least) return least;
+    const int len = least + (longest - least) * lane / 31;
+    const float inv = 1.f / static_cast<float>(len);
+    int pieces = 0;  // (rounded about right: only the choice depends on it)
+    for (int b = 0; b < p.B; ++b) {
+        const int x = __shfl_sync(0xffffffffu, b < 32 ? n[0] : n[1], b & 31);
+        pieces += static_cast<int>(fmaf(static_cast<float>(x), inv, 0.999f));
+    }
+    const int waves = (pieces * p.Hkv + kTcAtOnce - 1) / kTcAtOnce;
+    const unsigned cost = static_cast<unsigned>(waves * (len + kTcStart));
+    const unsigned best = __reduce_min_sync(0xffffffffu, cost);
+    const int at = __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1;
+    return __shfl_sync(0xffffffffu, len, at);
+}
+
 template <bool DUAL>
-__device__ __forceinline__ void tc_work(const PagedParams& p, TcWork& w) {
+__device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork& w) {
     constexpr int ROWS = DUAL ? kTcRows : 2 * kTcRows;
-    const int per_unit = DUAL ? (p.num_splits + 1) / 2 : p.num_splits;
+    const int per_unit = DUAL ? tc_pieces(p.num_splits) : p.num_splits;
     unsigned lin = blockIdx.x;
     const int si = static_cast<int>(lin % per_unit);
     lin /= per_unit;
@@ -126,17 +161,34 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, TcWork& w) {
     w.p0 = w.start + r0 / p.G;
     w.p1 = w.start + (min(r0 + ROWS, w.rows) - 1) / p.G;
     w.list = key_list<kTcKeys>(p.window, p.sinks, w.p0, w.p1);
+    if constexpr (DUAL) {
+        // Pieces of equal length; the slots take a half each (all of it goes to the
+        // first one where there is no workspace).
+        const int pieces = min(per_unit, max(1, (w.list.n + piece - 1) / piece));
+        w.live = si < pieces;
+        if (!w.live) return;
+        const int e0 = static_cast<int>(static_cast<long long>(w.list.n) * si / pieces);
+        const int e1 = static_cast<int>(static_cast<long long>(w.list.n) * (si + 1) / pieces);
+        const int mid = p.num_splits > 1 ? (e0 + e1 + 1) / 2 : e1;
+        w.used = pieces == 1 && mid == e1 ? 1 : 2 * pieces;
+        w.split[0] = 2 * si, w.split[1] = 2 * si + 1;
+        w.row0[0] = w.row0[1] = r0;
+        w.i0[0] = e0, w.i0[1] = mid;
+        w.n[0] = w.nmax = mid - e0;
+        w.n[1] = e1 - mid;
+        return;
+    }
     w.used = max(1, (w.list.n + p.tiles_per_split - 1) / p.tiles_per_split);
-    w.live = (DUAL ? 2 * si : si) < w.used;
+    w.live = si < w.used;
     if (!w.live) return;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         // Slot 0 takes the later rows, whose tile ends last: the issuer serves
-        // it first. Dual: the same rows, splits 2 si and 2 si + 1.
-        w.split[t] = DUAL ? 2 * si + t : si;
-        w.row0[t] = DUAL ? r0 : r0 + (1 - t) * kTcRows;
-        w.i0[t] = w.split[t] * p.tiles_per_split;
-        if (w.row0[t] >= w.rows || w.split[t] >= w.used) continue;
+        // it first.
+        w.split[t] = si;
+        w.row0[t] = r0 + (1 - t) * kTcRows;
+        w.i0[t] = si * p.tiles_per_split;
+        if (w.row0[t] >= w.rows) continue;
         const int last = w.start + (min(w.row0[t] + kTcRows, w.rows) - 1) / p.G;
         const int end = w.list.ns + max(0, last / kTcKeys + 1 - w.list.lo);
         w.n[t] = max(0, min(min(w.list.n, w.i0[t] + p.tiles_per_split), end) - w.i0[t]);
@@ -214,6 +266,12 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
     }
+    if constexpr (DUAL) {
+        if (warp == 2) {
+            const int piece = p.balance ? tc_piece(p, lane) : 2 * p.tiles_per_split;
+            if (lane == 0) misc[2] = piece;
+        }
+    }
     if (warp == 1) {
         tmem_alloc(sbase + L::MISC_OFF, 512);
         tmem_relinquish();
@@ -222,11 +280,12 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
+    const int piece = DUAL ? static_cast<int>(misc[2]) : 0;
 
     if (warp < 4 || warp >= L::CONV_WARP0) {
         setmaxnreg_dec<L::CTRL_REGS>();
         TcWork w;
-        tc_work<DUAL>(p, w);
+        tc_work<DUAL>(p, piece, w);
         if (w.live && warp == 0) {
             // -------------------------------------------------------- producer
             // Entries in the issuer's order: K_0; then per step j: V_j, K_{j+1}.
@@ -497,19 +556,20 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
         // ------------------------------------------------------------ softmax
         setmaxnreg_inc<L::SOFTMAX_REGS>();
         TcWork w;
-        tc_work<DUAL>(p, w);
+        tc_work<DUAL>(p, piece, w);
         const int t = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;
         const int n = t ? w.n[1] : w.n[0];
         const int first_row = t ? w.row0[1] : w.row0[0];
         const int split = t ? w.split[1] : w.split[0];
+        const bool part = !DUAL || n > 0;  // whether the slot has a part of the unit
         const int i0 = t ? w.i0[1] : w.i0[0];
         // Warps of a tile that no sequence of the call has rows for (20 of 128 rows:
         // three of four) leave their lanes of Q, S and P as they are: those rows
         // of O mean nothing and are not read. They take no part in the barriers
         // either; polling them would slow the others' shared-memory traffic.
-        if (w.live && first_row < w.rows && split < w.used && quarter < p.row_warps) {
+        if (w.live && first_row < w.rows && part && quarter < p.row_warps) {
             const int row = first_row + r;
             const bool row_ok = row < w.rows;
             const int i = (row_ok ? row : w.rows - 1) / p.G;
@@ -770,7 +830,7 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                 if (ok) tc_fence_after();
             }
             if (ok) {
-                const float f = w.used == 1 ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+                const float f = w.used == 1 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 const long long at = static_cast<long long>(split) * p.total_q * p.H + out_row;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
@@ -803,11 +863,20 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                     }
                 }
                 if (row_ok) {
+                    // States that the row does not use are marked as empty for the
+                    // merge: those of a slot without a part, and the last ones.
+                    if (p.num_splits > 1 && (!DUAL || t == 0)) {
+                        const long long stride = static_cast<long long>(p.total_q) * p.H;
+                        if (DUAL && w.n[1] == 0 && w.used > 1) p.ws_m[(split + 1) * stride + out_row] = -INFINITY;
+                        if (split == 0)
+                            for (int s = w.used == 1 ? 0 : w.used; s < p.num_splits; ++s)
+                                p.ws_m[s * stride + out_row] = -INFINITY;
+                    }
                     if (w.used == 1) {
                         p.lse[static_cast<long long>(head) * p.total_q + w.nt.first + i] =
-                            l > 0.f ? (m - kPShift + log2f(l)) * 0.69314718055994530942f : -INFINITY;
+                            state_lse(m, l);
                     } else {
-                        p.ws_m[at] = l > 0.f ? m : -INFINITY;
+                        p.ws_m[at] = state_ref(m, l);
                         p.ws_l[at] = l;
                     }
                 }
@@ -838,7 +907,7 @@ cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const int per_unit = DUAL ? (p.num_splits + 1) / 2 : p.num_splits;
+    const int per_unit = DUAL ? tc_pieces(p.num_splits) : p.num_splits;
     const long long ctas = static_cast<long long>(p.B) * p.Hkv * per_unit * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_paged_tc_kernel<D, DUAL>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
