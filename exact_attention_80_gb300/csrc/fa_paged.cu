@@ -661,11 +661,12 @@ struct Plan {
 Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     Plan c;
     const long long rows = static_cast<long long>(max_q) * G;
-    // The tensor-core kernel from 17 rows at d = 128, from 33 at d = 64: up to there
-    // two blocks of 16 rows, which read K and V twice, are as fast (16 sequences of
-    // 32 rows over up to 16200 keys: 144 against 138 us at d = 128, 100 against 115
-    // at d = 64; at 36 rows 191 against 140 and 127 against 114).
-    c.tc = d <= 128 && rows > (d == 64 ? 2 * kRows : kRows);
+    // The tensor-core kernel from 17 rows on (d = 256: no room in shared memory). One
+    // block of 16 rows is faster here, two, which read K and V twice, are not (16
+    // sequences over up to 16200 keys, us here and there: 16 rows 87 and 92 at d =
+    // 128, 55 and 82 at d = 64; 20 rows 128 and 106, 94 and 82; four of up to 2000
+    // keys at d = 64, 20 rows: 14 and 17).
+    c.tc = d <= 128 && rows > kRows;
     c.dual = c.tc && rows <= kTcRows;
     c.block_rows = !c.tc ? kRows : c.dual ? kTcRows : 2 * kTcRows;
     c.block_keys = c.tc ? kTcKeys : rows_keys(d);
@@ -691,9 +692,9 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 // sequences at hand (tc_piece), so only the most pieces of a sequence are chosen
 // here: an even share of all of them, ten rounds a piece for its start and end,
 // and half a piece for the last ones, with sequences at two thirds of the longest
-// on average (five drafted tokens, pieces of the longest against us: 16 contexts
-// of up to 16200 keys, 2: 138, 3: 113, 4: 117, 5: 124; 64 of 32768, 1: 741, 2: 709,
-// 3: 739; 80 of 8192, 1: 268, 2: 289).
+// on average (five drafted tokens, pieces of the longest and us: 16 contexts of up
+// to 16200 keys, 1: 137, 2: 129, 3: 106, 4: 109; 64 of 32768, 1: 605, 2: 579, 3: 609;
+// 80 of 8192, 1: 219, 2: 245; 2 of 16200, 8: 24.8, 10: 24.5, 12: 28.7).
 int best_splits(int B, long long units, long long rounds, int slots, bool dual, bool many_rows) {
     if (dual && B > 1) {
         int best = 1;
@@ -704,7 +705,7 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
             const double cost = std::max(even, R / c + start);
             if (best_cost < 0. || cost < best_cost) best = c, best_cost = cost;
         }
-        return static_cast<int>(std::min(2ll * best, std::max(1ll, rounds)));
+        return best;
     }
     // (Partial sums of 256 rows cost more than they even out: two chunks of 2048
     // tokens over 16384 keys, 341 us with one split, 430 with four.)
@@ -714,7 +715,7 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
     long long best = 1;
     double best_cost = -1.;
     for (long long s = 1; s <= most; ++s) {
-        const long long ctas = dual ? units * tc_pieces(static_cast<int>(s)) : units * s;
+        const long long ctas = units * s;
         const double each = static_cast<double>((rounds + s - 1) / s) + start;
         const double cost = (B == 1 || many_rows ? static_cast<double>((ctas + slots - 1) / slots) * each
                                                  : (1. + 0.65 * static_cast<double>(ctas) / slots) * each) +
@@ -832,8 +833,9 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     p.block_keys = c.block_keys;
     p.row_blocks = static_cast<int>(c.row_blocks);
     p.num_splits = num_splits;
-    p.dual = c.dual ? 1 : 0;
-    p.row_warps = c.dual ? (max_seqlen_q * p.G + 31) / 32 : 4;
+    const int row_warps = (max_seqlen_q * p.G + 31) / 32;
+    p.shares = !c.dual ? 0 : row_warps > 2 ? 1 : row_warps == 2 ? 2 : 4;
+    p.slot_warps = p.shares == 1 ? row_warps : 4;
     p.balance = c.dual && num_splits > 1 && B > 1 && B <= fa::kTcBalance;
     p.tiles_per_split = static_cast<int>((c.tiles + num_splits - 1) / num_splits);
     p.scale_log2 = scale * 1.4426950408889634f;

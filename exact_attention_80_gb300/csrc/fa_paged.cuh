@@ -82,9 +82,10 @@ struct PagedParams {
     int window, sinks;
     int row_blocks, num_splits, tiles_per_split;  // row blocks of block_rows rows, tiles of block_keys keys
     int block_rows, block_keys;
-    // fa_paged_tc.cu: the two tile slots take the same rows and two splits; warps
-    // of a row tile that can have rows; whether the CTAs choose the pieces' length.
-    int dual, row_warps, balance;
+    // fa_paged_tc.cu: shares of a key tile's columns that copies of the rows take
+    // (1, 2 or 4; 0: full tiles); softmax warps of a tile slot; whether the CTAs
+    // choose the pieces' length.
+    int shares, slot_warps, balance;
     float scale_log2;
     long long wait_limit;
     unsigned* status;
@@ -169,8 +170,6 @@ constexpr int kTcKeys = 128;
 constexpr int kTcAtOnce = 152;      // its CTAs running at a time: one per SM
 constexpr int kTcStart = 5;         // start and end of a CTA, in key tiles of a pair of slots
 constexpr int kTcBalance = 64;      // sequences up to which a call's pieces are balanced
-// Pieces of a unit at most, where a piece leaves the states of two slots.
-__host__ __device__ __forceinline__ int tc_pieces(int num_splits) { return num_splits > 1 ? num_splits / 2 : 1; }
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream);
 inline int log2_exact(int x) {
     int n = 0;

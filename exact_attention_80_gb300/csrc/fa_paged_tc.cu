@@ -19,9 +19,13 @@
 // reciprocal; scores are handled in groups of 16 keys, the smallest page.
 //
 // DUAL: at most 128 rows (drafts, short chunks). Both tile slots take the same
-// rows, each with a key split of its own, so that the two still alternate on the
-// tensor core (16 sequences of five drafted tokens over up to 16200 keys: 120
-// us, against 200 with one tile slot idle).
+// rows, each with half of the CTA's keys, so that the two still alternate on the
+// tensor core; their states meet in shared memory at the end. With at most 32
+// (64) rows a slot's 128 lanes hold them four times (twice), and each copy's
+// warps take their share of a tile's columns with weights of zero for the others:
+// the MMAs cost the same, and four warps rather than one form a tile's
+// exponentials (five drafted tokens, 20 rows, 64 contexts of up to 32768 keys: 579
+// us against 709 without shares; one of 131072: 60 against 76).
 //
 // Roles, by warp: 0 producer (Q is written by the softmax threads; K and V pages
 // by TMA into two rings), 1 issuer, 2-3 idle, 4-11 softmax (thread = row = TMEM
@@ -38,8 +42,10 @@
 namespace fa {
 namespace {
 
-template <int D, bool DUAL>
+// SHARES: 0 for full tiles, else the dual form and its shares.
+template <int D, int SHARES>
 struct TcLayout {
+    static constexpr bool DUAL = SHARES > 0;
     static constexpr int BM = 128, BN = kTcKeys;
     static constexpr int ROW_BYTES = D < 128 ? D : 128;   // swizzled row of codes
     // Dual slots share one row tile, which leaves room for deeper rings.
@@ -56,6 +62,9 @@ struct TcLayout {
     static constexpr uint32_t V_OFF = K_OFF + KSTAGES * SLOT;
     static constexpr uint32_t V16_OFF = V_OFF + VSTAGES * SLOT;
     static constexpr uint32_t BAR_OFF = V16_OFF + 2 * V16;
+    // DUAL, at the end: fp32 O of both slots' 128 lanes, then m and l.
+    static constexpr uint32_t ML_OFF = 2 * BM * D * 4;
+    static_assert(!DUAL || ML_OFF + 2 * 2 * BM * 4 <= BAR_OFF, "the states overwrite barriers");
     static constexpr int BAR_QFULL = 0;                    // [tile] one arrival per softmax warp with rows
     static constexpr int BAR_KFULL = 2;
     static constexpr int BAR_KEMPTY = BAR_KFULL + KSTAGES;
@@ -91,7 +100,7 @@ struct TcWork {
     NewTokens nt;
     int b, h, rows, start;
     int used;      // states that its rows leave (1: the result)
-    int split[2];  // state of each tile slot
+    int split;     // the state that this CTA leaves
     int row0[2];   // first row of each tile slot
     KeyList list;
     int i0[2];     // first list entry of its part
@@ -104,8 +113,8 @@ struct TcWork {
 // Key tiles of a piece, the share of a CTA's two slots, where all row blocks are
 // one per sequence: their lengths differ, and so the pieces are cut as long as
 // makes the waves of CTAs shortest (16 sequences of five drafted tokens over 4600
-// to 16200 keys, 8 kv heads: 113 us, against 123 with the same length for all
-// calls of the shape). Called by a whole warp; every lane tries one length.
+// to 16200 keys, 8 kv heads: 8 % less time than with the same length for all calls
+// of the shape). Called by a whole warp; every lane tries one length.
 __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
     int n[kTcBalance / 32];
     int longest = 0;
@@ -119,7 +128,7 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
         longest = max(longest, n[i]);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
-    const int least = 2 * p.tiles_per_split;  // as the workspace allows
+    const int least = p.tiles_per_split;  // as the workspace allows
     if (longest <= least) return least;
     const int len = least + (longest - least) * lane / 31;
     const float inv = 1.f / static_cast<float>(len);
@@ -138,7 +147,7 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
 template <bool DUAL>
 __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork& w) {
     constexpr int ROWS = DUAL ? kTcRows : 2 * kTcRows;
-    const int per_unit = DUAL ? tc_pieces(p.num_splits) : p.num_splits;
+    const int per_unit = p.num_splits;
     unsigned lin = blockIdx.x;
     const int si = static_cast<int>(lin % per_unit);
     lin /= per_unit;
@@ -162,16 +171,15 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     w.p1 = w.start + (min(r0 + ROWS, w.rows) - 1) / p.G;
     w.list = key_list<kTcKeys>(p.window, p.sinks, w.p0, w.p1);
     if constexpr (DUAL) {
-        // Pieces of equal length; the slots take a half each (all of it goes to the
-        // first one where there is no workspace).
+        // Pieces of equal length; the slots take a half each.
         const int pieces = min(per_unit, max(1, (w.list.n + piece - 1) / piece));
+        w.used = pieces;
         w.live = si < pieces;
         if (!w.live) return;
         const int e0 = static_cast<int>(static_cast<long long>(w.list.n) * si / pieces);
         const int e1 = static_cast<int>(static_cast<long long>(w.list.n) * (si + 1) / pieces);
-        const int mid = p.num_splits > 1 ? (e0 + e1 + 1) / 2 : e1;
-        w.used = pieces == 1 && mid == e1 ? 1 : 2 * pieces;
-        w.split[0] = 2 * si, w.split[1] = 2 * si + 1;
+        const int mid = (e0 + e1 + 1) / 2;
+        w.split = si;
         w.row0[0] = w.row0[1] = r0;
         w.i0[0] = e0, w.i0[1] = mid;
         w.n[0] = w.nmax = mid - e0;
@@ -181,11 +189,11 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     w.used = max(1, (w.list.n + p.tiles_per_split - 1) / p.tiles_per_split);
     w.live = si < w.used;
     if (!w.live) return;
+    w.split = si;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         // Slot 0 takes the later rows, whose tile ends last: the issuer serves
         // it first.
-        w.split[t] = si;
         w.row0[t] = r0 + (1 - t) * kTcRows;
         w.i0[t] = si * p.tiles_per_split;
         if (w.row0[t] >= w.rows) continue;
@@ -227,9 +235,10 @@ __device__ __forceinline__ int tc_page(const PagedParams& p, const TcWork& w, co
     return id;
 }
 
-template <int D, bool DUAL>
-__global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_kernel(const __grid_constant__ PagedParams p) {
-    using L = TcLayout<D, DUAL>;
+template <int D, int SHARES>
+__global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_kernel(const __grid_constant__ PagedParams p) {
+    using L = TcLayout<D, SHARES>;
+    constexpr bool DUAL = L::DUAL;
     constexpr int BN = L::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -253,9 +262,9 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(L::BAR_HFULL + t), L::CONV_WARPS);
             mbar_init(bar(L::BAR_HEMPTY + t), 1);
-            mbar_init(bar(L::BAR_QFULL + t), p.row_warps);
+            mbar_init(bar(L::BAR_QFULL + t), p.slot_warps);
             mbar_init(bar(L::BAR_SFULL + t), 1);
-            mbar_init(bar(L::BAR_PFULL + t), p.row_warps);
+            mbar_init(bar(L::BAR_PFULL + t), p.slot_warps);
             mbar_init(bar(L::BAR_OFULL + t), 1);
         }
         mbar_init(bar(L::BAR_DRAIN), 1);
@@ -268,7 +277,7 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
     }
     if constexpr (DUAL) {
         if (warp == 2) {
-            const int piece = p.balance ? tc_piece(p, lane) : 2 * p.tiles_per_split;
+            const int piece = p.balance ? tc_piece(p, lane) : p.tiles_per_split;
             if (lane == 0) misc[2] = piece;
         }
     }
@@ -559,18 +568,22 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
         tc_work<DUAL>(p, piece, w);
         const int t = (warp - 4) >> 2;
         const int quarter = warp & 3;
-        const int r = quarter * 32 + lane;
+        const int r = quarter * 32 + lane;  // TMEM lane, row of the Q tile
+        // Shares: with at most 32 (64) rows, every 32 (64) lanes hold them again,
+        // and each copy takes a quarter (half) of the key tile's columns.
+        constexpr int shares = DUAL ? SHARES : 1;
+        const int tile_row = shares == 4 ? lane : shares == 2 ? r & 63 : r;
+        const int share = shares == 4 ? quarter : shares == 2 ? quarter >> 1 : 0;
         const int n = t ? w.n[1] : w.n[0];
         const int first_row = t ? w.row0[1] : w.row0[0];
-        const int split = t ? w.split[1] : w.split[0];
         const bool part = !DUAL || n > 0;  // whether the slot has a part of the unit
         const int i0 = t ? w.i0[1] : w.i0[0];
-        // Warps of a tile that no sequence of the call has rows for (20 of 128 rows:
-        // three of four) leave their lanes of Q, S and P as they are: those rows
-        // of O mean nothing and are not read. They take no part in the barriers
-        // either; polling them would slow the others' shared-memory traffic.
-        if (w.live && first_row < w.rows && part && quarter < p.row_warps) {
-            const int row = first_row + r;
+        // A warp of a tile that no sequence of the call has rows for leaves its
+        // lanes of Q, S and P as they are: those rows of O mean nothing and are
+        // not read. It takes no part in the barriers either; polling them would
+        // slow the others' shared-memory traffic.
+        if (w.live && first_row < w.rows && part && quarter < p.slot_warps) {
+            const int row = first_row + tile_row;
             const bool row_ok = row < w.rows;
             const int i = (row_ok ? row : w.rows - 1) / p.G;
             const int head = w.h * p.G + (row_ok ? row : w.rows - 1) - i * p.G;
@@ -669,12 +682,13 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                     alpha = move ? ex2(m - m_use) : 1.f;
                 };
                 if constexpr (DUAL) {
-                    // 32 columns of S at a time, read twice (for the maximum, then for
-                    // the exponentials), in loops that are not unrolled: where few
-                    // warps run this code, long straight stretches of it wait for
-                    // their instructions (20 rows: 120 us against 140; the other way
-                    // round for full tiles, 2 x 2048 tokens over 16384 keys: 395
-                    // against 328).
+                    // This share's columns, 32 of S at a time: read once where they
+                    // are all of them, else twice (for the maximum, then for the
+                    // exponentials) in loops that are not unrolled: where few warps
+                    // run this code, long straight stretches of it wait for their
+                    // instructions (20 rows without shares: 120 us against 140; the
+                    // other way round for full tiles, 2 x 2048 tokens over 16384
+                    // keys: 395 against 328).
                     const bool whole = __all_sync(0xffffffffu, valid >= BN && (p.window <= 0 || valid <= p.window ||
                                                                                 p.sinks - key0 >= BN));
                     auto chunk = [&](int cc, float (&s)[32], float (&kc)[2], float (&vc)[2]) {
@@ -696,10 +710,7 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                                 if (c >= end || (c < from && c >= sink)) s[c] = -INFINITY;
                         }
                     };
-#pragma unroll 1
-                    for (int cc = 0; cc < BN / 32; ++cc) {
-                        float s[32], kc[2], vc[2];
-                        chunk(cc, s, kc, vc);
+                    auto maximum = [&](const float (&s)[32], const float (&kc)[2], const float (&vc)[2]) {
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             float a = max3f(s[16 * g], s[16 * g + 1], s[16 * g + 2]);
@@ -711,12 +722,8 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                             a = max3f(a, s[16 * g + 14], s[16 * g + 15]);
                             top = fmaxf(top, fmaf(fmaxf(a, b), kc[g], vc[g]));
                         }
-                    }
-                    reference();
-#pragma unroll 1
-                    for (int cc = 0; cc < BN / 32; ++cc) {
-                        float s[32], kc[2], vc[2];
-                        chunk(cc, s, kc, vc);
+                    };
+                    auto exponentials = [&](int cc, const float (&s)[32], const float (&kc)[2], const float (&vc)[2]) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
@@ -738,6 +745,37 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                         }
                         // P's 16 columns lie over S columns that have been read.
                         tmem_st16(tS + cc * 16, pk);
+                    };
+                    const uint32_t zero[16] = {};
+                    if constexpr (shares == 4) {
+                        float s[32], kc[2], vc[2];
+                        chunk(share, s, kc, vc);
+                        // The weights of the other shares' keys are zero for these
+                        // rows.
+#pragma unroll
+                        for (int cc = 1; cc < 4; ++cc) tmem_st16(tS + ((share + cc) & 3) * 16, zero);
+                        maximum(s, kc, vc);
+                        reference();
+                        exponentials(share, s, kc, vc);
+                    } else {
+                        const int c0 = 2 * share, c1 = shares == 2 ? c0 + 2 : BN / 32;
+#pragma unroll 1
+                        for (int cc = c0; cc < c1; ++cc) {
+                            float s[32], kc[2], vc[2];
+                            chunk(cc, s, kc, vc);
+                            maximum(s, kc, vc);
+                        }
+                        reference();
+#pragma unroll 1
+                        for (int cc = c0; cc < c1; ++cc) {
+                            float s[32], kc[2], vc[2];
+                            chunk(cc, s, kc, vc);
+                            exponentials(cc, s, kc, vc);
+                        }
+                        if constexpr (shares == 2) {
+#pragma unroll
+                            for (int cc = 0; cc < 2; ++cc) tmem_st16(tS + ((c0 ^ 2) + cc) * 16, zero);
+                        }
                     }
                 } else {
                     float s[BN];
@@ -829,9 +867,77 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                 ok = tc_wait_warp(bar(L::BAR_OFULL + t), 0, p, abort_flag, kStatusWaitO);
                 if (ok) tc_fence_after();
             }
-            if (ok) {
+            if constexpr (DUAL) {
+                // The states of both slots' rows and their shares meet in shared
+                // memory, which no copy or MMA of this CTA uses any more once all of
+                // them have come here. (A warp that gave up comes here as well.)
+                constexpr int UNITS = D / 4;  // float4 units of a row
+                const int slots = w.n[1] > 0 ? 2 : 1, warps = p.slot_warps * slots;
+                auto meet = [&] { asm volatile("bar.sync 1, %0;" ::"r"(32 * warps) : "memory"); };
+                meet();
+                float4* stage = reinterpret_cast<float4*>(smem);
+                float* ml = reinterpret_cast<float*>(smem + L::ML_OFF);  // [slot][m, l][128 lanes]
+                if (ok) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + cc * 32, o);
+                        tmem_wait_ld();
+                        // (Units swapped row by row: no bank conflicts.)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            stage[(t * 128 + r) * UNITS + ((cc * 8 + e) ^ (lane & (UNITS - 1)))] =
+                                make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                    }
+                    ml[t * 256 + r] = state_ref(m, l);
+                    ml[t * 256 + 128 + r] = l;
+                }
+                meet();
+                const int here = min(kTcRows, w.rows - first_row);
+                // (Warp `quarter` of slot t is t * slot_warps + quarter of them all.)
+                for (int u = (t * p.slot_warps + quarter) * 32 + lane; u < here * UNITS && !*abort_flag; u += 32 * warps) {
+                    const int rr = u / UNITS, c = u - rr * UNITS;
+                    float mm = -INFINITY, ll = 0.f;
+                    // A row's copies lie 128 / shares lanes apart.
+                    for (int s = 0; s < slots; ++s)
+                        for (int x = 0; x < shares; ++x) mm = fmaxf(mm, ml[s * 256 + rr + x * (128 / shares)]);
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int s = 0; s < slots; ++s)
+                        for (int x = 0; x < shares; ++x) {
+                            const int at = rr + x * (128 / shares);
+                            const float ms = ml[s * 256 + at];
+                            const float f = ms == -INFINITY ? 0.f : ex2(ms - mm);
+                            const float4 y = stage[(s * 128 + at) * UNITS + (c ^ (at & 31 & (UNITS - 1)))];
+                            ll = fmaf(f, ml[s * 256 + 128 + at], ll);
+                            a.x = fmaf(f, y.x, a.x), a.y = fmaf(f, y.y, a.y), a.z = fmaf(f, y.z, a.z),
+                            a.w = fmaf(f, y.w, a.w);
+                        }
+                    const int qi = (first_row + rr) / p.G, qh = w.h * p.G + (first_row + rr) - qi * p.G;
+                    const long long to = static_cast<long long>(w.nt.first + qi) * p.H + qh;
+                    // States that the row does not use are marked as empty for the
+                    // merge.
+                    if (w.split == 0 && p.num_splits > 1)
+                        for (int s = (w.used == 1 ? 0 : w.used) + c; s < p.num_splits; s += UNITS)
+                            p.ws_m[static_cast<long long>(s) * p.total_q * p.H + to] = -INFINITY;
+                    if (w.used == 1) {
+                        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                        *reinterpret_cast<uint2*>(p.o + to * D + 4 * c) =
+                            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+                        if (c == 0)
+                            p.lse[static_cast<long long>(qh) * p.total_q + w.nt.first + qi] = state_lse(mm, ll);
+                    } else {
+                        const long long at = static_cast<long long>(w.split) * p.total_q * p.H + to;
+                        *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
+                        if (c == 0) {
+                            p.ws_m[at] = state_ref(mm, ll);
+                            p.ws_l[at] = ll;
+                        }
+                    }
+                }
+            } else if (ok) {
                 const float f = w.used == 1 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const long long at = static_cast<long long>(split) * p.total_q * p.H + out_row;
+                const long long at = static_cast<long long>(w.split) * p.total_q * p.H + out_row;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -864,14 +970,10 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
                 }
                 if (row_ok) {
                     // States that the row does not use are marked as empty for the
-                    // merge: those of a slot without a part, and the last ones.
-                    if (p.num_splits > 1 && (!DUAL || t == 0)) {
-                        const long long stride = static_cast<long long>(p.total_q) * p.H;
-                        if (DUAL && w.n[1] == 0 && w.used > 1) p.ws_m[(split + 1) * stride + out_row] = -INFINITY;
-                        if (split == 0)
-                            for (int s = w.used == 1 ? 0 : w.used; s < p.num_splits; ++s)
-                                p.ws_m[s * stride + out_row] = -INFINITY;
-                    }
+                    // merge.
+                    if (w.split == 0 && p.num_splits > 1)
+                        for (int s = w.used == 1 ? 0 : w.used; s < p.num_splits; ++s)
+                            p.ws_m[static_cast<long long>(s) * p.total_q * p.H + out_row] = -INFINITY;
                     if (w.used == 1) {
                         p.lse[static_cast<long long>(head) * p.total_q + w.nt.first + i] =
                             state_lse(m, l);
@@ -891,34 +993,39 @@ __global__ void __launch_bounds__(TcLayout<D, DUAL>::THREADS, 1) fa_paged_tc_ker
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool DUAL>
+template <int D, int SHARES>
 cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
-    using L = TcLayout<D, DUAL>;
+    using L = TcLayout<D, SHARES>;
     static ContextCache<int> attr_set;
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         // The setmaxnreg split is sized for exactly LAUNCH_REGS per thread.
         cudaFuncAttributes a;
-        cudaError_t err = cudaFuncGetAttributes(&a, fa_paged_tc_kernel<D, DUAL>);
+        cudaError_t err = cudaFuncGetAttributes(&a, fa_paged_tc_kernel<D, SHARES>);
         if (err != cudaSuccess) return err;
         if (a.numRegs != L::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
         *out = 1;
-        return cudaFuncSetAttribute(fa_paged_tc_kernel<D, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_paged_tc_kernel<D, SHARES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const int per_unit = DUAL ? tc_pieces(p.num_splits) : p.num_splits;
-    const long long ctas = static_cast<long long>(p.B) * p.Hkv * per_unit * p.row_blocks;
+    const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(fa_paged_tc_kernel<D, DUAL>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
+    return launch_dependent(fa_paged_tc_kernel<D, SHARES>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
                             stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream) {
-    if (p.dual) return d == 64 ? launch_tc<64, true>(p, stream) : launch_tc<128, true>(p, stream);
-    return d == 64 ? launch_tc<64, false>(p, stream) : launch_tc<128, false>(p, stream);
+    auto launch = [&](auto d_) {
+        constexpr int D = decltype(d_)::value;
+        return p.shares == 0   ? launch_tc<D, 0>(p, stream)
+               : p.shares == 1 ? launch_tc<D, 1>(p, stream)
+               : p.shares == 2 ? launch_tc<D, 2>(p, stream)
+                               : launch_tc<D, 4>(p, stream);
+    };
+    return d == 64 ? launch(Index<64>{}) : launch(Index<128>{});
 }
 
 }  // namespace fa
