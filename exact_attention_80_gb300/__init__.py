@@ -640,6 +640,14 @@ def _cache_view(k_cache, v_cache, k_scale, v_scale, index):
         raise ValueError(f"k_cache and v_cache must be [num_pages, Hkv, page_size, d], got {tuple(shape)} and "
                          f"{tuple(v_cache.shape)}")
     pages, heads, size, d = shape
+    kt, vt, u8, f8, f32 = k_cache.dtype, v_cache.dtype, torch.uint8, torch.float8_e4m3fn, torch.float32
+    if ((kt is u8 or kt is f8) and (vt is u8 or vt is f8) and k_scale.dtype is f32 and v_scale.dtype is f32
+            and k_scale.shape == (pages, heads) == v_scale.shape and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and k_cache.get_device() == index == v_cache.get_device()
+            and k_scale.get_device() == index == v_scale.get_device()):
+        return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
+                                 heads, size, d), heads, d
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
             raise TypeError(f"{name} must hold e4m3 codes (uint8 or float8_e4m3fn), got {t.dtype}")
@@ -650,23 +658,24 @@ def _cache_view(k_cache, v_cache, k_scale, v_scale, index):
             raise TypeError(f"{name} must be float32, got {t.dtype}")
         if tuple(t.shape) != (pages, heads) or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be contiguous {(pages, heads)} on device {index}")
-    return _PAGED_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
-                             heads, size, d), heads, d
+    raise ValueError("k_cache, v_cache, k_scale and v_scale do not agree")
 
 
 def _batch_view(page_table, cu_seqlens, seqlens_k, index):
     """(B, max_pages) of a batch's device arrays."""
     import torch
 
+    i32 = torch.int32
+    shape = page_table.shape
+    if (page_table.dtype is i32 and cu_seqlens.dtype is i32 and seqlens_k.dtype is i32 and len(shape) == 2
+            and shape[0] > 0 and cu_seqlens.shape == (shape[0] + 1,) and seqlens_k.shape == (shape[0],)
+            and page_table.is_contiguous() and cu_seqlens.is_contiguous() and seqlens_k.is_contiguous()
+            and page_table.get_device() == index == cu_seqlens.get_device() and seqlens_k.get_device() == index):
+        return shape
     for t, name in ((page_table, "page_table"), (cu_seqlens, "cu_seqlens"), (seqlens_k, "seqlens_k")):
         if t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != index:
             raise ValueError(f"{name} must be contiguous int32 on device {index}")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
-    if B < 1 or tuple(cu_seqlens.shape) != (B + 1,) or tuple(seqlens_k.shape) != (B,):
-        raise ValueError("page_table [B, max_pages], cu_seqlens [B+1] and seqlens_k [B] must agree on B >= 1")
-    return B, max_pages
+    raise ValueError("page_table [B, max_pages], cu_seqlens [B+1] and seqlens_k [B] must agree on B >= 1")
 
 
 def _check_out(t, name, shape, dtype, index):
