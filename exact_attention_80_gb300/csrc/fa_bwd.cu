@@ -221,6 +221,8 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
                                           uint32_t nd, float sl2, int lim, bool key_ok, uint32_t (&pk)[16],
                                           uint32_t (&dk)[16], int end = 0) {
     const uint64_t sl2x2 = f2pack(sl2, sl2);
+    // (One bit per column rather than two comparisons each.)
+    const uint32_t seen = WIN && key_ok ? low_bits(end) & ~low_bits(lim) : 0u;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         float l4[4], d4[4];
@@ -239,7 +241,8 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
             // The exponential runs for every element and the mask selects after
             // it (x is finite or -inf: no NaN), so there are no branches.
             const float ex = ex2(x[h]);
-            pv[h] = MASK ? ((key_ok && 4 * u + h >= lim && (!WIN || 4 * u + h < end)) ? ex : 0.f) : ex;
+            if constexpr (WIN && MASK) pv[h] = (seen & (1u << (4 * u + h))) ? ex : 0.f;
+            else pv[h] = MASK ? ((key_ok && 4 * u + h >= lim) ? ex : 0.f) : ex;
         }
         const uint64_t g01 = fadd2(f2pack(__uint_as_float(dp[4 * u]), __uint_as_float(dp[4 * u + 1])),
                                    f2pack(d4[0], d4[1]));

@@ -101,21 +101,19 @@ __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long l
 // 32-key chunks that an edge crosses, and leaving out the exponentials of chunks
 // that no row of the warp sees, costs more than it saves: the branches keep the
 // chunks' instructions apart, 216 -> 332 us for 2 x 32 heads of 8192, window
-// 1024, d = 64.)
+// 1024, d = 64. One bit per key, from shifts: with a comparison per key and edge
+// the same call takes 216 us against 203.)
 template <int BN>
 __device__ __forceinline__ void win_mask(const FwdParams& p, int pos, int kv0, float (&s)[BN]) {
     const int valid = pos - kv0 + 1;
-    if (valid < BN) {
+    const int from = p.window > 0 ? valid - p.window : 0, sink = p.sinks - kv0;
+    if (valid < BN || (from > 0 && sink < BN)) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c)
-            if (c >= valid) s[c] = -INFINITY;
-    }
-    if (p.window > 0) {
-        const int from = valid - p.window, sink = p.sinks - kv0;
-        if (from > 0 && sink < BN) {
+        for (int g = 0; g < BN / 32; ++g) {
+            const uint32_t seen = low_bits(valid - 32 * g) & (~low_bits(from - 32 * g) | low_bits(sink - 32 * g));
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-                if (c < from && c >= sink) s[c] = -INFINITY;
+            for (int c = 0; c < 32; ++c)
+                if (!(seen & (1u << c))) s[32 * g + c] = -INFINITY;
         }
     }
 }

@@ -704,10 +704,11 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                         for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(raw[e]);
                         if (!whole) {
                             const int end = valid - 32 * cc, from = p.window > 0 ? end - p.window : 0;
-                            const int sink = p.sinks - key0 - 32 * cc;
+                            const uint32_t seen =
+                                low_bits(end) & (~low_bits(from) | low_bits(p.sinks - key0 - 32 * cc));
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (c >= end || (c < from && c >= sink)) s[c] = -INFINITY;
+                                if (!(seen & (1u << c))) s[c] = -INFINITY;
                         }
                     };
                     auto maximum = [&](const float (&s)[32], const float (&kc)[2], const float (&vc)[2]) {
@@ -787,17 +788,16 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                         for (int e = 0; e < 32; ++e) s[cc * 32 + e] = __uint_as_float(raw[e]);
                     }
                     tmem_wait_ld();
-                    if (valid < BN) {
+                    const int from = p.window > 0 ? valid - p.window : 0, sink = p.sinks - key0;
+                    if (valid < BN || (from > 0 && sink < BN)) {
+                        // One bit per key: half the instructions of comparisons.
 #pragma unroll
-                        for (int c = 0; c < BN; ++c)
-                            if (c >= valid) s[c] = -INFINITY;
-                    }
-                    if (p.window > 0) {
-                        const int from = valid - p.window, sink = p.sinks - key0;
-                        if (from > 0 && sink < BN) {
+                        for (int g = 0; g < BN / 32; ++g) {
+                            const uint32_t seen =
+                                low_bits(valid - 32 * g) & (~low_bits(from - 32 * g) | low_bits(sink - 32 * g));
 #pragma unroll
-                            for (int c = 0; c < BN; ++c)
-                                if (c < from && c >= sink) s[c] = -INFINITY;
+                            for (int c = 0; c < 32; ++c)
+                                if (!(seen & (1u << c))) s[32 * g + c] = -INFINITY;
                         }
                     }
                     __syncwarp();
