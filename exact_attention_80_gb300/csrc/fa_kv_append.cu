@@ -188,6 +188,24 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : 3) fa_kv_append
             c[i] = *reinterpret_cast<const uint4*>(row + c1);
         }
     }
+    // The slots' positions, all at once; a slot without a token takes row 0.
+    int at[PER];
+    if constexpr (!SPLIT) {
+        if (turn && live) {
+            const int* axis = rope_axis(p.r, v);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int slot = lo + slot0 + i * slot_step;
+                at[i] = slot >= hi ? 0 : p.r.positions ? axis[tok0 + slot] : (blk << p.log_page) + slot;
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const bool outside = static_cast<unsigned>(at[i]) >= static_cast<unsigned>(p.r.max_pos);
+                bad = bad || outside;
+                at[i] = outside ? 0 : at[i];
+            }
+        }
+    }
     int page = -1;
     if (live) {
         page = p.page_table[static_cast<long long>(b) * p.max_pages + blk];
@@ -202,7 +220,13 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : 3) fa_kv_append
         const int slot = lo + slot0 + i * slot_step;
         unpack_bf16x8(a[i], x);
         unpack_bf16x8(c[i], y);
-        if (turn && live && slot < hi && !bad) {
+        if constexpr (!SPLIT) {
+            if (turn && live) {
+                float co[8], si[8];
+                rope_row(p.r, v, at[i], co, si);
+                rope_apply(p.r.interleaved != 0, co, si, x, y);
+            }
+        } else if (turn && live && slot < hi && !bad) {
             float co[8], si[8];
             if (rope_coeffs<SPLIT>(p.r, v, tok0 + slot, (blk << p.log_page) + slot, co, si))
                 rope_apply(p.r.interleaved != 0, co, si, x, y);

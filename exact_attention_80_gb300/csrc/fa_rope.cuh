@@ -42,6 +42,24 @@ __device__ __forceinline__ void rope_columns(const RopeParams& r, int v, int& c0
     c1 = (pair && !r.interleaved) ? 8 * v + (r.rot >> 1) : 16 * v + 8;
 }
 
+// Where the positions of the axis that pair 8 v turns with begin.
+__device__ __forceinline__ const int* rope_axis(const RopeParams& r, int v) {
+    int a = 0;
+    while (a + 1 < r.axes && 8 * v >= r.sec_end[a]) ++a;
+    return r.positions + a * r.pos_stride;
+}
+// Cosines and sines of pairs 8 v .. 8 v + 7 at a position of the table.
+__device__ __forceinline__ void rope_row(const RopeParams& r, int v, int pos, float (&c)[8], float (&s)[8]) {
+    const float* row = r.table + static_cast<long long>(pos) * r.rot + 8 * v;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float4 x = reinterpret_cast<const float4*>(row)[k];
+        const float4 y = reinterpret_cast<const float4*>(row + (r.rot >> 1))[k];
+        c[4 * k] = x.x, c[4 * k + 1] = x.y, c[4 * k + 2] = x.z, c[4 * k + 3] = x.w;
+        s[4 * k] = y.x, s[4 * k + 1] = y.y, s[4 * k + 2] = y.z, s[4 * k + 3] = y.w;
+    }
+}
+
 // Cosines and (signed) sines of pairs 8 v .. 8 v + 7 of token `tok` (own_pos
 // stands in where there is no position array). False where a position of these
 // pairs is outside the table, which is then not read. SPLIT: sections may end
@@ -50,23 +68,15 @@ __device__ __forceinline__ void rope_columns(const RopeParams& r, int v, int& c0
 template <bool SPLIT>
 __device__ __forceinline__ bool rope_coeffs(const RopeParams& r, int v, long long tok, int own_pos,
                                             float (&c)[8], float (&s)[8]) {
-    const int i0 = 8 * v;
-    const int half = r.rot >> 1;
-    int a = 0;
-    while (a + 1 < r.axes && i0 >= r.sec_end[a]) ++a;
-    const int* at = r.positions + a * r.pos_stride + tok;
     if constexpr (!SPLIT) {
-        const int pos = r.positions ? *at : own_pos;
+        const int pos = r.positions ? rope_axis(r, v)[tok] : own_pos;
         if (static_cast<unsigned>(pos) >= static_cast<unsigned>(r.max_pos)) return false;
-        const float* row = r.table + static_cast<long long>(pos) * r.rot + i0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float4 x = reinterpret_cast<const float4*>(row)[k];
-            const float4 y = reinterpret_cast<const float4*>(row + half)[k];
-            c[4 * k] = x.x, c[4 * k + 1] = x.y, c[4 * k + 2] = x.z, c[4 * k + 3] = x.w;
-            s[4 * k] = y.x, s[4 * k + 1] = y.y, s[4 * k + 2] = y.z, s[4 * k + 3] = y.w;
-        }
+        rope_row(r, v, pos, c, s);
     } else {
+        const int i0 = 8 * v;
+        int a = 0;
+        while (a + 1 < r.axes && i0 >= r.sec_end[a]) ++a;
+        const int* at = r.positions + a * r.pos_stride + tok;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             while (a + 1 < r.axes && i0 + k >= r.sec_end[a]) {
@@ -76,7 +86,7 @@ __device__ __forceinline__ bool rope_coeffs(const RopeParams& r, int v, long lon
             if (static_cast<unsigned>(*at) >= static_cast<unsigned>(r.max_pos)) return false;
             const float* row = r.table + static_cast<long long>(*at) * r.rot + i0 + k;
             c[k] = row[0];
-            s[k] = row[half];
+            s[k] = row[r.rot >> 1];
         }
     }
 #pragma unroll
