@@ -36,6 +36,7 @@ FA_MAX_SPLITS = 256
 FA_MAX_AXES = 4
 
 _lib = None
+_compiled = None  # the module _calls, from load_library
 
 
 class FAError(RuntimeError):
@@ -104,7 +105,26 @@ def load_library() -> ctypes.CDLL:
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
     _lib = lib
+    _load_calls(lib)
     return lib
+
+
+def _load_calls(lib):
+    """The compiled form of the calls that a few microseconds matter to (csrc/fa_calls.cpp), where
+    PyTorch is installed."""
+    global _compiled
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return
+    if not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_calls.so")):
+        raise RuntimeError("_calls.so is missing: build it with `python -m exact_attention_80_gb300.build`")
+    from . import _calls as calls  # type: ignore[attr-defined]
+
+    calls.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.fa_rope, lib.fa_kv_append_fp8, lib.fa_fwd_paged_fp8, lib.fa_paged_num_splits,
+        lib.fa_paged_workspace_bytes, lib.fa_fwd_window, lib.fa_bwd_window, lib.fa_bwd_window_workspace_bytes)))
+    _compiled = calls
 
 
 def fa_status_string(status: int) -> str:
@@ -459,8 +479,10 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
 
 # ------------------------------------------ rotary positions and the paged cache
 # These calls are short (a decode step of a few sequences runs in a few
-# microseconds on the GPU), so their checks touch each tensor once, and the
-# interface's structs are packed as bytes.
+# microseconds on the GPU). On the current stream and with plain arguments rope,
+# kv_append_fp8, attention_paged_fp8 and the window's two calls run in the
+# compiled module _calls; it answers None where an argument is anything else, and the forms below, whose
+# checks touch each tensor once, say what is wrong or take the call.
 _ROTATION = struct.Struct(f"PPii{FA_MAX_AXES}iii")   # fa_rotation
 _ROPE_TENSOR = struct.Struct("PPi6q")                # fa_rope_tensor
 _PAGED_CACHE = struct.Struct("PPPPiiii")             # fa_paged_cache
@@ -608,6 +630,12 @@ def fa_rope(q, k, q_out, k_out, table, positions, sections=None, interleaved=Fal
 def rope(q, k, table, positions, sections=None, interleaved=False, inverse=False, stream=None):
     """:func:`fa_rope` into new contiguous outputs. Returns ``(q_out, k_out)``, or ``q_out`` where
     ``k`` is None."""
+    if stream is None and _compiled is not None:
+        out = _compiled.rope(q, k, table, positions, sections, interleaved, inverse)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_rope")
+            return out
     q_out, k_out = _rope(q, k, None, None, table, positions, sections, interleaved, inverse, stream)
     if stream is not None:
         _used_on(stream, q_out, k_out)
@@ -740,6 +768,13 @@ def kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
                   table=None, positions=None, sections=None, interleaved=False, stream=None):
     """:func:`fa_kv_append_fp8` into new rotated queries; returns them (None without ``q``). Tokens
     past ``cu_seqlens[B]`` are left as allocated."""
+    if stream is None and _compiled is not None:
+        out = _compiled.append(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k, max_seqlen,
+                            table, positions, sections, interleaved)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_kv_append_fp8")
+            return None if out is True else out
     q_out = _append(q, k, v, None, True, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
                     max_seqlen, table, positions, sections, interleaved, stream)
     if stream is not None:
@@ -814,6 +849,13 @@ def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     """:func:`fa_fwd_paged_fp8` into new outputs, with a workspace of its own (``num_splits`` None:
     the library's proposal). Returns ``(o, lse)``; rows past ``cu_seqlens_q[B]`` are left as
     allocated."""
+    if stream is None and _compiled is not None:
+        out = _compiled.paged(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+                           max_seqlen_k, window, sinks, scale, num_splits)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_fwd_paged_fp8")
+            return out
     o, lse, ws = _paged(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
                         max_seqlen_q, max_seqlen_k, None, num_splits, window, sinks, scale, stream)
     if stream is not None:
@@ -857,6 +899,12 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
 
 def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
     """Allocate ``o`` and ``lse`` and run :func:`fa_fwd_window`. Returns ``(o, lse)``."""
+    if stream is None and _compiled is not None:
+        out = _compiled.window(q, k, v, window, sinks, scale)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_fwd_window")
+            return out
     import torch
 
     o = torch.empty_like(q)
@@ -893,6 +941,12 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
 def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0, scale: float | None = None,
                               stream=None):
     """Allocate ``(dq, dk, dv)`` and the workspace and run :func:`fa_bwd_window`."""
+    if stream is None and _compiled is not None:
+        out = _compiled.window_backward(q, k, v, o, lse, dout, window, sinks, scale)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_bwd_window")
+            return out
     import torch
 
     B, H, Hkv, Nq, Nk, d, _ = _grouped(q, k, v)

@@ -2,7 +2,9 @@
 
 Each ``csrc/*.cu`` translation unit is compiled by ``nvcc`` in parallel, then
 linked into one shared library beside this file. Only a CUDA toolkit with
-sm_103a support is needed (the build cross-compiles without a GPU).
+sm_103a support is needed (the build cross-compiles without a GPU). Where
+PyTorch is installed, ``csrc/fa_calls.cpp`` is built beside them as the Python
+module ``_calls`` against its headers.
 
 Usage: ``python -m exact_attention_80_gb300.build [--ptxas-verbose]``
 """
@@ -10,16 +12,19 @@ Usage: ``python -m exact_attention_80_gb300.build [--ptxas-verbose]``
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa_gb300.so")
+CALLS = os.path.join(PKG, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,6 +51,26 @@ def _compile(nvcc: str, src: str, ptxas_verbose: bool) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
+def build_calls() -> str | None:
+    """Compile ``csrc/fa_calls.cpp`` into the module ``_calls``; None without PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
+    torch = spec.submodule_search_locations[0]
+    inc, tmp = os.path.join(torch, "include"), CALLS + ".tmp"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
+           "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "fa_calls.cpp"), "-o", tmp,
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fa_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(ptxas_verbose: bool = False, quiet: bool = True) -> str:
     """Compile every CUDA source and link the library; returns its path."""
     nvcc = nvcc_path()
@@ -53,12 +78,14 @@ def build(ptxas_verbose: bool = False, quiet: bool = True) -> str:
     srcs = sources()
     logs = []
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        calls = ex.submit(build_calls)
         futs = [ex.submit(_compile, nvcc, s, ptxas_verbose) for s in srcs]
         objs = []
         for f in futs:
             obj, log = f.result()
             objs.append(obj)
             logs.append(log)
+        calls.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

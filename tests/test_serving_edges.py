@@ -260,3 +260,69 @@ def test_window_past_32_bit_offsets():
     assert rel(o[:, -G:, -R:], ro) <= 2.0 ** -7 and np.abs(f64(lse[:, -G:, -R:]) - rl).max() <= 1e-3
     assert rel(dq[:, -G:, -R:], rq) <= 2.0 ** -7
     assert rel(dk[:, -1:, -R:], rk[:, :, -R:]) <= 2.0 ** -7 and rel(dv[:, -1:, -R:], rv[:, :, -R:]) <= 2.0 ** -7
+
+
+def test_compiled_calls_equal_the_python_ones():
+    """The compiled form of a call and the Python one (taken on a stream that is named) give the same bits, and
+    errors come from either as they should."""
+    fa.load_library()
+    here = torch.cuda.current_stream()
+    q, k = normal((2, 4, 33, 64), 1), normal((2, 2, 33, 64), 2)
+    table = torch.rand(99, 64, device="cuda")
+    pos = torch.randint(0, 99, (3, 2, 33), dtype=torch.int32, device="cuda")
+    fused = normal((50, 8, 128), 3)
+    rows, rpos = torch.rand(99, 96, device="cuda"), torch.randint(0, 99, (1, 50), dtype=torch.int32, device="cuda")
+    for a, kw in (((q, k, table, pos), dict(sections=(8, 12, 12))), ((q, None, table, pos[0]), dict(inverse=True)),
+                  ((q.transpose(1, 2).contiguous().transpose(1, 2), k, table, pos), dict(sections=[8, 24, 0])),
+                  ((fused[:, :6], fused[:, 6:], rows, rpos), dict(interleaved=True)),
+                  ((q[:1].expand(2, 4, 33, 64), k, table, pos[1]), {})):
+        assert fa._compiled.rope(*a, kw.get("sections"), kw.get("interleaved", False), kw.get("inverse", False)) is not None
+        x, y = fa.rope(*a, **kw), fa.rope(*a, **kw, stream=here)
+        ok()
+        for u, v in zip(x if a[1] is not None else (x,), y if a[1] is not None else (y,)):
+            assert torch.equal(u, v) and u.is_contiguous() and u.dtype is torch.bfloat16
+    lens, d, page = [50, 20], 128, 16
+    cache, pages = cache_of(lens, page, 1, d, 1)
+    cu = i32([0, 3, 4])
+    for qq, kw in ((fused[:4, :6], dict(table=rows)), (None, {}),
+                   (fused[:4, :6], dict(table=rows, positions=rpos[0, :4].contiguous(), interleaved=True)),
+                   (fused[:4, :6], dict(table=rows, positions=rpos[:, :4].repeat(2, 1).contiguous(), sections=(20, 28)))):
+        got = []
+        for stream in (None, here):
+            c = [x.clone() for x in cache]
+            got.append([fa.kv_append_fp8(qq, fused[:4, 6:7], fused[:4, 7:], *c, pages, cu, i32(lens), 3, **kw,
+                                         stream=stream)] + c)
+            ok()
+        assert (got[0][0] is None) == (qq is None)
+        assert all(x is None or torch.equal(x, y) for x, y in zip(*got))
+    qd = normal((4, 6, 128), 9)
+    for kw in ({}, dict(num_splits=2, window=9, sinks=2), dict(scale=0.2)):
+        x, y = (fa.attention_paged_fp8(qd, *cache, pages, cu, i32(lens), 3, 60, **kw, stream=s) for s in (None, here))
+        ok()
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    w = [normal(x, i, 0.5) for i, x in enumerate([(2, 4, 150, 64), (2, 2, 170, 64), (2, 2, 170, 64), (2, 4, 150, 64)])]
+    for kw in (dict(sinks=3), dict(scale=0.2)):
+        x, y = (fa.attention_window(*w[:3], 40, **kw, stream=s) for s in (None, here))
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+        x, y = (fa.attention_window_backward(*w[:3], *x, w[3], 40, **kw, stream=s) for s in (None, here))
+        ok()
+        assert torch.equal(x[1], y[1]) and torch.equal(x[2], y[2])
+        # (dQ is summed by atomics: at most a rounding of bf16 apart, and of the fp32 sums.)
+        assert (x[0].float() - y[0].float()).abs().max() <= 2.0 ** -7 * y[0].float().abs().max()
+    # Errors: a status of the library's, and what only the Python form names.
+    for bad, err in ((lambda: fa.attention_paged_fp8(qd, *cache, pages, cu, i32(lens), 3, 60, sinks=1), fa.FAError),
+                     (lambda: fa.attention_paged_fp8(qd, *cache, pages, cu, i32(lens), 3, 10 ** 6), fa.FAError),
+                     (lambda: fa.attention_paged_fp8(qd.float(), *cache, pages, cu, i32(lens), 3, 60), TypeError),
+                     (lambda: fa.attention_paged_fp8(qd, *cache, pages.long(), cu, i32(lens), 3, 60), ValueError),
+                     (lambda: fa.rope(q, k, table[:, :40].contiguous(), pos[0]), fa.FAError),
+                     (lambda: fa.rope(q, k, table, pos[0], sections=(8, 8)), ValueError),
+                     (lambda: fa.rope(q, k, table.cpu(), pos[0]), ValueError),
+                     (lambda: fa.attention_window(*w[:3], 0, 1), fa.FAError),
+                     (lambda: fa.attention_window(w[0], w[1][:, :, :9], w[2], 4), ValueError),
+                     (lambda: fa.attention_window_backward(*w[:3], w[3], torch.zeros(2, 4, 149, device="cuda"), w[3], 4), ValueError),
+                     (lambda: fa.attention_window_backward(*w[:3], w[3].half(), torch.zeros(2, 4, 150, device="cuda"), w[3], 4), TypeError),
+                     (lambda: fa.kv_append_fp8(None, fused[:4, 6:7], fused[:4, 7:], *cache, pages, cu, i32(lens), 0), fa.FAError),
+                     (lambda: fa.kv_append_fp8(None, fused[:4, 6:7], fused[:3, 7:], *cache, pages, cu, i32(lens), 3), ValueError)):
+        with pytest.raises(err):
+            bad()
+    ok()
