@@ -681,8 +681,11 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 }
 
 // Splits that finish earliest, in rounds of 128 keys; a CTA's start and end cost
-// about two, leaving and merging partial states some more. One sequence: waves
-// of CTAs of equal length. Several: their lengths differ, so the longest CTA
+// about two, leaving and merging partial states some more. In one wave only the
+// longest CTA counts, and the merge costs two (one token for 8 heads of 64 over 512
+// keys: 11.4 us with one split, 9.3 with three, 8.7 with five; four contexts of up
+// to 700: 12.0 and 8.5 with six). One sequence in several waves: CTAs of equal
+// length. Several sequences: their lengths differ, so the longest CTA
 // comes on top of an even share of all of them, at two thirds of the longest
 // length (measured: 64 contexts of 8192 to 32768, 512 units: 600 us with one
 // split, 511 with three, 480 with eight; one of 131072, 8 units: 52 us in one
@@ -710,13 +713,20 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
     // (Partial sums of 256 rows cost more than they even out: two chunks of 2048
     // tokens over 16384 keys, 341 us with one split, 430 with four.)
     if (many_rows && units >= slots) return 1;
-    const long long most = std::max(1ll, std::min(static_cast<long long>(FA_MAX_SPLITS), rounds / 2));
+    // (A split of less than one round leaves warps idle, of less than two a slot.)
+    const long long most =
+        std::max(1ll, std::min(static_cast<long long>(FA_MAX_SPLITS), dual || many_rows ? rounds / 2 : rounds));
     const double start = many_rows ? 8. : 2.;
     long long best = 1;
     double best_cost = -1.;
     for (long long s = 1; s <= most; ++s) {
         const long long ctas = units * s;
         const double each = static_cast<double>((rounds + s - 1) / s) + start;
+        if (!many_rows && ctas <= slots) {
+            const double cost = each + (s > 1 ? 2. + 0.02 * static_cast<double>(s) : 0.);
+            if (best_cost < 0. || cost < best_cost) best = s, best_cost = cost;
+            continue;
+        }
         const double cost = (B == 1 || many_rows ? static_cast<double>((ctas + slots - 1) / slots) * each
                                                  : (1. + 0.65 * static_cast<double>(ctas) / slots) * each) +
                             (s > 1 ? 4. + 0.1 * static_cast<double>(B == 1 ? s : 4 * s) : 0.);
@@ -762,7 +772,7 @@ int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_
     if (B < 1 || Hkv < 1 || H < Hkv || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || !fa::valid_d(d)) return 0;
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
     const long long units = static_cast<long long>(B) * Hkv * c.row_blocks;
-    const long long rounds = std::max(1ll, c.tiles * c.block_keys / 128);
+    const long long rounds = (c.tiles * c.block_keys + 127) / 128;
     // CTAs at once: one per SM for the tensor-core kernel.
     return fa::best_splits(B, units, rounds, 152 * (c.tc ? 1 : fa::rows_ctas(d)), c.dual, c.tc && !c.dual);
 }
