@@ -4,8 +4,8 @@
 //
 // A call on a few tokens takes the GPU a few microseconds, so the interpreter's
 // share of it counts (one call after the other, us, with ctypes and here: 8
-// rotated tokens 15 and 5.2, 128 appended ones 19 and 4.4, one token decoded in two
-// launches 22 and 9.9). A call that is not plain (a tensor of another type, shape, layout or
+// rotated tokens 15 and 5.2, 128 appended ones 19 and 4.4, one token decoded over
+// 516 keys 20 and 7.4). A call that is not plain (a tensor of another type, shape, layout or
 // device than the operator takes, a subclass, an argument that is not a number)
 // returns None before anything happened: the Python form of the same call then
 // says what is wrong, or handles it. A status other than FA_OK is returned as a

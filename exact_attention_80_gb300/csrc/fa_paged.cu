@@ -1,6 +1,6 @@
-// fa_paged.cu — attention over the paged e4m3 cache: the kernel for few query
-// rows per kv head (single tokens, drafted tokens), the merge of its key
-// splits, and the C entry points.
+// fa_paged.cu — attention over the paged e4m3 cache: the kernel for up to 16 query
+// rows per kv head (single tokens, a few drafted ones), the merge of key splits, and
+// the C entry points.
 //
 // A CTA owns (sequence, kv head, 16 query rows, key split). Its rows are the
 // (query token, head of the group) pairs of the kv head, so a group's heads
@@ -60,6 +60,7 @@ namespace {
 
 constexpr int kRows = 16;      // query rows per CTA
 constexpr int kWarps = 4;
+constexpr int kClusterSplits = 8;  // splits that can be a cluster (the portable size)
 // Keys of a warp's tile, and CTAs an SM holds. A warp's tile is a chain of
 // dependent steps, so throughput comes from the warps beside it: short tiles and
 // two- or three-slot rings, for as many CTAs as the registers allow. Measured on
@@ -85,7 +86,8 @@ struct PagedLayout {
     static constexpr uint32_t Q_OFF = kWarps * RING;
     static constexpr uint32_t BAR_OFF = Q_OFF + Q_BYTES;
     static constexpr uint32_t ML_OFF = BAR_OFF + kWarps * STAGES * 8;  // [warp][m, l][16 rows]
-    static constexpr uint32_t BYTES = ML_OFF + kWarps * 2 * kRows * 4;
+    static constexpr uint32_t CTA_ML_OFF = ML_OFF + kWarps * 2 * kRows * 4;  // [m, l][16 rows] of the CTA
+    static constexpr uint32_t BYTES = CTA_ML_OFF + 2 * kRows * 4;
     static constexpr size_t ALLOC = BYTES + 1024;
     static_assert(RING >= kRows * D * 4, "a warp's O is staged in its ring");
     static_assert(TILE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
@@ -139,7 +141,35 @@ __device__ __forceinline__ int key_of(int j) {
     return D == 64 ? j : (j >> 1) | ((j & 1) << 2);
 }
 
-template <int D>
+// Shared memory of the cluster's CTA `rank` at this CTA's address.
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                 : "r"(addr)
+                 : "memory");
+    return x;
+}
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// CLUSTER: the splits of a unit are a cluster, whose CTAs read one another's
+// states at the end: no workspace traffic and no second launch (one token for 8
+// heads of 64 over 516 keys, five splits: 7.0 us against 7.9 through the workspace,
+// replayed from a graph; 11.3 with one split). Every CTA of a cluster comes to both
+// of its meetings, whatever it found.
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     fa_paged_rows_kernel(const __grid_constant__ PagedParams p) {
     using L = PagedLayout<D>;
@@ -166,13 +196,15 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     // Unit: row blocks fastest (they share K and V in L2), then splits, heads.
-    unsigned lin = blockIdx.x;
+    // (A cluster's CTAs are consecutive: its splits.)
+    unsigned lin = CLUSTER ? blockIdx.x / p.num_splits : blockIdx.x;
     const int rb = static_cast<int>(lin % p.row_blocks);
     lin /= p.row_blocks;
-    const int split = static_cast<int>(lin % p.num_splits);
-    lin /= p.num_splits;
+    const int split = static_cast<int>(CLUSTER ? blockIdx.x % p.num_splits : lin % p.num_splits);
+    if (!CLUSTER) lin /= p.num_splits;
     const int h = static_cast<int>(lin % p.Hkv);
     const int b = static_cast<int>(lin / p.Hkv);
+    // (All CTAs of a cluster agree on the two returns below.)
     NewTokens nt;
     if (!new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt)) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
@@ -186,7 +218,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     const int p1 = start + (min(r0 + kRows, rows) - 1) / p.G;
     const KeyList list = key_list<KEYS>(p.window, p.sinks, p0, p1);
     const int used = max(1, (list.n + p.tiles_per_split - 1) / p.tiles_per_split);
-    if (split >= used) return;
+    if (!CLUSTER && split >= used) return;
     const int i0 = split * p.tiles_per_split;
     const int i1 = min(list.n, i0 + p.tiles_per_split);
     const int mine = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);  // this warp's tiles: i0 + warp + 4 k
@@ -503,10 +535,24 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4*>(stage + (g + 8 * e) * D + 16 * x + 4 * t) =
                 make_float4(o[x][0][2 * e], o[x][1][2 * e], o[x][0][2 * e + 1], o[x][1][2 * e + 1]);
-    if (__syncthreads_or(!ok)) return;
+    const bool failed = __syncthreads_or(!ok);
+    if (!CLUSTER && failed) return;
 
     const float* mls = reinterpret_cast<const float*>(smem + L::ML_OFF);
     constexpr int VEC = D / 4;  // float4 units of a row
+    auto place = [&](int r) -> long long {
+        const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
+        return static_cast<long long>(nt.first + i) * p.H + h * p.G + j;
+    };
+    auto put = [&](int r, int c, const float4& a, float mm, float ll) {
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        *reinterpret_cast<uint2*>(p.o + place(r) * D + 4 * c) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        if (c == 0) {
+            const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
+            p.lse[static_cast<long long>(h * p.G + j) * p.total_q + nt.first + i] = state_lse(mm, ll);
+        }
+    };
     for (int u = threadIdx.x; u < kRows * VEC; u += kWarps * 32) {
         const int r = u / VEC, c = u - r * VEC;
         if (r0 + r >= rows) break;
@@ -523,18 +569,23 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             ll = fmaf(f, mls[w * 2 * kRows + kRows + r], ll);
             a.x = fmaf(f, x.x, a.x), a.y = fmaf(f, x.y, a.y), a.z = fmaf(f, x.z, a.z), a.w = fmaf(f, x.w, a.w);
         }
-        const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
-        const long long row = static_cast<long long>(nt.first + i) * p.H + h * p.G + j;
+        if constexpr (CLUSTER) {
+            // (Over warp 0's state of this unit, which this thread alone reads.)
+            *reinterpret_cast<float4*>(smem + (r * VEC + c) * 16) = a;
+            if (c == 0) {
+                float* own = reinterpret_cast<float*>(smem + L::CTA_ML_OFF);
+                own[r] = state_ref(mm, ll);
+                own[kRows + r] = ll;
+            }
+            continue;
+        }
+        const long long row = place(r);
         // States that the row does not use are marked as empty for the merge.
         if (split == 0 && p.num_splits > 1)
             for (int s = (used == 1 ? 0 : used) + c; s < p.num_splits; s += VEC)
                 p.ws_m[static_cast<long long>(s) * p.total_q * p.H + row] = -INFINITY;
         if (used == 1) {
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            *reinterpret_cast<uint2*>(p.o + row * D + 4 * c) =
-                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-            if (c == 0)
-                p.lse[static_cast<long long>(h * p.G + j) * p.total_q + nt.first + i] = state_lse(mm, ll);
+            put(r, c, a, mm, ll);
         } else {
             const long long at = static_cast<long long>(split) * p.total_q * p.H + row;
             *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
@@ -543,6 +594,41 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
                 p.ws_l[at] = ll;
             }
         }
+    }
+    if constexpr (CLUSTER) {
+        __syncwarp();
+        cluster_meet();
+        // The CTAs take units of the rows in turn; a failed wait leaves them out.
+        for (int u = split * kWarps * 32 + threadIdx.x; u < kRows * VEC && !failed; u += p.num_splits * kWarps * 32) {
+            const int r = u / VEC, c = u - r * VEC;
+            if (r0 + r >= rows) break;
+            float m_of[kClusterSplits], l_of[kClusterSplits];
+            float4 x[kClusterSplits];
+            float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int s = 0; s < kClusterSplits; ++s) {
+                m_of[s] = -INFINITY;
+                if (s < used) {
+                    m_of[s] = ld_cluster(map_rank(sbase + L::CTA_ML_OFF + r * 4, s));
+                    l_of[s] = ld_cluster(map_rank(sbase + L::CTA_ML_OFF + (kRows + r) * 4, s));
+                    x[s] = ld_cluster_v4(map_rank(sbase + (r * VEC + c) * 16, s));
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < kClusterSplits; ++s) mm = fmaxf(mm, m_of[s]);
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < kClusterSplits; ++s) {
+                if (m_of[s] == -INFINITY) continue;  // no key, or no such split
+                const float f = ex2(m_of[s] - mm);
+                ll = fmaf(f, l_of[s], ll);
+                a.x = fmaf(f, x[s].x, a.x), a.y = fmaf(f, x[s].y, a.y);
+                a.z = fmaf(f, x[s].z, a.z), a.w = fmaf(f, x[s].w, a.w);
+            }
+            put(r, c, a, mm, ll);
+        }
+        __syncwarp();
+        cluster_meet();  // no CTA leaves while another reads its states
     }
 }
 
@@ -682,9 +768,9 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 
 // Splits that finish earliest, in rounds of 128 keys; a CTA's start and end cost
 // about two, leaving and merging partial states some more. In one wave only the
-// longest CTA counts, and the merge costs two (one token for 8 heads of 64 over 512
-// keys: 11.4 us with one split, 9.3 with three, 8.7 with five; four contexts of up
-// to 700: 12.0 and 8.5 with six). One sequence in several waves: CTAs of equal
+// longest CTA counts, and the merge costs two rounds, or half a one in a cluster (one
+// token for 8 heads of 64 over 512 keys: 11.3 us with one split, 7.9 with three, 7.0
+// with five; four contexts of up to 700: 11.9 and 6.8 with six). One sequence in several waves: CTAs of equal
 // length. Several sequences: their lengths differ, so the longest CTA
 // comes on top of an even share of all of them, at two thirds of the longest
 // length (measured: 64 contexts of 8192 to 32768, 512 units: 600 us with one
@@ -723,7 +809,8 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
         const long long ctas = units * s;
         const double each = static_cast<double>((rounds + s - 1) / s) + start;
         if (!many_rows && ctas <= slots) {
-            const double cost = each + (s > 1 ? 2. + 0.02 * static_cast<double>(s) : 0.);
+            const double merge = s == 1 ? 0. : !dual && s <= kClusterSplits ? 0.5 : 2. + 0.02 * static_cast<double>(s);
+            const double cost = each + merge;
             if (best_cost < 0. || cost < best_cost) best = s, best_cost = cost;
             continue;
         }
@@ -735,21 +822,27 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
     return static_cast<int>(best);
 }
 
-template <int D>
+template <int D, bool CLUSTER>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
     using L = PagedLayout<D>;
     static ContextCache<int> attr_set;
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         *out = 1;
-        return cudaFuncSetAttribute(fa_paged_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_paged_rows_kernel<D, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
     const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(fa_paged_rows_kernel<D>, dim3(static_cast<unsigned>(ctas)), kWarps * 32, L::ALLOC,
-                            stream, p);
+    return launch_dependent_clusters(fa_paged_rows_kernel<D, CLUSTER>, dim3(static_cast<unsigned>(ctas)),
+                                     CLUSTER ? static_cast<unsigned>(p.num_splits) : 1u, kWarps * 32, L::ALLOC, stream,
+                                     p);
+}
+// The splits of a call as clusters: where all of its CTAs run at once, since a
+// CTA that is done holds its place until the others of its cluster are.
+bool as_clusters(const Plan& c, long long units, int num_splits, int d) {
+    return !c.tc && num_splits > 1 && num_splits <= kClusterSplits && units * num_splits <= 152 * rows_ctas(d);
 }
 
 template <int D>
@@ -851,10 +944,16 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit = fa::kDefaultWaitLimit;
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+    if (fa::as_clusters(c, static_cast<long long>(B) * Hkv * c.row_blocks, num_splits, d)) {
+        const cudaError_t e = d == 64    ? fa::launch_rows<64, true>(p, stream)
+                              : d == 128 ? fa::launch_rows<128, true>(p, stream)
+                                         : fa::launch_rows<256, true>(p, stream);
+        return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    }
     cudaError_t e = c.tc       ? fa::launch_paged_tc(p, d, stream)
-                    : d == 64  ? fa::launch_rows<64>(p, stream)
-                    : d == 128 ? fa::launch_rows<128>(p, stream)
-                               : fa::launch_rows<256>(p, stream);
+                    : d == 64  ? fa::launch_rows<64, false>(p, stream)
+                    : d == 128 ? fa::launch_rows<128, false>(p, stream)
+                               : fa::launch_rows<256, false>(p, stream);
     if (e == cudaSuccess && num_splits > 1)
         e = d == 64 ? fa::launch_merge<64>(p, stream)
                     : d == 128 ? fa::launch_merge<128>(p, stream) : fa::launch_merge<256>(p, stream);

@@ -408,7 +408,7 @@ fa_status fa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_
  * The keys of a row block are split into num_splits parts (FA_MAX_SPLITS at
  * most; fa_paged_num_splits proposes a number), whose partial states meet in
  * the workspace (fa_paged_workspace_bytes; none for one split) and are merged
- * by a second launch. Slots behind a sequence's end may hold anything. Queries
+ * by a second launch, or, where they are few, within the first one. Slots behind a sequence's end may hold anything. Queries
  * past cu_seqlens_q[B] are not written. Broken offsets and lengths: that
  * sequence is neither read nor written, FA_ERR_SEQLENS from fa_device_status;
  * a page that is not one of the cache: FA_ERR_PAGES, the sequence's result is
