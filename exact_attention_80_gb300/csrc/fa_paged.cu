@@ -747,14 +747,14 @@ struct Plan {
 Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     Plan c;
     const long long rows = static_cast<long long>(max_q) * G;
-    // The tensor-core kernel from 17 rows on (d = 256: no room in shared memory). One
-    // block of 16 rows is faster here, two, which read K and V twice, are not (16
-    // sequences over up to 16200 keys, us here and there: 16 rows 87 and 92 at d =
-    // 128, 55 and 82 at d = 64; 20 rows 128 and 106, 94 and 82; four of up to 2000
-    // keys at d = 64, 20 rows: 14 and 17).
-    c.tc = d <= 128 && rows > kRows;
-    c.dual = c.tc && rows <= kTcRows;
-    c.block_rows = !c.tc ? kRows : c.dual ? kTcRows : 2 * kTcRows;
+    // The tensor-core kernel from 17 rows on. One block of 16 rows is faster here,
+    // two, which read K and V twice, are not (16 sequences over up to 16200 keys, us
+    // here and there: 16 rows 87 and 92 at d = 128, 55 and 82 at d = 64; 20 rows 128
+    // and 106, 94 and 82; four of up to 2000 keys at d = 64, 20 rows: 14 and 17; 16
+    // of up to 8000 at d = 256, 40 rows: 75 and 40).
+    c.tc = rows > kRows;
+    c.dual = c.tc && rows <= kTcRows && d <= 128;
+    c.block_rows = !c.tc ? kRows : c.dual || d == 256 ? kTcRows : 2 * kTcRows;
     c.block_keys = c.tc ? kTcKeys : rows_keys(d);
     c.row_blocks = (rows + c.block_rows - 1) / c.block_rows;
     const long long K = c.block_keys;

@@ -27,6 +27,14 @@
 // exponentials (five drafted tokens, 20 rows, 64 contexts of up to 32768 keys: 579
 // us against 709 without shares; one of 131072: 60 against 76).
 //
+// D = 256 (WIDE): O takes half of TMEM, so a CTA owns one tile of 128 rows, and S
+// has two buffers: the tensor core forms S of tile j + 2 behind PV of tile j while
+// the softmax (four warps) is at tile j + 1. Eight warps convert V, whose f16 form
+// has one buffer: a tile is converted while S takes the tensor core (chunks of 1024
+// tokens over 8192 keys, 16 + 2 heads: 190 us, 1300 TFLOP/s; 1283 us with 16 rows
+// per CTA in the other kernel; 40 rows over 16 contexts of up to 8000 keys: 40 us
+// against 75).
+//
 // Roles, by warp: 0 producer (Q is written by the softmax threads; K and V pages
 // by TMA into two rings), 1 issuer, 2-3 idle, 4-11 softmax (thread = row = TMEM
 // lane), 12-15 converters (two warps took 2200 cycles a tile beside the
@@ -47,21 +55,25 @@ template <int D, int SHARES>
 struct TcLayout {
     static constexpr bool DUAL = SHARES > 0;
     static constexpr int BM = 128, BN = kTcKeys;
-    static constexpr int ROW_BYTES = D < 128 ? D : 128;   // swizzled row of codes
+    static constexpr bool WIDE = D == 256;                // one row tile, S in two buffers
+    static constexpr int ROW_BYTES = D < 128 ? D : 128;   // swizzled row of codes (D = 256: in two parts)
+    static constexpr int PARTS = D / ROW_BYTES;
+    static constexpr uint32_t PART = BN * ROW_BYTES;      // bytes of a part of a K or V tile (or of a term of Q)
     // Dual slots share one row tile, which leaves room for deeper rings.
-    static constexpr int KSTAGES = D == 64 ? 6 : DUAL ? 4 : 3;
-    static constexpr int VSTAGES = D == 64 ? 6 : DUAL ? 3 : 2;
+    static constexpr int KSTAGES = WIDE ? 2 : D == 64 ? 6 : DUAL ? 4 : 3;
+    static constexpr int VSTAGES = WIDE ? 1 : D == 64 ? 6 : DUAL ? 3 : 2;
+    static constexpr int VBUFS = WIDE ? 1 : 2;            // V tiles in f16
     static constexpr int THREADS = 512;
-    static constexpr int CONV_WARP0 = 12, CONV_WARPS = 4;
+    static constexpr int CONV_WARP0 = WIDE ? 8 : 12, CONV_WARPS = 16 - CONV_WARP0;
     static constexpr uint32_t Q_TERM = BM * D;            // one e4m3 term of a row tile
     static constexpr uint32_t Q_TILE = 2 * Q_TERM;
     static constexpr uint32_t SLOT = BN * D;              // codes of a K or V tile
     static constexpr uint32_t V16 = BN * D * 2;           // V tile in f16: 64-column chunks of 128-byte rows
     static constexpr uint32_t Q_OFF = 0;
-    static constexpr uint32_t K_OFF = Q_OFF + (DUAL ? 1 : 2) * Q_TILE;
+    static constexpr uint32_t K_OFF = Q_OFF + (DUAL || WIDE ? 1 : 2) * Q_TILE;
     static constexpr uint32_t V_OFF = K_OFF + KSTAGES * SLOT;
     static constexpr uint32_t V16_OFF = V_OFF + VSTAGES * SLOT;
-    static constexpr uint32_t BAR_OFF = V16_OFF + 2 * V16;
+    static constexpr uint32_t BAR_OFF = V16_OFF + VBUFS * V16;
     // DUAL, at the end: fp32 O of both slots' 128 lanes, then m and l.
     static constexpr uint32_t ML_OFF = 2 * BM * D * 4;
     static_assert(!DUAL || ML_OFF + 2 * 2 * BM * 4 <= BAR_OFF, "the states overwrite barriers");
@@ -84,10 +96,12 @@ struct TcLayout {
     __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * BN; }
     __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
     static constexpr int LAUNCH_REGS = 128, CTRL_REGS = 56, SOFTMAX_REGS = 200;
-    static_assert(256 * CTRL_REGS + 256 * SOFTMAX_REGS == THREADS * LAUNCH_REGS, "register split");
+    static_assert((WIDE ? 384 : 256) * CTRL_REGS + (WIDE ? 128 : 256) * SOFTMAX_REGS <= THREADS * LAUNCH_REGS,
+                  "register split");
     static_assert(ALLOC <= 232448, "shared memory over the 227 KB per-CTA limit");
     static_assert(ALLOC > 232448 / 2, "two CTAs per SM would contend for TMEM");
-    static_assert(256 + 2 * D <= 512, "O overflows TMEM");
+    static_assert(256 + (WIDE ? 1 : 2) * D <= 512, "O overflows TMEM");
+    static_assert(!(WIDE && DUAL), "no room");
 };
 
 // kind::f16 with f16 operands (format code 0), fp32 accumulator.
@@ -144,9 +158,9 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
     return __shfl_sync(0xffffffffu, len, at);
 }
 
-template <bool DUAL>
+template <bool DUAL, bool WIDE>
 __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork& w) {
-    constexpr int ROWS = DUAL ? kTcRows : 2 * kTcRows;
+    constexpr int ROWS = DUAL || WIDE ? kTcRows : 2 * kTcRows;
     const int per_unit = p.num_splits;
     unsigned lin = blockIdx.x;
     const int si = static_cast<int>(lin % per_unit);
@@ -191,10 +205,10 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     if (!w.live) return;
     w.split = si;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < (WIDE ? 1 : 2); ++t) {
         // Slot 0 takes the later rows, whose tile ends last: the issuer serves
         // it first.
-        w.row0[t] = r0 + (1 - t) * kTcRows;
+        w.row0[t] = WIDE ? r0 : r0 + (1 - t) * kTcRows;
         w.i0[t] = si * p.tiles_per_split;
         if (w.row0[t] >= w.rows) continue;
         const int last = w.start + (min(w.row0[t] + kTcRows, w.rows) - 1) / p.G;
@@ -238,7 +252,7 @@ __device__ __forceinline__ int tc_page(const PagedParams& p, const TcWork& w, co
 template <int D, int SHARES>
 __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_kernel(const __grid_constant__ PagedParams p) {
     using L = TcLayout<D, SHARES>;
-    constexpr bool DUAL = L::DUAL;
+    constexpr bool DUAL = L::DUAL, WIDE = L::WIDE;
     constexpr int BN = L::BN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
     if (warp < 4 || warp >= L::CONV_WARP0) {
         setmaxnreg_dec<L::CTRL_REGS>();
         TcWork w;
-        tc_work<DUAL>(p, piece, w);
+        tc_work<DUAL, L::WIDE>(p, piece, w);
         if (w.live && warp == 0) {
             // -------------------------------------------------------- producer
             // Entries in the issuer's order: K_0; then per step j: V_j, K_{j+1}.
@@ -321,7 +335,10 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 for (int i = 0; i < per; ++i) {
                     const int id = __shfl_sync(0xffffffffu, ids, first + i);
                     if (id >= 0 && leader)
-                        tma_load_2d(dst + i * page_bytes, map, full, 0, (id * p.Hkv + w.h) << p.log_page);
+#pragma unroll
+                        for (int c = 0; c < L::PARTS; ++c)
+                            tma_load_2d(dst + c * L::PART + ((i * L::ROW_BYTES) << p.log_page), map, full, c * 128,
+                                        (id * p.Hkv + w.h) << p.log_page);
                 }
             };
             int k_issued = 0, v_issued = 0;
@@ -346,6 +363,25 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 ++v_issued;
                 return true;
             };
+            if constexpr (WIDE) {
+                // K runs two tiles ahead of V: pages of its own.
+                int ids[2], ahead[2];  // of K, of V: the batch at hand and the next one
+#pragma unroll
+                for (int s = 0; s < 2; ++s) ids[s] = batch_of(0, 0), ahead[s] = batch_of(0, 1);
+                auto tile = [&](int s, int j) -> bool {
+                    const int first = (j << log_per) & 31;
+                    if (first == 0 && j > 0) {
+                        ids[s] = ahead[s];
+                        ahead[s] = batch_of(0, (j << log_per >> 5) + 1);
+                    }
+                    return s ? load_v(ids[1], first) : load_k(ids[0], first);
+                };
+                for (int j = 0; j < min(2, w.nmax) && ok; ++j) ok = tile(0, j);
+                for (int j = 0; j < w.nmax && ok; ++j) {
+                    ok = tile(1, j);
+                    if (ok && j + 2 < w.nmax) ok = tile(0, j + 2);
+                }
+            } else {
             constexpr int SEQS = DUAL ? 2 : 1;  // sequences of tiles
             int cur[SEQS], next[SEQS];          // the batch of the tile whose V comes next, and the one behind it
 #pragma unroll
@@ -368,6 +404,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     }
                     if (ok && j + 1 < n) ok = load_k(cur[t], first_next);
                 }
+            }
             }
             if (ok) {
                 // No arrival may be in flight when the CTA exits.
@@ -396,14 +433,16 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 return (static_cast<uint64_t>(hi) << 32) | (lo + (off >> 4));
             };
             auto issue_s = [&](int t, int slot) {
-                const uint32_t qa = L::Q_OFF + (DUAL ? 0 : t) * L::Q_TILE, kb = L::K_OFF + slot * L::SLOT;
+                const uint32_t qa = L::Q_OFF + (DUAL || WIDE ? 0 : t) * L::Q_TILE, kb = L::K_OFF + slot * L::SLOT;
 #pragma unroll
                 for (int term = 0; term < 2; ++term)
 #pragma unroll
                     for (int kk = 0; kk < D / 32; ++kk)
                         if (leader)
-                            umma_ss_f8(tmem + L::S_COL(t), desc(kmaj_lo, kmaj_hi, qa + term * L::Q_TERM + kk * 32),
-                                       desc(kmaj_lo, kmaj_hi, kb + kk * 32), IDESC_S, (term | kk) ? 1u : 0u);
+                            umma_ss_f8(tmem + L::S_COL(t),
+                                       desc(kmaj_lo, kmaj_hi, qa + term * L::Q_TERM + (kk >> 2) * L::PART + (kk & 3) * 32),
+                                       desc(kmaj_lo, kmaj_hi, kb + (kk >> 2) * L::PART + (kk & 3) * 32), IDESC_S,
+                                       (term | kk) ? 1u : 0u);
                 if (leader) umma_commit(bar(L::BAR_SFULL + t));
             };
             auto issue_pv = [&](int t, int buf, bool accumulate) {
@@ -411,7 +450,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
                     if (leader)
-                        umma_ts(tmem + L::O_COL(t), tmem + L::S_COL(t) + kk * 8, desc(vmn_lo, vmn_hi, vb + kk * 2048),
+                        umma_ts(tmem + L::O_COL(WIDE ? 0 : t), tmem + L::S_COL(t) + kk * 8, desc(vmn_lo, vmn_hi, vb + kk * 2048),
                                 IDESC_O, (accumulate || kk > 0) ? 1u : 0u);
             };
             int k_used = 0;  // K entries waited for
@@ -422,7 +461,32 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 return r;
             };
             bool ok = true;
-            if constexpr (DUAL) {
+            if constexpr (WIDE) {
+                // S of tile j goes to buffer j & 1, two tiles ahead of its PV: the
+                // tensor core forms S_{j+2} while the softmax is at tile j + 1.
+                auto next_s = [&](int j) -> bool {
+                    const int slot = k_used % L::KSTAGES;
+                    if (!wait_k()) return false;
+                    tc_fence_after();
+                    issue_s(j & 1, slot);
+                    if (leader) umma_commit(bar(L::BAR_KEMPTY + slot));
+                    return true;
+                };
+                ok = tc_wait_warp(bar(L::BAR_QFULL + 0), 0, p, abort_flag, kStatusWaitQ);
+                for (int j = 0; j < min(2, w.nmax) && ok; ++j) ok = next_s(j);
+                for (int j = 0; j < w.nmax && ok; ++j) {
+                    ok = tc_wait_warp(bar(L::BAR_HFULL), j & 1, p, abort_flag, kStatusWaitKvFull);
+                    if (ok) ok = tc_wait_warp(bar(L::BAR_PFULL + (j & 1)), (j >> 1) & 1, p, abort_flag, kStatusWaitP);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(j & 1, 0, j > 0);
+                    if (leader) {
+                        umma_commit(bar(L::BAR_HEMPTY));
+                        umma_commit(bar(L::BAR_OFULL));  // phase j: PV_j is done
+                    }
+                    if (j + 2 < w.nmax) ok = next_s(j + 2);
+                }
+            } else if constexpr (DUAL) {
                 int v_used = 0;  // V entries waited for
                 // S of slot t from the next K entry.
                 auto next_s = [&](int t) -> bool {
@@ -506,20 +570,21 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             // A lane converts one 16-code unit u of every ROW_STEP-th key from row0
             // on: its addresses are a register and constants.
             constexpr int ROW_STEP = D == 64 ? 32 : 16, PIECES = BN / ROW_STEP;
-            const int r8 = lane & 7, cw = warp - L::CONV_WARP0;
+            const int r8 = lane & 7, cw = (warp - L::CONV_WARP0) & 3, part = (warp - L::CONV_WARP0) >> 2;
             const int u = D == 64 ? lane >> 3 : (cw & 1) * 4 + (lane >> 3);
             const int row0 = (D == 64 ? cw : cw >> 1) * 8 + r8;
-            const uint32_t src_lane = sbase + L::V_OFF + row0 * L::ROW_BYTES +
+            const uint32_t src_lane = sbase + L::V_OFF + part * L::PART + row0 * L::ROW_BYTES +
                                       ((D == 64 ? u ^ (r8 >> 1) : u ^ r8) << 4);
-            const uint32_t dst_lane = sbase + L::V16_OFF + (u >> 2) * (BN * 128) + row0 * 128 +
+            const uint32_t dst_lane = sbase + L::V16_OFF + (2 * part + (u >> 2)) * (BN * 128) + row0 * 128 +
                                       (((2 * (u & 3)) ^ r8) << 4);
             const int entries = DUAL ? w.n[0] + w.n[1] : w.nmax;
             const int both = 2 * min(w.n[0], w.n[1]);  // dual: entries that alternate between the slots
             bool ok = true;
             for (int e = 0; e < entries && ok; ++e) {
-                const int s = e % L::VSTAGES, buf = e & 1;
-                if (e >= 2)
-                    ok = tc_wait_warp(bar(L::BAR_HEMPTY + buf), ((e >> 1) - 1) & 1, p, abort_flag, kStatusWaitKvEmpty);
+                const int s = e % L::VSTAGES, buf = e % L::VBUFS;
+                if (e >= L::VBUFS)
+                    ok = tc_wait_warp(bar(L::BAR_HEMPTY + buf), (e / L::VBUFS - 1) & 1, p, abort_flag,
+                                      kStatusWaitKvEmpty);
                 if (ok)
                     ok = tc_wait_warp(bar(L::BAR_VFULL + s), (e / L::VSTAGES) & 1, p, abort_flag, kStatusWaitKvFull);
                 if (!ok) break;
@@ -558,15 +623,16 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 }
             }
             // The issuer's last releases must have arrived before the CTA exits.
-            for (int e = max(0, entries - 2); e < entries && ok; ++e)
-                ok = tc_wait_warp(bar(L::BAR_HEMPTY + (e & 1)), (e >> 1) & 1, p, abort_flag, kStatusWaitKvEmpty);
+            for (int e = max(0, entries - L::VBUFS); e < entries && ok; ++e)
+                ok = tc_wait_warp(bar(L::BAR_HEMPTY + e % L::VBUFS), (e / L::VBUFS) & 1, p, abort_flag,
+                                  kStatusWaitKvEmpty);
         }
     } else {
         // ------------------------------------------------------------ softmax
         setmaxnreg_inc<L::SOFTMAX_REGS>();
         TcWork w;
-        tc_work<DUAL>(p, piece, w);
-        const int t = (warp - 4) >> 2;
+        tc_work<DUAL, L::WIDE>(p, piece, w);
+        const int t = WIDE ? 0 : (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // TMEM lane, row of the Q tile
         // Shares: with at most 32 (64) rows, every 32 (64) lanes hold them again,
@@ -622,7 +688,8 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                         decode_e4m3x4(hi[k], z);
                         lo[k] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
                     }
-                    const uint32_t at = hi_at + (D == 64 ? (u ^ ((r >> 1) & 3)) << 4 : (u ^ (r & 7)) << 4);
+                    const uint32_t at = hi_at + (D == 64 ? (u ^ ((r >> 1) & 3)) << 4
+                                                         : (u >> 3) * L::PART + (((u & 7) ^ (r & 7)) << 4));
                     st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
                     st_shared_v4(at + L::Q_TERM, lo[0], lo[1], lo[2], lo[3]);
                 }
@@ -631,7 +698,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 if (lane == 0) mbar_arrive(bar(L::BAR_QFULL + t));
             }
             const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-            const uint32_t tS = tmem + lane_field + L::S_COL(t);
+            const uint32_t tS0 = tmem + lane_field + L::S_COL(t);
             const uint32_t tO = tmem + lane_field + L::O_COL(t);
             const int* table = p.page_table + static_cast<long long>(w.b) * p.max_pages;
             // Scales of the next tile, 16-key group `lane & 7` per lane, loaded a
@@ -669,7 +736,9 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 }
                 scales_of(id_next, ks_next, vs_next);
                 id_next = entry_of(j + 2);
-                ok = tc_wait_warp(bar(L::BAR_SFULL + t), j & 1, p, abort_flag, kStatusWaitS);
+                const int buf = WIDE ? j & 1 : t;  // S of this tile
+                const uint32_t tS = WIDE ? tS0 + buf * BN : tS0;
+                ok = tc_wait_warp(bar(L::BAR_SFULL + buf), (WIDE ? j >> 1 : j) & 1, p, abort_flag, kStatusWaitS);
                 if (!ok) break;
                 tc_fence_after();
                 const int key0 = w.list.tile(i0 + j) * BN;
@@ -840,6 +909,11 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     }
                 }
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    if constexpr (WIDE) {  // (elsewhere S_j comes behind PV_{j-1})
+                        ok = tc_wait_warp(bar(L::BAR_OFULL), (j - 1) & 1, p, abort_flag, kStatusWaitO);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
                     const uint64_t ax2 = f2pack(alpha, alpha);
 #pragma unroll 1
                     for (int cc = 0; cc < D / 32; ++cc) {
@@ -859,12 +933,15 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::BAR_PFULL + t));
+                if (lane == 0) mbar_arrive(bar(L::BAR_PFULL + buf));
                 l = fmaf(l, alpha, sum);
                 m = m_new;
             }
             if (ok && n > 0) {
-                ok = tc_wait_warp(bar(L::BAR_OFULL + t), 0, p, abort_flag, kStatusWaitO);
+                // (Wide: a phase per tile. S of the last one told that the last but two is
+                // done, no more, so the last but one is waited for first.)
+                if (WIDE && n > 1) ok = tc_wait_warp(bar(L::BAR_OFULL), n & 1, p, abort_flag, kStatusWaitO);
+                if (ok) ok = tc_wait_warp(bar(L::BAR_OFULL + t), WIDE ? (n - 1) & 1 : 0, p, abort_flag, kStatusWaitO);
                 if (ok) tc_fence_after();
             }
             if constexpr (DUAL) {
@@ -1025,6 +1102,7 @@ cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream) {
                : p.shares == 2 ? launch_tc<D, 2>(p, stream)
                                : launch_tc<D, 4>(p, stream);
     };
+    if (d == 256) return launch_tc<256, 0>(p, stream);
     return d == 64 ? launch(Index<64>{}) : launch(Index<128>{});
 }
 

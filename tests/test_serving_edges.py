@@ -326,3 +326,32 @@ def test_compiled_calls_equal_the_python_ones():
         with pytest.raises(err):
             bad()
     ok()
+
+
+@pytest.mark.parametrize("case", [
+    # new tokens, cache lengths, page, H, Hkv, window, sinks, splits
+    ([17], [17], 16, 1, 1, 0, 0, None),
+    ([20, 3], [129, 128], 128, 4, 4, 0, 0, None),
+    ([40, 0, 65], [300, 9, 700], 32, 8, 2, 0, 0, 3),
+    ([129], [1500], 64, 2, 1, 0, 0, 1),
+    ([300, 130], [900, 2100], 16, 4, 2, 200, 3, 2),
+    ([5, 8], [1300, 600], 64, 16, 2, 129, 64, None),
+    ([70], [4000], 16, 4, 2, 1, 0, 4),
+])
+def test_wide_heads_many_rows(case):
+    """d = 256 with more than 16 rows a kv head: one row tile, S in two buffers."""
+    ns, lens, page, H, Hkv, window, sinks, splits = case
+    d = 256
+    cache, table = cache_of(lens, page, Hkv, d, 21)
+    g = torch.Generator().manual_seed(4)
+    grow = torch.exp2(torch.randint(-3, 4, (sum(ns), 1, 1), generator=g).float()).cuda()
+    q = (normal((sum(ns), H, d), 8).float() * grow).to(torch.bfloat16)  # some rows' maxima move often
+    cu = i32([0] + list(np.cumsum(ns)))
+    o, lse = fa.attention_paged_fp8(q, *cache, table, cu, i32(lens), max(ns), max(lens), window=window, sinks=sinks,
+                                    num_splits=splits)
+    ok()
+    # Rows up to eight times as large: elements of Q far below the row's largest (24 or so) are off by 2^-18 of
+    # it, scores by about sqrt(256) 2^-18 24 scale = 1e-4, weights by as much beside P's 2^-11.
+    ref, ref_lse, a = paged_oracle(q, cache, table, ns, lens, window, sinks)
+    assert np.all(np.abs(f64(o) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * a)
+    assert np.all(np.abs(f64(lse) - ref_lse) <= 2e-3)
