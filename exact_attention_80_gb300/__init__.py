@@ -94,6 +94,10 @@ def load_library() -> ctypes.CDLL:
     lib.fa_fwd_paged_fp8.restype = i
     lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
     lib.fa_fwd_window.restype = i
+    lib.fa_fwd_window_splitkv.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, i, vp]
+    lib.fa_fwd_window_splitkv.restype = i
+    lib.fa_window_num_splits.argtypes = [i, i, i, i, i, i, i, i]
+    lib.fa_window_num_splits.restype = i
     lib.fa_bwd_window_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
     lib.fa_bwd_window_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
@@ -123,7 +127,8 @@ def _load_calls(lib):
 
     calls.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fa_rope, lib.fa_kv_append_fp8, lib.fa_fwd_paged_fp8, lib.fa_paged_num_splits,
-        lib.fa_paged_workspace_bytes, lib.fa_fwd_window, lib.fa_bwd_window, lib.fa_bwd_window_workspace_bytes)))
+        lib.fa_paged_workspace_bytes, lib.fa_fwd_window, lib.fa_bwd_window, lib.fa_bwd_window_workspace_bytes,
+        lib.fa_window_num_splits, lib.fa_fwd_window_splitkv, lib.fa_combine)))
     _compiled = calls
 
 
@@ -897,10 +902,29 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     _check(st, "fa_fwd_window")
 
 
-def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, stream=None):
-    """Allocate ``o`` and ``lse`` and run :func:`fa_fwd_window`. Returns ``(o, lse)``."""
+def fa_window_num_splits(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
+    """The key splits the library proposes for a windowed forward (0 for arguments out of range)."""
+    return load_library().fa_window_num_splits(B, H, Hkv, Nq, Nk, d, window, sinks)
+
+
+def fa_fwd_window_splitkv(q, k, v, workspace, num_splits: int, window: int, sinks: int = 0,
+                          scale: float | None = None, stream=None):
+    """The windowed forward with split keys: partial states into ``workspace`` (fp32, at least
+    ``fa_splitkv_workspace_bytes`` bytes), merged by :func:`fa_combine`."""
+    B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
+    _need_workspace(workspace, fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits), "workspace", q.device)
+    st = _on_stream(index, stream, load_library().fa_fwd_window_splitkv, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale, window,
+                    sinks, num_splits)
+    _check(st, "fa_fwd_window_splitkv")
+
+
+def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, num_splits: int | None = None,
+                     stream=None):
+    """Allocate ``o`` and ``lse`` and run :func:`fa_fwd_window`, or :func:`fa_fwd_window_splitkv` and the
+    merge (``num_splits`` None: as the library proposes). Returns ``(o, lse)``."""
     if stream is None and _compiled is not None:
-        out = _compiled.window(q, k, v, window, sinks, scale)
+        out = _compiled.window(q, k, v, window, sinks, scale, num_splits)
         if out is not None:
             if type(out) is int:
                 raise FAError(out, "fa_fwd_window")
@@ -909,8 +933,22 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
 
     o = torch.empty_like(q)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
-    _used_on(stream, o, lse)
+    B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
+    if num_splits is None:
+        num_splits = fa_window_num_splits(B, H, Hkv, Nq, Nk, d, window, sinks) or 1
+    if num_splits == 1:
+        fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
+        _used_on(stream, o, lse)
+        return o, lse
+    nbytes = fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits)
+    if nbytes == 0:
+        raise FAError(5, "fa_fwd_window_splitkv")
+    ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
+    fa_fwd_window_splitkv(q, k, v, ws, num_splits, window, sinks, scale, stream)
+    st = _on_stream(index, stream, load_library().fa_combine, ws.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Nq, d,
+                    num_splits)
+    _check(st, "fa_combine")
+    _used_on(stream, o, lse, ws)
     return o, lse
 
 

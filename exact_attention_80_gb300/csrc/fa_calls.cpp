@@ -38,6 +38,9 @@ struct {
     decltype(&::fa_fwd_window) window;
     decltype(&::fa_bwd_window) window_backward;
     decltype(&::fa_bwd_window_workspace_bytes) window_workspace;
+    decltype(&::fa_window_num_splits) window_splits;
+    decltype(&::fa_fwd_window_splitkv) window_splitkv;
+    decltype(&::fa_combine) combine;
 } lib;
 
 bool tensor(PyObject* o, const at::Tensor** t) {
@@ -323,20 +326,34 @@ PyObject* call_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// window(q, k, v, window, sinks, scale or None) -> (o, lse)
+// window(q, k, v, window, sinks, scale or None, num_splits or None) -> (o, lse)
 PyObject* call_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     const at::Tensor *q, *k, *v;
-    int window, sinks;
-    NOT_PLAIN_UNLESS(n == 6 && tensor(a[0], &q) && tensor(a[1], &k) && tensor(a[2], &v) && number(a[3], &window) &&
-                     number(a[4], &sinks));
+    int window, sinks, splits = 0;
+    NOT_PLAIN_UNLESS(n == 7 && tensor(a[0], &q) && tensor(a[1], &k) && tensor(a[2], &v) && number(a[3], &window) &&
+                     number(a[4], &sinks) && (a[6] == Py_None || (number(a[6], &splits) && splits >= 1 &&
+                                                                 splits <= FA_MAX_SPLITS)));
     const int index = current_index(*q);
     Dense c;
     float scale;
     NOT_PLAIN_UNLESS(index >= 0 && dense(*q, *k, *v, index, &c) && scale_of(a[5], c.d, &scale));
     at::Tensor out[2] = {at::empty(q->sizes(), q->options()),
                          at::empty({c.B, c.H, c.Nq}, q->options().dtype(at::kFloat))};
+    if (a[6] == Py_None) splits = lib.window_splits(c.B, c.H, c.Hkv, c.Nq, c.Nk, c.d, window, sinks);
+    at::Tensor workspace;
+    if (splits > 1)
+        workspace = at::empty({static_cast<int64_t>(splits) * c.B * c.H * c.Nq * (c.d + 2)},
+                              q->options().dtype(at::kFloat));
     const fa_status s = launch(index, [&](cudaStream_t stream) {
+        if (splits > 1) {
+            const fa_status first = lib.window_splitkv(q->data_ptr(), k->data_ptr(), v->data_ptr(),
+                                                       workspace.data_ptr(), c.B, c.H, c.Hkv, c.Nq, c.Nk, c.d, scale,
+                                                       window, sinks, splits, stream);
+            if (first != FA_OK) return first;
+            return lib.combine(workspace.data_ptr(), out[0].data_ptr(), static_cast<float*>(out[1].data_ptr()), c.B,
+                               c.H, c.Nq, c.d, splits, stream);
+        }
         return lib.window(q->data_ptr(), k->data_ptr(), v->data_ptr(), out[0].data_ptr(),
                           static_cast<float*>(out[1].data_ptr()), c.B, c.H, c.Hkv, c.Nq, c.Nk, c.d, scale, window,
                           sinks, stream);
@@ -375,8 +392,10 @@ PyObject* call_window_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // init: addresses of the library's entry points, in the order of `lib`.
 PyObject* call_init(PyObject*, PyObject* args) {
-    unsigned long long f[8];
-    if (!PyArg_ParseTuple(args, "KKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7])) return nullptr;
+    unsigned long long f[11];
+    if (!PyArg_ParseTuple(args, "KKKKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
+                          &f[10]))
+        return nullptr;
     lib.rope = reinterpret_cast<decltype(lib.rope)>(static_cast<uintptr_t>(f[0]));
     lib.append = reinterpret_cast<decltype(lib.append)>(static_cast<uintptr_t>(f[1]));
     lib.paged = reinterpret_cast<decltype(lib.paged)>(static_cast<uintptr_t>(f[2]));
@@ -385,6 +404,9 @@ PyObject* call_init(PyObject*, PyObject* args) {
     lib.window = reinterpret_cast<decltype(lib.window)>(static_cast<uintptr_t>(f[5]));
     lib.window_backward = reinterpret_cast<decltype(lib.window_backward)>(static_cast<uintptr_t>(f[6]));
     lib.window_workspace = reinterpret_cast<decltype(lib.window_workspace)>(static_cast<uintptr_t>(f[7]));
+    lib.window_splits = reinterpret_cast<decltype(lib.window_splits)>(static_cast<uintptr_t>(f[8]));
+    lib.window_splitkv = reinterpret_cast<decltype(lib.window_splitkv)>(static_cast<uintptr_t>(f[9]));
+    lib.combine = reinterpret_cast<decltype(lib.combine)>(static_cast<uintptr_t>(f[10]));
     Py_RETURN_NONE;
 }
 

@@ -19,8 +19,9 @@ namespace fa {
 constexpr int kSmallSinks = 32;
 
 struct WinList {
-    int ns, lo, n;  // tiles 0 .. ns - 1, then tile lo on; n in all
-    __device__ __forceinline__ int tile(int j) const { return j < ns ? j : lo + (j - ns); }
+    int ns, lo, n;  // tiles at .. at + ns - 1, then tile lo on; n in all
+    int at;         // 0, or where a key split begins within the sinks
+    __device__ __forceinline__ int tile(int j) const { return j < ns ? at + j : lo + (j - ns); }
 };
 
 // The list of rows at positions p0 .. p1 (p0 may be negative: rows with no key).
@@ -29,6 +30,7 @@ __device__ __forceinline__ WinList win_list(const FwdParams& p, int p0, int p1) 
     WinList w;
     w.ns = 0;
     w.lo = 0;
+    w.at = 0;
     const int end = p1 < 0 ? 0 : p1 / BN + 1;
     if (p.window > 0) {
         const int first = max(0, p0 - p.window + 1) / BN;
@@ -55,14 +57,16 @@ struct WorkWin : Work<QT> {
 
 template <int QT, int BN>
 __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long lin, WorkWin<QT>& w) {
-    // As compute_work (one split, dense): head groups, units heaviest first.
+    // As compute_work (dense): head groups, units heaviest first, splits of a unit
+    // beside one another.
+    w.split = static_cast<int>(lin % p.num_splits);
+    lin /= p.num_splits;
     const long long per_group = static_cast<long long>(p.head_group) * p.n_units;
     const int group = static_cast<int>(lin / per_group);
     const int r = static_cast<int>(lin % per_group);
     const int heads_here = min(p.head_group, p.BH - group * p.head_group);
     const int unit = p.n_units - 1 - r / heads_here;
     w.bh = group * p.head_group + r % heads_here;
-    w.split = 0;
     w.zq = w.bh;
     const int b = w.bh / p.H;
     w.zk = b * p.Hkv + (w.bh - b * p.H) / p.group;
@@ -94,6 +98,27 @@ __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long l
         // window may be sinks.
         w.hole[t] = w.list.ns > 0 || (w.list.lo > 0) ? max(0, min(first, end) - w.list.lo) : 0;
         w.steps[t] = w.n[t] - w.hole[t];
+    }
+    if (p.num_splits > 1) {
+        // This split's part of the list, entries i0 .. i1 - 1: again a run of sink
+        // tiles and one of window tiles, with what is left of the holes between.
+        const WinList all = w.list;
+        const int each = (all.n + p.num_splits - 1) / p.num_splits;
+        const int i0 = min(w.split * each, all.n), i1 = min(i0 + each, all.n);
+        w.list.n = w.nmax = i1 - i0;
+        w.list.ns = max(0, min(all.ns, i1) - i0);
+        w.list.at = i0;
+        w.list.lo = all.lo + max(0, i0 - all.ns);
+        w.small = w.small && i0 == 0 && i1 > 0;
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+            const int hole0 = max(all.ns, i0), hole1 = min(all.ns + w.hole[t], i1);
+            w.n[t] = max(0, min(w.n[t], i1) - i0);
+            w.hole[t] = max(0, hole1 - hole0);
+            // A hole up to the split's end: the tile ends before it.
+            if (w.n[t] == w.list.ns + w.hole[t]) w.n[t] = w.list.ns, w.hole[t] = 0;
+            w.steps[t] = w.n[t] - w.hole[t];
+        }
     }
 }
 

@@ -291,6 +291,18 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
                         int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream);
 
 /*
+ * fa_fwd_window_splitkv — the same with the keys of every row block split into
+ * num_splits parts, for few rows over many keys: partial states into a workspace
+ * of fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits) bytes, which fa_combine
+ * merges into O and LSE. fa_window_num_splits proposes a number (1: fa_fwd_window
+ * alone; 0 for arguments out of range).
+ */
+int fa_window_num_splits(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks);
+fa_status fa_fwd_window_splitkv(const void* q, const void* k, const void* v, void* workspace, int B, int H, int Hkv,
+                                int Nq, int Nk, int d, float scale, int window, int sinks, int num_splits,
+                                cudaStream_t stream);
+
+/*
  * fa_bwd_window — its backward: dq [B][H][Nq][d], dk, dv [B][Hkv][Nk][d] bf16
  * from q, k, v, the forward's o and lse, and dout; the gradients of a kv head
  * are summed over the query heads of its group in fp32. As fa_bwd otherwise

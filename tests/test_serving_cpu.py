@@ -118,6 +118,14 @@ def test_window_refuses(lib, kw, code):
     assert _window(lib, **kw) == code
 
 
+@pytest.mark.parametrize("kw,code", [(k, c) for k, c in BAD_WINDOW if not {"o", "lse"} & set(k)] + [
+    (dict(splits=0), 5), (dict(splits=257), 5), (dict(ws=0), 6), (dict(ws=FAKE + 8), 6)])
+def test_window_splitkv_refuses(lib, kw, code):
+    a = dict(q=FAKE, k=FAKE, v=FAKE, ws=FAKE, B=1, H=4, Hkv=2, Nq=8, Nk=8, d=64, scale=0.125, window=4, sinks=1, splits=2)
+    a.update(kw)
+    assert lib.fa_fwd_window_splitkv(*a.values(), 0) == code
+
+
 @pytest.mark.parametrize("kw,code", BAD_WINDOW + [(dict(ws=0), 6), (dict(ws=FAKE + 4), 6), (dict(dk=0), 1),
                                                  (dict(dout=FAKE + 8), 2)])
 def test_window_backward_refuses(lib, kw, code):
@@ -145,6 +153,8 @@ def test_sizes(lib):
     assert fa.fa_bwd_window_workspace_bytes(2, 4, 2, 300, 300, 128, 0, 0) >= base > 0
     assert fa.fa_bwd_window_workspace_bytes(2, 4, 3, 300, 300, 128, 0, 0) == 0
     assert fa.fa_bwd_window_workspace_bytes(2, 4, 2, 300, 300, 96, 0, 0) == 0
+    assert fa.fa_window_num_splits(1, 8, 2, 1, 4096, 64, 0) > 1 == fa.fa_window_num_splits(8, 32, 8, 4096, 4096, 64, 0)
+    assert fa.fa_window_num_splits(1, 5, 2, 1, 4096, 64, 0) == 0 == fa.fa_window_num_splits(1, 4, 2, 1, 4096, 64, 0, 3)
     # The library's own structs are as long as the ones the binding packs.
     assert fa._ROTATION.size == 48 and fa._ROPE_TENSOR.size == 72 and fa._PAGED_CACHE.size == 48
 

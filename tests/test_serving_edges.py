@@ -355,3 +355,30 @@ def test_wide_heads_many_rows(case):
     ref, ref_lse, a = paged_oracle(q, cache, table, ns, lens, window, sinks)
     assert np.all(np.abs(f64(o) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -9 * a)
     assert np.all(np.abs(f64(lse) - ref_lse) <= 2e-3)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("case", [
+    # B, H, Hkv, N, M, window, sinks, splits
+    (1, 2, 1, 1, 4096, 0, 0, 16), (1, 2, 1, 1, 200, 0, 0, 7), (2, 4, 2, 300, 900, 0, 0, 3),
+    (1, 2, 2, 257, 2000, 700, 300, 5),   # sinks of three tiles, cut within them, and a gap
+    (1, 2, 1, 512, 3000, 130, 4, 2),     # a first step of the sinks alone, and a hole behind it
+    (1, 2, 1, 512, 3000, 1, 0, 4), (1, 1, 1, 400, 100, 0, 0, 2),  # rows that see no key
+    (1, 2, 1, 200, 1500, 400, 129, 64),  # more splits than tiles
+    (1, 3, 1, 129, 129, 60, 10, None), (1, 8, 2, 5, 3000, 0, 0, None),
+])
+def test_window_with_split_keys(case, d):
+    """Split keys give the result of the whole: P rounded to bf16 (2^-8 of a weight) and O (2^-8)."""
+    B, H, Hkv, N, M, window, sinks, splits = case
+    q, k, v = normal((B, H, N, d), 1), normal((B, Hkv, M, d), 2), normal((B, Hkv, M, d), 3)
+    o, lse = fa.attention_window(q, k, v, window, sinks, num_splits=splits)
+    o2, lse2 = fa.attention_window(q, k, v, window, sinks, num_splits=splits, stream=torch.cuda.current_stream())
+    ok()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    scale = fa.default_scale(d)
+    ref, rl = orc.window_forward(f64(q), f64(k), f64(v), scale, window, sinks)
+    a = orc.window_forward(f64(q), f64(k), np.abs(f64(v)), scale, window, sinks)[0]
+    assert np.all(np.abs(f64(o) - ref) <= 2.0 ** -8 * np.abs(ref) + 1.1 * 2.0 ** -8 * a)
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(f64(lse)), empty) and np.all(f64(o)[empty] == 0)
+    assert np.all(np.abs(f64(lse)[~empty] - rl[~empty]) <= 1e-3)
