@@ -965,7 +965,7 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         }
         std::conditional_t<DUAL, WorkDual, std::conditional_t<WIN, WorkWin<QT>, Work<QT>>> w;
         if constexpr (DUAL) compute_work_dual<BN>(p, lin, w);
-        else if constexpr (WIN) compute_work_win<QT, BN>(p, lin, w);
+        else if constexpr (WIN) compute_work_win<QT, BN, !PERSIST>(p, lin, w);
         else compute_work<QT, BN>(p, lin, w);
         const int q_row = (M64 && lane >= 16) ? (1 << 30) : (DUAL ? w.q0 : tile_row0(p, w.q0, t)) + r;
         // This tile's key split: the CTA's, or its own in a dual-range CTA.

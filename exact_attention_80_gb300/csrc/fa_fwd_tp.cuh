@@ -167,7 +167,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     std::conditional_t<WIN, WorkWin<QT>, Work<QT>> w;
-    if constexpr (WIN) compute_work_win<QT, BN>(p, blockIdx.x, w);
+    if constexpr (WIN) compute_work_win<QT, BN, true>(p, blockIdx.x, w);
     else compute_work<QT, BN>(p, blockIdx.x, w);
 
     if (threadIdx.x == 0) {

@@ -55,12 +55,17 @@ struct WorkWin : Work<QT> {
     bool small;
 };
 
-template <int QT, int BN>
+// SPLIT: key splits (launches of persistent CTAs have none, and no registers to
+// spare for them: 203 against 212 us at d = 64).
+template <int QT, int BN, bool SPLIT>
 __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long lin, WorkWin<QT>& w) {
     // As compute_work (dense): head groups, units heaviest first, splits of a unit
     // beside one another.
-    w.split = static_cast<int>(lin % p.num_splits);
-    lin /= p.num_splits;
+    w.split = 0;
+    if constexpr (SPLIT) {
+        w.split = static_cast<int>(lin % p.num_splits);
+        lin /= p.num_splits;
+    }
     const long long per_group = static_cast<long long>(p.head_group) * p.n_units;
     const int group = static_cast<int>(lin / per_group);
     const int r = static_cast<int>(lin % per_group);
@@ -99,7 +104,7 @@ __device__ __forceinline__ void compute_work_win(const FwdParams& p, long long l
         w.hole[t] = w.list.ns > 0 || (w.list.lo > 0) ? max(0, min(first, end) - w.list.lo) : 0;
         w.steps[t] = w.n[t] - w.hole[t];
     }
-    if (p.num_splits > 1) {
+    if (SPLIT && p.num_splits > 1) {
         // This split's part of the list, entries i0 .. i1 - 1: again a run of sink
         // tiles and one of window tiles, with what is left of the holes between.
         const WinList all = w.list;
@@ -202,7 +207,7 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             const long long lin = win_unit<PERSIST>(p, k);
             if (lin < 0) continue;
             WorkWin<QT> w;
-            compute_work_win<QT, BN>(p, lin, w);
+            compute_work_win<QT, BN, !PERSIST>(p, lin, w);
             if (w.nmax == 0) continue;
             if (!PERSIST) ok = load_q(w, 0);
             // Entry e: K_0; then per step j: V_j, K_{j+1}.
@@ -291,7 +296,7 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             const long long lin = win_unit<PERSIST>(p, k);
             if (lin < 0) continue;
             WorkWin<QT> w;
-            compute_work_win<QT, BN>(p, lin, w);
+            compute_work_win<QT, BN, !PERSIST>(p, lin, w);
             if (w.nmax == 0) continue;
             auto active = [&](int t, int j) {
                 return j < w.n[t] && !(j >= w.list.ns && j < w.list.ns + w.hole[t]);

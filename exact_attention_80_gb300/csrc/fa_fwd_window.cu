@@ -106,15 +106,16 @@ fa_status window_forward(const void* q, const void* k, const void* v, void* o, f
     p.o_scale = 1.f;
     p.wait_limit = kDefaultWaitLimit;
     if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-    // Persistent CTAs where the units fill at least four waves and list few key
-    // tiles, as for the dense forward: the start and end of a unit overlap its
-    // neighbours' (2 x 32 heads of 8192, window 1024, d = 64: 216 against 225 us;
-    // window 128: 83 against 107; with 3.4 waves 79 against 76).
+    // Persistent CTAs where the units fill at least four waves (three if they list
+    // four key tiles at most) and list few key tiles, as for the dense forward: the
+    // start and end of a unit overlap its neighbours' (2 x 32 heads of 8192, d = 64,
+    // us, persistent and not: window 1024 and 4 sinks 204 and 214, window 128 74 and
+    // 103; 16 heads, d = 128, 3.4 waves: 76 and 74, window 128 28 and 34).
     const long long listed =
         window > 0 ? std::min<long long>((Nk + 127) / 128, (window + 126) / 128 + 2 + (sinks + 127) / 128)
                    : (Nk + 127) / 128;
     p.total_units = ctas;
-    if (!workspace && d <= 128 && ctas >= 4ll * sms && listed <= 16) {
+    if (!workspace && d <= 128 && ctas >= (listed <= 4 ? 3ll : 4ll) * sms && listed <= 16) {
         const unsigned all = static_cast<unsigned>(sms);
         const cudaError_t e = d == 64 ? launch_fwd_win_d64_persist(p, all, stream)
                                       : launch_fwd_win_d128_persist(p, all, stream);
