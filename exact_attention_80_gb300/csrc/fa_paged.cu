@@ -256,23 +256,25 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             id[e] = __shfl_sync(0xffffffffu, ids[e], k & 31);
             there += id[e] >= 0 ? 1 : 0;
         }
-        if (lane == 0) {
-            const int s = k % L::STAGES;
-            const uint32_t dst = ring + s * L::SLOT, bar = bar0 + 8 * s;
-            const int rows_each = min(page_size, KEYS);
+        const int s = k % L::STAGES;
+        const uint32_t dst = ring + s * L::SLOT, bar = bar0 + 8 * s;
+        const int rows_each = min(page_size, KEYS);
+        if (lane == 0) mbar_arrive_expect_tx(bar, there * rows_each * D * 2);
+        __syncwarp();
+        // A lane per page and tensor.
+        const int e = lane >> 1;
+        int page = id[0];
+#pragma unroll
+        for (int i = 1; i < GROUPS; ++i)
+            if (e == i) page = id[i];
+        if (e < GROUPS && page >= 0) {
             const int key0 = list.tile(i0 + warp + kWarps * k) * KEYS;
-            mbar_arrive_expect_tx(bar, there * rows_each * D * 2);
+            const int row = ((page * p.Hkv + h) << p.log_page) + (per == 1 ? key0 & (page_size - 1) : 0);
+            const CUtensorMap* map = (lane & 1) ? &p.tm_v : &p.tm_k;
 #pragma unroll
-            for (int e = 0; e < GROUPS; ++e) {
-                if (id[e] < 0) continue;
-                const int row = ((id[e] * p.Hkv + h) << p.log_page) + (per == 1 ? key0 & (page_size - 1) : 0);
-#pragma unroll
-                for (int c = 0; c < L::PARTS; ++c) {
-                    const uint32_t at = dst + c * (KEYS * 128) + e * rows_each * L::ROW_BYTES;
-                    tma_load_2d(at, &p.tm_k, bar, c * 128, row);
-                    tma_load_2d(at + L::TILE, &p.tm_v, bar, c * 128, row);
-                }
-            }
+            for (int c = 0; c < L::PARTS; ++c)
+                tma_load_2d(dst + (lane & 1) * L::TILE + c * (KEYS * 128) + e * rows_each * L::ROW_BYTES, map, bar, c * 128,
+                            row);
         }
         __syncwarp();
     };
@@ -747,11 +749,10 @@ struct Plan {
 Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     Plan c;
     const long long rows = static_cast<long long>(max_q) * G;
-    // The tensor-core kernel from 17 rows on. One block of 16 rows is faster here,
-    // two, which read K and V twice, are not (16 sequences over up to 16200 keys, us
-    // here and there: 16 rows 87 and 92 at d = 128, 55 and 82 at d = 64; 20 rows 128
-    // and 106, 94 and 82; four of up to 2000 keys at d = 64, 20 rows: 14 and 17; 16
-    // of up to 8000 at d = 256, 40 rows: 75 and 40).
+    // The tensor-core kernel from 17 rows on. One block of 16 rows is no slower here,
+    // two, which read K and V twice, are (16 sequences over up to 16200 keys, us here
+    // and there: 16 rows 87 and 84 at d = 128, 55 and 62 at d = 64; 20 rows 128 and
+    // 87, 94 and 64; 16 of up to 8000 at d = 256, 40 rows: 75 and 40).
     c.tc = rows > kRows;
     c.dual = c.tc && rows <= kTcRows && d <= 128;
     c.block_rows = !c.tc ? kRows : c.dual || d == 256 ? kTcRows : 2 * kTcRows;
@@ -767,8 +768,8 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 }
 
 // Splits that finish earliest, in rounds of 128 keys; a CTA's start and end cost
-// about two, leaving and merging partial states some more. In one wave only the
-// longest CTA counts, and the merge costs two rounds, or half a one in a cluster (one
+// about two, leaving and merging partial states some more. While the CTAs leave half
+// of the places free, only the longest one counts, and the merge costs two rounds, or half a one in a cluster (one
 // token for 8 heads of 64 over 512 keys: 11.3 us with one split, 7.9 with three, 7.0
 // with five; four contexts of up to 700: 11.9 and 6.8 with six). One sequence in several waves: CTAs of equal
 // length. Several sequences: their lengths differ, so the longest CTA
@@ -782,8 +783,8 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 // here: an even share of all of them, ten rounds a piece for its start and end,
 // and half a piece for the last ones, with sequences at two thirds of the longest
 // on average (five drafted tokens, pieces of the longest and us: 16 contexts of up
-// to 16200 keys, 1: 137, 2: 129, 3: 106, 4: 109; 64 of 32768, 1: 605, 2: 579, 3: 609;
-// 80 of 8192, 1: 219, 2: 245; 2 of 16200, 8: 24.8, 10: 24.5, 12: 28.7).
+// to 16200 keys, 1: 103, 2: 104, 3: 86, 4: 89; 64 of 32768, 1: 543, 2: 528, 3: 547; 80 of
+// 8192, 1: 193, 2: 228; 2 of 16200, 8: 24.3, 10: 24.2, 12: 27.0).
 int best_splits(int B, long long units, long long rounds, int slots, bool dual, bool many_rows) {
     if (dual && B > 1) {
         int best = 1;
@@ -808,7 +809,7 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
     for (long long s = 1; s <= most; ++s) {
         const long long ctas = units * s;
         const double each = static_cast<double>((rounds + s - 1) / s) + start;
-        if (!many_rows && ctas <= slots) {
+        if (!many_rows && 2 * ctas <= slots) {
             const double merge = s == 1 ? 0. : !dual && s <= kClusterSplits ? 0.5 : 2. + 0.02 * static_cast<double>(s);
             const double cost = each + merge;
             if (best_cost < 0. || cost < best_cost) best = s, best_cost = cost;

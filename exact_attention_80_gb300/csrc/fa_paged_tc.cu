@@ -24,8 +24,8 @@
 // (64) rows a slot's 128 lanes hold them four times (twice), and each copy's
 // warps take their share of a tile's columns with weights of zero for the others:
 // the MMAs cost the same, and four warps rather than one form a tile's
-// exponentials (five drafted tokens, 20 rows, 64 contexts of up to 32768 keys: 579
-// us against 709 without shares; one of 131072: 60 against 76).
+// exponentials (five drafted tokens, 20 rows, for 64 contexts of up to 32768 keys:
+// 528 us, a fifth less than without shares; for one of 131072: 57).
 //
 // D = 256 (WIDE): O takes half of TMEM, so a CTA owns one tile of 128 rows, and S
 // has two buffers: the tensor core forms S of tile j + 2 behind PV of tile j while
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const bool leader = elect_one();
             const int* table = p.page_table + static_cast<long long>(w.b) * p.max_pages;
             const int per = BN >> p.log_page;  // pages per tile (page_size <= 128)
-            const uint32_t page_bytes = static_cast<uint32_t>(D) << p.log_page;
+            const uint32_t page_bytes = static_cast<uint32_t>(D) << p.log_page, part_bytes = page_bytes / L::PARTS;
             // Page ids come 32 at a time, a lane each, the next 32 on their way: a
             // tile's copies never wait for the page table. Batch q of a
             // sequence holds the pages 32 q .. of its tiles in order.
@@ -330,16 +330,20 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                            : -1;
             };
             auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full, int ids, int first) {
-                const unsigned here = __ballot_sync(0xffffffffu, ids >= 0 && lane >= first && lane < first + per);
+                // A lane per page: issued one after the other by a single lane, pages of
+                // 32 tokens hold the whole CTA up (five drafted tokens for 16 contexts of
+                // up to 16200 keys: 106 us against 87).
+                const bool mine = ids >= 0 && lane >= first && lane < first + per;
+                const unsigned here = __ballot_sync(0xffffffffu, mine);
                 if (leader) mbar_arrive_expect_tx(full, __popc(here) * page_bytes);
-                for (int i = 0; i < per; ++i) {
-                    const int id = __shfl_sync(0xffffffffu, ids, first + i);
-                    if (id >= 0 && leader)
+                __syncwarp();
+                if (mine) {
 #pragma unroll
-                        for (int c = 0; c < L::PARTS; ++c)
-                            tma_load_2d(dst + c * L::PART + ((i * L::ROW_BYTES) << p.log_page), map, full, c * 128,
-                                        (id * p.Hkv + w.h) << p.log_page);
+                    for (int c = 0; c < L::PARTS; ++c)
+                        tma_load_2d(dst + c * L::PART + (lane - first) * part_bytes, map, full, c * 128,
+                                    (ids * p.Hkv + w.h) << p.log_page);
                 }
+                __syncwarp();
             };
             int k_issued = 0, v_issued = 0;
             bool ok = true;
@@ -570,7 +574,8 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             // A lane converts one 16-code unit u of every ROW_STEP-th key from row0
             // on: its addresses are a register and constants.
             constexpr int ROW_STEP = D == 64 ? 32 : 16, PIECES = BN / ROW_STEP;
-            const int r8 = lane & 7, cw = (warp - L::CONV_WARP0) & 3, part = (warp - L::CONV_WARP0) >> 2;
+            const int r8 = lane & 7, cw = WIDE ? warp & 3 : warp - L::CONV_WARP0;
+            const int part = WIDE ? (warp - L::CONV_WARP0) >> 2 : 0;  // 128-column part of V
             const int u = D == 64 ? lane >> 3 : (cw & 1) * 4 + (lane >> 3);
             const int row0 = (D == 64 ? cw : cw >> 1) * 8 + r8;
             const uint32_t src_lane = sbase + L::V_OFF + part * L::PART + row0 * L::ROW_BYTES +
@@ -581,9 +586,9 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const int both = 2 * min(w.n[0], w.n[1]);  // dual: entries that alternate between the slots
             bool ok = true;
             for (int e = 0; e < entries && ok; ++e) {
-                const int s = e % L::VSTAGES, buf = e % L::VBUFS;
+                const int s = e % L::VSTAGES, buf = WIDE ? 0 : e & 1;
                 if (e >= L::VBUFS)
-                    ok = tc_wait_warp(bar(L::BAR_HEMPTY + buf), (e / L::VBUFS - 1) & 1, p, abort_flag,
+                    ok = tc_wait_warp(bar(L::BAR_HEMPTY + buf), ((WIDE ? e : e >> 1) - 1) & 1, p, abort_flag,
                                       kStatusWaitKvEmpty);
                 if (ok)
                     ok = tc_wait_warp(bar(L::BAR_VFULL + s), (e / L::VSTAGES) & 1, p, abort_flag, kStatusWaitKvFull);
