@@ -382,3 +382,38 @@ def test_window_with_split_keys(case, d):
     empty = np.isneginf(rl)
     assert np.array_equal(np.isneginf(f64(lse)), empty) and np.all(f64(o)[empty] == 0)
     assert np.all(np.abs(f64(lse)[~empty] - rl[~empty]) <= 1e-3)
+
+
+@pytest.mark.parametrize("new,d,splits", [(1, 64, 4), (1, 256, 2), (4, 128, 8), (10, 128, 3), (20, 64, 1), (40, 128, 2),
+                                          (90, 128, 2), (30, 256, 3)])
+def test_broken_batches_in_every_kernel(new, d, splits):
+    """Offsets, lengths and pages that are wrong: that sequence alone is left as it was and reported, whichever
+    kernel takes the call (single tokens as clusters, row copies, full tiles, wide heads)."""
+    page, Hkv, H = 16, 2, 8
+    lens = [200, 300, 250]
+    cache, table = cache_of(lens, page, Hkv, d, 31, max_pages=20)
+    q = normal((3 * new, H, d), 4)
+    good = [0, new, 2 * new, 3 * new]
+    full = fa.attention_paged_fp8(q, *cache, table, i32(good), i32(lens), new, 320, num_splits=splits)
+    ok()
+    for cu, ln, at, code, broken in (([0, new, 2 * new, 3 * new + 1], lens, None, 12, [2]),
+                                     (good, [200, new - 1, 250], None, 12, [1]), (good, [321, 300, 250], None, 12, [0]),
+                                     ([0, new, new - 1, 3 * new], lens, None, 12, [1, 2]),
+                                     (good, lens, (1, 3, 10 ** 6), 14, [1]), (good, lens, (2, 15, -7), 14, [2])):
+        t = table.clone()
+        if at:
+            t[at[0], at[1]] = at[2]
+        o = torch.full_like(q, 3.0)
+        lse = torch.full((H, 3 * new), 2.0, device="cuda")
+        ws = torch.empty(max(1, fa.fa_paged_workspace_bytes(3 * new, H, d, splits) // 4), device="cuda")
+        fa.fa_fwd_paged_fp8(q, *cache, o, lse, t, i32(cu), i32(ln), new, 320, ws, splits)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(clear=True) == code
+        for b in range(3):
+            rows = slice(b * new, (b + 1) * new)
+            if b not in broken and cu == good:
+                same = torch.equal(o[rows], full[0][rows]) and torch.equal(lse[:, rows], full[1][:, rows])
+                # (The lengths of a batch also choose where its sequences are cut.)
+                assert same or (o[rows].float() - full[0][rows].float()).abs().max() <= 2.0 ** -6
+            elif code == 12 and b in broken and cu == good:
+                assert torch.all(o[rows] == 3.0) and torch.all(lse[:, rows] == 2.0)
