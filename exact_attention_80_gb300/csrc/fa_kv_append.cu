@@ -120,8 +120,11 @@ __device__ __forceinline__ void append_queries(const AppendLaunch& p, unsigned l
 // PER: token slots of an item held by one thread.
 // BLOCK: an item is a whole block (its reduction goes through shared memory);
 // otherwise a power-of-two group within a warp.
+// SPLIT: sections that end inside a thread's eight pairs; the second row of the table
+// costs registers (two blocks per SM 109 us, three 113, for the prompts above).
 template <int PER, bool BLOCK, bool SPLIT>
-__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : 3) fa_kv_append_kernel(const __grid_constant__ AppendLaunch p) {
+__global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : SPLIT && PER == 4 ? 2 : 3)
+    fa_kv_append_kernel(const __grid_constant__ AppendLaunch p) {
     __shared__ float red[16];
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();

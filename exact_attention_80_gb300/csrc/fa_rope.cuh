@@ -73,20 +73,30 @@ __device__ __forceinline__ bool rope_coeffs(const RopeParams& r, int v, long lon
         if (static_cast<unsigned>(pos) >= static_cast<unsigned>(r.max_pos)) return false;
         rope_row(r, v, pos, c, s);
     } else {
+        // The row of the first pair's axis, then over its end those of the axes behind it
+        // (an axis without pairs is not read).
         const int i0 = 8 * v;
         int a = 0;
         while (a + 1 < r.axes && i0 >= r.sec_end[a]) ++a;
-        const int* at = r.positions + a * r.pos_stride + tok;
+        const int pos = r.positions[a * r.pos_stride + tok];
+        if (static_cast<unsigned>(pos) >= static_cast<unsigned>(r.max_pos)) return false;
+        rope_row(r, v, pos, c, s);
+#pragma unroll 1
+        for (++a; a < r.axes && r.sec_end[a - 1] < i0 + 8; ++a) {
+            if (r.sec_end[a] == r.sec_end[a - 1]) continue;
+            const int next = r.positions[a * r.pos_stride + tok];
+            if (static_cast<unsigned>(next) >= static_cast<unsigned>(r.max_pos)) return false;
+            const float* row = r.table + static_cast<long long>(next) * r.rot + i0;
+            const int from = r.sec_end[a - 1] - i0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            while (a + 1 < r.axes && i0 + k >= r.sec_end[a]) {
-                ++a;
-                at += r.pos_stride;
+            for (int k = 0; k < 2; ++k) {
+                const float4 x = reinterpret_cast<const float4*>(row)[k];
+                const float4 y = reinterpret_cast<const float4*>(row + (r.rot >> 1))[k];
+                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * k + e >= from) c[4 * k + e] = xs[e], s[4 * k + e] = ys[e];
             }
-            if (static_cast<unsigned>(*at) >= static_cast<unsigned>(r.max_pos)) return false;
-            const float* row = r.table + static_cast<long long>(*at) * r.rot + i0 + k;
-            c[k] = row[0];
-            s[k] = row[r.rot >> 1];
         }
     }
 #pragma unroll
