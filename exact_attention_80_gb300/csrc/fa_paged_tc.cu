@@ -45,6 +45,7 @@
 
 #include "fa.h"
 #include "fa_paged.cuh"
+#include "fa_paged_phases.h"
 #include "fa_rope.cuh"
 
 namespace fa {
@@ -86,7 +87,7 @@ struct TcLayout {
     static constexpr int BAR_HEMPTY = BAR_HFULL + 2;         // [buffer]
     static constexpr int BAR_SFULL = BAR_HEMPTY + 2;         // [tile]
     static constexpr int BAR_PFULL = BAR_SFULL + 2;          // [tile] one arrival per softmax warp with rows
-    static constexpr int BAR_OFULL = BAR_PFULL + 2;          // [tile]
+    static constexpr int BAR_OFULL = BAR_PFULL + 2;          // [tile] (WIDE: as fa_paged_phases.h says)
     static constexpr int BAR_DRAIN = BAR_OFULL + 2;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     issue_pv(j & 1, 0, j > 0);
                     if (leader) {
                         umma_commit(bar(L::BAR_HEMPTY));
-                        umma_commit(bar(L::BAR_OFULL));  // phase j: PV_j is done
+                        umma_commit(bar(L::BAR_OFULL + wide_pv_barrier(j, w.nmax)));
                     }
                     if (j + 2 < w.nmax) ok = next_s(j + 2);
                 }
@@ -915,7 +916,8 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 }
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     if constexpr (WIDE) {  // (elsewhere S_j comes behind PV_{j-1})
-                        ok = tc_wait_warp(bar(L::BAR_OFULL), (j - 1) & 1, p, abort_flag, kStatusWaitO);
+                        ok = tc_wait_warp(bar(L::BAR_OFULL + wide_pv_barrier(j - 1, n)), wide_pv_parity(j - 1, n), p,
+                                          abort_flag, kStatusWaitO);
                         if (!ok) break;
                         tc_fence_after();
                     }
@@ -943,10 +945,8 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                 m = m_new;
             }
             if (ok && n > 0) {
-                // (Wide: a phase per tile. S of the last one told that the last but two is
-                // done, no more, so the last but one is waited for first.)
-                if (WIDE && n > 1) ok = tc_wait_warp(bar(L::BAR_OFULL), n & 1, p, abort_flag, kStatusWaitO);
-                if (ok) ok = tc_wait_warp(bar(L::BAR_OFULL + t), WIDE ? (n - 1) & 1 : 0, p, abort_flag, kStatusWaitO);
+                ok = tc_wait_warp(bar(L::BAR_OFULL + (WIDE ? wide_pv_barrier(n - 1, n) : t)),
+                                  WIDE ? wide_pv_parity(n - 1, n) : 0u, p, abort_flag, kStatusWaitO);
                 if (ok) tc_fence_after();
             }
             if constexpr (DUAL) {
