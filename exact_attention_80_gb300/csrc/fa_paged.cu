@@ -38,6 +38,7 @@
 
 #include "fa.h"
 #include "fa_paged.cuh"
+#include "fa_paged_phases.h"
 #include "fa_rope.cuh"
 
 namespace fa {
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             id[e] = __shfl_sync(0xffffffffu, ids[e], k & 31);
             there += id[e] >= 0 ? 1 : 0;
         }
-        const int s = k % L::STAGES;
+        const int s = ring_slot(k, L::STAGES);
         const uint32_t dst = ring + s * L::SLOT, bar = bar0 + 8 * s;
         const int rows_each = min(page_size, KEYS);
         if (lane == 0) mbar_arrive_expect_tx(bar, there * rows_each * D * 2);
@@ -363,7 +364,8 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     for (int x = 0; x < X; x += 2)
         v_lane[x / 2] = tile_unit<D>(8 * ((lane >> 3) & 1) + key_of<D>(lane & 7), x + (lane >> 4));
 
-    for (int k = 0; k < mine; ++k) {
+    int k = 0;
+    for (; k < mine; ++k) {
         if ((k & 31) == 0) {
             const int i = i0 + warp + kWarps * (k + lane);
 #pragma unroll
@@ -376,8 +378,8 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
                 si[e] = 1.f / vs;
             }
         }
-        const int slot = k % L::STAGES;
-        ok = __all_sync(0xffffffffu, wait_bounded(bar0 + 8 * slot, (k / L::STAGES) & 1, p.wait_limit, p.status,
+        const int slot = ring_slot(k, L::STAGES);
+        ok = __all_sync(0xffffffffu, wait_bounded(bar0 + 8 * slot, ring_parity(k, L::STAGES), p.wait_limit, p.status,
                                                   kStatusWaitKvFull));
         if (!ok) break;
         const int key0 = list.tile(i0 + warp + kWarps * k) * KEYS;
@@ -512,8 +514,11 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         if (k + L::STAGES < mine) issue_next(k + L::STAGES);
     }
     if (!ok) {
-        // Copies still in flight land before the CTA goes away.
-        for (int s = 0; s < ahead; ++s) wait_bounded(bar0 + 8 * s, 0, p.wait_limit, p.status, kStatusWaitDrain);
+        // Copies still in flight land before the ring is used again and the CTA goes
+        // away: those of the tile that was waited for and of the ones behind it.
+        for (const int end = ring_issued(k, L::STAGES, mine); k < end; ++k)
+            wait_bounded(bar0 + 8 * ring_slot(k, L::STAGES), ring_parity(k, L::STAGES), p.wait_limit, p.status,
+                         kStatusWaitDrain);
     }
 
     // The warps' states meet: O rows staged in each warp's ring, m and l beside.

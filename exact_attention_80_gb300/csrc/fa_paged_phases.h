@@ -25,4 +25,11 @@ namespace fa {
 FA_PHASES_FN int wide_pv_barrier(int j, int n) { return j == n - 1 ? 1 : 0; }
 FA_PHASES_FN uint32_t wide_pv_parity(int j, int n) { return j == n - 1 ? 0u : static_cast<uint32_t>(j & 1); }
 
+// fa_paged.cu: the copies of a warp's tile k complete phase k / stages of slot
+// k % stages of its ring. At the wait for tile k the copies of the tiles up to
+// ring_issued have started (tile k + stages follows when tile k's slot is free).
+FA_PHASES_FN int ring_slot(int k, int stages) { return k % stages; }
+FA_PHASES_FN uint32_t ring_parity(int k, int stages) { return static_cast<uint32_t>(k / stages & 1); }
+FA_PHASES_FN int ring_issued(int k, int stages, int tiles) { return k + stages < tiles ? k + stages : tiles; }
+
 }  // namespace fa

@@ -20,6 +20,9 @@ SOURCE = """
 extern "C" {
 int pv_barrier(int j, int n) { return fa::wide_pv_barrier(j, n); }
 unsigned pv_parity(int j, int n) { return fa::wide_pv_parity(j, n); }
+int slot(int k, int stages) { return fa::ring_slot(k, stages); }
+unsigned parity(int k, int stages) { return fa::ring_parity(k, stages); }
+int issued(int k, int stages, int tiles) { return fa::ring_issued(k, stages, tiles); }
 }
 """
 
@@ -61,3 +64,21 @@ def test_wide_heads_wait_for_the_product_before(phases):
             for done in (j - 1, j):
                 completed = [sum(phases.pv_barrier(i, n) == b for i in range(done)) for b in range(2)]
                 assert passes(completed[bar], parity) == (done == j), (n, j, done)
+
+
+@pytest.mark.parametrize("stages", [2, 3])
+def test_a_warp_that_gives_up_waits_for_its_copies(phases, stages):
+    """Few rows: a warp whose wait for tile k ran out leaves its ring only when all copies that it started have
+    landed, whatever the tile, and whichever of them land first."""
+    for tiles in range(1, 4 * stages + 2):
+        for k in range(tiles):
+            # The loop's own order: the first `stages` tiles, then tile i + stages behind tile i.
+            started = list(range(min(stages, tiles))) + [i + stages for i in range(k) if i + stages < tiles]
+            flying = [e for e in started if e >= k]  # tiles before k were waited for one by one
+            assert flying == list(range(k, phases.issued(k, stages, tiles)))
+            for landed in range(1 << len(flying)):
+                done = set(range(k)) | {e for i, e in enumerate(flying) if landed >> i & 1}
+                completed = [sum(e % stages == s for e in done) for s in range(stages)]
+                waits = [passes(completed[phases.slot(e, stages)], phases.parity(e, stages))
+                         for e in range(k, phases.issued(k, stages, tiles))]
+                assert all(waits) == (len(done) == len(started))
