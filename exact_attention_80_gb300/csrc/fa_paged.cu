@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         const __nv_bfloat16* src =
             p.q + (static_cast<long long>(nt.first + i) * p.H + h * p.G + j) * D + 16 * t;
         uint4 raw[C][2];
-        float mx = 0.f;
+        uint32_t mx = 0u;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -304,16 +304,14 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
                 raw[c][u] = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * u);
                 float x[8];
                 unpack_bf16x8(raw[c][u], x);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]));
+                mx = abs_bits_max(mx, x);
             }
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // Exponent of the largest element to 7; f and 1 / f stay normal.
-        const int ex = mx > 0.f ? min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 120) : 0;
-        const float f = exp2i(7 - ex > 120 ? 120 : 7 - ex);
-        rowf[e] = p.scale_log2 * (1.f / f);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        float f, undo;
+        query_scale(mx, f, undo);
+        rowf[e] = p.scale_log2 * undo;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll

@@ -25,6 +25,22 @@ __device__ __forceinline__ float usable_scale(float s) { return fminf(fmaxf(s, 0
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+// The scale of a query row, from the bits of its largest |element| as an unsigned
+// maximum (where every NaN and infinity lies above all finite values): `f`, a power
+// of two, brings that element to [2^7, 2^8); f and 1 / f stay normal. `undo` is 1 / f,
+// or NaN where the row holds an element that is not finite: the operands would make
+// a finite number of it (e4m3 has no infinity), so the row's scores are made NaN.
+__device__ __forceinline__ uint32_t abs_bits_max(uint32_t m, const float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
+    return m;
+}
+__device__ __forceinline__ void query_scale(uint32_t bits, float& f, float& undo) {
+    const int ex = bits > 0u ? min(max(static_cast<int>(bits >> 23) - 127, -100), 120) : 0;
+    f = exp2i(min(7 - ex, 120));
+    undo = bits < 0x7f800000u ? 1.f / f : __uint_as_float(0x7fffffffu);
+}
+
 // Four e4m3 codes as two packed f16 pairs (codes 0 and 1, 2 and 3): exact.
 __device__ __forceinline__ void decode_e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\t"

@@ -665,17 +665,16 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             {
                 // Q's two e4m3 terms into the tile's swizzled rows.
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * D);
-                float mx = 0.f;
+                uint32_t mx = 0u;
 #pragma unroll 4
                 for (int u = 0; u < D / 8; ++u) {
                     float x[8];
                     unpack_bf16x8(src[u], x);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(x[k]));
+                    mx = abs_bits_max(mx, x);
                 }
-                const int ex = mx > 0.f ? min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 120) : 0;
-                const float f = exp2i(min(7 - ex, 120));
-                rowf *= 1.f / f;
+                float f, undo;
+                query_scale(mx, f, undo);
+                rowf *= undo;
                 const uint32_t hi_at = sbase + L::Q_OFF + t * L::Q_TILE + r * L::ROW_BYTES;
 #pragma unroll 2
                 for (int u = 0; u < (DUAL && t == 1 ? 0 : D / 16); ++u) {

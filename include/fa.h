@@ -425,7 +425,9 @@ fa_status fa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_
  * sequence is neither read nor written, FA_ERR_SEQLENS from fa_device_status;
  * a page that is not one of the cache: FA_ERR_PAGES, the sequence's result is
  * undefined. Scores and sums are fp32; Q enters the products as f16 after an
- * exact power-of-two scale per row, P as f16 (relative rounding 2^-11).
+ * exact power-of-two scale per row, P as f16 (relative rounding 2^-11). A query
+ * row that holds an infinity or a NaN gives NaN in its O and LSE, and leaves the
+ * other rows as they are.
  */
 int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k, int d, int window, int sinks);
 size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits);

@@ -1,0 +1,94 @@
+"""The edges of what the serving calls state in include/fa.h: elements that are not finite,
+queries whose elements lie far apart, and the paths that only large batches take.
+
+Tolerances as in test_serving.py (2^-8 |o| + 2^-10 sum_j w_j |v_j|, LSE 5e-4) unless a test
+says otherwise.
+"""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import exact_attention_80_gb300 as fa  # noqa: E402
+import oracle.serving as orc  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    fa.load_library()
+    fa.fa_device_status(clear=True)
+
+
+def ok():
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_OK
+
+
+def normal(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(torch.bfloat16).cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def cache_of(lens, page, Hkv, d, seed):
+    """A cache of random codes and scales in shuffled pages: [k, v, k_scale, v_scale], table."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    P = sum(need)
+    ids = torch.randperm(P, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at: at + n]
+        at += n
+    codes = [(torch.randn((P, Hkv, page, d), generator=g, device="cuda") * 90).clamp(-448, 448)
+             .to(torch.float8_e4m3fn).view(torch.uint8)
+             for _ in range(2)]
+    scales = [torch.exp2(torch.randint(-8, -5, (P, Hkv), generator=g, device="cuda").float()) for _ in range(2)]
+    return codes + scales, table
+
+
+def paged_oracle(q, cache, table, ns, lens, window=0, sinks=0):
+    cu = np.concatenate([[0], np.cumsum(ns)]).astype(np.int32)
+    kc, vc, ks, vs = (x.cpu().numpy() for x in cache)
+    return orc.paged(f64(q), kc, vc, ks, vs, table.cpu().numpy(), cu, lens, fa.default_scale(q.shape[-1]), window, sinks)
+
+
+# 8 rows per token: the kernel for up to 16 rows (as clusters, through the workspace and
+# unsplit), row copies of four and two, full tiles of one row block, several row blocks.
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,splits", [(1, 4), (2, 1), (2, 12), (4, 2), (8, 1), (15, 3), (40, 1), (40, 2)])
+def test_queries_that_are_not_finite(n, d, splits):
+    """A row that holds an infinity or a NaN gives NaN, also where each of its scores is minus infinity; the
+    other rows keep their bits."""
+    H, Hkv, page, lens = 8, 1, 16, [700, 450]
+    cache, table = cache_of(lens, page, Hkv, d, 3)
+    cache[0] &= 0x7F        # keys above zero
+    cache[0].clamp_(8, 0x7E)
+    q = normal((2 * n, H, d), n)
+    args = (*cache, table, i32([0, n, 2 * n]), i32(lens), n, 700)
+    want, want_lse = fa.attention_paged_fp8(q, *args, num_splits=splits)
+    ok()
+    bad = torch.zeros((2 * n, H), dtype=torch.bool, device="cuda")
+    for i, x in enumerate((float("inf"), -float("inf"), float("nan"))):
+        at, h, c = (i * 7 + 1) % (2 * n), 2 * i + 1, (i * 29 + 5) % d
+        q[at, h, c] = x
+        bad[at, h] = True
+    q[n, 0, 3], q[n, 0, 4], bad[n, 0] = float("inf"), -float("inf"), True
+    q[2 * n - 1, 6, d - 1], bad[2 * n - 1, 6] = -float("inf"), True
+    o, lse = fa.attention_paged_fp8(q, *args, num_splits=splits)
+    ok()
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse.t()[bad]).all()
+    assert torch.equal(o[~bad], want[~bad]) and torch.equal(lse.t()[~bad], want_lse.t()[~bad])
