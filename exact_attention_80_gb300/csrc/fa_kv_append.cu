@@ -54,11 +54,12 @@ struct AppendLaunch {
     unsigned* status;
 };
 
-// Largest absolute value of a thread's two vectors; fmaxf drops NaN.
+// Largest finite absolute value of a thread's two vectors: |x| + 0 x is NaN where x is
+// not finite, and fmaxf drops NaN.
 __device__ __forceinline__ float amax16(const float (&x)[8], const float (&y)[8]) {
     float m = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaxf(fabsf(x[k]), fabsf(y[k])));
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaxf(fmaf(x[k], 0.f, fabsf(x[k])), fmaf(y[k], 0.f, fabsf(y[k]))));
     return m;
 }
 
@@ -69,9 +70,13 @@ __device__ __forceinline__ int scale_exponent(float a) {
     return a > 0.f ? min(max(e, kScaleExpMin), kScaleExpMax) : kScaleExpMin;
 }
 
+// Eight codes of x inv; what is not finite becomes e4m3's NaN (x inv + 0 x is NaN for an
+// infinity, which the conversion alone would make 448).
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
-    return make_uint2(pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                      pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = fmaf(x[k], inv, x[k] * 0.f);
+    return make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
 }
 
 // Sixteen codes times `f` (a power of two below one), rounded to e4m3 again.

@@ -397,6 +397,8 @@ typedef struct {
  * amax <= 448 * 2^e over the block's tokens (e >= -100). The first slot of a
  * page starts a block anew; an append behind earlier tokens keeps the larger of
  * the old and the new scale, and rounds the earlier codes again where it grew.
+ * An element that is not finite (a key's, after the rotation) is stored as NaN
+ * and does not count for the scale.
  * The other slots keep their bytes. A sequence whose offsets or length are
  * broken, and a page that is not one of the cache, is neither read nor written
  * (FA_ERR_SEQLENS, FA_ERR_PAGES from fa_device_status); a position outside the

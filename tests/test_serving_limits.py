@@ -92,3 +92,45 @@ def test_queries_that_are_not_finite(n, d, splits):
     ok()
     assert torch.isnan(o[bad]).all() and torch.isnan(lse.t()[bad]).all()
     assert torch.equal(o[~bad], want[~bad]) and torch.equal(lse.t()[~bad], want_lse.t()[~bad])
+
+
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("n", [1, 3, 16, 70, 300])
+def test_appended_infinities(n, rotate):
+    """A new key or value that is infinite is stored as NaN, a rotated key's partner with it; its block keeps
+    the scale and the codes that it has with zeros in those places."""
+    d, Hkv, page = 64, 2, 64
+    lens = [n + 40]
+    k, v = normal((n, Hkv, d), 1), normal((n, Hkv, d), 2)
+    cu, ln = i32([0, n]), i32(lens)
+    pages = -(-lens[0] // page)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()[None]
+    old = [torch.randint(0x20, 0x60, (pages, Hkv, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    old += [torch.full((pages, Hkv), 2.0 ** -12, device="cuda") for _ in range(2)]
+    cs = None
+    if rotate:
+        ang = torch.rand((lens[0], d // 2), device="cuda") + 0.2
+        cs = torch.cat([ang.cos(), ang.sin()], 1)
+    at = torch.zeros((n, Hkv, d), dtype=torch.bool, device="cuda")
+    at[0, 0, 5] = at[n // 2, 1, 17] = at[n - 1, 0, d - 1] = True
+    hit = at | at.roll(d // 2, -1) if rotate else at  # pairs are half a head apart
+    inf = torch.where(torch.arange(d, device="cuda") % 2 == 0, float("inf"), -float("inf")).to(torch.bfloat16).expand_as(k)
+    runs = []
+    for kk, vv in ((torch.where(at, inf, k), torch.where(at, inf, v)),
+                   (torch.where(hit, torch.zeros_like(k), k), torch.where(at, torch.zeros_like(v), v))):
+        c = [x.clone() for x in old]
+        fa.kv_append_fp8(None, kk, vv, *c, table, cu, ln, n, table=cs)
+        ok()
+        runs.append(c)
+    (kc, vc, ks, vs), (kz, vz, ksz, vsz) = runs
+    assert torch.equal(ks, ksz) and torch.equal(vs, vsz)
+    slot = torch.arange(40, lens[0], device="cuda")
+    for got, want, places in ((kc, kz, hit), (vc, vz, at)):
+        want = want.clone()
+        pg = table[0].long()[slot // page]
+        rows = want[pg, :, slot % page]
+        want[pg, :, slot % page] = torch.where(places, torch.full_like(rows, 0x7F), rows)
+        # (The sign of a NaN or of a zero is not fixed.)
+        assert torch.equal(got & 0x7F, want & 0x7F)
+        assert torch.equal(torch.where(got & 0x7F == 0, 0, got)[want & 0x7F != 0x7F],
+                           torch.where(want & 0x7F == 0, 0, want)[want & 0x7F != 0x7F])
