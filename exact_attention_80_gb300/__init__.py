@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa_gb300.so")
@@ -49,7 +50,7 @@ class FAError(RuntimeError):
 
 def load_library() -> ctypes.CDLL:
     """Load the in-tree CUDA library (build it with ``exact_attention_80_gb300.build``)."""
-    global _lib
+    global _lib, _compiled
     if _lib is not None:
         return _lib
     if not os.path.exists(LIB_PATH):
@@ -108,28 +109,35 @@ def load_library() -> ctypes.CDLL:
     lib.fa_device_status.restype = i
     lib.fa_status_string.argtypes = [i]
     lib.fa_status_string.restype = ctypes.c_char_p
-    _lib = lib
-    _load_calls(lib)
+    _compiled = _load_calls(lib)
+    _lib = lib  # only now: a load that failed is tried again by the next call
     return lib
 
 
 def _load_calls(lib):
-    """The compiled form of the calls that a few microseconds matter to (csrc/fa_calls.cpp), where
-    PyTorch is installed."""
-    global _compiled
+    """The compiled form of the calls that a few microseconds matter to (csrc/fa_calls.cpp). None, with a
+    warning, where the module is missing or belongs to another PyTorch: the Python forms then take
+    every call. None without PyTorch, or with one that has no CUDA."""
     try:
-        import torch  # noqa: F401
+        import torch
     except ImportError:
-        return
-    if not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_calls.so")):
-        raise RuntimeError("_calls.so is missing: build it with `python -m exact_attention_80_gb300.build`")
-    from . import _calls as calls  # type: ignore[attr-defined]
+        return None
+    if torch.version.cuda is None:
+        return None
+    try:
+        from . import _calls as calls  # type: ignore[attr-defined]
 
+        if calls.torch_version != str(torch.__version__):
+            raise ImportError(f"built against PyTorch {calls.torch_version}, this is {torch.__version__}")
+    except (ImportError, AttributeError) as e:
+        warnings.warn(f"exact_attention_80_gb300: the compiled calls are not there ({e}), short calls take longer; "
+                      "build them with `python -m exact_attention_80_gb300.build`", RuntimeWarning, stacklevel=3)
+        return None
     calls.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fa_rope, lib.fa_kv_append_fp8, lib.fa_fwd_paged_fp8, lib.fa_paged_num_splits,
         lib.fa_paged_workspace_bytes, lib.fa_fwd_window, lib.fa_bwd_window, lib.fa_bwd_window_workspace_bytes,
         lib.fa_window_num_splits, lib.fa_fwd_window_splitkv, lib.fa_combine)))
-    _compiled = calls
+    return calls
 
 
 def fa_status_string(status: int) -> str:
@@ -486,8 +494,9 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
 # These calls are short (a decode step of a few sequences runs in a few
 # microseconds on the GPU). On the current stream and with plain arguments rope,
 # kv_append_fp8, attention_paged_fp8 and the window's two calls run in the
-# compiled module _calls; it answers None where an argument is anything else, and the forms below, whose
-# checks touch each tensor once, say what is wrong or take the call.
+# compiled module _calls, where it is there; it answers None where an argument is
+# anything else, and the forms below, whose checks touch each tensor once, say
+# what is wrong or take the call.
 _ROTATION = struct.Struct(f"PPii{FA_MAX_AXES}iii")   # fa_rotation
 _ROPE_TENSOR = struct.Struct("PPi6q")                # fa_rope_tensor
 _PAGED_CACHE = struct.Struct("PPPPiiii")             # fa_paged_cache

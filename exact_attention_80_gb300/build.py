@@ -3,8 +3,9 @@
 Each ``csrc/*.cu`` translation unit is compiled by ``nvcc`` in parallel, then
 linked into one shared library beside this file. Only a CUDA toolkit with
 sm_103a support is needed (the build cross-compiles without a GPU). Where
-PyTorch is installed, ``csrc/fa_calls.cpp`` is built beside them as the Python
-module ``_calls`` against its headers.
+PyTorch with CUDA is installed, ``csrc/fa_calls.cpp`` is built beside them as
+the Python module ``_calls`` against its headers. The library does without
+that module: where it cannot be built, the build says so and goes on.
 
 Usage: ``python -m exact_attention_80_gb300.build [--ptxas-verbose]``
 """
@@ -14,6 +15,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -52,21 +54,34 @@ def _compile(nvcc: str, src: str, ptxas_verbose: bool) -> tuple[str, str]:
 
 
 def build_calls() -> str | None:
-    """Compile ``csrc/fa_calls.cpp`` into the module ``_calls``; None without PyTorch."""
+    """Compile ``csrc/fa_calls.cpp`` into the module ``_calls``. None, and no module left from an earlier
+    build, where there is no PyTorch with CUDA or the module does not compile against it."""
+    if os.path.exists(CALLS):
+        os.remove(CALLS)
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
     torch = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
+        return None
+    with open(os.path.join(torch, "version.py"), encoding="utf-8") as f:
+        version = re.search(r"^__version__ *(?::.*?)?= *['\"](.*?)['\"]", f.read(), re.M).group(1)
     inc, tmp = os.path.join(torch, "include"), CALLS + ".tmp"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
-    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
-           "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", f'-DFA_TORCH_VERSION="{version}"',
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "fa_calls.cpp"), "-o", tmp,
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on fa_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = "" if r.returncode == 0 else f"{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        why = str(e)
+    if why:
+        sys.stderr.write(f"the module _calls was not built (the library works without it, short calls take longer): "
+                         f"g++ failed on fa_calls.cpp:\n{why}\n")
+        return None
     os.replace(tmp, CALLS)
     return CALLS
 
