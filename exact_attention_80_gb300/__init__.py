@@ -149,6 +149,13 @@ def _check(status: int, what: str) -> None:
         raise FAError(status, what)
 
 
+def _int32(x):
+    """``x`` where the interface's 32-bit int holds it: ctypes would pass on its low bits."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise OverflowError(f"{x} does not fit the library's 32-bit int")
+    return x
+
+
 def _stream_handle(stream):
     import torch
 
@@ -225,7 +232,7 @@ def causal_code(causal) -> int:
         return _CAUSAL_NAMES[causal]
     if isinstance(causal, bool):
         return CAUSAL_TOP_LEFT if causal else CAUSAL_NONE
-    return int(causal)
+    return _int32(int(causal))
 
 
 def default_scale(d: int) -> float:
@@ -251,7 +258,7 @@ def fa_fwd_rows(q, k, v, o, lse, rows_per_cta: int, causal=False, scale: float |
     _need_o_lse(o, lse, B, H, Nq, d, q.device)
     scale = default_scale(d) if scale is None else float(scale)
     st = load_library().fa_fwd_rows(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Nq, Nk, d,
-                                    scale, causal_code(causal), int(rows_per_cta),
+                                    scale, causal_code(causal), _int32(int(rows_per_cta)),
                                     _stream_handle(stream))
     _check(st, "fa_fwd_rows")
 
@@ -298,7 +305,7 @@ def fa_fwd_fp8_splitkv(q, k, v, q_descale: float, k_descale: float, v_descale: f
     scale = default_scale(d) if scale is None else float(scale)
     st = load_library().fa_fwd_fp8_splitkv(_ptr(q), _ptr(k), _ptr(v), float(q_descale),
                                            float(k_descale), float(v_descale), _ptr(workspace), B, H,
-                                           Nq, Nk, d, scale, causal_code(causal), int(num_splits),
+                                           Nq, Nk, d, scale, causal_code(causal), _int32(int(num_splits)),
                                            _stream_handle(stream))
     _check(st, "fa_fwd_fp8_splitkv")
 
@@ -324,7 +331,7 @@ def attention_fp8(q, k, v, q_descale: float = 1.0, k_descale: float = 1.0, v_des
 
 
 def fa_bwd_workspace_bytes(B: int, H: int, Nq: int, d: int) -> int:
-    return int(load_library().fa_bwd_workspace_bytes(B, H, Nq, d))
+    return int(load_library().fa_bwd_workspace_bytes(*map(_int32, (B, H, Nq, d))))
 
 
 def fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal=False,
@@ -393,7 +400,7 @@ def fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int
     scale = default_scale(d) if scale is None else float(scale)
     st = load_library().fa_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                       _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, H, total_q,
-                                      total_k, int(max_seqlen_q), d, scale, causal_code(causal),
+                                      total_k, _int32(int(max_seqlen_q)), d, scale, causal_code(causal),
                                       _stream_handle(stream))
     _check(st, "fa_fwd_varlen")
 
@@ -411,7 +418,7 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, cau
 
 
 def fa_splitkv_workspace_bytes(B: int, H: int, Nq: int, d: int, num_splits: int) -> int:
-    return int(load_library().fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits))
+    return int(load_library().fa_splitkv_workspace_bytes(*map(_int32, (B, H, Nq, d, num_splits))))
 
 
 def fa_fwd_splitkv(q, k, v, workspace, num_splits: int, causal=False,
@@ -422,7 +429,7 @@ def fa_fwd_splitkv(q, k, v, workspace, num_splits: int, causal=False,
                     q.device)
     scale = default_scale(d) if scale is None else float(scale)
     st = load_library().fa_fwd_splitkv(_ptr(q), _ptr(k), _ptr(v), _ptr(workspace), B, H, Nq, Nk,
-                                       d, scale, causal_code(causal), int(num_splits),
+                                       d, scale, causal_code(causal), _int32(int(num_splits)),
                                        _stream_handle(stream))
     _check(st, "fa_fwd_splitkv")
 
@@ -439,7 +446,7 @@ def fa_combine(workspace, o, lse, B: int, H: int, Nq: int, d: int, num_splits: i
 
 
 def fa_fwd_grid_ctas(B: int, H: int, Nq: int, d: int, num_splits: int = 1) -> int:
-    return int(load_library().fa_fwd_grid_ctas(B, H, Nq, d, num_splits))
+    return int(load_library().fa_fwd_grid_ctas(*map(_int32, (B, H, Nq, d, num_splits))))
 
 
 def fa_device_status(clear: bool = True, stream=None) -> int:
@@ -486,7 +493,7 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
     fn.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp]
     fn.restype = i
     st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Nq, Nk, d, scale,
-            causal_code(causal), int(num_splits), _stream_handle(stream))
+            causal_code(causal), _int32(int(num_splits)), _stream_handle(stream))
     _check(st, "fa_fwd_splitkv_static")
 
 
@@ -758,8 +765,8 @@ def _append(q, k, v, q_out, make, k_cache, v_cache, k_scale, v_scale, page_table
     elif positions is not None:
         raise ValueError("positions without a table")
     st = _on_stream(index, stream, load_library().fa_kv_append_fp8, qp, k.data_ptr(), v.data_ptr(), op, rope, cache,
-                    page_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), B, H, n, max_seqlen, max_pages,
-                    qs, ks, vs)
+                    page_table.data_ptr(), cu_seqlens.data_ptr(), seqlens_k.data_ptr(), B, H, n, _int32(max_seqlen),
+                    max_pages, qs, ks, vs)
     if st != FA_OK:
         raise FAError(st, "fa_kv_append_fp8")
     return q_out
@@ -799,11 +806,12 @@ def kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
 def fa_paged_num_splits(B: int, H: int, Hkv: int, max_seqlen_q: int, max_seqlen_k: int, d: int, window: int = 0,
                         sinks: int = 0) -> int:
     """The key splits the library proposes for a paged call (0 for arguments out of range)."""
-    return load_library().fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks)
+    return load_library().fa_paged_num_splits(
+        *map(_int32, (B, H, Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks)))
 
 
 def fa_paged_workspace_bytes(total_q: int, H: int, d: int, num_splits: int) -> int:
-    return load_library().fa_paged_workspace_bytes(total_q, H, d, num_splits)
+    return load_library().fa_paged_workspace_bytes(*map(_int32, (total_q, H, d, num_splits)))
 
 
 def _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
@@ -820,6 +828,8 @@ def _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens
     if width != d:
         raise ValueError(f"q has head dim {d}, the cache {width}")
     B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, index)
+    for x in (max_seqlen_q, max_seqlen_k, window, sinks, num_splits or 1):
+        _int32(x)
     lib = load_library()
     if o is None:
         if num_splits is None:
@@ -907,13 +917,13 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     _check_out(lse, "lse", (B, H, Nq), torch.float32, index)
     st = _on_stream(index, stream, load_library().fa_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                     o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
-                    window, sinks)
+                    _int32(window), _int32(sinks))
     _check(st, "fa_fwd_window")
 
 
 def fa_window_num_splits(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
     """The key splits the library proposes for a windowed forward (0 for arguments out of range)."""
-    return load_library().fa_window_num_splits(B, H, Hkv, Nq, Nk, d, window, sinks)
+    return load_library().fa_window_num_splits(*map(_int32, (B, H, Hkv, Nq, Nk, d, window, sinks)))
 
 
 def fa_fwd_window_splitkv(q, k, v, workspace, num_splits: int, window: int, sinks: int = 0,
@@ -923,8 +933,8 @@ def fa_fwd_window_splitkv(q, k, v, workspace, num_splits: int, window: int, sink
     B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
     _need_workspace(workspace, fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits), "workspace", q.device)
     st = _on_stream(index, stream, load_library().fa_fwd_window_splitkv, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale, window,
-                    sinks, num_splits)
+                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
+                    _int32(window), _int32(sinks), _int32(num_splits))
     _check(st, "fa_fwd_window_splitkv")
 
 
@@ -963,7 +973,7 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
 
 def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int, window: int,
                                   sinks: int = 0) -> int:
-    return load_library().fa_bwd_window_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, sinks)
+    return load_library().fa_bwd_window_workspace_bytes(*map(_int32, (B, H, Hkv, Nq, Nk, d, window, sinks)))
 
 
 def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sinks: int = 0,
@@ -980,8 +990,8 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
                     q.device)
     st = _on_stream(index, stream, load_library().fa_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                     o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale, window,
-                    sinks)
+                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
+                    _int32(window), _int32(sinks))
     _check(st, "fa_bwd_window")
 
 
