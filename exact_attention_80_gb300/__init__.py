@@ -13,6 +13,7 @@ no fallback: if the library is missing or a call fails, an exception says so.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import warnings
@@ -571,7 +572,8 @@ def _heads_view(t, name):
 
 
 def _rotation(table, positions, axes, sections, interleaved, tokens, index):
-    """fa_rotation of a table and of positions that hold ``axes`` rows."""
+    """fa_rotation of a table and of positions that hold ``axes`` rows; ``tokens`` is the tokens' shape,
+    (B, N) or (N,)."""
     import torch
 
     rows, rot = table.shape
@@ -581,8 +583,10 @@ def _rotation(table, positions, axes, sections, interleaved, tokens, index):
     if positions is not None:
         if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != index:
             raise ValueError(f"positions must be contiguous int32 [axes, tokens] on device {index}")
-        if positions.numel() != axes * tokens:
-            raise ValueError(f"positions must hold {tokens} tokens for each axis, got {tuple(positions.shape)}")
+        # One axis of [B, N] tensors may also come flat; [N, B], say, holds as many numbers for other tokens.
+        shape, flat = tuple(positions.shape), (math.prod(tokens),)
+        if shape not in (tokens, (axes, *tokens)) and (axes != 1 or shape not in (flat, (1, *flat))):
+            raise ValueError(f"positions must have shape {tokens} or {('axes', *tokens)}, got {shape}")
         at = positions.data_ptr()
     if axes > FA_MAX_AXES:
         raise FAError(18, "rotation")
@@ -629,7 +633,7 @@ def _rope(q, k, q_out, k_out, table, positions, sections, interleaved, inverse, 
     if positions is None:
         raise TypeError("positions must be a tensor")
     axes = positions.shape[0] if positions.dim() == dim - 1 else 1
-    rope = _rotation(table, positions, axes, sections, interleaved, B * N, index)
+    rope = _rotation(table, positions, axes, sections, interleaved, (B, N) if dim == 4 else (N,), index)
     st = _on_stream(index, stream, load_library().fa_rope, packed[0], packed[1], rope, B, N, d, 1 if inverse else 0)
     if st != FA_OK:
         raise FAError(st, "fa_rope")
@@ -761,7 +765,7 @@ def _append(q, k, v, q_out, make, k_cache, v_cache, k_scale, v_scale, page_table
     rope = None
     if table is not None:
         axes = positions.shape[0] if positions is not None and positions.dim() == 2 else 1
-        rope = _rotation(table, positions, axes, sections, interleaved, n, index)
+        rope = _rotation(table, positions, axes, sections, interleaved, (n,), index)
     elif positions is not None:
         raise ValueError("positions without a table")
     st = _on_stream(index, stream, load_library().fa_kv_append_fp8, qp, k.data_ptr(), v.data_ptr(), op, rope, cache,

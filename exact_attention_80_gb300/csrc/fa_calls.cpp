@@ -98,15 +98,22 @@ bool array(const at::Tensor& t, at::ScalarType type, int index) {
            t.is_contiguous();
 }
 
-// fa_rotation of a table and of `axes` rows of positions (null: none).
+// fa_rotation of a table and of `axes` rows of positions (null: none) for tokens
+// [B, N] (`dense`) or [N].
 bool rotation(const at::Tensor& table, const at::Tensor* positions, long long axes, PyObject* sections,
-              int interleaved, long long count, int index, fa_rotation* r) {
+              int interleaved, bool dense, long long B, long long N, int index, fa_rotation* r) {
     if (!array(table, at::kFloat, index) || table.dim() != 2 || table.size(0) > INT_MAX || table.size(1) > INT_MAX)
         return false;
     if (axes < 1 || axes > FA_MAX_AXES) return false;
     std::memset(r, 0, sizeof(*r));
     if (positions) {
-        if (!array(*positions, at::kInt, index) || positions->numel() != axes * count) return false;
+        if (!array(*positions, at::kInt, index)) return false;
+        const auto n = positions->sizes();
+        const size_t dim = n.size(), tokens = dense ? 2 : 1;  // dimensions of the tokens
+        const bool fits = (dim == tokens || dim == tokens + 1) && n[dim - 1] == N && (!dense || n[dim - 2] == B);
+        // (One axis of [B, N] tokens may come flat.)
+        if (!fits && !(dense && axes == 1 && positions->numel() == B * N && (dim == 1 || (dim == 2 && n[0] == 1))))
+            return false;
         r->positions = static_cast<const int*>(positions->data_ptr());
     }
     r->table = static_cast<const float*>(table.data_ptr());
@@ -235,7 +242,7 @@ PyObject* call_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const long long axes = positions->dim() == t[0]->dim() - 1 ? positions->size(0) : 1;
     fa_rotation r;
-    NOT_PLAIN_UNLESS(rotation(*table, positions, axes, a[4], interleaved, v[0].B * v[0].N, index, &r));
+    NOT_PLAIN_UNLESS(rotation(*table, positions, axes, a[4], interleaved, t[0]->dim() == 4, v[0].B, v[0].N, index, &r));
     at::Tensor out[2];
     fa_rope_tensor x[2];
     for (int i = 0; i < (t[1] ? 2 : 1); ++i) {
@@ -274,7 +281,7 @@ PyObject* call_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fa_rotation r;
     if (table) {
         const long long axes = positions && positions->dim() == 2 ? positions->size(0) : 1;
-        NOT_PLAIN_UNLESS(rotation(*table, positions, axes, a[13], interleaved, kt.n, index, &r));
+        NOT_PLAIN_UNLESS(rotation(*table, positions, axes, a[13], interleaved, false, 1, kt.n, index, &r));
     }
     at::Tensor out;
     if (q) out = at::empty({qt.n, qt.h, qt.d}, q->options());

@@ -86,3 +86,28 @@ def test_numbers_past_32_bits_are_refused(stub):
                 call(n)
                 pytest.fail(f"call {i} took {n}")
     assert not stub.calls
+
+
+def test_positions_of_another_shape_are_refused(stub):
+    """Positions belong to tokens by their shape: as many numbers in another order are an error."""
+    q, k, table = bf(2, 4, 9, 64), bf(2, 2, 9, 64), torch.zeros(100, 64)
+    for shape in ((2, 9), (1, 2, 9), (18,), (1, 18)):  # flat: as one axis lies in memory
+        fa.rope(q, k, table, i32(*shape))
+    fa.rope(q, k, table, i32(2, 2, 9), sections=(16, 16))
+    t, kv, c, batch = bf(6, 4, 64), bf(6, 2, 64), cache_args(), [i32(3, 4), i32(4), i32(3)]
+    for shape in ((6,), (1, 6)):
+        fa.rope(t, kv, table, i32(*shape))
+        fa.kv_append_fp8(t, kv, kv, *c, *batch, 2, table=table, positions=i32(*shape))
+    fa.kv_append_fp8(t, kv, kv, *c, *batch, 2, table=table, positions=i32(2, 6), sections=(16, 16))
+    n = len(stub.calls)
+    assert n == 10
+    bad = [lambda s=s: fa.rope(q, k, table, i32(*s)) for s in ((9, 2), (1, 9, 2), (18, 1), (3, 6), (1, 1, 2, 9), (6, 3))]
+    bad += [lambda: fa.rope(q, k, table, i32(2, 9, 2), sections=(16, 16)),
+            lambda: fa.rope(q, k, table, i32(2, 18), sections=(16, 16))]
+    for s in ((2, 3), (1, 6, 1), (3, 2, 1), (1, 1, 6)):
+        bad += [lambda s=s: fa.rope(t, kv, table, i32(*s)),
+                lambda s=s: fa.kv_append_fp8(t, kv, kv, *c, *batch, 2, table=table, positions=i32(*s))]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    assert len(stub.calls) == n

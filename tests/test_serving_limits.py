@@ -134,3 +134,25 @@ def test_appended_infinities(n, rotate):
         assert torch.equal(got & 0x7F, want & 0x7F)
         assert torch.equal(torch.where(got & 0x7F == 0, 0, got)[want & 0x7F != 0x7F],
                            torch.where(want & 0x7F == 0, 0, want)[want & 0x7F != 0x7F])
+
+
+def test_compiled_calls_look_at_the_positions_shape():
+    """The compiled calls take the shapes that the Python forms take, and leave the others to them."""
+    q, table = normal((2, 4, 9, 64), 1), torch.rand(50, 64, device="cuda")
+    pos = torch.randint(0, 50, (18,), dtype=torch.int32, device="cuda")
+    want = fa.rope(q, None, table, pos.view(2, 9), stream=torch.cuda.current_stream())
+    for shape in ((2, 9), (1, 2, 9), (18,), (1, 18)):
+        assert torch.equal(fa._compiled.rope(q, None, table, pos.view(shape), None, False, False), want)
+    for shape in ((9, 2), (1, 9, 2), (18, 1), (3, 6), (1, 1, 2, 9)):
+        assert fa._compiled.rope(q, None, table, pos.view(shape), None, False, False) is None
+        with pytest.raises(ValueError):
+            fa.rope(q, None, table, pos.view(shape))
+    cache, pages = cache_of([6], 16, 2, 64, 1)
+    k = normal((6, 2, 64), 2)
+    for shape, takes in (((6,), True), ((1, 6), True), ((6, 1), False), ((2, 3), False), ((1, 6, 1), False)):
+        out = fa._compiled.append(None, k, k, *cache, pages, i32([0, 6]), i32([6]), 6, table, pos[:6].view(shape), None,
+                                  False)
+        assert (out is True) == takes and (takes or out is None)
+    assert fa._compiled.paged(normal((6, 4, 64), 3), *cache, pages, i32([0, 6]), i32([6]), 6, 2 ** 32 + 6, 0, 0, None,
+                              None) is None
+    ok()
