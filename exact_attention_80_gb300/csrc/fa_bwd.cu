@@ -280,7 +280,9 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
 // for the tiles of the sinks, which see every row behind them (16 heads of 8192
 // rows in groups of four, window 1024, 4 sinks, d = 128: a sink tile has 512
 // steps, another 72). Units are ordered tile by tile over all kv heads, the
-// sinks' first.
+// sinks' first. P and dS are rounded to bf16 for their products here as well: the
+// other operands (dO, Q, K) are bf16, which f16 does not hold, and kind::f16 takes
+// both in one type.
 template <int D, bool WIN = false>
 __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
     using L = LayoutBwd<D>;
@@ -821,7 +823,9 @@ constexpr int kFewKeys = 16;
 // a small difference: the rounding of bf16 O then dominates dS (measured on
 // N(0, 1) inputs with two visible keys: dQ, dK off by 3.8e-3 against 2.3e-3).
 // Such a row gets D = sum_j P_j dP_j from q, K, V and dO in fp32, at two dot
-// products per key; from about sixteen keys on the rounding averages out.
+// products per key; from about sixteen keys on the rounding averages out, and D
+// comes from O as in the dense backward (an error of up to 2^-8 sum_c |dO_c O_c|,
+// the larger part of what dQ and dK are off by).
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_win_pre_kernel(const __nv_bfloat16* __restrict__ q,
                                                              const __nv_bfloat16* __restrict__ k,

@@ -10,6 +10,10 @@
 // the later rows' tile has no part in the window tiles that only the earlier
 // rows see (a hole right behind the sinks), and the earlier rows' tile ends
 // before the list does. Heads share kv heads in groups of H / Hkv.
+//
+// P is rounded to bf16 for its product, as in the dense forward: kind::f16 takes
+// both operands in one type, and V as f16 could overflow (as bf16 P a weight is off
+// by up to 2^-8; f16 would be eight times finer). Scores, sums and O are fp32.
 #pragma once
 
 #include "fa_fwd_common.cuh"

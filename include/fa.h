@@ -285,7 +285,8 @@ long long fa_fwd_grid_ctas(int B, int H, int Nq, int d, int num_splits);
  * (with sinks = 0). Rows that see no key (p < 0) get O = 0, LSE = -inf. Only the
  * key tiles a unit's rows see are read. K and V must be finite, as in fa_fwd: a
  * key that some rows of a tile see and others do not is multiplied by zero for
- * the others.
+ * the others. Scores, sums and O are fp32; P enters its product as bf16
+ * (relative rounding 2^-8), the type of V, as in fa_fwd.
  */
 fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
                         int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream);
@@ -307,7 +308,10 @@ fa_status fa_fwd_window_splitkv(const void* q, const void* k, const void* v, voi
  * from q, k, v, the forward's o and lse, and dout; the gradients of a kv head
  * are summed over the query heads of its group in fp32. As fa_bwd otherwise
  * (dQ is summed over key tiles by fp32 atomics, so its last bits can differ
- * between runs). workspace: fa_bwd_window_workspace_bytes, 16-byte aligned.
+ * between runs). P and dS = P (dP - D) enter their products as bf16, the type of
+ * Q, K and dO; D is formed from the bf16 o and dout, or, for rows that see at
+ * most 16 keys, from P and dP in fp32.
+ * workspace: fa_bwd_window_workspace_bytes, 16-byte aligned.
  */
 size_t fa_bwd_window_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks);
 fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -422,14 +426,21 @@ fa_status fa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_
  * The keys of a row block are split into num_splits parts (FA_MAX_SPLITS at
  * most; fa_paged_num_splits proposes a number), whose partial states meet in
  * the workspace (fa_paged_workspace_bytes; none for one split) and are merged
- * by a second launch, or, where they are few, within the first one. Slots behind a sequence's end may hold anything. Queries
- * past cu_seqlens_q[B] are not written. Broken offsets and lengths: that
- * sequence is neither read nor written, FA_ERR_SEQLENS from fa_device_status;
- * a page that is not one of the cache: FA_ERR_PAGES, the sequence's result is
- * undefined. Scores and sums are fp32; Q enters the products as f16 after an
- * exact power-of-two scale per row, P as f16 (relative rounding 2^-11). A query
- * row that holds an infinity or a NaN gives NaN in its O and LSE, and leaves the
- * other rows as they are.
+ * by a second launch, or, where they are few, within the first one. Slots behind
+ * a sequence's end may hold anything. Queries past cu_seqlens_q[B] are not
+ * written. Broken offsets and lengths: that sequence is neither read nor written,
+ * FA_ERR_SEQLENS from fa_device_status; a page that is not one of the cache:
+ * FA_ERR_PAGES, the sequence's result is undefined.
+ * Scores and sums are fp32, P enters its product as f16 (relative rounding
+ * 2^-11). Q enters after an exact power-of-two scale per row:
+ *   - where max_seqlen_q * H / Hkv <= 16 as f16, exact for elements down to
+ *     2^-22 of the row's largest;
+ *   - else as the sum of two e4m3 terms, exact for elements down to 2^-9 of the
+ *     row's largest, and off by at most 2^-17 of that largest one below: with
+ *     columns far above the others (2^8, say) a score moves by up to
+ *     2^-17 max|q| sum|k| scale.
+ * A query row that holds an infinity or a NaN gives NaN in its O and LSE, and
+ * leaves the other rows as they are.
  */
 int fa_paged_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k, int d, int window, int sinks);
 size_t fa_paged_workspace_bytes(int total_q, int H, int d, int num_splits);

@@ -156,3 +156,41 @@ def test_compiled_calls_look_at_the_positions_shape():
     assert fa._compiled.paged(normal((6, 4, 64), 3), *cache, pages, i32([0, 6]), i32([6]), 6, 2 ** 32 + 6, 0, 0, None,
                               None) is None
     ok()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,splits", [(2, 1), (4, 2), (5, 1), (8, 3), (15, 1), (40, 1), (40, 2)])
+@pytest.mark.parametrize("e", [4, 6, 10])
+def test_queries_with_outlier_columns(n, splits, e, d):
+    """Rows whose largest columns lie 2^e above the rest, in every kernel.
+
+    Up to 16 rows a kv head an element of Q is off by nothing here (f16 after a power-of-two scale holds the
+    eight bits of everything down to 2^-24 of the row's largest). From 17 rows on two e4m3 terms hold what is at
+    least 2^-9 of the largest, and are off by at most 2^-10 where the largest lies in [2^7, 2^8): 2^-17 of it.
+    A score is then off by e_j = scale sum_c |dq_c k_jc|, and by its 2 d / 32 accumulations in fp32, each by
+    2^-23 of sum_c |q_c k_jc|. Weights change by a factor of at most exp(2 e), O by (exp(2 e) - 1) sum_j w_j |v_j|,
+    LSE by e, e the largest e_j."""
+    H, Hkv, page, lens = 8, 1, 32, [600, 333]
+    cache, table = cache_of(lens, page, Hkv, d, 5)
+    for s in cache[2:]:
+        s *= 2.0 ** (5 - e)  # scores of about the same size for every e
+    q = normal((2 * n, H, d), n + d)
+    cols = torch.randperm(d, generator=torch.Generator().manual_seed(e))[:3]
+    q[:, :, cols.cuda()] *= 2.0 ** e
+    o, lse = fa.attention_paged_fp8(q, *cache, table, i32([0, n, 2 * n]), i32(lens), n, max(lens), num_splits=splits)
+    ok()
+    ref, ref_lse, a = paged_oracle(q, cache, table, [n, n], lens)
+    Q, scale = np.abs(f64(q)), fa.default_scale(d)
+    top = 2.0 ** np.floor(np.log2(Q.max(2, keepdims=True)))
+    off = np.where(Q < 2.0 ** -9 * top, 2.0 ** -17 * top, 0.0) if n * H > 16 else np.zeros_like(Q)
+    off = off + Q * (2 * d / 32) * 2.0 ** -23
+    err = np.zeros((2 * n, H))
+    for b in range(2):
+        pages = table[b, : -(-lens[b] // page)].long()
+        k = (cache[0][pages, 0].view(torch.float8_e4m3fn).double() * cache[2][pages, 0, None, None].double())
+        k = np.abs(k.reshape(-1, d)[: lens[b]].cpu().numpy())
+        rows = slice(b * n, (b + 1) * n)
+        err[rows] = scale * (off[rows] @ k.T).max(2)
+    bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + np.expm1(2 * err))[:, :, None] * a
+    assert np.all(np.abs(f64(o) - ref) <= bound)
+    assert np.all(np.abs(f64(lse) - ref_lse) <= 5e-4 + err.T)
