@@ -194,3 +194,61 @@ def test_queries_with_outlier_columns(n, splits, e, d):
     bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -10 + np.expm1(2 * err))[:, :, None] * a
     assert np.all(np.abs(f64(o) - ref) <= bound)
     assert np.all(np.abs(f64(lse) - ref_lse) <= 5e-4 + err.T)
+
+
+PLACES = {64: 4 * 152, 128: 3 * 152, 256: 2 * 152}  # CTAs of the 16-row kernel that run at once
+
+
+def check(o, lse, want):
+    ref, ref_lse, a = want
+    assert np.all(np.abs(f64(o) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * a)
+    assert np.all(np.abs(f64(lse) - ref_lse) <= 5e-4)
+
+
+def run_paged(ns, lens, page, H, Hkv, d, splits, window=0, sinks=0, seed=7):
+    assert max(ns) * H // Hkv <= 16  # the kernel for few rows
+    cache, table = cache_of(lens, page, Hkv, d, seed)
+    table[table < 0] = 0
+    q = normal((sum(ns), H, d), seed)
+    # States that no CTA fills hold NaN.
+    ws = torch.full((max(1, fa.fa_paged_workspace_bytes(sum(ns), H, d, splits) // 4),), float("nan"), device="cuda")
+    o, lse = torch.empty_like(q), torch.empty((H, sum(ns)), device="cuda")
+    fa.fa_fwd_paged_fp8(q, *cache, o, lse, table, i32([0] + list(np.cumsum(ns))), i32(lens), max(ns), max(lens), ws, splits,
+                        window, sinks)
+    ok()
+    check(o, lse, paged_oracle(q, cache, table, ns, lens, window, sinks))
+    return ws
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("ns,H,Hkv,page,splits,window,sinks", [
+    ([1, 1, 1, 1, 1], 8, 2, 16, 9, 0, 0), ([1, 0, 1, 1, 1], 4, 4, 64, 16, 0, 0), ([3, 4, 1, 2, 4], 8, 2, 32, 12, 0, 0),
+    ([1, 1, 2, 1, 2], 16, 2, 128, 10, 700, 40),
+])
+def test_few_rows_through_the_workspace(ns, H, Hkv, page, splits, window, sinks, d):
+    """More splits than a cluster holds: states meet in the workspace, some sequences leave one, some all."""
+    assert splits > 8
+    run_paged(ns, [20, 5, 700, 5000, 2049], page, H, Hkv, d, splits, window, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("splits", [2, 5, 8])
+def test_few_rows_of_more_splits_than_places(splits, d):
+    """At most eight splits, but more CTAs than run at once: no clusters."""
+    Hkv = 4
+    B = PLACES[d] // (Hkv * splits) + 1
+    assert B * Hkv * splits > PLACES[d]
+    lens = np.random.default_rng(splits).integers(1, 1500, B)
+    lens[:4] = 1, 16, 1500, 33
+    run_paged([1] * B, [int(x) for x in lens], 16, 8, Hkv, d, splits)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("splits,length,window,sinks", [(1, 5200, 0, 0), (1, 9000, 4700, 40), (1, 8300, 8200, 3000),
+                                                        (3, 14000, 0, 0), (9, 38000, 0, 0)])
+def test_few_rows_over_many_tiles(splits, length, window, sinks, page, d):
+    """More than 32 key tiles a warp: page ids and scales are fetched anew."""
+    keys = 16 if d == 256 else 32  # of a warp's tile; four warps
+    assert (min(length, window or length) // splits) > 4 * 32 * keys
+    run_paged([2, 1], [length, 777], page, 8, 2, d, splits, window, sinks)
