@@ -252,3 +252,26 @@ def test_few_rows_over_many_tiles(splits, length, window, sinks, page, d):
     keys = 16 if d == 256 else 32  # of a warp's tile; four warps
     assert (min(length, window or length) // splits) > 4 * 32 * keys
     run_paged([2, 1], [length, 777], page, 8, 2, d, splits, window, sinks)
+
+
+@pytest.mark.parametrize("new,d,splits", [(1, 64, 4), (1, 128, 1), (1, 256, 2), (1, 128, 12), (4, 128, 8), (10, 128, 3),
+                                          (20, 64, 1), (40, 128, 2), (90, 128, 2), (30, 256, 3)])
+def test_broken_offsets_leave_the_others_their_results(new, d, splits):
+    """Offsets past the tokens or decreasing: the sequences whose offsets are good get their results, the rows of
+    no good sequence keep what they held."""
+    page, Hkv, H, lens = 16, 2, 8, [200, 300, 250]
+    cache, table = cache_of(lens, page, Hkv, d, 31)
+    table[table < 0] = 0
+    q = normal((3 * new, H, d), 4)
+    want = paged_oracle(q, cache, table, [new] * 3, lens)
+    for cu, good in (([0, new, 2 * new, 3 * new + 1], 2), ([0, new, new - 1, 3 * new], 1), ([0, new, 3 * new, 3 * new], 1),
+                     ([0, new, 2 * new, -1], 2)):
+        o = torch.full_like(q, 3.0)
+        lse = torch.full((H, 3 * new), 2.0, device="cuda")
+        ws = torch.empty(max(1, fa.fa_paged_workspace_bytes(3 * new, H, d, splits) // 4), device="cuda")
+        fa.fa_fwd_paged_fp8(q, *cache, o, lse, table, i32(cu), i32(lens), new, 300, ws, splits)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(clear=True) == fa.FA_ERR_SEQLENS
+        rows = good * new
+        check(o[:rows], lse[:, :rows], [want[0][:rows], want[1][:, :rows], want[2][:rows]])
+        assert torch.all(o[rows:] == 3.0) and torch.all(lse[:, rows:] == 2.0)
