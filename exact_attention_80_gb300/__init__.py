@@ -12,6 +12,7 @@ no fallback: if the library is missing or a call fails, an exception says so.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -163,6 +164,29 @@ def _stream_handle(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _allocating(stream, t):
+    """What a call on ``stream`` allocates inside belongs to that stream (None: the current one). Memory of
+    the current stream might still be in use there by work that ``stream`` does not wait for."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
+                             torch.cuda.ExternalStream(int(stream), device=t.device))
+
+
+def _given(stream, *tensors):
+    """Outputs of a call on ``stream``, which the caller uses on the current stream: their memory, once given
+    back, waits for that stream as well."""
+    if stream is not None:
+        import torch
+
+        for t in tensors:
+            if t is not None:
+                t.record_stream(torch.cuda.current_stream(t.device))
+    return tensors
 
 
 def _ptr(t):
@@ -318,17 +342,18 @@ def attention_fp8(q, k, v, q_descale: float = 1.0, k_descale: float = 1.0, v_des
     import torch
 
     B, H, Nq, Nk, d = _bhnd8(q, k, v)
-    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    if num_splits == 1:
-        fa_fwd_fp8(q, k, v, q_descale, k_descale, v_descale, o, lse, causal, scale, stream)
-    else:
-        ws = torch.empty(fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits) // 4,
-                         dtype=torch.float32, device=q.device)
-        fa_fwd_fp8_splitkv(q, k, v, q_descale, k_descale, v_descale, ws, num_splits, causal, scale,
-                           stream)
-        fa_combine(ws, o, lse, B, H, Nq, d, num_splits, stream)
-    return o, lse
+    with _allocating(stream, q):
+        o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        if num_splits == 1:
+            fa_fwd_fp8(q, k, v, q_descale, k_descale, v_descale, o, lse, causal, scale, stream)
+        else:
+            ws = torch.empty(fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits) // 4,
+                             dtype=torch.float32, device=q.device)
+            fa_fwd_fp8_splitkv(q, k, v, q_descale, k_descale, v_descale, ws, num_splits, causal, scale,
+                               stream)
+            fa_combine(ws, o, lse, B, H, Nq, d, num_splits, stream)
+    return _given(stream, o, lse)
 
 
 def fa_bwd_workspace_bytes(B: int, H: int, Nq: int, d: int) -> int:
@@ -364,11 +389,12 @@ def attention_backward(q, k, v, o, lse, dout, causal=False, scale: float | None 
     import torch
 
     B, H, Nq, Nk, d = _bhnd(q, k, v)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = torch.empty(max(1, fa_bwd_workspace_bytes(B, H, Nq, d) // 4), dtype=torch.float32,
-                     device=q.device)
-    fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, ws, causal, scale, stream)
-    return dq, dk, dv
+    with _allocating(stream, q):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(max(1, fa_bwd_workspace_bytes(B, H, Nq, d) // 4), dtype=torch.float32,
+                         device=q.device)
+        fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, ws, causal, scale, stream)
+    return _given(stream, dq, dk, dv)
 
 
 def fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, causal=False,
@@ -412,10 +438,11 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, cau
     :func:`fa_fwd_varlen`. Returns ``(o, lse)``."""
     import torch
 
-    o = torch.empty_like(q)
-    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, causal, scale, stream)
-    return o, lse
+    with _allocating(stream, q):
+        o = torch.empty_like(q)
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        fa_fwd_varlen(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, causal, scale, stream)
+    return _given(stream, o, lse)
 
 
 def fa_splitkv_workspace_bytes(B: int, H: int, Nq: int, d: int, num_splits: int) -> int:
@@ -464,18 +491,19 @@ def attention(q, k, v, causal=False, scale: float | None = None, num_splits: int
     import torch
 
     B, H, Nq, Nk, d = _bhnd(q, k, v)
-    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    if num_splits == 1:
-        fa_fwd(q, k, v, o, lse, causal, scale, stream)
-    else:
-        nbytes = fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits)
-        if nbytes == 0:
-            raise FAError(5, "fa_splitkv_workspace_bytes")
-        ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
-        fa_fwd_splitkv(q, k, v, ws, num_splits, causal, scale, stream)
-        fa_combine(ws, o, lse, B, H, Nq, d, num_splits, stream)
-    return o, lse
+    with _allocating(stream, q):
+        o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        if num_splits == 1:
+            fa_fwd(q, k, v, o, lse, causal, scale, stream)
+        else:
+            nbytes = fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits)
+            if nbytes == 0:
+                raise FAError(5, "fa_splitkv_workspace_bytes")
+            ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
+            fa_fwd_splitkv(q, k, v, ws, num_splits, causal, scale, stream)
+            fa_combine(ws, o, lse, B, H, Nq, d, num_splits, stream)
+    return _given(stream, o, lse)
 
 
 def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
@@ -534,19 +562,6 @@ def _on_stream(index, stream, fn, *args):
         return fn(*args, _raw_stream(index) if stream is None else int(getattr(stream, "cuda_stream", stream)))
     with torch.cuda.device(index):
         return fn(*args, _raw_stream(index) if stream is None else int(getattr(stream, "cuda_stream", stream)))
-
-
-def _used_on(stream, *tensors):
-    """Tensors allocated for a call stay allocated until ``stream`` has passed it
-    (None: the allocating stream, which needs nothing)."""
-    if stream is None:
-        return
-    import torch
-
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream if hasattr(stream, "cuda_stream") else
-                            torch.cuda.ExternalStream(int(stream), device=t.device))
 
 
 def _heads_view(t, name):
@@ -661,9 +676,9 @@ def rope(q, k, table, positions, sections=None, interleaved=False, inverse=False
             if type(out) is int:
                 raise FAError(out, "fa_rope")
             return out
-    q_out, k_out = _rope(q, k, None, None, table, positions, sections, interleaved, inverse, stream)
-    if stream is not None:
-        _used_on(stream, q_out, k_out)
+    with _allocating(stream, q):
+        q_out, k_out = _rope(q, k, None, None, table, positions, sections, interleaved, inverse, stream)
+    _given(stream, q_out, k_out)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -800,10 +815,10 @@ def kv_append_fp8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
             if type(out) is int:
                 raise FAError(out, "fa_kv_append_fp8")
             return None if out is True else out
-    q_out = _append(q, k, v, None, True, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
-                    max_seqlen, table, positions, sections, interleaved, stream)
-    if stream is not None:
-        _used_on(stream, q_out)
+    with _allocating(stream, k):
+        q_out = _append(q, k, v, None, True, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, seqlens_k,
+                        max_seqlen, table, positions, sections, interleaved, stream)
+    _given(stream, q_out)
     return q_out
 
 
@@ -821,7 +836,7 @@ def fa_paged_workspace_bytes(total_q: int, H: int, d: int, num_splits: int) -> i
 def _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
            max_seqlen_k, workspace, num_splits, window, sinks, scale, stream):
     """The checks and the call of fa_fwd_paged_fp8; ``o`` None: outputs and the workspace are
-    allocated (``num_splits`` None: the library's proposal). Returns ``(o, lse, workspace)``."""
+    allocated (``num_splits`` None: the library's proposal). Returns ``(o, lse)``."""
     import torch
 
     index = q.get_device()
@@ -855,7 +870,7 @@ def _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens
                     default_scale(d) if scale is None else scale, window, sinks, num_splits)
     if st != FA_OK:
         raise FAError(st, "fa_fwd_paged_fp8")
-    return o, lse, workspace
+    return o, lse
 
 
 def fa_fwd_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k,
@@ -884,11 +899,10 @@ def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
             if type(out) is int:
                 raise FAError(out, "fa_fwd_paged_fp8")
             return out
-    o, lse, ws = _paged(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
+    with _allocating(stream, q):
+        o, lse = _paged(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
                         max_seqlen_q, max_seqlen_k, None, num_splits, window, sinks, scale, stream)
-    if stream is not None:
-        _used_on(stream, o, lse, ws)
-    return o, lse
+    return _given(stream, o, lse)
 
 
 # ------------------------------------------------ sliding windows, grouped heads
@@ -954,25 +968,24 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
             return out
     import torch
 
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
     if num_splits is None:
         num_splits = fa_window_num_splits(B, H, Hkv, Nq, Nk, d, window, sinks) or 1
-    if num_splits == 1:
-        fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
-        _used_on(stream, o, lse)
-        return o, lse
-    nbytes = fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits)
-    if nbytes == 0:
-        raise FAError(5, "fa_fwd_window_splitkv")
-    ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
-    fa_fwd_window_splitkv(q, k, v, ws, num_splits, window, sinks, scale, stream)
-    st = _on_stream(index, stream, load_library().fa_combine, ws.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Nq, d,
-                    num_splits)
-    _check(st, "fa_combine")
-    _used_on(stream, o, lse, ws)
-    return o, lse
+    with _allocating(stream, q):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        if num_splits == 1:
+            fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
+        else:
+            nbytes = fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits)
+            if nbytes == 0:
+                raise FAError(5, "fa_fwd_window_splitkv")
+            ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
+            fa_fwd_window_splitkv(q, k, v, ws, num_splits, window, sinks, scale, stream)
+            st = _on_stream(index, stream, load_library().fa_combine, ws.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H,
+                            Nq, d, num_splits)
+            _check(st, "fa_combine")
+    return _given(stream, o, lse)
 
 
 def fa_bwd_window_workspace_bytes(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int, window: int,
@@ -1011,12 +1024,12 @@ def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0
     import torch
 
     B, H, Hkv, Nq, Nk, d, _ = _grouped(q, k, v)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     nbytes = fa_bwd_window_workspace_bytes(B, H, Hkv, Nq, Nk, d, window, sinks)
-    ws = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
-    fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, ws, window, sinks, scale, stream)
-    _used_on(stream, dq, dk, dv, ws)
-    return dq, dk, dv
+    with _allocating(stream, q):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
+        fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, ws, window, sinks, scale, stream)
+    return _given(stream, dq, dk, dv)
 
 
 _SIDE_STREAMS = {}
