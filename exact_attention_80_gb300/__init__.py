@@ -867,7 +867,7 @@ def _paged(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens
     st = _on_stream(index, stream, lib.fa_fwd_paged_fp8, q.data_ptr(), cache, page_table.data_ptr(),
                     cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), o.data_ptr(), lse.data_ptr(),
                     workspace.data_ptr() if num_splits > 1 else 0, B, H, n, max_seqlen_q, max_seqlen_k, max_pages,
-                    default_scale(d) if scale is None else scale, window, sinks, num_splits)
+                    default_scale(d) if scale is None else float(scale), window, sinks, num_splits)
     if st != FA_OK:
         raise FAError(st, "fa_fwd_paged_fp8")
     return o, lse
@@ -934,7 +934,7 @@ def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale: float | N
     _check_out(o, "o", (B, H, Nq, d), torch.bfloat16, index)
     _check_out(lse, "lse", (B, H, Nq), torch.float32, index)
     st = _on_stream(index, stream, load_library().fa_fwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                    o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
+                    o.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else float(scale),
                     _int32(window), _int32(sinks))
     _check(st, "fa_fwd_window")
 
@@ -951,7 +951,7 @@ def fa_fwd_window_splitkv(q, k, v, workspace, num_splits: int, window: int, sink
     B, H, Hkv, Nq, Nk, d, index = _grouped(q, k, v)
     _need_workspace(workspace, fa_splitkv_workspace_bytes(B, H, Nq, d, num_splits), "workspace", q.device)
     st = _on_stream(index, stream, load_library().fa_fwd_window_splitkv, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
+                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else float(scale),
                     _int32(window), _int32(sinks), _int32(num_splits))
     _check(st, "fa_fwd_window_splitkv")
 
@@ -1007,7 +1007,7 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sin
                     q.device)
     st = _on_stream(index, stream, load_library().fa_bwd_window, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                     o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else scale,
+                    workspace.data_ptr(), B, H, Hkv, Nq, Nk, d, default_scale(d) if scale is None else float(scale),
                     _int32(window), _int32(sinks))
     _check(st, "fa_bwd_window")
 

@@ -111,3 +111,24 @@ def test_positions_of_another_shape_are_refused(stub):
         with pytest.raises(ValueError):
             call()
     assert len(stub.calls) == n
+
+
+def test_scales_and_numbers_of_other_types(stub):
+    """A scale may be any number that float() takes, as in the dense calls; an int any that is one."""
+    np = pytest.importorskip("numpy")
+    q, k = bf(1, 4, 9, 64), bf(1, 2, 12, 64)
+    o, lse, ws = q.clone(), torch.zeros(1, 4, 9), torch.zeros(1 << 16)
+    t, c, batch = bf(6, 4, 64), cache_args(), [i32(3, 4), i32(4), i32(3)]
+    for scale in (0.25, np.float32(0.25), np.float64(0.25), torch.tensor(0.25), 1):
+        for n in (5, np.int64(5), np.int32(5)):
+            fa.fa_fwd_window(q, k, k, o, lse, n, scale=scale)
+            fa.fa_fwd_window_splitkv(q, k, k, ws, 2, n, scale=scale)
+            fa.attention_window(q, k, k, n, scale=scale)
+            fa.attention_window_backward(q, k, k, o, lse, o, n, scale=scale)
+            fa.attention_paged_fp8(t, *c, *batch, 2, 60, n, scale=scale)
+        for _, args in stub.calls:
+            assert sum(type(a) is float and a == float(scale) for a in args) == 1
+        stub.calls.clear()
+    for call in (lambda: fa.attention_window(q, k, k, 5, scale="0.25x"), lambda: fa.attention_window(q, k, k, 5, scale=[1])):
+        with pytest.raises((TypeError, ValueError)):
+            call()
