@@ -40,8 +40,9 @@ namespace {
 // Time of a call in steps of a CTA (one key tile, about 1.1 us): its waves of CTAs,
 // four steps for a CTA's start and end, and for split keys the second launch and
 // the partial states, which are written and read. Few rows over many keys leave
-// most SMs idle otherwise (one row of 8 heads of 64 over 4096 keys: 36 us in one
-// part, 9.6 in sixteen; 2 heads of 4096 rows, no window: 41 us, 28 in four).
+// most SMs idle otherwise (one row of 8 heads of 64 over 4096 keys, replayed from a
+// graph: 36 us in one part, 9.2 in sixteen; 2 heads of 4096 rows, no window: 42 us,
+// 29 in four).
 int window_splits(long long units, long long tiles, long long rows, int d, int sms) {
     if (units >= sms) return 1;
     long long best = 1;
@@ -109,8 +110,8 @@ fa_status window_forward(const void* q, const void* k, const void* v, void* o, f
     // Persistent CTAs where the units fill at least four waves (three if they list
     // four key tiles at most) and list few key tiles, as for the dense forward: the
     // start and end of a unit overlap its neighbours' (2 x 32 heads of 8192, d = 64,
-    // us, persistent and not: window 1024 and 4 sinks 204 and 214, window 128 74 and
-    // 103; 16 heads, d = 128, 3.4 waves: 76 and 74, window 128 28 and 34).
+    // us, persistent and not: window 1024 and 4 sinks 206 and 216, window 128 76 and
+    // 105; 16 heads, d = 128, 3.4 waves: 77 and 76, window 128 29 and 35).
     const long long listed =
         window > 0 ? std::min<long long>((Nk + 127) / 128, (window + 126) / 128 + 2 + (sinks + 127) / 128)
                    : (Nk + 127) / 128;

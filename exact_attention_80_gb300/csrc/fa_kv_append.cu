@@ -135,8 +135,8 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : SPLIT && PER ==
     if (threadIdx.x == 0) griddep_launch_dependents();
     // Item blocks are spread evenly among the query blocks: items wait for long
     // chains of loads, queries for bandwidth, so each fills the other's gaps
-    // (six ragged prompts of 4001 tokens, 32 + 2 * 8 heads, d = 128: 87 us; the
-    // items alone take 47, the queries 52).
+    // (six ragged prompts of 4001 tokens, 32 + 2 * 8 heads, d = 128: 83 us; the
+    // items alone took 47, the queries 52, when both took 87).
     const unsigned long long total_blocks = gridDim.x;
     const unsigned before = static_cast<unsigned>(blockIdx.x * static_cast<unsigned long long>(p.item_blocks) / total_blocks);
     const unsigned after =

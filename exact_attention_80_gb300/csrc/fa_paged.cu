@@ -65,11 +65,12 @@ constexpr int kClusterSplits = 8;  // splits that can be a cluster (the portable
 // Keys of a warp's tile, and CTAs an SM holds. A warp's tile is a chain of
 // dependent steps, so throughput comes from the warps beside it: short tiles and
 // two- or three-slot rings, for as many CTAs as the registers allow. Measured on
-// 64 contexts of 8192 to 32768 tokens (32 at d = 256, up to 16384), TB/s:
-//   d = 64:  two CTAs of six-slot rings 3.4, three 4.5, four 5.0, five 4.8; tiles
-//            of 64 keys, three CTAs, 4.8
-//   d = 128: two CTAs of three-slot rings 5.7, three of two slots 6.5
-//   d = 256: tiles of 32 keys, one CTA, 4.7; of 16 keys, two CTAs, 5.6
+// 64 contexts of 8192 to 32768 tokens (32 of 4096 to 16384 at d = 256), 32 + 8 heads,
+// TB/s:
+//   d = 64:  two CTAs of six-slot rings 3.4, three of four 4.2, four of three 4.8,
+//            five of two 4.6; tiles of 64 keys, three CTAs, 4.6
+//   d = 128: two CTAs of three-slot rings 5.7, three of two slots 6.3
+//   d = 256: tiles of 32 keys, one CTA, 4.5; of 16 keys, two CTAs, 5.5
 __host__ __device__ constexpr int rows_keys(int d) { return d == 256 ? 16 : 32; }
 __host__ __device__ constexpr int rows_ctas(int d) { return d == 64 ? 4 : d == 128 ? 3 : 2; }
 template <int D>
@@ -167,8 +168,8 @@ __device__ __forceinline__ void cluster_meet() {
 
 // CLUSTER: the splits of a unit are a cluster, whose CTAs read one another's
 // states at the end: no workspace traffic and no second launch (one token for 8
-// heads of 64 over 516 keys, five splits: 7.0 us against 7.9 through the workspace,
-// replayed from a graph; 11.3 with one split). Every CTA of a cluster comes to both
+// heads of 64 over 516 keys, five splits: 6.1 us against 7.4 through the workspace,
+// replayed from a graph; 9.5 with one split). Every CTA of a cluster comes to both
 // of its meetings, whatever it found.
 template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
@@ -753,9 +754,10 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
     Plan c;
     const long long rows = static_cast<long long>(max_q) * G;
     // The tensor-core kernel from 17 rows on. One block of 16 rows is no slower here,
-    // two, which read K and V twice, are (16 sequences over up to 16200 keys, us here
-    // and there: 16 rows 87 and 84 at d = 128, 55 and 62 at d = 64; 20 rows 128 and
-    // 87, 94 and 64; 16 of up to 8000 at d = 256, 40 rows: 75 and 40).
+    // two, which read K and V twice, are (32 + 8 heads, 16 sequences of 4600 to 16200
+    // keys, us here and there: 16 rows 87 and 85 at d = 128, 61 and 69 at d = 64; 20
+    // rows 132 and 87, 93 and 70; of 2000 to 8000 keys at d = 256: 16 rows 94 and 113,
+    // 20 rows 137 and 113, 40 rows 202 and 114).
     c.tc = rows > kRows;
     c.dual = c.tc && rows <= kTcRows && d <= 128;
     c.block_rows = !c.tc ? kRows : c.dual || d == 256 ? kTcRows : 2 * kTcRows;
@@ -772,22 +774,28 @@ Plan plan_of(int G, int max_q, int max_k, int d, int window, int sinks) {
 
 // Splits that finish earliest, in rounds of 128 keys; a CTA's start and end cost
 // about two, leaving and merging partial states some more. While the CTAs leave half
-// of the places free, only the longest one counts, and the merge costs two rounds, or half a one in a cluster (one
-// token for 8 heads of 64 over 512 keys: 11.3 us with one split, 7.9 with three, 7.0
-// with five; four contexts of up to 700: 11.9 and 6.8 with six). One sequence in several waves: CTAs of equal
-// length. Several sequences: their lengths differ, so the longest CTA
-// comes on top of an even share of all of them, at two thirds of the longest
-// length (measured: 64 contexts of 8192 to 32768, 512 units: 600 us with one
-// split, 511 with three, 480 with eight; one of 131072, 8 units: 52 us in one
-// wave of splits, 74 in four).
+// of the places free, only the longest one counts, and the merge costs two rounds,
+// or half a one in a cluster (replayed from a graph, one token for 8 heads of 64 over
+// 516 keys: 9.5 us with one split, 7.1 with three, 6.1 with five; four contexts of
+// up to 700: 11.5 and 6.6 with six). One sequence in several waves: CTAs of equal
+// length. Several sequences: their lengths differ, so the longest CTA comes on top
+// of an even share of all of them, at two thirds of the longest length (64 contexts
+// of 8192 to 32768, 512 units: 582 us with one split, 479 with three, 426 with eight,
+// 438 with the 16 proposed; all of 20480, 542, 429, 415, and 423 with the ten
+// proposed; one of 131072, 8 units: 55 us in one wave of splits, 80 in four).
 //
-// Pairs of slots (dual): a CTA takes pieces of whatever length balances the
-// sequences at hand (tc_piece), so only the most pieces of a sequence are chosen
-// here: an even share of all of them, ten rounds a piece for its start and end,
-// and half a piece for the last ones, with sequences at two thirds of the longest
-// on average (five drafted tokens, pieces of the longest and us: 16 contexts of up
-// to 16200 keys, 1: 103, 2: 104, 3: 86, 4: 89; 64 of 32768, 1: 543, 2: 528, 3: 547; 80 of
-// 8192, 1: 193, 2: 228; 2 of 16200, 8: 24.3, 10: 24.2, 12: 27.0).
+// Pairs of slots (dual): of 2 to 64 sequences (kTcBalance) a CTA takes pieces of
+// whatever length balances those at hand (tc_piece), so only the most pieces of a
+// sequence are chosen here: an even share of all of them, ten rounds a piece for its
+// start and end, and half a piece for the last ones, with sequences at two thirds of
+// the longest on average (five drafted tokens, pieces of the longest and us: 16
+// contexts of 4600 to 16200 keys, 1: 103, 2: 104, 3: 87, 4: 90; 64 of up to 32768, 1:
+// 535, 2: 529, 3: 561; 80 of 8192, 1: 195, 2: 229; 2 of 16200, 8: 26, 10: 25, 12: 28).
+// Lengths are not known here: sequences of one length would rather stay whole (16 of
+// 10125 keys, 1: 71, the three proposed: 83; of 16200, 106 and 117), and a bound above
+// the lengths at hand cuts them more coarsely than they need (one token for one
+// sequence of 8192 keys: 18 us at a bound of 8192, 25 at 32768, 34 at 131072; for 16:
+// 66, 72, 83).
 int best_splits(int B, long long units, long long rounds, int slots, bool dual, bool many_rows) {
     if (dual && B > 1) {
         int best = 1;
@@ -801,7 +809,7 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
         return best;
     }
     // (Partial sums of 256 rows cost more than they even out: two chunks of 2048
-    // tokens over 16384 keys, 341 us with one split, 430 with four.)
+    // tokens over 16384 keys, 398 us with one split, 477 with four.)
     if (many_rows && units >= slots) return 1;
     // (A split of less than one round leaves warps idle, of less than two a slot.)
     const long long most =

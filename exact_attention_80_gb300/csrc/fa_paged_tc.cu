@@ -25,15 +25,15 @@
 // warps take their share of a tile's columns with weights of zero for the others:
 // the MMAs cost the same, and four warps rather than one form a tile's
 // exponentials (five drafted tokens, 20 rows, for 64 contexts of up to 32768 keys:
-// 528 us, a fifth less than without shares; for one of 131072: 57).
+// 529 us, a fifth less than without shares; for one of 131072: 58).
 //
 // D = 256 (WIDE): O takes half of TMEM, so a CTA owns one tile of 128 rows, and S
 // has two buffers: the tensor core forms S of tile j + 2 behind PV of tile j while
 // the softmax (four warps) is at tile j + 1. Eight warps convert V, whose f16 form
 // has one buffer: a tile is converted while S takes the tensor core (chunks of 1024
-// tokens over 8192 keys, 16 + 2 heads: 190 us, 1300 TFLOP/s; 1283 us with 16 rows
-// per CTA in the other kernel; 40 rows over 16 contexts of up to 8000 keys: 40 us
-// against 75).
+// tokens over 8192 keys, 16 + 2 heads: 197 us, 1300 TFLOP/s; 1216 us with 16 rows
+// per CTA in the other kernel; 40 rows a kv head, 32 + 8 heads, over 16 contexts of
+// up to 8000 keys: 114 us against 202).
 //
 // Roles, by warp: 0 producer (Q is written by the softmax threads; K and V pages
 // by TMA into two rings), 1 issuer, 2-3 idle, 4-11 softmax (thread = row = TMEM
@@ -761,8 +761,8 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     // exponentials) in loops that are not unrolled: where few warps
                     // run this code, long straight stretches of it wait for their
                     // instructions (20 rows without shares: 120 us against 140; the
-                    // other way round for full tiles, 2 x 2048 tokens over 16384
-                    // keys: 395 against 328).
+                    // other way round for full tiles, 2048 and 1642 tokens over 16384
+                    // and 9967 keys: 395 against 328).
                     const bool whole = __all_sync(0xffffffffu, valid >= BN && (p.window <= 0 || valid <= p.window ||
                                                                                 p.sinks - key0 >= BN));
                     auto chunk = [&](int cc, float (&s)[32], float (&kc)[2], float (&vc)[2]) {
