@@ -507,7 +507,7 @@ const char* fa_status_string(fa_status status) {
         case FA_ERR_CAUSAL:
             return "FA_ERR_CAUSAL: causal must be FA_CAUSAL_NONE, _TOP_LEFT or _BOTTOM_RIGHT";
         case FA_ERR_SEQLENS:
-            return "FA_ERR_SEQLENS: cu_seqlens are not a valid partition (see fa_fwd_varlen)";
+            return "FA_ERR_SEQLENS: cu_seqlens are not a valid partition, or a cache length is out of range";
         case FA_ERR_TILE:
             return "FA_ERR_TILE: rows_per_cta is not offered for this head dim (see fa_fwd_rows)";
         case FA_ERR_PAGES:

@@ -376,7 +376,8 @@ fa_status fa_rope(const fa_rope_tensor* q, const fa_rope_tensor* k, const fa_rot
  * fa_fwd_paged_fp8 takes any scales in that range, and a smaller V scale (zero,
  * for a block of zeros) as 2^-100. The V scales that carry a row's weight should
  * lie within 2^100 of one another: a key's weight is held relative to the largest
- * weight times V scale of its row. Cached values must be finite.
+ * weight times V scale of its row. Cached values must be finite (a value that is NaN
+ * may reach rows that do not see its key: they multiply it by zero).
  */
 typedef struct {
     void* k;
@@ -393,7 +394,7 @@ typedef struct {
  *   v_stride, q_stride elements apart, heads d apart), q_out [total_new][H][d]
  *   bf16 (written, contiguous). q and q_out may both be NULL.
  *   cu_seqlens int32 [B + 1]: sequence b brings tokens cu_seqlens[b] ..
- *   cu_seqlens[b + 1] - 1 (at most max_new); seqlens_k int32 [B]: its cache
+ *   cu_seqlens[b + 1] - 1 (at most max_new <= total_new); seqlens_k int32 [B]: its cache
  *   length with them, so they take cache positions seqlens_k[b] - n .. - 1.
  *   rope: as above, positions [axes][total_new]; positions NULL means the
  *   cache positions (one axis); rope NULL appends without a rotation.
@@ -422,7 +423,8 @@ fa_status fa_kv_append_fp8(const void* q, const void* k, const void* v, void* q_
  *   h / (H / Hkv). Sequence b's queries are its last tokens: query i of n is at
  *   position p = seqlens_k[b] - n + i and sees key j iff j <= p and
  *   (window = 0, or j > p - window, or j < sinks).
- *   seqlens_k[b] <= max_seqlen_k <= max_pages * page_size.
+ *   seqlens_k[b] <= max_seqlen_k <= max_pages * page_size, a sequence's
+ *   queries <= max_seqlen_q <= total_q.
  * The keys of a row block are split into num_splits parts (FA_MAX_SPLITS at
  * most; fa_paged_num_splits proposes a number), whose partial states meet in
  * the workspace (fa_paged_workspace_bytes; none for one split) and are merged

@@ -131,3 +131,30 @@ def test_workspaces_last_until_their_stream_has_passed(calls, busy, name, handle
     assert fa.fa_device_status(clear=True) == fa.FA_OK
     same(name, got, want)
     assert all(torch.isnan(x).all() for x in junk), name
+
+
+@pytest.mark.parametrize("name", ["rope", "paged splits", "window splits", "window backward", "dense splits"])
+def test_captured_on_a_forked_stream(calls, name):
+    """A capture that forks to another stream: what the call allocates there belongs to the graph."""
+    want = calls[name](None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    calls[name](side)  # warm-up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = calls[name](side)
+        here.wait_stream(side)
+        again = calls[name](here)
+    junk = [torch.full((1 << n,), math.nan, device="cuda") for n in range(16, 26)]
+    for _ in range(2):
+        for x in (*tensors(got), *tensors(again)):
+            x.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(clear=True) == fa.FA_OK
+        same(name, got, want)
+        same(name, again, want)
+    assert all(torch.isnan(x).all() for x in junk)

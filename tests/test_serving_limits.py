@@ -275,3 +275,48 @@ def test_broken_offsets_leave_the_others_their_results(new, d, splits):
         rows = good * new
         check(o[:rows], lse[:, :rows], [want[0][:rows], want[1][:, :rows], want[2][:rows]])
         assert torch.all(o[rows:] == 3.0) and torch.all(lse[:, rows:] == 2.0)
+
+
+@pytest.mark.parametrize("n,H,d,window,sinks", [(1, 8, 64, 0, 0), (1, 8, 128, 500, 4), (2, 16, 256, 0, 0), (5, 8, 128, 0, 0),
+                                                (40, 8, 64, 0, 0), (90, 8, 128, 300, 20), (30, 8, 256, 0, 0)])
+def test_captured_steps_while_the_sequences_grow(n, H, d, window, sinks):
+    """One capture of an append and the attention under a fixed bound, replayed while the batch's lengths, its
+    offsets and its pages change: the results of the lengths at hand."""
+    Hkv, page, bound, B = 2, 32, 4096, 3
+    per = bound // page
+    g = torch.Generator().manual_seed(n)
+    pages = torch.randperm(B * per, generator=g).to(torch.int32).view(B, per).cuda()
+    cache = [torch.zeros((B * per, Hkv, page, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.ones((B * per, Hkv), device="cuda") for _ in range(2)]
+    # The cache holds every token already: rows behind a sequence's end are other values.
+    fill = normal((B * bound, Hkv, d), 1), normal((B * bound, Hkv, d), 2)
+    fa.kv_append_fp8(None, *fill, *cache, pages, i32([0, bound, 2 * bound, 3 * bound]), i32([bound] * B), bound)
+    total = B * n
+    q, k, v = normal((total, H, d), 3), normal((total, Hkv, d), 4), normal((total, Hkv, d), 5)
+    table, cu, lens = pages.clone(), i32([0, n, 2 * n, 3 * n]), i32([n] * B)
+    ang = torch.rand((bound, d // 2), generator=g).cuda()
+    cs = torch.cat([ang.cos(), ang.sin()], 1)
+
+    def step():
+        qr = fa.kv_append_fp8(q, k, v, *cache, table, cu, lens, n, table=cs)
+        return (qr, *fa.attention_paged_fp8(qr, *cache, table, cu, lens, n, bound, window, sinks))
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qr, o, lse = step()
+    rng = np.random.default_rng(n)
+    for i, top in enumerate((n, n + 1, 40 + n, 129 + n, 700, 2000, bound)):
+        ls = [top, max(n, top // 3), int(rng.integers(n, max(n, top) + 1))]
+        ns = [n, 0, max(1, n - 1)] if i % 2 else [n, n, n]
+        at = [0] + [int(x) for x in np.cumsum(ns)]
+        table.copy_(pages[torch.tensor([i % 3, (i + 1) % 3, (i + 2) % 3], device="cuda")])
+        cu.copy_(i32(at))
+        lens.copy_(i32(ls))
+        o.fill_(9.0)
+        lse.fill_(9.0)
+        graph.replay()
+        ok()
+        rows = at[-1]
+        check(o[:rows], lse[:, :rows], paged_oracle(qr[:rows], cache, table, ns, ls, window, sinks))
+        assert torch.all(o[rows:] == 9.0) and torch.all(lse[:, rows:] == 9.0)
