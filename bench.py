@@ -196,10 +196,13 @@ def measured_peaks():
         return FALLBACK_BF16_TFLOPS, FALLBACK_HBM_GBS, "fallback"
 
 
-# Sources that do not build or launch the forward kernels (the split merge, the
-# allocation-free wrapper, the backward): a change there leaves their recorded
-# DRAM traffic valid.
-NOT_FORWARD = ("fa_combine.cu", "fa_noalloc.cu", "fa_bwd.cu")
+# Sources that do not build or launch the dense forward kernels (the split merge, the
+# allocation-free wrapper, the backward, and the rotation's, the paged cache's and the
+# window's own): a change there leaves their recorded DRAM traffic valid. (What the
+# window changes inside the forward kernels is in fa_fwd_win.cuh, which counts.)
+NOT_FORWARD = ("fa_combine.cu", "fa_noalloc.cu", "fa_bwd.cu", "fa_launch.h", "fa_rope.cu", "fa_rope.cuh",
+               "fa_kv_append.cu", "fa_paged.cu", "fa_paged.cuh", "fa_paged_phases.h", "fa_paged_tc.cu",
+               "fa_fwd_window.cu")
 
 
 def kernel_source_hash() -> str:
