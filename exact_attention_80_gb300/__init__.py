@@ -173,8 +173,10 @@ def _allocating(stream, t):
         return contextlib.nullcontext()
     import torch
 
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else
-                             torch.cuda.ExternalStream(int(stream), device=t.device))
+    if not hasattr(stream, "cuda_stream"):  # a handle; ExternalStream takes 0 for none at all
+        stream = (torch.cuda.default_stream(t.device) if int(stream) in (0, 1) else
+                  torch.cuda.ExternalStream(int(stream), device=t.device))
+    return torch.cuda.stream(stream)
 
 
 def _given(stream, *tensors):

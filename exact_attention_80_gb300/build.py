@@ -65,7 +65,8 @@ def build_calls() -> str | None:
     if not os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")):
         return None
     with open(os.path.join(torch, "version.py"), encoding="utf-8") as f:
-        version = re.search(r"^__version__ *(?::.*?)?= *['\"](.*?)['\"]", f.read(), re.M).group(1)
+        version = re.search(r"^__version__ *(?::.*?)?= *['\"](.*?)['\"]", f.read(), re.M)
+    version = version.group(1) if version else "an unknown version"  # (which the binding will not take)
     inc, tmp = os.path.join(torch, "include"), CALLS + ".tmp"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", f'-DFA_TORCH_VERSION="{version}"',

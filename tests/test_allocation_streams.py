@@ -133,6 +133,29 @@ def test_workspaces_last_until_their_stream_has_passed(calls, busy, name, handle
     assert all(torch.isnan(x).all() for x in junk), name
 
 
+@pytest.mark.parametrize("name", NAMES)
+def test_the_default_stream_by_its_handle(calls, busy, name):
+    """Handle 0 is the default stream: the call's memory is that stream's, whatever the current one still reads."""
+    want = calls[name](None)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        held = [torch.full_like(x, 3.0) for x in tensors(want)]
+        torch.cuda.synchronize()
+        busy()
+        copies = [x.clone() for x in held]
+        del held
+        got = calls[name](0)
+        with torch.cuda.stream(torch.cuda.default_stream()):
+            # Memory of the default stream's that the call gave back follows it in order.
+            junk = [torch.full((1 << n,), math.nan, device="cuda") for n in range(16, 27)]
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_OK
+    assert all(torch.all(x == 3.0) for x in copies) and all(torch.isnan(x).all() for x in junk)
+    same(name, got, want)
+
+
 @pytest.mark.parametrize("name", ["rope", "paged splits", "window splits", "window backward", "dense splits"])
 def test_captured_on_a_forked_stream(calls, name):
     """A capture that forks to another stream: what the call allocates there belongs to the graph."""

@@ -320,3 +320,42 @@ def test_captured_steps_while_the_sequences_grow(n, H, d, window, sinks):
         rows = at[-1]
         check(o[:rows], lse[:, :rows], paged_oracle(qr[:rows], cache, table, ns, ls, window, sinks))
         assert torch.all(o[rows:] == 9.0) and torch.all(lse[:, rows:] == 9.0)
+
+
+@pytest.mark.parametrize("n,d", [(1, 64), (2, 128), (6, 128), (50, 64), (40, 256)])
+def test_sequences_that_share_pages(n, d):
+    """Three sequences with the same first pages, and one named twice: the bits of the call on copies of them."""
+    H, Hkv, page, lens = 8, 2, 16, [170, 300, 170, 64 + n]
+    cache, table = cache_of(lens, page, Hkv, d, 9)
+    shared = 64 // page
+    for b in (1, 3):
+        table[b, :shared] = table[0, :shared]
+    table[2] = table[0]
+    own = [torch.empty((sum(-(-x // page) for x in lens), *x.shape[1:]), dtype=x.dtype, device="cuda") for x in cache]
+    apart, at = torch.full_like(table, -1), 0
+    for b, length in enumerate(lens):
+        used = -(-length // page)
+        for x, y in zip(own, cache):
+            x[at: at + used] = y[table[b, :used].long()]
+        apart[b, :used] = torch.arange(at, at + used, device="cuda")
+        at += used
+    q = normal((4 * n, H, d), 2)
+    batch = (i32([i * n for i in range(5)]), i32(lens), n, max(lens))
+    for splits in (1, 3):
+        x, y = (fa.attention_paged_fp8(q, *c, t, *batch, num_splits=splits) for c, t in ((cache, table), (own, apart)))
+        ok()
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+def test_scales_of_other_number_types():
+    """A scale that float() takes gives the bits of the float."""
+    q, k, v = normal((1, 4, 70, 64), 1), normal((1, 2, 90, 64), 2), normal((1, 2, 90, 64), 3)
+    cache, table = cache_of([90], 16, 2, 64, 1)
+    p = normal((3, 4, 64), 4)
+    for scale in (np.float32(0.25), np.float64(0.25), torch.tensor(0.25)):
+        for n in (20, np.int64(20)):
+            for f in (lambda s, n: fa.attention_window(q, k, v, n, scale=s),
+                      lambda s, n: fa.attention_paged_fp8(p, *cache, table, i32([0, 3]), i32([90]), 3, 90, n, scale=s)):
+                x, y = f(scale, n), f(0.25, 20)
+                ok()
+                assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
