@@ -105,6 +105,8 @@ def load_library() -> ctypes.CDLL:
     lib.fa_bwd_window_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, i, vp]
     lib.fa_bwd_window.restype = i
+    lib.fa_fwd_packed.argtypes = [vp, vp, vp, vp, vp, packed, i, i, i, ll, ll, ll, f, i, i, i, vp]
+    lib.fa_fwd_packed.restype = i
     lib.fa_fwd_grid_ctas.argtypes = [i, i, i, i, i]
     lib.fa_fwd_grid_ctas.restype = ctypes.c_longlong
     lib.fa_device_status.argtypes = [vp, i]
@@ -1032,6 +1034,65 @@ def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0
         ws = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
         fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, ws, window, sinks, scale, stream)
     return _given(stream, dq, dk, dv)
+
+
+# ------------------------------------------------------------- packed sequences
+_PACKED_BATCH = struct.Struct("PPiiiii")  # fa_packed_batch
+
+
+def _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k):
+    """(fa_packed_batch, total_q, total_k, H, Hkv, d, token strides of q, k and v, device index) of a
+    packed batch."""
+    import torch
+
+    index = q.get_device()
+    n, H, d, qs = _tokens_view(q, "q", index)
+    m, Hkv, kd, ks = _tokens_view(k, "k", index)
+    vm, vh, vd, vs = _tokens_view(v, "v", index)
+    if (kd, vm, vh, vd) != (d, m, Hkv, d):
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
+    for t, name in ((cu_seqlens_q, "cu_seqlens_q"), (cu_seqlens_k, "cu_seqlens_k")):
+        if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name} must be contiguous int32 [B+1] on device {index}")
+    B = cu_seqlens_q.shape[0] - 1
+    if B < 1 or cu_seqlens_k.shape[0] != B + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must both have B+1 >= 2 entries")
+    batch = _PACKED_BATCH.pack(cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), _int32(B), _int32(n), _int32(m),
+                               _int32(max_seqlen_q), _int32(max_seqlen_k))
+    return batch, n, m, H, Hkv, d, (qs, ks, vs), index
+
+
+def fa_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, window: int = 0,
+                  sinks: int = 0, scale: float | None = None, fill: bool = False, stream=None):
+    """Causal attention over packed sequences (include/fa.h, fa_fwd_packed): ``q`` bf16 [total_q, H, d],
+    ``k`` and ``v`` [total_k, Hkv, d], H a multiple of Hkv, whose tokens may be strided (a fused
+    projection's rows), into caller-owned ``o`` bf16 [total_q, H, d] and ``lse`` fp32 [H, total_q].
+    ``cu_seqlens_*`` int32 [B+1] on the device, ``max_seqlen_*`` the longest sequence's tokens. Rows
+    that belong to no sequence stay as they are, or, with ``fill``, get 0 and -inf."""
+    import torch
+
+    batch, n, _, H, Hkv, d, strides, index = _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
+    _check_out(o, "o", (n, H, d), torch.bfloat16, index)
+    _check_out(lse, "lse", (H, n), torch.float32, index)
+    st = _on_stream(index, stream, load_library().fa_fwd_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    o.data_ptr(), lse.data_ptr(), batch, H, Hkv, d, *strides,
+                    default_scale(d) if scale is None else float(scale), _int32(window), _int32(sinks),
+                    1 if fill else 0)
+    _check(st, "fa_fwd_packed")
+
+
+def attention_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_seqlen_k: int, window: int = 0,
+                     sinks: int = 0, scale: float | None = None, stream=None):
+    """:func:`fa_fwd_packed` into new outputs. Returns ``(o, lse)``; rows that belong to no sequence
+    are 0 and -inf."""
+    import torch
+
+    with _allocating(stream, q):
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        fa_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window, sinks, scale,
+                      True, stream)
+    return _given(stream, o, lse)
 
 
 _SIDE_STREAMS = {}

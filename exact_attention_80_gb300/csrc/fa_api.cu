@@ -124,7 +124,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // rows (d = 64), which take a 64-byte box and the 64-byte swizzle.
 bool encode_map(CUtensorMap* map, const void* base, int d, long long rows, long long heads,
                 unsigned long long row_stride, unsigned long long head_stride, int box_rows,
-                bool bytes = false) {
+                bool bytes = false, int box_heads = 1) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
@@ -132,7 +132,8 @@ bool encode_map(CUtensorMap* map, const void* base, int d, long long rows, long 
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride),
                                    static_cast<cuuint64_t>(head_stride)};
     const bool row64 = bytes && d == 64;
-    const cuuint32_t box[3] = {bytes ? (row64 ? 64u : 128u) : 64u, static_cast<cuuint32_t>(box_rows), 1u};
+    const cuuint32_t box[3] = {bytes ? (row64 ? 64u : 128u) : 64u, static_cast<cuuint32_t>(box_rows),
+                               static_cast<cuuint32_t>(box_heads)};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     const CUresult r =
         enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
@@ -159,6 +160,18 @@ bool encode_rows_map8(CUtensorMap* map, const void* base, int d, int N, int BH, 
 bool encode_tokens_map(CUtensorMap* map, const void* base, int d, int total, int H, int box_rows) {
     return encode_map(map, base, d, total, H, static_cast<unsigned long long>(H) * d * 2,
                       static_cast<unsigned long long>(d) * 2, box_rows);
+}
+
+// The same with tokens `stride` elements apart.
+bool encode_strided_tokens_map(CUtensorMap* map, const void* base, int d, int total, int H, long long stride,
+                               int box_rows) {
+    return encode_map(map, base, d, total, H, static_cast<unsigned long long>(stride) * 2,
+                      static_cast<unsigned long long>(d) * 2, box_rows);
+}
+bool encode_token_heads_map(CUtensorMap* map, const void* base, int d, int total, int H, long long stride, int heads,
+                            int tokens) {
+    return encode_map(map, base, d, H, total, static_cast<unsigned long long>(d) * 2,
+                      static_cast<unsigned long long>(stride) * 2, heads, false, tokens);
 }
 
 bool valid_causal(int causal) {

@@ -25,14 +25,17 @@ using FwdLayout = std::conditional_t<D == 256, LayoutTP<D>, LayoutTM<D>>;
 // persistent CTAs (plain mode). All are forms of the two-tile kernel
 // (d = 64 or 128), but for e4m3 at d = 256.
 // M64: one 64-row query tile per CTA (bf16, d = 64 or 128). WIN: sliding window
-// with sinks and grouped heads (bf16).
-template <int D, bool F8 = false, bool DUAL = false, bool PERSIST = false, bool M64 = false, bool WIN = false>
+// with sinks and grouped heads (bf16). PACK: the same on packed sequences.
+template <int D, bool F8 = false, bool DUAL = false, bool PERSIST = false, bool M64 = false, bool WIN = false,
+          bool PACK = false>
 cudaError_t launch_fwd(const FwdParams& p, unsigned grid, cudaStream_t stream) {
     using L = std::conditional_t<
         PERSIST, LayoutTM<D, F8, true>,
         std::conditional_t<F8, std::conditional_t<D == 256, LayoutTP<D, true>, LayoutTM<D, true>>, FwdLayout<D>>>;
     constexpr auto kernel = [] {
-        if constexpr (WIN && D == 256) return fa_fwd_tpw_kernel<D>;
+        if constexpr (PACK && D == 256) return fa_fwd_tppack_kernel<D>;
+        else if constexpr (PACK) return fa_fwd_tmpack_kernel<D>;
+        else if constexpr (WIN && D == 256) return fa_fwd_tpw_kernel<D>;
         else if constexpr (WIN && PERSIST) return fa_fwd_tmwp_kernel<D>;
         else if constexpr (WIN) return fa_fwd_tmw_kernel<D>;
         else if constexpr (M64) return fa_fwd_tm64_kernel<D>;

@@ -1,0 +1,201 @@
+// fa_fwd_pack.cuh — what packed sequences of different lengths with grouped heads
+// change in the forward kernels: a unit's place in the batch, its query tiles, the
+// end of a sequence inside a key tile, and the output rows.
+//
+// A query tile's 128 rows are the heads of one kv head for 128 / G tokens (G = H /
+// Hkv), token by token, as one TMA box brings them from [token][H][d]: the group
+// shares every K and V tile, a tile spans fewer tokens, so that less of it lies above
+// the diagonal, and short sequences fill their tiles better (a prompt of 24 tokens,
+// G = 4: one tile of 96 rows, not four of 24). Row r is token r / G, head r % G.
+//
+// Units (two tiles; one at d = 256) are taken longest first over all sequences
+// (packed_pick): under a causal mask a unit's time grows with its last position, and
+// the last CTAs to start set the call's end.
+//
+// A key tile that a sequence ends in holds the next one's keys, or what lies behind
+// the last one. Their scores are masked, but a weight of zero does not undo an
+// infinity or a NaN in V: the producer overwrites those V rows with zeros, once per
+// unit, while the unit's last scores are formed.
+#pragma once
+
+#include "fa_fwd_win.cuh"
+#include "fa_packed.cuh"
+
+namespace fa {
+
+struct PackUnit {
+    int qbase, len_q;  // first query of the sequence, its number of queries (0: no unit)
+    int kbase, len_k;
+    int token;         // the unit's first query, within the sequence
+    int h;             // kv head
+};
+
+// The unit of CTA `lin` (kv heads fastest), found by one warp.
+template <int QT>
+__device__ __forceinline__ void pack_unit(const FwdParams& p, unsigned lin, int lane, PackUnit* u) {
+    const PackedSeqs s = {p.cu_q, p.cu_k, p.B, p.total_q, p.Nk, p.Nq, p.max_k};
+    PackedSeq x;
+    if (lin == 0)
+        for (int b = lane; b < p.B; b += 32)
+            if (!packed_seq(s, b, x)) atomicOr(p.status, kStatusBadSeqlens);
+    const int tokens = QT * p.tile_tokens;
+    auto level0 = [&](const PackedSeq& y) {  // of a sequence's first unit: its offset in units, rounded down
+        const int off = y.m - y.n;
+        return off >= 0 ? off / tokens : -((tokens - 1 - off) / tokens);
+    };
+    auto runs = [&](int b, int& a, int& n) {
+        PackedSeq y;
+        packed_seq(s, b, y);
+        a = level0(y);
+        n = (y.n + tokens - 1) / tokens;
+    };
+    int b = 0, level = 0;
+    const bool have = packed_pick(p.B, static_cast<int>(lin / p.Hkv), lane, runs, b, level);
+    if (lane == 0) {
+        x = {0, 0, 0, 0};
+        if (have) packed_seq(s, b, x);
+        *u = {x.q0, x.n, x.k0, x.m, have ? (level - level0(x)) * tokens : 0, static_cast<int>(lin % p.Hkv)};
+    }
+}
+
+// Rows that belong to no sequence (before the first one and behind the last): O = 0,
+// LSE = -inf where the call asks for it. One warp of each CTA, its share of them.
+template <int D>
+__device__ __forceinline__ void pack_fill(const FwdParams& p, int lane) {
+    if (!p.fill) return;
+    const int c0 = p.cu_q[0], c1 = p.cu_q[p.B];
+    if (!(0 <= c0 && c0 <= c1 && c1 <= p.total_q)) return;
+    const int rest = p.total_q - (c1 - c0);
+    for (long long i = blockIdx.x; i < rest; i += gridDim.x) {
+        const long long token = i < c0 ? i : i + (c1 - c0);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + token * p.H * D);
+        for (int e = lane; e < p.H * (D / 8); e += 32) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+        for (int h = lane; h < p.H; h += 32) p.lse[static_cast<long long>(h) * p.total_q + token] = -INFINITY;
+    }
+}
+
+// First token of tile slot t: with two slots the later rows come first (see tile_row0).
+template <int QT>
+__device__ __forceinline__ int pack_tile_token(const FwdParams& p, int first, int t) {
+    return first + (QT == 2 ? 1 - t : t) * p.tile_tokens;
+}
+
+template <int QT, int BN>
+__device__ __forceinline__ void pack_work(const FwdParams& p, const PackUnit& u, WorkWin<QT>& w) {
+    w.split = 0;
+    w.bh = u.h;
+    w.zq = u.h * p.group;
+    w.zk = u.h;
+    w.qbase = u.qbase;
+    w.kbase = u.kbase;
+    w.q0 = u.token;
+    w.kv_tile0 = 0;
+    w.kv_end = u.len_k;
+    w.causal_off = u.len_k - u.len_q;
+    w.rm = {0, 0, 0, u.len_q};
+    w.list = win_list<BN>(p, u.token + w.causal_off, min(u.token + QT * p.tile_tokens, u.len_q) - 1 + w.causal_off);
+    w.nmax = w.list.n;
+    w.small = QT == 2 && w.list.ns == 1 && p.sinks <= kSmallSinks;
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+        const int row0 = pack_tile_token<QT>(p, u.token, t);
+        w.n[t] = w.hole[t] = w.steps[t] = 0;
+        if (row0 >= u.len_q) continue;
+        const int last = min(row0 + p.tile_tokens, u.len_q) - 1 + w.causal_off;
+        if (last < 0) continue;
+        const int end = last / BN + 1;
+        const int first = p.window > 0 ? max(0, row0 + w.causal_off - p.window + 1) / BN : 0;
+        w.n[t] = w.list.ns + max(0, end - w.list.lo);
+        w.hole[t] = w.list.ns > 0 || w.list.lo > 0 ? max(0, min(first, end) - w.list.lo) : 0;
+        w.steps[t] = w.n[t] - w.hole[t];
+    }
+}
+
+// Keys of the unit's last key tile that the sequence has (BN or more: all).
+template <int BN, int QT>
+__device__ __forceinline__ int pack_tail(const WorkWin<QT>& w) {
+    return w.kv_end - w.list.tile(w.nmax - 1) * BN;
+}
+
+// Zeros over the rows of the last V tile that are not the sequence's; `entry` is its
+// number in the ring, the last one that the calling warp (the producer) issued, so its
+// phase is the one in progress or the one just completed. False where the wait failed.
+template <typename L, int QT>
+__device__ __forceinline__ bool pack_clean_v(const FwdParams& p, const WorkWin<QT>& w, uint32_t sbase, int entry,
+                                             uint32_t clean, volatile uint32_t* abort_flag, int lane) {
+    const int rows = pack_tail<L::BN>(w);
+    if (rows >= L::BN) return true;
+    const int slot = entry % L::STAGES;
+    if (!__all_sync(0xffffffffu, wait_phase(sbase + L::BAR_OFF + 8u * (L::BAR_KVFULL + slot), (entry / L::STAGES) & 1,
+                                            p, abort_flag, kStatusWaitKvFull)))
+        return false;
+    const uint32_t tile = sbase + L::SLOT_OFF + slot * L::SLOT_BYTES;
+    for (int c = 0; c < L::CHUNKS; ++c)
+        for (int at = rows * 128 + lane * 16; at < L::BN * 128; at += 512)
+            st_shared_v4(tile + c * (L::BN * 128) + at, 0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(clean);
+    return true;
+}
+
+// Output of a query tile by its 128 softmax threads (thread r = row r = TMEM lane r;
+// `token` its token): O / l as bf16 staged by each warp for its own 32 rows in `stage`
+// (the tile's Q, free by now), then written 128 bytes of a row per eight lanes. Rows
+// past the sequence, or past the tile's whole tokens, are left out. n = 0: no key.
+template <int D, int QT>
+__device__ __forceinline__ void pack_store(const FwdParams& p, const WorkWin<QT>& w, int token, int r, int n, float m,
+                                           float m_true, float l, float l_o, uint32_t tO, uint32_t stage) {
+    const int lane = r & 31, head = w.zq + r % p.group;
+    const bool row_ok = r < p.group * p.tile_tokens && token < w.rm.len_q;
+    const long long row = (static_cast<long long>(w.qbase) + token) * p.H + head;
+    const RowMap rm = {row, static_cast<long long>(head) * p.total_q + w.qbase + token, 0, row_ok ? 1 : 0};
+    const RowOut<D> out(p, rm, 0, 0, 0, m, m_true, l, l_o);
+    const uint32_t swz = static_cast<uint32_t>(r & 7);
+#pragma unroll 1
+    for (int c = 0; c < D / 64; ++c) {
+        uint32_t a[32], b[32];
+        if (n > 0) {
+            tmem_ld32(tO + c * 64, a);
+            tmem_ld32(tO + c * 64 + 32, b);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = b[i] = 0u;
+        }
+        const uint32_t line = stage + c * (kBM * 128) + r * 128;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t x0 = hh ? b[2 * i] : a[2 * i];
+                const uint32_t x1 = hh ? b[2 * i + 1] : a[2 * i + 1];
+                pk[i] = pack_bf16x2(__uint_as_float(x0) * out.f, __uint_as_float(x1) * out.f);
+            }
+#pragma unroll
+            for (int uu = 0; uu < 4; ++uu) {
+                const uint32_t u = static_cast<uint32_t>(hh * 4 + uu);
+                st_shared_v4(line + ((u ^ swz) << 4), pk[4 * uu], pk[4 * uu + 1], pk[4 * uu + 2], pk[4 * uu + 3]);
+            }
+        }
+    }
+    out.finish(p);
+    __syncwarp();
+#pragma unroll 1
+    for (int it = 0; it < 8; ++it) {
+        const int rr = it * 4 + (lane >> 3), u = lane & 7;
+        const bool ok = __shfl_sync(0xffffffffu, static_cast<int>(row_ok), rr) != 0;
+        const long long to = __shfl_sync(0xffffffffu, row, rr);
+        if (!ok) continue;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            float x[4];
+            ld_shared_v4f(stage + c * (kBM * 128) + ((r & ~31) + rr) * 128 + ((u ^ (rr & 7)) << 4), x);
+            *reinterpret_cast<float4*>(static_cast<__nv_bfloat16*>(p.o) + to * D + c * 64 + u * 8) =
+                make_float4(x[0], x[1], x[2], x[3]);
+        }
+    }
+}
+
+}  // namespace fa

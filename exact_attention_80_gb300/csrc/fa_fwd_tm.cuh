@@ -52,7 +52,7 @@
 #include <type_traits>
 
 #include "fa_fwd_common.cuh"
-#include "fa_fwd_win.cuh"
+#include "fa_fwd_pack.cuh"
 
 namespace fa {
 
@@ -132,7 +132,8 @@ struct LayoutTM {
     // completion per unit in which the tile has keys)
     static constexpr int BAR_QEMPTY = BAR_OFULL + Q_TILES;
     static constexpr int BAR_DRAIN = BAR_QEMPTY + Q_TILES;
-    static constexpr int NUM_BARS = BAR_DRAIN + 1;
+    static constexpr int BAR_VCLEAN = BAR_DRAIN + 1;  // packed: the last V tile's other rows are zeros
+    static constexpr int NUM_BARS = BAR_VCLEAN + 1;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;  // [0] tmem base, [1] abort
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr size_t ALLOC_BYTES = BYTES + 1024;  // slack for 1024 alignment
@@ -637,7 +638,9 @@ __device__ __forceinline__ void tm_persist_control(const FwdParams& p, uint32_t 
 // whose accumulator rows 16 q + i sit in TMEM lanes 32 q + i (i < 16) of lane
 // quarter q; lanes 16-31 of each quarter hold no row.
 // WIN: sliding window with sinks and grouped heads (bf16; tm_window_control).
-template <int D, bool F8, bool DUAL = false, bool PERSIST = false, bool M64 = false, bool WIN = false>
+// PACK: the same on packed sequences (fa_fwd_pack.cuh).
+template <int D, bool F8, bool DUAL = false, bool PERSIST = false, bool M64 = false, bool WIN = false,
+          bool PACK = false>
 __device__ __forceinline__ void tm_forward(const FwdParams& p) {
     using L = LayoutTM<D, F8, PERSIST>;
     constexpr int QT = L::Q_TILES;
@@ -676,6 +679,7 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
             mbar_init(bar(L::BAR_QEMPTY + t), 1);
         }
         mbar_init(bar(L::BAR_DRAIN), 1);
+        if constexpr (PACK) mbar_init(bar(L::BAR_VCLEAN), 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -683,6 +687,13 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         tma_prefetch_desc(&p.tm_q);
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
+    }
+    PackUnit* unit = nullptr;
+    if constexpr (PACK) {
+        __shared__ PackUnit unit_store;
+        unit = &unit_store;
+        if (warp == 2) pack_unit<QT>(p, blockIdx.x, lane, unit);
+        if (warp == 3) pack_fill<D>(p, lane);
     }
     if (warp == 1) {
         tmem_alloc(sbase + L::MISC_OFF, L::TMEM_COLS);
@@ -700,7 +711,7 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
       // The work record is derived inside each role, after its register limit
       // is set, so that no role carries fields it does not use.
       if constexpr (WIN) {
-        tm_window_control<D, L, PERSIST>(p, sbase, tmem, abort_flag, warp);
+        tm_window_control<D, L, PERSIST, PACK>(p, sbase, tmem, abort_flag, warp, unit);
       } else if constexpr (PERSIST) {
         tm_persist_control<D, F8>(p, sbase, tmem, abort_flag, warp);
       } else if constexpr (DUAL) {
@@ -965,9 +976,11 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         }
         std::conditional_t<DUAL, WorkDual, std::conditional_t<WIN, WorkWin<QT>, Work<QT>>> w;
         if constexpr (DUAL) compute_work_dual<BN>(p, lin, w);
+        else if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
         else if constexpr (WIN) compute_work_win<QT, BN, !PERSIST>(p, lin, w);
         else compute_work<QT, BN>(p, lin, w);
-        const int q_row = (M64 && lane >= 16) ? (1 << 30) : (DUAL ? w.q0 : tile_row0(p, w.q0, t)) + r;
+        const int q_row = PACK ? pack_tile_token<QT>(p, w.q0, t) + r / p.group :
+                          (M64 && lane >= 16) ? (1 << 30) : (DUAL ? w.q0 : tile_row0(p, w.q0, t)) + r;
         // This tile's key split: the CTA's, or its own in a dual-range CTA.
         int kv_tile0_t, kv_end_t, split_t;
         if constexpr (DUAL) {
@@ -1185,7 +1198,10 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         // A tile slot the CTA does not own (one tile per CTA, fa_fwd_rows) writes
         // nothing: its rows belong to another CTA.
         if (!DUAL && !PERSIST && t >= p.tiles_per_cta) ok = false;
-        if constexpr (PERSIST && !F8) {
+        if constexpr (PACK) {
+            if (ok)
+                pack_store<D>(p, w, q_row, r, n, m, m_true, l, l + lc, tO, sbase + L::Q_OFF + t * L::Q_TILE_BYTES);
+        } else if constexpr (PERSIST && !F8) {
             // Plain mode, dense: bf16 O staged per warp in its own buffer.
             if (ok && n > 0)
                 store_rows_tma_buf<D>(p, w.rm, w.zq, q_row - r, r, q_row, m, m_true, l, l + lc, tO,
@@ -1242,6 +1258,13 @@ template <int D>
 __global__ void __launch_bounds__(LayoutTM<D>::THREADS, 1)
     fa_fwd_tmw_kernel(const __grid_constant__ FwdParams p) {
     tm_forward<D, false, false, false, false, true>(p);
+}
+
+// The same on packed sequences.
+template <int D>
+__global__ void __launch_bounds__(LayoutTM<D>::THREADS, 1)
+    fa_fwd_tmpack_kernel(const __grid_constant__ FwdParams p) {
+    tm_forward<D, false, false, false, false, true, true>(p);
 }
 
 // The same, persistent CTAs.

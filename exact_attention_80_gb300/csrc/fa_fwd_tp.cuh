@@ -36,7 +36,7 @@
 #include <type_traits>
 
 #include "fa_fwd_common.cuh"
-#include "fa_fwd_win.cuh"
+#include "fa_fwd_pack.cuh"
 
 namespace fa {
 
@@ -107,7 +107,8 @@ struct LayoutTP {
     static constexpr int BAR_ALPHA = BAR_OSTAGED + Q_TILES;
     static constexpr int BAR_OREADY = BAR_ALPHA + 2 * Q_TILES;
     static constexpr int BAR_DRAIN = BAR_OREADY + 2 * Q_TILES;
-    static constexpr int NUM_BARS = BAR_DRAIN + 1;
+    static constexpr int BAR_VCLEAN = BAR_DRAIN + 1;  // packed: the last V tile's other rows are zeros
+    static constexpr int NUM_BARS = BAR_VCLEAN + 1;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;  // [0] tmem base, [1] abort
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr size_t ALLOC_BYTES = BYTES + 1024;  // slack for 1024 alignment
@@ -140,8 +141,8 @@ struct LayoutTP {
 };
 
 // WIN: sliding window with sinks and grouped heads (one query tile: a step per
-// tile of its list).
-template <int D, bool F8, bool WIN = false>
+// tile of its list). PACK: the same on packed sequences (fa_fwd_pack.cuh).
+template <int D, bool F8, bool WIN = false, bool PACK = false>
 __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     using L = LayoutTP<D, F8>;
     constexpr int QT = L::Q_TILES;
@@ -167,10 +168,20 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     std::conditional_t<WIN, WorkWin<QT>, Work<QT>> w;
-    if constexpr (WIN) compute_work_win<QT, BN, true>(p, blockIdx.x, w);
-    else compute_work<QT, BN>(p, blockIdx.x, w);
+    PackUnit* unit = nullptr;
+    if constexpr (PACK) {
+        __shared__ PackUnit unit_store;
+        unit = &unit_store;
+        if (warp == 2) pack_unit<QT>(p, blockIdx.x, lane, unit);
+        if (warp == 3) pack_fill<D>(p, lane);
+    } else if constexpr (WIN) {
+        compute_work_win<QT, BN, true>(p, blockIdx.x, w);
+    } else {
+        compute_work<QT, BN>(p, blockIdx.x, w);
+    }
 
     if (threadIdx.x == 0) {
+        mbar_init(bar(L::BAR_VCLEAN), 1);
         mbar_init(bar(L::BAR_QFULL), 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(bar(L::BAR_KVFULL + s), 1);
@@ -206,6 +217,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
+    if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
 
     if (warp < 4) {
       // Control warpgroup. setmaxnreg sits inside each role's branch so that
@@ -221,10 +233,18 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
             for (int t = 0; t < QT; ++t) nvalid += (w.n[t] > 0) ? 1 : 0;
             // (The failure-detection test hook withholds the Q tiles so that the
             // issuer's bounded wait runs out; nothing else changes.)
-            if (leader && !p.test_withhold_q) mbar_arrive_expect_tx(bar(L::BAR_QFULL), nvalid * L::Q_TILE_BYTES);
+            if (leader && !p.test_withhold_q)
+                mbar_arrive_expect_tx(bar(L::BAR_QFULL), nvalid * (PACK ? p.q_bytes : L::Q_TILE_BYTES));
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
-                if (leader && w.n[t] > 0 && !p.test_withhold_q) {
+                if constexpr (PACK) {
+                    if (leader && w.n[t] > 0)
+#pragma unroll
+                        for (int c = 0; c < L::CHUNKS; ++c)
+                            tma_load_3d(sbase + L::Q_OFF + t * L::Q_TILE_BYTES + c * (kBM * 128), &p.tm_q,
+                                        bar(L::BAR_QFULL), L::CHUNK_ELEMS * c, w.zq,
+                                        w.qbase + pack_tile_token<QT>(p, w.q0, t));
+                } else if (leader && w.n[t] > 0 && !p.test_withhold_q) {
 #pragma unroll
                     for (int c = 0; c < L::CHUNKS; ++c)
                         tma_load_3d(sbase + L::Q_OFF + t * L::Q_TILE_BYTES + c * (kBM * 128),
@@ -261,7 +281,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
                     const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
                     int row, zk;
                     if constexpr (WIN) {
-                        row = w.list.tile(tile) * BN;
+                        row = (PACK ? w.kbase : 0) + w.list.tile(tile) * BN;
                         zk = w.zk;
                     } else {
                         row = w.kbase + (w.kv_tile0 + tile) * BN;
@@ -274,6 +294,9 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
                 }
                 issued = e + 1;
                 pos.advance();
+            }
+            if constexpr (PACK) {
+                if (ok) ok = pack_clean_v<L>(p, w, sbase, total - 1, bar(L::BAR_VCLEAN), abort_flag, lane);
             }
             if (ok) {
                 // Producer tail: wait until the issuer has released the last use
@@ -374,6 +397,10 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
                 }
                 // O_t += P_t(j) V_j as each tile's P arrives.
                 ok = wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull);
+                if constexpr (PACK) {
+                    if (ok && j + 1 == w.nmax && pack_tail<BN>(w) < BN)
+                        ok = wait_all(bar(L::BAR_VCLEAN), 0, kStatusWaitKvFull);
+                }
                 if (!ok) break;
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
@@ -457,7 +484,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
         const int t = (warp - L::SOFTMAX_WARP0) >> 2;
         const int quarter = warp & 3;  // TMEM lane quarter this warp may access
         const int r = quarter * 32 + lane;
-        const int q_row = w.q0 + t * kBM + r;
+        const int q_row = PACK ? pack_tile_token<QT>(p, w.q0, t) + r / p.group : w.q0 + t * kBM + r;
         const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tO = tmem + lane_field + L::O_COL(t);
         const float sl2 = p.scale_log2;
@@ -635,7 +662,10 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
         const float o_scale = F8 ? p.o_scale : 1.f;
         const float m_out = F8 ? m - kP8Shift : m;
         const float l_o = F8 ? l : l + lc;
-        if (ok && !p.split_mode && !p.varlen && n > 0) {
+        if constexpr (PACK) {
+            if (ok)
+                pack_store<D>(p, w, q_row, r, n, m_out, m_true, l, l_o, tO, sbase + L::Q_OFF + t * L::Q_TILE_BYTES);
+        } else if (ok && !p.split_mode && !p.varlen && n > 0) {
             // Plain mode: bf16 O_t staged in Q_t's shared memory (8-bit inputs: in
             // the K/V slots), written with TMA.
             const uint32_t staging = F8 ? sbase + L::SLOT_OFF : sbase + L::Q_OFF + t * L::Q_TILE_BYTES;
@@ -665,6 +695,13 @@ template <int D>
 __global__ void __launch_bounds__(LayoutTP<D>::THREADS, 1)
     fa_fwd_tpw_kernel(const __grid_constant__ FwdParams p) {
     tp_forward<D, false, true>(p);
+}
+
+// The same on packed sequences.
+template <int D>
+__global__ void __launch_bounds__(LayoutTP<D>::THREADS, 1)
+    fa_fwd_tppack_kernel(const __grid_constant__ FwdParams p) {
+    tp_forward<D, false, true, true>(p);
 }
 
 // e4m3 Q, K, V with per-tensor descales (FA-3 page, section 7.3: 8-bit inputs

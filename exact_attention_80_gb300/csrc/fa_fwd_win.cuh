@@ -167,6 +167,20 @@ __device__ __forceinline__ long long win_unit(const FwdParams& p, int k) {
     return lin < p.total_units ? lin : -1;
 }
 
+// Packed sequences (fa_fwd_pack.cuh): a unit's place in the batch, its work, the token
+// of a query tile's first row, the keys that exist in its last key tile, and the
+// clearing of the others' values.
+struct PackUnit;
+template <int QT, int BN>
+__device__ __forceinline__ void pack_work(const FwdParams& p, const PackUnit& u, WorkWin<QT>& w);
+template <int QT>
+__device__ __forceinline__ int pack_tile_token(const FwdParams& p, int first, int t);
+template <int BN, int QT>
+__device__ __forceinline__ int pack_tail(const WorkWin<QT>& w);
+template <typename L, int QT>
+__device__ __forceinline__ bool pack_clean_v(const FwdParams& p, const WorkWin<QT>& w, uint32_t sbase, int entry,
+                                             uint32_t clean, volatile uint32_t* abort_flag, int lane);
+
 // Control warps of a two-tile CTA with a window: the producer and the issuer of
 // the dense kernel with the tile list and the holes. A tile that skips step
 // j + 1 gets no S there; its next S is issued in the step before its next one.
@@ -176,9 +190,11 @@ __device__ __forceinline__ long long win_unit(const FwdParams& p, int k) {
 // issued right behind the current unit's last PV; O_t is first overwritten by
 // the unit's PV_t(0), which waits for a P that the softmax threads hand over
 // only after their epilogue.
-template <int D, typename L, bool PERSIST>
+// PACK: one unit per CTA, `unit` its place in the batch of packed sequences.
+template <int D, typename L, bool PERSIST, bool PACK>
 __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t sbase, uint32_t tmem,
-                                                  volatile uint32_t* abort_flag, int warp) {
+                                                  volatile uint32_t* abort_flag, int warp, const PackUnit* unit) {
+    static_assert(!(PERSIST && PACK), "packed sequences take one unit per CTA");
     constexpr int QT = L::Q_TILES;
     constexpr int BN = L::BN;
     constexpr int ST = L::STAGES;
@@ -198,11 +214,13 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
                                                     kStatusWaitQ)))
                 return false;
             if (leader) {
-                mbar_arrive_expect_tx(bar(L::BAR_QFULL + t), L::Q_TILE_BYTES);
+                mbar_arrive_expect_tx(bar(L::BAR_QFULL + t), PACK ? p.q_bytes : L::Q_TILE_BYTES);
 #pragma unroll
                 for (int c = 0; c < L::CHUNKS; ++c)
                     tma_load_3d(sbase + L::Q_OFF + t * L::Q_TILE_BYTES + c * (kBM * L::ROW_BYTES), &p.tm_q,
-                                bar(L::BAR_QFULL + t), L::CHUNK_ELEMS * c, tile_row0(p, w.q0, t), w.zq);
+                                bar(L::BAR_QFULL + t), L::CHUNK_ELEMS * c,
+                                PACK ? w.zq : tile_row0(p, w.q0, t),
+                                PACK ? w.qbase + pack_tile_token<QT>(p, w.q0, t) : w.zq);
             }
             ++q_loads[t];
             return true;
@@ -211,7 +229,8 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             const long long lin = win_unit<PERSIST>(p, k);
             if (lin < 0) continue;
             WorkWin<QT> w;
-            compute_work_win<QT, BN, !PERSIST>(p, lin, w);
+            if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
+            else compute_work_win<QT, BN, !PERSIST>(p, lin, w);
             if (w.nmax == 0) continue;
             if (!PERSIST) ok = load_q(w, 0);
             // Entry e: K_0; then per step j: V_j, K_{j+1}.
@@ -223,7 +242,7 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
                 if (leader) {
                     mbar_arrive_expect_tx(bar(L::BAR_KVFULL + pos.slot), L::SLOT_BYTES);
                     const CUtensorMap* map = (e & 1) ? &p.tm_v : &p.tm_k;
-                    const int row = w.list.tile(e >> 1) * BN;
+                    const int row = (PACK ? w.kbase : 0) + w.list.tile(e >> 1) * BN;
 #pragma unroll
                     for (int c = 0; c < L::CHUNKS; ++c)
                         tma_load_3d(sbase + L::SLOT_OFF + pos.slot * L::SLOT_BYTES + c * (BN * L::ROW_BYTES), map,
@@ -235,6 +254,10 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
                     if (PERSIST) ok = load_q(w, 0);
                     if (ok) ok = load_q(w, 1);
                 }
+            }
+            if constexpr (PACK) {
+                if (ok)
+                    ok = pack_clean_v<L>(p, w, sbase, issued - 1, bar(L::BAR_VCLEAN), abort_flag, threadIdx.x & 31);
             }
         }
         if (ok) {
@@ -300,7 +323,8 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             const long long lin = win_unit<PERSIST>(p, k);
             if (lin < 0) continue;
             WorkWin<QT> w;
-            compute_work_win<QT, BN, !PERSIST>(p, lin, w);
+            if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
+            else compute_work_win<QT, BN, !PERSIST>(p, lin, w);
             if (w.nmax == 0) continue;
             auto active = [&](int t, int j) {
                 return j < w.n[t] && !(j >= w.list.ns && j < w.list.ns + w.hole[t]);
@@ -348,6 +372,9 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             for (int j = 0; j < w.nmax && ok; ++j) {
                 const int sv = slot_v, sk = slot_k;
                 const bool k_next = (j + 1 < w.nmax);
+                if constexpr (PACK) {
+                    if (!k_next && pack_tail<BN>(w) < BN) ok = wait_all(bar(L::BAR_VCLEAN), 0, kStatusWaitKvFull);
+                }
 #pragma unroll
                 for (int t = 0; t < QT && ok; ++t) {
                     const bool act = active(t, j);

@@ -76,6 +76,12 @@ struct FwdParams {
     // Sliding-window launches (bottom-right): window 0 = none; heads in groups
     // of `group` = H / Hkv share a kv head.
     int window, sinks, group, Hkv;
+    // Packed launches (fa_fwd_packed): B sequences (cu_q, cu_k, total_q, Nk = total_k,
+    // Nq and max_k the bounds of their lengths). tm_q is bf16 [total_q][H][d], box
+    // {64, group, tile_tokens}: a query tile holds all heads of a kv head for
+    // tile_tokens = 128 / group tokens, token by token; q_bytes of it are loaded.
+    int B, max_k, tile_tokens, fill;
+    uint32_t q_bytes;
 };
 
 // Backward (d = 128): one CTA per (head, 128-key tile).
@@ -105,6 +111,8 @@ cudaError_t launch_fwd_win_d128(const FwdParams& p, unsigned grid, cudaStream_t 
 cudaError_t launch_fwd_win_d64_persist(const FwdParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_fwd_win_d128_persist(const FwdParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_fwd_win_d256(const FwdParams& p, unsigned grid, cudaStream_t stream);
+// Packed sequences, grouped heads, window with sinks (bf16).
+cudaError_t launch_fwd_packed(const FwdParams& p, int d, unsigned grid, cudaStream_t stream);
 // e4m3 Q, K, V (tm_q/tm_k/tm_v are byte maps, box {128, rows, 1}, or {64,
 // rows, 1} with the 64-byte swizzle at d = 64); d = 64, 128, 256.
 cudaError_t launch_fwd_f8_d64(const FwdParams& p, unsigned grid, cudaStream_t stream);
@@ -189,11 +197,20 @@ fa_status check_common(const void* q, const void* k, const void* v, int B, int H
 bool valid_d(int d);
 // Head groups, window and sinks of the sliding-window entry points.
 fa_status check_window(int H, int Hkv, int Nq, int Nk, int window, int sinks);
+// A packed batch and the operator's shape; the distance of a packed tensor's tokens.
+fa_status check_packed(const fa_packed_batch* batch, int H, int Hkv, int d, float scale, int window, int sinks);
+bool token_stride(long long stride, int heads, int d);
 // SMs of the current device (cached).
 cudaError_t sm_count(int* out);
 // The driver's cuTensorMapEncodeTiled, or null.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // bf16 [BH][N][d] as a 3-D TMA map, box {64, box_rows, 1}, 128-byte swizzle.
 bool encode_rows_map(CUtensorMap* map, const void* base, int d, int N, int BH, int box_rows);
+// bf16 [total][H][d] whose tokens are `stride` elements apart, as rows = tokens, heads
+// slowest, box {64, box_rows, 1}; or as rows = heads, tokens slowest, box {64, heads, tokens}.
+bool encode_strided_tokens_map(CUtensorMap* map, const void* base, int d, int total, int H, long long stride,
+                               int box_rows);
+bool encode_token_heads_map(CUtensorMap* map, const void* base, int d, int total, int H, long long stride, int heads,
+                            int tokens);
 
 }  // namespace fa

@@ -319,6 +319,42 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
                         int Nq, int Nk, int d, float scale, int window, int sinks, cudaStream_t stream);
 
 /*
+ * fa_packed_batch — sequences of different lengths packed one behind the other:
+ * sequence b owns query tokens cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 and key
+ * tokens cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1 (DEVICE int32 [B + 1] each; they
+ * may be the same array). Required: cu[0] >= 0, nondecreasing, cu_seqlens_q[B] <=
+ * total_q, cu_seqlens_k[B] <= total_k, every length <= max_seqlen_q or max_seqlen_k;
+ * total_q, total_k < 2^30, B <= 2^22. Sequences may be empty. A sequence whose
+ * offsets break the requirements is neither read nor written, FA_ERR_SEQLENS from
+ * fa_device_status.
+ */
+typedef struct {
+    const int* cu_seqlens_q;
+    const int* cu_seqlens_k;
+    int B, total_q, total_k, max_seqlen_q, max_seqlen_k;
+} fa_packed_batch;
+
+/*
+ * fa_fwd_packed — causal attention over packed sequences with grouped heads, a
+ * sliding window and sinks.
+ *   q [total_q][H][d], k, v [total_k][Hkv][d] bf16 (read), their tokens q_stride,
+ *   k_stride and v_stride elements apart (multiples of 8, at least heads * d: a fused
+ *   projection's rows may be read where they are); o bf16 [total_q][H][d], lse fp32
+ *   [H][total_q] (written). H is a multiple of Hkv, H / Hkv at most 128, query head h
+ *   reads kv head h / (H / Hkv).
+ * Each sequence is an attention problem of its own, with n queries and m keys: query i
+ * is at position p = i + m - n and sees key j iff j <= p and (window = 0, or j > p -
+ * window, or j < sinks), as in fa_fwd_window. Rows that see no key get O = 0, LSE =
+ * -inf. What other sequences hold, and what lies outside of all of them, has no
+ * influence on a sequence (it may be infinite or NaN); its own K and V must be finite.
+ * Rows of o and lse that belong to no sequence are left as they are, or, with `fill`
+ * != 0, get O = 0 and LSE = -inf. Roundings as fa_fwd_window.
+ */
+fa_status fa_fwd_packed(const void* q, const void* k, const void* v, void* o, float* lse,
+                        const fa_packed_batch* batch, int H, int Hkv, int d, long long q_stride, long long k_stride,
+                        long long v_stride, float scale, int window, int sinks, int fill, cudaStream_t stream);
+
+/*
  * fa_rotation — rotary positions. The first `rot` columns of a head (rot a
  * multiple of 16, at most d; the others are left as they are) form rot / 2
  * pairs: columns (i, i + rot / 2), or (2 i, 2 i + 1) when `interleaved`. Pair i
