@@ -107,6 +107,10 @@ def load_library() -> ctypes.CDLL:
     lib.fa_bwd_window.restype = i
     lib.fa_fwd_packed.argtypes = [vp, vp, vp, vp, vp, packed, i, i, i, ll, ll, ll, f, i, i, i, vp]
     lib.fa_fwd_packed.restype = i
+    lib.fa_bwd_packed_workspace_bytes.argtypes = [i] * 10
+    lib.fa_bwd_packed_workspace_bytes.restype = ctypes.c_size_t
+    lib.fa_bwd_packed.argtypes = [vp] * 10 + [packed, i, i, i, packed, f, i, i, i, vp]
+    lib.fa_bwd_packed.restype = i
     lib.fa_fwd_grid_ctas.argtypes = [i, i, i, i, i]
     lib.fa_fwd_grid_ctas.restype = ctypes.c_longlong
     lib.fa_device_status.argtypes = [vp, i]
@@ -1038,6 +1042,7 @@ def attention_window_backward(q, k, v, o, lse, dout, window: int, sinks: int = 0
 
 # ------------------------------------------------------------- packed sequences
 _PACKED_BATCH = struct.Struct("PPiiiii")  # fa_packed_batch
+_PACKED_STRIDES = struct.Struct("7q")      # fa_packed_strides
 
 
 def _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k):
@@ -1093,6 +1098,58 @@ def attention_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max
         fa_fwd_packed(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window, sinks, scale,
                       True, stream)
     return _given(stream, o, lse)
+
+
+def fa_bwd_packed_workspace_bytes(B: int, total_q: int, total_k: int, max_seqlen_q: int, max_seqlen_k: int, H: int,
+                                  Hkv: int, d: int, window: int = 0, sinks: int = 0) -> int:
+    return load_library().fa_bwd_packed_workspace_bytes(
+        *map(_int32, (B, total_q, total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks)))
+
+
+def fa_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                  max_seqlen_k: int, window: int = 0, sinks: int = 0, scale: float | None = None, fill: bool = False,
+                  stream=None):
+    """Backward of :func:`fa_fwd_packed` into caller-owned ``dq``, ``dk``, ``dv`` (bf16, shaped like q, k,
+    v, whose tokens may be strided, as ``dout``'s may); ``workspace`` fp32 of at least
+    ``fa_bwd_packed_workspace_bytes`` bytes. Rows of the gradients that belong to no sequence stay as
+    they are, or, with ``fill``, get 0."""
+    import torch
+
+    batch, n, m, H, Hkv, d, strides, index = _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
+    _check_out(o, "o", (n, H, d), torch.bfloat16, index)
+    _check_out(lse, "lse", (H, n), torch.float32, index)
+    strides = list(strides)
+    for t, name, like in ((dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
+        if not isinstance(t, torch.Tensor) or t.shape != like.shape:
+            raise ValueError(f"{name} must be a tensor of shape {tuple(like.shape)}")
+        strides.append(_tokens_view(t, name, index)[3])
+    B = cu_seqlens_q.shape[0] - 1
+    _need_workspace(workspace, fa_bwd_packed_workspace_bytes(B, n, m, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks),
+                    "workspace", q.device)
+    st = _on_stream(index, stream, load_library().fa_bwd_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                    o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                    workspace.data_ptr(), batch, H, Hkv, d, _PACKED_STRIDES.pack(*strides),
+                    default_scale(d) if scale is None else float(scale), _int32(window), _int32(sinks),
+                    1 if fill else 0)
+    _check(st, "fa_bwd_packed")
+
+
+def attention_packed_backward(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
+                              max_seqlen_k: int, window: int = 0, sinks: int = 0, scale: float | None = None,
+                              stream=None):
+    """Allocate ``(dq, dk, dv)`` and the workspace and run :func:`fa_bwd_packed`; rows that belong to no
+    sequence are 0."""
+    import torch
+
+    _, n, m, H, Hkv, d, _, _ = _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
+    nbytes = fa_bwd_packed_workspace_bytes(cu_seqlens_q.shape[0] - 1, n, m, max_seqlen_q, max_seqlen_k, H, Hkv, d, window,
+                                           sinks)
+    with _allocating(stream, q):
+        dq, dk, dv = (torch.empty(t.shape, dtype=torch.bfloat16, device=q.device) for t in (q, k, v))
+        ws = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
+        fa_bwd_packed(q, k, v, o, dout, lse, dq, dk, dv, ws, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                      window, sinks, scale, True, stream)
+    return _given(stream, dq, dk, dv)
 
 
 _SIDE_STREAMS = {}

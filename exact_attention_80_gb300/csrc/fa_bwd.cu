@@ -64,6 +64,7 @@
 #include "fa.h"
 #include "fa_internal.h"
 #include "fa_launch.h"
+#include "fa_packed.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -98,9 +99,24 @@ struct BwdParams {
     // [128 keys][d], which the last launch adds in order.
     int sink_tiles, sink_parts, parts;
     float* dkv_part;
+    // Packed sequences (the window's fields apply; tensors token-major [total][heads][d],
+    // tokens these many elements apart): rows of nlse2, ndd and dq_acc are [H][rows_pad],
+    // a sequence's at pad_row. Partial sums of the sinks' tiles (the first sink_tiles of
+    // each sequence) come first, [b][tile], then the others', by tile_slot.
+    PackedSeqs seqs;
+    long long rows_pad;
+    long long q_stride, k_stride, v_stride, do_stride, dq_stride, dk_stride, dv_stride;
+    int fill;
 };
 
 namespace {
+
+// First padded row of sequence b, whose first query is q0: a multiple of 64, with room
+// for its queries in whole steps of 64 before the next sequence's.
+__host__ __device__ __forceinline__ long long pad_row(int q0, int b) { return (q0 & ~63) + 64ll * b; }
+// Number of its first key tile among all sequences' (k0: its first key), with a number
+// for each of its tiles before the next sequence's.
+__host__ __device__ __forceinline__ long long tile_slot(int k0, int b) { return k0 / 128 + static_cast<long long>(b); }
 
 constexpr int kBwdKeys = 128;   // keys per CTA (TMEM lanes of S^T, dP^T, dV, dK)
 constexpr int kBwdHalf = 64;    // queries per step
@@ -199,12 +215,12 @@ __device__ __forceinline__ void bwd_steps(const BwdParams& p, int kt, int& h0, i
 // The steps of a key tile under a window: rows from the one at its first key to
 // the last whose window reaches its last key, or to the end where the tile
 // holds a sink.
-__device__ __forceinline__ void bwd_steps_win(const BwdParams& p, int kt, int& h0, int& n) {
-    const int off = p.Nk - p.Nq;
+__device__ __forceinline__ void bwd_steps_win(const BwdParams& p, int Nq, int Nk, int kt, int& h0, int& n) {
+    const int off = Nk - Nq;
     const int k0 = kt * kBwdKeys;
-    const int k1 = min(k0 + kBwdKeys, p.Nk) - 1;
+    const int k1 = min(k0 + kBwdKeys, Nk) - 1;
     const int first = max(0, k0 - off);
-    int last = p.Nq - 1;
+    int last = Nq - 1;
     if (p.window > 0 && k0 >= p.sinks) last = min(last, k1 - off + p.window - 1);
     h0 = first / kBwdHalf;
     n = last < first ? 0 : last / kBwdHalf - h0 + 1;
@@ -258,6 +274,62 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
     }
 }
 
+// A packed batch's unit: its sequence (number b), key tile and part, and the number of
+// its first part's partial sums.
+struct BwdUnit {
+    PackedSeq s;
+    int b, kt, part, parts;
+    long long sums;
+    bool live;
+};
+__device__ __forceinline__ int key_tiles(const PackedSeq& s) { return (s.m + kBwdKeys - 1) / kBwdKeys; }
+// Number of the partial sums of tile kt, kv head h.
+__device__ __forceinline__ long long bwd_sums(const BwdParams& p, const PackedSeq& s, int b, int kt, int h) {
+    if (kt < p.sink_tiles) return ((static_cast<long long>(b) * p.sink_tiles + kt) * p.Hkv + h) * p.sink_parts;
+    const long long sinks = p.sink_parts > 1 ? static_cast<long long>(p.seqs.B) * p.sink_tiles * p.Hkv * p.sink_parts : 0;
+    return sinks + ((tile_slot(s.k0, b) + kt) * p.Hkv + h) * p.parts;
+}
+// Unit number `at` of a kv head, found by one warp: the sinks' tiles first, then the
+// others; of each, a tile's parts beside one another.
+__device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h, int lane, BwdUnit* u) {
+    PackedSeq s;
+    if (blockIdx.x == 0)
+        for (int b = lane; b < p.seqs.B; b += 32)
+            if (!packed_seq(p.seqs, b, s)) atomicOr(p.status, kStatusBadSeqlens);
+    int sinks = 0;  // units of the sinks' tiles
+    if (p.sink_tiles > 0) {
+        for (int b = lane; b < p.seqs.B; b += 32) {
+            packed_seq(p.seqs, b, s);
+            sinks += min(key_tiles(s), p.sink_tiles);
+        }
+        sinks = __reduce_add_sync(0xffffffffu, sinks) * p.sink_parts;
+    }
+    const bool sink = at < sinks;
+    const int parts = sink ? p.sink_parts : p.parts, r = (sink ? at : at - sinks) / parts;
+    // Levels count a sequence's tiles from its last one up.
+    auto runs = [&](int b, int& a, int& n) {
+        PackedSeq y;
+        packed_seq(p.seqs, b, y);
+        const int tiles = key_tiles(y), first = min(tiles, p.sink_tiles);
+        a = sink ? tiles - first : 0;
+        n = sink ? first : tiles - first;
+    };
+    int b = 0, level = 0;
+    const bool live = packed_pick(p.seqs.B, r, lane, runs, b, level);
+    if (lane == 0) {
+        *u = {};
+        u->live = live;
+        if (live) {
+            packed_seq(p.seqs, b, u->s);
+            u->b = b;
+            u->kt = key_tiles(u->s) - 1 - level;
+            u->parts = parts;
+            u->part = (sink ? at : at - sinks) % parts;
+            u->sums = bwd_sums(p, u->s, b, u->kt, h);
+        }
+    }
+}
+
 // One CTA per (head, key-tile unit, head-dim part), stepping over the queries
 // 64 at a time. A unit is one 128-key tile, or under a causal mask the pair of
 // tiles kt and k_tiles - 1 - kt, run one after the other: the steps of a tile
@@ -283,8 +355,15 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
 // sinks' first. P and dS are rounded to bf16 for their products here as well: the
 // other operands (dO, Q, K) are bf16, which f16 does not hold, and kind::f16 takes
 // both in one type.
-template <int D, bool WIN = false>
+//   PACK: the same on packed sequences. Units are taken longest first over all
+// sequences (packed_pick: a key tile sees the more rows the further it lies from its
+// sequence's end), the sinks' first. Rows of a tile that are not the sequence's (its
+// last keys', its last step's queries') hold other tokens: the issuer overwrites them
+// with zeros before the MMAs read them, since a weight of zero does not undo an
+// infinity or a NaN.
+template <int D, bool WIN = false, bool PACK = false>
 __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
+    static_assert(WIN || !PACK, "packed sequences take the window's form");
     using L = LayoutBwd<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -298,10 +377,22 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     // CTA = (head, key-tile unit, head-dim part), the part fastest.
     const int hd = static_cast<int>(blockIdx.x % L::HALVES);
     const int unit_lin = static_cast<int>(blockIdx.x / L::HALVES);
-    const int bh = WIN ? unit_lin % p.BHkv : unit_lin / p.tile_units;
+    const int bh = WIN ? unit_lin % p.BHkv : unit_lin / p.tile_units;  // (PACK: the kv head)
     int ui = WIN ? unit_lin / p.BHkv : unit_lin % p.tile_units;
     int part = 0, parts = 1;
-    if constexpr (WIN) {
+    BwdUnit u = {};
+    if constexpr (PACK) {
+        __shared__ BwdUnit unit;
+        if (warp == 2) bwd_pack_unit(p, ui, bh, lane, &unit);
+        __syncthreads();
+        u = unit;
+        if (!u.live) return;
+        ui = u.kt;
+        part = u.part;
+        parts = u.parts;
+    }
+    const int Nq = PACK ? u.s.n : p.Nq, Nk = PACK ? u.s.m : p.Nk;
+    if constexpr (WIN && !PACK) {
         const int sink_units = p.sink_tiles * p.sink_parts;
         const bool sink = ui < sink_units;
         parts = sink ? p.sink_parts : p.parts;
@@ -318,7 +409,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     } else {
         kts[1] = ui;
     }
-    if constexpr (WIN) bwd_steps_win(p, kts[0], h0s[0], ns[0]);
+    if constexpr (WIN) bwd_steps_win(p, Nq, Nk, kts[0], h0s[0], ns[0]);
     else bwd_steps(p, kts[0], h0s[0], ns[0]);
     if (nt == 2) bwd_steps(p, kts[1], h0s[1], ns[1]);
     else ns[1] = 0, h0s[1] = 0;
@@ -344,8 +435,14 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
     auto NS = [&](int tt) {
         return WIN ? max(0, min(s1 - (head_first + tt) * ns[0], ns[0]) - HB(tt)) : ns[tt];
     };
-    auto ZQ = [&](int tt) { return WIN ? (bh / p.Hkv) * p.H + (bh % p.Hkv) * p.group + head_first + tt : bh; };
-    auto ROW0 = [&](int tt) { return static_cast<size_t>(ZQ(tt)) * p.Nq_pad; };
+    auto ZQ = [&](int tt) {
+        return PACK ? bh * p.group + head_first + tt
+                    : WIN ? (bh / p.Hkv) * p.H + (bh % p.Hkv) * p.group + head_first + tt : bh;
+    };
+    auto ROW0 = [&](int tt) {
+        return PACK ? static_cast<size_t>(ZQ(tt)) * p.rows_pad + pad_row(u.s.q0, u.b)
+                    : static_cast<size_t>(ZQ(tt)) * p.Nq_pad;
+    };
 
     if (threadIdx.x == 0) {
         mbar_init(bar(L::BAR_KV), 1);
@@ -406,7 +503,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                                                       kStatusWaitKvEmpty));
             if (!ok) break;
             if (leader && (!WIN || tt == 0)) {
-                const int k0 = KT(tt) * kBwdKeys;
+                const int k0 = (PACK ? u.s.k0 : 0) + KT(tt) * kBwdKeys;
                 mbar_arrive_expect_tx(bar(L::BAR_KV), 2 * L::V_BYTES);
                 for (int c = 0; c < L::CHUNKS; ++c) {
                     tma_load_3d(sbase + L::K_OFF + c * L::KV_CHUNK, &p.tm_k, bar(L::BAR_KV), 64 * c, k0, bh);
@@ -426,9 +523,10 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                     const uint32_t sb = sbase + L::STAGE_OFF + st * L::STAGE_BYTES;
                     const uint32_t rb = sbase + L::ROWS_OFF + st * 2 * L::ROWS_BYTES;
                     mbar_arrive_expect_tx(bar(L::BAR_QFULL + st), L::STAGE_BYTES + 2 * L::ROWS_BYTES);
+                    const int y = (PACK ? u.s.q0 : 0) + q0;
                     for (int c = 0; c < L::CHUNKS; ++c) {
-                        tma_load_3d(sb + L::Q_IN + c * L::QH_CHUNK, &p.tm_q, bar(L::BAR_QFULL + st), 64 * c, q0, zq);
-                        tma_load_3d(sb + L::DO_IN + c * L::QH_CHUNK, &p.tm_do, bar(L::BAR_QFULL + st), 64 * c, q0,
+                        tma_load_3d(sb + L::Q_IN + c * L::QH_CHUNK, &p.tm_q, bar(L::BAR_QFULL + st), 64 * c, y, zq);
+                        tma_load_3d(sb + L::DO_IN + c * L::QH_CHUNK, &p.tm_do, bar(L::BAR_QFULL + st), 64 * c, y,
                                     zq);
                     }
                     bulk_load(rb + L::NL_IN, p.nlse2 + row0 + q0, L::ROWS_BYTES, bar(L::BAR_QFULL + st));
@@ -473,8 +571,12 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         // S^T_G = K Q_G^T and dP^T_G = V dO_G^T into buffer G & 1 (lanes = keys,
         // 64 query columns each), reading ring slot G % STAGES; first, from
         // G = 2 on, the readout group must have taken that buffer's dQ^T of two
-        // steps back out.
-        auto issue_sdp = [&](int G) -> bool {
+        // steps back out. `rows`: the step's queries that the sequence has (PACK).
+        auto clear_rows = [&](uint32_t tile, int from, int rows) {  // rows from .. rows - 1 of 128 bytes
+            for (int at = from * 128 + lane * 16; at < rows * 128; at += 512)
+                st_shared_v4(sbase + tile + at, 0u, 0u, 0u, 0u);
+        };
+        auto issue_sdp = [&](int G, int rows) -> bool {
             if (G >= 2) {
                 if (!wait_all(bar(L::BAR_DQREAD + (G & 1)), ((G - 2) >> 1) & 1, kStatusWaitO)) return false;
             }
@@ -482,6 +584,13 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             if (!wait_all(bar(L::BAR_QFULL + st), (G / L::STAGES) & 1, kStatusWaitQ)) return false;
             tc_fence_after();
             const uint32_t sb = L::STAGE_OFF + st * L::STAGE_BYTES;
+            if constexpr (PACK) {
+                if (rows < kBwdHalf) {
+                    for (int c = 0; c < 2 * L::CHUNKS; ++c) clear_rows(sb + c * L::QH_CHUNK, rows, kBwdHalf);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
             const uint32_t col = L::BUF_COL(G & 1);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -549,6 +658,19 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             }
             if (!ok) break;
             tc_fence_after();
+            if constexpr (PACK) {
+                const int keys = Nk - KT(0) * kBwdKeys;
+                if (tt == 0 && keys < kBwdKeys) {
+                    for (int c = 0; c < L::CHUNKS; ++c) {
+                        clear_rows(L::K_OFF + c * L::KV_CHUNK, keys, kBwdKeys);
+                        clear_rows(L::V_OFF + c * L::KV_CHUNK, keys, kBwdKeys);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            // Queries of the pass's step h that the sequence has.
+            auto left = [&](int h) { return PACK ? Nq - (H0(tt) + h) * kBwdHalf : kBwdHalf; };
             // The tile's first MMA into dV and dK waits until the compute group
             // has read the previous tile's out of TMEM.
             auto first_vkq = [&](int G) -> bool {
@@ -559,22 +681,22 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                 return issue_vkq(G, !WIN || tt == 0);
             };
             if constexpr (L::STAGES >= 3) {
-                if (ok) ok = issue_sdp(gb);
-                if (ok && n > 1) ok = issue_sdp(gb + 1);
+                if (ok) ok = issue_sdp(gb, left(0));
+                if (ok && n > 1) ok = issue_sdp(gb + 1, left(1));
                 for (int a = 0; a < n && ok; a += 2) {
                     ok = a == 0 ? first_vkq(gb) : issue_vkq(gb + a, false);
                     if (ok && a + 1 < n) ok = issue_vkq(gb + a + 1, false);
                     // The next pair's S^T and dP^T.
-                    for (int h = a + 2; h < a + 4 && h < n && ok; ++h) ok = issue_sdp(gb + h);
+                    for (int h = a + 2; h < a + 4 && h < n && ok; ++h) ok = issue_sdp(gb + h, left(h));
                 }
             } else {
                 // One stage: step G + 1's Q and dO load once step G's dV and dK
                 // MMAs have read the stage, so its S^T and dP^T follow step G's
                 // MMAs.
-                if (ok) ok = issue_sdp(gb);
+                if (ok) ok = issue_sdp(gb, left(0));
                 for (int h = 0; h < n && ok; ++h) {
                     ok = h == 0 ? first_vkq(gb) : issue_vkq(gb + h, false);
-                    if (ok && h + 1 < n) ok = issue_sdp(gb + h + 1);
+                    if (ok && h + 1 < n) ok = issue_sdp(gb + h + 1, left(h + 1));
                 }
             }
             // K and V free for the next tile once every MMA so far is done.
@@ -589,7 +711,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         const int g = (warp - 4) >> 2;       // 32-query chunk of each step
         const int r = quarter * 32 + lane;   // TMEM lane: key row
         const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
-        const int off = p.causal_br ? p.Nk - p.Nq : 0;
+        const int off = p.causal_br ? Nk - Nq : 0;
         const float sl2 = p.scale_log2;
         bool ok = true;
         int gb = 0;
@@ -598,8 +720,8 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             const int h0 = H0(tt);
             const int k0 = KT(tt) * kBwdKeys;
             const int key = k0 + r;
-            const bool key_ok = key < p.Nk;
-            const bool key_tail = k0 + kBwdKeys > p.Nk;
+            const bool key_ok = key < Nk;
+            const bool key_tail = k0 + kBwdKeys > Nk;
             for (int h = 0; h < n && ok; ++h) {
                 const int G = gb + h;
                 const int b = G & 1;
@@ -671,10 +793,13 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             }
             if (ok && last_pass) {
                 // This CTA's head-dim part of the key row's dK and dV.
-                __nv_bfloat16* dkp =
-                    static_cast<__nv_bfloat16*>(p.dk) + (static_cast<size_t>(bh) * p.Nk + key) * D + hd * L::DH;
-                __nv_bfloat16* dvp =
-                    static_cast<__nv_bfloat16*>(p.dv) + (static_cast<size_t>(bh) * p.Nk + key) * D + hd * L::DH;
+                size_t at_k = (static_cast<size_t>(bh) * p.Nk + key) * D, at_v = at_k;
+                if constexpr (PACK) {
+                    at_k = static_cast<size_t>(u.s.k0 + key) * p.dk_stride + static_cast<size_t>(bh) * D;
+                    at_v = static_cast<size_t>(u.s.k0 + key) * p.dv_stride + static_cast<size_t>(bh) * D;
+                }
+                __nv_bfloat16* dkp = static_cast<__nv_bfloat16*>(p.dk) + at_k + hd * L::DH;
+                __nv_bfloat16* dvp = static_cast<__nv_bfloat16*>(p.dv) + at_v + hd * L::DH;
 #pragma unroll 1
                 for (int j = 0; j < L::DH_CHUNKS; ++j) {
                     const int cc = L::DH_CHUNKS * g + j;
@@ -694,8 +819,9 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                     }
                     if constexpr (WIN) {
                         if (parts > 1) {
-                            float* at = p.dkv_part + (static_cast<size_t>(unit_lin) * 2 * kBwdKeys + r) * D +
-                                        hd * L::DH + cc * 32;
+                            const size_t unit = PACK ? static_cast<size_t>(u.sums + part)
+                                                     : static_cast<size_t>(unit_lin);
+                            float* at = p.dkv_part + (unit * 2 * kBwdKeys + r) * D + hd * L::DH + cc * 32;
                             uint4* dk4 = reinterpret_cast<uint4*>(at);
                             uint4* dv4 = reinterpret_cast<uint4*>(at + kBwdKeys * D);
 #pragma unroll
@@ -977,6 +1103,193 @@ __global__ void __launch_bounds__(256) fa_bwd_win_post_kernel(const __grid_const
         is_v ? 1.f : p.scale);
 }
 
+// The sequence that padded row `row` (a multiple of 64) or, by `tiles`, key tile `row`
+// belongs to, found by one warp: its number, or -1. Sixty-four padded rows or a tile
+// have one sequence at most.
+__device__ __forceinline__ int bwd_pack_find(const BwdParams& p, long long row, bool tiles, int lane, PackedSeq& s) {
+    for (int c = 0; c < p.seqs.B; c += 32) {
+        const int b = c + lane;
+        PackedSeq y = {0, 0, 0, 0};
+        bool here = b < p.seqs.B && packed_seq(p.seqs, b, y);
+        if (here) {
+            const long long at = row - (tiles ? tile_slot(y.k0, b) : pad_row(y.q0, b));
+            here = at >= 0 && at < (tiles ? key_tiles(y) : y.n);
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, here);
+        if (who) {
+            const int from = __ffs(who) - 1;
+            s.q0 = __shfl_sync(0xffffffffu, y.q0, from);
+            s.n = __shfl_sync(0xffffffffu, y.n, from);
+            s.k0 = __shfl_sync(0xffffffffu, y.k0, from);
+            s.m = __shfl_sync(0xffffffffu, y.m, from);
+            return c + from;
+        }
+    }
+    return -1;
+}
+struct BwdPlace {
+    PackedSeq s;
+    int b;
+};
+
+// Sixteen bytes of a row in fp32, and the dot product over a row's LANES threads.
+__device__ __forceinline__ void bwd_load8(const __nv_bfloat16* src, float (&x)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(src);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+}
+template <int LANES>
+__device__ __forceinline__ float bwd_dot(unsigned mine, const float (&a)[8], const float (&b)[8]) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+    for (int w = LANES / 2; w > 0; w >>= 1) s += __shfl_xor_sync(mine, s, w);
+    return s;
+}
+
+// fa_bwd_win_pre_kernel on packed sequences: a block takes 64 padded rows of a head,
+// which are one sequence's.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_pack_pre_kernel(const __nv_bfloat16* __restrict__ q,
+                                                              const __nv_bfloat16* __restrict__ k,
+                                                              const __nv_bfloat16* __restrict__ v,
+                                                              const __nv_bfloat16* __restrict__ o,
+                                                              const __nv_bfloat16* __restrict__ dout,
+                                                              const float* __restrict__ lse,
+                                                              const __grid_constant__ BwdParams p) {
+    constexpr int LANES = D / 8, ROWS = 256 / LANES;
+    __shared__ BwdPlace place;
+    const int lane = threadIdx.x % LANES, h = blockIdx.y, c = lane * 8;
+    const long long first = static_cast<long long>(blockIdx.x) * kBwdHalf;
+    if (threadIdx.x < 32) {
+        BwdPlace x = {};
+        x.b = bwd_pack_find(p, first, false, threadIdx.x, x.s);
+        if (threadIdx.x == 0) place = x;
+    }
+    __syncthreads();
+    if (place.b < 0) return;
+    const PackedSeq s = place.s;
+    const int i0 = static_cast<int>(first - pad_row(s.q0, place.b));
+    const unsigned mine = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
+#pragma unroll 2
+    for (int r = threadIdx.x / LANES; r < kBwdHalf; r += ROWS) {
+        const int i = i0 + r;
+        const long long row = static_cast<long long>(h) * p.rows_pad + first + r;
+        float dd = 0.f, nl = -INFINITY;
+        if (i < s.n) {
+            float4* z = reinterpret_cast<float4*>(p.dq_acc + row * D);
+            z[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+            z[lane + LANES] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const long long token = s.q0 + i;
+            const float l = lse[static_cast<long long>(h) * p.seqs.total_q + token];
+            float g[8], a[8];
+            bwd_load8(dout + token * p.do_stride + static_cast<long long>(h) * D + c, g);
+            nl = (l == -INFINITY) ? -INFINITY : -(l * kLog2e);
+            // Visible keys: [0, ns) and [w0, pos].
+            const int pos = i + s.m - s.n;
+            const int w0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+            const int ns = min(p.sinks, w0);
+            const int seen = pos < 0 ? 0 : ns + pos + 1 - w0;
+            if (seen > kFewKeys) {
+                bwd_load8(o + (token * p.H + h) * D + c, a);
+                dd = bwd_dot<LANES>(mine, a, g);
+            } else if (nl != -INFINITY) {
+                bwd_load8(q + token * p.q_stride + static_cast<long long>(h) * D + c, a);
+                const long long head = static_cast<long long>(h / p.group) * D + c;
+                for (int n = 0; n < seen; ++n) {
+                    const long long key = s.k0 + (n < ns ? n : w0 + (n - ns));
+                    float kr[8], vr[8];
+                    bwd_load8(k + key * p.k_stride + head, kr);
+                    bwd_load8(v + key * p.v_stride + head, vr);
+                    dd = fmaf(ex2(fmaf(bwd_dot<LANES>(mine, a, kr), p.scale_log2, nl)), bwd_dot<LANES>(mine, g, vr), dd);
+                }
+            }
+        }
+        if (lane == 0) {
+            const_cast<float*>(p.ndd)[row] = -dd;
+            const_cast<float*>(p.nlse2)[row] = nl;
+        }
+    }
+}
+
+// The last launch on packed sequences: a block writes dQ of 64 padded rows of a head,
+// or, behind those, dK or dV of a key tile whose sums were left in parts, added part by
+// part in order. Rows that belong to no sequence get zeros where the call asks for it.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_pack_post_kernel(const __grid_constant__ BwdParams p,
+                                                               __nv_bfloat16* __restrict__ dq, long long q_blocks) {
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
+    constexpr int LANES = D / 8, ROWS = 256 / LANES;
+    __shared__ BwdPlace place;
+    const int lane = threadIdx.x % LANES, c = lane * 8;
+    auto put = [&](__nv_bfloat16* dst, const float (&x)[8], float f) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
+                                                    pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
+    };
+    auto get = [&](const float* src, float (&x)[8]) {
+        const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    };
+    const bool is_q = blockIdx.x < q_blocks;
+    long long lin = is_q ? blockIdx.x : blockIdx.x - q_blocks;
+    const int heads = is_q ? p.H : 2 * p.Hkv;
+    const int h = static_cast<int>(lin % heads);
+    lin /= heads;
+    const long long first = is_q ? lin * kBwdHalf : lin;  // padded row, or tile
+    if (threadIdx.x < 32) {
+        BwdPlace x = {};
+        x.b = bwd_pack_find(p, first, !is_q, threadIdx.x, x.s);
+        if (threadIdx.x == 0) place = x;
+    }
+    __syncthreads();
+    const PackedSeq s = place.s;
+    if (place.b >= 0 && is_q) {
+        const int i0 = static_cast<int>(first - pad_row(s.q0, place.b));
+#pragma unroll
+        for (int e = 0; e < kBwdHalf / ROWS; ++e) {
+            const int r = e * ROWS + threadIdx.x / LANES;
+            if (i0 + r >= s.n) continue;
+            float x[8];
+            get(p.dq_acc + (static_cast<long long>(h) * p.rows_pad + first + r) * D + c, x);
+            put(dq + (static_cast<long long>(s.q0) + i0 + r) * p.dq_stride + static_cast<long long>(h) * D + c, x, p.scale);
+        }
+    } else if (place.b >= 0) {
+        const int kt = static_cast<int>(first - tile_slot(s.k0, place.b)), head = h >> 1, is_v = h & 1;
+        const int parts = kt < p.sink_tiles ? p.sink_parts : p.parts;
+        const long long sums = bwd_sums(p, s, place.b, kt, head);
+        for (int r = threadIdx.x / LANES; r < kBwdKeys && parts > 1; r += ROWS) {
+            const int key = kt * kBwdKeys + r;
+            if (key >= s.m) break;
+            float x[8], y[8];
+            for (int i = 0; i < parts; ++i) {
+                get(p.dkv_part + (((sums + i) * 2 + is_v) * kBwdKeys + r) * D + c, y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = i == 0 ? y[e] : x[e] + y[e];
+            }
+            put(static_cast<__nv_bfloat16*>(is_v ? p.dv : p.dk) +
+                    (static_cast<long long>(s.k0) + key) * (is_v ? p.dv_stride : p.dk_stride) +
+                    static_cast<long long>(head) * D + c,
+                x, is_v ? 1.f : p.scale);
+        }
+    }
+    if (!p.fill) return;
+    auto zeros = [&](__nv_bfloat16* dst, const int* cu, int total, int n, long long stride) {
+        const int c0 = cu[0], c1 = cu[p.seqs.B];
+        if (!(0 <= c0 && c0 <= c1 && c1 <= total)) return;
+        for (long long i = blockIdx.x; i < total - (c1 - c0); i += gridDim.x)
+            for (int e = threadIdx.x; e < n * LANES; e += 256)
+                *reinterpret_cast<uint4*>(dst + (i < c0 ? i : i + (c1 - c0)) * stride + e * 8) = make_uint4(0u, 0u, 0u, 0u);
+    };
+    zeros(dq, p.seqs.cu_q, p.seqs.total_q, p.H, p.dq_stride);
+    zeros(static_cast<__nv_bfloat16*>(p.dk), p.seqs.cu_k, p.seqs.total_k, p.Hkv, p.dk_stride);
+    zeros(static_cast<__nv_bfloat16*>(p.dv), p.seqs.cu_k, p.seqs.total_k, p.Hkv, p.dv_stride);
+}
+
 // How a windowed backward is cut into parts (host side). Each step of a CTA
 // takes about as long as any other, a CTA's start and end about kUnitCost
 // steps, leaving and adding partial sums kPartCost more; 152 CTAs run at once.
@@ -1016,6 +1329,48 @@ BwdParts bwd_parts(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int
     return c;
 }
 
+// The same for a packed batch, whose lengths the host does not know: the longest CTA
+// against an even share of the steps that sequences of the longest length would have.
+struct BwdPackParts {
+    int sink_tiles, sink_parts, parts;
+    long long tiles, slots;  // key tiles at most, and the numbers that tile_slot gives them
+    size_t part_floats;
+};
+BwdPackParts bwd_pack_parts(int B, int total_k, int max_q, int max_k, int H, int Hkv, int d, int window, int sinks) {
+    constexpr long long kUnitCost = 4, kPartCost = 6;
+    BwdPackParts c = {0, 1, 1, 0, 0, 0};
+    const long long halves = d == 256 ? 2 : 1, G = H / Hkv, seqs = std::min(B, total_k);
+    const long long k_tiles = (static_cast<long long>(max_k) + kBwdKeys - 1) / kBwdKeys;
+    c.tiles = std::min((total_k + seqs * (kBwdKeys - 1)) / kBwdKeys, seqs * k_tiles);
+    c.slots = total_k / kBwdKeys + static_cast<long long>(B) + 1;
+    const long long all = (static_cast<long long>(max_q) + kBwdHalf - 1) / kBwdHalf;
+    if (window > 0)
+        c.sink_tiles = static_cast<int>(std::min(k_tiles, (static_cast<long long>(sinks) + kBwdKeys - 1) / kBwdKeys));
+    const long long reach =
+        window > 0 ? std::min(all, (kBwdKeys + static_cast<long long>(window) + kBwdHalf - 2) / kBwdHalf + 1) : all;
+    const long long steps = G * reach, sink_steps = G * all, heads = Hkv * halves;
+    const long long sink_units = std::min(c.tiles, seqs * c.sink_tiles), others = c.tiles - sink_units;
+    // (Without a window half of a causal sequence's steps are not there.)
+    const double work = static_cast<double>(heads) * (static_cast<double>(others) * steps * (window > 0 ? 1. : 0.5) +
+                                                      static_cast<double>(sink_units) * sink_steps * 0.5);
+    double best = -1.;
+    for (long long p = 1; p <= 16 && (p == 1 || p <= steps); ++p) {
+        const long long piece = std::max(8ll, (steps + p - 1) / p);
+        const long long sp = c.sink_tiles > 0 ? std::min(64ll, (sink_steps + piece - 1) / piece) : 1;
+        const double extra = kUnitCost + (p > 1 ? kPartCost : 0);
+        const double longest = static_cast<double>(
+            std::max((steps + p - 1) / p, c.sink_tiles > 0 ? (sink_steps + sp - 1) / sp : 0)) + extra;
+        const double even = (work + static_cast<double>(heads) * (others * p + sink_units * sp) * extra) / 152.;
+        const double cost = std::max(longest, even);
+        if (best < 0. || cost < 0.9 * best) best = cost, c.parts = static_cast<int>(p), c.sink_parts = static_cast<int>(sp);
+    }
+    const long long sums = (c.sink_parts > 1 ? static_cast<long long>(B) * c.sink_tiles * Hkv * c.sink_parts : 0) +
+                           (c.parts > 1 ? c.slots * Hkv * c.parts : 0);
+    c.part_floats = static_cast<size_t>(sums) * 2 * kBwdKeys * d;
+    return c;
+}
+long long packed_rows_pad(int total_q, int B) { return (total_q + 64ll * (B + 1ll) + 127) / 128 * 128; }
+
 }  // namespace
 
 template <int D>
@@ -1030,7 +1385,7 @@ cudaError_t launch_bwd_pre(const void* o, const void* dout, const float* lse, fl
     return cudaGetLastError();
 }
 
-template <int D, bool WIN>
+template <int D, bool WIN, bool PACK = false>
 cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
     using L = LayoutBwd<D>;
     // Kernel attributes belong to the context: set once per device and context.
@@ -1038,16 +1393,17 @@ cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         *out = 1;
-        return cudaFuncSetAttribute(fa_bwd_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_bwd_kernel<D, WIN, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC_BYTES));
     });
     if (e != cudaSuccess) return e;
-    const long long units = WIN ? static_cast<long long>(p.BHkv) * (p.sink_tiles * p.sink_parts +
+    const long long units = PACK  ? p.tile_units * static_cast<long long>(p.Hkv)
+                            : WIN ? static_cast<long long>(p.BHkv) * (p.sink_tiles * p.sink_parts +
                                                                       (p.k_tiles - p.sink_tiles) * p.parts)
                                 : static_cast<long long>(p.BH) * p.tile_units;
     const long long ctas = units * L::HALVES;
     if (ctas < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    fa_bwd_kernel<D, WIN><<<static_cast<unsigned>(ctas), L::THREADS, L::ALLOC_BYTES, stream>>>(p);
+    fa_bwd_kernel<D, WIN, PACK><<<static_cast<unsigned>(ctas), L::THREADS, L::ALLOC_BYTES, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -1096,6 +1452,24 @@ cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, con
     if (post > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_bwd_win_post_kernel<D>, dim3(static_cast<unsigned>(post)), 256, 0, stream, p,
                             static_cast<__nv_bfloat16*>(dq), q_rows, k_rows);
+}
+
+// The three launches on packed sequences.
+template <int D>
+cudaError_t launch_bwd_pack(const BwdParams& p, const void* q, const void* k, const void* v, const void* o,
+                            const void* dout, const float* lse, void* dq, long long slots, cudaStream_t stream) {
+    using T = const __nv_bfloat16*;
+    const dim3 grid(static_cast<unsigned>(p.rows_pad / kBwdHalf), static_cast<unsigned>(p.H), 1);
+    fa_bwd_pack_pre_kernel<D><<<grid, 256, 0, stream>>>(static_cast<T>(q), static_cast<T>(k), static_cast<T>(v),
+                                                        static_cast<T>(o), static_cast<T>(dout), lse, p);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_bwd_main<D, true, true>(p, stream);
+    if (e != cudaSuccess) return e;
+    const long long q_blocks = p.rows_pad / kBwdHalf * p.H;
+    const long long k_blocks = p.parts > 1 || p.sink_parts > 1 ? slots * 2 * p.Hkv : 0;
+    if (q_blocks + k_blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    return launch_dependent(fa_bwd_pack_post_kernel<D>, dim3(static_cast<unsigned>(q_blocks + k_blocks)), 256, 0, stream,
+                            p, static_cast<__nv_bfloat16*>(dq), q_blocks);
 }
 
 }  // namespace fa
@@ -1225,6 +1599,86 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
     const cudaError_t e = d == 64    ? fa::launch_bwd_win<64>(p, q, k, v, o, dout, lse, dq, stream)
                           : d == 128 ? fa::launch_bwd_win<128>(p, q, k, v, o, dout, lse, dq, stream)
                                      : fa::launch_bwd_win<256>(p, q, k, v, o, dout, lse, dq, stream);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_bwd_packed_workspace_bytes(int B, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int H, int Hkv,
+                                     int d, int window, int sinks) {
+    const int none = 0;
+    const fa_packed_batch c = {&none, &none, B, total_q, total_k, max_seqlen_q, max_seqlen_k};
+    if (fa::check_packed(&c, H, Hkv, d, 1.f, window, sinks) != FA_OK) return 0;
+    const size_t rows = static_cast<size_t>(fa::packed_rows_pad(total_q, B)) * H;
+    return (rows * (static_cast<size_t>(d) + 2) +
+            fa::bwd_pack_parts(B, total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks).part_floats) *
+           sizeof(float);
+}
+
+fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                        void* dq, void* dk, void* dv, void* workspace, const fa_packed_batch* batch, int H, int Hkv,
+                        int d, const fa_packed_strides* strides, float scale, int window, int sinks, int fill,
+                        cudaStream_t stream) {
+    if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !strides) return FA_ERR_NULL;
+    const fa_status s = fa::check_packed(batch, H, Hkv, d, scale, window, sinks);
+    if (s != FA_OK) return s;
+    for (const void* x : {q, k, v, o, dout, static_cast<const void*>(dq), static_cast<const void*>(dk),
+                          static_cast<const void*>(dv)})
+        if (!fa::aligned(x, 16)) return FA_ERR_ALIGN;
+    if (!fa::aligned(lse, 4)) return FA_ERR_ALIGN;
+    for (long long x : {strides->q, strides->dout, strides->dq})
+        if (!fa::token_stride(x, H, d)) return FA_ERR_STRIDE;
+    for (long long x : {strides->k, strides->v, strides->dk, strides->dv})
+        if (!fa::token_stride(x, Hkv, d)) return FA_ERR_STRIDE;
+    if (!workspace || !fa::aligned(workspace, 16)) return FA_ERR_WORKSPACE;
+    fa::BwdParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (!fa::encode_strided_tokens_map(&p.tm_q, q, d, batch->total_q, H, strides->q, fa::kBwdHalf) ||
+        !fa::encode_strided_tokens_map(&p.tm_do, dout, d, batch->total_q, H, strides->dout, fa::kBwdHalf) ||
+        !fa::encode_strided_tokens_map(&p.tm_k, k, d, batch->total_k, Hkv, strides->k, fa::kBwdKeys) ||
+        !fa::encode_strided_tokens_map(&p.tm_v, v, d, batch->total_k, Hkv, strides->v, fa::kBwdKeys))
+        return FA_ERR_CUDA;
+    p.rows_pad = fa::packed_rows_pad(batch->total_q, batch->B);
+    const size_t rows = static_cast<size_t>(p.rows_pad) * H;
+    float* ws = static_cast<float*>(workspace);
+    p.dq_acc = ws;
+    p.nlse2 = ws + rows * d;
+    p.ndd = p.nlse2 + rows;
+    p.dkv_part = ws + rows * (static_cast<size_t>(d) + 2);  // 16-byte aligned: rows_pad is a multiple of 128
+    p.dk = dk;
+    p.dv = dv;
+    p.H = H;
+    p.Hkv = p.BHkv = Hkv;
+    p.group = H / Hkv;
+    p.causal = 1;
+    p.causal_br = 1;
+    p.window = window;
+    p.sinks = sinks;
+    p.seqs = {batch->cu_seqlens_q, batch->cu_seqlens_k, batch->B,           batch->total_q,
+              batch->total_k,      batch->max_seqlen_q, batch->max_seqlen_k};
+    p.q_stride = strides->q;
+    p.k_stride = strides->k;
+    p.v_stride = strides->v;
+    p.do_stride = strides->dout;
+    p.dq_stride = strides->dq;
+    p.dk_stride = strides->dk;
+    p.dv_stride = strides->dv;
+    p.fill = fill ? 1 : 0;
+    const fa::BwdPackParts c = fa::bwd_pack_parts(batch->B, batch->total_k, batch->max_seqlen_q, batch->max_seqlen_k, H,
+                                                  Hkv, d, window, sinks);
+    p.sink_tiles = c.sink_tiles;
+    p.sink_parts = c.sink_parts;
+    p.parts = c.parts;
+    // Units of a kv head: no more sinks' tiles than the sequences have, the others for the rest.
+    const long long sink_units = std::min(c.tiles, static_cast<long long>(std::min(batch->B, batch->total_k)) * c.sink_tiles);
+    const long long units = sink_units * c.sink_parts + c.tiles * c.parts;
+    if (units * Hkv * 2 > 0x7fffffffll) return FA_ERR_SHAPE;
+    p.tile_units = static_cast<int>(units);
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.wait_limit = fa::kDefaultWaitLimit;
+    if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+    const cudaError_t e = d == 64    ? fa::launch_bwd_pack<64>(p, q, k, v, o, dout, lse, dq, c.slots, stream)
+                          : d == 128 ? fa::launch_bwd_pack<128>(p, q, k, v, o, dout, lse, dq, c.slots, stream)
+                                     : fa::launch_bwd_pack<256>(p, q, k, v, o, dout, lse, dq, c.slots, stream);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -355,6 +355,27 @@ fa_status fa_fwd_packed(const void* q, const void* k, const void* v, void* o, fl
                         long long v_stride, float scale, int window, int sinks, int fill, cudaStream_t stream);
 
 /*
+ * fa_bwd_packed — its backward: dq [total_q][H][d], dk, dv [total_k][Hkv][d] bf16 from
+ * q, k, v, the forward's o and lse, and dout [total_q][H][d]; every tensor but o and
+ * lse by the distance of its tokens in elements (multiples of 8, at least heads * d:
+ * the gradient of a fused projection may be written where it belongs). The gradients
+ * of a kv head are summed over its group, and dQ over key tiles, as in fa_bwd_window
+ * (fp32 atomics: dQ's last bits can differ between runs, dK's and dV's do not); P, dS
+ * and D as there. dout must be finite where it belongs to a sequence. Rows of dq, dk
+ * and dv that belong to no sequence are left as they are, or, with `fill` != 0, get 0.
+ * workspace: fa_bwd_packed_workspace_bytes, 16-byte aligned (0: arguments out of range).
+ */
+typedef struct {
+    long long q, k, v, dout, dq, dk, dv;
+} fa_packed_strides;
+size_t fa_bwd_packed_workspace_bytes(int B, int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int H, int Hkv,
+                                     int d, int window, int sinks);
+fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
+                        void* dq, void* dk, void* dv, void* workspace, const fa_packed_batch* batch, int H, int Hkv,
+                        int d, const fa_packed_strides* strides, float scale, int window, int sinks, int fill,
+                        cudaStream_t stream);
+
+/*
  * fa_rotation — rotary positions. The first `rot` columns of a head (rot a
  * multiple of 16, at most d; the others are left as they are) form rot / 2
  * pairs: columns (i, i + rot / 2), or (2 i, 2 i + 1) when `interleaved`. Pair i
