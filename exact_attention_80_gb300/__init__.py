@@ -111,6 +111,12 @@ def load_library() -> ctypes.CDLL:
     lib.fa_bwd_packed_workspace_bytes.restype = ctypes.c_size_t
     lib.fa_bwd_packed.argtypes = [vp] * 10 + [packed, i, i, i, packed, f, i, i, i, vp]
     lib.fa_bwd_packed.restype = i
+    lib.fa_prefix_num_splits.argtypes = [i] * 8 + [ctypes.POINTER(i)]
+    lib.fa_prefix_num_splits.restype = i
+    lib.fa_fwd_prefix_fp8.argtypes = [vp, packed, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, f, i, i, vp]
+    lib.fa_fwd_prefix_fp8.restype = i
+    lib.fa_kv_read_fp8.argtypes = [packed, vp, vp, vp, vp, vp, i, i, i, ll, ll, i, vp]
+    lib.fa_kv_read_fp8.restype = i
     lib.fa_fwd_grid_ctas.argtypes = [i, i, i, i, i]
     lib.fa_fwd_grid_ctas.restype = ctypes.c_longlong
     lib.fa_device_status.argtypes = [vp, i]
@@ -911,6 +917,120 @@ def attention_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
         o, lse = _paged(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
                         max_seqlen_q, max_seqlen_k, None, num_splits, window, sinks, scale, stream)
     return _given(stream, o, lse)
+
+
+def fa_prefix_num_splits(B: int, H: int, Hkv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int, prefix_len: int,
+                         d: int):
+    """The key splits the library proposes for a call with a shared prefix: of the sequences' own keys
+    and of the prefix (0 and 0 for arguments out of range)."""
+    shared = ctypes.c_int(0)
+    own = load_library().fa_prefix_num_splits(
+        *map(_int32, (B, H, Hkv, total_q, max_seqlen_q, max_seqlen_k, prefix_len, d)), ctypes.byref(shared))
+    return (own, shared.value) if own > 0 else (0, 0)
+
+
+def _prefix(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+            max_seqlen_k, prefix_len, workspace, num_splits, prefix_splits, scale, stream):
+    """The checks and the call of fa_fwd_prefix_fp8; ``o`` None: outputs and the workspace are allocated
+    (splits None: the library's proposal). Returns ``(o, lse)``."""
+    import torch
+
+    index = q.get_device()
+    n, H, d, qs = _tokens_view(q, "q", index)
+    if qs != H * d:
+        raise ValueError("q must be contiguous")
+    cache, hkv, width = _cache_view(k_cache, v_cache, k_scale, v_scale, index)
+    if width != d:
+        raise ValueError(f"q has head dim {d}, the cache {width}")
+    B, max_pages = _batch_view(page_table, cu_seqlens_q, seqlens_k, index)
+    for x in (max_seqlen_q, max_seqlen_k, prefix_len, num_splits or 1, prefix_splits or 1):
+        _int32(x)
+    if o is None:
+        own, shared = fa_prefix_num_splits(B, H, hkv, n, max_seqlen_q, max_seqlen_k, prefix_len, d)
+        num_splits = (own or 1) if num_splits is None else num_splits
+        prefix_splits = (shared or 1) if prefix_splits is None else prefix_splits
+        o = torch.empty((n, H, d), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((H, n), dtype=torch.float32, device=q.device)
+        nbytes = fa_paged_workspace_bytes(n, H, d, num_splits + prefix_splits)
+        workspace = torch.empty(max(1, nbytes // 4), dtype=torch.float32, device=q.device)
+    else:
+        _check_out(o, "o", (n, H, d), torch.bfloat16, index)
+        _check_out(lse, "lse", (H, n), torch.float32, index)
+        _need_workspace(workspace, fa_paged_workspace_bytes(n, H, d, num_splits + prefix_splits), "workspace", q.device)
+    st = _on_stream(index, stream, load_library().fa_fwd_prefix_fp8, q.data_ptr(), cache, page_table.data_ptr(),
+                    cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                    B, H, n, max_seqlen_q, max_seqlen_k, max_pages, prefix_len,
+                    default_scale(d) if scale is None else float(scale), num_splits, prefix_splits)
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_prefix_fp8")
+    return o, lse
+
+
+def fa_fwd_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k,
+                      max_seqlen_q: int, max_seqlen_k: int, prefix_len: int, workspace, num_splits: int = 1,
+                      prefix_splits: int = 1, scale: float | None = None, stream=None):
+    """:func:`fa_fwd_paged_fp8` for a batch whose sequences begin with the same ``prefix_len`` tokens, in
+    the same pages of the table, which are attended to once for all (include/fa.h,
+    fa_fwd_prefix_fp8). ``workspace`` fp32 of at least ``fa_paged_workspace_bytes`` bytes for
+    ``num_splits + prefix_splits`` splits."""
+    if o is None:
+        raise TypeError("o and lse must be tensors")
+    _prefix(q, k_cache, v_cache, k_scale, v_scale, o, lse, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+            max_seqlen_k, prefix_len, workspace, num_splits, prefix_splits, scale, stream)
+
+
+def attention_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_k,
+                         max_seqlen_q: int, max_seqlen_k: int, prefix_len: int, scale: float | None = None,
+                         num_splits: int | None = None, prefix_splits: int | None = None, stream=None):
+    """:func:`fa_fwd_prefix_fp8` into new outputs, with a workspace of its own (splits None: the
+    library's proposal). Returns ``(o, lse)``; rows past ``cu_seqlens_q[B]`` are left as allocated."""
+    with _allocating(stream, q):
+        o, lse = _prefix(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
+                         max_seqlen_q, max_seqlen_k, prefix_len, None, num_splits, prefix_splits, scale, stream)
+    return _given(stream, o, lse)
+
+
+def fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, k_out, v_out, page_table, cu_seqlens, starts=None,
+                   fill: bool = False, stream=None):
+    """Cached keys and values back as packed rows (include/fa.h, fa_kv_read_fp8) into caller-owned
+    ``k_out`` and ``v_out`` bf16 [total, Hkv, d], whose tokens may be strided: row
+    ``cu_seqlens[b] + i`` is token ``starts[b] + i`` of sequence b (``starts`` int32 [B], None: from
+    token 0 on). Rows that belong to no sequence stay as they are, or, with ``fill``, get 0."""
+    import torch
+
+    index = k_cache.get_device()
+    cache, hkv, d = _cache_view(k_cache, v_cache, k_scale, v_scale, index)
+    n, h, kd, ks = _tokens_view(k_out, "k_out", index)
+    vn, vh, vd, vs = _tokens_view(v_out, "v_out", index)
+    if (h, kd) != (hkv, d) or (vn, vh, vd) != (n, h, kd):
+        raise ValueError(f"k_out {tuple(k_out.shape)}, v_out {tuple(v_out.shape)} and a cache of {hkv} heads of {d} do "
+                         "not agree")
+    arrays = ((page_table, "page_table", 2), (cu_seqlens, "cu_seqlens", 1))
+    for t, name, dim in arrays if starts is None else (*arrays, (starts, "starts", 1)):
+        if t.dtype is not torch.int32 or t.dim() != dim or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError(f"{name} must be contiguous int32 with {dim} dimensions on device {index}")
+    B, max_pages = page_table.shape
+    if B < 1 or cu_seqlens.shape[0] != B + 1 or (starts is not None and starts.shape[0] != B):
+        raise ValueError("page_table [B, max_pages], cu_seqlens [B+1] and starts [B] must agree on B >= 1")
+    st = _on_stream(index, stream, load_library().fa_kv_read_fp8, cache, page_table.data_ptr(), cu_seqlens.data_ptr(),
+                    0 if starts is None else starts.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, _int32(n),
+                    max_pages, ks, vs, 1 if fill else 0)
+    if st != FA_OK:
+        raise FAError(st, "fa_kv_read_fp8")
+
+
+def kv_read_fp8(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, starts=None, total: int = 0, stream=None):
+    """:func:`fa_kv_read_fp8` into new tensors of ``total`` rows, at least ``cu_seqlens[B]``. Returns
+    ``(k, v)``; rows that belong to no sequence are 0."""
+    import torch
+
+    if total < 1:
+        raise ValueError("total must give the rows of k and v, at least one")
+    shape = (total, k_cache.shape[1], k_cache.shape[-1])
+    with _allocating(stream, k_cache):
+        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
+        fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, k, v, page_table, cu_seqlens, starts, True, stream)
+    return _given(stream, k, v)
 
 
 # ------------------------------------------------ sliding windows, grouped heads

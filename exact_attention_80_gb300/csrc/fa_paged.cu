@@ -205,26 +205,31 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     const int split = static_cast<int>(CLUSTER ? blockIdx.x % p.num_splits : lin % p.num_splits);
     if (!CLUSTER) lin /= p.num_splits;
     const int h = static_cast<int>(lin % p.Hkv);
-    const int b = static_cast<int>(lin / p.Hkv);
-    // (All CTAs of a cluster agree on the two returns below.)
+    int b = static_cast<int>(lin / p.Hkv);
+    // (All CTAs of a cluster agree on the returns below.)
     NewTokens nt;
-    if (!new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt)) {
+    if (!paged_tokens(p, b, nt)) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
         return;
     }
     const int rows = nt.n * p.G;
     const int r0 = rb * kRows;
     if (r0 >= rows) return;
-    const int start = nt.len - nt.n;  // position of the first query
-    const int p0 = start + r0 / p.G;
-    const int p1 = start + (min(r0 + kRows, rows) - 1) / p.G;
+    if (p.base_pages > 0) {
+        if (p.whole) b = paged_first(p, lane);
+        else if (h == 0 && rb == 0 && split == 0 && warp == 0) paged_check_prefix(p, b, lane);
+        if (b < 0) return;
+    }
+    const int start = paged_start(p, nt), step = paged_step(p);  // position of the first query
+    const int p0 = start + step * (r0 / p.G);
+    const int p1 = start + step * ((min(r0 + kRows, rows) - 1) / p.G);
     const KeyList list = key_list<KEYS>(p.window, p.sinks, p0, p1);
     const int used = max(1, (list.n + p.tiles_per_split - 1) / p.tiles_per_split);
     if (!CLUSTER && split >= used) return;
     const int i0 = split * p.tiles_per_split;
     const int i1 = min(list.n, i0 + p.tiles_per_split);
     const int mine = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);  // this warp's tiles: i0 + warp + 4 k
-    const int* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+    const int* table = paged_table(p, b);
     const int page_size = 1 << p.log_page;
     const int last_page = (nt.len - 1) >> p.log_page;
 
@@ -293,7 +298,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         const int r = r0 + g + 8 * e;
         const bool ok = r < rows;
         const int i = (ok ? r : r0) / p.G, j = (ok ? r : r0) - i * p.G;
-        pos[e] = ok ? start + i : p1;
+        pos[e] = ok ? start + step * i : p1;
         const __nv_bfloat16* src =
             p.q + (static_cast<long long>(nt.first + i) * p.H + h * p.G + j) * D + 16 * t;
         uint4 raw[C][2];
@@ -587,13 +592,14 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         }
         const long long row = place(r);
         // States that the row does not use are marked as empty for the merge.
+        const bool done = used == 1 && !p.join;
         if (split == 0 && p.num_splits > 1)
-            for (int s = (used == 1 ? 0 : used) + c; s < p.num_splits; s += VEC)
-                p.ws_m[static_cast<long long>(s) * p.total_q * p.H + row] = -INFINITY;
-        if (used == 1) {
+            for (int s = (done ? 0 : used) + c; s < p.num_splits; s += VEC)
+                p.ws_m[static_cast<long long>(p.state0 + s) * p.total_q * p.H + row] = -INFINITY;
+        if (done) {
             put(r, c, a, mm, ll);
         } else {
-            const long long at = static_cast<long long>(split) * p.total_q * p.H + row;
+            const long long at = static_cast<long long>(p.state0 + split) * p.total_q * p.H + row;
             *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
             if (c == 0) {
                 p.ws_m[at] = state_ref(mm, ll);
@@ -659,7 +665,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     const int i = static_cast<int>(rest % p.max_q);
     const int b = static_cast<int>(rest / p.max_q);
     NewTokens nt;
-    bool live = b < p.B && new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, nt) && i < nt.n;
+    bool live = b < p.B && paged_tokens(p, b, nt) && i < nt.n;
     const long long row = live ? static_cast<long long>(nt.first + i) * p.H + head : 0;
     const long long stride = static_cast<long long>(p.total_q) * p.H;
     const int states = live ? p.num_splits : 0;
@@ -845,7 +851,7 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    const long long ctas = static_cast<long long>(p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent_clusters(fa_paged_rows_kernel<D, CLUSTER>, dim3(static_cast<unsigned>(ctas)),
                                      CLUSTER ? static_cast<unsigned>(p.num_splits) : 1u, kWarps * 32, L::ALLOC, stream,
@@ -866,6 +872,93 @@ cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(four ? fa_paged_merge_kernel<D, 4> : fa_paged_merge_kernel<D, 1>,
                             dim3(static_cast<unsigned>(blocks)), 128, 0, stream, p);
+}
+
+// What the paged calls check alike: the cache, the batch's arrays and bounds, the
+// shape, the scale.
+fa_status check_paged(const void* q, const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens_q,
+                      const int* seqlens_k, const void* o, const float* lse, int B, int H, int total_q,
+                      int max_seqlen_q, int max_seqlen_k, int max_pages, float scale) {
+    if (!q || !cache || !page_table || !cu_seqlens_q || !seqlens_k || !o || !lse) return FA_ERR_NULL;
+    const fa_status sc = check_cache(cache);
+    if (sc != FA_OK) return sc;
+    const int Hkv = cache->Hkv;
+    if (B < 1 || H < 1 || total_q < 1 || max_seqlen_q < 1 || max_seqlen_q > total_q || max_seqlen_k < 1 ||
+        max_pages < 1)
+        return FA_ERR_SHAPE;
+    if (H < Hkv || H % Hkv) return FA_ERR_GROUP;
+    if (static_cast<long long>(max_pages) * cache->page_size > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
+    if (max_seqlen_k > max_pages * cache->page_size) return FA_ERR_SHAPE;
+    if (static_cast<long long>(max_seqlen_q) * (H / Hkv) > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_SCALE;
+    return FA_OK;
+}
+bool paged_aligned(const void* q, const void* o, const float* lse, const int* page_table, const int* cu_seqlens_q,
+                   const int* seqlens_k) {
+    return aligned(q, 16) && aligned(o, 16) && aligned(lse, 4) && aligned(page_table, 4) && aligned(cu_seqlens_q, 4) &&
+           aligned(seqlens_k, 4);
+}
+
+// The parameters of a launch over `seqs` sequences of at most max_q new tokens and max_k
+// keys, cut into num_splits; the cache's maps and the arrays are set already.
+void cut_paged(PagedParams& p, const Plan& c, int seqs, int max_q, int max_k, int num_splits) {
+    p.max_q = max_q;
+    p.max_k = max_k;
+    p.block_rows = c.block_rows;
+    p.block_keys = c.block_keys;
+    p.row_blocks = static_cast<int>(c.row_blocks);
+    p.num_splits = num_splits;
+    const long long row_warps = (static_cast<long long>(max_q) * p.G + 31) / 32;
+    p.shares = !c.dual ? 0 : row_warps > 2 ? 1 : row_warps == 2 ? 2 : 4;
+    p.slot_warps = p.shares == 1 ? static_cast<int>(row_warps) : 4;
+    p.balance = c.dual && num_splits > 1 && seqs > 1 && seqs <= kTcBalance;
+    p.tiles_per_split = static_cast<int>((c.tiles + num_splits - 1) / num_splits);
+}
+bool encode_cache(PagedParams& p, const fa_paged_cache* cache, const Plan& c) {
+    const long long rows = static_cast<long long>(cache->num_pages) * cache->Hkv * cache->page_size;
+    const int box = std::min(cache->page_size, c.block_keys);
+    return encode_cache_map(&p.tm_k, cache->k, cache->d, rows, box) &&
+           encode_cache_map(&p.tm_v, cache->v, cache->d, rows, box);
+}
+// Everything of a call that does not depend on how it is cut.
+cudaError_t fill_paged(PagedParams& p, const void* q, const fa_paged_cache* cache, const int* page_table,
+                       const int* cu_seqlens_q, const int* seqlens_k, void* o, float* lse, void* workspace, int B,
+                       int H, int total_q, int max_pages, int states, float scale) {
+    std::memset(&p, 0, sizeof(p));
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.k_scale = cache->k_scale;
+    p.v_scale = cache->v_scale;
+    p.page_table = page_table;
+    p.cu = cu_seqlens_q;
+    p.lens = seqlens_k;
+    if (states > 1) {
+        const size_t part = static_cast<size_t>(states) * total_q * H;
+        p.ws_o = static_cast<float*>(workspace);
+        p.ws_m = p.ws_o + part * cache->d;
+        p.ws_l = p.ws_m + part;
+    }
+    p.B = B;
+    p.H = H;
+    p.Hkv = cache->Hkv;
+    p.G = H / cache->Hkv;
+    p.total_q = total_q;
+    p.num_pages = cache->num_pages;
+    p.log_page = log2_exact(cache->page_size);
+    p.max_pages = max_pages;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.wait_limit = kDefaultWaitLimit;
+    return device_status_ptr(&p.status);
+}
+cudaError_t launch_paged(const PagedParams& p, const Plan& c, int d, cudaStream_t stream) {
+    return c.tc       ? launch_paged_tc(p, d, stream)
+           : d == 64  ? launch_rows<64, false>(p, stream)
+           : d == 128 ? launch_rows<128, false>(p, stream)
+                      : launch_rows<256, false>(p, stream);
+}
+cudaError_t launch_paged_merge(const PagedParams& p, int d, cudaStream_t stream) {
+    return d == 64 ? launch_merge<64>(p, stream) : d == 128 ? launch_merge<128>(p, stream) : launch_merge<256>(p, stream);
 }
 
 }  // namespace
@@ -892,84 +985,80 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
                            const int* seqlens_k, void* o, float* lse, void* workspace, int B, int H, int total_q,
                            int max_seqlen_q, int max_seqlen_k, int max_pages, float scale, int window, int sinks,
                            int num_splits, cudaStream_t stream) {
-    if (!q || !cache || !page_table || !cu_seqlens_q || !seqlens_k || !o || !lse) return FA_ERR_NULL;
-    const fa_status sc = fa::check_cache(cache);
+    const fa_status sc = fa::check_paged(q, cache, page_table, cu_seqlens_q, seqlens_k, o, lse, B, H, total_q, max_seqlen_q,
+                                         max_seqlen_k, max_pages, scale);
     if (sc != FA_OK) return sc;
-    const int Hkv = cache->Hkv, d = cache->d;
-    if (B < 1 || H < 1 || total_q < 1 || max_seqlen_q < 1 || max_seqlen_q > total_q || max_seqlen_k < 1 ||
-        max_pages < 1)
-        return FA_ERR_SHAPE;
-    if (H < Hkv || H % Hkv) return FA_ERR_GROUP;
-    if (static_cast<long long>(max_pages) * cache->page_size > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
-    if (max_seqlen_k > max_pages * cache->page_size) return FA_ERR_SHAPE;
-    if (static_cast<long long>(max_seqlen_q) * (H / Hkv) > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
-    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_SCALE;
     if (window < 0 || sinks < 0 || (window == 0 && sinks != 0) || sinks > 0x40000000 || window > 0x40000000)
         return FA_ERR_WINDOW;
     if (num_splits < 1 || num_splits > FA_MAX_SPLITS) return FA_ERR_SPLITS;
-    if (!fa::aligned(q, 16) || !fa::aligned(o, 16) || !fa::aligned(lse, 4) || !fa::aligned(page_table, 4) ||
-        !fa::aligned(cu_seqlens_q, 4) || !fa::aligned(seqlens_k, 4))
-        return FA_ERR_ALIGN;
+    if (!fa::paged_aligned(q, o, lse, page_table, cu_seqlens_q, seqlens_k)) return FA_ERR_ALIGN;
     if (num_splits > 1 && (!workspace || !fa::aligned(workspace, 16))) return FA_ERR_WORKSPACE;
+    const int d = cache->d;
     fa::PagedParams p;
-    std::memset(&p, 0, sizeof(p));
-    const long long rows = static_cast<long long>(cache->num_pages) * Hkv * cache->page_size;
-    const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k, d, window, sinks);
-    const int box = std::min(cache->page_size, c.block_keys);
-    if (!fa::encode_cache_map(&p.tm_k, cache->k, d, rows, box) || !fa::encode_cache_map(&p.tm_v, cache->v, d, rows, box))
+    if (fa::fill_paged(p, q, cache, page_table, cu_seqlens_q, seqlens_k, o, lse, workspace, B, H, total_q, max_pages,
+                       num_splits, scale) != cudaSuccess)
         return FA_ERR_CUDA;
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.o = static_cast<__nv_bfloat16*>(o);
-    p.lse = lse;
-    p.k_scale = cache->k_scale;
-    p.v_scale = cache->v_scale;
-    p.page_table = page_table;
-    p.cu = cu_seqlens_q;
-    p.lens = seqlens_k;
-    if (num_splits > 1) {
-        const size_t part = static_cast<size_t>(num_splits) * total_q * H;
-        p.ws_o = static_cast<float*>(workspace);
-        p.ws_m = p.ws_o + part * d;
-        p.ws_l = p.ws_m + part;
-    }
-    p.B = B;
-    p.H = H;
-    p.Hkv = Hkv;
-    p.G = H / Hkv;
-    p.total_q = total_q;
-    p.max_q = max_seqlen_q;
-    p.max_k = max_seqlen_k;
-    p.num_pages = cache->num_pages;
-    p.log_page = fa::log2_exact(cache->page_size);
-    p.max_pages = max_pages;
     p.window = window;
     p.sinks = sinks;
-    p.block_rows = c.block_rows;
-    p.block_keys = c.block_keys;
-    p.row_blocks = static_cast<int>(c.row_blocks);
-    p.num_splits = num_splits;
-    const int row_warps = (max_seqlen_q * p.G + 31) / 32;
-    p.shares = !c.dual ? 0 : row_warps > 2 ? 1 : row_warps == 2 ? 2 : 4;
-    p.slot_warps = p.shares == 1 ? row_warps : 4;
-    p.balance = c.dual && num_splits > 1 && B > 1 && B <= fa::kTcBalance;
-    p.tiles_per_split = static_cast<int>((c.tiles + num_splits - 1) / num_splits);
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.wait_limit = fa::kDefaultWaitLimit;
-    if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-    if (fa::as_clusters(c, static_cast<long long>(B) * Hkv * c.row_blocks, num_splits, d)) {
+    const fa::Plan c = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k, d, window, sinks);
+    fa::cut_paged(p, c, B, max_seqlen_q, max_seqlen_k, num_splits);
+    if (!fa::encode_cache(p, cache, c)) return FA_ERR_CUDA;
+    if (fa::as_clusters(c, static_cast<long long>(B) * p.Hkv * c.row_blocks, num_splits, d)) {
         const cudaError_t e = d == 64    ? fa::launch_rows<64, true>(p, stream)
                               : d == 128 ? fa::launch_rows<128, true>(p, stream)
                                          : fa::launch_rows<256, true>(p, stream);
         return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
-    cudaError_t e = c.tc       ? fa::launch_paged_tc(p, d, stream)
-                    : d == 64  ? fa::launch_rows<64, false>(p, stream)
-                    : d == 128 ? fa::launch_rows<128, false>(p, stream)
-                               : fa::launch_rows<256, false>(p, stream);
-    if (e == cudaSuccess && num_splits > 1)
-        e = d == 64 ? fa::launch_merge<64>(p, stream)
-                    : d == 128 ? fa::launch_merge<128>(p, stream) : fa::launch_merge<256>(p, stream);
+    cudaError_t e = fa::launch_paged(p, c, d, stream);
+    if (e == cudaSuccess && num_splits > 1) e = fa::launch_paged_merge(p, d, stream);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int prefix_len, int d,
+                         int* prefix_splits) {
+    if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q) return 0;
+    const int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    const int shared = own > 0 ? fa_paged_num_splits(1, H, Hkv, total_q, prefix_len, d, 0, 0) : 0;
+    *prefix_splits = std::min(shared, FA_MAX_SPLITS / 2);
+    return shared > 0 ? std::min(own, FA_MAX_SPLITS / 2) : 0;
+}
+
+fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens_q,
+                            const int* seqlens_k, void* o, float* lse, void* workspace, int B, int H, int total_q,
+                            int max_seqlen_q, int max_seqlen_k, int max_pages, int prefix_len, float scale,
+                            int num_splits, int prefix_splits, cudaStream_t stream) {
+    const fa_status sc = fa::check_paged(q, cache, page_table, cu_seqlens_q, seqlens_k, o, lse, B, H, total_q, max_seqlen_q,
+                                         max_seqlen_k, max_pages, scale);
+    if (sc != FA_OK) return sc;
+    const int d = cache->d;
+    if (prefix_len < 1 || prefix_len % cache->page_size || prefix_len >= max_seqlen_k) return FA_ERR_SHAPE;
+    if (static_cast<long long>(total_q) * (H / cache->Hkv) > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
+    if (num_splits < 1 || prefix_splits < 1 || num_splits > FA_MAX_SPLITS || prefix_splits > FA_MAX_SPLITS - num_splits)
+        return FA_ERR_SPLITS;
+    if (!fa::paged_aligned(q, o, lse, page_table, cu_seqlens_q, seqlens_k)) return FA_ERR_ALIGN;
+    if (!workspace || !fa::aligned(workspace, 16)) return FA_ERR_WORKSPACE;
+    fa::PagedParams p;
+    if (fa::fill_paged(p, q, cache, page_table, cu_seqlens_q, seqlens_k, o, lse, workspace, B, H, total_q, max_pages,
+                       num_splits + prefix_splits, scale) != cudaSuccess)
+        return FA_ERR_CUDA;
+    p.join = 1;
+    p.base_len = prefix_len;
+    p.base_pages = prefix_len / cache->page_size;
+    // The prefix, for all rows at once; then the sequences' own keys; then the merge.
+    p.whole = 1;
+    p.state0 = num_splits;
+    const fa::Plan cp = fa::plan_of(p.G, total_q, prefix_len, d, 0, 0);
+    fa::cut_paged(p, cp, 1, total_q, prefix_len, prefix_splits);
+    if (!fa::encode_cache(p, cache, cp)) return FA_ERR_CUDA;
+    if (fa::launch_paged(p, cp, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+    p.whole = 0;
+    p.state0 = 0;
+    const fa::Plan c = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    fa::cut_paged(p, c, B, max_seqlen_q, max_seqlen_k - prefix_len, num_splits);
+    if (!fa::encode_cache(p, cache, c)) return FA_ERR_CUDA;
+    if (fa::launch_paged(p, c, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+    p.num_splits = num_splits + prefix_splits;
+    return fa::launch_paged_merge(p, d, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

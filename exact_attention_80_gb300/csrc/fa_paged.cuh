@@ -105,7 +105,61 @@ struct PagedParams {
     float scale_log2;
     long long wait_limit;
     unsigned* status;
+    // A batch that shares a prefix (fa_fwd_prefix_fp8): its keys up to base_len, in the
+    // first base_pages entries of the table, are one part, the sequences' own keys the
+    // other. `whole`: this launch is the first part, one problem of all total_q rows
+    // that see all max_k keys. `join`: states are left for a merge in any case, as
+    // numbers state0 .. state0 + num_splits - 1.
+    int base_len, base_pages, whole, join, state0;
 };
+
+// The new tokens of sequence b (the launch's one problem where `whole`), positions and
+// lengths without the keys of a shared prefix. False where they are broken.
+__device__ __forceinline__ bool paged_tokens(const PagedParams& p, int b, NewTokens& t) {
+    if (p.whole) {
+        t = {0, p.total_q, p.max_k};
+        return true;
+    }
+    if (p.base_len == 0) return new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, t);
+    const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.lens[b] - p.base_len;
+    // (A sequence that brings nothing need not hold the prefix.)
+    const bool ok = 0 <= c0 && n >= 0 && n <= p.total_q - c0 && n <= p.max_q && (n == 0 || (n <= len && len <= p.max_k));
+    t.first = ok ? c0 : 0;
+    t.n = ok ? n : 0;
+    t.len = ok && n > 0 ? len : 0;
+    return ok;
+}
+// Positions: of the first row's token, and their step from token to token (`whole`: the
+// last key's for all).
+__device__ __forceinline__ int paged_start(const PagedParams& p, const NewTokens& t) {
+    return p.whole ? t.len - 1 : t.len - t.n;
+}
+__device__ __forceinline__ int paged_step(const PagedParams& p) { return p.whole ? 0 : 1; }
+
+// The pages of the table's row b that the launch reads.
+__device__ __forceinline__ const int* paged_table(const PagedParams& p, int b) {
+    return p.page_table + static_cast<long long>(b) * p.max_pages + (p.whole ? 0 : p.base_pages);
+}
+
+// The first sequence that brings tokens (-1: none). Called by a whole warp.
+__device__ __forceinline__ int paged_first(const PagedParams& p, int lane) {
+    for (int c = 0; c < p.B; c += 32) {
+        const int at = c + lane;
+        const unsigned who = __ballot_sync(0xffffffffu, at < p.B && p.cu[at + 1] > p.cu[at]);
+        if (who) return c + __ffs(who) - 1;
+    }
+    return -1;
+}
+// Reports a table of sequence b that does not begin with the shared prefix's pages, those
+// of the first sequence that brings tokens. Called by a whole warp.
+__device__ __forceinline__ void paged_check_prefix(const PagedParams& p, int b, int lane) {
+    const int first = paged_first(p, lane);
+    if (first < 0 || first == b) return;
+    const int* x = p.page_table + static_cast<long long>(first) * p.max_pages;
+    const int* y = p.page_table + static_cast<long long>(b) * p.max_pages;
+    for (int i = lane; i < p.base_pages; i += 32)
+        if (x[i] != y[i]) atomicOr(p.status, kStatusBadPage);
+}
 
 // What a partial state leaves as its reference m: -inf marks a state that saw no
 // key, or that no CTA filled; a NaN sum stays one through the merge.

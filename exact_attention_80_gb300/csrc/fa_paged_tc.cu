@@ -113,7 +113,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 
 struct TcWork {
     NewTokens nt;
-    int b, h, rows, start;
+    int b, h, rows, start;  // (b: the row of its pages in the table)
     int used;      // states that its rows leave (1: the result)
     int split;     // the state that this CTA leaves
     int row0[2];   // first row of each tile slot
@@ -138,7 +138,7 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
         const int b = lane + 32 * i;
         NewTokens t;
         n[i] = 0;
-        if (b < p.B && new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, t) && t.n > 0)
+        if (b < p.B && paged_tokens(p, b, t) && t.n > 0)
             n[i] = key_list<kTcKeys>(p.window, p.sinks, t.len - t.n, t.len - 1).n;
         longest = max(longest, n[i]);
     }
@@ -172,7 +172,7 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     w.h = static_cast<int>(lin % p.Hkv);
     w.b = static_cast<int>(lin / p.Hkv);
     w.nmax = w.n[0] = w.n[1] = 0;
-    w.live = new_tokens(p.cu, p.lens, w.b, p.total_q, p.max_q, p.max_k, w.nt);
+    w.live = paged_tokens(p, w.b, w.nt);
     if (!w.live) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
         return;
@@ -181,9 +181,16 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     const int r0 = unit * ROWS;
     w.live = r0 < w.rows;
     if (!w.live) return;
-    w.start = w.nt.len - w.nt.n;
-    w.p0 = w.start + r0 / p.G;
-    w.p1 = w.start + (min(r0 + ROWS, w.rows) - 1) / p.G;
+    if (p.base_pages > 0) {
+        if (p.whole) w.b = paged_first(p, threadIdx.x & 31);
+        else if (r0 == 0 && w.h == 0 && si == 0 && threadIdx.x < 32) paged_check_prefix(p, w.b, threadIdx.x);
+        w.live = w.b >= 0;
+        if (!w.live) return;
+    }
+    w.start = paged_start(p, w.nt);
+    const int step = paged_step(p);
+    w.p0 = w.start + step * (r0 / p.G);
+    w.p1 = w.start + step * ((min(r0 + ROWS, w.rows) - 1) / p.G);
     w.list = key_list<kTcKeys>(p.window, p.sinks, w.p0, w.p1);
     if constexpr (DUAL) {
         // Pieces of equal length; the slots take a half each.
@@ -212,7 +219,7 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
         w.row0[t] = WIDE ? r0 : r0 + (1 - t) * kTcRows;
         w.i0[t] = si * p.tiles_per_split;
         if (w.row0[t] >= w.rows) continue;
-        const int last = w.start + (min(w.row0[t] + kTcRows, w.rows) - 1) / p.G;
+        const int last = w.start + step * ((min(w.row0[t] + kTcRows, w.rows) - 1) / p.G);
         const int end = w.list.ns + max(0, last / kTcKeys + 1 - w.list.lo);
         w.n[t] = max(0, min(min(w.list.n, w.i0[t] + p.tiles_per_split), end) - w.i0[t]);
         w.nmax = max(w.nmax, w.n[t]);
@@ -317,7 +324,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             // tile's pages are copied one by one; pages behind the sequence's end
             // are left out.
             const bool leader = elect_one();
-            const int* table = p.page_table + static_cast<long long>(w.b) * p.max_pages;
+            const int* table = paged_table(p, w.b);
             const int per = BN >> p.log_page;  // pages per tile (page_size <= 128)
             const uint32_t page_bytes = static_cast<uint32_t>(D) << p.log_page, part_bytes = page_bytes / L::PARTS;
             // Page ids come 32 at a time, a lane each, the next 32 on their way: a
@@ -659,7 +666,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const bool row_ok = row < w.rows;
             const int i = (row_ok ? row : w.rows - 1) / p.G;
             const int head = w.h * p.G + (row_ok ? row : w.rows - 1) - i * p.G;
-            const int pos = w.start + i;
+            const int pos = w.start + paged_step(p) * i;
             const long long out_row = static_cast<long long>(w.nt.first + i) * p.H + head;
             float rowf = p.scale_log2;
             {
@@ -705,7 +712,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
             const uint32_t tS0 = tmem + lane_field + L::S_COL(t);
             const uint32_t tO = tmem + lane_field + L::O_COL(t);
-            const int* table = p.page_table + static_cast<long long>(w.b) * p.max_pages;
+            const int* table = paged_table(p, w.b);
             // Scales of the next tile, 16-key group `lane & 7` per lane, loaded a
             // tile ahead; the page-table entries two tiles ahead, and looked at
             // only then (a test right behind the load would wait for it).
@@ -998,17 +1005,18 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     const long long to = static_cast<long long>(w.nt.first + qi) * p.H + qh;
                     // States that the row does not use are marked as empty for the
                     // merge.
+                    const bool done = w.used == 1 && !p.join;
                     if (w.split == 0 && p.num_splits > 1)
-                        for (int s = (w.used == 1 ? 0 : w.used) + c; s < p.num_splits; s += UNITS)
-                            p.ws_m[static_cast<long long>(s) * p.total_q * p.H + to] = -INFINITY;
-                    if (w.used == 1) {
+                        for (int s = (done ? 0 : w.used) + c; s < p.num_splits; s += UNITS)
+                            p.ws_m[static_cast<long long>(p.state0 + s) * p.total_q * p.H + to] = -INFINITY;
+                    if (done) {
                         const float inv = ll == 0.f ? 0.f : 1.f / ll;
                         *reinterpret_cast<uint2*>(p.o + to * D + 4 * c) =
                             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
                         if (c == 0)
                             p.lse[static_cast<long long>(qh) * p.total_q + w.nt.first + qi] = state_lse(mm, ll);
                     } else {
-                        const long long at = static_cast<long long>(w.split) * p.total_q * p.H + to;
+                        const long long at = static_cast<long long>(p.state0 + w.split) * p.total_q * p.H + to;
                         *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
                         if (c == 0) {
                             p.ws_m[at] = state_ref(mm, ll);
@@ -1017,8 +1025,9 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     }
                 }
             } else if (ok) {
-                const float f = w.used == 1 ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const long long at = static_cast<long long>(w.split) * p.total_q * p.H + out_row;
+                const bool done = w.used == 1 && !p.join;
+                const float f = done ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                const long long at = static_cast<long long>(p.state0 + w.split) * p.total_q * p.H + out_row;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -1031,7 +1040,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                         for (int e = 0; e < 32; ++e) o[e] = 0u;
                     }
                     if (!row_ok) continue;
-                    if (w.used == 1) {
+                    if (done) {
                         uint4* dst = reinterpret_cast<uint4*>(p.o + out_row * D + cc * 32);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -1053,9 +1062,9 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     // States that the row does not use are marked as empty for the
                     // merge.
                     if (w.split == 0 && p.num_splits > 1)
-                        for (int s = w.used == 1 ? 0 : w.used; s < p.num_splits; ++s)
-                            p.ws_m[static_cast<long long>(s) * p.total_q * p.H + out_row] = -INFINITY;
-                    if (w.used == 1) {
+                        for (int s = done ? 0 : w.used; s < p.num_splits; ++s)
+                            p.ws_m[static_cast<long long>(p.state0 + s) * p.total_q * p.H + out_row] = -INFINITY;
+                    if (done) {
                         p.lse[static_cast<long long>(head) * p.total_q + w.nt.first + i] =
                             state_lse(m, l);
                     } else {
@@ -1090,7 +1099,7 @@ cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    const long long ctas = static_cast<long long>(p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_paged_tc_kernel<D, SHARES>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
                             stream, p);

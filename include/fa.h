@@ -509,6 +509,48 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
                            int num_splits, cudaStream_t stream);
 
 /*
+ * fa_fwd_prefix_fp8 — fa_fwd_paged_fp8 (without a window) for a batch whose sequences
+ * begin with the same tokens: prefix_len of them, a multiple of the page size, in the
+ * same pages. Arguments, outputs and roundings as there; every sequence that brings
+ * queries names the prefix's pages in the first prefix_len / page_size entries of its
+ * row of page_table, and its queries lie behind the prefix (seqlens_k[b] - n >=
+ * prefix_len; else FA_ERR_SEQLENS, and the sequence is not written). The prefix is
+ * attended to once, by the queries of all sequences together, the keys behind it
+ * sequence by sequence, and the two parts' states are merged. A row of page_table that
+ * begins with other pages than that of the first sequence with queries: FA_ERR_PAGES,
+ * its sequence's result is undefined. prefix_len < max_seqlen_k.
+ * The sequences' own keys are cut into num_splits parts, the prefix into
+ * prefix_splits (together FA_MAX_SPLITS at most; fa_prefix_num_splits proposes both: it
+ * returns the first, 0 for arguments out of range). workspace:
+ * fa_paged_workspace_bytes(total_q, H, d, num_splits + prefix_splits), 16-byte aligned.
+ */
+int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int prefix_len, int d,
+                         int* prefix_splits);
+fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens_q,
+                            const int* seqlens_k, void* o, float* lse, void* workspace, int B, int H, int total_q,
+                            int max_seqlen_q, int max_seqlen_k, int max_pages, int prefix_len, float scale,
+                            int num_splits, int prefix_splits, cudaStream_t stream);
+
+/*
+ * fa_kv_read_fp8 — cached keys and values back as packed bf16 rows, for attention over
+ * them (fa_fwd_packed), or to move a context elsewhere.
+ *   k_out, v_out bf16 [total][Hkv][d] (written), tokens k_stride and v_stride elements
+ *   apart (multiples of 8, at least Hkv * d); cu_seqlens int32 [B + 1]: row
+ *   cu_seqlens[b] + i is token starts[b] + i of sequence b (starts int32 [B], or NULL:
+ *   from token 0 on). Keys come as they were cached, rotated if they were.
+ * A value is its code times its scale in fp32, rounded to bf16: exact for the
+ * power-of-two scales of fa_kv_append_fp8; NaN stays NaN. A sequence whose offsets are
+ * no valid partition, or whose tokens pass max_pages * page_size, is not read
+ * (FA_ERR_SEQLENS from fa_device_status), nor are tokens whose page is not one of the
+ * cache (FA_ERR_PAGES): their rows are not written. Rows that belong to no sequence
+ * (before cu_seqlens[0], from cu_seqlens[B] on) stay as they are, or, with `fill` != 0,
+ * get 0.
+ */
+fa_status fa_kv_read_fp8(const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens, const int* starts,
+                         void* k_out, void* v_out, int B, int total, int max_pages, long long k_stride,
+                         long long v_stride, int fill, cudaStream_t stream);
+
+/*
  * fa_device_status — SYNCHRONISES `stream`, then reads the library's device
  * error word: FA_OK; FA_ERR_TIMEOUT if any kernel since the last clear gave up
  * on a bounded wait (it then exits cleanly and leaves its outputs undefined);
