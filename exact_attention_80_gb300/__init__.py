@@ -150,7 +150,8 @@ def _load_calls(lib):
     calls.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         lib.fa_rope, lib.fa_kv_append_fp8, lib.fa_fwd_paged_fp8, lib.fa_paged_num_splits,
         lib.fa_paged_workspace_bytes, lib.fa_fwd_window, lib.fa_bwd_window, lib.fa_bwd_window_workspace_bytes,
-        lib.fa_window_num_splits, lib.fa_fwd_window_splitkv, lib.fa_combine)))
+        lib.fa_window_num_splits, lib.fa_fwd_window_splitkv, lib.fa_combine, lib.fa_fwd_packed, lib.fa_bwd_packed,
+        lib.fa_bwd_packed_workspace_bytes, lib.fa_fwd_prefix_fp8, lib.fa_prefix_num_splits, lib.fa_kv_read_fp8)))
     return calls
 
 
@@ -543,8 +544,8 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
 # ------------------------------------------ rotary positions and the paged cache
 # These calls are short (a decode step of a few sequences runs in a few
 # microseconds on the GPU). On the current stream and with plain arguments rope,
-# kv_append_fp8, attention_paged_fp8 and the window's two calls run in the
-# compiled module _calls, where it is there; it answers None where an argument is
+# kv_append_fp8, kv_read_fp8, attention_paged_fp8, attention_prefix_fp8 and the two
+# calls each of the window and of packed sequences run in the compiled module _calls, where it is there; it answers None where an argument is
 # anything else, and the forms below, whose checks touch each tensor once, say
 # what is wrong or take the call.
 _ROTATION = struct.Struct(f"PPii{FA_MAX_AXES}iii")   # fa_rotation
@@ -984,6 +985,13 @@ def attention_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_s
                          num_splits: int | None = None, prefix_splits: int | None = None, stream=None):
     """:func:`fa_fwd_prefix_fp8` into new outputs, with a workspace of its own (splits None: the
     library's proposal). Returns ``(o, lse)``; rows past ``cu_seqlens_q[B]`` are left as allocated."""
+    if stream is None and _compiled is not None:
+        out = _compiled.prefix(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q,
+                               max_seqlen_k, prefix_len, scale, num_splits, prefix_splits)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_fwd_prefix_fp8")
+            return out
     with _allocating(stream, q):
         o, lse = _prefix(q, k_cache, v_cache, k_scale, v_scale, None, None, page_table, cu_seqlens_q, seqlens_k,
                          max_seqlen_q, max_seqlen_k, prefix_len, None, num_splits, prefix_splits, scale, stream)
@@ -1022,9 +1030,15 @@ def fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, k_out, v_out, page_table,
 def kv_read_fp8(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, starts=None, total: int = 0, stream=None):
     """:func:`fa_kv_read_fp8` into new tensors of ``total`` rows, at least ``cu_seqlens[B]``. Returns
     ``(k, v)``; rows that belong to no sequence are 0."""
+    if stream is None and _compiled is not None:
+        out = _compiled.read(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, starts, total)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_kv_read_fp8")
+            return out
     import torch
 
-    if total < 1:
+    if _int32(total) < 1:
         raise ValueError("total must give the rows of k and v, at least one")
     shape = (total, k_cache.shape[1], k_cache.shape[-1])
     with _allocating(stream, k_cache):
@@ -1210,8 +1224,15 @@ def attention_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max
                      sinks: int = 0, scale: float | None = None, stream=None):
     """:func:`fa_fwd_packed` into new outputs. Returns ``(o, lse)``; rows that belong to no sequence
     are 0 and -inf."""
+    if stream is None and _compiled is not None:
+        out = _compiled.packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window, sinks, scale)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_fwd_packed")
+            return out
     import torch
 
+    _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)
     with _allocating(stream, q):
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
@@ -1259,6 +1280,13 @@ def attention_packed_backward(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k,
                               stream=None):
     """Allocate ``(dq, dk, dv)`` and the workspace and run :func:`fa_bwd_packed`; rows that belong to no
     sequence are 0."""
+    if stream is None and _compiled is not None:
+        out = _compiled.packed_backward(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                                        window, sinks, scale)
+        if out is not None:
+            if type(out) is int:
+                raise FAError(out, "fa_bwd_packed")
+            return out
     import torch
 
     _, n, m, H, Hkv, d, _, _ = _packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k)

@@ -1,6 +1,7 @@
-// fa_calls.cpp — the Python module `_calls`: rope, kv_append_fp8,
-// attention_paged_fp8, attention_window and attention_window_backward for plain
-// arguments, from the tensors' checks to the launch.
+// fa_calls.cpp — the Python module `_calls`: rope, kv_append_fp8, kv_read_fp8,
+// attention_paged_fp8, attention_prefix_fp8, attention_window, attention_packed and
+// the backward of the last two for plain arguments, from the tensors' checks to the
+// launch.
 //
 // A call on a few tokens takes the GPU a few microseconds, so the interpreter's
 // share of it counts (one call after the other, us, with ctypes and here: 8
@@ -41,6 +42,12 @@ struct {
     decltype(&::fa_window_num_splits) window_splits;
     decltype(&::fa_fwd_window_splitkv) window_splitkv;
     decltype(&::fa_combine) combine;
+    decltype(&::fa_fwd_packed) packed;
+    decltype(&::fa_bwd_packed) packed_backward;
+    decltype(&::fa_bwd_packed_workspace_bytes) packed_workspace;
+    decltype(&::fa_fwd_prefix_fp8) prefix;
+    decltype(&::fa_prefix_num_splits) prefix_splits;
+    decltype(&::fa_kv_read_fp8) read;
 } lib;
 
 bool tensor(PyObject* o, const at::Tensor** t) {
@@ -134,15 +141,17 @@ bool rotation(const at::Tensor& table, const at::Tensor* positions, long long ax
     return true;
 }
 
-// The cache's four tensors and the batch's three.
+// The cache's four tensors and the batch's three (the last may be None where
+// `optional`: lens null).
 struct Paged {
     fa_paged_cache cache;
     const int *table, *cu, *lens;
     int B, max_pages;
 };
-bool paged(PyObject* const* a, int index, Paged* p) {
+bool paged(PyObject* const* a, int index, Paged* p, bool optional = false) {
     const at::Tensor* t[7];
-    for (int i = 0; i < 7; ++i)
+    const int arrays = optional && a[6] == Py_None ? 6 : 7;
+    for (int i = 0; i < arrays; ++i)
         if (!tensor(a[i], &t[i])) return false;
     if (t[0]->dim() != 4 || t[0]->sizes() != t[1]->sizes()) return false;
     const auto n = t[0]->sizes();
@@ -154,17 +163,18 @@ bool paged(PyObject* const* a, int index, Paged* p) {
     }
     for (int i = 0; i < 4; ++i)
         if (n[i] > INT_MAX) return false;
-    for (int i = 4; i < 7; ++i)
+    for (int i = 4; i < arrays; ++i)
         if (!array(*t[i], at::kInt, index)) return false;
-    if (t[4]->dim() != 2 || t[5]->dim() != 1 || t[6]->dim() != 1) return false;
+    if (t[4]->dim() != 2 || t[5]->dim() != 1) return false;
     const long long B = t[4]->size(0), width = t[4]->size(1);
-    if (B < 1 || B >= INT_MAX || width > INT_MAX || t[5]->size(0) != B + 1 || t[6]->size(0) != B) return false;
+    if (B < 1 || B >= INT_MAX || width > INT_MAX || t[5]->size(0) != B + 1) return false;
+    if (arrays == 7 && (t[6]->dim() != 1 || t[6]->size(0) != B)) return false;
     p->cache = {t[0]->data_ptr(), t[1]->data_ptr(), static_cast<float*>(t[2]->data_ptr()),
                 static_cast<float*>(t[3]->data_ptr()), static_cast<int>(n[0]), static_cast<int>(n[1]),
                 static_cast<int>(n[2]), static_cast<int>(n[3])};
     p->table = static_cast<const int*>(t[4]->data_ptr());
     p->cu = static_cast<const int*>(t[5]->data_ptr());
-    p->lens = static_cast<const int*>(t[6]->data_ptr());
+    p->lens = arrays == 7 ? static_cast<const int*>(t[6]->data_ptr()) : nullptr;
     p->B = static_cast<int>(B);
     p->max_pages = static_cast<int>(width);
     return true;
@@ -184,6 +194,43 @@ bool dense(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, int in
         if (n[i] > INT_MAX || m[i] > INT_MAX) return false;
     *c = {static_cast<int>(n[0]), static_cast<int>(n[1]), static_cast<int>(m[1]),
           static_cast<int>(n[2]), static_cast<int>(m[2]), static_cast<int>(n[3])};
+    return true;
+}
+// q [total_q, H, d], k and v [total_k, Hkv, d], cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+// max_seqlen_k, window, sinks of a packed call, from a[0] on in this order (between k, v
+// and the offsets `skip` other arguments).
+struct Packed {
+    const at::Tensor *q, *k, *v;
+    Tokens qt, kt, vt;
+    fa_packed_batch batch;
+    int H, Hkv, d, window, sinks, index;
+};
+bool packed(PyObject* const* a, int skip, Packed* c) {
+    const at::Tensor* cu[2];
+    PyObject* const* b = a + 3 + skip;
+    if (!tensor(a[0], &c->q) || !tensor(a[1], &c->k) || !tensor(a[2], &c->v) || !tensor(b[0], &cu[0]) ||
+        !tensor(b[1], &cu[1]))
+        return false;
+    if (!number(b[2], &c->batch.max_seqlen_q) || !number(b[3], &c->batch.max_seqlen_k) || !number(b[4], &c->window) ||
+        !number(b[5], &c->sinks))
+        return false;
+    const int index = c->index = c->q->is_cuda() && c->q->get_device() == c10::cuda::current_device()
+                                     ? static_cast<int>(c->q->get_device()) : -1;
+    if (index < 0 || !tokens(*c->q, index, &c->qt) || !tokens(*c->k, index, &c->kt) || !tokens(*c->v, index, &c->vt))
+        return false;
+    if (c->kt.d != c->qt.d || c->vt.n != c->kt.n || c->vt.h != c->kt.h || c->vt.d != c->kt.d) return false;
+    for (int i = 0; i < 2; ++i)
+        if (!array(*cu[i], at::kInt, index) || cu[i]->dim() != 1 || cu[i]->size(0) != cu[0]->size(0)) return false;
+    const long long B = cu[0]->size(0) - 1;
+    if (B < 1 || B > INT_MAX) return false;
+    c->batch.cu_seqlens_q = static_cast<const int*>(cu[0]->data_ptr());
+    c->batch.cu_seqlens_k = static_cast<const int*>(cu[1]->data_ptr());
+    c->batch.B = static_cast<int>(B);
+    c->batch.total_q = static_cast<int>(c->qt.n);
+    c->batch.total_k = static_cast<int>(c->kt.n);
+    c->H = static_cast<int>(c->qt.h);
+    c->Hkv = static_cast<int>(c->kt.h);
+    c->d = static_cast<int>(c->qt.d);
     return true;
 }
 // A scale argument: None is 1 / sqrt(d), rounded once to fp32.
@@ -397,11 +444,116 @@ PyObject* call_window_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// packed(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window, sinks, scale or None) -> (o, lse)
+PyObject* call_packed(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Packed c;
+    float scale;
+    NOT_PLAIN_UNLESS(n == 10 && packed(a, 0, &c) && scale_of(a[9], c.d, &scale));
+    at::Tensor out[2] = {at::empty({c.qt.n, c.qt.h, c.qt.d}, c.q->options()),
+                         at::empty({c.qt.h, c.qt.n}, c.q->options().dtype(at::kFloat))};
+    const fa_status s = launch(c.index, [&](cudaStream_t stream) {
+        return lib.packed(c.q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), out[0].data_ptr(),
+                          static_cast<float*>(out[1].data_ptr()), &c.batch, c.H, c.Hkv, c.d, c.qt.stride, c.kt.stride,
+                          c.vt.stride, scale, c.window, c.sinks, 1, stream);
+    });
+    return s == FA_OK ? tuple_of(out, 2) : PyLong_FromLong(s);
+    END_HANDLE_TH_ERRORS
+}
+
+// packed_backward(q, k, v, o, lse, dout, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, window, sinks, scale or
+// None) -> (dq, dk, dv)
+PyObject* call_packed_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Packed c;
+    float scale;
+    const at::Tensor *o, *lse, *dout;
+    NOT_PLAIN_UNLESS(n == 13 && tensor(a[3], &o) && tensor(a[4], &lse) && tensor(a[5], &dout) && packed(a, 3, &c) &&
+                     scale_of(a[12], c.d, &scale));
+    Tokens dt;
+    NOT_PLAIN_UNLESS(array(*o, at::kBFloat16, c.index) && o->sizes() == c.q->sizes() &&
+                     array(*lse, at::kFloat, c.index) && lse->dim() == 2 && lse->size(0) == c.qt.h &&
+                     lse->size(1) == c.qt.n && tokens(*dout, c.index, &dt) && dout->sizes() == c.q->sizes());
+    at::Tensor out[3] = {at::empty({c.qt.n, c.qt.h, c.qt.d}, c.q->options()),
+                         at::empty({c.kt.n, c.kt.h, c.kt.d}, c.q->options()),
+                         at::empty({c.kt.n, c.kt.h, c.kt.d}, c.q->options())};
+    const fa_packed_batch& b = c.batch;
+    const size_t bytes = lib.packed_workspace(b.B, b.total_q, b.total_k, b.max_seqlen_q, b.max_seqlen_k, c.H, c.Hkv, c.d,
+                                              c.window, c.sinks);
+    at::Tensor workspace = at::empty({static_cast<int64_t>(bytes < 4 ? 1 : bytes / 4)}, c.q->options().dtype(at::kFloat));
+    const long long kv = c.kt.h * c.kt.d;
+    const fa_packed_strides strides = {c.qt.stride, c.kt.stride, c.vt.stride, dt.stride, c.qt.h * c.qt.d, kv, kv};
+    const fa_status s = launch(c.index, [&](cudaStream_t stream) {
+        return lib.packed_backward(c.q->data_ptr(), c.k->data_ptr(), c.v->data_ptr(), o->data_ptr(), dout->data_ptr(),
+                                   static_cast<const float*>(lse->data_ptr()), out[0].data_ptr(), out[1].data_ptr(),
+                                   out[2].data_ptr(), workspace.data_ptr(), &b, c.H, c.Hkv, c.d, &strides, scale,
+                                   c.window, c.sinks, 1, stream);
+    });
+    return s == FA_OK ? tuple_of(out, 3) : PyLong_FromLong(s);
+    END_HANDLE_TH_ERRORS
+}
+
+// prefix(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens_q, seqlens_k, max_seqlen_q, max_seqlen_k,
+// prefix_len, scale or None, num_splits or None, prefix_splits or None) -> (o, lse)
+PyObject* call_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor* q;
+    int max_q, max_k, prefix_len, splits = 0, shared = 0;
+    NOT_PLAIN_UNLESS(n == 14 && tensor(a[0], &q) && number(a[8], &max_q) && number(a[9], &max_k) &&
+                     number(a[10], &prefix_len));
+    for (int i = 0; i < 2; ++i) {
+        int* x = i ? &shared : &splits;
+        NOT_PLAIN_UNLESS(a[12 + i] == Py_None || (number(a[12 + i], x) && *x >= 1 && *x < FA_MAX_SPLITS));
+    }
+    const int index = current_index(*q);
+    Tokens t;
+    Paged p;
+    float scale;
+    NOT_PLAIN_UNLESS(index >= 0 && tokens(*q, index, &t) && t.stride == t.h * t.d && paged(a + 1, index, &p) &&
+                     p.cache.d == t.d && scale_of(a[11], p.cache.d, &scale));
+    const int H = static_cast<int>(t.h), total = static_cast<int>(t.n), d = static_cast<int>(t.d);
+    int both[2] = {1, 1};
+    both[0] = lib.prefix_splits(p.B, H, p.cache.Hkv, total, max_q, max_k, prefix_len, d, &both[1]);
+    if (both[0] < 1) both[0] = both[1] = 1;  // (out of range: the call says so)
+    if (!splits) splits = both[0];
+    if (!shared) shared = both[1];
+    at::Tensor out[2] = {at::empty({t.n, t.h, t.d}, q->options()), at::empty({t.h, t.n}, q->options().dtype(at::kFloat))};
+    const size_t bytes = lib.workspace_bytes(total, H, d, splits + shared);
+    at::Tensor workspace = at::empty({static_cast<int64_t>(bytes < 4 ? 1 : bytes / 4)}, q->options().dtype(at::kFloat));
+    const fa_status s = launch(index, [&](cudaStream_t stream) {
+        return lib.prefix(q->data_ptr(), &p.cache, p.table, p.cu, p.lens, out[0].data_ptr(),
+                          static_cast<float*>(out[1].data_ptr()), workspace.data_ptr(), p.B, H, total, max_q, max_k,
+                          p.max_pages, prefix_len, scale, splits, shared, stream);
+    });
+    return s == FA_OK ? tuple_of(out, 2) : PyLong_FromLong(s);
+    END_HANDLE_TH_ERRORS
+}
+
+// read(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, starts or None, total) -> (k, v)
+PyObject* call_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    const at::Tensor* cache;
+    int total;
+    NOT_PLAIN_UNLESS(n == 8 && tensor(a[0], &cache) && number(a[7], &total) && total >= 1);
+    const int index = current_index(*cache);
+    Paged p;
+    NOT_PLAIN_UNLESS(index >= 0 && paged(a, index, &p, true));
+    at::Tensor out[2];
+    for (at::Tensor& t : out) t = at::empty({total, p.cache.Hkv, p.cache.d}, cache->options().dtype(at::kBFloat16));
+    const long long stride = static_cast<long long>(p.cache.Hkv) * p.cache.d;
+    const fa_status s = launch(index, [&](cudaStream_t stream) {
+        return lib.read(&p.cache, p.table, p.cu, p.lens, out[0].data_ptr(), out[1].data_ptr(), p.B, total, p.max_pages,
+                        stride, stride, 1, stream);
+    });
+    return s == FA_OK ? tuple_of(out, 2) : PyLong_FromLong(s);
+    END_HANDLE_TH_ERRORS
+}
+
 // init: addresses of the library's entry points, in the order of `lib`.
 PyObject* call_init(PyObject*, PyObject* args) {
-    unsigned long long f[11];
-    if (!PyArg_ParseTuple(args, "KKKKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
-                          &f[10]))
+    unsigned long long f[17];
+    if (!PyArg_ParseTuple(args, "KKKKKKKKKKKKKKKKK", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8], &f[9],
+                          &f[10], &f[11], &f[12], &f[13], &f[14], &f[15], &f[16]))
         return nullptr;
     lib.rope = reinterpret_cast<decltype(lib.rope)>(static_cast<uintptr_t>(f[0]));
     lib.append = reinterpret_cast<decltype(lib.append)>(static_cast<uintptr_t>(f[1]));
@@ -414,6 +566,12 @@ PyObject* call_init(PyObject*, PyObject* args) {
     lib.window_splits = reinterpret_cast<decltype(lib.window_splits)>(static_cast<uintptr_t>(f[8]));
     lib.window_splitkv = reinterpret_cast<decltype(lib.window_splitkv)>(static_cast<uintptr_t>(f[9]));
     lib.combine = reinterpret_cast<decltype(lib.combine)>(static_cast<uintptr_t>(f[10]));
+    lib.packed = reinterpret_cast<decltype(lib.packed)>(static_cast<uintptr_t>(f[11]));
+    lib.packed_backward = reinterpret_cast<decltype(lib.packed_backward)>(static_cast<uintptr_t>(f[12]));
+    lib.packed_workspace = reinterpret_cast<decltype(lib.packed_workspace)>(static_cast<uintptr_t>(f[13]));
+    lib.prefix = reinterpret_cast<decltype(lib.prefix)>(static_cast<uintptr_t>(f[14]));
+    lib.prefix_splits = reinterpret_cast<decltype(lib.prefix_splits)>(static_cast<uintptr_t>(f[15]));
+    lib.read = reinterpret_cast<decltype(lib.read)>(static_cast<uintptr_t>(f[16]));
     Py_RETURN_NONE;
 }
 
@@ -429,6 +587,10 @@ PyMethodDef methods[] = {
     {"paged", fast(call_paged), METH_FASTCALL, nullptr},
     {"window", fast(call_window), METH_FASTCALL, nullptr},
     {"window_backward", fast(call_window_backward), METH_FASTCALL, nullptr},
+    {"packed", fast(call_packed), METH_FASTCALL, nullptr},
+    {"packed_backward", fast(call_packed_backward), METH_FASTCALL, nullptr},
+    {"prefix", fast(call_prefix), METH_FASTCALL, nullptr},
+    {"read", fast(call_read), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
 

@@ -177,3 +177,43 @@ def window_backward(q, k, v, dout, scale, window, sinks):
             dk[b, c] += ds.T @ q[b, h] * scale
             dv[b, c] += w.T @ do
     return dq, dk, dv
+
+
+def packed_forward(q, k, v, cu_q, cu_k, scale, window=0, sinks=0):
+    """q [T, H, d], k and v [S, Hkv, d], sequences at cu_q and cu_k: (o, lse [H, T], a = sum of weight * |value|)."""
+    T, H, d = q.shape
+    g = H // k.shape[1]
+    o, lse, a = np.zeros((T, H, d)), np.full((H, T), -np.inf), np.zeros((T, H, d))
+    for b in range(len(cu_q) - 1):
+        rows, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        for h in range(H):
+            o[rows, h], lse[h, rows], w = attend(q[rows, h], k[keys, h // g], v[keys, h // g], scale, window, sinks)
+            a[rows, h] = w @ np.abs(v[keys, h // g])
+    return o, lse, a
+
+
+def packed_backward(q, k, v, dout, cu_q, cu_k, scale, window=0, sinks=0):
+    """(dq, dk, dv) of sum(o * dout); the gradients of a shared head are summed over its group."""
+    g = q.shape[1] // k.shape[1]
+    dq, dk, dv = np.zeros(q.shape), np.zeros(k.shape), np.zeros(v.shape)
+    for b in range(len(cu_q) - 1):
+        rows, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        for h in range(q.shape[1]):
+            c = h // g
+            o, _, w = attend(q[rows, h], k[keys, c], v[keys, c], scale, window, sinks)
+            do = dout[rows, h]
+            ds = w * (do @ v[keys, c].T - (do * o).sum(1, keepdims=True))
+            dq[rows, h] = ds @ k[keys, c] * scale
+            dk[keys, c] += ds.T @ q[rows, h] * scale
+            dv[keys, c] += w.T @ do
+    return dq, dk, dv
+
+
+def read(codes, scale, page_table, starts, lengths, page_size):
+    """Cached values [T, Hkv, d] of tokens starts[b] .. starts[b] + lengths[b] - 1 of each sequence b, one behind the other."""
+    rows = []
+    for b, (s, n) in enumerate(zip(starts, lengths)):
+        for j in range(s, s + n):
+            pg = page_table[b, j // page_size]
+            rows.append(VALUES[codes[pg, :, j % page_size]] * scale[pg].astype(np.float64)[:, None])
+    return np.array(rows).reshape(len(rows), codes.shape[1], codes.shape[3])
