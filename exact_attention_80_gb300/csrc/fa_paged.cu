@@ -171,7 +171,8 @@ __device__ __forceinline__ void cluster_meet() {
 // heads of 64 over 516 keys, five splits: 6.1 us against 7.4 through the workspace,
 // replayed from a graph; 9.5 with one split). Every CTA of a cluster comes to both
 // of its meetings, whatever it found.
-template <int D, bool CLUSTER>
+// PART: a part of a batch that shares a prefix (PagedParams).
+template <int D, bool CLUSTER, bool PART>
 __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     fa_paged_rows_kernel(const __grid_constant__ PagedParams p) {
     using L = PagedLayout<D>;
@@ -208,19 +209,19 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     int b = static_cast<int>(lin / p.Hkv);
     // (All CTAs of a cluster agree on the returns below.)
     NewTokens nt;
-    if (!paged_tokens(p, b, nt)) {
+    if (!paged_tokens<PART>(p, b, nt)) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
         return;
     }
     const int rows = nt.n * p.G;
     const int r0 = rb * kRows;
     if (r0 >= rows) return;
-    if (p.base_pages > 0) {
+    if constexpr (PART) {
         if (p.whole) b = paged_first(p, lane);
         else if (h == 0 && rb == 0 && split == 0 && warp == 0) paged_check_prefix(p, b, lane);
         if (b < 0) return;
     }
-    const int start = paged_start(p, nt), step = paged_step(p);  // position of the first query
+    const int start = paged_start<PART>(p, nt), step = paged_step<PART>(p);  // position of the first query
     const int p0 = start + step * (r0 / p.G);
     const int p1 = start + step * ((min(r0 + kRows, rows) - 1) / p.G);
     const KeyList list = key_list<KEYS>(p.window, p.sinks, p0, p1);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     const int i0 = split * p.tiles_per_split;
     const int i1 = min(list.n, i0 + p.tiles_per_split);
     const int mine = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);  // this warp's tiles: i0 + warp + 4 k
-    const int* table = paged_table(p, b);
+    const int* table = paged_table<PART>(p, b);
     const int page_size = 1 << p.log_page;
     const int last_page = (nt.len - 1) >> p.log_page;
 
@@ -592,14 +593,14 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         }
         const long long row = place(r);
         // States that the row does not use are marked as empty for the merge.
-        const bool done = used == 1 && !p.join;
+        const bool done = used == 1 && !PART;
         if (split == 0 && p.num_splits > 1)
             for (int s = (done ? 0 : used) + c; s < p.num_splits; s += VEC)
-                p.ws_m[static_cast<long long>(p.state0 + s) * p.total_q * p.H + row] = -INFINITY;
+                p.ws_m[static_cast<long long>(paged_state0<PART>(p) + s) * p.total_q * p.H + row] = -INFINITY;
         if (done) {
             put(r, c, a, mm, ll);
         } else {
-            const long long at = static_cast<long long>(p.state0 + split) * p.total_q * p.H + row;
+            const long long at = static_cast<long long>(paged_state0<PART>(p) + split) * p.total_q * p.H + row;
             *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
             if (c == 0) {
                 p.ws_m[at] = state_ref(mm, ll);
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
 // saw no key. W warps (1 or 4) share a row, each with eight partial rows in
 // flight: the merge of a single sequence's few rows over many splits is a matter
 // of latency alone.
-template <int D, int W>
+template <int D, int W, bool PART>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
     constexpr int PER = D / 32, U = 8;
     __shared__ float weight[4][FA_MAX_SPLITS];
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     const int i = static_cast<int>(rest % p.max_q);
     const int b = static_cast<int>(rest / p.max_q);
     NewTokens nt;
-    bool live = b < p.B && paged_tokens(p, b, nt) && i < nt.n;
+    bool live = b < p.B && paged_tokens<PART>(p, b, nt) && i < nt.n;
     const long long row = live ? static_cast<long long>(nt.first + i) * p.H + head : 0;
     const long long stride = static_cast<long long>(p.total_q) * p.H;
     const int states = live ? p.num_splits : 0;
@@ -840,20 +841,20 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
     return static_cast<int>(best);
 }
 
-template <int D, bool CLUSTER>
+template <int D, bool CLUSTER, bool PART>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
     using L = PagedLayout<D>;
     static ContextCache<int> attr_set;
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         *out = 1;
-        return cudaFuncSetAttribute(fa_paged_rows_kernel<D, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_paged_rows_kernel<D, CLUSTER, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    const long long ctas = static_cast<long long>(PART && p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent_clusters(fa_paged_rows_kernel<D, CLUSTER>, dim3(static_cast<unsigned>(ctas)),
+    return launch_dependent_clusters(fa_paged_rows_kernel<D, CLUSTER, PART>, dim3(static_cast<unsigned>(ctas)),
                                      CLUSTER ? static_cast<unsigned>(p.num_splits) : 1u, kWarps * 32, L::ALLOC, stream,
                                      p);
 }
@@ -863,14 +864,14 @@ bool as_clusters(const Plan& c, long long units, int num_splits, int d) {
     return !c.tc && num_splits > 1 && num_splits <= kClusterSplits && units * num_splits <= 152 * rows_ctas(d);
 }
 
-template <int D>
+template <int D, bool PART>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.max_q * p.H;
     // Four warps a row while that leaves the grid within about one wave.
     const bool four = p.num_splits > 8 && rows <= 4096;
     const long long blocks = four ? rows : (rows + 3) / 4;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(four ? fa_paged_merge_kernel<D, 4> : fa_paged_merge_kernel<D, 1>,
+    return launch_dependent(four ? fa_paged_merge_kernel<D, 4, PART> : fa_paged_merge_kernel<D, 1, PART>,
                             dim3(static_cast<unsigned>(blocks)), 128, 0, stream, p);
 }
 
@@ -951,14 +952,18 @@ cudaError_t fill_paged(PagedParams& p, const void* q, const fa_paged_cache* cach
     p.wait_limit = kDefaultWaitLimit;
     return device_status_ptr(&p.status);
 }
+template <bool PART>
 cudaError_t launch_paged(const PagedParams& p, const Plan& c, int d, cudaStream_t stream) {
-    return c.tc       ? launch_paged_tc(p, d, stream)
-           : d == 64  ? launch_rows<64, false>(p, stream)
-           : d == 128 ? launch_rows<128, false>(p, stream)
-                      : launch_rows<256, false>(p, stream);
+    return c.tc       ? launch_paged_tc(p, d, PART, stream)
+           : d == 64  ? launch_rows<64, false, PART>(p, stream)
+           : d == 128 ? launch_rows<128, false, PART>(p, stream)
+                      : launch_rows<256, false, PART>(p, stream);
 }
+template <bool PART>
 cudaError_t launch_paged_merge(const PagedParams& p, int d, cudaStream_t stream) {
-    return d == 64 ? launch_merge<64>(p, stream) : d == 128 ? launch_merge<128>(p, stream) : launch_merge<256>(p, stream);
+    return d == 64    ? launch_merge<64, PART>(p, stream)
+           : d == 128 ? launch_merge<128, PART>(p, stream)
+                      : launch_merge<256, PART>(p, stream);
 }
 
 }  // namespace
@@ -1004,13 +1009,13 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
     fa::cut_paged(p, c, B, max_seqlen_q, max_seqlen_k, num_splits);
     if (!fa::encode_cache(p, cache, c)) return FA_ERR_CUDA;
     if (fa::as_clusters(c, static_cast<long long>(B) * p.Hkv * c.row_blocks, num_splits, d)) {
-        const cudaError_t e = d == 64    ? fa::launch_rows<64, true>(p, stream)
-                              : d == 128 ? fa::launch_rows<128, true>(p, stream)
-                                         : fa::launch_rows<256, true>(p, stream);
+        const cudaError_t e = d == 64    ? fa::launch_rows<64, true, false>(p, stream)
+                              : d == 128 ? fa::launch_rows<128, true, false>(p, stream)
+                                         : fa::launch_rows<256, true, false>(p, stream);
         return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
     }
-    cudaError_t e = fa::launch_paged(p, c, d, stream);
-    if (e == cudaSuccess && num_splits > 1) e = fa::launch_paged_merge(p, d, stream);
+    cudaError_t e = fa::launch_paged<false>(p, c, d, stream);
+    if (e == cudaSuccess && num_splits > 1) e = fa::launch_paged_merge<false>(p, d, stream);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1041,7 +1046,6 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
     if (fa::fill_paged(p, q, cache, page_table, cu_seqlens_q, seqlens_k, o, lse, workspace, B, H, total_q, max_pages,
                        num_splits + prefix_splits, scale) != cudaSuccess)
         return FA_ERR_CUDA;
-    p.join = 1;
     p.base_len = prefix_len;
     p.base_pages = prefix_len / cache->page_size;
     // The prefix, for all rows at once; then the sequences' own keys; then the merge.
@@ -1050,15 +1054,15 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
     const fa::Plan cp = fa::plan_of(p.G, total_q, prefix_len, d, 0, 0);
     fa::cut_paged(p, cp, 1, total_q, prefix_len, prefix_splits);
     if (!fa::encode_cache(p, cache, cp)) return FA_ERR_CUDA;
-    if (fa::launch_paged(p, cp, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+    if (fa::launch_paged<true>(p, cp, d, stream) != cudaSuccess) return FA_ERR_CUDA;
     p.whole = 0;
     p.state0 = 0;
     const fa::Plan c = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
     fa::cut_paged(p, c, B, max_seqlen_q, max_seqlen_k - prefix_len, num_splits);
     if (!fa::encode_cache(p, cache, c)) return FA_ERR_CUDA;
-    if (fa::launch_paged(p, c, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+    if (fa::launch_paged<true>(p, c, d, stream) != cudaSuccess) return FA_ERR_CUDA;
     p.num_splits = num_splits + prefix_splits;
-    return fa::launch_paged_merge(p, d, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return fa::launch_paged_merge<true>(p, d, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

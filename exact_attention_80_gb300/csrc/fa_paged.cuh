@@ -105,22 +105,23 @@ struct PagedParams {
     float scale_log2;
     long long wait_limit;
     unsigned* status;
-    // A batch that shares a prefix (fa_fwd_prefix_fp8): its keys up to base_len, in the
-    // first base_pages entries of the table, are one part, the sequences' own keys the
-    // other. `whole`: this launch is the first part, one problem of all total_q rows
-    // that see all max_k keys. `join`: states are left for a merge in any case, as
-    // numbers state0 .. state0 + num_splits - 1.
-    int base_len, base_pages, whole, join, state0;
+    // A batch that shares a prefix (fa_fwd_prefix_fp8; the kernels' PART forms): its keys
+    // up to base_len, in the first base_pages entries of the table, are one part, the
+    // sequences' own keys the other. `whole`: this launch is the first part, one problem
+    // of all total_q rows that see all max_k keys. Either part leaves its states for a
+    // merge in any case, as numbers state0 .. state0 + num_splits - 1.
+    int base_len, base_pages, whole, state0;
 };
 
 // The new tokens of sequence b (the launch's one problem where `whole`), positions and
 // lengths without the keys of a shared prefix. False where they are broken.
+template <bool PART>
 __device__ __forceinline__ bool paged_tokens(const PagedParams& p, int b, NewTokens& t) {
+    if constexpr (!PART) return new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, t);
     if (p.whole) {
         t = {0, p.total_q, p.max_k};
         return true;
     }
-    if (p.base_len == 0) return new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, t);
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.lens[b] - p.base_len;
     // (A sequence that brings nothing need not hold the prefix.)
     const bool ok = 0 <= c0 && n >= 0 && n <= p.total_q - c0 && n <= p.max_q && (n == 0 || (n <= len && len <= p.max_k));
@@ -131,14 +132,24 @@ __device__ __forceinline__ bool paged_tokens(const PagedParams& p, int b, NewTok
 }
 // Positions: of the first row's token, and their step from token to token (`whole`: the
 // last key's for all).
+template <bool PART>
 __device__ __forceinline__ int paged_start(const PagedParams& p, const NewTokens& t) {
-    return p.whole ? t.len - 1 : t.len - t.n;
+    return PART && p.whole ? t.len - 1 : t.len - t.n;
 }
-__device__ __forceinline__ int paged_step(const PagedParams& p) { return p.whole ? 0 : 1; }
+template <bool PART>
+__device__ __forceinline__ int paged_step(const PagedParams& p) {
+    return PART && p.whole ? 0 : 1;
+}
+// Number of the first of the states that the launch leaves.
+template <bool PART>
+__device__ __forceinline__ int paged_state0(const PagedParams& p) {
+    return PART ? p.state0 : 0;
+}
 
 // The pages of the table's row b that the launch reads.
+template <bool PART>
 __device__ __forceinline__ const int* paged_table(const PagedParams& p, int b) {
-    return p.page_table + static_cast<long long>(b) * p.max_pages + (p.whole ? 0 : p.base_pages);
+    return p.page_table + static_cast<long long>(b) * p.max_pages + (PART && !p.whole ? p.base_pages : 0);
 }
 
 // The first sequence that brings tokens (-1: none). Called by a whole warp.
@@ -240,7 +251,7 @@ constexpr int kTcKeys = 128;
 constexpr int kTcAtOnce = 152;      // its CTAs running at a time: one per SM
 constexpr int kTcStart = 5;         // start and end of a CTA, in key tiles of a pair of slots
 constexpr int kTcBalance = 64;      // sequences up to which a call's pieces are balanced
-cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream);
+cudaError_t launch_paged_tc(const PagedParams& p, int d, bool part, cudaStream_t stream);
 inline int log2_exact(int x) {
     int n = 0;
     while ((1 << n) < x) ++n;

@@ -130,6 +130,7 @@ struct TcWork {
 // makes the waves of CTAs shortest (16 sequences of five drafted tokens over 4600
 // to 16200 keys, 8 kv heads: 8 % less time than with the same length for all calls
 // of the shape). Called by a whole warp; every lane tries one length.
+template <bool PART>
 __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
     int n[kTcBalance / 32];
     int longest = 0;
@@ -138,7 +139,7 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
         const int b = lane + 32 * i;
         NewTokens t;
         n[i] = 0;
-        if (b < p.B && paged_tokens(p, b, t) && t.n > 0)
+        if (b < p.B && paged_tokens<PART>(p, b, t) && t.n > 0)
             n[i] = key_list<kTcKeys>(p.window, p.sinks, t.len - t.n, t.len - 1).n;
         longest = max(longest, n[i]);
     }
@@ -159,7 +160,7 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
     return __shfl_sync(0xffffffffu, len, at);
 }
 
-template <bool DUAL, bool WIDE>
+template <bool DUAL, bool WIDE, bool PART>
 __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork& w) {
     constexpr int ROWS = DUAL || WIDE ? kTcRows : 2 * kTcRows;
     const int per_unit = p.num_splits;
@@ -172,7 +173,7 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     w.h = static_cast<int>(lin % p.Hkv);
     w.b = static_cast<int>(lin / p.Hkv);
     w.nmax = w.n[0] = w.n[1] = 0;
-    w.live = paged_tokens(p, w.b, w.nt);
+    w.live = paged_tokens<PART>(p, w.b, w.nt);
     if (!w.live) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
         return;
@@ -181,14 +182,14 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     const int r0 = unit * ROWS;
     w.live = r0 < w.rows;
     if (!w.live) return;
-    if (p.base_pages > 0) {
+    if constexpr (PART) {
         if (p.whole) w.b = paged_first(p, threadIdx.x & 31);
         else if (r0 == 0 && w.h == 0 && si == 0 && threadIdx.x < 32) paged_check_prefix(p, w.b, threadIdx.x);
         w.live = w.b >= 0;
         if (!w.live) return;
     }
-    w.start = paged_start(p, w.nt);
-    const int step = paged_step(p);
+    w.start = paged_start<PART>(p, w.nt);
+    const int step = paged_step<PART>(p);
     w.p0 = w.start + step * (r0 / p.G);
     w.p1 = w.start + step * ((min(r0 + ROWS, w.rows) - 1) / p.G);
     w.list = key_list<kTcKeys>(p.window, p.sinks, w.p0, w.p1);
@@ -257,7 +258,8 @@ __device__ __forceinline__ int tc_page(const PagedParams& p, const TcWork& w, co
     return id;
 }
 
-template <int D, int SHARES>
+// PART: a part of a batch that shares a prefix (PagedParams).
+template <int D, int SHARES, bool PART>
 __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_kernel(const __grid_constant__ PagedParams p) {
     using L = TcLayout<D, SHARES>;
     constexpr bool DUAL = L::DUAL, WIDE = L::WIDE;
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
     }
     if constexpr (DUAL) {
         if (warp == 2) {
-            const int piece = p.balance ? tc_piece(p, lane) : p.tiles_per_split;
+            const int piece = p.balance ? tc_piece<PART>(p, lane) : p.tiles_per_split;
             if (lane == 0) misc[2] = piece;
         }
     }
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
     if (warp < 4 || warp >= L::CONV_WARP0) {
         setmaxnreg_dec<L::CTRL_REGS>();
         TcWork w;
-        tc_work<DUAL, L::WIDE>(p, piece, w);
+        tc_work<DUAL, L::WIDE, PART>(p, piece, w);
         if (w.live && warp == 0) {
             // -------------------------------------------------------- producer
             // Entries in the issuer's order: K_0; then per step j: V_j, K_{j+1}.
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             // tile's pages are copied one by one; pages behind the sequence's end
             // are left out.
             const bool leader = elect_one();
-            const int* table = paged_table(p, w.b);
+            const int* table = paged_table<PART>(p, w.b);
             const int per = BN >> p.log_page;  // pages per tile (page_size <= 128)
             const uint32_t page_bytes = static_cast<uint32_t>(D) << p.log_page, part_bytes = page_bytes / L::PARTS;
             // Page ids come 32 at a time, a lane each, the next 32 on their way: a
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
         // ------------------------------------------------------------ softmax
         setmaxnreg_inc<L::SOFTMAX_REGS>();
         TcWork w;
-        tc_work<DUAL, L::WIDE>(p, piece, w);
+        tc_work<DUAL, L::WIDE, PART>(p, piece, w);
         const int t = WIDE ? 0 : (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane;  // TMEM lane, row of the Q tile
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const bool row_ok = row < w.rows;
             const int i = (row_ok ? row : w.rows - 1) / p.G;
             const int head = w.h * p.G + (row_ok ? row : w.rows - 1) - i * p.G;
-            const int pos = w.start + paged_step(p) * i;
+            const int pos = w.start + paged_step<PART>(p) * i;
             const long long out_row = static_cast<long long>(w.nt.first + i) * p.H + head;
             float rowf = p.scale_log2;
             {
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
             const uint32_t tS0 = tmem + lane_field + L::S_COL(t);
             const uint32_t tO = tmem + lane_field + L::O_COL(t);
-            const int* table = paged_table(p, w.b);
+            const int* table = paged_table<PART>(p, w.b);
             // Scales of the next tile, 16-key group `lane & 7` per lane, loaded a
             // tile ahead; the page-table entries two tiles ahead, and looked at
             // only then (a test right behind the load would wait for it).
@@ -1005,10 +1007,10 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     const long long to = static_cast<long long>(w.nt.first + qi) * p.H + qh;
                     // States that the row does not use are marked as empty for the
                     // merge.
-                    const bool done = w.used == 1 && !p.join;
+                    const bool done = w.used == 1 && !PART;
                     if (w.split == 0 && p.num_splits > 1)
                         for (int s = (done ? 0 : w.used) + c; s < p.num_splits; s += UNITS)
-                            p.ws_m[static_cast<long long>(p.state0 + s) * p.total_q * p.H + to] = -INFINITY;
+                            p.ws_m[static_cast<long long>(paged_state0<PART>(p) + s) * p.total_q * p.H + to] = -INFINITY;
                     if (done) {
                         const float inv = ll == 0.f ? 0.f : 1.f / ll;
                         *reinterpret_cast<uint2*>(p.o + to * D + 4 * c) =
@@ -1016,7 +1018,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                         if (c == 0)
                             p.lse[static_cast<long long>(qh) * p.total_q + w.nt.first + qi] = state_lse(mm, ll);
                     } else {
-                        const long long at = static_cast<long long>(p.state0 + w.split) * p.total_q * p.H + to;
+                        const long long at = static_cast<long long>(paged_state0<PART>(p) + w.split) * p.total_q * p.H + to;
                         *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
                         if (c == 0) {
                             p.ws_m[at] = state_ref(mm, ll);
@@ -1025,9 +1027,9 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     }
                 }
             } else if (ok) {
-                const bool done = w.used == 1 && !p.join;
+                const bool done = w.used == 1 && !PART;
                 const float f = done ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const long long at = static_cast<long long>(p.state0 + w.split) * p.total_q * p.H + out_row;
+                const long long at = static_cast<long long>(paged_state0<PART>(p) + w.split) * p.total_q * p.H + out_row;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -1063,7 +1065,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     // merge.
                     if (w.split == 0 && p.num_splits > 1)
                         for (int s = done ? 0 : w.used; s < p.num_splits; ++s)
-                            p.ws_m[static_cast<long long>(p.state0 + s) * p.total_q * p.H + out_row] = -INFINITY;
+                            p.ws_m[static_cast<long long>(paged_state0<PART>(p) + s) * p.total_q * p.H + out_row] = -INFINITY;
                     if (done) {
                         p.lse[static_cast<long long>(head) * p.total_q + w.nt.first + i] =
                             state_lse(m, l);
@@ -1083,7 +1085,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D, int SHARES>
+template <int D, int SHARES, bool PART>
 cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
     using L = TcLayout<D, SHARES>;
     static ContextCache<int> attr_set;
@@ -1091,32 +1093,39 @@ cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
     const cudaError_t e = attr_set.get(&done, [](int* out) {
         // The setmaxnreg split is sized for exactly LAUNCH_REGS per thread.
         cudaFuncAttributes a;
-        cudaError_t err = cudaFuncGetAttributes(&a, fa_paged_tc_kernel<D, SHARES>);
+        cudaError_t err = cudaFuncGetAttributes(&a, fa_paged_tc_kernel<D, SHARES, PART>);
         if (err != cudaSuccess) return err;
         if (a.numRegs != L::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
         *out = 1;
-        return cudaFuncSetAttribute(fa_paged_tc_kernel<D, SHARES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(fa_paged_tc_kernel<D, SHARES, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    const long long ctas = static_cast<long long>(PART && p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    return launch_dependent(fa_paged_tc_kernel<D, SHARES>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
+    return launch_dependent(fa_paged_tc_kernel<D, SHARES, PART>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
                             stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tc(const PagedParams& p, int d, cudaStream_t stream) {
+namespace {
+template <bool PART>
+cudaError_t launch_form(const PagedParams& p, int d, cudaStream_t stream) {
     auto launch = [&](auto d_) {
         constexpr int D = decltype(d_)::value;
-        return p.shares == 0   ? launch_tc<D, 0>(p, stream)
-               : p.shares == 1 ? launch_tc<D, 1>(p, stream)
-               : p.shares == 2 ? launch_tc<D, 2>(p, stream)
-                               : launch_tc<D, 4>(p, stream);
+        return p.shares == 0   ? launch_tc<D, 0, PART>(p, stream)
+               : p.shares == 1 ? launch_tc<D, 1, PART>(p, stream)
+               : p.shares == 2 ? launch_tc<D, 2, PART>(p, stream)
+                               : launch_tc<D, 4, PART>(p, stream);
     };
-    if (d == 256) return launch_tc<256, 0>(p, stream);
+    if (d == 256) return launch_tc<256, 0, PART>(p, stream);
     return d == 64 ? launch(Index<64>{}) : launch(Index<128>{});
+}
+}  // namespace
+
+cudaError_t launch_paged_tc(const PagedParams& p, int d, bool part, cudaStream_t stream) {
+    return part ? launch_form<true>(p, d, stream) : launch_form<false>(p, d, stream);
 }
 
 }  // namespace fa
