@@ -61,6 +61,7 @@ namespace {
 
 constexpr int kRows = 16;      // query rows per CTA
 constexpr int kWarps = 4;
+constexpr int kPlaces = 152;   // SMs
 constexpr int kClusterSplits = 8;  // splits that can be a cluster (the portable size)
 // Keys of a warp's tile, and CTAs an SM holds. A warp's tile is a chain of
 // dependent steps, so throughput comes from the warps beside it: short tiles and
@@ -73,7 +74,7 @@ constexpr int kClusterSplits = 8;  // splits that can be a cluster (the portable
 //   d = 256: tiles of 32 keys, one CTA, 4.5; of 16 keys, two CTAs, 5.5
 __host__ __device__ constexpr int rows_keys(int d) { return d == 256 ? 16 : 32; }
 __host__ __device__ constexpr int rows_ctas(int d) { return d == 64 ? 4 : d == 128 ? 3 : 2; }
-template <int D>
+template <int D, bool PART = false>
 struct PagedLayout {
     static constexpr int ROW_BYTES = D < 128 ? D : 128;  // bytes of a swizzled row
     static constexpr int PARTS = D / ROW_BYTES;          // row parts (128-byte columns of a key)
@@ -84,9 +85,9 @@ struct PagedLayout {
     static constexpr int STAGES = D == 64 ? 3 : 2;
     static constexpr uint32_t RING = STAGES * SLOT;      // per warp
     static constexpr bool Q_SHARED = D == 256;           // Q fragments in shared memory, not registers
-    static constexpr uint32_t Q_BYTES = Q_SHARED ? kRows * D * 2 : 0;
+    static constexpr uint32_t Q_BYTES = Q_SHARED ? kRows * D * 2 : 0;  // (PART: each warp its own)
     static constexpr uint32_t Q_OFF = kWarps * RING;
-    static constexpr uint32_t BAR_OFF = Q_OFF + Q_BYTES;
+    static constexpr uint32_t BAR_OFF = Q_OFF + (PART ? kWarps : 1) * Q_BYTES;
     static constexpr uint32_t ML_OFF = BAR_OFF + kWarps * STAGES * 8;  // [warp][m, l][16 rows]
     static constexpr uint32_t CTA_ML_OFF = ML_OFF + kWarps * 2 * kRows * 4;  // [m, l][16 rows] of the CTA
     static constexpr uint32_t BYTES = CTA_ML_OFF + 2 * kRows * 4;
@@ -175,7 +176,7 @@ __device__ __forceinline__ void cluster_meet() {
 template <int D, bool CLUSTER, bool PART>
 __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     fa_paged_rows_kernel(const __grid_constant__ PagedParams p) {
-    using L = PagedLayout<D>;
+    using L = PagedLayout<D, PART>;
     constexpr int KEYS = L::KEYS, NT = KEYS / 8, GROUPS = L::GROUPS;
     constexpr int C = D / 64;    // 64-column parts of the contraction: one 16-byte load each
     constexpr int X = D / 16;    // 16-column units of O
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = sbase + warp * L::RING;
+    const uint32_t q_off = L::Q_OFF + (PART ? warp * L::Q_BYTES : 0);
     const uint32_t bar0 = sbase + L::BAR_OFF + warp * L::STAGES * 8;
     if (lane == 0) {
         for (int s = 0; s < L::STAGES; ++s) mbar_init(bar0 + 8 * s, 1);
@@ -199,38 +201,65 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     // Unit: row blocks fastest (they share K and V in L2), then splits, heads.
-    // (A cluster's CTAs are consecutive: its splits.)
-    unsigned lin = CLUSTER ? blockIdx.x / p.num_splits : blockIdx.x;
-    const int rb = static_cast<int>(lin % p.row_blocks);
-    lin /= p.row_blocks;
-    const int split = static_cast<int>(CLUSTER ? blockIdx.x % p.num_splits : lin % p.num_splits);
-    if (!CLUSTER) lin /= p.num_splits;
-    const int h = static_cast<int>(lin % p.Hkv);
-    int b = static_cast<int>(lin / p.Hkv);
+    // (A cluster's CTAs are consecutive: its splits.) PART: one row block. Where the
+    // sequences' own units fill the GPU (solo), every warp has one of its own, heads
+    // fastest: their lengths differ, and one wave of short units ends together, where
+    // four warps a unit took 2.7 uneven waves (64 sequences of 260 to 2000 keys, 8 kv
+    // heads).
+    const bool whole = PART && blockIdx.x < p.whole_ctas, solo = PART && !whole && p.solo;
+    const int num_splits = whole ? p.shared.num_splits : p.num_splits;
+    const int state0 = whole ? p.shared.state0 : 0;
+    unsigned lin = CLUSTER ? blockIdx.x / num_splits : blockIdx.x;
+    int rb = 0, split, h, b;
+    PagedUnit unit = {};
+    if constexpr (PART) {
+        if (!whole) lin -= p.whole_ctas;
+        if (solo) {
+            lin = lin * kWarps + warp;
+            if (!paged_unit<KEYS>(p, static_cast<int>(lin / p.Hkv), kPlaces * rows_ctas(D) * kWarps / p.Hkv, lane, unit)) return;
+            b = unit.b;
+            split = unit.split;
+        } else {
+            split = static_cast<int>(lin % num_splits);
+            lin /= num_splits;
+            b = whole ? 0 : static_cast<int>(lin / p.Hkv);
+        }
+        h = static_cast<int>(lin % p.Hkv);
+    } else {
+        rb = static_cast<int>(lin % p.row_blocks);
+        lin /= p.row_blocks;
+        split = static_cast<int>(CLUSTER ? blockIdx.x % num_splits : lin % num_splits);
+        if (!CLUSTER) lin /= num_splits;
+        h = static_cast<int>(lin % p.Hkv);
+        b = static_cast<int>(lin / p.Hkv);
+    }
     // (All CTAs of a cluster agree on the returns below.)
     NewTokens nt;
-    if (!paged_tokens<PART>(p, b, nt)) {
-        if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
+    if (!paged_tokens<PART>(p, whole, b, nt)) {
+        if (solo ? lane == 0 : threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
         return;
     }
     const int rows = nt.n * p.G;
     const int r0 = rb * kRows;
     if (r0 >= rows) return;
     if constexpr (PART) {
-        if (p.whole) b = paged_first(p, lane);
-        else if (h == 0 && rb == 0 && split == 0 && warp == 0) paged_check_prefix(p, b, lane);
+        if (whole) b = paged_first(p, lane);
+        else if (h == 0 && split == 0) paged_check_prefix(p, b, lane);
         if (b < 0) return;
     }
-    const int start = paged_start<PART>(p, nt), step = paged_step<PART>(p);  // position of the first query
+    const int start = paged_start(whole, nt), step = whole ? 0 : 1;  // position of the first query
     const int p0 = start + step * (r0 / p.G);
     const int p1 = start + step * ((min(r0 + kRows, rows) - 1) / p.G);
     const KeyList list = key_list<KEYS>(p.window, p.sinks, p0, p1);
-    const int used = max(1, (list.n + p.tiles_per_split - 1) / p.tiles_per_split);
+    const int tiles_per_split = whole ? p.shared.tiles_per_split : p.tiles_per_split;
+    const int used = solo ? unit.used : max(1, (list.n + tiles_per_split - 1) / tiles_per_split);
     if (!CLUSTER && split >= used) return;
-    const int i0 = split * p.tiles_per_split;
-    const int i1 = min(list.n, i0 + p.tiles_per_split);
-    const int mine = max(0, (i1 - i0 - warp + kWarps - 1) / kWarps);  // this warp's tiles: i0 + warp + 4 k
-    const int* table = paged_table<PART>(p, b);
+    const int i0 = solo ? unit.i0 : split * tiles_per_split;
+    const int i1 = solo ? unit.i1 : min(list.n, i0 + tiles_per_split);
+    // This warp's tiles: first + stride k.
+    const int first = solo ? i0 : i0 + warp, stride = solo ? 1 : kWarps;
+    const int mine = max(0, (i1 - first + stride - 1) / stride);
+    const int* table = paged_table<PART>(p, whole, b);
     const int page_size = 1 << p.log_page;
     const int last_page = (nt.len - 1) >> p.log_page;
 
@@ -250,7 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     // Page ids of the warp's next 32 tiles to copy, one tile per lane.
     int ids[GROUPS];
     auto fetch_ids = [&](int k) {
-        const int i = i0 + warp + kWarps * (k + lane);
+        const int i = first + stride * (k + lane);
 #pragma unroll
         for (int e = 0; e < GROUPS; ++e) ids[e] = i < i1 && e < per ? page_of(list.tile(i), e) : -1;
     };
@@ -276,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         for (int i = 1; i < GROUPS; ++i)
             if (e == i) page = id[i];
         if (e < GROUPS && page >= 0) {
-            const int key0 = list.tile(i0 + warp + kWarps * k) * KEYS;
+            const int key0 = list.tile(first + stride * k) * KEYS;
             const int row = ((page * p.Hkv + h) << p.log_page) + (per == 1 ? key0 & (page_size - 1) : 0);
             const CUtensorMap* map = (lane & 1) ? &p.tm_v : &p.tm_k;
 #pragma unroll
@@ -316,9 +345,10 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         }
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        float f, undo;
-        query_scale(mx, f, undo);
-        rowf[e] = p.scale_log2 * undo;
+        const float f = exp2i(query_exponent(mx));
+        // (Exact, as the inverse exponent's power would be, which lets the loop below
+        // be scheduled worse: 441 us for 64 contexts of up to 32768 keys against 437.)
+        rowf[e] = p.scale_log2 * query_undo(mx, 1.f / f);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -331,8 +361,8 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
                     const uint32_t z = pack_f16x2(x[4 * k + 2] * f, x[4 * k + 3] * f);
                     const int ks = 2 * u + k;
                     if constexpr (L::Q_SHARED) {
-                        if (warp == 0) {
-                            uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::Q_OFF) + ((c * 4 + ks) * 32 + lane) * 4;
+                        if (PART || warp == 0) {
+                            uint32_t* dst = reinterpret_cast<uint32_t*>(smem + q_off) + ((c * 4 + ks) * 32 + lane) * 4;
                             dst[e] = a;
                             dst[2 + e] = z;
                         }
@@ -344,7 +374,10 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             }
         }
     }
-    if constexpr (L::Q_SHARED) __syncthreads();
+    if constexpr (L::Q_SHARED) {
+        if constexpr (PART) __syncwarp();
+        else __syncthreads();
+    }
 
     float o[X][2][4];  // [16-column unit][even, odd column of a pair][row g: 2, row g + 8: 2]
 #pragma unroll
@@ -372,7 +405,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     int k = 0;
     for (; k < mine; ++k) {
         if ((k & 31) == 0) {
-            const int i = i0 + warp + kWarps * (k + lane);
+            const int i = first + stride * (k + lane);
 #pragma unroll
             for (int e = 0; e < GROUPS; ++e) {
                 const int id = i < i1 && e < per ? page_of(list.tile(i), e) : -1;
@@ -387,7 +420,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         ok = __all_sync(0xffffffffu, wait_bounded(bar0 + 8 * slot, ring_parity(k, L::STAGES), p.wait_limit, p.status,
                                                   kStatusWaitKvFull));
         if (!ok) break;
-        const int key0 = list.tile(i0 + warp + kWarps * k) * KEYS;
+        const int key0 = list.tile(first + stride * k) * KEYS;
         const uint32_t ks_at = ring + slot * L::SLOT, vs_at = ks_at + L::TILE;
 
         float s[NT][4];
@@ -404,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             for (int ks = 0; ks < 4; ++ks) {
                 uint32_t a[4];
                 if constexpr (L::Q_SHARED) {
-                    ld_shared_v4(a, sbase + L::Q_OFF + ((c * 4 + ks) * 32 + lane) * 16);
+                    ld_shared_v4(a, sbase + q_off + ((c * 4 + ks) * 32 + lane) * 16);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) a[e] = qf[c][ks][e];
@@ -547,15 +580,35 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4*>(stage + (g + 8 * e) * D + 16 * x + 4 * t) =
                 make_float4(o[x][0][2 * e], o[x][1][2 * e], o[x][0][2 * e + 1], o[x][1][2 * e + 1]);
+    auto place = [&](int r) -> long long {
+        const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
+        return static_cast<long long>(nt.first + i) * p.H + h * p.G + j;
+    };
+    if constexpr (PART) {
+        if (solo) {
+            // The warp's own state.
+            __syncwarp();
+            for (int u = lane; u < kRows * (D / 4) && ok; u += 32) {
+                const int r = u / (D / 4), c = u - r * (D / 4);
+                if (r >= rows) break;
+                const long long row = place(r), at = static_cast<long long>(split) * p.total_q * p.H + row;
+                *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = *reinterpret_cast<const float4*>(stage + r * D + 4 * c);
+                if (c == 0) {
+                    p.ws_m[at] = state_ref(ml[r], ml[kRows + r]);
+                    p.ws_l[at] = ml[kRows + r];
+                }
+                // States that the row does not use are marked as empty for the merge.
+                for (int s = used + c; s < num_splits && split == 0; s += D / 4)
+                    p.ws_m[static_cast<long long>(s) * p.total_q * p.H + row] = -INFINITY;
+            }
+            return;
+        }
+    }
     const bool failed = __syncthreads_or(!ok);
     if (!CLUSTER && failed) return;
 
     const float* mls = reinterpret_cast<const float*>(smem + L::ML_OFF);
     constexpr int VEC = D / 4;  // float4 units of a row
-    auto place = [&](int r) -> long long {
-        const int i = (r0 + r) / p.G, j = (r0 + r) - i * p.G;
-        return static_cast<long long>(nt.first + i) * p.H + h * p.G + j;
-    };
     auto put = [&](int r, int c, const float4& a, float mm, float ll) {
         const float inv = ll == 0.f ? 0.f : 1.f / ll;
         *reinterpret_cast<uint2*>(p.o + place(r) * D + 4 * c) =
@@ -594,13 +647,13 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         const long long row = place(r);
         // States that the row does not use are marked as empty for the merge.
         const bool done = used == 1 && !PART;
-        if (split == 0 && p.num_splits > 1)
-            for (int s = (done ? 0 : used) + c; s < p.num_splits; s += VEC)
-                p.ws_m[static_cast<long long>(paged_state0<PART>(p) + s) * p.total_q * p.H + row] = -INFINITY;
+        if (split == 0 && num_splits > 1)
+            for (int s = (done ? 0 : used) + c; s < num_splits; s += VEC)
+                p.ws_m[static_cast<long long>(state0 + s) * p.total_q * p.H + row] = -INFINITY;
         if (done) {
             put(r, c, a, mm, ll);
         } else {
-            const long long at = static_cast<long long>(paged_state0<PART>(p) + split) * p.total_q * p.H + row;
+            const long long at = static_cast<long long>(state0 + split) * p.total_q * p.H + row;
             *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
             if (c == 0) {
                 p.ws_m[at] = state_ref(mm, ll);
@@ -666,7 +719,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     const int i = static_cast<int>(rest % p.max_q);
     const int b = static_cast<int>(rest / p.max_q);
     NewTokens nt;
-    bool live = b < p.B && paged_tokens<PART>(p, b, nt) && i < nt.n;
+    bool live = b < p.B && paged_tokens<PART>(p, false, b, nt) && i < nt.n;
     const long long row = live ? static_cast<long long>(nt.first + i) * p.H + head : 0;
     const long long stride = static_cast<long long>(p.total_q) * p.H;
     const int states = live ? p.num_splits : 0;
@@ -843,7 +896,7 @@ int best_splits(int B, long long units, long long rounds, int slots, bool dual, 
 
 template <int D, bool CLUSTER, bool PART>
 cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
-    using L = PagedLayout<D>;
+    using L = PagedLayout<D, PART>;
     static ContextCache<int> attr_set;
     int done = 0;
     const cudaError_t e = attr_set.get(&done, [](int* out) {
@@ -852,11 +905,22 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(PART && p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    if constexpr (PART) {
+        // Warps for the sequences' own parts, as paged_unit counts them.
+        const long long places = static_cast<long long>(kPlaces) * rows_ctas(D) * kWarps;
+        const long long units = std::min(ctas, std::max(places, static_cast<long long>(p.B) * p.Hkv));
+        ctas = p.whole_ctas + (p.whole ? 0 : p.solo ? (units + kWarps - 1) / kWarps : ctas);
+    }
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent_clusters(fa_paged_rows_kernel<D, CLUSTER, PART>, dim3(static_cast<unsigned>(ctas)),
                                      CLUSTER ? static_cast<unsigned>(p.num_splits) : 1u, kWarps * 32, L::ALLOC, stream,
                                      p);
+}
+// Whether the warps of the sequences' own parts behind a prefix take units alone: where
+// there is a unit for every CTA that runs at once.
+bool solo_units(const Plan& own, int B, int Hkv, int d) {
+    return !own.tc && static_cast<long long>(B) * Hkv >= static_cast<long long>(kPlaces) * rows_ctas(d);
 }
 // The splits of a call as clusters: where all of its CTAs run at once, since a
 // CTA that is done holds its place until the others of its cluster are.
@@ -1022,7 +1086,15 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
 int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int prefix_len, int d,
                          int* prefix_splits) {
     if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q) return 0;
-    const int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    if (own > 0) {
+        // Warps with units alone cut the sequences by their lengths at hand: room for
+        // twice the mean number of splits.
+        const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+        const long long warps = static_cast<long long>(fa::kPlaces) * fa::rows_ctas(d) * fa::kWarps;
+        if (fa::solo_units(c, B, Hkv, d))
+            own = static_cast<int>(std::min(c.tiles, 2 * warps / (static_cast<long long>(B) * Hkv) + 1));
+    }
     const int shared = own > 0 ? fa_paged_num_splits(1, H, Hkv, total_q, prefix_len, d, 0, 0) : 0;
     *prefix_splits = std::min(shared, FA_MAX_SPLITS / 2);
     return shared > 0 ? std::min(own, FA_MAX_SPLITS / 2) : 0;
@@ -1048,19 +1120,30 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
         return FA_ERR_CUDA;
     p.base_len = prefix_len;
     p.base_pages = prefix_len / cache->page_size;
-    // The prefix, for all rows at once; then the sequences' own keys; then the merge.
+    // The prefix, for all rows at once, and the sequences' own keys, in one launch where
+    // both have few rows; then the merge.
+    const fa::Plan whole = fa::plan_of(p.G, total_q, prefix_len, d, 0, 0);
+    const fa::Plan own = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
     p.whole = 1;
     p.state0 = num_splits;
-    const fa::Plan cp = fa::plan_of(p.G, total_q, prefix_len, d, 0, 0);
-    fa::cut_paged(p, cp, 1, total_q, prefix_len, prefix_splits);
-    if (!fa::encode_cache(p, cache, cp)) return FA_ERR_CUDA;
-    if (fa::launch_paged<true>(p, cp, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+    fa::cut_paged(p, whole, 1, total_q, prefix_len, prefix_splits);
+    const long long ctas = p.Hkv * whole.row_blocks * prefix_splits;
+    if (ctas > 0x7fffffffll) return FA_ERR_SHAPE;
+    if (!whole.tc) {
+        p.whole_ctas = static_cast<unsigned>(ctas);
+        p.shared = {p.max_q, p.max_k, p.row_blocks, p.num_splits, p.tiles_per_split, p.state0};
+    }
+    if (whole.tc || own.tc) {
+        if (!fa::encode_cache(p, cache, whole)) return FA_ERR_CUDA;
+        if (fa::launch_paged<true>(p, whole, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+        p.whole_ctas = 0;
+    }
     p.whole = 0;
     p.state0 = 0;
-    const fa::Plan c = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
-    fa::cut_paged(p, c, B, max_seqlen_q, max_seqlen_k - prefix_len, num_splits);
-    if (!fa::encode_cache(p, cache, c)) return FA_ERR_CUDA;
-    if (fa::launch_paged<true>(p, c, d, stream) != cudaSuccess) return FA_ERR_CUDA;
+    fa::cut_paged(p, own, B, max_seqlen_q, max_seqlen_k - prefix_len, num_splits);
+    p.solo = fa::solo_units(own, B, p.Hkv, d);
+    if (!fa::encode_cache(p, cache, own)) return FA_ERR_CUDA;
+    if (fa::launch_paged<true>(p, own, d, stream) != cudaSuccess) return FA_ERR_CUDA;
     p.num_splits = num_splits + prefix_splits;
     return fa::launch_paged_merge<true>(p, d, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

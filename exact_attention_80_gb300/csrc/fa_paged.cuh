@@ -26,19 +26,21 @@ __device__ __forceinline__ float usable_scale(float s) { return fminf(fmaxf(s, 0
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // The scale of a query row, from the bits of its largest |element| as an unsigned
-// maximum (where every NaN and infinity lies above all finite values): `f`, a power
-// of two, brings that element to [2^7, 2^8); f and 1 / f stay normal. `undo` is 1 / f,
-// or NaN where the row holds an element that is not finite: the operands would make
+// maximum (where every NaN and infinity lies above all finite values): f, a power of
+// two, brings that element to [2^7, 2^8); f and 1 / f stay normal. The scores' factor
+// back is 1 / f, or NaN where the row holds an element that is not finite: the operands would make
 // a finite number of it (e4m3 has no infinity), so the row's scores are made NaN.
 __device__ __forceinline__ uint32_t abs_bits_max(uint32_t m, const float (&x)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7fffffffu);
     return m;
 }
-__device__ __forceinline__ void query_scale(uint32_t bits, float& f, float& undo) {
+__device__ __forceinline__ int query_exponent(uint32_t bits) {  // of f
     const int ex = bits > 0u ? min(max(static_cast<int>(bits >> 23) - 127, -100), 120) : 0;
-    f = exp2i(min(7 - ex, 120));
-    undo = bits < 0x7f800000u ? 1.f / f : __uint_as_float(0x7fffffffu);
+    return min(7 - ex, 120);
+}
+__device__ __forceinline__ float query_undo(uint32_t bits, float inverse) {
+    return bits < 0x7f800000u ? inverse : __uint_as_float(0x7fffffffu);
 }
 
 // Four e4m3 codes as two packed f16 pairs (codes 0 and 1, 2 and 3): exact.
@@ -111,15 +113,23 @@ struct PagedParams {
     // of all total_q rows that see all max_k keys. Either part leaves its states for a
     // merge in any case, as numbers state0 .. state0 + num_splits - 1.
     int base_len, base_pages, whole, state0;
+    // A launch of fa_paged_rows_kernel that takes both parts: the first `whole_ctas`
+    // CTAs have the prefix, cut as `shared` says, the others the sequences' own keys;
+    // `solo`: each warp of those a unit of its own (paged_unit).
+    unsigned whole_ctas;
+    int solo;
+    struct {
+        int max_q, max_k, row_blocks, num_splits, tiles_per_split, state0;
+    } shared;
 };
 
-// The new tokens of sequence b (the launch's one problem where `whole`), positions and
-// lengths without the keys of a shared prefix. False where they are broken.
+// The new tokens of sequence b (of the one problem where `whole`), positions and lengths
+// without the keys of a shared prefix. False where they are broken.
 template <bool PART>
-__device__ __forceinline__ bool paged_tokens(const PagedParams& p, int b, NewTokens& t) {
+__device__ __forceinline__ bool paged_tokens(const PagedParams& p, bool whole, int b, NewTokens& t) {
     if constexpr (!PART) return new_tokens(p.cu, p.lens, b, p.total_q, p.max_q, p.max_k, t);
-    if (p.whole) {
-        t = {0, p.total_q, p.max_k};
+    if (whole) {
+        t = {0, p.total_q, p.base_len};
         return true;
     }
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.lens[b] - p.base_len;
@@ -130,26 +140,84 @@ __device__ __forceinline__ bool paged_tokens(const PagedParams& p, int b, NewTok
     t.len = ok && n > 0 ? len : 0;
     return ok;
 }
-// Positions: of the first row's token, and their step from token to token (`whole`: the
-// last key's for all).
+// Position of the first row's token (`whole`: the last key's, for all rows).
+__device__ __forceinline__ int paged_start(bool whole, const NewTokens& t) { return whole ? t.len - 1 : t.len - t.n; }
+// The pages of the table's row b that the part reads.
 template <bool PART>
-__device__ __forceinline__ int paged_start(const PagedParams& p, const NewTokens& t) {
-    return PART && p.whole ? t.len - 1 : t.len - t.n;
-}
-template <bool PART>
-__device__ __forceinline__ int paged_step(const PagedParams& p) {
-    return PART && p.whole ? 0 : 1;
-}
-// Number of the first of the states that the launch leaves.
-template <bool PART>
-__device__ __forceinline__ int paged_state0(const PagedParams& p) {
-    return PART ? p.state0 : 0;
+__device__ __forceinline__ const int* paged_table(const PagedParams& p, bool whole, int b) {
+    return p.page_table + static_cast<long long>(b) * p.max_pages + (PART && !whole ? p.base_pages : 0);
 }
 
-// The pages of the table's row b that the launch reads.
-template <bool PART>
-__device__ __forceinline__ const int* paged_table(const PagedParams& p, int b) {
-    return p.page_table + static_cast<long long>(b) * p.max_pages + (PART && !p.whole ? p.base_pages : 0);
+// A unit of the sequences' own parts: sequence b, its split `split` of `used`, key tiles
+// i0 .. i1 - 1. Splits are as long as lets all units run at once, of which there may be
+// `most` per kv head, and at least p.tiles_per_split tiles, so that the workspace holds
+// them. Unit `r` in the order of the sequences, found by a whole warp; false where there
+// is none. (Lengths are divided in floats, rounded about right: every warp gets the
+// same numbers, and never more splits than tiles / length, rounded up.)
+struct PagedUnit {
+    int b, split, used, i0, i1;
+};
+template <int KEYS>
+__device__ __forceinline__ bool paged_unit(const PagedParams& p, int r, int most, int lane, PagedUnit& u) {
+    auto tiles_of = [&](int i) {  // -1: none
+        NewTokens t;
+        if (i >= p.B) return -1;
+        if (!paged_tokens<true>(p, false, i, t)) return 0;  // broken: one unit, which reports it
+        return t.n > 0 ? (t.len + KEYS - 1) / KEYS : -1;
+    };
+    const int t0 = tiles_of(lane), t1 = p.B > 32 ? tiles_of(32 + lane) : -1;  // the others are read again
+    int sum = 0, live = 0;
+    auto each = [&](auto&& f) {
+        f(t0);
+        if (p.B > 32) f(t1);
+#pragma unroll 1
+        for (int c = 64; c < p.B; c += 32) f(tiles_of(c + lane));
+    };
+    each([&](int t) { sum += max(t, 0), live += t >= 0 ? 1 : 0; });
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    live = __reduce_add_sync(0xffffffffu, live);
+    float inv;
+    auto pieces = [&](int t) { return t < 0 ? 0 : max(1, static_cast<int>(fmaf(static_cast<float>(t), inv, 0.999f))); };
+    // A sequence's last split is half full on average: tried first. One whole length per
+    // sequence on top of its share never is too many.
+    int length = max((p.max_k + KEYS - 1) / KEYS, 1);
+#pragma unroll 1
+    for (int round = 0; round < 2 && most > live; ++round) {
+        const int room = most - (round ? live : live / 2);
+        const int at = (sum + room - 1) / room;
+        inv = 1.f / static_cast<float>(at);
+        int k = 0;
+        each([&](int t) { k += pieces(t); });
+        if (round || __reduce_add_sync(0xffffffffu, k) <= most) {
+            length = at;
+            break;
+        }
+    }
+    inv = 1.f / static_cast<float>(max(length, p.tiles_per_split));
+#pragma unroll 1
+    for (int c = 0; c < p.B; c += 32) {
+        int tiles = c == 0 ? t0 : c == 32 ? t1 : tiles_of(c + lane);
+        const int k = pieces(tiles);
+        int upto = k;  // units of this and the lower lanes
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, r < upto);
+        if (here) {
+            const int who = __ffs(here) - 1;
+            u.b = c + who;
+            u.split = r - __shfl_sync(0xffffffffu, upto - k, who);
+            u.used = __shfl_sync(0xffffffffu, k, who);
+            tiles = max(__shfl_sync(0xffffffffu, tiles, who), 0);
+            // Even parts.
+            u.i0 = static_cast<int>(static_cast<long long>(tiles) * u.split / u.used);
+            u.i1 = static_cast<int>(static_cast<long long>(tiles) * (u.split + 1) / u.used);
+            return true;
+        }
+        r -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
 }
 
 // The first sequence that brings tokens (-1: none). Called by a whole warp.
@@ -168,8 +236,19 @@ __device__ __forceinline__ void paged_check_prefix(const PagedParams& p, int b, 
     if (first < 0 || first == b) return;
     const int* x = p.page_table + static_cast<long long>(first) * p.max_pages;
     const int* y = p.page_table + static_cast<long long>(b) * p.max_pages;
-    for (int i = lane; i < p.base_pages; i += 32)
-        if (x[i] != y[i]) atomicOr(p.status, kStatusBadPage);
+    bool same = true;
+    for (int i0 = lane; i0 < p.base_pages; i0 += 256) {  // eight loads of each in flight
+        int u[8], v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + 32 * k;
+            u[k] = i < p.base_pages ? x[i] : 0;
+            v[k] = i < p.base_pages ? y[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) same = same && u[k] == v[k];
+    }
+    if (!same) atomicOr(p.status, kStatusBadPage);
 }
 
 // What a partial state leaves as its reference m: -inf marks a state that saw no
@@ -220,6 +299,9 @@ template <int OFF>
 __device__ __forceinline__ void st_shared_v4_at(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0 + %1], {%2, %3, %4, %5};" ::"r"(addr), "n"(OFF), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 // f(Index<0>) .. f(Index<N - 1>): a loop whose index is a constant, for immediate
 // operands.

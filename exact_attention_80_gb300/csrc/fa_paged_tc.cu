@@ -139,7 +139,7 @@ __device__ __forceinline__ int tc_piece(const PagedParams& p, int lane) {
         const int b = lane + 32 * i;
         NewTokens t;
         n[i] = 0;
-        if (b < p.B && paged_tokens<PART>(p, b, t) && t.n > 0)
+        if (b < p.B && paged_tokens<PART>(p, false, b, t) && t.n > 0)
             n[i] = key_list<kTcKeys>(p.window, p.sinks, t.len - t.n, t.len - 1).n;
         longest = max(longest, n[i]);
     }
@@ -173,7 +173,7 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
     w.h = static_cast<int>(lin % p.Hkv);
     w.b = static_cast<int>(lin / p.Hkv);
     w.nmax = w.n[0] = w.n[1] = 0;
-    w.live = paged_tokens<PART>(p, w.b, w.nt);
+    w.live = paged_tokens<PART>(p, PART && p.whole, w.b, w.nt);
     if (!w.live) {
         if (threadIdx.x == 0) atomicOr(p.status, kStatusBadSeqlens);
         return;
@@ -188,8 +188,8 @@ __device__ __forceinline__ void tc_work(const PagedParams& p, int piece, TcWork&
         w.live = w.b >= 0;
         if (!w.live) return;
     }
-    w.start = paged_start<PART>(p, w.nt);
-    const int step = paged_step<PART>(p);
+    w.start = paged_start(PART && p.whole, w.nt);
+    const int step = PART && p.whole ? 0 : 1;
     w.p0 = w.start + step * (r0 / p.G);
     w.p1 = w.start + step * ((min(r0 + ROWS, w.rows) - 1) / p.G);
     w.list = key_list<kTcKeys>(p.window, p.sinks, w.p0, w.p1);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             // tile's pages are copied one by one; pages behind the sequence's end
             // are left out.
             const bool leader = elect_one();
-            const int* table = paged_table<PART>(p, w.b);
+            const int* table = paged_table<PART>(p, PART && p.whole, w.b);
             const int per = BN >> p.log_page;  // pages per tile (page_size <= 128)
             const uint32_t page_bytes = static_cast<uint32_t>(D) << p.log_page, part_bytes = page_bytes / L::PARTS;
             // Page ids come 32 at a time, a lane each, the next 32 on their way: a
@@ -668,44 +668,56 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const bool row_ok = row < w.rows;
             const int i = (row_ok ? row : w.rows - 1) / p.G;
             const int head = w.h * p.G + (row_ok ? row : w.rows - 1) - i * p.G;
-            const int pos = w.start + paged_step<PART>(p) * i;
+            const int pos = w.start + (PART && p.whole ? 0 : i);
             const long long out_row = static_cast<long long>(w.nt.first + i) * p.H + head;
             float rowf = p.scale_log2;
             {
-                // Q's two e4m3 terms into the tile's swizzled rows.
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + out_row * D);
-                uint32_t mx = 0u;
-#pragma unroll 4
-                for (int u = 0; u < D / 8; ++u) {
-                    float x[8];
-                    unpack_bf16x8(src[u], x);
-                    mx = abs_bits_max(mx, x);
-                }
-                float f, undo;
-                query_scale(mx, f, undo);
-                rowf *= undo;
-                const uint32_t hi_at = sbase + L::Q_OFF + t * L::Q_TILE + r * L::ROW_BYTES;
-#pragma unroll 2
-                for (int u = 0; u < (DUAL && t == 1 ? 0 : D / 16); ++u) {
-                    float x[16];
-                    float(&x0)[8] = *reinterpret_cast<float(*)[8]>(x);
-                    float(&x1)[8] = *reinterpret_cast<float(*)[8]>(x + 8);
-                    unpack_bf16x8(src[2 * u], x0);
-                    unpack_bf16x8(src[2 * u + 1], x1);
-                    uint32_t hi[4], lo[4];
+                // Q's two e4m3 terms into the tile's swizzled rows. The warp reads its 32
+                // rows together, eight columns a lane, whole lines at a time (a thread for
+                // its own row took 7.5 us at d = 128, two passes over lines that 32 lanes
+                // touch one by one; this 5.8, most of it the conversions themselves).
+                constexpr int LPR = D / 8, RPI = 32 / LPR;      // lanes of a row, rows of a load
+                constexpr int LOADS = 4;                        // at once
+                const int c8 = lane % LPR;
+                const bool writes = !(DUAL && t == 1);
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32 / RPI; i0 += LOADS) {
+                    uint4 raw[LOADS];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float y[4], z[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = x[4 * k + e] * f;
-                        hi[k] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
-                        decode_e4m3x4(hi[k], z);
-                        lo[k] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+                    for (int k = 0; k < LOADS; ++k) {
+                        const long long from = __shfl_sync(0xffffffffu, out_row, (i0 + k) * RPI + lane / LPR);
+                        raw[k] = reinterpret_cast<const uint4*>(p.q + from * D)[c8];
                     }
-                    const uint32_t at = hi_at + (D == 64 ? (u ^ ((r >> 1) & 3)) << 4
-                                                         : (u >> 3) * L::PART + (((u & 7) ^ (r & 7)) << 4));
-                    st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
-                    st_shared_v4(at + L::Q_TERM, lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int k = 0; k < LOADS; ++k) {
+                        float x[8];
+                        unpack_bf16x8(raw[k], x);
+                        uint32_t mx = abs_bits_max(0u, x);
+#pragma unroll
+                        for (int o = LPR / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const int fe = query_exponent(mx);
+                        const float f = exp2i(fe), undo = query_undo(mx, exp2i(-fe));
+                        const float mine = __shfl_sync(0xffffffffu, undo, (lane % RPI) * LPR);
+                        if (lane / RPI == i0 + k) rowf = p.scale_log2 * mine;
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int e4 = 0; e4 < 2; ++e4) {
+                            float y[4], z[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = x[4 * e4 + e] * f;
+                            hi[e4] = pack_e4m3x4(y[0], y[1], y[2], y[3]);
+                            decode_e4m3x4(hi[e4], z);
+                            lo[e4] = pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+                        }
+                        const int R = quarter * 32 + (i0 + k) * RPI + lane / LPR, u = c8 >> 1;  // row, 16-byte unit
+                        const uint32_t at = sbase + L::Q_OFF + t * L::Q_TILE + R * L::ROW_BYTES + (c8 & 1) * 8 +
+                                            (D == 64 ? (u ^ ((R >> 1) & 3)) << 4
+                                                     : (u >> 3) * L::PART + (((u & 7) ^ (R & 7)) << 4));
+                        if (writes) {
+                            st_shared_v2(at, hi[0], hi[1]);
+                            st_shared_v2(at + L::Q_TERM, lo[0], lo[1]);
+                        }
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -714,7 +726,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             const uint32_t lane_field = static_cast<uint32_t>(quarter * 32) << 16;
             const uint32_t tS0 = tmem + lane_field + L::S_COL(t);
             const uint32_t tO = tmem + lane_field + L::O_COL(t);
-            const int* table = paged_table<PART>(p, w.b);
+            const int* table = paged_table<PART>(p, PART && p.whole, w.b);
             // Scales of the next tile, 16-key group `lane & 7` per lane, loaded a
             // tile ahead; the page-table entries two tiles ahead, and looked at
             // only then (a test right behind the load would wait for it).
@@ -1010,7 +1022,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     const bool done = w.used == 1 && !PART;
                     if (w.split == 0 && p.num_splits > 1)
                         for (int s = (done ? 0 : w.used) + c; s < p.num_splits; s += UNITS)
-                            p.ws_m[static_cast<long long>(paged_state0<PART>(p) + s) * p.total_q * p.H + to] = -INFINITY;
+                            p.ws_m[static_cast<long long>((PART ? p.state0 : 0) + s) * p.total_q * p.H + to] = -INFINITY;
                     if (done) {
                         const float inv = ll == 0.f ? 0.f : 1.f / ll;
                         *reinterpret_cast<uint2*>(p.o + to * D + 4 * c) =
@@ -1018,7 +1030,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                         if (c == 0)
                             p.lse[static_cast<long long>(qh) * p.total_q + w.nt.first + qi] = state_lse(mm, ll);
                     } else {
-                        const long long at = static_cast<long long>(paged_state0<PART>(p) + w.split) * p.total_q * p.H + to;
+                        const long long at = static_cast<long long>((PART ? p.state0 : 0) + w.split) * p.total_q * p.H + to;
                         *reinterpret_cast<float4*>(p.ws_o + at * D + 4 * c) = a;
                         if (c == 0) {
                             p.ws_m[at] = state_ref(mm, ll);
@@ -1029,7 +1041,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
             } else if (ok) {
                 const bool done = w.used == 1 && !PART;
                 const float f = done ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-                const long long at = static_cast<long long>(paged_state0<PART>(p) + w.split) * p.total_q * p.H + out_row;
+                const long long at = static_cast<long long>((PART ? p.state0 : 0) + w.split) * p.total_q * p.H + out_row;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -1065,7 +1077,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
                     // merge.
                     if (w.split == 0 && p.num_splits > 1)
                         for (int s = done ? 0 : w.used; s < p.num_splits; ++s)
-                            p.ws_m[static_cast<long long>(paged_state0<PART>(p) + s) * p.total_q * p.H + out_row] = -INFINITY;
+                            p.ws_m[static_cast<long long>((PART ? p.state0 : 0) + s) * p.total_q * p.H + out_row] = -INFINITY;
                     if (done) {
                         p.lse[static_cast<long long>(head) * p.total_q + w.nt.first + i] =
                             state_lse(m, l);
