@@ -1133,14 +1133,16 @@ struct BwdPlace {
 };
 
 // Sixteen bytes of a row in fp32, and the dot product over a row's LANES threads.
-__device__ __forceinline__ void bwd_load8(const __nv_bfloat16* src, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(src);
+__device__ __forceinline__ void bwd_unpack8(const uint4& u, float (&x)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         x[2 * e] = __uint_as_float(w[e] << 16);
         x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
     }
+}
+__device__ __forceinline__ void bwd_load8(const __nv_bfloat16* src, float (&x)[8]) {
+    bwd_unpack8(*reinterpret_cast<const uint4*>(src), x);
 }
 template <int LANES>
 __device__ __forceinline__ float bwd_dot(unsigned mine, const float (&a)[8], const float (&b)[8]) {
@@ -1151,20 +1153,28 @@ __device__ __forceinline__ float bwd_dot(unsigned mine, const float (&a)[8], con
     return s;
 }
 
-// fa_bwd_win_pre_kernel on packed sequences: a block takes 64 padded rows of a head,
-// which are one sequence's.
+// fa_bwd_win_pre_kernel on packed sequences: a block takes 64 padded rows, which are one
+// sequence's, of pre_heads(D) heads. Bound by memory (O and dO are read, the fp32 dQ is
+// zeroed): the rows of up to four passes are loaded before the first is used. Rows that
+// see few keys come in a loop of their own behind, four keys at a time: one key after the
+// other they took longer than all other rows (24 documents of up to 2047 tokens, 16 heads
+// of 128: 88 us).
+__host__ __device__ constexpr int pre_heads(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
 template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_pack_pre_kernel(const __nv_bfloat16* __restrict__ q,
-                                                              const __nv_bfloat16* __restrict__ k,
-                                                              const __nv_bfloat16* __restrict__ v,
-                                                              const __nv_bfloat16* __restrict__ o,
-                                                              const __nv_bfloat16* __restrict__ dout,
-                                                              const float* __restrict__ lse,
-                                                              const __grid_constant__ BwdParams p) {
-    constexpr int LANES = D / 8, ROWS = 256 / LANES;
+__global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bfloat16* __restrict__ q,
+                                                                 const __nv_bfloat16* __restrict__ k,
+                                                                 const __nv_bfloat16* __restrict__ v,
+                                                                 const __nv_bfloat16* __restrict__ o,
+                                                                 const __nv_bfloat16* __restrict__ dout,
+                                                                 const float* __restrict__ lse,
+                                                                 const __grid_constant__ BwdParams p) {
+    constexpr int LANES = D / 8, ROWS = 256 / LANES, PASSES = kBwdHalf / ROWS, U = PASSES < 4 ? PASSES : 4;
     __shared__ BwdPlace place;
-    const int lane = threadIdx.x % LANES, h = blockIdx.y, c = lane * 8;
-    const long long first = static_cast<long long>(blockIdx.x) * kBwdHalf;
+    const int lane = threadIdx.x % LANES, c = lane * 8, r0 = threadIdx.x / LANES;
+    // (Heads fastest: the blocks at hand read whole tokens.)
+    const unsigned parts = (p.H + pre_heads(D) - 1) / pre_heads(D);
+    const long long first = static_cast<long long>(blockIdx.x / parts) * kBwdHalf;
+    const int h0 = static_cast<int>(blockIdx.x % parts) * pre_heads(D), h1 = min(p.H, h0 + pre_heads(D));
     if (threadIdx.x < 32) {
         BwdPlace x = {};
         x.b = bwd_pack_find(p, first, false, threadIdx.x, x.s);
@@ -1175,44 +1185,81 @@ __global__ void __launch_bounds__(256) fa_bwd_pack_pre_kernel(const __nv_bfloat1
     const PackedSeq s = place.s;
     const int i0 = static_cast<int>(first - pad_row(s.q0, place.b));
     const unsigned mine = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
-#pragma unroll 2
-    for (int r = threadIdx.x / LANES; r < kBwdHalf; r += ROWS) {
-        const int i = i0 + r;
-        const long long row = static_cast<long long>(h) * p.rows_pad + first + r;
-        float dd = 0.f, nl = -INFINITY;
-        if (i < s.n) {
-            float4* z = reinterpret_cast<float4*>(p.dq_acc + row * D);
-            z[lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-            z[lane + LANES] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const long long token = s.q0 + i;
-            const float l = lse[static_cast<long long>(h) * p.seqs.total_q + token];
-            float g[8], a[8];
-            bwd_load8(dout + token * p.do_stride + static_cast<long long>(h) * D + c, g);
-            nl = (l == -INFINITY) ? -INFINITY : -(l * kLog2e);
-            // Visible keys: [0, ns) and [w0, pos].
-            const int pos = i + s.m - s.n;
-            const int w0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-            const int ns = min(p.sinks, w0);
-            const int seen = pos < 0 ? 0 : ns + pos + 1 - w0;
-            if (seen > kFewKeys) {
-                bwd_load8(o + (token * p.H + h) * D + c, a);
-                dd = bwd_dot<LANES>(mine, a, g);
-            } else if (nl != -INFINITY) {
-                bwd_load8(q + token * p.q_stride + static_cast<long long>(h) * D + c, a);
-                const long long head = static_cast<long long>(h / p.group) * D + c;
-                for (int n = 0; n < seen; ++n) {
-                    const long long key = s.k0 + (n < ns ? n : w0 + (n - ns));
-                    float kr[8], vr[8];
-                    bwd_load8(k + key * p.k_stride + head, kr);
-                    bwd_load8(v + key * p.v_stride + head, vr);
-                    dd = fmaf(ex2(fmaf(bwd_dot<LANES>(mine, a, kr), p.scale_log2, nl)), bwd_dot<LANES>(mine, g, vr), dd);
+    const uint32_t zero[8] = {};
+    // Visible keys of row i: [0, ns) and [w0, w0 + seen - ns).
+    auto visible = [&](int i, int& ns, int& w0) {
+        const int pos = i + s.m - s.n;
+        w0 = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+        ns = min(p.sinks, w0);
+        return pos < 0 ? 0 : ns + pos + 1 - w0;
+    };
+    bool few = false;
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h) {
+#pragma unroll 1
+        for (int e0 = 0; e0 < PASSES; e0 += U) {
+            uint4 g_raw[U], o_raw[U];
+            float l[U];
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                const long long token = s.q0 + min(i0 + r0 + (e0 + e) * ROWS, s.n - 1);
+                l[e] = lse[static_cast<long long>(h) * p.seqs.total_q + token];
+                g_raw[e] = *reinterpret_cast<const uint4*>(dout + token * p.do_stride + static_cast<long long>(h) * D + c);
+                o_raw[e] = *reinterpret_cast<const uint4*>(o + (token * p.H + h) * D + c);
+            }
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                const int r = r0 + (e0 + e) * ROWS, i = i0 + r;
+                const long long row = static_cast<long long>(h) * p.rows_pad + first + r;
+                if (i < s.n) st_global_v8(p.dq_acc + row * D + c, zero);
+                float g[8], a[8];
+                bwd_unpack8(g_raw[e], g);
+                bwd_unpack8(o_raw[e], a);
+                const float dd = bwd_dot<LANES>(mine, a, g);
+                int ns, w0;
+                const int seen = visible(i, ns, w0);
+                const bool by_keys = i < s.n && seen > 0 && seen <= kFewKeys;
+                few = few || by_keys;
+                if (lane == 0) {
+                    if (!by_keys) const_cast<float*>(p.ndd)[row] = i < s.n && seen > 0 ? -dd : 0.f;
+                    const_cast<float*>(p.nlse2)[row] = i < s.n && l[e] != -INFINITY ? -(l[e] * kLog2e) : -INFINITY;
                 }
             }
         }
-        if (lane == 0) {
-            const_cast<float*>(p.ndd)[row] = -dd;
-            const_cast<float*>(p.nlse2)[row] = nl;
+    }
+    if (!few) return;
+#pragma unroll 1
+    for (int e = 0; e < PASSES * (h1 - h0); ++e) {
+        const int h = h0 + e / PASSES, r = r0 + e % PASSES * ROWS, i = i0 + r;
+        int ns, w0;
+        const int seen = visible(i, ns, w0);
+        if (i >= s.n || seen == 0 || seen > kFewKeys) continue;
+        const long long token = s.q0 + i, head = static_cast<long long>(h / p.group) * D + c;
+        const float l = lse[static_cast<long long>(h) * p.seqs.total_q + token];
+        const float nl = l == -INFINITY ? -INFINITY : -(l * kLog2e);
+        float a[8], g[8], dd = 0.f;
+        bwd_load8(q + token * p.q_stride + static_cast<long long>(h) * D + c, a);
+        bwd_load8(dout + token * p.do_stride + static_cast<long long>(h) * D + c, g);
+#pragma unroll 1
+        for (int n0 = 0; n0 < seen; n0 += 4) {
+            uint4 k_raw[4], v_raw[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int n = min(n0 + u, seen - 1);
+                const long long key = s.k0 + (n < ns ? n : w0 + (n - ns));
+                k_raw[u] = *reinterpret_cast<const uint4*>(k + key * p.k_stride + head);
+                v_raw[u] = *reinterpret_cast<const uint4*>(v + key * p.v_stride + head);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float kr[8], vr[8];
+                bwd_unpack8(k_raw[u], kr);
+                bwd_unpack8(v_raw[u], vr);
+                const float w = ex2(fmaf(bwd_dot<LANES>(mine, a, kr), p.scale_log2, nl)), dp = bwd_dot<LANES>(mine, g, vr);
+                if (n0 + u < seen) dd = fmaf(w, dp, dd);
+            }
         }
+        if (lane == 0) const_cast<float*>(p.ndd)[static_cast<long long>(h) * p.rows_pad + first + r] = -dd;
     }
 }
 
@@ -1459,8 +1506,9 @@ template <int D>
 cudaError_t launch_bwd_pack(const BwdParams& p, const void* q, const void* k, const void* v, const void* o,
                             const void* dout, const float* lse, void* dq, long long slots, cudaStream_t stream) {
     using T = const __nv_bfloat16*;
-    const dim3 grid(static_cast<unsigned>(p.rows_pad / kBwdHalf), static_cast<unsigned>(p.H), 1);
-    fa_bwd_pack_pre_kernel<D><<<grid, 256, 0, stream>>>(static_cast<T>(q), static_cast<T>(k), static_cast<T>(v),
+    const long long blocks = p.rows_pad / kBwdHalf * ((p.H + pre_heads(D) - 1) / pre_heads(D));
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    fa_bwd_pack_pre_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(static_cast<T>(q), static_cast<T>(k), static_cast<T>(v),
                                                         static_cast<T>(o), static_cast<T>(dout), lse, p);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_bwd_main<D, true, true>(p, stream);

@@ -7,7 +7,9 @@
 // K and V together). A thread holds one token's sixteen codes at a time, of one head's K
 // or V after the other: sixteen bytes loaded, 32 written, all loads of a thread
 // independent of one another behind the token's page. Which sequence a token belongs to
-// is found once per block, so the chain is offsets, page, codes.
+// is found once per block, so the chain is offsets, page, codes. A thread's 32 bytes go
+// out as one store: as two of sixteen, each leaves half of every sector to the other
+// (eight contexts of up to 16200 tokens, 8 heads of 128: 84.7 us against 66.1, 6.06 TB/s).
 #include <algorithm>
 #include <cstring>
 
@@ -35,7 +37,7 @@ constexpr int kReadThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_constant__ ReadParams p) {
-    constexpr int LANES = D / 16, TOKENS = kReadThreads / LANES, UNROLL = 8;
+    constexpr int LANES = D / 16, TOKENS = kReadThreads / LANES, UNROLL = 16;
     __shared__ int seq_of[TOKENS];
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
@@ -63,9 +65,7 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_c
         return p.out[w] + static_cast<long long>(token) * p.stride[w] + static_cast<long long>(item >> 1) * D + lane * 16;
     };
     auto put = [&](__nv_bfloat16* to, const uint32_t (&x)[8]) {
-        uint4* y = reinterpret_cast<uint4*>(to);
-        y[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        y[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        st_global_v8(to, x);
     };
     if (b < 0) {
         if (!p.fill) return;

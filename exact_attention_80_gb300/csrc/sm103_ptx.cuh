@@ -76,6 +76,13 @@ __device__ __forceinline__ void ld_shared_v4f(uint32_t addr, float (&x)[4]) {
                  : "memory");
 }
 
+// 32-byte global store (32-byte aligned): whole sectors.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&x)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 // 4-byte shared-memory store and load.
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
