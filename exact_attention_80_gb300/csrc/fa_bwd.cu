@@ -122,12 +122,16 @@ constexpr int kBwdKeys = 128;   // keys per CTA (TMEM lanes of S^T, dP^T, dV, dK
 constexpr int kBwdHalf = 64;    // queries per step
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+// WIN: the form under a window (and on packed sequences). At d = 64 TMEM then holds a
+// third step buffer; the dense form gains nothing from it (1069 against 1063 us for 8 x 32
+// heads of 2048 rows; under a window of 512 with heads in groups of four 406 against 448).
+template <int D, bool WIN = false>
 struct LayoutBwd {
     static_assert(D == 64 || D == 128 || D == 256, "head dim 64, 128 or 256");
     static constexpr int DH = D < 128 ? D : 128;        // head-dim columns of dV, dK, dQ a CTA owns
     static constexpr int HALVES = D / DH;               // CTAs per key tile
-    static constexpr int STAGES = D == 256 ? 1 : 3;     // Q/dO (+ -LSE log2e, -D) ring slots
+    static constexpr int BUFS = D == 64 && WIN ? 3 : 2;        // step buffers in TMEM
+    static constexpr int STAGES = D == 256 ? 1 : BUFS == 3 ? 5 : 3;  // Q/dO (+ -LSE log2e, -D) ring slots
     // warp 0 producer, warp 1 issuer, warps 2-3 idle, warps 4-11 compute (two
     // per TMEM lane quarter, one per 32-query chunk of a step), warps 12-15
     // dQ readout (one per lane quarter; at D = 64 the first two only).
@@ -154,7 +158,7 @@ struct LayoutBwd {
     static constexpr uint32_t STAGE_OFF = V_OFF + V_BYTES;           // [stage]: Q, dO
     static constexpr uint32_t Q_IN = 0, DO_IN = QH_BYTES;
     static constexpr uint32_t DS_OFF = STAGE_OFF + STAGES * STAGE_BYTES;  // [buffer]
-    static constexpr uint32_t ROWS_OFF = DS_OFF + 2 * DS_BYTES;     // [stage]: -LSE log2e, -D
+    static constexpr uint32_t ROWS_OFF = DS_OFF + BUFS * DS_BYTES;     // [stage]: -LSE log2e, -D
     static constexpr uint32_t NL_IN = 0, ND_IN = ROWS_BYTES;
     static constexpr uint32_t BAR_OFF = ROWS_OFF + STAGES * 2 * ROWS_BYTES;
     static_assert(STAGE_OFF % 1024 == 0 && STAGE_BYTES % 1024 == 0 && QH_CHUNK % 1024 == 0 &&
@@ -163,22 +167,23 @@ struct LayoutBwd {
     static constexpr int BAR_QFULL = 1;                    // [stage]
     static constexpr int BAR_QEMPTY = BAR_QFULL + STAGES;   // [stage]
     static constexpr int BAR_SFULL = BAR_QEMPTY + STAGES;   // [buffer] S^T, dP^T done
-    static constexpr int BAR_PREADY = BAR_SFULL + 2;    // [buffer] P^T, dS^T written (one arrival per compute warp)
-    static constexpr int BAR_DQFULL = BAR_PREADY + 2;   // [buffer] dQ^T done (and every earlier MMA)
-    static constexpr int BAR_DQREAD = BAR_DQFULL + 2;   // [buffer] dQ^T read (one arrival per readout warp)
-    static constexpr int BAR_KVFREE = BAR_DQREAD + 2;   // the first of two key tiles' MMAs done
+    static constexpr int BAR_PREADY = BAR_SFULL + BUFS;    // [buffer] P^T, dS^T written (one arrival per compute warp)
+    static constexpr int BAR_DQFULL = BAR_PREADY + BUFS;   // [buffer] dQ^T done (and every earlier MMA)
+    static constexpr int BAR_DQREAD = BAR_DQFULL + BUFS;   // [buffer] dQ^T read (one arrival per readout warp)
+    static constexpr int BAR_KVFREE = BAR_DQREAD + BUFS;   // the first of two key tiles' MMAs done
     static constexpr int BAR_ACCFREE = BAR_KVFREE + 1;  // its dK, dV read out of TMEM (one arrival per compute warp)
     static constexpr int BAR_DRAIN = BAR_ACCFREE + 1;
     static constexpr int NUM_BARS = BAR_DRAIN + 1;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr uint32_t BYTES = MISC_OFF + 16;
     static constexpr size_t ALLOC_BYTES = BYTES + 1024;
-    // TMEM columns. Buffer b (b = step & 1) at 128 b: S^T in its first 64
+    // TMEM columns. Buffer b (b = step % BUFS) at 128 b: S^T in its first 64
     // columns (then P^T packed over their first halves, then dQ^T), dP^T in
     // the next 64 (then dS^T packed over their first halves). dV and dK last
     // (D columns each).
     __host__ __device__ static constexpr uint32_t BUF_COL(int b) { return 128u * static_cast<uint32_t>(b); }
-    static constexpr uint32_t DP_IN = 64, DV_COL = 256, DK_COL = 384;
+    static constexpr uint32_t DP_IN = 64, DV_COL = 128 * BUFS, DK_COL = DV_COL + (512 - DV_COL) / 2;
+    static_assert(DV_COL + 2 * DH <= 512 && DK_COL + DH <= 512, "dV and dK overflow TMEM");
     static_assert(ALLOC_BYTES <= 232448, "shared memory over the 227 KB per-CTA limit");
     static_assert(THREADS * 128 <= 65536, "registers: 128 per thread at most");
 };
@@ -335,7 +340,7 @@ __device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h,
 // tiles kt and k_tiles - 1 - kt, run one after the other: the steps of a tile
 // fall with its index, so every pair has about the same number of steps and no
 // CTA is left with the few steps of a last tile alone. The two tiles share the
-// step sequence: global step G (over both tiles) uses TMEM buffer G & 1 and
+// step sequence: global step G (over both tiles) uses TMEM buffer G % BUFS and
 // ring slot G % STAGES. Between the tiles K and V are reloaded once the first
 // tile's MMAs are done (KVFREE) and the first MMA into dV and dK waits until
 // the compute group has read the first tile's out of TMEM (ACCFREE).
@@ -362,9 +367,9 @@ __device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h,
 // with zeros before the MMAs read them, since a weight of zero does not undo an
 // infinity or a NaN.
 template <int D, bool WIN = false, bool PACK = false>
-__global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(LayoutBwd<D, WIN>::THREADS, 1) fa_bwd_kernel(const __grid_constant__ BwdParams p) {
     static_assert(WIN || !PACK, "packed sequences take the window's form");
-    using L = LayoutBwd<D>;
+    using L = LayoutBwd<D, WIN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             mbar_init(bar(L::BAR_QFULL + st), 1);
             mbar_init(bar(L::BAR_QEMPTY + st), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < L::BUFS; ++b) {
             mbar_init(bar(L::BAR_SFULL + b), 1);
             mbar_init(bar(L::BAR_PREADY + b), L::COMPUTE_WARPS);
             mbar_init(bar(L::BAR_DQFULL + b), 1);
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
         auto desc = [](uint32_t lo, uint32_t hi, uint32_t off) -> uint64_t {
             return (static_cast<uint64_t>(hi) << 32) | (lo + (off >> 4));
         };
-        // S^T_G = K Q_G^T and dP^T_G = V dO_G^T into buffer G & 1 (lanes = keys,
+        // S^T_G = K Q_G^T and dP^T_G = V dO_G^T into buffer G % BUFS (lanes = keys,
         // 64 query columns each), reading ring slot G % STAGES; first, from
         // G = 2 on, the readout group must have taken that buffer's dQ^T of two
         // steps back out. `rows`: the step's queries that the sequence has (PACK).
@@ -577,8 +582,8 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                 st_shared_v4(sbase + tile + at, 0u, 0u, 0u, 0u);
         };
         auto issue_sdp = [&](int G, int rows) -> bool {
-            if (G >= 2) {
-                if (!wait_all(bar(L::BAR_DQREAD + (G & 1)), ((G - 2) >> 1) & 1, kStatusWaitO)) return false;
+            if (G >= L::BUFS) {
+                if (!wait_all(bar(L::BAR_DQREAD + G % L::BUFS), (G / L::BUFS - 1) & 1, kStatusWaitO)) return false;
             }
             const int st = G % L::STAGES;
             if (!wait_all(bar(L::BAR_QFULL + st), (G / L::STAGES) & 1, kStatusWaitQ)) return false;
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                     __syncwarp();
                 }
             }
-            const uint32_t col = L::BUF_COL(G & 1);
+            const uint32_t col = L::BUF_COL(G % L::BUFS);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t in_a = (kk & 3) * 32 + (kk >> 2) * L::KV_CHUNK;
@@ -605,19 +610,19 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                     umma_ss(tmem + col + L::DP_IN, av, bdo, IDESC_S, kk > 0 ? 1u : 0u);
                 }
             }
-            if (leader) umma_commit(bar(L::BAR_SFULL + (G & 1)));
+            if (leader) umma_commit(bar(L::BAR_SFULL + G % L::BUFS));
             return true;
         };
         // dV += P^T_G dO_G, dK += dS^T_G Q_G (A from TMEM: 16 queries = 8 packed
         // columns, each 32-query chunk packed into the first 16 of its own 32;
         // B MN-major, 16 query rows = 2048 bytes), then dQ^T_G = K^T dS^T_G
-        // over buffer G & 1's S^T columns (after the dV MMAs that read P^T
+        // over the buffer's S^T columns (after the dV MMAs that read P^T
         // there, in issue order): A = K MN-major (M = head dim), B = dS^T
         // MN-major (N = queries), 16 keys = 2048 bytes per MMA. `first`: the
         // tile's first step, which starts dV and dK.
         auto issue_vkq = [&](int G, bool first) -> bool {
-            const int b = G & 1;
-            if (!wait_all(bar(L::BAR_PREADY + b), (G >> 1) & 1, kStatusWaitP)) return false;
+            const int b = G % L::BUFS;
+            if (!wait_all(bar(L::BAR_PREADY + b), (G / L::BUFS) & 1, kStatusWaitP)) return false;
             tc_fence_after();
             const int st = G % L::STAGES;
             // B of dV and dK: this CTA's head-dim part of dO_G and Q_G.
@@ -647,20 +652,44 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             return true;
         };
         bool ok = true;
-        int gb = 0;        // global index of the tile's first step
-        int kv_loads = 0;
-        for (int tt = 0; tt < nt && ok; ++tt) {
-            const int n = NS(tt);
-            if (n == 0) continue;
-            if (!WIN || tt == 0) {
-                ok = wait_all(bar(L::BAR_KV), kv_loads & 1, kStatusWaitKvFull);
-                ++kv_loads;
+        // The MMAs of n steps, in an order that leaves the compute and readout groups
+        // another step's work while one step's MMAs run.
+        auto run = [&](int n, auto&& sdp, auto&& vkq) {
+            if constexpr (L::BUFS == 3) {
+                // S^T and dP^T two steps ahead, into the buffer whose dQ^T was read out
+                // while the last step's MMAs ran: the issuer never waits for a readout.
+                ok = sdp(0);
+                if (ok && n > 1) ok = sdp(1);
+                for (int a = 0; a < n && ok; ++a) {
+                    ok = vkq(a);
+                    if (ok && a + 2 < n) ok = sdp(a + 2);
+                }
+            } else if constexpr (L::STAGES >= 3) {
+                ok = sdp(0);
+                if (ok && n > 1) ok = sdp(1);
+                for (int a = 0; a < n && ok; a += 2) {
+                    ok = vkq(a);
+                    if (ok && a + 1 < n) ok = vkq(a + 1);
+                    // The next pair's S^T and dP^T.
+                    for (int h = a + 2; h < a + 4 && h < n && ok; ++h) ok = sdp(h);
+                }
+            } else {
+                // One stage: step G + 1's Q and dO load once step G's dV and dK
+                // MMAs have read the stage, so its S^T and dP^T follow step G's
+                // MMAs.
+                ok = sdp(0);
+                for (int h = 0; h < n && ok; ++h) {
+                    ok = vkq(h);
+                    if (ok && h + 1 < n) ok = sdp(h + 1);
+                }
             }
-            if (!ok) break;
-            tc_fence_after();
+        };
+        if constexpr (PACK || L::BUFS == 3) {
+            ok = wait_all(bar(L::BAR_KV), 0, kStatusWaitKvFull);
+            if (ok) tc_fence_after();
             if constexpr (PACK) {
                 const int keys = Nk - KT(0) * kBwdKeys;
-                if (tt == 0 && keys < kBwdKeys) {
+                if (ok && keys < kBwdKeys) {
                     for (int c = 0; c < L::CHUNKS; ++c) {
                         clear_rows(L::K_OFF + c * L::KV_CHUNK, keys, kBwdKeys);
                         clear_rows(L::V_OFF + c * L::KV_CHUNK, keys, kBwdKeys);
@@ -669,39 +698,41 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                     __syncwarp();
                 }
             }
-            // Queries of the pass's step h that the sequence has.
-            auto left = [&](int h) { return PACK ? Nq - (H0(tt) + h) * kBwdHalf : kBwdHalf; };
-            // The tile's first MMA into dV and dK waits until the compute group
-            // has read the previous tile's out of TMEM.
-            auto first_vkq = [&](int G) -> bool {
-                if (tt > 0 && handoff) {
-                    if (!wait_all(bar(L::BAR_ACCFREE), 0, kStatusWaitO)) return false;
-                    tc_fence_after();
-                }
-                return issue_vkq(G, !WIN || tt == 0);
+            // The passes' steps follow one another without a break. `pos`: the next
+            // step's place among the head's.
+            int pos = s0 % ns[0];
+            auto sdp = [&](int G) {
+                const int rows = PACK ? Nq - (h0s[0] + pos) * kBwdHalf : kBwdHalf;
+                if (++pos == ns[0]) pos = 0;
+                return issue_sdp(G, rows);
             };
-            if constexpr (L::STAGES >= 3) {
-                if (ok) ok = issue_sdp(gb, left(0));
-                if (ok && n > 1) ok = issue_sdp(gb + 1, left(1));
-                for (int a = 0; a < n && ok; a += 2) {
-                    ok = a == 0 ? first_vkq(gb) : issue_vkq(gb + a, false);
-                    if (ok && a + 1 < n) ok = issue_vkq(gb + a + 1, false);
-                    // The next pair's S^T and dP^T.
-                    for (int h = a + 2; h < a + 4 && h < n && ok; ++h) ok = issue_sdp(gb + h, left(h));
+            if (ok) run(n_all, sdp, [&](int G) { return issue_vkq(G, G == 0); });
+        } else {
+            int gb = 0;        // global index of the tile's first step
+            int kv_loads = 0;
+            for (int tt = 0; tt < nt && ok; ++tt) {
+                const int n = NS(tt);
+                if (n == 0) continue;
+                if (!WIN || tt == 0) {
+                    ok = wait_all(bar(L::BAR_KV), kv_loads & 1, kStatusWaitKvFull);
+                    ++kv_loads;
                 }
-            } else {
-                // One stage: step G + 1's Q and dO load once step G's dV and dK
-                // MMAs have read the stage, so its S^T and dP^T follow step G's
-                // MMAs.
-                if (ok) ok = issue_sdp(gb, left(0));
-                for (int h = 0; h < n && ok; ++h) {
-                    ok = h == 0 ? first_vkq(gb) : issue_vkq(gb + h, false);
-                    if (ok && h + 1 < n) ok = issue_sdp(gb + h + 1, left(h + 1));
-                }
+                if (!ok) break;
+                tc_fence_after();
+                // The tile's first MMA into dV and dK waits until the compute group
+                // has read the previous tile's out of TMEM.
+                auto vkq = [&](int h) -> bool {
+                    if (h == 0 && tt > 0 && handoff) {
+                        if (!wait_all(bar(L::BAR_ACCFREE), 0, kStatusWaitO)) return false;
+                        tc_fence_after();
+                    }
+                    return issue_vkq(gb + h, h == 0 && (!WIN || tt == 0));
+                };
+                run(n, [&](int h) { return issue_sdp(gb + h, kBwdHalf); }, vkq);
+                // K and V free for the next tile once every MMA so far is done.
+                if (ok && tt == 0 && handoff && leader) umma_commit(bar(L::BAR_KVFREE));
+                gb += n;
             }
-            // K and V free for the next tile once every MMA so far is done.
-            if (ok && tt == 0 && handoff && leader) umma_commit(bar(L::BAR_KVFREE));
-            gb += n;
         }
         if (leader) umma_commit(bar(L::BAR_DRAIN));
         bwd_wait(bar(L::BAR_DRAIN), 0, p, abort_flag, kStatusWaitDrain, false);
@@ -724,7 +755,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             const bool key_tail = k0 + kBwdKeys > Nk;
             for (int h = 0; h < n && ok; ++h) {
                 const int G = gb + h;
-                const int b = G & 1;
+                const int b = G % L::BUFS;
                 const int q0 = (h0 + h) * kBwdHalf;
                 // Every entry of the step is visible unless the tile holds missing
                 // keys or (causal) crosses the diagonal; padded query rows carry
@@ -732,7 +763,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
                 bool masked = key_tail || (p.causal && k0 + kBwdKeys - 1 > q0 + off);
                 if constexpr (WIN)  // the step's last row has left the window of the tile's first key
                     masked = masked || (p.window > 0 && k0 <= q0 + kBwdHalf - 1 + off - p.window);
-                ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_SFULL + b), (G >> 1) & 1, p, abort_flag, kStatusWaitS));
+                ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_SFULL + b), (G / L::BUFS) & 1, p, abort_flag, kStatusWaitS));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t col = L::BUF_COL(b) + 32 * g;
@@ -787,7 +818,7 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             const bool last_pass = !WIN || tt == nt - 1;
             if (ok && n > 0 && last_pass) {
                 const int G = gb + n - 1;
-                ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_DQFULL + (G & 1)), (G >> 1) & 1, p, abort_flag,
+                ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_DQFULL + G % L::BUFS), (G / L::BUFS) & 1, p, abort_flag,
                                                       kStatusWaitO));
                 if (ok) tc_fence_after();
             }
@@ -868,8 +899,8 @@ __global__ void __launch_bounds__(LayoutBwd<D>::THREADS, 1) fa_bwd_kernel(const 
             const size_t row0 = ROW0(tt);
             for (int h = 0; h < n && ok; ++h) {
                 const int G = gb + h;
-                const int b = G & 1;
-                ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_DQFULL + b), (G >> 1) & 1, p, abort_flag, kStatusWaitO));
+                const int b = G % L::BUFS;
+                ok = __all_sync(0xffffffffu, bwd_wait(bar(L::BAR_DQFULL + b), (G / L::BUFS) & 1, p, abort_flag, kStatusWaitO));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t lo[32], hi[32];
@@ -1434,7 +1465,7 @@ cudaError_t launch_bwd_pre(const void* o, const void* dout, const float* lse, fl
 
 template <int D, bool WIN, bool PACK = false>
 cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
-    using L = LayoutBwd<D>;
+    using L = LayoutBwd<D, WIN>;
     // Kernel attributes belong to the context: set once per device and context.
     static ContextCache<int> attr_set;
     int done = 0;
