@@ -320,7 +320,8 @@ __device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h,
         n = sink ? first : tiles - first;
     };
     int b = 0, level = 0;
-    const bool live = packed_pick(p.seqs.B, r, lane, runs, b, level);
+    PackedCursor first = {0, 0};
+    const bool live = packed_pick(p.seqs.B, r, lane, runs, b, level, first);
     if (lane == 0) {
         *u = {};
         u->live = live;
@@ -1138,22 +1139,32 @@ __global__ void __launch_bounds__(256) fa_bwd_win_post_kernel(const __grid_const
 // belongs to, found by one warp: its number, or -1. Sixty-four padded rows or a tile
 // have one sequence at most.
 __device__ __forceinline__ int bwd_pack_find(const BwdParams& p, long long row, bool tiles, int lane, PackedSeq& s) {
-    for (int c = 0; c < p.seqs.B; c += 32) {
-        const int b = c + lane;
-        PackedSeq y = {0, 0, 0, 0};
-        bool here = b < p.seqs.B && packed_seq(p.seqs, b, y);
-        if (here) {
-            const long long at = row - (tiles ? tile_slot(y.k0, b) : pad_row(y.q0, b));
-            here = at >= 0 && at < (tiles ? key_tiles(y) : y.n);
+    // (128 sequences at a time: their loads are in flight together.)
+    for (int c = 0; c < p.seqs.B; c += 128) {
+        PackedSeq y[4];
+        bool here[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int b = c + 32 * u + lane;
+            y[u] = {0, 0, 0, 0};
+            here[u] = b < p.seqs.B && packed_seq(p.seqs, b, y[u]);
         }
-        const unsigned who = __ballot_sync(0xffffffffu, here);
-        if (who) {
-            const int from = __ffs(who) - 1;
-            s.q0 = __shfl_sync(0xffffffffu, y.q0, from);
-            s.n = __shfl_sync(0xffffffffu, y.n, from);
-            s.k0 = __shfl_sync(0xffffffffu, y.k0, from);
-            s.m = __shfl_sync(0xffffffffu, y.m, from);
-            return c + from;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int b = c + 32 * u + lane;
+            if (here[u]) {
+                const long long at = row - (tiles ? tile_slot(y[u].k0, b) : pad_row(y[u].q0, b));
+                here[u] = at >= 0 && at < (tiles ? key_tiles(y[u]) : y[u].n);
+            }
+            const unsigned who = __ballot_sync(0xffffffffu, here[u]);
+            if (who) {
+                const int from = __ffs(who) - 1;
+                s.q0 = __shfl_sync(0xffffffffu, y[u].q0, from);
+                s.n = __shfl_sync(0xffffffffu, y[u].n, from);
+                s.k0 = __shfl_sync(0xffffffffu, y[u].k0, from);
+                s.m = __shfl_sync(0xffffffffu, y[u].m, from);
+                return c + 32 * u + from;
+            }
         }
     }
     return -1;
@@ -1415,7 +1426,8 @@ struct BwdPackParts {
     size_t part_floats;
 };
 BwdPackParts bwd_pack_parts(int B, int total_k, int max_q, int max_k, int H, int Hkv, int d, int window, int sinks) {
-    constexpr long long kUnitCost = 4, kPartCost = 6;
+    // (At d = 256 a step takes more than twice as long, a CTA's start and end do not.)
+    const double kUnitCost = d == 256 ? 2. : 4., kPartCost = d == 256 ? 2. : 6.;
     BwdPackParts c = {0, 1, 1, 0, 0, 0};
     const long long halves = d == 256 ? 2 : 1, G = H / Hkv, seqs = std::min(B, total_k);
     const long long k_tiles = (static_cast<long long>(max_k) + kBwdKeys - 1) / kBwdKeys;
@@ -1435,7 +1447,7 @@ BwdPackParts bwd_pack_parts(int B, int total_k, int max_q, int max_k, int H, int
     for (long long p = 1; p <= 16 && (p == 1 || p <= steps); ++p) {
         const long long piece = std::max(8ll, (steps + p - 1) / p);
         const long long sp = c.sink_tiles > 0 ? std::min(64ll, (sink_steps + piece - 1) / piece) : 1;
-        const double extra = kUnitCost + (p > 1 ? kPartCost : 0);
+        const double extra = kUnitCost + (p > 1 ? kPartCost : 0.);
         const double longest = static_cast<double>(
             std::max((steps + p - 1) / p, c.sink_tiles > 0 ? (sink_steps + sp - 1) / sp : 0)) + extra;
         const double even = (work + static_cast<double>(heads) * (others * p + sink_units * sp) * extra) / 152.;

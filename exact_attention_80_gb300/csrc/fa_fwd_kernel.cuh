@@ -34,6 +34,7 @@ cudaError_t launch_fwd(const FwdParams& p, unsigned grid, cudaStream_t stream) {
         std::conditional_t<F8, std::conditional_t<D == 256, LayoutTP<D, true>, LayoutTM<D, true>>, FwdLayout<D>>>;
     constexpr auto kernel = [] {
         if constexpr (PACK && D == 256) return fa_fwd_tppack_kernel<D>;
+        else if constexpr (PACK && PERSIST) return fa_fwd_tmpackp_kernel<D>;
         else if constexpr (PACK) return fa_fwd_tmpack_kernel<D>;
         else if constexpr (WIN && D == 256) return fa_fwd_tpw_kernel<D>;
         else if constexpr (WIN && PERSIST) return fa_fwd_tmwp_kernel<D>;

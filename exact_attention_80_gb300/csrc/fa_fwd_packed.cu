@@ -9,7 +9,10 @@
 
 namespace fa {
 
-cudaError_t launch_fwd_packed(const FwdParams& p, int d, unsigned grid, cudaStream_t stream) {
+cudaError_t launch_fwd_packed(const FwdParams& p, int d, bool persist, unsigned grid, cudaStream_t stream) {
+    if (persist)
+        return d == 64 ? launch_fwd<64, false, false, true, false, true, true>(p, grid, stream)
+                       : launch_fwd<128, false, false, true, false, true, true>(p, grid, stream);
     return d == 64    ? launch_fwd<64, false, false, false, false, true, true>(p, grid, stream)
            : d == 128 ? launch_fwd<128, false, false, false, false, true, true>(p, grid, stream)
                       : launch_fwd<256, false, false, false, false, true, true>(p, grid, stream);
@@ -89,5 +92,16 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
     p.o_scale = 1.f;
     p.wait_limit = fa::kDefaultWaitLimit;
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-    return fa::launch_fwd_packed(p, d, static_cast<unsigned>(ctas), stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    int sms = 0;
+    if (fa::sm_count(&sms) != cudaSuccess) return FA_ERR_CUDA;
+    // Persistent CTAs where the units fill three waves, at d = 128 with lists of up to 64
+    // key tiles: a unit's start and end overlap its neighbours', its steps take a little
+    // longer (16 + 4 heads; us, one unit per CTA and persistent: d = 64, four prompts of
+    // 8000 tokens 569 and 546; d = 128, 64 of 500, 16 kv heads 175 and 152, one of 16000
+    // with one of 9000 905 and 934; 1.8 waves of long lists, d = 64: 204 and 215).
+    const long long reach = window > 0 ? std::min<long long>(batch->max_seqlen_k, static_cast<long long>(window) + unit + sinks)
+                                       : batch->max_seqlen_k;
+    const bool persist = d <= 128 && ctas >= 3ll * sms && (d == 64 || reach <= 64 * 128);
+    const unsigned grid = static_cast<unsigned>(persist ? sms : ctas);
+    return fa::launch_fwd_packed(p, d, persist, grid, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -132,7 +132,10 @@ struct LayoutTM {
     // completion per unit in which the tile has keys)
     static constexpr int BAR_QEMPTY = BAR_OFULL + Q_TILES;
     static constexpr int BAR_DRAIN = BAR_QEMPTY + Q_TILES;
-    static constexpr int BAR_VCLEAN = BAR_DRAIN + 1;  // packed: the last V tile's other rows are zeros
+    // [slot] persistent CTAs on packed sequences: the ring of units (kPackRing)
+    static constexpr int BAR_UFULL = BAR_DRAIN + 1;
+    static constexpr int BAR_UEMPTY = BAR_UFULL + 4;
+    static constexpr int BAR_VCLEAN = BAR_UEMPTY + 4;  // packed: a unit's last V tile cleared
     static constexpr int NUM_BARS = BAR_VCLEAN + 1;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;  // [0] tmem base, [1] abort
     static constexpr uint32_t BYTES = MISC_OFF + 16;
@@ -680,6 +683,12 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         }
         mbar_init(bar(L::BAR_DRAIN), 1);
         if constexpr (PACK) mbar_init(bar(L::BAR_VCLEAN), 1);
+        if constexpr (PACK && PERSIST) {
+            for (int s = 0; s < kPackRing; ++s) {
+                mbar_init(bar(L::BAR_UFULL + s), 1);
+                mbar_init(bar(L::BAR_UEMPTY + s), kPackReaders);
+            }
+        }
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -688,12 +697,18 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         tma_prefetch_desc(&p.tm_k);
         tma_prefetch_desc(&p.tm_v);
     }
-    PackUnit* unit = nullptr;
+    PackRing* ring = nullptr;
     if constexpr (PACK) {
-        __shared__ PackUnit unit_store;
-        unit = &unit_store;
-        if (warp == 2) pack_unit<QT>(p, blockIdx.x, lane, unit);
-        if (warp == 3) pack_fill<D>(p, lane);
+        __shared__ PackRing ring_store;
+        ring = &ring_store;
+        if (warp == 2 && !PERSIST) {
+            PackedCursor at = {0, 0};
+            pack_unit<QT>(p, blockIdx.x, lane, &ring->unit[0], at);
+        }
+        if (warp == 3) {
+            if (blockIdx.x == 0) pack_check(p, lane);
+            pack_fill<D>(p, lane);
+        }
     }
     if (warp == 1) {
         tmem_alloc(sbase + L::MISC_OFF, L::TMEM_COLS);
@@ -711,7 +726,8 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
       // The work record is derived inside each role, after its register limit
       // is set, so that no role carries fields it does not use.
       if constexpr (WIN) {
-        tm_window_control<D, L, PERSIST, PACK>(p, sbase, tmem, abort_flag, warp, unit);
+        if (PACK && PERSIST && warp == 2) pack_feed<QT, L>(p, ring, sbase, lane, abort_flag);
+        else tm_window_control<D, L, PERSIST, PACK>(p, sbase, tmem, abort_flag, warp, ring);
       } else if constexpr (PERSIST) {
         tm_persist_control<D, F8>(p, sbase, tmem, abort_flag, warp);
       } else if constexpr (DUAL) {
@@ -965,18 +981,20 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         // Persistent CTAs walk their units (persist_unit); the phases of S_t
         // and O_t carry over: s_phase counts the tile's earlier key steps,
         // o_phase its earlier units with keys. A one-unit CTA runs the body once.
-        const int rounds = PERSIST ? static_cast<int>((p.total_units + gridDim.x - 1) / gridDim.x) : 1;
+        const int rounds = PACK && PERSIST ? 0x7fffffff : PERSIST ? static_cast<int>((p.total_units + gridDim.x - 1) / gridDim.x) : 1;
         int s_phase = 0, o_phase = 0;
         bool ok = true;
         for (int k = 0; k < rounds && ok; ++k) {
         long long lin = blockIdx.x;
-        if constexpr (PERSIST) {
+        if constexpr (PERSIST && !PACK) {
             lin = persist_unit(p, k);
             if (lin < 0) continue;
         }
         std::conditional_t<DUAL, WorkDual, std::conditional_t<WIN, WorkWin<QT>, Work<QT>>> w;
         if constexpr (DUAL) compute_work_dual<BN>(p, lin, w);
-        else if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
+        else if constexpr (PACK && PERSIST) {
+            if (!pack_next<QT, BN, L>(p, ring, sbase, k, abort_flag, w, ok)) break;
+        } else if constexpr (PACK) pack_first<QT, BN>(p, ring, w);
         else if constexpr (WIN) compute_work_win<QT, BN, !PERSIST>(p, lin, w);
         else compute_work<QT, BN>(p, lin, w);
         const int q_row = PACK ? pack_tile_token<QT>(p, w.q0, t) + r / p.group :
@@ -1200,7 +1218,9 @@ __device__ __forceinline__ void tm_forward(const FwdParams& p) {
         if (!DUAL && !PERSIST && t >= p.tiles_per_cta) ok = false;
         if constexpr (PACK) {
             if (ok)
-                pack_store<D>(p, w, q_row, r, n, m, m_true, l, l + lc, tO, sbase + L::Q_OFF + t * L::Q_TILE_BYTES);
+                pack_store<D, QT, PERSIST>(p, w, q_row, r, n, m, m_true, l, l + lc, tO,
+                                           PERSIST ? sbase + L::OST_OFF + t * L::OST_TILE_BYTES + quarter * L::OST_WARP_BYTES
+                                                   : sbase + L::Q_OFF + t * L::Q_TILE_BYTES);
         } else if constexpr (PERSIST && !F8) {
             // Plain mode, dense: bf16 O staged per warp in its own buffer.
             if (ok && n > 0)
@@ -1267,7 +1287,13 @@ __global__ void __launch_bounds__(LayoutTM<D>::THREADS, 1)
     tm_forward<D, false, false, false, false, true, true>(p);
 }
 
-// The same, persistent CTAs.
+template <int D>
+__global__ void __launch_bounds__(LayoutTM<D, false, true>::THREADS, 1)
+    fa_fwd_tmpackp_kernel(const __grid_constant__ FwdParams p) {
+    tm_forward<D, false, false, true, false, true, true>(p);
+}
+
+// Window, persistent CTAs.
 template <int D>
 __global__ void __launch_bounds__(LayoutTM<D, false, true>::THREADS, 1)
     fa_fwd_tmwp_kernel(const __grid_constant__ FwdParams p) {

@@ -107,7 +107,7 @@ struct LayoutTP {
     static constexpr int BAR_ALPHA = BAR_OSTAGED + Q_TILES;
     static constexpr int BAR_OREADY = BAR_ALPHA + 2 * Q_TILES;
     static constexpr int BAR_DRAIN = BAR_OREADY + 2 * Q_TILES;
-    static constexpr int BAR_VCLEAN = BAR_DRAIN + 1;  // packed: the last V tile's other rows are zeros
+    static constexpr int BAR_VCLEAN = BAR_DRAIN + 1;  // packed: the last V tile cleared
     static constexpr int NUM_BARS = BAR_VCLEAN + 1;
     static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;  // [0] tmem base, [1] abort
     static constexpr uint32_t BYTES = MISC_OFF + 16;
@@ -172,8 +172,14 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     if constexpr (PACK) {
         __shared__ PackUnit unit_store;
         unit = &unit_store;
-        if (warp == 2) pack_unit<QT>(p, blockIdx.x, lane, unit);
-        if (warp == 3) pack_fill<D>(p, lane);
+        if (warp == 2) {
+            PackedCursor at = {0, 0};
+            pack_unit<QT>(p, blockIdx.x, lane, unit, at);
+        }
+        if (warp == 3) {
+            if (blockIdx.x == 0) pack_check(p, lane);
+            pack_fill<D>(p, lane);
+        }
     } else if constexpr (WIN) {
         compute_work_win<QT, BN, true>(p, blockIdx.x, w);
     } else {
@@ -181,7 +187,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
     }
 
     if (threadIdx.x == 0) {
-        mbar_init(bar(L::BAR_VCLEAN), 1);
+        if constexpr (PACK) mbar_init(bar(L::BAR_VCLEAN), 1);
         mbar_init(bar(L::BAR_QFULL), 1);
         for (int s = 0; s < ST; ++s) {
             mbar_init(bar(L::BAR_KVFULL + s), 1);
@@ -296,7 +302,9 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
                 pos.advance();
             }
             if constexpr (PACK) {
-                if (ok) ok = pack_clean_v<L>(p, w, sbase, total - 1, bar(L::BAR_VCLEAN), abort_flag, lane);
+                const int there = pack_tail<BN>(w);
+                if (ok && there < BN)
+                    ok = pack_clean_v<L>(p, sbase, total - 1, there, bar(L::BAR_VCLEAN), abort_flag, lane);
             }
             if (ok) {
                 // Producer tail: wait until the issuer has released the last use
@@ -397,11 +405,12 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
                 }
                 // O_t += P_t(j) V_j as each tile's P arrives.
                 ok = wait_all(bar(L::BAR_KVFULL + pos.slot), pos.phase, kStatusWaitKvFull);
-                if constexpr (PACK) {
-                    if (ok && j + 1 == w.nmax && pack_tail<BN>(w) < BN)
-                        ok = wait_all(bar(L::BAR_VCLEAN), 0, kStatusWaitKvFull);
-                }
                 if (!ok) break;
+                if constexpr (PACK) {
+                    if (j + 1 == w.nmax && pack_tail<BN>(w) < BN)
+                        ok = wait_all(bar(L::BAR_VCLEAN), 0, kStatusWaitKvFull);
+                    if (!ok) break;
+                }
 #pragma unroll
                 for (int t = 0; t < QT; ++t) {
                     if (ok && j < w.n[t]) {
@@ -664,7 +673,7 @@ __device__ __forceinline__ void tp_forward(const FwdParams& p) {
         const float l_o = F8 ? l : l + lc;
         if constexpr (PACK) {
             if (ok)
-                pack_store<D>(p, w, q_row, r, n, m_out, m_true, l, l_o, tO, sbase + L::Q_OFF + t * L::Q_TILE_BYTES);
+                pack_store<D, QT, false>(p, w, q_row, r, n, m_out, m_true, l, l_o, tO, sbase + L::Q_OFF + t * L::Q_TILE_BYTES);
         } else if (ok && !p.split_mode && !p.varlen && n > 0) {
             // Plain mode: bf16 O_t staged in Q_t's shared memory (8-bit inputs: in
             // the K/V slots), written with TMA.

@@ -167,19 +167,23 @@ __device__ __forceinline__ long long win_unit(const FwdParams& p, int k) {
     return lin < p.total_units ? lin : -1;
 }
 
-// Packed sequences (fa_fwd_pack.cuh): a unit's place in the batch, its work, the token
-// of a query tile's first row, the keys that exist in its last key tile, and the
-// clearing of the others' values.
+// Packed sequences (fa_fwd_pack.cuh): a unit's place in the batch, a CTA's only one and a
+// persistent CTA's next one as work, the token of a query tile's first row, the keys that exist in
+// its last key tile, and the clearing of the others' values.
 struct PackUnit;
+struct PackRing;
 template <int QT, int BN>
-__device__ __forceinline__ void pack_work(const FwdParams& p, const PackUnit& u, WorkWin<QT>& w);
+__device__ __forceinline__ void pack_first(const FwdParams& p, const PackRing* ring, WorkWin<QT>& w);
+template <int QT, int BN, typename L>
+__device__ __forceinline__ bool pack_next(const FwdParams& p, PackRing* ring, uint32_t sbase, int k,
+                                          volatile uint32_t* abort_flag, WorkWin<QT>& w, bool& ok);
 template <int QT>
 __device__ __forceinline__ int pack_tile_token(const FwdParams& p, int first, int t);
 template <int BN, int QT>
 __device__ __forceinline__ int pack_tail(const WorkWin<QT>& w);
-template <typename L, int QT>
-__device__ __forceinline__ bool pack_clean_v(const FwdParams& p, const WorkWin<QT>& w, uint32_t sbase, int entry,
-                                             uint32_t clean, volatile uint32_t* abort_flag, int lane);
+template <typename L>
+__device__ __forceinline__ bool pack_clean_v(const FwdParams& p, uint32_t sbase, int entry, int rows, uint32_t clean,
+                                             volatile uint32_t* abort_flag, int lane);
 
 // Control warps of a two-tile CTA with a window: the producer and the issuer of
 // the dense kernel with the tile list and the holes. A tile that skips step
@@ -190,16 +194,15 @@ __device__ __forceinline__ bool pack_clean_v(const FwdParams& p, const WorkWin<Q
 // issued right behind the current unit's last PV; O_t is first overwritten by
 // the unit's PV_t(0), which waits for a P that the softmax threads hand over
 // only after their epilogue.
-// PACK: one unit per CTA, `unit` its place in the batch of packed sequences.
+// PACK: packed sequences, whose units come through `ring`.
 template <int D, typename L, bool PERSIST, bool PACK>
 __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t sbase, uint32_t tmem,
-                                                  volatile uint32_t* abort_flag, int warp, const PackUnit* unit) {
-    static_assert(!(PERSIST && PACK), "packed sequences take one unit per CTA");
+                                                  volatile uint32_t* abort_flag, int warp, PackRing* ring) {
     constexpr int QT = L::Q_TILES;
     constexpr int BN = L::BN;
     constexpr int ST = L::STAGES;
     auto bar = [&](int i) -> uint32_t { return sbase + L::BAR_OFF + 8u * i; };
-    const int rounds = win_rounds<PERSIST>(p);
+    const int rounds = PACK && PERSIST ? 0x7fffffff : win_rounds<PERSIST>(p);
     const bool leader = elect_one();
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -207,6 +210,25 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
         int issued = 0;        // K/V entries issued, all units
         int q_loads[QT] = {};  // Q_t loads issued
         bool ok = true;
+        // PACK: the last V tile of a unit whose sequence ends in it is cleared behind
+        // that end once the next unit's first loads are on their way. The issuer waits for
+        // one clearing at a time, so the next one is handed over when the tile before it
+        // has been used: its slot was released (which the slot's next load has waited for).
+        int dirty = -1, dirty_rows = 0, cleared = -1;
+        auto clean = [&] {
+            if constexpr (PACK) {
+                if (ok && dirty >= 0) {
+                    if (PERSIST && cleared >= 0 && issued <= cleared + ST)
+                        ok = __all_sync(0xffffffffu, wait_phase(bar(L::BAR_KVEMPTY + cleared % ST), (cleared / ST) & 1, p,
+                                                                abort_flag, kStatusWaitKvEmpty));
+                    if (ok)
+                        ok = pack_clean_v<L>(p, sbase, dirty, dirty_rows, bar(L::BAR_VCLEAN), abort_flag,
+                                             threadIdx.x & 31);
+                    cleared = dirty;
+                }
+                dirty = -1;
+            }
+        };
         auto load_q = [&](const WorkWin<QT>& w, int t) -> bool {
             if (w.steps[t] == 0) return true;
             if (PERSIST && q_loads[t] > 0 &&
@@ -226,12 +248,20 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
             return true;
         };
         for (int k = 0; k < rounds && ok; ++k) {
-            const long long lin = win_unit<PERSIST>(p, k);
-            if (lin < 0) continue;
             WorkWin<QT> w;
-            if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
-            else compute_work_win<QT, BN, !PERSIST>(p, lin, w);
-            if (w.nmax == 0) continue;
+            if constexpr (PACK && PERSIST) {
+                if (!pack_next<QT, BN, L>(p, ring, sbase, k, abort_flag, w, ok)) break;
+            } else if constexpr (PACK) {
+                pack_first<QT, BN>(p, ring, w);
+            } else {
+                const long long lin = win_unit<PERSIST>(p, k);
+                if (lin < 0) continue;
+                compute_work_win<QT, BN, !PERSIST>(p, lin, w);
+            }
+            if (w.nmax == 0) {
+                clean();  // (the next unit may be given out only when the issuer has come past this one)
+                continue;
+            }
             if (!PERSIST) ok = load_q(w, 0);
             // Entry e: K_0; then per step j: V_j, K_{j+1}.
             for (int e = 0; e < 2 * w.nmax && ok; ++e) {
@@ -253,13 +283,15 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
                 if (e == 0) {
                     if (PERSIST) ok = load_q(w, 0);
                     if (ok) ok = load_q(w, 1);
+                    clean();
                 }
             }
             if constexpr (PACK) {
-                if (ok)
-                    ok = pack_clean_v<L>(p, w, sbase, issued - 1, bar(L::BAR_VCLEAN), abort_flag, threadIdx.x & 31);
+                dirty_rows = pack_tail<BN>(w);
+                if (dirty_rows < BN) dirty = issued - 1;
             }
         }
+        clean();
         if (ok) {
             // No commit arrival may be in flight when the CTA exits: the last uses
             // of the K/V slots and of the Q tiles.
@@ -316,15 +348,21 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
                             IDESC_O, (accumulate || kk > 0) ? 1u : 0u);
         };
         RingPos<ST> pos;
+        int cleaned = 0;      // PACK: cleared V tiles waited for
         int p_seen[QT] = {};  // P_t phases waited for, all units
         int q_seen[QT] = {};  // Q_t phases waited for
         bool ok = true;
         for (int k = 0; k < rounds && ok; ++k) {
-            const long long lin = win_unit<PERSIST>(p, k);
-            if (lin < 0) continue;
             WorkWin<QT> w;
-            if constexpr (PACK) pack_work<QT, BN>(p, *unit, w);
-            else compute_work_win<QT, BN, !PERSIST>(p, lin, w);
+            if constexpr (PACK && PERSIST) {
+                if (!pack_next<QT, BN, L>(p, ring, sbase, k, abort_flag, w, ok)) break;
+            } else if constexpr (PACK) {
+                pack_first<QT, BN>(p, ring, w);
+            } else {
+                const long long lin = win_unit<PERSIST>(p, k);
+                if (lin < 0) continue;
+                compute_work_win<QT, BN, !PERSIST>(p, lin, w);
+            }
             if (w.nmax == 0) continue;
             auto active = [&](int t, int j) {
                 return j < w.n[t] && !(j >= w.list.ns && j < w.list.ns + w.hole[t]);
@@ -373,7 +411,8 @@ __device__ __forceinline__ void tm_window_control(const FwdParams& p, uint32_t s
                 const int sv = slot_v, sk = slot_k;
                 const bool k_next = (j + 1 < w.nmax);
                 if constexpr (PACK) {
-                    if (!k_next && pack_tail<BN>(w) < BN) ok = wait_all(bar(L::BAR_VCLEAN), 0, kStatusWaitKvFull);
+                    if (!k_next && pack_tail<BN>(w) < BN)
+                        ok = wait_all(bar(L::BAR_VCLEAN), cleaned++ & 1, kStatusWaitKvFull);
                 }
 #pragma unroll
                 for (int t = 0; t < QT && ok; ++t) {

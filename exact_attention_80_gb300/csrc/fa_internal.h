@@ -112,7 +112,7 @@ cudaError_t launch_fwd_win_d64_persist(const FwdParams& p, unsigned grid, cudaSt
 cudaError_t launch_fwd_win_d128_persist(const FwdParams& p, unsigned grid, cudaStream_t stream);
 cudaError_t launch_fwd_win_d256(const FwdParams& p, unsigned grid, cudaStream_t stream);
 // Packed sequences, grouped heads, window with sinks (bf16).
-cudaError_t launch_fwd_packed(const FwdParams& p, int d, unsigned grid, cudaStream_t stream);
+cudaError_t launch_fwd_packed(const FwdParams& p, int d, bool persist, unsigned grid, cudaStream_t stream);
 // e4m3 Q, K, V (tm_q/tm_k/tm_v are byte maps, box {128, rows, 1}, or {64,
 // rows, 1} with the 64-byte swizzle at d = 64); d = 64, 128, 256.
 cudaError_t launch_fwd_f8_d64(const FwdParams& p, unsigned grid, cudaStream_t stream);

@@ -32,51 +32,93 @@ __device__ __forceinline__ bool packed_seq(const PackedSeqs& p, int b, PackedSeq
 }
 
 // Sequence b has n units at levels a .. a + n - 1, one each (runs(b, a, n); n = 0:
-// none); a unit's time grows with its level. Picks the unit of rank r when they are
-// taken from the highest level down, so that the longest start first whatever the
-// sequences' lengths and order are; by bisection over the levels, a few dozen
-// instructions each, without a list in memory or a launch that makes one. Called by
-// a whole warp; false where there is no such unit.
+// none); a unit's time grows with its level. Finds the unit of rank r: for up to 128
+// sequences as they are taken from the highest level down, so that the longest start
+// first whatever the sequences' lengths and order are (by bisection over the levels, a few
+// dozen instructions each, without a list in memory or a launch that makes one); for more,
+// whose units are short beside the whole, in the order of the sequences, each from its
+// highest level down. Called by a whole warp; false where there is no such unit.
+//
+// `at`: where the search begins, the first 128-sequence block that r may lie in and the
+// units before it; callers whose ranks rise keep it from one call to the next.
+constexpr int kPackedSorted = 128;
+struct PackedCursor {
+    int block, before;
+};
 template <typename F>
-__device__ __forceinline__ bool packed_pick(int B, int r, int lane, F&& runs, int& b, int& level) {
-    int a0 = 0, n0 = 0;  // of the first 32 sequences; the others are read again in each round
-    if (lane < B) runs(lane, a0, n0);
-    auto each = [&](auto&& f) {
-        f(lane, a0, n0);
-        for (int c = 32; c < B; c += 32) {
-            int a = 0, n = 0;
-            if (c + lane < B) runs(c + lane, a, n);
-            f(c + lane, a, n);
+__device__ __forceinline__ bool packed_pick(int B, int r, int lane, F&& runs, int& b, int& level, PackedCursor& at) {
+    constexpr int CHUNKS = kPackedSorted / 32;
+    int a[CHUNKS], n[CHUNKS];  // of a block of sequences, the loads of all four in flight at once
+    auto load = [&](int first) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            a[c] = n[c] = 0;
+            if (first + 32 * c < B && first + 32 * c + lane < B) runs(first + 32 * c + lane, a[c], n[c]);
         }
     };
+    if (B > kPackedSorted) {
+        for (; at.block < B; at.block += kPackedSorted) {
+            load(at.block);
+            int k = 0;
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) k += n[c];
+            k = __reduce_add_sync(0xffffffffu, k);
+            if (r < at.before + k) break;
+            at.before += k;
+        }
+        if (at.block >= B) return false;
+        int left = r - at.before;
+        b = -1;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            int upto = n[c];  // units of this and the lower lanes
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const unsigned here = __ballot_sync(0xffffffffu, left < upto);
+            if (b < 0 && here) {
+                const int who = __ffs(here) - 1;
+                b = at.block + 32 * c + who;
+                level = __shfl_sync(0xffffffffu, a[c] + upto - 1 - left, who);
+            }
+            left -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+        return b >= 0;
+    }
+    load(0);
     int lo = 0x7fffffff, hi = -0x7fffffff, all = 0;
-    each([&](int, int a, int n) {
-        if (n > 0) lo = min(lo, a), hi = max(hi, a + n - 1), all += n;
-    });
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+        if (n[c] > 0) lo = min(lo, a[c]), hi = max(hi, a[c] + n[c] - 1), all += n[c];
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     all = __reduce_add_sync(0xffffffffu, all);
     if (r >= all) return false;
-    auto from = [&](int at) {  // units at this level or above
+    auto from = [&](int l) {  // units at this level or above
         int k = 0;
-        each([&](int, int a, int n) { k += min(max(a + n - at, 0), n); });
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+            if (32 * c < B) k += min(max(a[c] + n[c] - l, 0), n[c]);
         return __reduce_add_sync(0xffffffffu, k);
     };
+#pragma unroll 1
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
         if (from(mid) > r) lo = mid;
         else hi = mid - 1;
     }
     level = lo;
-    int at = r - from(lo + 1);
+    int left = r - from(lo + 1);
     b = -1;
-    each([&](int i, int a, int n) {
-        const bool here = n > 0 && a <= lo && lo < a + n;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        const bool here = n[c] > 0 && a[c] <= lo && lo < a[c] + n[c];
         const unsigned who = __ballot_sync(0xffffffffu, here);
-        const unsigned mine = __ballot_sync(0xffffffffu, here && __popc(who & low_bits(lane)) == at);
-        if (b < 0 && mine) b = (i - lane) + __ffs(mine) - 1;
-        at -= __popc(who);
-    });
+        const unsigned mine = __ballot_sync(0xffffffffu, here && __popc(who & low_bits(lane)) == left);
+        if (b < 0 && mine) b = 32 * c + __ffs(mine) - 1;
+        left -= __popc(who);
+    }
     return b >= 0;
 }
 

@@ -196,6 +196,90 @@ def test_order_of_the_sequences(d):
     assert torch.equal(g2[1], g[1][idx]) and torch.equal(g2[2], g[2][idx])
 
 
+MANY = [
+    # H, Hkv, queries, keys (None: the same), window, sinks: so many units that CTAs take several
+    (32, 32, [130, 1, 0, 64, 200, 7, 0, 100, 129, 255, 256, 1, 300, 90, 33], None, 0, 0),
+    (64, 32, [130, 1, 0, 64, 50, 7, 0, 100, 129, 70, 128, 1, 9, 90, 33], [130, 5, 7, 300, 0, 200, 0, 100, 10, 70, 128, 1, 9, 90, 33], 0, 0),
+    (32, 16, [1 + 41 * b % 120 for b in range(34)], None, 30, 3),                       # more than 32 sequences
+    (8, 4, [1 + 41 * b % 60 for b in range(150)], [1 + 31 * b % 200 for b in range(150)], 0, 0),  # than 128
+    (8, 4, [b % 3 * (b % 40) for b in range(300)], [b % 50 for b in range(300)], 20, 1),          # than 256, a third with no query
+    (16, 16, [700, 1500, 40, 900, 2000, 3, 1800], None, 400, 130),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_packed_batches_of_many_units(case, d):
+    """Each sequence's outputs are those of a call with it alone, bit for bit; the first ones' are the oracle's."""
+    H, Hkv, ns, ms, window, sinks = MANY[case]
+    ms = ms or ns
+    cu_q, cu_k = cu_of(ns), cu_of(ms)
+    q, k, v, do = (x.cuda() for x in make(int(cu_q[-1]), max(1, int(cu_k[-1])), H, Hkv, d, 100 * case + d))
+    batch = (dev(cu_q), dev(cu_k), *bounds(ns, ms), window, sinks)
+    o, lse = fa.attention_packed(q, k, v, *batch)
+    grads = fa.attention_packed_backward(q, k, v, o, lse, do, *batch)
+    ok()
+    some = [b for b in range(len(ns)) if ns[b]]
+    for b in some if len(some) < 20 else some[:6] + some[-6:]:
+        rows, keys = slice(cu_q[b], cu_q[b + 1]), slice(cu_k[b], cu_k[b + 1])
+        kk, vv = (x[keys] if ms[b] else x[:1] for x in (k, v))
+        one = (dev([0, ns[b]]), dev([0, ms[b]]), ns[b], max(1, ms[b]), window, sinks)
+        o1, l1 = fa.attention_packed(q[rows], kk, vv, *one)
+        g1 = fa.attention_packed_backward(q[rows], kk, vv, o1, l1, do[rows], *one)
+        ok()
+        assert torch.equal(o[rows], o1) and torch.equal(lse[:, rows], l1), b
+        # (dQ is a sum in any order, and here dK and dV of a sequence alone may be sums of parts: a rounding apart.)
+        for x, y in zip((grads[0][rows], grads[1][keys], grads[2][keys]), g1):
+            if x.numel():
+                assert (x.float() - y.float()).abs().max() <= 2.0 ** -7 * y.float().abs().max() + 1e-30, b
+    n = min(3, len(ns))
+    rows, keys = slice(0, cu_q[n]), slice(0, cu_k[n])
+    out, lim, lse_ref = reference(q[rows].cpu(), k[keys].cpu(), v[keys].cpu(), do[rows].cpu(), cu_q[: n + 1], cu_k[: n + 1],
+                                  window, sinks)
+    check(o[rows], out["o"], lim["o"], "o")
+    check_lse(lse[:, rows], lse_ref)
+    for name, x, s in zip(("dq", "dk", "dv"), grads, (rows, keys, keys)):
+        check(x[s], out[name], lim[name], name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_broken_and_foreign_things_in_batches_of_many_units(d):
+    """NaN in other sequences and around them, rows of no sequence, and a broken sequence, where CTAs take several units."""
+    H, Hkv = 16, 4
+    ns = [1 + 41 * b % 90 for b in range(140)]
+    cu = cu_of(ns, 6)
+    T = int(cu[-1]) + 70
+    q, k, v, _ = (x.cuda() for x in make(T, T, H, Hkv, d, 2))
+    o, lse = fa.attention_packed(q, k, v, dev(cu), dev(cu), max(ns), max(ns), 50, 2)
+    ok()
+    out = torch.ones(T, dtype=torch.bool)
+    out[cu[0]: cu[-1]] = False
+    assert torch.all(o[out] == 0) and torch.all(lse[:, out] == -float("inf"))
+    odd = torch.zeros(T, dtype=torch.bool)
+    for b in range(1, 140, 2):
+        odd[cu[b]: cu[b + 1]] = True
+    x = [t.clone() for t in (q, k, v)]
+    for t in x:
+        t[odd | out] = float("nan")
+    mine = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    fa.fa_fwd_packed(*x, *mine, dev(cu), dev(cu), max(ns), max(ns), 50, 2)
+    ok()
+    good = ~(odd | out)
+    assert torch.equal(mine[0][good], o[good]) and torch.equal(mine[1][:, good], lse[:, good])
+    assert torch.all(mine[0][out] == 7.0) and torch.all(mine[1][:, out] == 7.0)
+    bad = cu.copy()
+    bad[71] = 2 ** 31 - 1  # sequences 70 and 71
+    mine = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    fa.fa_fwd_packed(q, k, v, *mine, dev(bad), dev(cu), max(ns), max(ns), 50, 2)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_ERR_SEQLENS
+    for b in (0, 1, 69, 72, 139):
+        s = slice(cu[b], cu[b + 1])
+        assert torch.equal(mine[0][s], o[s]) and torch.equal(mine[1][:, s], lse[:, s])
+    s = slice(cu[70], cu[72])
+    assert torch.all(mine[0][s] == 7.0) and torch.all(mine[1][:, s] == 7.0)
+
+
 def test_strided_tokens():
     """A fused projection's columns, and gradients written into one: the same bits as separate tensors."""
     H, Hkv, d, ns = 8, 2, 128, [300, 1, 77]

@@ -111,6 +111,14 @@ PREFIX = [
     ([1, 0, 1, 0], [9, 5, 3, 0], 64, 16, 4, 2, 128, None),        # sequences that bring nothing
     ([0, 1, 2], [0, 77, 2], 48, 16, 3, 1, 128, (4, 2)),           # the first one brings nothing and holds nothing
     ([2] * 100, [2 + b % 50 for b in range(100)], 144, 16, 2, 1, 64, None),
+    # so many sequences that each warp has a share of one for itself
+    ([1] * 160, [1 + 37 * b % 150 for b in range(160)], 64, 16, 8, 4, 64, None),
+    ([1] * 160, [1 + b % 3 if b != 97 else 2500 for b in range(160)], 128, 64, 4, 4, 64, None),   # one far longer
+    ([1 + b % 2 for b in range(120)], [2 + 29 * b % 300 for b in range(120)], 48, 16, 8, 4, 128, None),
+    ([1] * 115, [1 + 29 * b % 300 for b in range(115)], 256, 128, 28, 4, 128, (1, 1)),
+    ([int(b % 5 > 0) for b in range(120)], [int(b % 5 > 0) + b % 7 for b in range(120)], 32, 16, 4, 4, 128, (3, 2)),  # some idle
+    ([1] * 77, [1 + 13 * b % 120 for b in range(77)], 96, 32, 8, 4, 256, None),
+    ([int(b > 70) for b in range(80)], [9 if b > 70 else 0 for b in range(80)], 16, 16, 4, 4, 256, (4, 1)),
 ]
 
 
@@ -188,6 +196,35 @@ def test_prefix_broken_batches():
                     assert torch.all(o[s] == 3.0) and torch.all(lse[:, s] == 2.0), change
             elif "cu" not in change:
                 assert (o[s].float() - want[0][s].float()).abs().max() <= 2.0 ** -6 * want[0].float().abs().max()
+
+
+def test_prefix_broken_batches_of_many():
+    """As above, where each warp has a share of a sequence for itself."""
+    prefix, page, H, Hkv, d, B = 64, 16, 4, 4, 128, 130
+    lens, ns = [prefix + 1 + 11 * b % 90 for b in range(B)], [1] * B
+    cache = Cache(lens, page, Hkv, d, 8, shared=prefix)
+    q, cu = normal((B, H, d), 1).cuda(), cu_of(ns)
+    g = cache.gpu()
+    most = cache.table.shape[1] * page
+    want = fa.attention_prefix_fp8(q, *g, dev(cache.table), dev(cu), dev(lens), 1, most, prefix)
+    ok()
+    own, shared = fa.fa_prefix_num_splits(B, H, Hkv, B, 1, most, prefix, d)
+    ws = torch.empty(fa.fa_paged_workspace_bytes(B, H, d, own + shared) // 4, device="cuda")
+    for length, at, code, broken in ((prefix, None, 12, [77]), (3, None, 12, [77]), (most + 1, None, 12, [77]),
+                                     (None, (77, 1, 0), 14, None), (None, (77, 4, 99999), 14, None), (None, (0, 0, -7), 14, None)):
+        table, n = cache.table.copy(), list(lens)
+        if at:
+            table[at[:2]] = at[2] if at[2] or table[at[:2]] else 1
+        else:
+            n[77] = length
+        o, lse = torch.full_like(q, 3.0), torch.full((H, B), 2.0, device="cuda")
+        fa.fa_fwd_prefix_fp8(q, *g, o, lse, dev(table), dev(cu), dev(n), 1, most, prefix, ws, own, shared)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(clear=True) == code, (length, at)
+        if broken:
+            assert torch.all(o[77] == 3.0) and torch.all(lse[:, 77] == 2.0)
+            keep = [b for b in range(B) if b != 77]
+            assert (o[keep].float() - want[0][keep].float()).abs().max() <= 2.0 ** -6 * want[0].float().abs().max()
 
 
 def test_prefix_rows_behind_the_last_sequence_are_left():
@@ -324,6 +361,66 @@ def test_read_broken_batches_touch_nothing():
                 assert torch.equal(x[0][s], k[s]) and torch.equal(x[1][s], v[s]), change
             elif b in broken and not (change.get("cu") and b != 2 and change["cu"][0] == 0):
                 assert torch.all(x[0][s] == 3.0) and torch.all(x[1][s] == 3.0), change
+
+
+def test_read_captured_replayed_and_on_a_side_stream():
+    ns, page, Hkv, d = [20, 50], 16, 2, 128
+    cache = Cache([40, 60], page, Hkv, d, 3)
+    g, table, cu = cache.gpu(), dev(cache.table), dev(cu_of(ns))
+    starts = dev([0, 0])
+    eager = []
+    for first in ([0, 10], [20, 3]):
+        starts.copy_(dev(first))
+        eager.append(fa.kv_read_fp8(*g, table, cu, starts, 70))
+    ok()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        k, v = fa.kv_read_fp8(*g, table, cu, starts, 70)
+    for i in (0, 1, 0):
+        starts.copy_(dev(([0, 10], [20, 3])[i]))
+        k.fill_(9.0)
+        graph.replay()
+        ok()
+        assert torch.equal(k, eager[i][0]) and torch.equal(v, eager[i][1])
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        x = [t.clone() for t in g]
+        side.wait_stream(torch.cuda.current_stream())
+        ks, vs = fa.kv_read_fp8(*x, table, cu, starts, 70, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(ks, eager[0][0]) and torch.equal(vs, eager[0][1])
+    ok()
+
+
+def test_two_graphs_of_prefix_calls_keep_their_workspaces():
+    """Two captured calls, replayed in turn and on two streams at once, each with its own partials."""
+    prefix, page, H, Hkv, d, B = 256, 32, 8, 2, 128, 12
+    calls = []
+    for i in range(2):
+        lens = [prefix + 1 + (30 + 7 * i) * b for b in range(B)]
+        cache = Cache(lens, page, Hkv, d, 5 + i, shared=prefix)
+        q = normal((B, H, d), 2 + i).cuda()
+        args = [q, *cache.gpu(), dev(cache.table), dev(cu_of([1] * B)), dev(lens), 1, max(lens), prefix, None, 4, 4]
+        calls.append((args, *fa.attention_prefix_fp8(*args[:11], num_splits=4, prefix_splits=4)))
+    ok()
+    graphs = []
+    for args, _, _ in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = fa.attention_prefix_fp8(*args[:11], num_splits=4, prefix_splits=4)
+        graphs.append((graph, out))
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for (graph, out), s in zip(graphs, sides):
+            out[0].fill_(9.0)
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                graph.replay()
+        for s in sides:
+            torch.cuda.current_stream().wait_stream(s)
+        for (_, out), (_, o, lse) in zip(graphs, calls):
+            assert torch.equal(out[0], o) and torch.equal(out[1], lse)
+    ok()
 
 
 # ---------------------------------------------------------------- used together
