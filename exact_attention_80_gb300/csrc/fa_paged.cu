@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         }
     }
     __syncwarp();
-    griddep_wait();
+    if (!paged_wait<PART>(p)) return;
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     // Unit: row blocks fastest (they share K and V in L2), then splits, heads.
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
         if (!whole) lin -= p.whole_ctas;
         if (solo) {
             lin = lin * kWarps + warp;
-            if (!paged_unit<KEYS>(p, static_cast<int>(lin / p.Hkv), kPlaces * rows_ctas(D) * kWarps / p.Hkv, lane, unit)) return;
+            if (!paged_unit<KEYS>(p, static_cast<int>(lin / p.Hkv), p.places / p.Hkv, lane, unit)) return;
             b = unit.b;
             split = unit.split;
         } else {
@@ -908,9 +908,8 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
     long long ctas = static_cast<long long>(p.B) * p.Hkv * p.num_splits * p.row_blocks;
     if constexpr (PART) {
         // Warps for the sequences' own parts, as paged_unit counts them.
-        const long long places = static_cast<long long>(kPlaces) * rows_ctas(D) * kWarps;
-        const long long units = std::min(ctas, std::max(places, static_cast<long long>(p.B) * p.Hkv));
-        ctas = p.whole_ctas + (p.whole ? 0 : p.solo ? (units + kWarps - 1) / kWarps : ctas);
+        const long long units = std::min(ctas, std::max(static_cast<long long>(p.places), static_cast<long long>(p.B) * p.Hkv));
+        ctas = p.whole_ctas + (p.whole ? 0 : p.solo ? (units + kWarps - 1) / kWarps : ctas) + p.early;
     }
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent_clusters(fa_paged_rows_kernel<D, CLUSTER, PART>, dim3(static_cast<unsigned>(ctas)),
@@ -921,6 +920,43 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
 // there is a unit for every CTA that runs at once.
 bool solo_units(const Plan& own, int B, int Hkv, int d) {
     return !own.tc && static_cast<long long>(B) * Hkv >= static_cast<long long>(kPlaces) * rows_ctas(d);
+}
+// The splits of a shared prefix that the tensor-core kernel takes beside the sequences'
+// own parts (its SMs hold nothing else): both cut so that the whole ends earliest, with
+// the prefix on a part of the SMs, in microseconds of CTAs fitted to 21 batches on a GB300,
+// B x prefix + own keys from 2 x 2900 + 50 to 64 x 65536 + 2000. (64 sequences, 16384 + up
+// to 2000 keys, 32 + 8 heads, d = 128: 73 us with the prefix on all SMs first, in 19 parts,
+// 61 with six; 16 of five tokens, 8160 + up to 4000: 67 with eight, 55 with three.)
+int prefix_splits_beside(const Plan& w, const Plan& own, int B, int H, int Hkv, int total_q, int max_own, int d,
+                         int* prefix_splits) {
+    const double start = d == 64 ? 6. : d == 128 ? 8. : 24., tile = 1.6;  // a prefix CTA, a key tile of it
+    const bool solo = solo_units(own, B, Hkv, d);
+    const int at_once = own.tc ? 1 : rows_ctas(d);  // own CTAs of an SM
+    const double own_start = own.tc ? 12. : solo ? 12. : 10.;
+    const double own_key = own.tc ? 0.003 : solo ? (d == 64 ? 0.03 : d == 128 ? 0.04 : 0.07) : d == 64 ? 0.01 : d == 128 ? 0.02 : 0.035;
+    const double merge = 0.5e-6 * total_q * H * d;  // per split
+    const double units = static_cast<double>(B) * Hkv * own.row_blocks;
+    const long long whole = static_cast<long long>(Hkv) * w.row_blocks;
+    int best = 1;
+    double least = -1.;
+    for (const int s : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+        if (s > 1 && s > w.tiles) break;
+        const long long ctas = whole * s;
+        const double each = start + tile * static_cast<double>((w.tiles + s - 1) / s);
+        const double end = each * static_cast<double>((ctas + kPlaces - 1) / kPlaces);
+        const double beside = static_cast<double>(std::max(0ll, kPlaces - ctas)) * at_once;
+        for (const int a : {1, 2, 3, 4, 6, 8, 12, 16, 24}) {
+            if (a > 1 && 128ll * a > max_own + 63) break;
+            // Sequences of six tenths of the longest length on average; a warp is a quarter
+            // of a CTA.
+            const double parts = (a > 1 ? units * (0.6 * a + 0.5) : units) / (solo ? kWarps : 1);
+            const double part = own_start + own_key * max_own / a;
+            const double even = (static_cast<double>(ctas) * each + parts * part / at_once) / kPlaces + 0.45 * part;
+            const double cost = std::max(parts <= beside ? part : even, end) + merge * (s + a);
+            if (least < 0. || cost < least) least = cost, best = a, *prefix_splits = s;
+        }
+    }
+    return best;
 }
 // The splits of a call as clusters: where all of its CTAs run at once, since a
 // CTA that is done holds its place until the others of its cluster are.
@@ -1087,17 +1123,19 @@ int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, i
                          int* prefix_splits) {
     if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q) return 0;
     int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
-    if (own > 0) {
-        // Warps with units alone cut the sequences by their lengths at hand: room for
-        // twice the mean number of splits.
-        const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
-        const long long warps = static_cast<long long>(fa::kPlaces) * fa::rows_ctas(d) * fa::kWarps;
-        if (fa::solo_units(c, B, Hkv, d))
-            own = static_cast<int>(std::min(c.tiles, 2 * warps / (static_cast<long long>(B) * Hkv) + 1));
-    }
-    const int shared = own > 0 ? fa_paged_num_splits(1, H, Hkv, total_q, prefix_len, d, 0, 0) : 0;
+    if (own < 1) return 0;
+    const fa::Plan w = fa::plan_of(H / Hkv, total_q, prefix_len, d, 0, 0);
+    const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    if (w.tc && !w.dual) return fa::prefix_splits_beside(w, c, B, H, Hkv, total_q, max_seqlen_k - prefix_len, d, prefix_splits);
+    const int shared = fa_paged_num_splits(1, H, Hkv, total_q, prefix_len, d, 0, 0);
+    if (shared < 1) return 0;
+    // Warps with units alone cut the sequences by their lengths at hand: room for
+    // twice the mean number of splits.
+    const long long warps = static_cast<long long>(fa::kPlaces) * fa::rows_ctas(d) * fa::kWarps;
+    if (fa::solo_units(c, B, Hkv, d))
+        own = static_cast<int>(std::min(c.tiles, 2 * warps / (static_cast<long long>(B) * Hkv) + 1));
     *prefix_splits = std::min(shared, FA_MAX_SPLITS / 2);
-    return shared > 0 ? std::min(own, FA_MAX_SPLITS / 2) : 0;
+    return std::min(own, FA_MAX_SPLITS / 2);
 }
 
 fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens_q,
@@ -1137,11 +1175,13 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
         if (!fa::encode_cache(p, cache, whole)) return FA_ERR_CUDA;
         if (fa::launch_paged<true>(p, whole, d, stream) != cudaSuccess) return FA_ERR_CUDA;
         p.whole_ctas = 0;
+        p.early = 1;
     }
     p.whole = 0;
     p.state0 = 0;
     fa::cut_paged(p, own, B, max_seqlen_q, max_seqlen_k - prefix_len, num_splits);
     p.solo = fa::solo_units(own, B, p.Hkv, d);
+    p.places = fa::kPlaces * fa::rows_ctas(d) * fa::kWarps * (p.early ? 2 : 1);
     if (!fa::encode_cache(p, cache, own)) return FA_ERR_CUDA;
     if (fa::launch_paged<true>(p, own, d, stream) != cudaSuccess) return FA_ERR_CUDA;
     p.num_splits = num_splits + prefix_splits;

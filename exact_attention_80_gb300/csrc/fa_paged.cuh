@@ -115,14 +115,32 @@ struct PagedParams {
     int base_len, base_pages, whole, state0;
     // A launch of fa_paged_rows_kernel that takes both parts: the first `whole_ctas`
     // CTAs have the prefix, cut as `shared` says, the others the sequences' own keys;
-    // `solo`: each warp of those a unit of its own (paged_unit).
+    // `solo`: each warp of those a unit of its own (paged_unit), `places` of them, or twice
+    // as many as run at once beside a launch that has part of the SMs.
     unsigned whole_ctas;
-    int solo;
+    int solo, places;
+    // The second launch of a call that takes two: it need not wait for the first one, whose
+    // CTAs have all waited for what came before when this grid may start, so the two run
+    // side by side; one CTA more, the last, waits for the first launch, and by it the merge
+    // does.
+    int early;
     struct {
         int max_q, max_k, row_blocks, num_splits, tiles_per_split, state0;
     } shared;
 };
 
+// Waits for the grid before this one in the stream; false for the CTA that is there for
+// that alone.
+template <bool PART>
+__device__ __forceinline__ bool paged_wait(const PagedParams& p) {
+    if (PART && p.early) {
+        if (blockIdx.x + 1 < gridDim.x) return true;
+        griddep_wait();
+        return false;
+    }
+    griddep_wait();
+    return true;
+}
 // The new tokens of sequence b (of the one problem where `whole`), positions and lengths
 // without the keys of a shared prefix. False where they are broken.
 template <bool PART>

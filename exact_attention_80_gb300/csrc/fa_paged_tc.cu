@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
     volatile uint32_t* abort_flag = misc + 1;
     auto bar = [&](int i) -> uint32_t { return sbase + L::BAR_OFF + 8u * i; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    griddep_wait();
+    if (!paged_wait<PART>(p)) return;
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     if (threadIdx.x == 0) {
@@ -1113,7 +1113,8 @@ cudaError_t launch_tc(const PagedParams& p, cudaStream_t stream) {
                                     static_cast<int>(L::ALLOC));
     });
     if (e != cudaSuccess) return e;
-    const long long ctas = static_cast<long long>(PART && p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks;
+    const long long ctas = static_cast<long long>(PART && p.whole ? 1 : p.B) * p.Hkv * p.num_splits * p.row_blocks +
+                           (PART ? p.early : 0);
     if (ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_paged_tc_kernel<D, SHARES, PART>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC,
                             stream, p);
