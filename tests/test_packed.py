@@ -304,6 +304,33 @@ def test_strided_tokens():
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+def test_tokens_behind_four_gigabytes(d):
+    """Tokens so far apart that their offsets do not fit 32 bits: the bits of tokens that lie together."""
+    if torch.cuda.mem_get_info()[0] < 40e9:
+        pytest.skip("needs 40 GB of device memory")
+    H, Hkv, ns, window, sinks = 4, 2, [900, 1, 700], 300, 2
+    T, gap = sum(ns), 2 ** 21
+    q, k, v, do = (x.cuda() for x in make(T, T, H, Hkv, d, 5))
+    batch = (dev(cu_of(ns)), dev(cu_of(ns)), max(ns), max(ns), window, sinks)
+    o, lse = fa.attention_packed(q, k, v, *batch)
+    grads = fa.attention_packed_backward(q, k, v, o, lse, do, *batch)
+    wide = torch.empty((T, gap), dtype=torch.bfloat16, device="cuda")
+    place = lambda i, h: wide[:, i * 2 ** 17: i * 2 ** 17 + h * d].unflatten(1, (h, d))  # noqa: E731
+    far = [place(i, x.shape[1]) for i, x in enumerate((q, k, v, do, *grads))]
+    assert gap * (T - 1) > 2 ** 31
+    for x, y in zip(far, (q, k, v, do)):
+        x.copy_(y)
+    of, lf = fa.attention_packed(*far[:3], *batch)
+    ws = torch.empty(fa.fa_bwd_packed_workspace_bytes(len(ns), T, T, max(ns), max(ns), H, Hkv, d, window, sinks) // 4,
+                     device="cuda")
+    fa.fa_bwd_packed(*far[:3], of, far[3], lf, *far[4:], ws, *batch)
+    ok()
+    assert torch.equal(o, of) and torch.equal(lse, lf)
+    assert torch.equal(far[5], grads[1]) and torch.equal(far[6], grads[2])
+    assert (far[4].float() - grads[0].float()).abs().max() <= 2.0 ** -7 * grads[0].float().abs().max()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_what_is_not_the_sequences_has_no_influence(d, bad):
     """Infinities and NaN in other sequences, before the first and behind the last one: the same bits."""

@@ -423,6 +423,105 @@ def test_two_graphs_of_prefix_calls_keep_their_workspaces():
     ok()
 
 
+def test_read_and_prefix_behind_four_gigabytes():
+    """Pages, rows and strides whose offsets do not fit 32 bits: the bits of small ones."""
+    page, Hkv, d, H, B, prefix = 128, 8, 256, 16, 3, 256
+    P = 2 ** 31 // (Hkv * page * d) + 9 if torch.cuda.mem_get_info()[0] > 40e9 else 0
+    if not P:
+        pytest.skip("needs 40 GB of device memory")
+    lens = [prefix + 70, prefix + 300, prefix + 1]
+    cache = Cache(lens, page, Hkv, d, 5, shared=prefix, spare=0)
+    small, n = cache.gpu(), cache.codes[0].shape[0]
+    big = [torch.empty((P, *x.shape[1:]), dtype=x.dtype, device="cuda") for x in small]
+    for x, y in zip(big, small):
+        x[P - n:] = y
+    far = np.where(cache.table >= 0, cache.table + P - n, -1)
+    q, one = normal((B, H, d), 1).cuda(), cu_of([1] * B)
+    out = []
+    for g, table in ((small, cache.table), (big, far)):
+        o, lse = fa.attention_prefix_fp8(q, *g, dev(table), dev(one), dev(lens), 1, max(lens), prefix)
+        k, v = fa.kv_read_fp8(*g, dev(table), dev(cu_of(lens)), None, sum(lens))
+        ok()
+        out.append((o, lse, k, v))
+    for x, y in zip(*out):
+        assert torch.equal(x, y)
+    wide = torch.empty((sum(lens), 2 ** 22), dtype=torch.bfloat16, device="cuda")
+    k, v = (wide[:, at: at + Hkv * d].unflatten(1, (Hkv, d)) for at in (0, 2 ** 21))
+    assert k.stride(0) * (k.shape[0] - 1) > 2 ** 31
+    fa.fa_kv_read_fp8(*small, k, v, dev(cache.table), dev(cu_of(lens)))
+    ok()
+    assert torch.equal(k, out[0][2]) and torch.equal(v, out[0][3])
+
+
+def test_pages_named_twice():
+    """Sequences that hold the same pages, and a page that a sequence holds twice."""
+    page, Hkv, d, H, prefix = 16, 2, 64, 4, 32
+    cache = Cache([prefix + 50], page, Hkv, d, 5, shared=prefix)
+    row = cache.table[0].copy()
+    row[3] = row[2]
+    cache.table = np.stack([row, cache.table[0], row])
+    lens = [prefix + 45, prefix + 50, prefix + 33]
+    g, table = cache.gpu(), dev(cache.table)
+    q, cu = normal((3, H, d), 1), cu_of([1] * 3)
+    o, lse = fa.attention_prefix_fp8(q.cuda(), *g, table, dev(cu), dev(lens), 1, max(lens), prefix)
+    k, v = fa.kv_read_fp8(*g, table, dev(cu_of(lens)), None, sum(lens))
+    ok()
+    check(o, lse, *cache.want(q, cu, lens, d))
+    for x, c, s in zip((k, v), cache.codes, cache.scale):
+        assert np.array_equal(f64(x), orc.read(c, s, cache.table, [0] * 3, lens, page))
+
+
+@pytest.mark.parametrize("d,H,Hkv,B,n", [(128, 32, 8, 60, 1), (128, 32, 8, 12, 5), (256, 16, 2, 31, 1), (64, 8, 8, 4, 1)])
+def test_steps_that_follow_without_a_break(d, H, Hkv, B, n):
+    """Tokens appended and attended to step after step, with nothing in between, and in a graph: what each step alone
+    gives, launch after launch."""
+    prefix, page, steps = 640, 64, 12
+    lens0 = [prefix + 1 + 23 * b % 200 for b in range(B)]
+    cache = Cache([x + steps * n for x in lens0], page, Hkv, d, 7, shared=prefix)
+    table, cu = dev(cache.table), dev(cu_of([n] * B))
+    most = max(lens0) + steps * n
+    tokens = [[normal((B * n, h, d), 3 * i + j).cuda() for j, h in enumerate((H, Hkv, Hkv))] for i in range(steps)]
+
+    def run(pause):
+        g = cache.gpu()
+        lens = dev(lens0)
+        q, out = torch.empty_like(tokens[0][0]), []
+        for t in tokens:
+            lens += n
+            q.copy_(t[0])
+            pause()
+            fa.kv_append_fp8(None, t[1], t[2], *g, table, cu, lens, n)
+            pause()
+            out.append(fa.attention_prefix_fp8(q, *g, table, cu, lens, n, most, prefix))
+            pause()
+        return out
+
+    want = run(torch.cuda.synchronize)
+    ok()
+    for _ in range(3):
+        got = run(lambda: None)
+        ok()
+        for x, y in zip(got, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    g, lens, q = cache.gpu(), dev(lens0), torch.empty_like(tokens[0][0])
+    with torch.cuda.graph(graph, stream=side):
+        out = []
+        for t in tokens:
+            lens += n
+            q.copy_(t[0])
+            fa.kv_append_fp8(None, t[1], t[2], *g, table, cu, lens, n)
+            out.append(fa.attention_prefix_fp8(q, *g, table, cu, lens, n, most, prefix))
+    for _ in range(2):
+        lens.copy_(dev(lens0))
+        for x, y in zip(g, cache.gpu()):
+            x.copy_(y)
+        graph.replay()
+        ok()
+        for x, y in zip(out, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 # ---------------------------------------------------------------- used together
 @pytest.mark.parametrize("d,page,H,Hkv", [(64, 16, 4, 2), (128, 64, 8, 2), (256, 32, 6, 2)])
 def test_prompts_context_read_back_and_tokens_behind_a_prefix(d, page, H, Hkv):
