@@ -1197,10 +1197,10 @@ __device__ __forceinline__ float bwd_dot(unsigned mine, const float (&a)[8], con
 
 // fa_bwd_win_pre_kernel on packed sequences: a block takes 64 padded rows, which are one
 // sequence's, of pre_heads(D) heads. Bound by memory (O and dO are read, the fp32 dQ is
-// zeroed): the rows of up to four passes are loaded before the first is used. Rows that
-// see few keys come in a loop of their own behind, four keys at a time: one key after the
-// other they took longer than all other rows (24 documents of up to 2047 tokens, 16 heads
-// of 128: 88 us).
+// zeroed; 63 us, 6.8 TB/s, for 24 documents of up to 2047 tokens, 16 heads of 128): four
+// rows of a thread are loaded before the first is used. Rows that see few keys come in a
+// loop of their own behind, four keys at a time: one key after the other they took longer
+// than all other rows (the same documents: 88 us).
 __host__ __device__ constexpr int pre_heads(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
 template <int D>
 __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bfloat16* __restrict__ q,
@@ -1210,7 +1210,7 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
                                                                  const __nv_bfloat16* __restrict__ dout,
                                                                  const float* __restrict__ lse,
                                                                  const __grid_constant__ BwdParams p) {
-    constexpr int LANES = D / 8, ROWS = 256 / LANES, PASSES = kBwdHalf / ROWS, U = PASSES < 4 ? PASSES : 4;
+    constexpr int LANES = D / 8, ROWS = 256 / LANES, PASSES = kBwdHalf / ROWS, U = 4;
     __shared__ BwdPlace place;
     const int lane = threadIdx.x % LANES, c = lane * 8, r0 = threadIdx.x / LANES;
     // (Heads fastest: the blocks at hand read whole tokens.)
@@ -1236,36 +1236,36 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
         return pos < 0 ? 0 : ns + pos + 1 - w0;
     };
     bool few = false;
+    const int items = PASSES * (h1 - h0);
 #pragma unroll 1
-    for (int h = h0; h < h1; ++h) {
-#pragma unroll 1
-        for (int e0 = 0; e0 < PASSES; e0 += U) {
-            uint4 g_raw[U], o_raw[U];
-            float l[U];
+    for (int e0 = 0; e0 < items; e0 += U) {
+        uint4 g_raw[U], o_raw[U];
+        float l[U];
 #pragma unroll
-            for (int e = 0; e < U; ++e) {
-                const long long token = s.q0 + min(i0 + r0 + (e0 + e) * ROWS, s.n - 1);
-                l[e] = lse[static_cast<long long>(h) * p.seqs.total_q + token];
-                g_raw[e] = *reinterpret_cast<const uint4*>(dout + token * p.do_stride + static_cast<long long>(h) * D + c);
-                o_raw[e] = *reinterpret_cast<const uint4*>(o + (token * p.H + h) * D + c);
-            }
+        for (int e = 0; e < U; ++e) {
+            const int x = min(e0 + e, items - 1), h = h0 + x / PASSES;
+            const long long token = s.q0 + min(i0 + r0 + x % PASSES * ROWS, s.n - 1);
+            l[e] = lse[static_cast<long long>(h) * p.seqs.total_q + token];
+            g_raw[e] = *reinterpret_cast<const uint4*>(dout + token * p.do_stride + static_cast<long long>(h) * D + c);
+            o_raw[e] = *reinterpret_cast<const uint4*>(o + (token * p.H + h) * D + c);
+        }
 #pragma unroll
-            for (int e = 0; e < U; ++e) {
-                const int r = r0 + (e0 + e) * ROWS, i = i0 + r;
-                const long long row = static_cast<long long>(h) * p.rows_pad + first + r;
-                if (i < s.n) st_global_v8(p.dq_acc + row * D + c, zero);
-                float g[8], a[8];
-                bwd_unpack8(g_raw[e], g);
-                bwd_unpack8(o_raw[e], a);
-                const float dd = bwd_dot<LANES>(mine, a, g);
-                int ns, w0;
-                const int seen = visible(i, ns, w0);
-                const bool by_keys = i < s.n && seen > 0 && seen <= kFewKeys;
-                few = few || by_keys;
-                if (lane == 0) {
-                    if (!by_keys) const_cast<float*>(p.ndd)[row] = i < s.n && seen > 0 ? -dd : 0.f;
-                    const_cast<float*>(p.nlse2)[row] = i < s.n && l[e] != -INFINITY ? -(l[e] * kLog2e) : -INFINITY;
-                }
+        for (int e = 0; e < U; ++e) {
+            const int x = e0 + e, h = h0 + x / PASSES, r = r0 + x % PASSES * ROWS, i = i0 + r;
+            if (x >= items) break;  // (the whole block)
+            const long long row = static_cast<long long>(h) * p.rows_pad + first + r;
+            if (i < s.n) st_global_v8(p.dq_acc + row * D + c, zero);
+            float g[8], a[8];
+            bwd_unpack8(g_raw[e], g);
+            bwd_unpack8(o_raw[e], a);
+            const float dd = bwd_dot<LANES>(mine, a, g);
+            int ns, w0;
+            const int seen = visible(i, ns, w0);
+            const bool by_keys = i < s.n && seen > 0 && seen <= kFewKeys;
+            few = few || by_keys;
+            if (lane == 0) {
+                if (!by_keys) const_cast<float*>(p.ndd)[row] = i < s.n && seen > 0 ? -dd : 0.f;
+                const_cast<float*>(p.nlse2)[row] = i < s.n && l[e] != -INFINITY ? -(l[e] * kLog2e) : -INFINITY;
             }
         }
     }
@@ -1305,17 +1305,21 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
     }
 }
 
-// The last launch on packed sequences: a block writes dQ of 64 padded rows of a head,
-// or, behind those, dK or dV of a key tile whose sums were left in parts, added part by
-// part in order. Rows that belong to no sequence get zeros where the call asks for it.
+// The last launch on packed sequences: a block writes dQ of 64 padded rows of pre_heads(D)
+// heads, or, behind those, dK or dV of kPostKeys keys of a tile whose sums were left in
+// parts, added part by part in order. Four rows of a thread, or parts of one, are loaded
+// before the first is used; bound by memory (38000 tokens in six documents, 16 heads of 64,
+// window 1024, 4 sinks: 35 us, 6.7 TB/s; with a head and a tile per block, a row after the
+// other, 61). Rows that belong to no sequence get zeros where the call asks for it.
+constexpr int kPostKeys = 32;
 template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_pack_post_kernel(const __grid_constant__ BwdParams p,
-                                                               __nv_bfloat16* __restrict__ dq, long long q_blocks) {
+__global__ void __launch_bounds__(256, 4) fa_bwd_pack_post_kernel(const __grid_constant__ BwdParams p,
+                                                                  __nv_bfloat16* __restrict__ dq, long long q_blocks) {
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();
-    constexpr int LANES = D / 8, ROWS = 256 / LANES;
+    constexpr int LANES = D / 8, ROWS = 256 / LANES, PASSES = kBwdHalf / ROWS, U = 4;
     __shared__ BwdPlace place;
-    const int lane = threadIdx.x % LANES, c = lane * 8;
+    const int lane = threadIdx.x % LANES, c = lane * 8, r0 = threadIdx.x / LANES;
     auto put = [&](__nv_bfloat16* dst, const float (&x)[8], float f) {
         *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0] * f, x[1] * f), pack_bf16x2(x[2] * f, x[3] * f),
                                                     pack_bf16x2(x[4] * f, x[5] * f), pack_bf16x2(x[6] * f, x[7] * f));
@@ -1326,39 +1330,65 @@ __global__ void __launch_bounds__(256) fa_bwd_pack_post_kernel(const __grid_cons
     };
     const bool is_q = blockIdx.x < q_blocks;
     long long lin = is_q ? blockIdx.x : blockIdx.x - q_blocks;
-    const int heads = is_q ? p.H : 2 * p.Hkv;
+    const int heads = is_q ? (p.H + pre_heads(D) - 1) / pre_heads(D) : 2 * p.Hkv * (kBwdKeys / kPostKeys);
     const int h = static_cast<int>(lin % heads);
     lin /= heads;
-    const long long first = is_q ? lin * kBwdHalf : lin;  // padded row, or tile
+    // The padded row, or the tile by its number (the sinks' alone: by theirs).
+    const long long first = is_q ? lin * kBwdHalf : lin;
     if (threadIdx.x < 32) {
         BwdPlace x = {};
-        x.b = bwd_pack_find(p, first, !is_q, threadIdx.x, x.s);
+        if (is_q || p.parts > 1) {
+            x.b = bwd_pack_find(p, first, !is_q, threadIdx.x, x.s);
+        } else {
+            x.b = static_cast<int>(lin / p.sink_tiles);
+            packed_seq(p.seqs, x.b, x.s);
+        }
         if (threadIdx.x == 0) place = x;
     }
     __syncthreads();
     const PackedSeq s = place.s;
     if (place.b >= 0 && is_q) {
         const int i0 = static_cast<int>(first - pad_row(s.q0, place.b));
+        const int h0 = h * pre_heads(D), items = PASSES * (min(p.H, h0 + pre_heads(D)) - h0);
+#pragma unroll 1
+        for (int e0 = 0; e0 < items; e0 += U) {
+            float x[U][8];
 #pragma unroll
-        for (int e = 0; e < kBwdHalf / ROWS; ++e) {
-            const int r = e * ROWS + threadIdx.x / LANES;
-            if (i0 + r >= s.n) continue;
-            float x[8];
-            get(p.dq_acc + (static_cast<long long>(h) * p.rows_pad + first + r) * D + c, x);
-            put(dq + (static_cast<long long>(s.q0) + i0 + r) * p.dq_stride + static_cast<long long>(h) * D + c, x, p.scale);
+            for (int e = 0; e < U; ++e) {
+                const int at = min(e0 + e, items - 1), r = min(r0 + at % PASSES * ROWS, s.n - 1 - i0);
+                get(p.dq_acc + (static_cast<long long>(h0 + at / PASSES) * p.rows_pad + first + r) * D + c, x[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < U; ++e) {
+                const int at = e0 + e, r = r0 + at % PASSES * ROWS;
+                if (at < items && i0 + r < s.n)
+                    put(dq + (static_cast<long long>(s.q0) + i0 + r) * p.dq_stride +
+                            static_cast<long long>(h0 + at / PASSES) * D + c,
+                        x[e], p.scale);
+            }
         }
     } else if (place.b >= 0) {
-        const int kt = static_cast<int>(first - tile_slot(s.k0, place.b)), head = h >> 1, is_v = h & 1;
+        const int kt = static_cast<int>(p.parts > 1 ? first - tile_slot(s.k0, place.b) : lin % p.sink_tiles);
+        const int quarter = h % (kBwdKeys / kPostKeys), head = h / (kBwdKeys / kPostKeys) >> 1;
+        const int is_v = h / (kBwdKeys / kPostKeys) & 1;
         const int parts = kt < p.sink_tiles ? p.sink_parts : p.parts;
         const long long sums = bwd_sums(p, s, place.b, kt, head);
-        for (int r = threadIdx.x / LANES; r < kBwdKeys && parts > 1; r += ROWS) {
+#pragma unroll 1
+        for (int r = quarter * kPostKeys + r0; r < (quarter + 1) * kPostKeys && parts > 1; r += ROWS) {
             const int key = kt * kBwdKeys + r;
             if (key >= s.m) break;
-            float x[8], y[8];
-            for (int i = 0; i < parts; ++i) {
-                get(p.dkv_part + (((sums + i) * 2 + is_v) * kBwdKeys + r) * D + c, y);
+            float x[8];
+#pragma unroll 1
+            for (int n0 = 0; n0 < parts; n0 += U) {
+                float y[U][8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = i == 0 ? y[e] : x[e] + y[e];
+                for (int n = 0; n < U; ++n)
+                    get(p.dkv_part + (((sums + min(n0 + n, parts - 1)) * 2 + is_v) * kBwdKeys + r) * D + c, y[n]);
+#pragma unroll
+                for (int n = 0; n < U; ++n)
+                    if (n0 + n < parts)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = n0 + n == 0 ? y[n][e] : x[e] + y[n][e];
             }
             put(static_cast<__nv_bfloat16*>(is_v ? p.dv : p.dk) +
                     (static_cast<long long>(s.k0) + key) * (is_v ? p.dv_stride : p.dk_stride) +
@@ -1556,8 +1586,9 @@ cudaError_t launch_bwd_pack(const BwdParams& p, const void* q, const void* k, co
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_bwd_main<D, true, true>(p, stream);
     if (e != cudaSuccess) return e;
-    const long long q_blocks = p.rows_pad / kBwdHalf * p.H;
-    const long long k_blocks = p.parts > 1 || p.sink_parts > 1 ? slots * 2 * p.Hkv : 0;
+    const long long q_blocks = blocks;
+    const long long k_tiles = p.parts > 1 ? slots : p.sink_parts > 1 ? static_cast<long long>(p.seqs.B) * p.sink_tiles : 0;
+    const long long k_blocks = k_tiles * 2 * p.Hkv * (kBwdKeys / kPostKeys);
     if (q_blocks + k_blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_bwd_pack_post_kernel<D>, dim3(static_cast<unsigned>(q_blocks + k_blocks)), 256, 0, stream,
                             p, static_cast<__nv_bfloat16*>(dq), q_blocks);
