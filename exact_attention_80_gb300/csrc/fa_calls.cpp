@@ -513,7 +513,8 @@ PyObject* call_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      p.cache.d == t.d && scale_of(a[11], p.cache.d, &scale));
     const int H = static_cast<int>(t.h), total = static_cast<int>(t.n), d = static_cast<int>(t.d);
     int both[2] = {1, 1};
-    both[0] = lib.prefix_splits(p.B, H, p.cache.Hkv, total, max_q, max_k, prefix_len, d, &both[1]);
+    if (!splits || !shared)
+        both[0] = lib.prefix_splits(p.B, H, p.cache.Hkv, total, max_q, max_k, prefix_len, d, &both[1]);
     if (both[0] < 1) both[0] = both[1] = 1;  // (out of range: the call says so)
     if (!splits) splits = both[0];
     if (!shared) shared = both[1];

@@ -1121,14 +1121,14 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
 
 int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int prefix_len, int d,
                          int* prefix_splits) {
-    if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q) return 0;
-    int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
-    if (own < 1) return 0;
+    if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q || B < 1 || Hkv < 1 ||
+        H < Hkv || H % Hkv || max_seqlen_q < 1 || !fa::valid_d(d))
+        return 0;
     const fa::Plan w = fa::plan_of(H / Hkv, total_q, prefix_len, d, 0, 0);
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
     if (w.tc && !w.dual) return fa::prefix_splits_beside(w, c, B, H, Hkv, total_q, max_seqlen_k - prefix_len, d, prefix_splits);
+    int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
     const int shared = fa_paged_num_splits(1, H, Hkv, total_q, prefix_len, d, 0, 0);
-    if (shared < 1) return 0;
     // Warps with units alone cut the sequences by their lengths at hand: room for
     // twice the mean number of splits.
     const long long warps = static_cast<long long>(fa::kPlaces) * fa::rows_ctas(d) * fa::kWarps;
