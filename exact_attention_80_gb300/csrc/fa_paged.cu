@@ -739,21 +739,35 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     };
     load(wi);
     int used = 0;
-    float mm = -INFINITY;
-    for (int s = lane; s < states; s += 32) {
-        const float m = p.ws_m[s * stride + row];
-        if (m != -INFINITY) used = s + 1, mm = fmaxf(mm, m);
-    }
-    used = __reduce_max_sync(0xffffffffu, used);
-    live = used > 0;
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f;
-    for (int s = lane; s < used; s += 32) {
-        const float m = p.ws_m[s * stride + row];
+    float mm = -INFINITY, ll = 0.f, ref;
+    if (PART && p.num_splits <= 32) {
+        // A state a lane: m and l in one trip to memory.
+        const float m = lane < states ? p.ws_m[lane * stride + row] : -INFINITY;
+        const float l = lane < states ? p.ws_l[lane * stride + row] : 0.f;
+        if (m != -INFINITY) used = lane + 1;
+        used = __reduce_max_sync(0xffffffffu, used);
+        live = used > 0;
+        mm = m;
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        ref = mm == -INFINITY ? 0.f : mm;
         const float f = ex2(m - ref);
-        weight[warp][s] = f;
-        if (m != -INFINITY) ll = fmaf(f, p.ws_l[s * stride + row], ll);
+        weight[warp][lane] = f;
+        if (m != -INFINITY) ll = f * l;
+    } else {
+        for (int s = lane; s < states; s += 32) {
+            const float m = p.ws_m[s * stride + row];
+            if (m != -INFINITY) used = s + 1, mm = fmaxf(mm, m);
+        }
+        used = __reduce_max_sync(0xffffffffu, used);
+        live = used > 0;
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        ref = mm == -INFINITY ? 0.f : mm;
+        for (int s = lane; s < used; s += 32) {
+            const float m = p.ws_m[s * stride + row];
+            const float f = ex2(m - ref);
+            weight[warp][s] = f;
+            if (m != -INFINITY) ll = fmaf(f, p.ws_l[s * stride + row], ll);
+        }
     }
     for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
     __syncwarp();
@@ -967,8 +981,10 @@ bool as_clusters(const Plan& c, long long units, int num_splits, int d) {
 template <int D, bool PART>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.max_q * p.H;
-    // Four warps a row while that leaves the grid within about one wave.
-    const bool four = p.num_splits > 8 && rows <= 4096;
+    // Four warps a row while that leaves the grid within about one wave (of the merge of a
+    // prefix's states, which holds more registers, a smaller one: 2048 rows of nine states,
+    // the whole call, 57 us with one warp, 60.5 with four).
+    const bool four = p.num_splits > 8 && rows <= (PART ? 1024 : 4096);
     const long long blocks = four ? rows : (rows + 3) / 4;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(four ? fa_paged_merge_kernel<D, 4, PART> : fa_paged_merge_kernel<D, 1, PART>,

@@ -111,6 +111,10 @@ PREFIX = [
     ([1, 0, 1, 0], [9, 5, 3, 0], 64, 16, 4, 2, 128, None),        # sequences that bring nothing
     ([0, 1, 2], [0, 77, 2], 48, 16, 3, 1, 128, (4, 2)),           # the first one brings nothing and holds nothing
     ([2] * 100, [2 + b % 50 for b in range(100)], 144, 16, 2, 1, 64, None),
+    ([1, 1, 1], [7, 400, 1300], 960, 16, 8, 2, 128, (20, 25)),    # more than 32 states, and than 128
+    ([1] * 12, [1 + 60 * b for b in range(12)], 2048, 64, 8, 2, 64, (40, 3)),
+    ([3] * 20, [90] * 20, 1536, 32, 8, 2, 128, (3, 120)),
+    ([1] * 24, [1 + 9 * b for b in range(24)], 1024, 64, 16, 2, 256, (2, 60)),
     # so many sequences that each warp has a share of one for itself
     ([1] * 160, [1 + 37 * b % 150 for b in range(160)], 64, 16, 8, 4, 64, None),
     ([1] * 160, [1 + b % 3 if b != 97 else 2500 for b in range(160)], 128, 64, 4, 4, 64, None),   # one far longer
@@ -239,6 +243,24 @@ def test_prefix_rows_behind_the_last_sequence_are_left():
         fa.fa_fwd_prefix_fp8(q, *g, o, lse, dev(cache.table), dev(cu_of(ns)), dev(lens), 4, max(lens), prefix, ws, *splits)
         ok()
         assert torch.all(o[6:] == 5.0) and torch.all(lse[:, 6:] == 5.0) and not torch.any(lse[:, :6] == 5.0)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prefix_workspace_of_sixteen_byte_alignment(d):
+    """The workspace at a multiple of 16 bytes that is none of 32: the same bits."""
+    prefix, page, H, Hkv = 640, 32, 8, 1
+    lens, ns = [prefix + 40 * b + 3 for b in range(12)], [3] * 12
+    cache = Cache(lens, page, Hkv, d, 8, shared=prefix)
+    q, out = normal((36, H, d), 1).cuda(), []
+    args = [*cache.gpu()]
+    for skip in (0, 4):
+        o, lse = torch.empty_like(q), torch.empty((H, 36), device="cuda")
+        ws = torch.empty(fa.fa_paged_workspace_bytes(36, H, d, 5) // 4 + 4, device="cuda")[skip:]
+        assert ws.data_ptr() % 32 == 4 * skip
+        fa.fa_fwd_prefix_fp8(q, *args, o, lse, dev(cache.table), dev(cu_of(ns)), dev(lens), 3, max(lens), prefix, ws, 2, 3)
+        ok()
+        out.append((o, lse))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
 
 
 def test_prefix_captured_replayed_and_on_a_side_stream():
