@@ -545,9 +545,10 @@ def fa_fwd_splitkv_static(q, k, v, o, lse, num_splits: int, causal=False,
 # These calls are short (a decode step of a few sequences runs in a few
 # microseconds on the GPU). On the current stream and with plain arguments rope,
 # kv_append_fp8, kv_read_fp8, attention_paged_fp8, attention_prefix_fp8 and the two
-# calls each of the window and of packed sequences run in the compiled module _calls, where it is there; it answers None where an argument is
-# anything else, and the forms below, whose checks touch each tensor once, say
-# what is wrong or take the call.
+# calls each of the window and of packed sequences run in the compiled module
+# _calls, where it is there; it answers None where an argument is anything else, and
+# the forms below, whose checks touch each tensor once, say what is wrong or take the
+# call.
 _ROTATION = struct.Struct(f"PPii{FA_MAX_AXES}iii")   # fa_rotation
 _ROPE_TENSOR = struct.Struct("PPi6q")                # fa_rope_tensor
 _PAGED_CACHE = struct.Struct("PPPPiiii")             # fa_paged_cache

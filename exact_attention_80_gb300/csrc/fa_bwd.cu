@@ -1732,7 +1732,8 @@ size_t fa_bwd_packed_workspace_bytes(int B, int total_q, int total_k, int max_se
     const size_t rows = static_cast<size_t>(fa::packed_rows_pad(total_q, B)) * H;
     return (rows * (static_cast<size_t>(d) + 2) +
             fa::bwd_pack_parts(B, total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks).part_floats) *
-           sizeof(float);
+               sizeof(float) +
+           16;  // (dQ's sums begin at a multiple of 32 bytes, for stores of that many)
 }
 
 fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -1760,7 +1761,7 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
         return FA_ERR_CUDA;
     p.rows_pad = fa::packed_rows_pad(batch->total_q, batch->B);
     const size_t rows = static_cast<size_t>(p.rows_pad) * H;
-    float* ws = static_cast<float*>(workspace);
+    float* ws = static_cast<float*>(workspace) + (fa::aligned(workspace, 32) ? 0 : 4);
     p.dq_acc = ws;
     p.nlse2 = ws + rows * d;
     p.ndd = p.nlse2 + rows;

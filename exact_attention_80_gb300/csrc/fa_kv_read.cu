@@ -8,8 +8,9 @@
 // or V after the other: sixteen bytes loaded, 32 written, all loads of a thread
 // independent of one another behind the token's page. Which sequence a token belongs to
 // is found once per block, so the chain is offsets, page, codes. A thread's 32 bytes go
-// out as one store: as two of sixteen, each leaves half of every sector to the other
-// (eight contexts of up to 16200 tokens, 8 heads of 128: 84.7 us against 66.1, 6.06 TB/s).
+// out as one store where the outputs and their tokens lie at multiples of 32 bytes (WIDE):
+// as two of sixteen, each leaves half of every sector to the other (eight contexts of up
+// to 16200 tokens, 8 heads of 128: 84.7 us against 64.6, 6.35 TB/s).
 #include <algorithm>
 #include <cstring>
 
@@ -35,7 +36,7 @@ struct ReadParams {
 
 constexpr int kReadThreads = 256;
 
-template <int D>
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int LANES = D / 16, TOKENS = kReadThreads / LANES, UNROLL = 16;
     __shared__ int seq_of[TOKENS];
@@ -65,7 +66,12 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_c
         return p.out[w] + static_cast<long long>(token) * p.stride[w] + static_cast<long long>(item >> 1) * D + lane * 16;
     };
     auto put = [&](__nv_bfloat16* to, const uint32_t (&x)[8]) {
-        st_global_v8(to, x);
+        if constexpr (WIDE) {
+            st_global_v8(to, x);
+        } else {
+            reinterpret_cast<uint4*>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+            reinterpret_cast<uint4*>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
     };
     if (b < 0) {
         if (!p.fill) return;
@@ -113,7 +119,8 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_c
 
 template <int D>
 cudaError_t launch_read(const ReadParams& p, dim3 grid, cudaStream_t stream) {
-    return launch_dependent(fa_kv_read_kernel<D>, grid, kReadThreads, 0, stream, p);
+    const bool wide = aligned(p.out[0], 32) && aligned(p.out[1], 32) && p.stride[0] % 16 == 0 && p.stride[1] % 16 == 0;
+    return launch_dependent(wide ? fa_kv_read_kernel<D, true> : fa_kv_read_kernel<D, false>, grid, kReadThreads, 0, stream, p);
 }
 
 }  // namespace

@@ -385,6 +385,38 @@ def test_rows_of_no_sequence(d):
     assert torch.equal(mine[0][~out], o[~out]) and torch.equal(mine[3][~out], grads[1][~out])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_sixteen_byte_alignment(d):
+    """Every tensor and the workspace at a multiple of 16 bytes that is none of 32, tokens an odd number of 16 bytes
+    apart: the same bits."""
+    H, Hkv, ns, window, sinks = 4, 2, [130, 1, 70], 60, 2
+    T = sum(ns)
+    q, k, v, do = (x.cuda() for x in make(T, T, H, Hkv, d, 8))
+    batch = (dev(cu_of(ns)), dev(cu_of(ns)), max(ns), max(ns), window, sinks)
+    o, lse = fa.attention_packed(q, k, v, *batch)
+    grads = fa.attention_packed_backward(q, k, v, o, lse, do, *batch)
+
+    def odd(h):
+        row = torch.zeros((T, h * d + 24), dtype=torch.bfloat16, device="cuda")
+        x = row[:, 8: 8 + h * d].unflatten(1, (h, d))
+        assert x.data_ptr() % 32 == 16 and x.stride(0) % 16 == 8
+        return x
+
+    far = [odd(h).copy_(x) for h, x in zip((H, Hkv, Hkv, H), (q, k, v, do))]
+    of = torch.empty(T * H * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(T, H, d)
+    lf = torch.empty(T * H + 1, device="cuda")[1:].view(H, T)
+    fa.fa_fwd_packed(*far[:3], of, lf, *batch)
+    assert of.data_ptr() % 32 == 16 and torch.equal(o, of) and torch.equal(lse, lf)
+    out = [odd(h) for h in (H, Hkv, Hkv)]
+    ws = torch.empty(fa.fa_bwd_packed_workspace_bytes(len(ns), T, T, max(ns), max(ns), H, Hkv, d, window, sinks) // 4 + 4,
+                     device="cuda")[4:]
+    assert ws.data_ptr() % 32 == 16
+    fa.fa_bwd_packed(*far[:3], of, far[3], lf, *out, ws, *batch)
+    ok()
+    assert torch.equal(out[1], grads[1]) and torch.equal(out[2], grads[2])
+    assert (out[0].float() - grads[0].float()).abs().max() <= 2.0 ** -7 * grads[0].float().abs().max()
+
+
 def test_broken_offsets_leave_the_others_their_results():
     H, Hkv, d, ns = 4, 2, 64, [40, 50, 60]
     T = sum(ns)

@@ -359,6 +359,24 @@ def test_read_strided_and_rows_of_no_sequence():
         assert torch.all(wide[rows, heads] == 3.0)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_read_into_rows_of_sixteen_byte_alignment(d):
+    """Outputs at a multiple of 16 bytes that is none of 32, and tokens an odd number of 16 bytes apart."""
+    ns, starts, page, Hkv = [20, 50], [5, 0], 16, 3
+    cache = Cache([25, 50], page, Hkv, d, 3)
+    g, args = cache.gpu(), (dev(cache.table), dev(cu_of(ns)), dev(starts))
+    k, v = fa.kv_read_fp8(*g, *args, 70)
+    for skip, gap in ((8, 0), (0, 8), (8, 24)):
+        out = []
+        for _ in range(2):
+            x = torch.zeros(70 * (Hkv * d + gap) + 8, dtype=torch.bfloat16, device="cuda")[skip:]
+            out.append(x.as_strided((70, Hkv, d), (Hkv * d + gap, d, 1)))
+        assert out[0].data_ptr() % 32 == 2 * skip
+        fa.fa_kv_read_fp8(*g, *out, *args)
+        ok()
+        assert torch.equal(out[0], k) and torch.equal(out[1], v)
+
+
 def test_read_broken_batches_touch_nothing():
     ns, page, Hkv, d = [20, 30, 10], 16, 1, 64
     cache = Cache([25, 30, 10], page, Hkv, d, 8)
