@@ -931,16 +931,18 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
                                      p);
 }
 // Whether the warps of the sequences' own parts behind a prefix take units alone: where
-// there is a unit for every CTA that runs at once.
+// there is a unit for every CTA that runs at once (and all key tiles can be counted in int).
 bool solo_units(const Plan& own, int B, int Hkv, int d) {
-    return !own.tc && static_cast<long long>(B) * Hkv >= static_cast<long long>(kPlaces) * rows_ctas(d);
+    return !own.tc && static_cast<long long>(B) * Hkv >= static_cast<long long>(kPlaces) * rows_ctas(d) &&
+           own.tiles <= 0x3fffffff / B;
 }
 // The splits of a shared prefix that the tensor-core kernel takes beside the sequences'
 // own parts (its SMs hold nothing else): both cut so that the whole ends earliest, with
 // the prefix on a part of the SMs, in microseconds of CTAs fitted to 21 batches on a GB300,
 // B x prefix + own keys from 2 x 2900 + 50 to 64 x 65536 + 2000. (64 sequences, 16384 + up
 // to 2000 keys, 32 + 8 heads, d = 128: 73 us with the prefix on all SMs first, in 19 parts,
-// 61 with six; 16 of five tokens, 8160 + up to 4000: 67 with eight, 55 with three.)
+// 61 with six, before the merge's last steps; 16 of five tokens, 8160 + up to 4000: 67
+// with eight, 55 with three.)
 int prefix_splits_beside(const Plan& w, const Plan& own, int B, int H, int Hkv, int total_q, int max_own, int d,
                          int* prefix_splits) {
     const double start = d == 64 ? 6. : d == 128 ? 8. : 24., tile = 1.6;  // a prefix CTA, a key tile of it
