@@ -1228,6 +1228,7 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
     const int i0 = static_cast<int>(first - pad_row(s.q0, place.b));
     const unsigned mine = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1u) << ((threadIdx.x & 31) & ~(LANES - 1));
     const uint32_t zero[8] = {};
+    const bool wide = reinterpret_cast<uintptr_t>(p.dq_acc) % 32 == 0;  // whole sectors a store
     // Visible keys of row i: [0, ns) and [w0, w0 + seen - ns).
     auto visible = [&](int i, int& ns, int& w0) {
         const int pos = i + s.m - s.n;
@@ -1254,7 +1255,12 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
             const int x = e0 + e, h = h0 + x / PASSES, r = r0 + x % PASSES * ROWS, i = i0 + r;
             if (x >= items) break;  // (the whole block)
             const long long row = static_cast<long long>(h) * p.rows_pad + first + r;
-            if (i < s.n) st_global_v8(p.dq_acc + row * D + c, zero);
+            float* sums = p.dq_acc + row * D + c;
+            if (i < s.n && wide) {
+                st_global_v8(sums, zero);
+            } else if (i < s.n) {
+                reinterpret_cast<float4*>(sums)[0] = reinterpret_cast<float4*>(sums)[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
             float g[8], a[8];
             bwd_unpack8(g_raw[e], g);
             bwd_unpack8(o_raw[e], a);
@@ -1732,8 +1738,7 @@ size_t fa_bwd_packed_workspace_bytes(int B, int total_q, int total_k, int max_se
     const size_t rows = static_cast<size_t>(fa::packed_rows_pad(total_q, B)) * H;
     return (rows * (static_cast<size_t>(d) + 2) +
             fa::bwd_pack_parts(B, total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks).part_floats) *
-               sizeof(float) +
-           16;  // (dQ's sums begin at a multiple of 32 bytes, for stores of that many)
+           sizeof(float);
 }
 
 fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -1761,7 +1766,7 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
         return FA_ERR_CUDA;
     p.rows_pad = fa::packed_rows_pad(batch->total_q, batch->B);
     const size_t rows = static_cast<size_t>(p.rows_pad) * H;
-    float* ws = static_cast<float*>(workspace) + (fa::aligned(workspace, 32) ? 0 : 4);
+    float* ws = static_cast<float*>(workspace);
     p.dq_acc = ws;
     p.nlse2 = ws + rows * d;
     p.ndd = p.nlse2 + rows;
