@@ -101,7 +101,8 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
     // with one of 9000 905 and 934; 1.8 waves of long lists, d = 64: 204 and 215).
     const long long reach = window > 0 ? std::min<long long>(batch->max_seqlen_k, static_cast<long long>(window) + unit + sinks)
                                        : batch->max_seqlen_k;
-    const bool persist = d <= 128 && ctas >= 3ll * sms && (d == 64 || reach <= 64 * 128);
+    // (A unit's time bounds the wait for the next but three: 2^24 keys take 0.1 s.)
+    const bool persist = d <= 128 && ctas >= 3ll * sms && reach <= (d == 64 ? 1 << 24 : 64 * 128);
     const unsigned grid = static_cast<unsigned>(persist ? sms : ctas);
     return fa::launch_fwd_packed(p, d, persist, grid, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
