@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     if (threadIdx.x == 0) griddep_launch_dependents();
 
     // Unit: row blocks fastest (they share K and V in L2), then splits, heads.
-    // (A cluster's CTAs are consecutive: its splits.) PART: one row block. Where the
-    // sequences' own units fill the GPU (solo), every warp has one of its own, heads
+    // (A cluster's CTAs are consecutive: its splits.) PART: the sequences' own units have
+    // one row block. Where those fill the GPU (solo), every warp has one of its own, heads
     // fastest: their lengths differ, and one wave of short units ends together, where
     // four warps a unit took 2.7 uneven waves (64 sequences of 260 to 2000 keys, 8 kv
     // heads).
@@ -220,6 +220,10 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
             b = unit.b;
             split = unit.split;
         } else {
+            if (whole) {
+                rb = static_cast<int>(lin % p.shared.row_blocks);
+                lin /= p.shared.row_blocks;
+            }
             split = static_cast<int>(lin % num_splits);
             lin /= num_splits;
             b = whole ? 0 : static_cast<int>(lin / p.Hkv);
@@ -930,6 +934,27 @@ cudaError_t launch_rows(const PagedParams& p, cudaStream_t stream) {
                                      CLUSTER ? static_cast<unsigned>(p.num_splits) : 1u, kWarps * 32, L::ALLOC, stream,
                                      p);
 }
+// How a shared prefix is cut, where the sequences' own parts are cut as `own`. Beyond 16
+// rows by blocks of 16 all the same, in one launch with the own parts, while a warp gets
+// no more than two key tiles where all run at once: a launch, Q's way into shared memory
+// and 128 rows of partial sums less (us, so and on the tensor cores; warps with 0.03
+// tiles, 17 sequences, 464 keys, 4 heads of 64 over one: 11.8 and 16.4; 0.35, 29, 1280, 8
+// heads of 128 over 4: 12.3 and 17.9; 2.6, 25 of four tokens, 14400, 2 heads of 64: 18.5
+// and 19.0; 3.3, 12, 5360, 56 heads of 64 over 8: 20.5 and 18.9; 5, 31, 10432, 14 heads of
+// 128 over 2: 30 and 22).
+Plan prefix_plan(const Plan& own, int total_q, int G, int Hkv, int prefix_len, int d) {
+    Plan c = plan_of(G, total_q, prefix_len, d, 0, 0);
+    const long long rows = static_cast<long long>(total_q) * G, blocks = (rows + kRows - 1) / kRows;
+    const long long tiles = (static_cast<long long>(prefix_len) + rows_keys(d) - 1) / rows_keys(d);
+    const long long warps = static_cast<long long>(kPlaces) * rows_ctas(d) * kWarps;
+    if (!c.tc || own.tc || tiles > 2 * warps || blocks * Hkv > 2 * warps / tiles) return c;
+    c.tc = c.dual = false;
+    c.block_rows = kRows;
+    c.block_keys = rows_keys(d);
+    c.row_blocks = blocks;
+    c.tiles = tiles;
+    return c;
+}
 // Whether the warps of the sequences' own parts behind a prefix take units alone: where
 // there is a unit for every CTA that runs at once (and all key tiles can be counted in int).
 bool solo_units(const Plan& own, int B, int Hkv, int d) {
@@ -1142,11 +1167,12 @@ int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, i
     if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q || B < 1 || Hkv < 1 ||
         H < Hkv || H % Hkv || max_seqlen_q < 1 || !fa::valid_d(d))
         return 0;
-    const fa::Plan w = fa::plan_of(H / Hkv, total_q, prefix_len, d, 0, 0);
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    const fa::Plan w = fa::prefix_plan(c, total_q, H / Hkv, Hkv, prefix_len, d);
     if (w.tc && !w.dual) return fa::prefix_splits_beside(w, c, B, H, Hkv, total_q, max_seqlen_k - prefix_len, d, prefix_splits);
     int own = fa_paged_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
-    const int shared = fa_paged_num_splits(1, H, Hkv, total_q, prefix_len, d, 0, 0);
+    const int shared = fa::best_splits(1, Hkv * w.row_blocks, (w.tiles * w.block_keys + 127) / 128,
+                                       fa::kPlaces * (w.tc ? 1 : fa::rows_ctas(d)), w.dual, false);
     // Warps with units alone cut the sequences by their lengths at hand: room for
     // twice the mean number of splits.
     const long long warps = static_cast<long long>(fa::kPlaces) * fa::rows_ctas(d) * fa::kWarps;
@@ -1177,9 +1203,9 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
     p.base_len = prefix_len;
     p.base_pages = prefix_len / cache->page_size;
     // The prefix, for all rows at once, and the sequences' own keys, in one launch where
-    // both have few rows; then the merge.
-    const fa::Plan whole = fa::plan_of(p.G, total_q, prefix_len, d, 0, 0);
+    // both are cut into blocks of 16 rows; then the merge.
     const fa::Plan own = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
+    const fa::Plan whole = fa::prefix_plan(own, total_q, p.G, p.Hkv, prefix_len, d);
     p.whole = 1;
     p.state0 = num_splits;
     fa::cut_paged(p, whole, 1, total_q, prefix_len, prefix_splits);

@@ -115,6 +115,14 @@ PREFIX = [
     ([1] * 12, [1 + 60 * b for b in range(12)], 2048, 64, 8, 2, 64, (40, 3)),
     ([3] * 20, [90] * 20, 1536, 32, 8, 2, 128, (3, 120)),
     ([1] * 24, [1 + 9 * b for b in range(24)], 1024, 64, 16, 2, 256, (2, 60)),
+    # prefixes long enough for the tensor-core kernel: pairs of slots, whole tiles, beside few sequences and many
+    ([1] * 16, [1 + 20 * b for b in range(16)], 8192, 64, 16, 4, 128, None),
+    ([1] * 16, [1 + 20 * b for b in range(16)], 10240, 128, 16, 4, 64, None),
+    ([1] * 24, [1 + 13 * b for b in range(24)], 6144, 64, 16, 2, 128, None),
+    ([2] * 12, [2 + 13 * b for b in range(12)], 8192, 32, 16, 2, 64, None),
+    ([1] * 24, [1 + 13 * b for b in range(24)], 2048, 64, 16, 2, 256, (3, 7)),
+    ([int(b % 4 > 0) for b in range(120)], [1 + 29 * b % 300 for b in range(120)], 2560, 64, 8, 4, 128, None),
+    ([1] * 80, [1 + 13 * b % 120 for b in range(80)], 1536, 32, 8, 4, 256, None),
     # so many sequences that each warp has a share of one for itself
     ([1] * 160, [1 + 37 * b % 150 for b in range(160)], 64, 16, 8, 4, 64, None),
     ([1] * 160, [1 + b % 3 if b != 97 else 2500 for b in range(160)], 128, 64, 4, 4, 64, None),   # one far longer
@@ -143,9 +151,10 @@ def test_prefix(case):
     check(op, lp, *want)
 
 
-def test_prefix_query_rows_that_are_not_finite():
+@pytest.mark.parametrize("prefix", [128, 20480])
+def test_prefix_query_rows_that_are_not_finite(prefix):
     """A row with a NaN or an infinity gives NaN, the others keep their results; rows of no sequence may hold anything."""
-    prefix, page, H, Hkv, d, ns, own = 128, 16, 4, 2, 128, [1] * 24, [1 + b for b in range(24)]
+    page, H, Hkv, d, ns, own = 16, 4, 2, 128, [1] * 24, [1 + b for b in range(24)]
     lens = [prefix + x for x in own]
     cache = Cache(lens, page, Hkv, d, 4, shared=prefix)
     q, cu = normal((30, H, d), 3).cuda(), cu_of(ns)
@@ -202,9 +211,10 @@ def test_prefix_broken_batches():
                 assert (o[s].float() - want[0][s].float()).abs().max() <= 2.0 ** -6 * want[0].float().abs().max()
 
 
-def test_prefix_broken_batches_of_many():
+@pytest.mark.parametrize("prefix", [64, 4096])
+def test_prefix_broken_batches_of_many(prefix):
     """As above, where each warp has a share of a sequence for itself."""
-    prefix, page, H, Hkv, d, B = 64, 16, 4, 4, 128, 130
+    page, H, Hkv, d, B = 16, 4, 4, 128, 130
     lens, ns = [prefix + 1 + 11 * b % 90 for b in range(B)], [1] * B
     cache = Cache(lens, page, Hkv, d, 8, shared=prefix)
     q, cu = normal((B, H, d), 1).cuda(), cu_of(ns)
@@ -215,7 +225,8 @@ def test_prefix_broken_batches_of_many():
     own, shared = fa.fa_prefix_num_splits(B, H, Hkv, B, 1, most, prefix, d)
     ws = torch.empty(fa.fa_paged_workspace_bytes(B, H, d, own + shared) // 4, device="cuda")
     for length, at, code, broken in ((prefix, None, 12, [77]), (3, None, 12, [77]), (most + 1, None, 12, [77]),
-                                     (None, (77, 1, 0), 14, None), (None, (77, 4, 99999), 14, None), (None, (0, 0, -7), 14, None)):
+                                     (None, (77, 1, 0), 14, None), (None, (77, prefix // page, 99999), 14, None),
+                                     (None, (0, 0, -7), 14, None)):
         table, n = cache.table.copy(), list(lens)
         if at:
             table[at[:2]] = at[2] if at[2] or table[at[:2]] else 1
@@ -515,7 +526,7 @@ def test_pages_named_twice():
 def test_steps_that_follow_without_a_break(d, H, Hkv, B, n):
     """Tokens appended and attended to step after step, with nothing in between, and in a graph: what each step alone
     gives, launch after launch."""
-    prefix, page, steps = 640, 64, 12
+    prefix, page, steps = 1280, 64, 12
     lens0 = [prefix + 1 + 23 * b % 200 for b in range(B)]
     cache = Cache([x + steps * n for x in lens0], page, Hkv, d, 7, shared=prefix)
     table, cu = dev(cache.table), dev(cu_of([n] * B))
