@@ -106,7 +106,7 @@ struct BwdParams {
     PackedSeqs seqs;
     long long rows_pad;
     long long q_stride, k_stride, v_stride, do_stride, dq_stride, dk_stride, dv_stride;
-    int fill;
+    int fill, block_heads;
 };
 
 namespace {
@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(LayoutBwd<D, WIN>::THREADS, 1) fa_bwd_kernel(c
     int part = 0, parts = 1;
     BwdUnit u = {};
     if constexpr (PACK) {
+        griddep_wait();
+        if (threadIdx.x == 0) griddep_launch_dependents();
         __shared__ BwdUnit unit;
         if (warp == 2) bwd_pack_unit(p, ui, bh, lane, &unit);
         __syncthreads();
@@ -1196,12 +1198,14 @@ __device__ __forceinline__ float bwd_dot(unsigned mine, const float (&a)[8], con
 }
 
 // fa_bwd_win_pre_kernel on packed sequences: a block takes 64 padded rows, which are one
-// sequence's, of pre_heads(D) heads. Bound by memory (O and dO are read, the fp32 dQ is
+// sequence's, of block_heads heads. Bound by memory (O and dO are read, the fp32 dQ is
 // zeroed; 63 us, 6.8 TB/s, for 24 documents of up to 2047 tokens, 16 heads of 128): four
 // rows of a thread are loaded before the first is used. Rows that see few keys come in a
 // loop of their own behind, four keys at a time: one key after the other they took longer
 // than all other rows (the same documents: 88 us).
-__host__ __device__ constexpr int pre_heads(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
+// (pre_heads(D) heads where those blocks fill the SMs twice, one where they do not: 240
+// tokens in twelve documents, 14 heads of 128, 13 us with two.)
+constexpr int pre_heads(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
 template <int D>
 __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bfloat16* __restrict__ q,
                                                                  const __nv_bfloat16* __restrict__ k,
@@ -1213,10 +1217,12 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
     constexpr int LANES = D / 8, ROWS = 256 / LANES, PASSES = kBwdHalf / ROWS, U = 4;
     __shared__ BwdPlace place;
     const int lane = threadIdx.x % LANES, c = lane * 8, r0 = threadIdx.x / LANES;
+    griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();
     // (Heads fastest: the blocks at hand read whole tokens.)
-    const unsigned parts = (p.H + pre_heads(D) - 1) / pre_heads(D);
+    const unsigned parts = (p.H + p.block_heads - 1) / p.block_heads;
     const long long first = static_cast<long long>(blockIdx.x / parts) * kBwdHalf;
-    const int h0 = static_cast<int>(blockIdx.x % parts) * pre_heads(D), h1 = min(p.H, h0 + pre_heads(D));
+    const int h0 = static_cast<int>(blockIdx.x % parts) * p.block_heads, h1 = min(p.H, h0 + p.block_heads);
     if (threadIdx.x < 32) {
         BwdPlace x = {};
         x.b = bwd_pack_find(p, first, false, threadIdx.x, x.s);
@@ -1311,7 +1317,7 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_pre_kernel(const __nv_bflo
     }
 }
 
-// The last launch on packed sequences: a block writes dQ of 64 padded rows of pre_heads(D)
+// The last launch on packed sequences: a block writes dQ of 64 padded rows of block_heads
 // heads, or, behind those, dK or dV of kPostKeys keys of a tile whose sums were left in
 // parts, added part by part in order. Four rows of a thread, or parts of one, are loaded
 // before the first is used; bound by memory (38000 tokens in six documents, 16 heads of 64,
@@ -1336,7 +1342,7 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_post_kernel(const __grid_c
     };
     const bool is_q = blockIdx.x < q_blocks;
     long long lin = is_q ? blockIdx.x : blockIdx.x - q_blocks;
-    const int heads = is_q ? (p.H + pre_heads(D) - 1) / pre_heads(D) : 2 * p.Hkv * (kBwdKeys / kPostKeys);
+    const int heads = is_q ? (p.H + p.block_heads - 1) / p.block_heads : 2 * p.Hkv * (kBwdKeys / kPostKeys);
     const int h = static_cast<int>(lin % heads);
     lin /= heads;
     // The padded row, or the tile by its number (the sinks' alone: by theirs).
@@ -1355,7 +1361,7 @@ __global__ void __launch_bounds__(256, 4) fa_bwd_pack_post_kernel(const __grid_c
     const PackedSeq s = place.s;
     if (place.b >= 0 && is_q) {
         const int i0 = static_cast<int>(first - pad_row(s.q0, place.b));
-        const int h0 = h * pre_heads(D), items = PASSES * (min(p.H, h0 + pre_heads(D)) - h0);
+        const int h0 = h * p.block_heads, items = PASSES * (min(p.H, h0 + p.block_heads) - h0);
 #pragma unroll 1
         for (int e0 = 0; e0 < items; e0 += U) {
             float x[U][8];
@@ -1529,6 +1535,10 @@ cudaError_t launch_bwd_main(const BwdParams& p, cudaStream_t stream) {
                                 : static_cast<long long>(p.BH) * p.tile_units;
     const long long ctas = units * L::HALVES;
     if (ctas < 1 || ctas > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    // (Packed sequences: its start under the first launch's end, 1 to 3 us less at any size.)
+    if constexpr (PACK)
+        return launch_dependent(fa_bwd_kernel<D, WIN, PACK>, dim3(static_cast<unsigned>(ctas)), L::THREADS, L::ALLOC_BYTES,
+                                stream, p);
     fa_bwd_kernel<D, WIN, PACK><<<static_cast<unsigned>(ctas), L::THREADS, L::ALLOC_BYTES, stream>>>(p);
     return cudaGetLastError();
 }
@@ -1582,14 +1592,25 @@ cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, con
 
 // The three launches on packed sequences.
 template <int D>
-cudaError_t launch_bwd_pack(const BwdParams& p, const void* q, const void* k, const void* v, const void* o,
+cudaError_t launch_bwd_pack(BwdParams p, const void* q, const void* k, const void* v, const void* o,
                             const void* dout, const float* lse, void* dq, long long slots, cudaStream_t stream) {
     using T = const __nv_bfloat16*;
-    const long long blocks = p.rows_pad / kBwdHalf * ((p.H + pre_heads(D) - 1) / pre_heads(D));
+    p.block_heads = pre_heads(D);
+    long long blocks = p.rows_pad / kBwdHalf * ((p.H + p.block_heads - 1) / p.block_heads);
+    if (blocks < 2 * 152) p.block_heads = 1, blocks = p.rows_pad / kBwdHalf * p.H;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-    fa_bwd_pack_pre_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(static_cast<T>(q), static_cast<T>(k), static_cast<T>(v),
-                                                        static_cast<T>(o), static_cast<T>(dout), lse, p);
-    cudaError_t e = cudaGetLastError();
+    // A grid below the number of SMs starts under the end of the one before it (9 to 320
+    // tokens: up to 2 us less; 534 tokens of 32 heads, 176 blocks: 2.5 us more, 24 documents
+    // 16).
+    cudaError_t e;
+    if (blocks <= 128) {
+        e = launch_dependent(fa_bwd_pack_pre_kernel<D>, dim3(static_cast<unsigned>(blocks)), 256, 0, stream, static_cast<T>(q),
+                             static_cast<T>(k), static_cast<T>(v), static_cast<T>(o), static_cast<T>(dout), lse, p);
+    } else {
+        fa_bwd_pack_pre_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+            static_cast<T>(q), static_cast<T>(k), static_cast<T>(v), static_cast<T>(o), static_cast<T>(dout), lse, p);
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess) e = launch_bwd_main<D, true, true>(p, stream);
     if (e != cudaSuccess) return e;
     const long long q_blocks = blocks;
