@@ -107,6 +107,7 @@ struct BwdParams {
     long long rows_pad;
     long long q_stride, k_stride, v_stride, do_stride, dq_stride, dk_stride, dv_stride;
     int fill, block_heads;
+    int pack_heads;  // kv heads whose units are taken together
 };
 
 namespace {
@@ -283,7 +284,7 @@ __device__ __forceinline__ void bwd_chunk(const uint32_t (&s)[32], const uint32_
 // its first part's partial sums.
 struct BwdUnit {
     PackedSeq s;
-    int b, kt, part, parts;
+    int b, h, kt, part, parts;
     long long sums;
     bool live;
 };
@@ -294,23 +295,33 @@ __device__ __forceinline__ long long bwd_sums(const BwdParams& p, const PackedSe
     const long long sinks = p.sink_parts > 1 ? static_cast<long long>(p.seqs.B) * p.sink_tiles * p.Hkv * p.sink_parts : 0;
     return sinks + ((tile_slot(s.k0, b) + kt) * p.Hkv + h) * p.parts;
 }
-// Unit number `at` of a kv head, found by one warp: the sinks' tiles first, then the
-// others; of each, a tile's parts beside one another.
-__device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h, int lane, BwdUnit* u) {
+// Unit number `lin`, found by one warp: the sinks' tiles first, then the others; of each, a
+// tile's parts beside one another.
+__device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, long long lin, int lane, BwdUnit* u) {
     PackedSeq s;
     if (blockIdx.x == 0)
         for (int b = lane; b < p.seqs.B; b += 32)
             if (!packed_seq(p.seqs, b, s)) atomicOr(p.status, kStatusBadSeqlens);
-    int sinks = 0;  // units of the sinks' tiles
-    if (p.sink_tiles > 0) {
-        for (int b = lane; b < p.seqs.B; b += 32) {
-            packed_seq(p.seqs, b, s);
-            sinks += min(key_tiles(s), p.sink_tiles);
-        }
-        sinks = __reduce_add_sync(0xffffffffu, sinks) * p.sink_parts;
-    }
-    const bool sink = at < sinks;
-    const int parts = sink ? p.sink_parts : p.parts, r = (sink ? at : at - sinks) / parts;
+    int sinks = 0, all = 0;  // a kv head's units of the sinks' tiles, and of the others
+    if (p.sink_tiles > 0)
+        sinks = p.sink_parts * packed_total(p.seqs.B, lane, [&](int b) {
+            PackedSeq y;
+            packed_seq(p.seqs, b, y);
+            return min(key_tiles(y), p.sink_tiles);
+        });
+    const long long sink_units = static_cast<long long>(sinks) * p.Hkv;
+    const bool sink = lin < sink_units;
+    const int parts = sink ? p.sink_parts : p.parts, together = sink ? p.Hkv : p.pack_heads;
+    if (together < p.Hkv)
+        all = p.parts * packed_total(p.seqs.B, lane, [&](int b) {
+            PackedSeq y;
+            packed_seq(p.seqs, b, y);
+            return max(key_tiles(y) - p.sink_tiles, 0);
+        });
+    PackedCursor first = {0, 0};
+    int h = 0, at = 0;
+    const bool there = packed_head(sink ? lin : lin - sink_units, p.Hkv, together, all, h, at);
+    const int r = at / parts;
     // Levels count a sequence's tiles from its last one up.
     auto runs = [&](int b, int& a, int& n) {
         PackedSeq y;
@@ -320,8 +331,7 @@ __device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h,
         n = sink ? first : tiles - first;
     };
     int b = 0, level = 0;
-    PackedCursor first = {0, 0};
-    const bool live = packed_pick(p.seqs.B, r, lane, runs, b, level, first);
+    const bool live = there && packed_pick(p.seqs.B, r, lane, runs, b, level, first);
     if (lane == 0) {
         *u = {};
         u->live = live;
@@ -330,7 +340,8 @@ __device__ __forceinline__ void bwd_pack_unit(const BwdParams& p, int at, int h,
             u->b = b;
             u->kt = key_tiles(u->s) - 1 - level;
             u->parts = parts;
-            u->part = (sink ? at : at - sinks) % parts;
+            u->h = h;
+            u->part = at % parts;
             u->sums = bwd_sums(p, u->s, b, u->kt, h);
         }
     }
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(LayoutBwd<D, WIN>::THREADS, 1) fa_bwd_kernel(c
     // CTA = (head, key-tile unit, head-dim part), the part fastest.
     const int hd = static_cast<int>(blockIdx.x % L::HALVES);
     const int unit_lin = static_cast<int>(blockIdx.x / L::HALVES);
-    const int bh = WIN ? unit_lin % p.BHkv : unit_lin / p.tile_units;  // (PACK: the kv head)
+    int bh = WIN ? unit_lin % p.BHkv : unit_lin / p.tile_units;  // (PACK: the unit's kv head)
     int ui = WIN ? unit_lin / p.BHkv : unit_lin % p.tile_units;
     int part = 0, parts = 1;
     BwdUnit u = {};
@@ -391,10 +402,11 @@ __global__ void __launch_bounds__(LayoutBwd<D, WIN>::THREADS, 1) fa_bwd_kernel(c
         griddep_wait();
         if (threadIdx.x == 0) griddep_launch_dependents();
         __shared__ BwdUnit unit;
-        if (warp == 2) bwd_pack_unit(p, ui, bh, lane, &unit);
+        if (warp == 2) bwd_pack_unit(p, unit_lin, lane, &unit);
         __syncthreads();
         u = unit;
         if (!u.live) return;
+        bh = u.h;
         ui = u.kt;
         part = u.part;
         parts = u.parts;
@@ -1816,6 +1828,14 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
     p.sink_tiles = c.sink_tiles;
     p.sink_parts = c.sink_parts;
     p.parts = c.parts;
+    // Kv heads whose Q, dO and dQ sums (8 bytes a value) stay in L2 together are taken before
+    // the next ones (32 heads of 128 without groups, eight documents of 2048: 1229 -> 950 us;
+    // 16 heads of 256, four of 4096: 3047 -> 2580), where that leaves two waves of units, the
+    // longest first (one document of 8192, 32 heads over 8, a head after the other: 1275 ->
+    // 1516), and without a window, whose tiles' rows lie close together (986 -> 1001).
+    const double head_bytes = 8. * d * p.group * batch->total_q;
+    const int together = static_cast<int>(std::min<double>(Hkv, 64e6 / head_bytes));
+    p.pack_heads = window > 0 || static_cast<double>(c.tiles) * c.parts * together < 2 * 152 ? Hkv : together;
     // Units of a kv head: no more sinks' tiles than the sequences have, the others for the rest.
     const long long sink_units = std::min(c.tiles, static_cast<long long>(std::min(batch->B, batch->total_k)) * c.sink_tiles);
     const long long units = sink_units * c.sink_parts + c.tiles * c.parts;

@@ -45,6 +45,31 @@ constexpr int kPackedSorted = 128;
 struct PackedCursor {
     int block, before;
 };
+// Unit number `lin` of `heads` heads with `all` units each: its head and its rank among
+// that head's. Heads come in groups of `together`, a group's units head by head for each
+// rank, all of a group's before the next group's. False: there is none.
+__device__ __forceinline__ bool packed_head(long long lin, int heads, int together, int all, int& h, int& rank) {
+    int first = 0, here = heads;
+    if (together < heads) {
+        const long long per = static_cast<long long>(all) * together;
+        if (per == 0) return false;
+        const int group = static_cast<int>(lin / per);
+        lin -= group * per;
+        first = group * together;
+        if (first >= heads) return false;
+        here = min(together, heads - first);
+    }
+    h = first + static_cast<int>(lin % here);
+    rank = static_cast<int>(lin / here);
+    return true;
+}
+// Sum over the sequences of what `units` says, by a whole warp.
+template <typename F>
+__device__ __forceinline__ int packed_total(int B, int lane, F&& units) {
+    int n = 0;
+    for (int b = lane; b < B; b += 32) n += units(b);
+    return __reduce_add_sync(0xffffffffu, n);
+}
 template <typename F>
 __device__ __forceinline__ bool packed_pick(int B, int r, int lane, F&& runs, int& b, int& level, PackedCursor& at) {
     constexpr int CHUNKS = kPackedSorted / 32;

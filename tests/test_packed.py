@@ -204,6 +204,9 @@ MANY = [
     (8, 4, [1 + 41 * b % 60 for b in range(150)], [1 + 31 * b % 200 for b in range(150)], 0, 0),  # than 128
     (8, 4, [b % 3 * (b % 40) for b in range(300)], [b % 50 for b in range(300)], 20, 1),          # than 256, a third with no query
     (16, 16, [700, 1500, 40, 900, 2000, 3, 1800], None, 400, 130),
+    # so many tokens and heads that the backward takes some heads before the others
+    (16, 16, [40, 300, 129, 1000, 1500, 0, 1000, 700, 1, 1600, 1000, 1300], None, 0, 0),
+    (32, 16, [33 + b % 60 for b in range(150)], None, 0, 0),
 ]
 
 
