@@ -200,8 +200,9 @@ __device__ __forceinline__ bool pack_clean_v(const FwdParams& p, uint32_t sbase,
 // Output of a query tile by its 128 softmax threads (thread r = row r = TMEM lane r;
 // `token` its token): O / l as bf16 staged by each warp for its own 32 rows, CHUNKS of 64
 // columns at a time, `step` bytes apart from `stage` on (row r's line at r * 128, or for
-// one chunk the warp's own 4 KB), then written 128 bytes of a row per eight lanes. Rows
-// past the sequence, or past the tile's whole tokens, are left out. n = 0: no key.
+// one chunk the warp's own 4 KB), then written as boxes of 32 rows or 128 bytes of a row per
+// eight lanes. Rows past the sequence, or past the tile's whole tokens, are left out. n = 0:
+// no key.
 template <int D, int QT, bool PERSIST>
 __device__ __forceinline__ void pack_store(const FwdParams& p, const WorkWin<QT>& w, int token, int r, int n, float m,
                                            float m_true, float l, float l_o, uint32_t tO, uint32_t stage) {
@@ -211,6 +212,12 @@ __device__ __forceinline__ void pack_store(const FwdParams& p, const WorkWin<QT>
     const long long row = (static_cast<long long>(w.qbase) + token) * p.H + head;
     const RowMap rm = {row, static_cast<long long>(head) * p.total_q + w.qbase + token, 0, row_ok ? 1 : 0};
     const RowOut<D> out(p, rm, 0, 0, 0, m, m_true, l, l_o);
+    // A warp whose 32 rows all exist hands them over as a box per chunk (persistent CTAs, d =
+    // 128: 2500 cycles of a unit against 4900 with stores of its own; eight prompts of 2048,
+    // 32 + 8 heads: 253 -> 235 us; four of 4096, 16 + 4 heads of 256, where a CTA has one unit
+    // and 64 KB to hand over at its end: 446 -> 451, so not there).
+    const bool box = D <= 128 && p.store_boxes && __all_sync(0xffffffffu, row_ok);
+    const int token0 = __shfl_sync(0xffffffffu, token, 0);
     const uint32_t swz = static_cast<uint32_t>(r & 7);
     const uint32_t mine = stage + (PERSIST ? 0 : (r & ~31) * 128);  // the warp's 32 lines
 #pragma unroll 1
@@ -226,6 +233,10 @@ __device__ __forceinline__ void pack_store(const FwdParams& p, const WorkWin<QT>
             } else {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) a[i] = b[i] = 0u;
+            }
+            if constexpr (PERSIST) {  // an earlier box may still be read
+                if (lane == 0) bulk_wait_group_read0();
+                __syncwarp();
             }
             const uint32_t line = mine + cc * STEP + lane * 128;
 #pragma unroll
@@ -243,6 +254,20 @@ __device__ __forceinline__ void pack_store(const FwdParams& p, const WorkWin<QT>
                     st_shared_v4(line + ((u ^ swz) << 4), pk[4 * uu], pk[4 * uu + 1], pk[4 * uu + 2], pk[4 * uu + 3]);
                 }
             }
+        }
+        if (box) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int cc = 0; cc < CHUNKS; ++cc)
+                    tma_store_3d(&p.tm_o, mine + cc * STEP, (c0 + cc) * 64, w.zq, w.qbase + token0);
+                bulk_commit_group();
+                // (Persistent CTAs wait before they write there again, and at their end.)
+                if constexpr (!PERSIST) bulk_wait_group_read0();
+            }
+            __syncwarp();
+            continue;
         }
         __syncwarp();
 #pragma unroll 1

@@ -61,6 +61,9 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
         !fa::encode_strided_tokens_map(&p.tm_k, k, d, batch->total_k, Hkv, k_stride, c.bn) ||
         !fa::encode_strided_tokens_map(&p.tm_v, v, d, batch->total_k, Hkv, v_stride, c.bn))
         return FA_ERR_CUDA;
+    p.store_boxes = 32 % G == 0;
+    if (p.store_boxes && !fa::encode_token_heads_map(&p.tm_o, o, d, batch->total_q, H, static_cast<long long>(H) * d, G, 32 / G))
+        return FA_ERR_CUDA;
     p.o = o;
     p.lse = lse;
     p.H = H;

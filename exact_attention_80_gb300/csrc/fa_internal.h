@@ -81,6 +81,7 @@ struct FwdParams {
     // {64, group, tile_tokens}: a query tile holds all heads of a kv head for
     // tile_tokens = 128 / group tokens, token by token; q_bytes of it are loaded.
     int B, max_k, tile_tokens, fill;
+    int store_boxes;  // packed: tm_o has boxes of the group's heads of 32 / group tokens
     uint32_t q_bytes;
 };
 
