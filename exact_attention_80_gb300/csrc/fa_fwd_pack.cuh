@@ -17,10 +17,10 @@
 // infinity or a NaN in V: the producer overwrites those V rows with zeros, once per
 // unit, while the unit's last scores are formed.
 //
-// Persistent CTAs (d <= 128, three waves of units and more, short key lists) take one unit
+// Persistent CTAs (d <= 128, two waves of units and more, short key lists) take one unit
 // of each round, forwards and backwards in turn; an idle warp finds them a few ahead and
 // hands them over in a ring, so that no other warp waits for the search (600 sequences of
-// 20 tokens, 16 + 4 heads, d = 128: 93 us; 356 with a CTA and a search per unit).
+// 20 tokens, 16 + 4 heads, d = 128: 93 us; 160 with a CTA and a search per unit).
 #pragma once
 
 #include "fa_fwd_win.cuh"

@@ -97,15 +97,16 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
     int sms = 0;
     if (fa::sm_count(&sms) != cudaSuccess) return FA_ERR_CUDA;
-    // Persistent CTAs where the units fill three waves, at d = 128 with lists of up to 64
-    // key tiles: a unit's start and end overlap its neighbours', its steps take a little
-    // longer (16 + 4 heads; us, one unit per CTA and persistent: d = 64, four prompts of
-    // 8000 tokens 569 and 546; d = 128, 64 of 500, 16 kv heads 175 and 152, one of 16000
-    // with one of 9000 905 and 934; 1.8 waves of long lists, d = 64: 204 and 215).
+    // Persistent CTAs where the units fill two waves, at d = 128 with lists of up to 64 key
+    // tiles: a unit's start and end overlap its neighbours', its steps take a little longer
+    // (us, one unit per CTA and persistent: d = 64, 16 + 4 heads, four prompts of 8000 tokens
+    // 561 and 542, 32 + 8, ten of 2000 262 and 217; d = 128, 16 heads, 64 of 500 152 and 144,
+    // 16 + 4, 2.5 waves in three of 2047 58 and 55; 1.6 waves in three of up to 1500, 16 + 8,
+    // 29.3 and 30.5; one of 16000 with one of 9000, 16 + 4, 900 and 934).
     const long long reach = window > 0 ? std::min<long long>(batch->max_seqlen_k, static_cast<long long>(window) + unit + sinks)
                                        : batch->max_seqlen_k;
     // (A unit's time bounds the wait for the next but three: 2^24 keys take 0.1 s.)
-    const bool persist = d <= 128 && ctas >= 3ll * sms && reach <= (d == 64 ? 1 << 24 : 64 * 128);
+    const bool persist = d <= 128 && ctas >= 2ll * sms && reach <= (d == 64 ? 1 << 24 : 64 * 128);
     const unsigned grid = static_cast<unsigned>(persist ? sms : ctas);
     return fa::launch_fwd_packed(p, d, persist, grid, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
