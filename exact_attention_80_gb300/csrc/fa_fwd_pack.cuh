@@ -15,7 +15,8 @@
 // A key tile that a sequence ends in holds the next one's keys, or what lies behind
 // the last one. Their scores are masked, but a weight of zero does not undo an
 // infinity or a NaN in V: the producer overwrites those V rows with zeros, once per
-// unit, while the unit's last scores are formed.
+// unit, while the unit's last scores are formed (persistent CTAs: behind the next unit's
+// first loads).
 //
 // Persistent CTAs (d <= 128, two waves of units and more, short key lists) take one unit
 // of each round, forwards and backwards in turn; an idle warp finds them a few ahead and

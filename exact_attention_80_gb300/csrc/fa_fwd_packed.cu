@@ -62,7 +62,8 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
         !fa::encode_strided_tokens_map(&p.tm_v, v, d, batch->total_k, Hkv, v_stride, c.bn))
         return FA_ERR_CUDA;
     p.store_boxes = 32 % G == 0;
-    if (p.store_boxes && !fa::encode_token_heads_map(&p.tm_o, o, d, batch->total_q, H, static_cast<long long>(H) * d, G, 32 / G))
+    if (p.store_boxes &&
+        !fa::encode_token_heads_map(&p.tm_o, o, d, batch->total_q, H, static_cast<long long>(H) * d, G, 32 / G))
         return FA_ERR_CUDA;
     p.o = o;
     p.lse = lse;
@@ -103,8 +104,7 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
     // 561 and 542, 32 + 8, ten of 2000 262 and 217; d = 128, 16 heads, 64 of 500 152 and 144,
     // 16 + 4, 2.5 waves in three of 2047 58 and 55; 1.6 waves in three of up to 1500, 16 + 8,
     // 29.3 and 30.5; one of 16000 with one of 9000, 16 + 4, 900 and 934).
-    const long long reach = window > 0 ? std::min<long long>(batch->max_seqlen_k, static_cast<long long>(window) + unit + sinks)
-                                       : batch->max_seqlen_k;
+    const long long reach = std::min<long long>(batch->max_seqlen_k, window > 0 ? window + unit + sinks : 1ll << 30);
     // (A unit's time bounds the wait for the next but three: 2^24 keys take 0.1 s.)
     const bool persist = d <= 128 && ctas >= 2ll * sms && reach <= (d == 64 ? 1 << 24 : 64 * 128);
     const unsigned grid = static_cast<unsigned>(persist ? sms : ctas);

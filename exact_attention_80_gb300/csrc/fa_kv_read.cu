@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_c
     const int first = blockIdx.y * p.per_block, last = min(p.items, first + p.per_block);
     auto dst = [&](int item) {
         const int w = item & 1;
-        return p.out[w] + static_cast<long long>(token) * p.stride[w] + static_cast<long long>(item >> 1) * D + lane * 16;
+        return p.out[w] + static_cast<long long>(token) * p.stride[w] + static_cast<long long>(item >> 1) * D +
+               lane * 16;
     };
     auto put = [&](__nv_bfloat16* to, const uint32_t (&x)[8]) {
         if constexpr (WIDE) {
@@ -97,7 +98,8 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_c
             const int i = i0 + u;
             if (i >= last) break;
             const long long cell = static_cast<long long>(page) * p.Hkv + (i >> 1);
-            c[u] = __ldcs(reinterpret_cast<const uint4*>(p.codes[i & 1] + ((cell << p.log_page) + slot) * D + lane * 16));
+            c[u] = __ldcs(
+                reinterpret_cast<const uint4*>(p.codes[i & 1] + ((cell << p.log_page) + slot) * D + lane * 16));
             f[u] = p.scale[i & 1][cell];
         }
 #pragma unroll
@@ -120,7 +122,8 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const __grid_c
 template <int D>
 cudaError_t launch_read(const ReadParams& p, dim3 grid, cudaStream_t stream) {
     const bool wide = aligned(p.out[0], 32) && aligned(p.out[1], 32) && p.stride[0] % 16 == 0 && p.stride[1] % 16 == 0;
-    return launch_dependent(wide ? fa_kv_read_kernel<D, true> : fa_kv_read_kernel<D, false>, grid, kReadThreads, 0, stream, p);
+    return launch_dependent(wide ? fa_kv_read_kernel<D, true> : fa_kv_read_kernel<D, false>, grid, kReadThreads, 0,
+                            stream, p);
 }
 
 }  // namespace
