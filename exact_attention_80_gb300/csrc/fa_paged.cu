@@ -1202,6 +1202,8 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
         return FA_ERR_CUDA;
     p.base_len = prefix_len;
     p.base_pages = prefix_len / cache->page_size;
+    p.own_q = max_seqlen_q;
+    p.own_k = max_seqlen_k - prefix_len;
     // The prefix, for all rows at once, and the sequences' own keys, in one launch where
     // both are cut into blocks of 16 rows; then the merge.
     const fa::Plan own = fa::plan_of(p.G, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);

@@ -113,6 +113,7 @@ struct PagedParams {
     // of all total_q rows that see all max_k keys. Either part leaves its states for a
     // merge in any case, as numbers state0 .. state0 + num_splits - 1.
     int base_len, base_pages, whole, state0;
+    int own_q, own_k;  // bounds of a sequence's new tokens and of its own keys, in either part's launch
     // A launch of fa_paged_rows_kernel that takes both parts: the first `whole_ctas`
     // CTAs have the prefix, cut as `shared` says, the others the sequences' own keys;
     // `solo`: each warp of those a unit of its own (paged_unit), `places` of them, or twice
@@ -152,7 +153,7 @@ __device__ __forceinline__ bool paged_tokens(const PagedParams& p, bool whole, i
     }
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.lens[b] - p.base_len;
     // (A sequence that brings nothing need not hold the prefix.)
-    const bool ok = 0 <= c0 && n >= 0 && n <= p.total_q - c0 && n <= p.max_q && (n == 0 || (n <= len && len <= p.max_k));
+    const bool ok = 0 <= c0 && n >= 0 && n <= p.total_q - c0 && n <= p.own_q && (n == 0 || (n <= len && len <= p.own_k));
     t.first = ok ? c0 : 0;
     t.n = ok ? n : 0;
     t.len = ok && n > 0 ? len : 0;
@@ -238,17 +239,19 @@ __device__ __forceinline__ bool paged_unit(const PagedParams& p, int r, int most
     return false;
 }
 
-// The first sequence that brings tokens (-1: none). Called by a whole warp.
+// The first sequence that brings tokens and is not broken (-1: none): the prefix's pages are
+// those of its row. Called by a whole warp.
 __device__ __forceinline__ int paged_first(const PagedParams& p, int lane) {
     for (int c = 0; c < p.B; c += 32) {
-        const int at = c + lane;
-        const unsigned who = __ballot_sync(0xffffffffu, at < p.B && p.cu[at + 1] > p.cu[at]);
+        NewTokens t;
+        const unsigned who =
+            __ballot_sync(0xffffffffu, c + lane < p.B && paged_tokens<true>(p, false, c + lane, t) && t.n > 0);
         if (who) return c + __ffs(who) - 1;
     }
     return -1;
 }
 // Reports a table of sequence b that does not begin with the shared prefix's pages, those
-// of the first sequence that brings tokens. Called by a whole warp.
+// of the first one (paged_first). Called by a whole warp.
 __device__ __forceinline__ void paged_check_prefix(const PagedParams& p, int b, int lane) {
     const int first = paged_first(p, lane);
     if (first < 0 || first == b) return;

@@ -242,6 +242,33 @@ def test_prefix_broken_batches_of_many(prefix):
             assert (o[keep].float() - want[0][keep].float()).abs().max() <= 2.0 ** -6 * want[0].float().abs().max()
 
 
+@pytest.mark.parametrize("prefix,page,H,Hkv,d,B", [(64, 16, 2, 1, 64, 3), (4096, 64, 8, 4, 128, 130), (1536, 32, 8, 4, 256, 24),
+                                                   (8192, 64, 16, 4, 128, 16), (64, 16, 4, 4, 128, 130)])
+def test_prefix_first_sequence_broken(prefix, page, H, Hkv, d, B):
+    """The first sequences are rejected, for their lengths or their offsets, and their rows of the table name no page: they
+    are not written, and the others keep their results."""
+    lens, ns = [prefix + 3 + 11 * b % 90 for b in range(B)], [1] * B
+    cache = Cache(lens, page, Hkv, d, 8, shared=prefix)
+    most = cache.table.shape[1] * page
+    q, cu = normal((B, H, d), 1), cu_of(ns)
+    want = cache.want(q, cu, lens, d)
+    args = [q.cuda(), *cache.gpu()]
+    splits = fa.fa_prefix_num_splits(B, H, Hkv, B, 1, most, prefix, d)
+    ws = torch.empty(fa.fa_paged_workspace_bytes(B, H, d, sum(splits)) // 4, device="cuda")
+    for count, length, first in ((1, prefix, 0), (2, 1, 0), (1, most + 1, 0), (1, None, -1)):
+        table, n, c = cache.table.copy(), list(lens), cu.copy()
+        table[:count] = -1
+        c[0] = first
+        if length:
+            n[:count] = [length] * count
+        o, lse = torch.full((B, H, d), 3.0, dtype=torch.bfloat16, device="cuda"), torch.full((H, B), 2.0, device="cuda")
+        fa.fa_fwd_prefix_fp8(*args, o, lse, dev(table), dev(c), dev(n), 1, most, prefix, ws, *splits)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(clear=True) == fa.FA_ERR_SEQLENS, (count, length)
+        assert torch.all(o[:count] == 3.0) and torch.all(lse[:, :count] == 2.0)
+        check(o, lse, *want, rows=slice(count, None))
+
+
 def test_prefix_rows_behind_the_last_sequence_are_left():
     prefix, page, H, Hkv, d = 32, 16, 4, 2, 64
     lens, ns = [prefix + 20, prefix + 50], [2, 4]
