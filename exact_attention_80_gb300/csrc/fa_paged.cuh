@@ -151,9 +151,9 @@ __device__ __forceinline__ bool paged_tokens(const PagedParams& p, bool whole, i
         t = {0, p.total_q, p.base_len};
         return true;
     }
+    // (All three loads at once. A sequence that brings nothing need not hold the prefix.)
     const int c0 = p.cu[b], n = p.cu[b + 1] - c0, len = p.lens[b] - p.base_len;
-    // (A sequence that brings nothing need not hold the prefix.)
-    const bool ok = 0 <= c0 && n >= 0 && n <= p.total_q - c0 && n <= p.own_q && (n == 0 || (n <= len && len <= p.own_k));
+    const bool ok = (0 <= c0) & (n >= 0) & (n <= p.total_q - c0) & (n <= p.own_q) & ((n == 0) | ((n <= len) & (len <= p.own_k)));
     t.first = ok ? c0 : 0;
     t.n = ok ? n : 0;
     t.len = ok && n > 0 ? len : 0;
@@ -243,9 +243,10 @@ __device__ __forceinline__ bool paged_unit(const PagedParams& p, int r, int most
 // those of its row. Called by a whole warp.
 __device__ __forceinline__ int paged_first(const PagedParams& p, int lane) {
     for (int c = 0; c < p.B; c += 32) {
+        const int at = c + lane;
         NewTokens t;
-        const unsigned who =
-            __ballot_sync(0xffffffffu, c + lane < p.B && paged_tokens<true>(p, false, c + lane, t) && t.n > 0);
+        const bool sound = paged_tokens<true>(p, false, min(at, p.B - 1), t);
+        const unsigned who = __ballot_sync(0xffffffffu, sound & (t.n > 0) & (at < p.B));
         if (who) return c + __ffs(who) - 1;
     }
     return -1;
