@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kWarps * 32, rows_ctas(D))
     }
     __syncwarp();
     if (!paged_wait<PART>(p)) return;
-    if (threadIdx.x == 0) griddep_launch_dependents();
+    paged_allow<PART>(p);
 
     // Unit: row blocks fastest (they share K and V in L2), then splits, heads.
     // (A cluster's CTAs are consecutive: its splits.) PART: the sequences' own units have
@@ -1043,6 +1043,18 @@ bool paged_aligned(const void* q, const void* o, const float* lse, const int* pa
            aligned(seqlens_k, 4);
 }
 
+// PagedParams::gate on the current device.
+__device__ unsigned g_fa_prefix_gate = 0u;
+cudaError_t gate_ptr(unsigned** ptr) {
+    static ContextCache<unsigned*> cache;
+    return cache.get(ptr, [](unsigned** out) {
+        void* p = nullptr;
+        const cudaError_t e = cudaGetSymbolAddress(&p, g_fa_prefix_gate);
+        *out = static_cast<unsigned*>(p);
+        return e;
+    });
+}
+
 // The parameters of a launch over `seqs` sequences of at most max_q new tokens and max_k
 // keys, cut into num_splits; the cache's maps and the arrays are set already.
 void cut_paged(PagedParams& p, const Plan& c, int seqs, int max_q, int max_k, int num_splits) {
@@ -1218,7 +1230,7 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
         p.shared = {p.max_q, p.max_k, p.row_blocks, p.num_splits, p.tiles_per_split, p.state0};
     }
     if (whole.tc || own.tc) {
-        if (!fa::encode_cache(p, cache, whole)) return FA_ERR_CUDA;
+        if (fa::gate_ptr(&p.gate) != cudaSuccess || !fa::encode_cache(p, cache, whole)) return FA_ERR_CUDA;
         if (fa::launch_paged<true>(p, whole, d, stream) != cudaSuccess) return FA_ERR_CUDA;
         p.whole_ctas = 0;
         p.early = 1;

@@ -123,8 +123,13 @@ struct PagedParams {
     // The second launch of a call that takes two: it need not wait for the first one, whose
     // CTAs have all waited for what came before when this grid may start, so the two run
     // side by side; one CTA more, the last, waits for the first launch, and by it the merge
-    // does.
+    // does. What came before is visible to a grid that waits, and starting says nothing of
+    // it, so it is passed on: the first launch's CTA 0 adds to `gate` behind its wait, before
+    // it allows this grid, and every thread of this one reads that count first (`gate` is the
+    // device's; all that ever happens to it is such adds, so a call's own or a later one
+    // is what is read).
     int early;
+    unsigned* gate;
     struct {
         int max_q, max_k, row_blocks, num_splits, tiles_per_split, state0;
     } shared;
@@ -135,12 +140,24 @@ struct PagedParams {
 template <bool PART>
 __device__ __forceinline__ bool paged_wait(const PagedParams& p) {
     if (PART && p.early) {
-        if (blockIdx.x + 1 < gridDim.x) return true;
+        if (blockIdx.x + 1 < gridDim.x) {
+            gate_acquire(p.gate);
+            return true;
+        }
         griddep_wait();
         return false;
     }
     griddep_wait();
     return true;
+}
+// Lets the next grid start.
+template <bool PART>
+__device__ __forceinline__ void paged_allow(const PagedParams& p) {
+    if (threadIdx.x == 0) {
+        // (The test makes it wait for the add; a grid whose CTA 0 says nothing is allowed by its end.)
+        const bool add = PART && p.gate && !p.early && blockIdx.x == 0;
+        if (!add || gate_release(p.gate) != 0xffffffffu) griddep_launch_dependents();
+    }
 }
 // The new tokens of sequence b (of the one problem where `whole`), positions and lengths
 // without the keys of a shared prefix. False where they are broken.

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(TcLayout<D, SHARES>::THREADS, 1) fa_paged_tc_k
     auto bar = [&](int i) -> uint32_t { return sbase + L::BAR_OFF + 8u * i; };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (!paged_wait<PART>(p)) return;
-    if (threadIdx.x == 0) griddep_launch_dependents();
+    paged_allow<PART>(p);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::KSTAGES; ++s) {

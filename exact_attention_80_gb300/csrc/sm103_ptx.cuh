@@ -76,6 +76,19 @@ __device__ __forceinline__ void ld_shared_v4f(uint32_t addr, float (&x)[4]) {
                  : "memory");
 }
 
+// What this thread has seen so far is passed on to who reads a count: a release, performed
+// when its result is there, and the acquire, for plain loads and for TMA behind it.
+__device__ __forceinline__ unsigned gate_release(unsigned* count) {
+    unsigned was;
+    asm volatile("atom.add.release.gpu.global.u32 %0, [%1], 1;" : "=r"(was) : "l"(count) : "memory");
+    return was;
+}
+__device__ __forceinline__ void gate_acquire(const unsigned* count) {
+    unsigned x;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(count) : "memory");
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // 32-byte global store (32-byte aligned): whole sectors.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&x)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),

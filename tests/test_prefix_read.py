@@ -269,6 +269,33 @@ def test_prefix_first_sequence_broken(prefix, page, H, Hkv, d, B):
         check(o, lse, *want, rows=slice(count, None))
 
 
+@pytest.mark.parametrize("prefix,page,H,Hkv,d,B,n", [(8192, 64, 16, 4, 128, 16, 1), (4096, 64, 32, 8, 128, 64, 1), (6144, 32, 32, 8, 128, 12, 5),
+                                                     (4096, 128, 16, 2, 256, 31, 1), (10240, 128, 16, 4, 64, 16, 1)])
+def test_prefix_reads_what_was_just_written(prefix, page, H, Hkv, d, B, n):
+    """Calls whose two launches run side by side, each right behind the copies that exchange everything they read: the
+    bits of calls on tensors that lie still."""
+    lens = [prefix + n + 37 * b % 500 for b in range(B)]
+    states = []
+    for seed, x in ((1, lens), (2, lens[::-1])):
+        cache = Cache(x, page, Hkv, d, seed, shared=prefix)
+        states.append([normal((B * n, H, d), seed).cuda(), *cache.gpu(), dev(cache.table), dev(x)])
+    cu = dev(cu_of([n] * B))
+    call = lambda *x: fa.attention_prefix_fp8(*x[:6], cu, x[6], n, max(lens), prefix)  # noqa: E731
+    want = []
+    for x in states:
+        want.append(call(*x))
+        ok()
+    one = [torch.empty_like(t) for t in states[0]]
+    got = []
+    for i in range(40):
+        for to, t in zip(one, states[i % 2]):
+            to.copy_(t)
+        got.append(call(*one))
+    ok()
+    for i, x in enumerate(got):
+        assert torch.equal(x[0], want[i % 2][0]) and torch.equal(x[1], want[i % 2][1]), i
+
+
 def test_prefix_rows_behind_the_last_sequence_are_left():
     prefix, page, H, Hkv, d = 32, 16, 4, 2, 64
     lens, ns = [prefix + 20, prefix + 50], [2, 4]
