@@ -1514,6 +1514,22 @@ BwdPackParts bwd_pack_parts(int B, int total_k, int max_q, int max_k, int H, int
     return c;
 }
 long long packed_rows_pad(int total_q, int B) { return (total_q + 64ll * (B + 1ll) + 127) / 128 * 128; }
+// Units of a kv head at most: no more sinks' tiles than the sequences have, the others for
+// the rest.
+long long bwd_pack_units(const BwdPackParts& c, int B, int total_k) {
+    return std::min(c.tiles, static_cast<long long>(std::min(B, total_k)) * c.sink_tiles) * c.sink_parts + c.tiles * c.parts;
+}
+// The tiles whose sums the last launch adds up (numbers of tile_slot, or the sinks' alone).
+long long bwd_pack_summed(const BwdPackParts& c, int B) {
+    return c.parts > 1 ? c.slots : c.sink_parts > 1 ? static_cast<long long>(B) * c.sink_tiles : 0;
+}
+// Whether the three launches' searches through the sequences end in time: the first and the
+// last launch's blocks go through half of them on average.
+bool bwd_pack_search(const BwdPackParts& c, int B, int total_q, int total_k, int H, int Hkv, int d) {
+    const long long rows = packed_rows_pad(total_q, B) / kBwdHalf * ((H + pre_heads(d) - 1) / pre_heads(d));
+    return packed_search(bwd_pack_units(c, B, total_k) * Hkv * (d == 256 ? 2 : 1) + rows +
+                             bwd_pack_summed(c, B) * Hkv * (kBwdKeys / kPostKeys), B);
+}
 
 }  // namespace
 
@@ -1605,7 +1621,7 @@ cudaError_t launch_bwd_win(const BwdParams& p, const void* q, const void* k, con
 // The three launches on packed sequences.
 template <int D>
 cudaError_t launch_bwd_pack(BwdParams p, const void* q, const void* k, const void* v, const void* o,
-                            const void* dout, const float* lse, void* dq, long long slots, cudaStream_t stream) {
+                            const void* dout, const float* lse, void* dq, long long k_tiles, cudaStream_t stream) {
     using T = const __nv_bfloat16*;
     p.block_heads = pre_heads(D);
     long long blocks = p.rows_pad / kBwdHalf * ((p.H + p.block_heads - 1) / p.block_heads);
@@ -1626,7 +1642,6 @@ cudaError_t launch_bwd_pack(BwdParams p, const void* q, const void* k, const voi
     if (e == cudaSuccess) e = launch_bwd_main<D, true, true>(p, stream);
     if (e != cudaSuccess) return e;
     const long long q_blocks = blocks;
-    const long long k_tiles = p.parts > 1 ? slots : p.sink_parts > 1 ? static_cast<long long>(p.seqs.B) * p.sink_tiles : 0;
     const long long k_blocks = k_tiles * 2 * p.Hkv * (kBwdKeys / kPostKeys);
     if (q_blocks + k_blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     return launch_dependent(fa_bwd_pack_post_kernel<D>, dim3(static_cast<unsigned>(q_blocks + k_blocks)), 256, 0, stream,
@@ -1769,9 +1784,9 @@ size_t fa_bwd_packed_workspace_bytes(int B, int total_q, int total_k, int max_se
     const fa_packed_batch c = {&none, &none, B, total_q, total_k, max_seqlen_q, max_seqlen_k};
     if (fa::check_packed(&c, H, Hkv, d, 1.f, window, sinks) != FA_OK) return 0;
     const size_t rows = static_cast<size_t>(fa::packed_rows_pad(total_q, B)) * H;
-    return (rows * (static_cast<size_t>(d) + 2) +
-            fa::bwd_pack_parts(B, total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks).part_floats) *
-           sizeof(float);
+    const fa::BwdPackParts parts = fa::bwd_pack_parts(B, total_k, max_seqlen_q, max_seqlen_k, H, Hkv, d, window, sinks);
+    if (!fa::bwd_pack_search(parts, B, total_q, total_k, H, Hkv, d)) return 0;
+    return (rows * (static_cast<size_t>(d) + 2) + parts.part_floats) * sizeof(float);
 }
 
 fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void* o, const void* dout, const float* lse,
@@ -1790,6 +1805,9 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
     for (long long x : {strides->k, strides->v, strides->dk, strides->dv})
         if (!fa::token_stride(x, Hkv, d)) return FA_ERR_STRIDE;
     if (!workspace || !fa::aligned(workspace, 16)) return FA_ERR_WORKSPACE;
+    const fa::BwdPackParts c = fa::bwd_pack_parts(batch->B, batch->total_k, batch->max_seqlen_q, batch->max_seqlen_k, H,
+                                                  Hkv, d, window, sinks);
+    if (!fa::bwd_pack_search(c, batch->B, batch->total_q, batch->total_k, H, Hkv, d)) return FA_ERR_SHAPE;
     fa::BwdParams p;
     std::memset(&p, 0, sizeof(p));
     if (!fa::encode_strided_tokens_map(&p.tm_q, q, d, batch->total_q, H, strides->q, fa::kBwdHalf) ||
@@ -1823,8 +1841,6 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
     p.dk_stride = strides->dk;
     p.dv_stride = strides->dv;
     p.fill = fill ? 1 : 0;
-    const fa::BwdPackParts c = fa::bwd_pack_parts(batch->B, batch->total_k, batch->max_seqlen_q, batch->max_seqlen_k, H,
-                                                  Hkv, d, window, sinks);
     p.sink_tiles = c.sink_tiles;
     p.sink_parts = c.sink_parts;
     p.parts = c.parts;
@@ -1836,18 +1852,17 @@ fa_status fa_bwd_packed(const void* q, const void* k, const void* v, const void*
     const double head_bytes = 8. * d * p.group * batch->total_q;
     const int together = static_cast<int>(std::min<double>(Hkv, 64e6 / head_bytes));
     p.pack_heads = window > 0 || static_cast<double>(c.tiles) * c.parts * together < 2 * 152 ? Hkv : together;
-    // Units of a kv head: no more sinks' tiles than the sequences have, the others for the rest.
-    const long long sink_units = std::min(c.tiles, static_cast<long long>(std::min(batch->B, batch->total_k)) * c.sink_tiles);
-    const long long units = sink_units * c.sink_parts + c.tiles * c.parts;
+    const long long units = fa::bwd_pack_units(c, batch->B, batch->total_k);
     if (units * Hkv * 2 > 0x7fffffffll) return FA_ERR_SHAPE;
     p.tile_units = static_cast<int>(units);
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit = fa::kDefaultWaitLimit;
     if (fa::device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-    const cudaError_t e = d == 64    ? fa::launch_bwd_pack<64>(p, q, k, v, o, dout, lse, dq, c.slots, stream)
-                          : d == 128 ? fa::launch_bwd_pack<128>(p, q, k, v, o, dout, lse, dq, c.slots, stream)
-                                     : fa::launch_bwd_pack<256>(p, q, k, v, o, dout, lse, dq, c.slots, stream);
+    const long long summed = fa::bwd_pack_summed(c, batch->B);
+    const cudaError_t e = d == 64    ? fa::launch_bwd_pack<64>(p, q, k, v, o, dout, lse, dq, summed, stream)
+                          : d == 128 ? fa::launch_bwd_pack<128>(p, q, k, v, o, dout, lse, dq, summed, stream)
+                                     : fa::launch_bwd_pack<256>(p, q, k, v, o, dout, lse, dq, summed, stream);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

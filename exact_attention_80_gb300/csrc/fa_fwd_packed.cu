@@ -55,6 +55,13 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
         return FA_ERR_STRIDE;
     const fa::FwdConfig c = fa::fwd_config(d);
     const int G = H / Hkv, tokens = 128 / G;
+    // Units: at most one that is not full per sequence that has a token.
+    const long long unit = static_cast<long long>(c.q_tiles) * tokens, B = std::min(batch->B, batch->total_q);
+    const long long units = std::min((batch->total_q + B * (unit - 1)) / unit,
+                                     B * ((batch->max_seqlen_q + unit - 1) / unit));
+    const long long ctas = units * Hkv;
+    if (ctas > 0x7fffffffll) return FA_ERR_SHAPE;
+    if (d == 256 && !fa::packed_search(ctas, batch->B)) return FA_ERR_SHAPE;
     fa::FwdParams p;
     std::memset(&p, 0, sizeof(p));
     if (!fa::encode_token_heads_map(&p.tm_q, q, d, batch->total_q, H, q_stride, G, tokens) ||
@@ -86,12 +93,6 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
     p.sinks = sinks;
     p.num_splits = 1;
     p.tiles_per_cta = c.q_tiles;
-    // Units: at most one that is not full per sequence that has a token.
-    const long long unit = static_cast<long long>(c.q_tiles) * tokens, B = std::min(batch->B, batch->total_q);
-    const long long units = std::min((batch->total_q + B * (unit - 1)) / unit,
-                                     B * ((batch->max_seqlen_q + unit - 1) / unit));
-    const long long ctas = units * Hkv;
-    if (ctas > 0x7fffffffll) return FA_ERR_SHAPE;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o_scale = 1.f;
     p.wait_limit = fa::kDefaultWaitLimit;
@@ -103,10 +104,14 @@ extern "C" fa_status fa_fwd_packed(const void* q, const void* k, const void* v, 
     // (us, one unit per CTA and persistent: d = 64, 16 + 4 heads, four prompts of 8000 tokens
     // 561 and 542, 32 + 8, ten of 2000 262 and 217; d = 128, 16 heads, 64 of 500 152 and 144,
     // 16 + 4, 2.5 waves in three of 2047 58 and 55; 1.6 waves in three of up to 1500, 16 + 8,
-    // 29.3 and 30.5; one of 16000 with one of 9000, 16 + 4, 900 and 934).
+    // 29.3 and 30.5; one of 16000 with one of 9000, 16 + 4, 900 and 934). Longer lists too
+    // where each unit's search through the sequences would take longest: persistent CTAs go
+    // through them once.
     const long long reach = std::min<long long>(batch->max_seqlen_k, window > 0 ? window + unit + sinks : 1ll << 30);
     // (A unit's time bounds the wait for the next but three: 2^24 keys take 0.1 s.)
-    const bool persist = d <= 128 && ctas >= 2ll * sms && reach <= (d == 64 ? 1 << 24 : 64 * 128);
+    const bool long_lists = d == 64 || !fa::packed_search(ctas, batch->B);
+    const bool persist = d <= 128 && ctas >= 2ll * sms && reach <= (long_lists ? 1 << 24 : 64 * 128);
+    if (!persist && !fa::packed_search(ctas, batch->B)) return FA_ERR_SHAPE;
     const unsigned grid = static_cast<unsigned>(persist ? sms : ctas);
     return fa::launch_fwd_packed(p, d, persist, grid, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

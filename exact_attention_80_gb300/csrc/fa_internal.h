@@ -201,6 +201,11 @@ fa_status check_window(int H, int Hkv, int Nq, int Nk, int window, int sinks);
 // A packed batch and the operator's shape; the distance of a packed tensor's tokens.
 fa_status check_packed(const fa_packed_batch* batch, int H, int Hkv, int d, float scale, int window, int sinks);
 bool token_stride(long long stride, int heads, int d);
+// Whether `blocks` blocks that each look through a batch of B sequences for their work do so
+// in a few seconds: 25 to 43 sequences a nanosecond are looked at on a GB300 (16384 of one
+// token, 2 heads of 256: forward 21.6 ms, step 52), so 2^37 take 3 to 6 s, and 2^22
+// sequences would take hours.
+inline bool packed_search(long long blocks, int B) { return B <= 128 || blocks <= (1ll << 37) / B; }
 // SMs of the current device (cached).
 cudaError_t sm_count(int* out);
 // The driver's cuTensorMapEncodeTiled, or null.

@@ -324,7 +324,10 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
  * tokens cu_seqlens_k[b] .. cu_seqlens_k[b + 1] - 1 (DEVICE int32 [B + 1] each; they
  * may be the same array). Required: cu[0] >= 0, nondecreasing, cu_seqlens_q[B] <=
  * total_q, cu_seqlens_k[B] <= total_k, every length <= max_seqlen_q or max_seqlen_k;
- * total_q, total_k < 2^30, B <= 2^22. Sequences may be empty. A sequence whose
+ * total_q, total_k < 2^30, B <= 2^22. Sequences may be empty. (Beyond 128 sequences
+ * each tile of the backward, and of the forward at d = 256, looks through all of them for
+ * its own: where that would take several seconds, more than 2^37 such looks, as for some
+ * 100000 sequences of 8 kv heads, the call is refused with FA_ERR_SHAPE.) A sequence whose
  * offsets break the requirements is neither read nor written, FA_ERR_SEQLENS from
  * fa_device_status.
  */

@@ -283,6 +283,30 @@ def test_broken_and_foreign_things_in_batches_of_many_units(d):
     assert torch.all(mine[0][s] == 7.0) and torch.all(mine[1][:, s] == 7.0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_by_the_hundred_thousand(d):
+    """So many that a search for every unit would take seconds, with a long one among them: that one gets the bits of a
+    call with it alone, a sequence of one token its value."""
+    H, B, N = 8, 1 << 17, 9000
+    ns = np.ones(B, np.int64)
+    at = 70000
+    ns[at] = N
+    cu, T = dev(cu_of(ns)), B + N - 1
+    g = torch.Generator(device="cuda").manual_seed(d)
+    q, k, v = (torch.randn((T, H, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    o, lse = fa.attention_packed(q, k, v, cu, cu, N, N)
+    ok()
+    one, rows = dev([0, N]), slice(at, at + N)
+    o1, l1 = fa.attention_packed(q[rows], k[rows], v[rows], one, one, N, N)
+    ok()
+    assert torch.equal(o[rows], o1) and torch.equal(lse[:, rows], l1)
+    out = torch.ones(T, dtype=torch.bool, device="cuda")
+    out[rows] = False
+    assert torch.equal(o[out], v[out])
+    want = (q.double() * k.double()).sum(-1).t() * fa.default_scale(d)
+    assert ((lse - want)[:, out]).abs().max() <= 1e-3
+
+
 def test_strided_tokens():
     """A fused projection's columns, and gradients written into one: the same bits as separate tensors."""
     H, Hkv, d, ns = 8, 2, 128, [300, 1, 77]

@@ -74,6 +74,33 @@ def test_packed_backward_refuses(lib, kw, code):
     assert _backward(lib, **kw) == code
 
 
+def _many(B, tokens=1):
+    return _batch(B=B, total_q=B * tokens, total_k=B * tokens, max_q=tokens, max_k=tokens)
+
+
+@pytest.mark.parametrize("B", [1 << 18, 1 << 20, 1 << 22])
+def test_searches_that_would_take_minutes_are_refused(lib, B):
+    """Where each of very many tiles would look through very many sequences (2^22 sequences: hours)."""
+    assert _forward(lib, batch=_many(B), d=256, H=8, Hkv=8, qs=2048, ks=2048, vs=2048) == 3
+    wide = dict(H=8, Hkv=8, strides=_strides(*[2048] * 7))
+    for d in (64, 128, 256):
+        assert _backward(lib, batch=_many(B), d=d, **wide) == 3
+        assert fa.fa_bwd_packed_workspace_bytes(B, B, B, 1, 1, 8, 8, d) == 0
+
+
+def test_searches_of_seconds_are_not(lib):
+    if torch.cuda.is_available():
+        pytest.skip("would launch on fake pointers; only meaningful without a GPU")
+    for B in (1 << 15, 1 << 16):
+        wide = dict(H=4, Hkv=2, strides=_strides(*[1024] * 7))
+        assert _forward(lib, batch=_many(B), d=256, H=4, Hkv=2, qs=1024, ks=512, vs=512) == 7
+        for d in (64, 128, 256):
+            assert _backward(lib, batch=_many(B), d=d, **wide) == 7
+            assert fa.fa_bwd_packed_workspace_bytes(B, B, B, 1, 1, 4, 2, d) > B * 64 * 4 * d * 4
+    assert _forward(lib, batch=_many(1 << 22), d=128, H=8, Hkv=8, qs=1024, ks=1024, vs=1024) == 7  # (one search a CTA)
+    assert _forward(lib, batch=_many(100, 1 << 20), d=256, H=8, Hkv=8, qs=2048, ks=2048, vs=2048) == 7
+
+
 def _cache(k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, pages=10, Hkv=2, page=16, d=64):
     return fa._PAGED_CACHE.pack(k, v, ks, vs, pages, Hkv, page, d)
 
