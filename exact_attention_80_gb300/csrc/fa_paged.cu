@@ -956,9 +956,12 @@ Plan prefix_plan(const Plan& own, int total_q, int G, int Hkv, int prefix_len, i
     return c;
 }
 // Whether the warps of the sequences' own parts behind a prefix take units alone: where
-// there is a unit for every CTA that runs at once (and all key tiles can be counted in int).
+// there is a unit for every CTA that runs at once (and all key tiles can be counted in int),
+// up to 1024 sequences, all of which every warp looks through (us so and with a CTA a unit,
+// one token behind 512 keys with 9 of its own, 8 kv heads of 128: 512 sequences 50 and 71,
+// 1024 110 and 131, 2048 340 and 252, 4096 1252 and 512).
 bool solo_units(const Plan& own, int B, int Hkv, int d) {
-    return !own.tc && static_cast<long long>(B) * Hkv >= static_cast<long long>(kPlaces) * rows_ctas(d) &&
+    return !own.tc && static_cast<long long>(B) * Hkv >= static_cast<long long>(kPlaces) * rows_ctas(d) && B <= 1024 &&
            own.tiles <= 0x3fffffff / B;
 }
 // The splits of a shared prefix that the tensor-core kernel takes beside the sequences'

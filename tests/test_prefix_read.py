@@ -269,6 +269,44 @@ def test_prefix_first_sequence_broken(prefix, page, H, Hkv, d, B):
         check(o, lse, *want, rows=slice(count, None))
 
 
+@pytest.mark.parametrize("B", [1024, 1025, 3000])
+@pytest.mark.parametrize("prefix", [64, 8192])
+def test_prefix_of_thousands_of_sequences(B, prefix):
+    """On either side of the number up to which each warp looks through all sequences: the paged call's results, a
+    sequence that brings nothing and a rejected one left as they were."""
+    page, H, Hkv, d = 16, 4, 2, 64
+    ns, lens = [1] * B, [prefix + 1 + 7 * b % 60 for b in range(B)]
+    ns[300], ns[999] = 0, 2
+    cache = Cache(lens, page, Hkv, d, 3, shared=prefix)
+    q, cu = normal((sum(ns), H, d), 1), cu_of(ns)
+    lens[700] = prefix
+    args = [q.cuda(), *cache.gpu()]
+    batch = [dev(cache.table), dev(cu), dev(lens)]
+    most = cache.table.shape[1] * page
+    splits = fa.fa_prefix_num_splits(B, H, Hkv, sum(ns), 2, most, prefix, d)
+    ws = torch.empty(fa.fa_paged_workspace_bytes(sum(ns), H, d, sum(splits)) // 4, device="cuda")
+    o, lse = torch.full_like(args[0], 3.0), torch.full((H, sum(ns)), 2.0, device="cuda")
+    fa.fa_fwd_prefix_fp8(*args, o, lse, *batch, 2, most, prefix, ws, *splits)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_ERR_SEQLENS
+    out = int(cu[700])
+    assert torch.all(o[out] == 3.0) and torch.all(lse[:, out] == 2.0)
+    op, lp = fa.attention_paged_fp8(*args, *batch, 2, most)
+    ok()
+    some = [int(cu[b]) for b in (0, 1, 299, 301, 699, 701, 998, 999, 1000, B - 1)] + [int(cu[999]) + 1]
+    seqs = [next(b for b in range(B) if cu[b] <= i < cu[b + 1]) for i in some]
+    small = type(cache).__new__(type(cache))
+    small.codes, small.scale, small.table = cache.codes, cache.scale, cache.table[seqs]
+    n = [lens[b] - (b == 999 and i == cu[999]) for b, i in zip(seqs, some)]
+    want = small.want(q[some], cu_of([1] * len(some)), n, d)
+    check(o[some], lse[:, some], *want)
+    keep = [i for i in range(sum(ns)) if i != out]
+    # (Each is off by 2^-8 |o| + 2^-10 a at most, and a, as |o|, is no larger than the largest |v|.)
+    largest = np.nanmax(np.abs(orc.VALUES[cache.codes[1]]) * cache.scale[1][:, :, None, None])
+    gap = (o[keep].float() - op[keep].float()).abs() - 2.0 ** -7 * op[keep].float().abs()
+    assert gap.max() <= (2.0 ** -9 + 2.0 ** -13) * largest
+
+
 @pytest.mark.parametrize("prefix,page,H,Hkv,d,B,n", [(8192, 64, 16, 4, 128, 16, 1), (4096, 64, 32, 8, 128, 64, 1), (6144, 32, 32, 8, 128, 12, 5),
                                                      (4096, 128, 16, 2, 256, 31, 1), (10240, 128, 16, 4, 64, 16, 1)])
 def test_prefix_reads_what_was_just_written(prefix, page, H, Hkv, d, B, n):
