@@ -548,7 +548,8 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
  * (FA_ERR_SEQLENS from fa_device_status), nor are tokens whose page is not one of the
  * cache (FA_ERR_PAGES): their rows are not written. Rows that belong to no sequence
  * (before cu_seqlens[0], from cu_seqlens[B] on) stay as they are, or, with `fill` != 0,
- * get 0.
+ * get 0. (Each piece of 16 to 64 tokens looks through all sequences: FA_ERR_SHAPE beyond
+ * 2^41 such looks, several seconds.)
  */
 fa_status fa_kv_read_fp8(const fa_paged_cache* cache, const int* page_table, const int* cu_seqlens, const int* starts,
                          void* k_out, void* v_out, int B, int total, int max_pages, long long k_stride,

@@ -141,6 +141,13 @@ def test_read_refuses(lib, kw, code):
     assert _read(lib, **kw) == code
 
 
+def test_reads_whose_search_would_take_minutes_are_refused(lib):
+    for B, total in ((1 << 24, 1 << 29), (1 << 28, 1 << 28), (2 ** 31 - 1, (1 << 30) - 1)):
+        assert _read(lib, B=B, total=total) == 3
+    if not torch.cuda.is_available():
+        assert _read(lib, B=1 << 16, total=1 << 27) == 7 and _read(lib, B=1, total=(1 << 30) - 1) == 7
+
+
 def test_valid_calls_without_a_gpu_report_a_cuda_error(lib):
     if torch.cuda.is_available():
         pytest.skip("would launch on fake pointers; only meaningful without a GPU")
