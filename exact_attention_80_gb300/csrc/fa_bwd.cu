@@ -112,13 +112,6 @@ struct BwdParams {
 
 namespace {
 
-// First padded row of sequence b, whose first query is q0: a multiple of 64, with room
-// for its queries in whole steps of 64 before the next sequence's.
-__host__ __device__ __forceinline__ long long pad_row(int q0, int b) { return (q0 & ~63) + 64ll * b; }
-// Number of its first key tile among all sequences' (k0: its first key), with a number
-// for each of its tiles before the next sequence's.
-__host__ __device__ __forceinline__ long long tile_slot(int k0, int b) { return k0 / 128 + static_cast<long long>(b); }
-
 constexpr int kBwdKeys = 128;   // keys per CTA (TMEM lanes of S^T, dP^T, dV, dK)
 constexpr int kBwdHalf = 64;    // queries per step
 constexpr float kLog2e = 1.4426950408889634f;
@@ -133,7 +126,8 @@ struct LayoutBwd {
     static constexpr int HALVES = D / DH;               // CTAs per key tile
     static constexpr int BUFS = D == 64 && WIN ? 3 : 2;        // step buffers in TMEM
     static constexpr int STAGES = D == 256 ? 1 : BUFS == 3 ? 5 : 3;  // Q/dO (+ -LSE log2e, -D) ring slots
-    // warp 0 producer, warp 1 issuer, warps 2-3 idle, warps 4-11 compute (two
+    // warp 0 producer, warp 1 issuer, warps 2-3 idle (packed sequences: warp 2 finds
+    // the unit), warps 4-11 compute (two
     // per TMEM lane quarter, one per 32-query chunk of a step), warps 12-15
     // dQ readout (one per lane quarter; at D = 64 the first two only).
     static constexpr int COMPUTE_WARPS = 8;
@@ -590,7 +584,7 @@ __global__ void __launch_bounds__(LayoutBwd<D, WIN>::THREADS, 1) fa_bwd_kernel(c
         };
         // S^T_G = K Q_G^T and dP^T_G = V dO_G^T into buffer G % BUFS (lanes = keys,
         // 64 query columns each), reading ring slot G % STAGES; first, from
-        // G = 2 on, the readout group must have taken that buffer's dQ^T of two
+        // G = BUFS on, the readout group must have taken that buffer's dQ^T of BUFS
         // steps back out. `rows`: the step's queries that the sequence has (PACK).
         auto clear_rows = [&](uint32_t tile, int from, int rows) {  // rows from .. rows - 1 of 128 bytes
             for (int at = from * 128 + lane * 16; at < rows * 128; at += 512)

@@ -31,20 +31,14 @@ __device__ __forceinline__ bool packed_seq(const PackedSeqs& p, int b, PackedSeq
     return ok;
 }
 
-// Sequence b has n units at levels a .. a + n - 1, one each (runs(b, a, n); n = 0:
-// none); a unit's time grows with its level. Finds the unit of rank r: for up to 128
-// sequences as they are taken from the highest level down, so that the longest start
-// first whatever the sequences' lengths and order are (by bisection over the levels, a few
-// dozen instructions each, without a list in memory or a launch that makes one); for more,
-// whose units are short beside the whole, in the order of the sequences, each from its
-// highest level down. Called by a whole warp; false where there is no such unit.
-//
-// `at`: where the search begins, the first 128-sequence block that r may lie in and the
-// units before it; callers whose ranks rise keep it from one call to the next.
-constexpr int kPackedSorted = 128;
-struct PackedCursor {
-    int block, before;
-};
+// First padded row of sequence b, whose first query is q0: a multiple of 64, with room
+// for its queries in whole steps of 64 before the next sequence's.
+__host__ __device__ __forceinline__ long long pad_row(int q0, int b) { return (q0 & ~63) + 64ll * b; }
+// Number of its first key tile among all sequences' (k0: its first key), with a number
+// for each of its tiles before the next sequence's.
+__host__ __device__ __forceinline__ long long tile_slot(int k0, int b) { return k0 / 128 + static_cast<long long>(b); }
+
+constexpr int kPackedSorted = 128;  // (packed_pick)
 // Unit number `lin` of `heads` heads with `all` units each: its head and its rank among
 // that head's. Heads come in groups of `together`, a group's units head by head for each
 // rank, all of a group's before the next group's. False: there is none.
@@ -70,6 +64,22 @@ __device__ __forceinline__ int packed_total(int B, int lane, F&& units) {
     for (int b = lane; b < B; b += 32) n += units(b);
     return __reduce_add_sync(0xffffffffu, n);
 }
+// Sequence b has n units at levels a .. a + n - 1, one each (runs(b, a, n); n = 0:
+// none); a unit's time grows with its level. Finds the unit of rank r: for up to 128
+// sequences as they are taken from the highest level down, so that the longest start
+// first whatever the sequences' lengths and order are (by bisection over the levels, a few
+// dozen instructions each, without a list in memory or a launch that makes one); for more,
+// where a search of this kind would read all sequences for each level, in the order of the
+// sequences, each from its highest level down. (A long sequence behind more than 128 short
+// ones then starts last: 16000 tokens before and behind 128 of 100, 16 heads over 4, us:
+// d = 64 557 and 673, d = 128 718 and 723, backward 1954 and 1955, 2405 and 2464.) Called by
+// a whole warp; false where there is no such unit.
+//
+// `at`: where the search begins, the first 128-sequence block that r may lie in and the
+// units before it; callers whose ranks rise keep it from one call to the next.
+struct PackedCursor {
+    int block, before;
+};
 template <typename F>
 __device__ __forceinline__ bool packed_pick(int B, int r, int lane, F&& runs, int& b, int& level, PackedCursor& at) {
     constexpr int CHUNKS = kPackedSorted / 32;
