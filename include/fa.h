@@ -329,7 +329,10 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
  * its own: where that would take several seconds, more than 2^37 such looks, as for some
  * 100000 sequences of 8 kv heads, the call is refused with FA_ERR_SHAPE.) A sequence whose
  * offsets break the requirements is neither read nor written, FA_ERR_SEQLENS from
- * fa_device_status.
+ * fa_device_status. (Each is judged by its own two offsets of either array: where offsets
+ * fall, a later sequence may lie over earlier ones without a fault of its own. Such a
+ * batch is reported all the same, but no result of it is defined; rows before the lowest
+ * and from the highest offset on stay as they are.)
  */
 typedef struct {
     const int* cu_seqlens_q;
@@ -546,7 +549,8 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
  * power-of-two scales of fa_kv_append_fp8; NaN stays NaN. A sequence whose offsets are
  * no valid partition, or whose tokens pass max_pages * page_size, is not read
  * (FA_ERR_SEQLENS from fa_device_status), nor are tokens whose page is not one of the
- * cache (FA_ERR_PAGES): their rows are not written. Rows that belong to no sequence
+ * cache (FA_ERR_PAGES): their rows are not written. (Where offsets fall and sequences lie
+ * over one another, a row may come from any of them.) Rows that belong to no sequence
  * (before cu_seqlens[0], from cu_seqlens[B] on) stay as they are, or, with `fill` != 0,
  * get 0. (Each piece of 16 to 64 tokens looks through all sequences: FA_ERR_SHAPE beyond
  * 2^41 such looks, several seconds.)

@@ -307,6 +307,30 @@ def test_sequences_by_the_hundred_thousand(d):
     assert ((lse - want)[:, out]).abs().max() <= 1e-3
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks,long", [(0, 0, 1), (60, 130, 1), (0, 0, 40)])
+def test_falling_offsets_are_reported_and_touch_nothing_else(d, window, sinks, long):
+    """Sequences that lie over one another because offsets fall: reported, and no row outside of them is written."""
+    H, Hkv, T = 4, 2, 300 * long
+    cu = dev([0, 100 * long, 50 * long, 200 * long, 20 * long, 120 * long])
+    q, k, v, do = (x.cuda() for x in make(T, T, H, Hkv, d, 4))
+    most = 150 * long
+    o, lse = fa.attention_packed(q, k, v, dev([0, T]), dev([0, T]), T, T, window, sinks)
+    ok()
+    mine = [torch.full_like(x, 7.0) for x in (q, lse, q, k, v)]
+    fa.fa_fwd_packed(q, k, v, mine[0], mine[1], cu, cu, most, most, window, sinks)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_ERR_SEQLENS
+    ws = torch.zeros(fa.fa_bwd_packed_workspace_bytes(5, T, T, most, most, H, Hkv, d, window, sinks) // 4 + 1024, device="cuda")
+    guard = ws[-1024:].fill_(5.0)
+    fa.fa_bwd_packed(q, k, v, o, do, lse, *mine[2:], ws, cu, cu, most, most, window, sinks)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(clear=True) == fa.FA_ERR_SEQLENS
+    assert torch.all(guard == 5.0)
+    for x in (mine[0], mine[1].t(), *mine[2:]):
+        assert torch.all(x[200 * long:] == 7.0)
+
+
 def test_strided_tokens():
     """A fused projection's columns, and gradients written into one: the same bits as separate tensors."""
     H, Hkv, d, ns = 8, 2, 128, [300, 1, 77]
