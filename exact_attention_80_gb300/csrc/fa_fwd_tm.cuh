@@ -57,7 +57,9 @@
 namespace fa {
 
 // Per head dim: K/V ring depth and the setmaxnreg split (control warpgroup /
-// softmax warpgroups), each the spill-free choice for that instantiation.
+// softmax warpgroups), each the spill-free choice for the dense instantiation. (Of the
+// others the window's spill 20 bytes at d = 64 with a unit per CTA, 24 and 80 with
+// persistent CTAs, and the packed one 52, persistent at d = 128.)
 template <int D>
 struct TmCfg;
 template <>
@@ -73,8 +75,8 @@ struct TmCfg<128> {
 template <int D>
 struct TmPersistCfg {
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    // Spill-free at both head dims (104 / 200 spilled at d = 64 once the kernels
-    // wait for the previous grid; 88 / 208 is also 2 % faster there).
+    // Spill-free at both head dims in the dense form (104 / 200 spilled at d = 64 once the
+    // kernels wait for the previous grid; 88 / 208 is also 2 % faster there).
     static constexpr int CTRL_REGS = 88, SOFTMAX_REGS = 208;
 };
 // 8-bit (e4m3) inputs: K/V slots are half the size, so the ring is deeper.

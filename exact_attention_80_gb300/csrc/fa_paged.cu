@@ -970,7 +970,9 @@ bool solo_units(const Plan& own, int B, int Hkv, int d) {
 // B x prefix + own keys from 2 x 2900 + 50 to 64 x 65536 + 2000. (64 sequences, 16384 + up
 // to 2000 keys, 32 + 8 heads, d = 128: 73 us with the prefix on all SMs first, in 19 parts,
 // 61 with six, before the merge's last steps; 16 of five tokens, 8160 + up to 4000: 67
-// with eight, 55 with three.)
+// with eight, 55 with three. All of those have lengths spread up to the longest; for
+// others it is further off: 64 of 16384 + 2000 each, 104 as proposed and 81 at best, one
+// of 2000 among 63 of 50, 53 and 37.)
 int prefix_splits_beside(const Plan& w, const Plan& own, int B, int H, int Hkv, int total_q, int max_own, int d,
                          int* prefix_splits) {
     const double start = d == 64 ? 6. : d == 128 ? 8. : 24., tile = 1.6;  // a prefix CTA, a key tile of it
