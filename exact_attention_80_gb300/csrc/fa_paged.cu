@@ -955,6 +955,11 @@ Plan prefix_plan(const Plan& own, int total_q, int G, int Hkv, int prefix_len, i
     c.tiles = tiles;
     return c;
 }
+// Sequences behind a prefix at most: each that brings tokens looks for the first one, past
+// those before it that do not (the second half of 131072 sequences past the first: 52 ms,
+// with 32 heads on one 224; 2^19 would take 0.8 and 3.6 s).
+constexpr int kPrefixSeqs = 1 << 19;
+
 // Whether the warps of the sequences' own parts behind a prefix take units alone: where
 // there is a unit for every CTA that runs at once (and all key tiles can be counted in int),
 // up to 1024 sequences, all of which every warp looks through (us so and with a CTA a unit,
@@ -1181,8 +1186,8 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
 
 int fa_prefix_num_splits(int B, int H, int Hkv, int total_q, int max_seqlen_q, int max_seqlen_k, int prefix_len, int d,
                          int* prefix_splits) {
-    if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q || B < 1 || Hkv < 1 ||
-        H < Hkv || H % Hkv || max_seqlen_q < 1 || !fa::valid_d(d))
+    if (!prefix_splits || prefix_len < 1 || prefix_len >= max_seqlen_k || total_q < max_seqlen_q || B < 1 ||
+        B > fa::kPrefixSeqs || Hkv < 1 || H < Hkv || H % Hkv || max_seqlen_q < 1 || !fa::valid_d(d))
         return 0;
     const fa::Plan c = fa::plan_of(H / Hkv, max_seqlen_q, max_seqlen_k - prefix_len, d, 0, 0);
     const fa::Plan w = fa::prefix_plan(c, total_q, H / Hkv, Hkv, prefix_len, d);
@@ -1207,7 +1212,7 @@ fa_status fa_fwd_prefix_fp8(const void* q, const fa_paged_cache* cache, const in
                                          max_seqlen_k, max_pages, scale);
     if (sc != FA_OK) return sc;
     const int d = cache->d;
-    if (prefix_len < 1 || prefix_len % cache->page_size || prefix_len >= max_seqlen_k) return FA_ERR_SHAPE;
+    if (prefix_len < 1 || prefix_len % cache->page_size || prefix_len >= max_seqlen_k || B > fa::kPrefixSeqs) return FA_ERR_SHAPE;
     if (static_cast<long long>(total_q) * (H / cache->Hkv) > 0x7fffffffll - 4096) return FA_ERR_SHAPE;
     if (num_splits < 1 || prefix_splits < 1 || num_splits > FA_MAX_SPLITS || prefix_splits > FA_MAX_SPLITS - num_splits)
         return FA_ERR_SPLITS;

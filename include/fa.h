@@ -525,7 +525,7 @@ fa_status fa_fwd_paged_fp8(const void* q, const fa_paged_cache* cache, const int
  * sequence by sequence, and the two parts' states are merged. A row of page_table that
  * begins with other pages than that of the first sequence with queries (of those that
  * are not reported with FA_ERR_SEQLENS): FA_ERR_PAGES, its sequence's result is
- * undefined. prefix_len < max_seqlen_k.
+ * undefined. prefix_len < max_seqlen_k, B <= 2^19.
  * The sequences' own keys are cut into num_splits parts, the prefix into
  * prefix_splits (together FA_MAX_SPLITS at most; fa_prefix_num_splits proposes both: it
  * returns the first, 0 for arguments out of range). workspace:

@@ -148,6 +148,15 @@ def test_reads_whose_search_would_take_minutes_are_refused(lib):
         assert _read(lib, B=1 << 16, total=1 << 27) == 7 and _read(lib, B=1, total=(1 << 30) - 1) == 7
 
 
+def test_prefix_of_more_sequences_than_can_look_for_the_first(lib):
+    for B in ((1 << 19) + 1, 2 ** 31 - 1):
+        assert _prefix(lib, B=B) == 3
+        assert fa.fa_prefix_num_splits(B, 4, 2, 8, 4, 64, 32, 64) == (0, 0)
+    assert fa.fa_prefix_num_splits(1 << 19, 4, 2, 1 << 19, 1, 64, 32, 64) != (0, 0)
+    if not torch.cuda.is_available():
+        assert _prefix(lib, B=1 << 19) == 7
+
+
 def test_valid_calls_without_a_gpu_report_a_cuda_error(lib):
     if torch.cuda.is_available():
         pytest.skip("would launch on fake pointers; only meaningful without a GPU")
